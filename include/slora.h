@@ -77,15 +77,18 @@ typedef enum slora_status {
 #define SLORA_DEV_BAD_PAGE 3      /* page-table entry outside [0, num_pages) */
 #define SLORA_DEV_BAD_SEGMENT 4   /* segment tokens disagree on their adapter, or bad bounds */
 #define SLORA_DEV_TIMEOUT 5       /* a bounded wait inside a kernel gave up */
+#define SLORA_DEV_BAD_LENGTH 6    /* KV length below the new tokens or beyond the block table */
+#define SLORA_DEV_BAD_POSITION 7  /* token position outside the rotation table */
 
 const char *slora_status_str(slora_status s);
 /* Message of the calling thread's last failed call ("" if none).  Valid until the
  * thread's next failing call. */
 const char *slora_last_error(void);
-/* Library version as major * 10000 + minor * 100 + patch: 200 (0.2.0).  0.2.0 adds
+/* Library version as major * 10000 + minor * 100 + patch: 300 (0.3.0).  0.2.0 added
  * slora_lora_apply_multi, residency under pool pressure (slora_adapters_acquire /
  * release, slora_pages_alloc_evict, slora_pool_get_stats, slora_lru_*) and the padded
- * batched-GEMM comparison path (slora_lora_apply_bmm). */
+ * batched-GEMM comparison path (slora_lora_apply_bmm); 0.3.0 adds the 8-bit KV cache in
+ * the pool's pages (slora_kv_*). */
 int32_t slora_version(void);
 
 /* ---------------------------------------------------------------------------
@@ -451,6 +454,126 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
                                       int32_t T, const int32_t *token_adapter_idx,
                                       const int32_t *seg_indptr, int32_t n_seg,
                                       const float *scaling, slora_stream_t stream);
+
+/* ---------------------------------------------------------------------------
+ * The 8-bit KV cache in the pool's pages, and the attention over it (explainer, "What to
+ * notice when reading": KV blocks and adapter rows are pages of one pool).
+ *
+ * Layout.  A page taken with slora_pages_alloc holds one block of tokens of one KV head,
+ * keys or values: rows [block_tokens][head_dim] of 8-bit codes from the page's start, with
+ * block_tokens = (hidden * 2 / head_dim) rounded down to a multiple of 8 (64 tokens at
+ * hidden 4096 and head_dim 128).  Bytes past the rows are not used.  One power-of-two scale
+ * per page, i.e. per block of tokens and head, for keys and values apart:
+ *     value = code * 2^exponent[page],   int8 exponent[num_pages], device memory of the cache
+ * The format is that of the codes:
+ *     SLORA_KV_E4M3  8-bit floats (4 exponent bits, 3 mantissa bits, largest value 448)
+ *     SLORA_KV_INT8  integers -127 .. 127
+ * A power of two lets a block's scale grow while it fills: the codes already there are
+ * divided by a power of two and rounded to nearest even, which is exact for 8-bit floats
+ * short of their subnormal range.
+ *
+ * slora_kv_create(): the cache of one layer's (or any) KV heads over `pool`'s pages.
+ *   n_kv_heads  1 .. 1024;  head_dim  64 or 128 (a page must hold 8 rows of it)
+ *   format      SLORA_KV_E4M3 or SLORA_KV_INT8
+ *   Allocates num_pages bytes for the exponents (set to 0) and the attention's workspace.  The pages stay
+ *   the pool's: the caller takes and returns them, and may use several caches over one pool
+ *   (each with exponents of its own).  Destroy a pool's caches before the pool;
+ *   slora_kv_destroy waits for the device, and NULL is a no-op.
+ * slora_kv_block_tokens(), slora_kv_exponents(): block_tokens, and the device address of the
+ *   exponents (for saving, moving or filling pages; a page's bytes are at slora_pool_base).
+ *
+ * slora_kv_batch: the sequences of an iteration, the same for append and attend.
+ *   n_tokens     T, 0 <= T <= 1 << 20: rows of q, k, v and out
+ *   n_seqs       S, 0 <= S <= 1 << 20
+ *   max_q        the most new tokens of a sequence, 1 or more: it chooses between kernels
+ *                and their grids, the results do not depend on it being tight, but a sequence
+ *                with more new tokens than max_q is the caller's error (SLORA_DEV_BAD_SEGMENT;
+ *                it is skipped)
+ *   max_blocks   width of the block table, 1 or more
+ *   tok_indptr   device int32 [S + 1]: sequence s's new tokens are rows
+ *                tok_indptr[s] .. tok_indptr[s+1]-1, in order (none: the sequence is skipped)
+ *   kv_len       device int32 [S]: the sequence's length with its new tokens; they stand at
+ *                positions kv_len[s] - n .. kv_len[s] - 1 of the cache
+ *   block_table  device int32 [S][max_blocks][n_kv_heads][2]: the pages of the keys (0) and
+ *                the values (1) of each block and head.  Entries of blocks that a call does not
+ *                touch are not read (they may be -1).  Sequences may share pages that
+ *                are only read.
+ *
+ * slora_kv_append(): writes the new tokens' keys and values to the cache, rotating queries and keys by their
+ * positions on the way.  Scales: a block's exponent is the smallest e >= -40 for which every
+ * finite |value| of its new tokens is at most 448 * 2^e (127 * 2^e for INT8); if the block
+ * already holds tokens of the sequence (its first new token is not the block's first row), the larger of
+ * that and its present exponent, and if that grew, the rows before it are rescaled.  Codes are
+ * value * 2^-e rounded to nearest even; infinities become the largest code, NaN the format's
+ * NaN (INT8: 0).  The rotation and the codes are computed from fp32, each product and sum
+ * rounded once.  A page may be written for one sequence only within a call.
+ *   k, v         device fp16 [T][n_kv_heads][head_dim]; row t starts at t * k_stride
+ *                (v_stride) elements, so the three can be parts of one buffer
+ *   q, q_out     device fp16 [T][n_q_heads][head_dim] with strides alike, or both NULL: q_out
+ *                gets the rotated queries (q_out may be q); needs rope
+ *   rope         the rotation, or NULL for none:
+ *     rot_dim      channels rotated, a multiple of 16, 16 .. head_dim; the others are copied
+ *     interleaved  0: channel i turns with i + rot_dim/2;  1: channel 2i with 2i + 1
+ *     cos, sin     device float [n_positions][rot_dim / 2], 16-byte aligned
+ *     positions    device int32 [T], or NULL for the tokens' positions in the cache.  A
+ *                  position outside [0, n_positions) leaves that token unrotated and sets
+ *                  SLORA_DEV_BAD_POSITION.
+ *
+ * slora_kv_attend(): out = softmax(softmax_scale * q K^T) V of every new token over its
+ * sequence's cache, written to out; keys and values of the new tokens themselves must be in
+ * the cache already (append first).  Query heads are grouped: head j reads KV head
+ * j / (n_q_heads / n_kv_heads).
+ *   q, out       device fp16 [T][n_q_heads][head_dim], row strides as above; out is not q
+ *   lse          device float [T][n_q_heads], or NULL: natural log of the softmax's denominator
+ *   causal       1: the token at position p sees positions <= p;  0: the whole sequence
+ *   window       0, or with causal 1: it sees positions p - window + 1 .. p only
+ * A token that sees nothing gets zeros and lse -inf.  Cache rows that no query sees may hold
+ * anything (their codes are never used, and pages wholly outside are not read).  Scores, the softmax's maxima
+ * and sums and the output sums are fp32; the weights are rounded to fp16 once
+ * for the product with the values, the output once.  Results of one call are deterministic for
+ * given sizes; the order of the partial sums depends on the batch and the number of SMs.
+ * Attends of one cache share its workspace: issue them on one stream, or order the streams.
+ *
+ * Both: strides are multiples of 8 elements and at least a row; pointers 16-byte aligned.  Errors:
+ * SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is launched),
+ * SLORA_ERR_UNSUPPORTED (head_dim or a page too small).  On the device a bad page id
+ * (SLORA_DEV_BAD_PAGE: that block is not written, or not seen), a kv_len below the number of new
+ * tokens (append) or beyond the block table (SLORA_DEV_BAD_LENGTH) and a tok_indptr that decreases or leaves
+ * [0, T] (SLORA_DEV_BAD_SEGMENT) set the pool's status word and skip that work; an attend
+ * with kv_len < n sees no key for its first n - kv_len tokens.  Enqueued on `stream`; nothing waits or allocates.
+ * ------------------------------------------------------------------------- */
+typedef struct slora_kv *slora_kv_t;
+enum { SLORA_KV_E4M3 = 0, SLORA_KV_INT8 = 1 };
+typedef struct slora_kv_batch {
+    int32_t n_tokens;
+    int32_t n_seqs;
+    int32_t max_q;
+    int32_t max_blocks;
+    const int32_t *tok_indptr;
+    const int32_t *kv_len;
+    const int32_t *block_table;
+} slora_kv_batch;
+typedef struct slora_kv_rope {
+    int32_t rot_dim;
+    int32_t interleaved;
+    int32_t n_positions;
+    int32_t reserved; /* 0 */
+    const float *cos;
+    const float *sin;
+    const int32_t *positions;
+} slora_kv_rope;
+slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, int32_t head_dim, int32_t format,
+                             slora_kv_t *out);
+slora_status slora_kv_destroy(slora_kv_t kv);
+slora_status slora_kv_block_tokens(slora_kv_t kv, int32_t *out);
+slora_status slora_kv_exponents(slora_kv_t kv, int8_t **out);
+slora_status slora_kv_append(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *k, int64_t k_stride,
+                             const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                             int64_t q_out_stride, int32_t n_q_heads, const slora_kv_rope *rope /*host*/,
+                             slora_stream_t stream);
+slora_status slora_kv_attend(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *q, int64_t q_stride,
+                             int32_t n_q_heads, void *out, int64_t out_stride, float *lse, float softmax_scale,
+                             int32_t causal, int32_t window, slora_stream_t stream);
 
 /* ---------------------------------------------------------------------------
  * Observability / test hooks.

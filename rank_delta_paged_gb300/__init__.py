@@ -43,6 +43,9 @@ __all__ = [
     "slora_lru_pin", "slora_lru_unpin", "slora_lru_victims",
     "slora_adapters_acquire", "slora_adapters_release", "slora_pages_alloc_evict", "slora_pool_get_stats",
     "slora_bmm_workspace_bytes", "slora_lora_apply_bmm",
+    "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope",
+    "slora_kv_create", "slora_kv_destroy", "slora_kv_block_tokens", "slora_kv_exponents",
+    "slora_kv_append", "slora_kv_attend",
 ]
 
 _I32, _I64, _U64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -104,6 +107,12 @@ _SIGS = {
     "slora_pool_get_stats": [_P, _P],
     "slora_bmm_workspace_bytes": [_P, _I32, _P],
     "slora_lora_apply_bmm": [_P, _I32, _P, _P, _I32, _P, _P, _P, ctypes.c_size_t, _P],
+    "slora_kv_create": [_P, _I32, _I32, _I32, _PP],
+    "slora_kv_destroy": [_P],
+    "slora_kv_block_tokens": [_P, _P],
+    "slora_kv_exponents": [_P, _PP],
+    "slora_kv_append": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P],
+    "slora_kv_attend": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
 }
 _RESTYPE = {"slora_status_str": ctypes.c_char_p, "slora_last_error": ctypes.c_char_p,
             "slora_version": _I32}
@@ -414,6 +423,69 @@ def slora_lora_apply_bmm(pool: int, proj: int, x, y, T: int, token_adapter_idx, 
     """The padded batched-GEMM comparison path (see include/slora.h)."""
     _call("slora_lora_apply_bmm", pool, proj, _ptr(x), _ptr(y), T, _ptr(token_adapter_idx), _ptr(scaling),
           _ptr(workspace), int(workspace_bytes), _stream(stream))
+
+
+# ---- the 8-bit KV cache in the pool's pages -------------------------------------------
+SLORA_KV_E4M3 = 0
+SLORA_KV_INT8 = 1
+
+
+class KVBatch(ctypes.Structure):
+    """slora_kv_batch: the sequences of an iteration.  The device arrays are kept alive by it."""
+    _fields_ = [("n_tokens", _I32), ("n_seqs", _I32), ("max_q", _I32), ("max_blocks", _I32),
+                ("tok_indptr", _P), ("kv_len", _P), ("block_table", _P)]
+
+    def __init__(self, n_tokens: int, n_seqs: int, max_q: int, max_blocks: int, tok_indptr, kv_len, block_table):
+        super().__init__(n_tokens, n_seqs, max_q, max_blocks, _ptr(tok_indptr), _ptr(kv_len), _ptr(block_table))
+        self._keep = (tok_indptr, kv_len, block_table)
+        self.ref = ctypes.addressof(self)
+
+
+class KVRope(ctypes.Structure):
+    """slora_kv_rope: the position rotation of an append.  The device arrays are kept alive by it."""
+    _fields_ = [("rot_dim", _I32), ("interleaved", _I32), ("n_positions", _I32), ("reserved", _I32),
+                ("cos", _P), ("sin", _P), ("positions", _P)]
+
+    def __init__(self, rot_dim: int, interleaved: bool, n_positions: int, cos, sin, positions=None):
+        super().__init__(rot_dim, int(interleaved), n_positions, 0, _ptr(cos), _ptr(sin), _ptr(positions))
+        self._keep = (cos, sin, positions)
+        self.ref = ctypes.addressof(self)
+
+
+def slora_kv_create(pool: int, n_kv_heads: int, head_dim: int, format: int = SLORA_KV_E4M3) -> int:
+    h = ctypes.c_void_p()
+    _call("slora_kv_create", pool, n_kv_heads, head_dim, format, ctypes.byref(h))
+    return h.value
+
+
+def slora_kv_destroy(kv: int) -> None:
+    _call("slora_kv_destroy", kv)
+
+
+def slora_kv_block_tokens(kv: int) -> int:
+    v = ctypes.c_int32()
+    _call("slora_kv_block_tokens", kv, ctypes.byref(v))
+    return v.value
+
+
+def slora_kv_exponents(kv: int) -> int:
+    """Device address of the int8 exponents, one per page of the pool."""
+    v = ctypes.c_void_p()
+    _call("slora_kv_exponents", kv, ctypes.byref(v))
+    return v.value
+
+
+def slora_kv_append(kv: int, batch: KVBatch, k, k_stride: int, v, v_stride: int, q=None, q_stride: int = 0,
+                    q_out=None, q_out_stride: int = 0, n_q_heads: int = 0, rope: Optional[KVRope] = None,
+                    stream=None) -> None:
+    _call("slora_kv_append", kv, batch.ref, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride, _ptr(q_out),
+          q_out_stride, n_q_heads, None if rope is None else rope.ref, _stream(stream))
+
+
+def slora_kv_attend(kv: int, batch: KVBatch, q, q_stride: int, n_q_heads: int, out, out_stride: int, lse=None,
+                    softmax_scale: float = 1.0, causal: bool = True, window: int = 0, stream=None) -> None:
+    _call("slora_kv_attend", kv, batch.ref, _ptr(q), q_stride, n_q_heads, _ptr(out), out_stride, _ptr(lse),
+          softmax_scale, int(causal), window, _stream(stream))
 
 
 def slora_adapter_pages(pool: int, adapter_id: int, proj: int, out) -> None:

@@ -1,0 +1,185 @@
+// The 8-bit KV cache in the pool's pages: what its kernels read about the cache and a batch,
+// the conversions between fp32 / fp16 and the 8-bit codes, and the kernel launchers.
+#pragma once
+
+#include <cstdint>
+
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include "slora.h"
+
+namespace slora {
+namespace kv {
+
+// Smallest exponent of a block's scale: 2^-40 is below the smallest fp16 subnormal over
+// the largest code (2^-24 / 448), rotated values included, so it never costs precision, and
+// a block of zeros starts there and can grow.
+constexpr int kMinExponent = -40;
+
+// Exponents beyond this are read as this; append writes -40 .. 11.  The softmax's sum carries
+// 2^-exponent of the value blocks, which must stay a normal fp32 number, and so must the
+// ratio of two scales.
+constexpr int kExpLimit = 60;
+
+struct Cache {
+    uint8_t *pool;          // page p starts at pool + p * page_bytes
+    int8_t *exps;           // [num_pages]
+    int64_t num_pages;
+    int64_t page_bytes;
+    int32_t n_kv;           // KV heads
+    int32_t bt;             // tokens per block (page)
+    int32_t *status;        // the pool's device status word
+};
+
+struct Batch {
+    int32_t T, S, max_q, max_blocks;
+    const int32_t *indptr;
+    const int32_t *kv_len;
+    const int32_t *table;   // [S][max_blocks][n_kv][2]
+};
+
+struct AppendArgs {
+    Cache c;
+    Batch b;
+    const __half *k, *v, *q;
+    __half *q_out;
+    int64_t k_stride, v_stride, q_stride, q_out_stride;
+    int32_t n_q;
+    int32_t rot, interleaved, n_pos;    // rot 0: no rotation
+    const float *cos, *sin;
+    const int32_t *positions;           // nullptr: positions in the cache
+};
+
+struct AttendArgs {
+    Cache c;
+    Batch b;
+    const __half *q;
+    __half *out;
+    float *lse;
+    int64_t q_stride, out_stride;
+    int32_t n_q, group;
+    float scale_log2;                   // softmax scale * log2(e)
+    int32_t causal, window;
+};
+
+// One sequence of a batch as the attention kernels see it: its new rows, its keys, and
+// whether its sizes can be used.
+struct Seq {
+    int32_t row0;   // first row of q / out
+    int32_t n;      // new tokens (0: skip)
+    int32_t len;    // keys
+};
+
+__device__ __forceinline__ Seq load_seq(const AttendArgs &a, int32_t s, int32_t *bad)
+{
+    Seq q;
+    const int32_t t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1];
+    q.row0 = t0;
+    q.n = t1 - t0;
+    q.len = a.b.kv_len[s];
+    if (t0 < 0 || t1 < t0 || t1 > a.b.T || q.n > a.b.max_q) {
+        *bad = SLORA_DEV_BAD_SEGMENT;
+        q.n = 0;
+    } else if (q.len < 0 || (int64_t)q.len > (int64_t)a.b.max_blocks * a.c.bt) {
+        *bad = SLORA_DEV_BAD_LENGTH;
+        q.n = 0;
+    }
+    return q;
+}
+
+// First key that any of the rows [r0, r1) of new tokens sees, and one past the last; tokens
+// counted from the sequence's first new one.
+__device__ __forceinline__ int32_t first_key(const AttendArgs &a, const Seq &q, int32_t tok)
+{
+    if (a.window == 0) return 0;
+    const int64_t p = (int64_t)q.len - q.n + tok - a.window + 1;
+    return p > 0 ? (int32_t)p : 0;
+}
+__device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, int32_t tok)
+{
+    if (!a.causal) return q.len;
+    const int32_t p = q.len - q.n + tok + 1;
+    return p > 0 ? p : 0;
+}
+
+// ---- codes ---------------------------------------------------------------------------
+template <int FMT>
+__device__ __forceinline__ constexpr float code_limit()
+{
+    return FMT == SLORA_KV_E4M3 ? 448.f : 127.f;
+}
+
+// Smallest e >= kMinExponent with amax <= limit * 2^e, amax finite and >= 0: compares the
+// significands, limit = 1.75 * 2^8 (E4M3) or 1.984375 * 2^6 (INT8).
+template <int FMT>
+__device__ __forceinline__ int fit_exponent(float amax)
+{
+    const uint32_t u = __float_as_uint(amax);
+    const int x = (int)(u >> 23) - 127;
+    const uint32_t top = FMT == SLORA_KV_E4M3 ? 0x600000u : 0x7E0000u;
+    const int e = x - (FMT == SLORA_KV_E4M3 ? 8 : 6) + ((u & 0x7FFFFFu) > top);
+    return e < kMinExponent ? kMinExponent : e;
+}
+
+// An exponent as read from memory that the caller may have written.
+__device__ __forceinline__ int clamp_exponent(int e)
+{
+    return e < -kExpLimit ? -kExpLimit : e > kExpLimit ? kExpLimit : e;
+}
+
+// 2^e, -126 <= e <= 127.
+__device__ __forceinline__ float pow2(int e)
+{
+    return __uint_as_float((uint32_t)(e + 127) << 23);
+}
+
+// Two values in units of the scale -> two codes (x in the low byte).
+template <int FMT>
+__device__ __forceinline__ uint32_t encode2(float x, float y)
+{
+    if (FMT == SLORA_KV_E4M3) {
+        uint16_t r;
+        asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
+        return r;
+    }
+    const int a = x != x ? 0 : __float2int_rn(fminf(fmaxf(x, -127.f), 127.f));
+    const int b = y != y ? 0 : __float2int_rn(fminf(fmaxf(y, -127.f), 127.f));
+    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8;
+}
+
+// Four codes -> fp16 pairs (bytes 0, 1) and (bytes 2, 3); exact in both formats.
+template <int FMT>
+__device__ __forceinline__ void decode4(uint32_t w, uint32_t &lo, uint32_t &hi)
+{
+    if (FMT == SLORA_KV_E4M3) {
+        asm("{\n\t.reg .b16 l, h;\n\tmov.b32 {l, h}, %2;\n\t"
+            "cvt.rn.f16x2.e4m3x2 %0, l;\n\tcvt.rn.f16x2.e4m3x2 %1, h;\n\t}"
+            : "=r"(lo), "=r"(hi)
+            : "r"(w));
+    } else {
+        // byte b + 128 in the low bits of the fp16 number 1024 is 1024 + 128 + b
+        const uint32_t u = w ^ 0x80808080u;
+        const __half2 off = __float2half2_rn(1152.f);
+        uint32_t p = __byte_perm(u, 0x64646464u, 0x4140), q = __byte_perm(u, 0x64646464u, 0x4342);
+        __half2 a = __hsub2(*reinterpret_cast<__half2 *>(&p), off);
+        __half2 b = __hsub2(*reinterpret_cast<__half2 *>(&q), off);
+        lo = *reinterpret_cast<uint32_t *>(&a);
+        hi = *reinterpret_cast<uint32_t *>(&b);
+    }
+}
+
+// ---- launchers -------------------------------------------------------------------------
+cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream,
+                          int *launches);
+
+// The attention's workspace: partial results of rows whose keys are split over several
+// CTAs, and one arrival counter per CTA (zero between calls).
+size_t decode_workspace_bytes(int num_sms);
+// The rows of sequences with at most small_rows (new tokens * group) rows per KV head; INT32_MAX: all.
+cudaError_t launch_attend_decode(const AttendArgs &a, const CUtensorMap &map, int box_rows, int head_dim, int fmt,
+                                 int32_t small_rows, void *ws, int num_sms, cudaStream_t stream, int *launches);
+
+}  // namespace kv
+}  // namespace slora

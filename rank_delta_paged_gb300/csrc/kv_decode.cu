@@ -1,0 +1,764 @@
+// Attention over the 8-bit paged KV cache for few rows per KV head: single tokens, drafted
+// tokens, and every row that has no larger tile to fill.
+//
+// For a row (new token t, query head j) with keys k_i = c_i 2^e, values v_i = d_i 2^f (codes
+// c, d; exponents e, f of the key's pages):
+//     s_i = q . c_i * 2^e * scale * log2(e)        m = max_i (s_i + f)
+//     w_i = 2^(s_i + f - m)                        out = sum_i w_i d_i / sum_i w_i 2^-f
+// The exponent of the value page goes into the weight, so that values enter the product as
+// plain codes, exact in fp16, and the weights of all pages share one scale; the sum of the
+// softmax takes it out again in fp32.
+//
+// What bounds it: the codes of the keys and values, each read once per KV head for all of its
+// group * n rows: 2 * head_dim bytes per token and head against a few hundred flops.  So the
+// work is cut into tiles of 64 tokens of one (sequence, KV head, group of 8 or 16 rows), all
+// tiles of the batch form one list, and every CTA takes an equal run of it: the memory system
+// sees the same load from every SM whatever the lengths.  A unit whose tiles fall into several
+// CTAs is joined by the last of them to finish, in the order of the list.
+//
+// Per CTA: one producer warp keeps a ring of tiles in flight by tensor-map copies (boxes of 16
+// rows, so a sequence's last page is not read past its last 16 tokens; the copy engine's swizzle spreads the rows
+// over the banks) and four consumer warps take 16 tokens of each tile: S^T = K Q^T and
+// O^T = V^T P^T with mma.sync m16n8k16, the tokens or the channels as the 16 rows and the
+// query rows as the 8 columns, so that a single row wastes 7 columns of a product that is far
+// from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers, two or one
+// instruction per pair.
+#include <mutex>
+
+#include "host_common.h"
+#include "internal.h"
+#include "kv.h"
+#include "ptx.h"
+
+namespace slora {
+namespace kv {
+namespace {
+
+constexpr int kTile = 64;                       // tokens per tile
+constexpr int kConsumers = 4;                   // warps, 16 tokens of a tile each
+constexpr int kThreads = 32 * (kConsumers + 1);
+constexpr int kCtasPerSm = 2;
+constexpr int kSeqChunks = 64;                  // partial sums of the tile counts
+constexpr int kMaxRows = 16;
+constexpr int kPartStride = 2 * kMaxRows + kMaxRows * 128;   // floats of one partial result: m, l, O
+
+struct Meta {
+    float ks[8];       // 2^exponent of the key pages, per 8 tokens of the tile
+    float lv[8];       // exponent of the value pages
+    float li[8];       // 2^-exponent of the value pages
+    uint32_t ok;       // bit g: tokens 8g .. 8g+7 of the tile were loaded
+    int32_t plain;     // every token of the tile is seen by every row
+    int32_t first, last;   // first / last tile of the unit within this CTA
+    int32_t whole;     // the unit lies within this CTA
+    int32_t j0;        // first token
+    int32_t row0, n, len;  // the sequence
+    int32_t head;      // KV head
+    int32_t r0;        // first row (token * group + head within the group)
+    int32_t c0, c1;    // first and last CTA of the unit
+    int32_t pad[3];
+};
+static_assert(sizeof(Meta) % 16 == 0, "Meta");
+
+template <int D, int NT>
+struct Shape {
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 5 : 4) : (NT == 1 ? 10 : 8);
+    static constexpr int kHalf = kTile * D;                  // bytes of a tile's keys
+    static constexpr int kStage = 2 * kHalf;
+    static constexpr int kMergeFloats = kConsumers * 8 * NT * (D + 2);
+    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStages * sizeof(Meta) + kMergeFloats * 4 + 256;
+};
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1)
+{
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+                 "{%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v)
+{
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int32_t c0, int32_t c1, int32_t c2,
+                                            uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                 "%3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+                 : "memory");
+}
+
+// Which token (of 8) is row m of an S^T tile.  The copy engine's swizzle moves 16-byte chunk
+// c of row t to chunk c ^ (t & 7) (128-byte rows) or c ^ (t >> 1 & 3) (64-byte rows).  Both the
+// reads of the keys (lanes 4m .. 4m+3 read chunks 0..3 of row m) and of the values (lane 4g + c
+// reads chunk g of rows 2c and 2c+1) touch every bank once if rows 2i and 2i+1 differ in the
+// half of the 128 bytes that their chunks 0..3 fall into and rows 0, 2, 4, 6 (1, 3, 5, 7)
+// have four different pairs of chunks.
+template <int D>
+__device__ __forceinline__ int token_of_row(int m)
+{
+    if (D == 128) return m ^ ((m & 1) << 2);
+    const int i = m >> 1;
+    return ((i & 1) | (i & 2) << 1) ^ (m & 1 ? 3 : 0);
+}
+
+struct DecodeParams {
+    AttendArgs a;
+    int32_t box_rows, small_rows;
+    int32_t rows;          // rows per unit: 8 * NT
+    int32_t min_tiles;     // a CTA's run is at least this long
+    float *part;           // [CTAs][2] partial results
+    int32_t *count;        // [CTAs] arrivals at units that start in the CTA, zero between calls
+};
+
+// Tiles of sequence s: tiles per unit, units per KV head.
+__device__ __forceinline__ void seq_tiles(const DecodeParams &p, const Seq &q, int32_t *tiles, int32_t *groups,
+                                          int32_t *first)
+{
+    *tiles = 0;
+    *groups = 0;
+    *first = 0;
+    const int64_t rows = (int64_t)q.n * p.a.group;
+    if (q.n == 0 || rows > p.small_rows) return;
+    const int32_t lo = first_key(p.a, q, 0) / kTile, hi = (end_key(p.a, q, q.n - 1) + kTile - 1) / kTile;
+    *tiles = hi > lo ? hi - lo : 1;     // a row that sees nothing still writes zeros
+    *groups = (int32_t)((rows + p.rows - 1) / p.rows);
+    *first = lo;
+}
+
+template <int D, int NT, int FMT>
+__global__ void __launch_bounds__(kThreads, kCtasPerSm)
+attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map)
+{
+    using Sh = Shape<D, NT>;
+    constexpr int NS = Sh::kStages;
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
+    Meta *meta = reinterpret_cast<Meta *>(ring + (size_t)NS * Sh::kStage);
+    float *merge = reinterpret_cast<float *>(meta + NS);
+    __shared__ uint64_t s_full[NS], s_empty[NS], s_merge[3];
+    __shared__ int64_t s_sum[kSeqChunks];
+    __shared__ int s_abort, s_last;
+
+    const AttendArgs &a = p.a;
+    int32_t *status = a.c.status;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < NS; ++i) {
+            mbar_init(&s_full[i], 1);
+            mbar_init(&s_empty[i], kConsumers);
+        }
+        mbar_init(&s_merge[0], kConsumers);
+        mbar_init(&s_merge[1], kConsumers);
+        mbar_init(&s_merge[2], 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Tiles of each run of `per` sequences; every CTA sums them for itself, which costs less
+    // than a launch.
+    const int S = a.b.S;
+    const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
+    int32_t bad = 0;
+    for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
+        int64_t t = 0;
+        for (int64_t s = (int64_t)c * per + lane; s < S && s < (int64_t)(c + 1) * per; s += 32) {
+            int32_t tiles, groups, first;
+            seq_tiles(p, load_seq(a, (int32_t)s, &bad), &tiles, &groups, &first);
+            t += (int64_t)tiles * groups;
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+        if (lane == 0) s_sum[c] = t * a.c.n_kv;
+    }
+    if (bad && blockIdx.x == 0) set_status(status, bad);
+    __syncthreads();
+    // This CTA's run [w0, w1) of the W tiles.
+    int64_t v0 = s_sum[2 * lane], v1 = s_sum[2 * lane + 1], W = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(~0u, W, o);
+        if (lane >= o) W += u;
+    }
+    const int64_t before = W - v0 - v1;          // tiles before chunk 2 * lane
+    W = __shfl_sync(~0u, W, 31);
+    int64_t run = (W + gridDim.x - 1) / gridDim.x;
+    if (run < p.min_tiles) run = p.min_tiles;
+    const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
+    if (w0 >= w1) return;
+    volatile int *abort = &s_abort;
+
+    if (warp == kConsumers) {
+        // ---- producer ------------------------------------------------------------------
+        // the sequence that holds tile w0: its chunk, then 32 sequences at a time
+        const unsigned hit = __ballot_sync(~0u, before <= w0);
+        const int at = 31 - __clz(hit);
+        int chunk = 2 * at;
+        int64_t base = __shfl_sync(~0u, before, at);
+        const int64_t half = __shfl_sync(~0u, v0, at);
+        if (base + half <= w0) {
+            base += half;
+            ++chunk;
+        }
+        int32_t s32 = chunk * per;               // first of the 32 sequences that the lanes hold
+        Seq q;
+        int32_t tiles, groups, first;
+        auto hold = [&](int32_t s) {
+            q.n = 0;
+            tiles = groups = first = 0;
+            int32_t ignore;
+            if (s + lane < S) {
+                q = load_seq(a, s + lane, &ignore);
+                seq_tiles(p, q, &tiles, &groups, &first);
+            }
+        };
+        hold(s32);
+        int at_lane = 0;
+        for (;; hold(s32 += 32)) {
+            if (s32 >= S) {       // the lengths changed under the call: nothing to copy
+                if (lane == 0) {
+                    set_status(status, SLORA_DEV_BAD_LENGTH);
+                    s_abort = 1;
+                }
+                return;
+            }
+            int64_t mine = (int64_t)tiles * groups * a.c.n_kv, sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int64_t u = __shfl_up_sync(~0u, sum, o);
+                if (lane >= o) sum += u;
+            }
+            const unsigned past = __ballot_sync(~0u, base + sum > w0);
+            if (past) {
+                at_lane = __ffs(past) - 1;
+                base += __shfl_sync(~0u, sum - mine, at_lane);
+                break;
+            }
+            base += __shfl_sync(~0u, sum, 31);
+        }
+        // position in the list: sequence, KV head, row group, tile
+        int32_t u_tiles = __shfl_sync(~0u, tiles, at_lane), u_groups = __shfl_sync(~0u, groups, at_lane);
+        int32_t u_first = __shfl_sync(~0u, first, at_lane);
+        int64_t in_seq = w0 - base;
+        int32_t head = (int32_t)(in_seq / ((int64_t)u_tiles * u_groups));
+        in_seq -= (int64_t)head * u_tiles * u_groups;
+        int32_t grp = (int32_t)(in_seq / u_tiles), tile = (int32_t)(in_seq - (int64_t)grp * u_tiles);
+        Seq u;
+        u.row0 = __shfl_sync(~0u, q.row0, at_lane);
+        u.n = __shfl_sync(~0u, q.n, at_lane);
+        u.len = __shfl_sync(~0u, q.len, at_lane);
+
+        const int R = p.box_rows, boxes = kTile / R;
+        const int gl = lane >> 1, kvl = lane & 1;      // this lane's box of a tile, and keys or values
+        const bool mover = lane < 2 * boxes;
+        int64_t w = w0;
+        // Page of this lane's box, one tile ahead of its use.
+        auto fetch = [&](int32_t s, int32_t hd, int32_t j0, const Seq &sq, int32_t *row) {
+            int32_t page = -1;
+            const int32_t j = j0 + gl * R;
+            const int32_t lo = first_key(a, sq, 0), hi = end_key(a, sq, sq.n - 1);
+            if (mover && j < hi && j + R > lo) {
+                const int32_t blk = j / a.c.bt;
+                *row = j - blk * a.c.bt;
+                page = a.b.table[(((int64_t)s * a.b.max_blocks + blk) * a.c.n_kv + hd) * 2 + kvl];
+                if (page < 0 || page >= a.c.num_pages) {
+                    set_status(status, SLORA_DEV_BAD_PAGE);
+                    page = -1;
+                }
+            }
+            return page;
+        };
+        int32_t row = 0, page = fetch(s32 + at_lane, head, (u_first + tile) * kTile, u, &row);
+        int stage = 0;
+        uint32_t parity = 1;
+        for (; w < w1; ++w) {
+            // the tile that this iteration issues
+            Meta m;
+            m.first = w == w0 || tile == 0;
+            m.last = w == w1 - 1 || tile == u_tiles - 1;
+            const int64_t u0 = w - tile, u1 = u0 + u_tiles;
+            m.whole = u0 >= w0 && u1 <= w1;
+            m.c0 = m.c1 = 0;
+            if (!m.whole) {
+                m.c0 = (int32_t)(u0 / run);
+                m.c1 = (int32_t)((u1 - 1) / run);
+            }
+            m.j0 = (u_first + tile) * kTile;
+            m.row0 = u.row0;
+            m.n = u.n;
+            m.len = u.len;
+            m.head = head;
+            m.r0 = grp * p.rows;
+            const int32_t rows = u.n * a.group, tok0 = m.r0 / a.group;
+            const int32_t r1 = m.r0 + p.rows < rows ? m.r0 + p.rows : rows, tok1 = (r1 - 1) / a.group;
+            const int32_t exponent = page >= 0 ? clamp_exponent(a.c.exps[page]) : 0;
+            const int32_t my_page = page, my_row = row;
+            const unsigned got = __ballot_sync(~0u, my_page >= 0);
+            // a box needs both its keys and its values
+            uint32_t ok = 0;
+            for (int g = 0; g < boxes; ++g)
+                if ((got >> (2 * g) & 3u) == 3u) ok |= ((1u << (R / 8)) - 1u) << (g * (R / 8));
+            m.ok = ok;
+            m.plain = ok == 0xFFu && m.j0 >= first_key(a, u, tok1) && m.j0 + kTile <= end_key(a, u, tok0);
+            // step to the next tile and start reading its page
+            if (++tile == u_tiles) {
+                tile = 0;
+                if (++grp == u_groups) {
+                    grp = 0;
+                    if (++head == a.c.n_kv) {
+                        head = 0;
+                        if (w + 1 < w1) {
+                            unsigned next;
+                            while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
+                                s32 += 32;
+                                at_lane = -1;
+                                hold(s32);
+                            }
+                            if (next == 0) {      // the lengths changed under the call
+                                if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
+                                break;
+                            }
+                            at_lane = __ffs(next) - 1;
+                            u_tiles = __shfl_sync(~0u, tiles, at_lane);
+                            u_groups = __shfl_sync(~0u, groups, at_lane);
+                            u_first = __shfl_sync(~0u, first, at_lane);
+                            u.row0 = __shfl_sync(~0u, q.row0, at_lane);
+                            u.n = __shfl_sync(~0u, q.n, at_lane);
+                            u.len = __shfl_sync(~0u, q.len, at_lane);
+                        }
+                    }
+                }
+            }
+            if (w + 1 < w1) page = fetch(s32 + at_lane, head, (u_first + tile) * kTile, u, &row);
+
+            wait_phase<false>(&s_empty[stage], parity, abort, status);
+            if (*abort) break;
+            uint8_t *dst = ring + (size_t)stage * Sh::kStage;
+            Meta *ms = &meta[stage];
+            const bool both = (got >> (lane & ~1) & 3u) == 3u;
+            if (my_page >= 0 && both)
+                tma_load_3d(smem_u32(dst) + kvl * Sh::kHalf + gl * R * D, &map, 0, my_row, my_page, &s_full[stage]);
+            if (mover) {
+                const int32_t e = my_page >= 0 && both ? exponent : 0;
+                for (int i = 0; i < R / 8; ++i) {
+                    const int g = gl * (R / 8) + i;
+                    if (kvl == 0) {
+                        ms->ks[g] = pow2(e);
+                    } else {
+                        ms->lv[g] = (float)e;
+                        ms->li[g] = pow2(-e);
+                    }
+                }
+            }
+            if (lane == 0) {
+                ms->ok = m.ok;
+                ms->plain = m.plain;
+                ms->first = m.first;
+                ms->last = m.last;
+                ms->whole = m.whole;
+                ms->j0 = m.j0;
+                ms->row0 = m.row0;
+                ms->n = m.n;
+                ms->len = m.len;
+                ms->head = m.head;
+                ms->r0 = m.r0;
+                ms->c0 = m.c0;
+                ms->c1 = m.c1;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(ok) * 16u * D);
+            if (++stage == NS) {
+                stage = 0;
+                parity ^= 1;
+            }
+        }
+        // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
+        const int64_t issued = w - w0;
+        for (int i = 0; i < NS && i < issued; ++i) {
+            const int64_t t = issued - 1 - i;
+            if (!mbar_wait_bounded(&s_full[t % NS], (uint32_t)(t / NS & 1), status)) break;
+        }
+        return;
+    }
+
+    // ---- consumers ---------------------------------------------------------------------
+    const int g = lane >> 2, c = lane & 3;
+    const int krow[2] = {token_of_row<D>(g), token_of_row<D>(g) + 8};
+    // the tokens of this lane's two rows of V^T P^T's inner index, in both halves of the 16
+    const int vrow[4] = {token_of_row<D>(2 * c), token_of_row<D>(2 * c + 1), token_of_row<D>(2 * c) + 8,
+                         token_of_row<D>(2 * c + 1) + 8};
+    constexpr int KS = D / 16;          // k steps of S^T, and 16-row tiles of O^T
+    float o[NT][KS][4], mx[NT][2], sum[NT][2];
+    uint32_t qf[NT][KS][2];
+    int stage = 0;
+    uint32_t parity = 0, mparity = 0, jparity = 0;
+
+    for (int64_t w = w0; w < w1; ++w) {
+        wait_phase<false>(&s_full[stage], parity, abort, status);
+        if (*abort) break;
+        const Meta &m = meta[stage];
+        const uint32_t kbase = smem_u32(ring + (size_t)stage * Sh::kStage) + warp * 16 * D;
+        const uint32_t vbase = kbase + Sh::kHalf;
+        const int32_t nrows = m.n * a.group - m.r0;       // rows of this unit
+        if (m.first) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t) {
+                mx[t][0] = mx[t][1] = -INFINITY;
+                sum[t][0] = sum[t][1] = 0.f;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
+                const int r = 8 * t + g;
+                const bool live = r < nrows;
+                const int tok = (m.r0 + r) / a.group, hd = (m.r0 + r) - tok * a.group;
+                const __half *src = a.q + (int64_t)(m.row0 + tok) * a.q_stride + ((int64_t)m.head * a.group + hd) * D;
+#pragma unroll
+                for (int i = 0; i < KS; ++i) {
+                    // k step i holds this lane's channels 4 (i & 3) .. + 3 of chunk c + 4 (i >> 2)
+                    uint2 v = make_uint2(0, 0);
+                    if (live) v = *reinterpret_cast<const uint2 *>(src + (c + 4 * (i >> 2)) * 16 + 4 * (i & 3));
+                    qf[t][i][0] = v.x;
+                    qf[t][i][1] = v.y;
+                }
+            }
+        }
+        // S^T: this warp's 16 tokens x the rows
+        float sc[NT][4];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+#pragma unroll
+        for (int h = 0; h < D / 64; ++h) {
+            uint4 kw[2];
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                const int tok = krow[x];
+                const int chunk = D == 128 ? (c + 4 * h) ^ (tok & 7) : c ^ (tok >> 1 & 3);
+                const uint32_t ad = kbase + tok * D + chunk * 16;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(kw[x].x), "=r"(kw[x].y), "=r"(kw[x].z), "=r"(kw[x].w)
+                             : "r"(ad));
+            }
+            const uint32_t wa[4] = {kw[0].x, kw[0].y, kw[0].z, kw[0].w}, wb[4] = {kw[1].x, kw[1].y, kw[1].z, kw[1].w};
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                uint32_t a0, a1, a2, a3;
+                decode4<FMT>(wa[j], a0, a2);
+                decode4<FMT>(wb[j], a1, a3);
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma16816(sc[t], a0, a1, a2, a3, qf[t][4 * h + j][0], qf[t][4 * h + j][1]);
+            }
+        }
+        const float f0 = m.ks[2 * warp] * a.scale_log2, f1 = m.ks[2 * warp + 1] * a.scale_log2;
+        const float lv0 = m.lv[2 * warp], lv1 = m.lv[2 * warp + 1];
+        const bool plain = m.plain != 0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            sc[t][0] = fmaf(sc[t][0], f0, lv0);
+            sc[t][1] = fmaf(sc[t][1], f0, lv0);
+            sc[t][2] = fmaf(sc[t][2], f1, lv1);
+            sc[t][3] = fmaf(sc[t][3], f1, lv1);
+        }
+        if (!plain) {
+            Seq q;
+            q.row0 = m.row0;
+            q.n = m.n;
+            q.len = m.len;
+            const bool ok0 = m.ok >> (2 * warp) & 1, ok1 = m.ok >> (2 * warp + 1) & 1;
+            const int j0 = m.j0 + warp * 16 + krow[0], j1 = j0 + 8;
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    const int r = 8 * t + 2 * c + x;
+                    const int tok = (m.r0 + (r < nrows ? r : 0)) / a.group;
+                    const int lo = first_key(a, q, tok), hi = end_key(a, q, tok);
+                    if (!(ok0 && j0 >= lo && j0 < hi)) sc[t][x] = -INFINITY;
+                    if (!(ok1 && j1 >= lo && j1 < hi)) sc[t][2 + x] = -INFINITY;
+                }
+        }
+        // A row's maximum is taken up only when a score passes it by 2^8 (the first one always does):
+        // the weights stay below 2^8, far inside fp16, and the rescaling of O is rare.
+        bool up = false;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x)
+                up |= fmaxf(sc[t][x], sc[t][2 + x]) > mx[t][x] + 8.f;
+        if (__any_sync(~0u, up)) {
+#pragma unroll
+            for (int t = 0; t < NT; ++t)
+#pragma unroll
+                for (int x = 0; x < 2; ++x) {
+                    float v = fmaxf(sc[t][x], sc[t][2 + x]);
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
+                    v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
+                    v = fmaxf(v, mx[t][x]);
+                    const float k = mx[t][x] == -INFINITY ? 0.f : ex2(mx[t][x] - v);
+                    mx[t][x] = v;
+                    sum[t][x] *= k;
+#pragma unroll
+                    for (int i = 0; i < KS; ++i) {
+                        o[t][i][x] *= k;
+                        o[t][i][2 + x] *= k;
+                    }
+                }
+        }
+        uint32_t pf[NT][2];
+        const float li0 = m.li[2 * warp], li1 = m.li[2 * warp + 1];
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const float b0 = mx[t][0] == -INFINITY ? 0.f : mx[t][0], b1 = mx[t][1] == -INFINITY ? 0.f : mx[t][1];
+            const float p0 = ex2(sc[t][0] - b0), p1 = ex2(sc[t][1] - b1);
+            const float p2 = ex2(sc[t][2] - b0), p3 = ex2(sc[t][3] - b1);
+            sum[t][0] += p0 * li0 + p2 * li1;
+            sum[t][1] += p1 * li0 + p3 * li1;
+            __half2 h0 = __floats2half2_rn(p0, p1), h1 = __floats2half2_rn(p2, p3);
+            pf[t][0] = transpose8x8(*reinterpret_cast<uint32_t *>(&h0));
+            pf[t][1] = transpose8x8(*reinterpret_cast<uint32_t *>(&h1));
+        }
+        // O^T += V^T P^T
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int tok = vrow[x];
+            if (D == 128) {
+                const uint32_t ad = vbase + tok * D + (g ^ (tok & 7)) * 16;
+                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(vw[x][0]), "=r"(vw[x][1]), "=r"(vw[x][D / 32 - 2]), "=r"(vw[x][D / 32 - 1])
+                             : "r"(ad));
+            } else {
+                const uint32_t ad = vbase + tok * D + ((g >> 1) ^ (tok >> 1 & 3)) * 16 + (g & 1) * 8;
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(vw[x][0]), "=r"(vw[x][1]) : "r"(ad));
+            }
+        }
+        if (!plain) {
+            // weights of unseen tokens are zero, but their codes may be NaN
+            Seq q;
+            q.row0 = m.row0;
+            q.n = m.n;
+            q.len = m.len;
+            const int lo = first_key(a, q, 0), hi = end_key(a, q, m.n - 1);
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                const int j = m.j0 + warp * 16 + vrow[x];
+                const bool ok = (m.ok >> (2 * warp + (x >> 1)) & 1) && j >= lo && j < hi;
+#pragma unroll
+                for (int i = 0; i < D / 32; ++i) vw[x][i] = ok ? vw[x][i] : 0u;
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < D / 32; ++i) {
+            uint32_t a0[2], a1[2], a2[2], a3[2];
+            // channels 4i, 4i+1 then 4i+2, 4i+3 of this lane's run, token pairs in one register
+            decode4<FMT>(__byte_perm(vw[0][i], vw[1][i], 0x5140), a0[0], a1[0]);
+            decode4<FMT>(__byte_perm(vw[0][i], vw[1][i], 0x7362), a0[1], a1[1]);
+            decode4<FMT>(__byte_perm(vw[2][i], vw[3][i], 0x5140), a2[0], a3[0]);
+            decode4<FMT>(__byte_perm(vw[2][i], vw[3][i], 0x7362), a2[1], a3[1]);
+#pragma unroll
+            for (int y = 0; y < 2; ++y)
+#pragma unroll
+                for (int t = 0; t < NT; ++t)
+                    mma16816(o[t][2 * i + y], a0[y], a1[y], a2[y], a3[y], pf[t][0], pf[t][1]);
+        }
+        const bool last = m.last != 0;
+        const bool whole = m.whole != 0;
+        const int32_t row0 = m.row0, head = m.head, r0 = m.r0, c0 = m.c0, c1 = m.c1;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_empty[stage]);
+        if (++stage == NS) {
+            stage = 0;
+            parity ^= 1;
+        }
+        if (!last) continue;
+
+        // ---- the unit's end: the four warps' results become one --------------------------
+        const int live = nrows < 8 * NT ? nrows : 8 * NT;
+        float *mm = merge, *ml = merge + kConsumers * 8 * NT, *mo = merge + 2 * kConsumers * 8 * NT;
+#pragma unroll
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 2; ++x) {
+                float l = sum[t][x];
+                l += __shfl_xor_sync(~0u, l, 4);
+                l += __shfl_xor_sync(~0u, l, 8);
+                l += __shfl_xor_sync(~0u, l, 16);
+                const int r = 8 * t + 2 * c + x;
+                if (r < live) {
+                    if (g == 0) {
+                        mm[warp * 8 * NT + r] = mx[t][x];
+                        ml[warp * 8 * NT + r] = l;
+                    }
+                    // accumulators x, 2 + x: channels 2i, 2i + 1 of this lane's D / 8
+#pragma unroll
+                    for (int i = 0; i < KS; ++i)
+                        *reinterpret_cast<float2 *>(&mo[(warp * 8 * NT + r) * D + g * (D / 8) + 2 * i]) =
+                            make_float2(o[t][i][x], o[t][i][2 + x]);
+                }
+            }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_merge[0]);
+        wait_phase<false>(&s_merge[0], mparity, abort, status);
+        if (*abort) break;
+        float *part = p.part + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kPartStride;
+        auto emit = [&](int r, int d, float2 v, float M, float L) {
+            const int tok = (r0 + r) / a.group, hd = (r0 + r) - tok * a.group;
+            const int64_t qh = (int64_t)head * a.group + hd;
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            __half2 h = __floats2half2_rn(v.x * inv, v.y * inv);
+            *reinterpret_cast<__half2 *>(a.out + (int64_t)(row0 + tok) * a.out_stride + qh * D + d) = h;
+            if (a.lse && d == 0)
+                a.lse[(int64_t)(row0 + tok) * a.n_q + qh] =
+                    L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+        };
+        for (int i = tid; i < live * (D / 2); i += 32 * kConsumers) {
+            const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
+            float M = -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kConsumers; ++k) M = fmaxf(M, mm[k * 8 * NT + r]);
+            const float B = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            float2 v = make_float2(0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kConsumers; ++k) {
+                const float e = ex2(mm[k * 8 * NT + r] - B);
+                const float2 x = *reinterpret_cast<const float2 *>(&mo[(k * 8 * NT + r) * D + d]);
+                L += ml[k * 8 * NT + r] * e;
+                v.x = fmaf(x.x, e, v.x);
+                v.y = fmaf(x.y, e, v.y);
+            }
+            if (whole) {
+                emit(r, d, v, M, L);
+            } else {
+                __stcg(reinterpret_cast<float2 *>(part + 2 * kMaxRows + r * D + d), v);
+                if (d == 0) {
+                    __stcg(part + r, M);
+                    __stcg(part + kMaxRows + r, L);
+                }
+            }
+        }
+        if (!whole) {
+            // the last CTA of the unit to arrive joins the parts in the order of the list
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_merge[1]);
+            wait_phase<false>(&s_merge[1], mparity, abort, status);
+            if (*abort) break;
+            if (tid == 0) {
+                __threadfence();
+                s_last = atomicAdd(&p.count[c0], 1) == c1 - c0;
+                if (s_last) p.count[c0] = 0;
+                __threadfence();
+                mbar_arrive(&s_merge[2]);
+            }
+            wait_phase<false>(&s_merge[2], jparity, abort, status);
+            if (*abort) break;
+            jparity ^= 1;
+            if (s_last) {
+                for (int i = tid; i < live * (D / 2); i += 32 * kConsumers) {
+                    const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
+                    auto slot = [&](int k) { return p.part + (size_t)(2 * k + (k == c0 ? 1 : 0)) * kPartStride; };
+                    float M = -INFINITY;
+                    for (int k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + r));
+                    const float B = M == -INFINITY ? 0.f : M;
+                    float L = 0.f;
+                    float2 v = make_float2(0.f, 0.f);
+                    for (int k = c0; k <= c1; ++k) {
+                        const float *sl = slot(k);
+                        const float e = ex2(__ldcg(sl + r) - B);
+                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kMaxRows + r * D + d));
+                        L += __ldcg(sl + kMaxRows + r) * e;
+                        v.x = fmaf(x.x, e, v.x);
+                        v.y = fmaf(x.y, e, v.y);
+                    }
+                    emit(r, d, v, M, L);
+                }
+            }
+        } else {
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_merge[1]);
+            wait_phase<false>(&s_merge[1], mparity, abort, status);
+            if (*abort) break;
+        }
+        mparity ^= 1;
+    }
+}
+
+template <int D, int NT, int FMT>
+cudaError_t launch(const DecodeParams &p, const CUtensorMap &map, int num_sms, cudaStream_t stream)
+{
+    static std::mutex mu;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 64 || !set[dev]) {
+            e = cudaFuncSetAttribute(attend_decode_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)Shape<D, NT>::kSmem);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) set[dev] = true;
+        }
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms * kCtasPerSm);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<D, NT>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<D, NT, FMT>, p, map);
+}
+
+template <int D>
+cudaError_t launch_d(const DecodeParams &p, const CUtensorMap &map, int fmt, int num_sms, cudaStream_t stream)
+{
+    if (p.rows == 8)
+        return fmt == SLORA_KV_E4M3 ? launch<D, 1, SLORA_KV_E4M3>(p, map, num_sms, stream)
+                                    : launch<D, 1, SLORA_KV_INT8>(p, map, num_sms, stream);
+    return fmt == SLORA_KV_E4M3 ? launch<D, 2, SLORA_KV_E4M3>(p, map, num_sms, stream)
+                                : launch<D, 2, SLORA_KV_INT8>(p, map, num_sms, stream);
+}
+
+}  // namespace
+
+size_t decode_workspace_bytes(int num_sms)
+{
+    const size_t ctas = (size_t)num_sms * kCtasPerSm;
+    return ctas * 2 * kPartStride * 4 + ctas * 4;
+}
+
+cudaError_t launch_attend_decode(const AttendArgs &a, const CUtensorMap &map, int box_rows, int head_dim, int fmt,
+                                 int32_t small_rows, void *ws, int num_sms, cudaStream_t stream, int *launches)
+{
+    DecodeParams p;
+    p.a = a;
+    p.box_rows = box_rows;
+    p.small_rows = small_rows;
+    p.rows = (int64_t)a.b.max_q * a.group <= 8 ? 8 : 16;
+    p.min_tiles = 2;
+    p.part = static_cast<float *>(ws);
+    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kCtasPerSm * 2 * kPartStride);
+    cudaError_t e = head_dim == 128 ? launch_d<128>(p, map, fmt, num_sms, stream)
+                                    : launch_d<64>(p, map, fmt, num_sms, stream);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace kv
+}  // namespace slora

@@ -12,9 +12,10 @@ from typing import Iterable, Optional
 import numpy as np
 import torch
 
-from . import (slora_adapter_register, slora_adapters_load, slora_adapters_evict,
-               slora_get_device_status, slora_lora_apply, slora_pages_alloc, slora_pool_create,
-               slora_pool_destroy, slora_adapter_is_resident)
+from . import (SLORA_KV_E4M3, SLORA_KV_INT8, slora_adapter_register, slora_adapters_load, slora_adapters_evict,
+               slora_get_device_status, slora_kv_block_tokens, slora_kv_create, slora_kv_destroy,
+               slora_kv_exponents, slora_lora_apply, slora_pages_alloc, slora_pool_base,
+               slora_pool_create, slora_pool_destroy, slora_adapter_is_resident)
 from .workloads import Workload
 
 
@@ -75,6 +76,55 @@ class PoolSession:
 
     def __exit__(self, *exc):
         self.close()
+
+
+class _DeviceBytes:
+    """Memory of the pool as torch.as_tensor takes it; `owner` lives as long as the tensor does."""
+
+    def __init__(self, address: int, shape, typestr: str, owner):
+        self.__cuda_array_interface__ = {"data": (address, False), "shape": tuple(shape), "typestr": typestr,
+                                         "version": 3, "strides": None}
+        self.owner = owner
+
+
+class _KVHandles:
+    """The pool and the cache over it; freed when the session and every view of its memory are gone."""
+
+    def __init__(self, device: int, hidden: int, num_pages: int, n_kv_heads: int, head_dim: int, fmt: int):
+        self.pool = slora_pool_create(device, hidden, num_pages, 1, 1)
+        self.kv = 0
+        self.kv = slora_kv_create(self.pool, n_kv_heads, head_dim, fmt)
+
+    def __del__(self):
+        if getattr(self, "kv", 0):
+            slora_kv_destroy(self.kv)
+        if getattr(self, "pool", 0):
+            slora_pool_destroy(self.pool)
+
+
+class KVSession:
+    """A pool whose pages all belong to one 8-bit KV cache, with its memory as torch tensors.
+
+    ``pages`` uint8 [num_pages][hidden * 2] and ``exponents`` int8 [num_pages] are the pool's
+    and the cache's own memory; ``block`` is the tokens of a page.
+    """
+
+    def __init__(self, hidden: int, num_pages: int, n_kv_heads: int, head_dim: int, fmt: str = "e4m3",
+                 device: int = 0):
+        self._h = _KVHandles(device, hidden, num_pages, n_kv_heads, head_dim,
+                             {"e4m3": SLORA_KV_E4M3, "int8": SLORA_KV_INT8}[fmt])
+        self.pool, self.kv = self._h.pool, self._h.kv
+        self.page_ids = np.empty(num_pages, np.int32)
+        slora_pages_alloc(self.pool, num_pages, self.page_ids)
+        self.block = slora_kv_block_tokens(self.kv)
+        dev = torch.device("cuda", device)
+        self.pages = torch.as_tensor(_DeviceBytes(slora_pool_base(self.pool), (num_pages, hidden * 2), "|u1", self._h),
+                                     device=dev)
+        self.exponents = torch.as_tensor(_DeviceBytes(slora_kv_exponents(self.kv), (num_pages,), "|i1", self._h),
+                                         device=dev)
+
+    def device_status(self) -> int:
+        return slora_get_device_status(self.pool)
 
 
 def prefetch_overlap(sess: PoolSession, K: int = 6, stream=None, mode: Optional[int] = None) -> dict:
