@@ -25,12 +25,13 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kFew = 4;
-constexpr int kMaxPasses = 8;      // 16384 bytes of codes per page over 256 threads of 8 codes
+constexpr int kMaxUnits = 128;     // pages per CTA at most
 constexpr int kQHeads = 4;         // query heads per group and step
 
 struct Params {
     AppendArgs a;
     int32_t slots;       // blocks of the cache, counted as above
+    int32_t per_seq;     // slots per sequence besides its tokens / block: 2, or 1 and no search if max_q is 1
     int32_t splits;      // CTAs per slot
     int32_t units;       // pages per CTA
     int64_t kv_ctas;     // slots * splits; later CTAs rotate queries
@@ -152,7 +153,75 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
     return a.positions ? a.positions[t] : in_cache;
 }
 
+// A block's nt <= kFew new rows of the pages [u0, u1): one page per group of lanes and step.
+// The rows' loads do not need the pages and go first; for a single token the next step's are
+// under way while one is written.
 template <int D, int FMT>
+__device__ __forceinline__ void few_rows(const AppendArgs &a, int32_t u0, int32_t u1, int32_t nt, int32_t held,
+                                         int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp)
+{
+    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
+    auto row_of = [&](int32_t u, int i) {
+        const __half *src = u & 1 ? a.v : a.k;
+        const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
+        return *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + i) * stride + (int64_t)(u >> 1) * D + ch * 8);
+    };
+    const uint4 zero = make_uint4(0, 0, 0, 0);
+    uint4 next = u0 + grp < u1 ? row_of(u0 + grp, 0) : zero;
+    Rot rot0;
+    rot0.on = false;
+    load_rot(a, position(a, row0, from), ch, rot0);
+    __syncthreads();
+    for (int32_t ub = u0; ub < u1; ub += GROUPS) {
+        const int32_t u = ub + grp;
+        const bool val = u & 1;
+        const int32_t page = u < u1 ? s_page[u - u0] : -1;
+        uint4 raw[kFew];
+        raw[0] = next;
+#pragma unroll
+        for (int i = 1; i < kFew; ++i) raw[i] = i < nt && page >= 0 ? row_of(u, i) : zero;
+        next = u + GROUPS < u1 ? row_of(u + GROUPS, 0) : zero;
+        float x[kFew][8];
+        float m = 0.f;
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            if (i >= nt) break;
+            unpack(raw[i], x[i]);
+            Rot r = rot0;
+            if (i > 0 && !val && page >= 0) load_rot(a, position(a, row0 + i, from + i), ch, r);
+            r.on = r.on && !val;
+            rotate<LPR>(a, r, ch, x[i]);
+            m = fmaxf(m, size_of(x[i]));
+        }
+#pragma unroll
+        for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+        if (page < 0) continue;
+        int e = fit_exponent<FMT>(m);
+        uint8_t *dst = a.c.pool + page * a.c.page_bytes;
+        if (held) {
+            const int old = s_exp[u - u0];
+            if (old >= e) {
+                e = old;
+            } else {
+                const float unit = pow2(old - e);
+                for (int r = 0; r < held; ++r) {
+                    uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
+                    *w = rescale8<FMT>(*w, unit);
+                }
+            }
+        }
+        if (ch == 0) a.c.exps[page] = (int8_t)e;
+        const float unit = pow2(-e);
+#pragma unroll
+        for (int i = 0; i < kFew; ++i) {
+            if (i >= nt) break;
+            *reinterpret_cast<uint2 *>(dst + (held + i) * D + ch * 8) = encode8<FMT>(x[i], unit);
+        }
+    }
+}
+
+template <int D, int FMT, int PASSES>
 __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 8;                 // lanes per row
@@ -160,6 +229,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
     __shared__ float s_max[2][kThreads / 32];
+    __shared__ int32_t s_page[kMaxUnits];
+    __shared__ int8_t s_exp[kMaxUnits];
 
     griddep_wait();
     griddep_launch_dependents();
@@ -215,10 +286,17 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     // ---- keys and values of one block of the cache ------------------------------------------
     const int32_t slot = (int32_t)(blockIdx.x / p.splits), part = (int32_t)(blockIdx.x - (int64_t)slot * p.splits);
     const int32_t bt = a.c.bt;
-    int32_t lo = 0, hi = a.b.S - 1;
-    while (lo < hi) {
-        const int32_t mid = (lo + hi + 1) / 2;
-        if ((int64_t)(a.b.indptr[mid] / bt) + 2ll * mid <= slot) lo = mid; else hi = mid - 1;
+    int32_t lo = slot;
+    if (p.per_seq == 2) {
+        // last sequence whose slots start at or before this one, 32 at a time; every warp for itself
+        lo = 0;
+        for (int32_t n = a.b.S; n > 1;) {
+            const int32_t step = (n + 31) / 32, at = lo + (tid & 31) * step;
+            const bool le = at < lo + n && (int64_t)(a.b.indptr[at] / bt) + 2ll * at <= slot;
+            const int k = 31 - __clz(__ballot_sync(~0u, le) | 1u);
+            n = n - k * step < step ? n - k * step : step;
+            lo += k * step;
+        }
     }
     const int32_t s = lo, t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s];
     const int32_t n = t1 - t0;
@@ -233,7 +311,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
     if (n == 0) return;
     const int32_t p0 = len - n;                                   // position of the first new token
-    const int64_t nth = slot - ((int64_t)(t0 / bt) + 2ll * s);    // nth touched block of the sequence
+    const int64_t nth = p.per_seq == 2 ? slot - ((int64_t)(t0 / bt) + 2ll * s) : 0;    // nth touched block of the sequence
     if (nth < 0 || p0 / bt + nth > (len - 1) / bt) return;
     const int32_t blk = p0 / bt + (int32_t)nth;
     const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
@@ -241,97 +319,44 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const int32_t row0 = t0 + from - p0;                          // first of the new tokens' rows
     const int32_t all = 2 * a.c.n_kv;
     const int32_t u0 = part * p.units, u1 = u0 + p.units < all ? u0 + p.units : all;
-    const int32_t *table = a.b.table + ((int64_t)s * a.b.max_blocks + blk) * all;
+    // the CTA's pages and, for a block that holds tokens, their exponents
+    if (tid < u1 - u0) {
+        int32_t page = a.b.table[((int64_t)s * a.b.max_blocks + blk) * all + u0 + tid];
+        if (page < 0 || page >= a.c.num_pages) {
+            set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+            page = -1;
+        }
+        s_page[tid] = page;
+        s_exp[tid] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
+    }
 
     if (nt <= kFew) {
-        // one page per group; unit: KV head * 2 + (0 keys, 1 values)
-        for (int32_t ub = u0; ub < u1; ub += GROUPS) {
-            const int32_t u = ub + grp;
-            const bool live = u < u1;
-            const int32_t head = u >> 1;
-            const bool val = u & 1;
-            int32_t page = live ? table[u] : -1;
-            if (live && (page < 0 || page >= a.c.num_pages)) {
-                if (ch == 0) set_status(a.c.status, SLORA_DEV_BAD_PAGE);
-                page = -1;
-            }
-            const __half *src = val ? a.v : a.k;
-            const int64_t stride = val ? a.v_stride : a.k_stride;
-            float x[kFew][8];
-            float m = 0.f;
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                if (i >= nt) break;
-                uint4 v = make_uint4(0, 0, 0, 0);
-                if (page >= 0)
-                    v = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + i) * stride + (int64_t)head * D + ch * 8);
-                unpack(v, x[i]);
-                Rot r;
-                r.on = false;
-                if (page >= 0 && !val) load_rot(a, position(a, row0 + i, from + i), ch, r);
-                float y[8];
-#pragma unroll
-                for (int j = 0; j < 8; ++j) y[j] = x[i][j];
-                rotate<LPR>(a, r, ch, y);
-                if (!val)
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) x[i][j] = y[j];
-                m = fmaxf(m, size_of(x[i]));
-            }
-#pragma unroll
-            for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-            // one lane of the group reads the old exponent, and the same one writes the new
-            int old = 0;
-            if (held && page >= 0 && ch == 0) old = clamp_exponent(a.c.exps[page]);
-            old = __shfl_sync(~0u, old, 0, LPR);
-            if (page < 0) continue;
-            int e = fit_exponent<FMT>(m);
-            uint8_t *dst = a.c.pool + page * a.c.page_bytes;
-            if (held) {
-                if (old >= e) {
-                    e = old;
-                } else {
-                    const float unit = pow2(old - e);
-                    for (int r = 0; r < held; ++r) {
-                        uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
-                        *w = rescale8<FMT>(*w, unit);
-                    }
-                }
-            }
-            if (ch == 0) a.c.exps[page] = (int8_t)e;
-            const float unit = pow2(-e);
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                if (i >= nt) break;
-                *reinterpret_cast<uint2 *>(dst + (held + i) * D + ch * 8) = encode8<FMT>(x[i], unit);
-            }
-        }
+        // one page per group and step; unit: KV head * 2 + (0 keys, 1 values)
+        few_rows<D, FMT>(a, u0, u1, nt, held, row0, from, s_page, s_exp);
         return;
     }
+    __syncthreads();
 
     int turn = 0;        // s_max alternates, so one barrier per page is enough
     for (int32_t u = u0; u < u1; ++u) {
         const int32_t head = u >> 1;
         const bool val = u & 1;
-        const int32_t page = table[u];
-        if (page < 0 || page >= a.c.num_pages) {
-            if (tid == 0) set_status(a.c.status, SLORA_DEV_BAD_PAGE);
-            continue;                       // the whole CTA: u, table and the check are uniform
-        }
+        const int32_t page = s_page[u - u0];
+        if (page < 0) continue;             // the whole CTA
         const __half *src = (val ? a.v : a.k) + (int64_t)head * D + ch * 8;
         const int64_t stride = val ? a.v_stride : a.k_stride;
-        const int old = clamp_exponent(a.c.exps[page]);
-        uint4 raw[kMaxPasses];
+        const int old = s_exp[u - u0];
+        uint4 raw[PASSES];
 #pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) {
+        for (int i = 0; i < PASSES; ++i) {
             const int r = i * GROUPS + grp;
             raw[i] = make_uint4(0, 0, 0, 0);
             if (r < nt) raw[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + r) * stride);
         }
-        float x[kMaxPasses][8];
+        float x[PASSES][8];
         float m = 0.f;
 #pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) {
+        for (int i = 0; i < PASSES; ++i) {
             if (i * GROUPS >= nt) break;
             const int r = i * GROUPS + grp;
             unpack(raw[i], x[i]);
@@ -366,7 +391,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if (tid == 0) a.c.exps[page] = (int8_t)e;
         const float unit = pow2(-e);
 #pragma unroll
-        for (int i = 0; i < kMaxPasses; ++i) {
+        for (int i = 0; i < PASSES; ++i) {
             const int r = i * GROUPS + grp;
             if (r < nt) *reinterpret_cast<uint2 *>(dst + (held + r) * D + ch * 8) = encode8<FMT>(x[i], unit);
         }
@@ -385,8 +410,15 @@ cudaError_t launch_d(const Params &p, int fmt, unsigned grid, cudaStream_t strea
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return fmt == SLORA_KV_E4M3 ? cudaLaunchKernelEx(&cfg, append_kernel<D, SLORA_KV_E4M3>, p)
-                                : cudaLaunchKernelEx(&cfg, append_kernel<D, SLORA_KV_INT8>, p);
+    // rows of a block over the CTA's groups: the registers for 4, 5 or 8 of them per lane (a
+    // page of up to 8192, 10240 or 16384 bytes)
+    const int passes = (p.a.c.bt + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
+    auto go = [&](auto e4m3, auto int8) {
+        return cudaLaunchKernelEx(&cfg, fmt == SLORA_KV_E4M3 ? e4m3 : int8, p);
+    };
+    if (passes <= 4) return go(append_kernel<D, SLORA_KV_E4M3, 4>, append_kernel<D, SLORA_KV_INT8, 4>);
+    if (passes <= 5) return go(append_kernel<D, SLORA_KV_E4M3, 5>, append_kernel<D, SLORA_KV_INT8, 5>);
+    return go(append_kernel<D, SLORA_KV_E4M3, 8>, append_kernel<D, SLORA_KV_INT8, 8>);
 }
 
 }  // namespace
@@ -397,13 +429,15 @@ cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sm
     p.a = a;
     const int groups = kThreads / (head_dim / 8);
     const int32_t all = 2 * a.c.n_kv;
-    p.slots = a.b.T / a.c.bt + 2 * a.b.S;
+    p.per_seq = a.b.max_q == 1 ? 1 : 2;
+    p.slots = p.per_seq == 1 ? a.b.S : a.b.T / a.c.bt + 2 * a.b.S;
     // Pages of one slot over several CTAs where the batch has few slots; a CTA's groups need
     // a page each when the blocks gain a token or so each.
     const int64_t want = 8ll * num_sms;
     int64_t splits = (want + p.slots - 1) / p.slots;
     const int64_t most = a.b.max_q <= kFew ? (all + groups - 1) / groups : all;
     if (splits > most) splits = most;
+    if (splits * kMaxUnits < all) splits = (all + kMaxUnits - 1) / kMaxUnits;
     p.units = (int32_t)((all + splits - 1) / splits);
     p.splits = (all + p.units - 1) / p.units;
     p.kv_ctas = (int64_t)p.slots * p.splits;

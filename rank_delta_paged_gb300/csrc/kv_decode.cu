@@ -23,6 +23,7 @@
 // query rows as the 8 columns, so that a single row wastes 7 columns of a product that is far
 // from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers, two or one
 // instruction per pair.
+#include <cstddef>
 #include <mutex>
 
 #include "host_common.h"
@@ -46,7 +47,6 @@ struct Meta {
     float ks[8];       // 2^exponent of the key pages, per 8 tokens of the tile
     float lv[8];       // exponent of the value pages
     float li[8];       // 2^-exponent of the value pages
-    uint32_t ok;       // bit g: tokens 8g .. 8g+7 of the tile were loaded
     int32_t plain;     // every token of the tile is seen by every row
     int32_t first, last;   // first / last tile of the unit within this CTA
     int32_t whole;     // the unit lies within this CTA
@@ -55,9 +55,10 @@ struct Meta {
     int32_t head;      // KV head
     int32_t r0;        // first row (token * group + head within the group)
     int32_t c0, c1;    // first and last CTA of the unit
+    uint32_t ok;       // bit g: tokens 8g .. 8g+7 of the tile were loaded
     int32_t pad[3];
 };
-static_assert(sizeof(Meta) % 16 == 0, "Meta");
+static_assert(sizeof(Meta) % 16 == 0 && offsetof(Meta, plain) % 16 == 0, "Meta");
 
 template <int D, int NT>
 struct Shape {
@@ -116,6 +117,7 @@ struct DecodeParams {
     int32_t box_rows, small_rows;
     int32_t rows;          // rows per unit: 8 * NT
     int32_t min_tiles;     // a CTA's run is at least this long
+    uint32_t bt_inverse;   // ceil(2^32 / block tokens): a token's block, or one more
     float *part;           // [CTAs][2] partial results
     int32_t *count;        // [CTAs] arrivals at units that start in the CTA, zero between calls
 };
@@ -259,129 +261,179 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         u.n = __shfl_sync(~0u, q.n, at_lane);
         u.len = __shfl_sync(~0u, q.len, at_lane);
 
-        const int R = p.box_rows, boxes = kTile / R;
-        const int gl = lane >> 1, kvl = lane & 1;      // this lane's box of a tile, and keys or values
-        const bool mover = lane < 2 * boxes;
-        int64_t w = w0;
-        // Page of this lane's box, one tile ahead of its use.
-        auto fetch = [&](int32_t s, int32_t hd, int32_t j0, const Seq &sq, int32_t *row) {
-            int32_t page = -1;
-            const int32_t j = j0 + gl * R;
-            const int32_t lo = first_key(a, sq, 0), hi = end_key(a, sq, sq.n - 1);
-            if (mover && j < hi && j + R > lo) {
-                const int32_t blk = j / a.c.bt;
-                *row = j - blk * a.c.bt;
-                page = a.b.table[(((int64_t)s * a.b.max_blocks + blk) * a.c.n_kv + hd) * 2 + kvl];
-                if (page < 0 || page >= a.c.num_pages) {
-                    set_status(status, SLORA_DEV_BAD_PAGE);
-                    page = -1;
-                }
-            }
-            return page;
-        };
-        int32_t row = 0, page = fetch(s32 + at_lane, head, (u_first + tile) * kTile, u, &row);
-        int stage = 0;
-        uint32_t parity = 1;
-        for (; w < w1; ++w) {
-            // the tile that this iteration issues
-            Meta m;
-            m.first = w == w0 || tile == 0;
-            m.last = w == w1 - 1 || tile == u_tiles - 1;
+        // What the tiles of a unit share, worked out when the list enters it.
+        struct Unit {
+            int32_t r0, whole, c0, c1;
+            int32_t lo, hi;                    // keys that any of its sequence's rows sees
+            int32_t plain_lo, plain_hi;        // keys that all of its rows see
+            const int32_t *table;              // entry (block 0, its head, keys)
+        } un;
+        auto enter = [&](int64_t w) {          // w: the unit's tile `tile` in the list
             const int64_t u0 = w - tile, u1 = u0 + u_tiles;
-            m.whole = u0 >= w0 && u1 <= w1;
-            m.c0 = m.c1 = 0;
-            if (!m.whole) {
-                m.c0 = (int32_t)(u0 / run);
-                m.c1 = (int32_t)((u1 - 1) / run);
+            un.whole = u0 >= w0 && u1 <= w1;
+            un.c0 = un.c1 = 0;
+            if (!un.whole) {
+                un.c0 = (int32_t)(u0 / run);
+                un.c1 = (int32_t)((u1 - 1) / run);
             }
-            m.j0 = (u_first + tile) * kTile;
-            m.row0 = u.row0;
-            m.n = u.n;
-            m.len = u.len;
-            m.head = head;
-            m.r0 = grp * p.rows;
-            const int32_t rows = u.n * a.group, tok0 = m.r0 / a.group;
-            const int32_t r1 = m.r0 + p.rows < rows ? m.r0 + p.rows : rows, tok1 = (r1 - 1) / a.group;
-            const int32_t exponent = page >= 0 ? clamp_exponent(a.c.exps[page]) : 0;
-            const int32_t my_page = page, my_row = row;
-            const unsigned got = __ballot_sync(~0u, my_page >= 0);
-            // a box needs both its keys and its values
-            uint32_t ok = 0;
-            for (int g = 0; g < boxes; ++g)
-                if ((got >> (2 * g) & 3u) == 3u) ok |= ((1u << (R / 8)) - 1u) << (g * (R / 8));
-            m.ok = ok;
-            m.plain = ok == 0xFFu && m.j0 >= first_key(a, u, tok1) && m.j0 + kTile <= end_key(a, u, tok0);
-            // step to the next tile and start reading its page
-            if (++tile == u_tiles) {
-                tile = 0;
-                if (++grp == u_groups) {
-                    grp = 0;
-                    if (++head == a.c.n_kv) {
-                        head = 0;
-                        if (w + 1 < w1) {
-                            unsigned next;
-                            while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
-                                s32 += 32;
-                                at_lane = -1;
-                                hold(s32);
+            un.r0 = grp * p.rows;
+            const int32_t rows = u.n * a.group, r1 = un.r0 + p.rows < rows ? un.r0 + p.rows : rows;
+            un.lo = first_key(a, u, 0);
+            un.hi = end_key(a, u, u.n - 1);
+            un.plain_lo = un.lo;
+            un.plain_hi = un.hi;
+            if (u.n > 1) {
+                un.plain_lo = first_key(a, u, (r1 - 1) / a.group);
+                un.plain_hi = end_key(a, u, un.r0 / a.group);
+            }
+            un.table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
+        };
+        enter(w0);
+
+        // A batch of tiles at a time, `lanes` lanes each, one lane per box: their page ids and
+        // their exponents are read together, one batch ahead of the copies.
+        const int R = p.box_rows, boxes = kTile / R, lanes = 2 * boxes, per_batch = 32 / lanes;
+        const int my_tile = lane / lanes, gl = (lane % lanes) >> 1, kvl = lane & 1;
+        const int32_t table_step = a.c.n_kv * 2;
+        struct Next {
+            bool want;                  // this lane's box: whether any row of the sequence needs it,
+            int32_t page, row;          // its page and first row there
+            int4 m0, m1, m2;            // the tile's Meta from `plain` on
+        };
+        int64_t ahead = w0;             // first tile of the list not yet described
+        bool broken = false;
+        auto describe = [&](Next &m) {
+            m.want = false;
+            m.page = 0;
+            int32_t count = w1 - ahead < per_batch ? (int32_t)(w1 - ahead) : per_batch;
+            if (broken) count = 0;
+            for (int b = 0; b < count; ++b) {
+                const int32_t j0 = (u_first + tile) * kTile;
+                if (b == my_tile) {
+                    const int32_t j = j0 + gl * R;
+                    m.want = j < un.hi && j + R > un.lo;
+                    if (m.want) {
+                        int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
+                        m.row = j - blk * a.c.bt;
+                        if (m.row < 0) {
+                            --blk;
+                            m.row += a.c.bt;
+                        }
+                        m.page = __ldg(un.table + (int64_t)blk * table_step + kvl);
+                    }
+                    m.m0 = make_int4(j0 >= un.plain_lo && j0 + kTile <= un.plain_hi,
+                                     (b == 0 && ahead == w0) || tile == 0,
+                                     ahead + b == w1 - 1 || tile == u_tiles - 1, un.whole);
+                    m.m1 = make_int4(j0, u.row0, u.n, u.len);
+                    m.m2 = make_int4(head, un.r0, un.c0, un.c1);
+                }
+                // step to the next tile
+                if (++tile == u_tiles) {
+                    tile = 0;
+                    if (++grp == u_groups) {
+                        grp = 0;
+                        if (++head == a.c.n_kv) {
+                            head = 0;
+                            if (ahead + b + 1 < w1) {
+                                unsigned next;
+                                while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
+                                    s32 += 32;
+                                    at_lane = -1;
+                                    hold(s32);
+                                }
+                                if (next == 0) {      // the lengths changed under the call
+                                    if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
+                                    broken = true;
+                                    count = b + 1;
+                                    break;
+                                }
+                                at_lane = __ffs(next) - 1;
+                                u_tiles = __shfl_sync(~0u, tiles, at_lane);
+                                u_groups = __shfl_sync(~0u, groups, at_lane);
+                                u_first = __shfl_sync(~0u, first, at_lane);
+                                u.row0 = __shfl_sync(~0u, q.row0, at_lane);
+                                u.n = __shfl_sync(~0u, q.n, at_lane);
+                                u.len = __shfl_sync(~0u, q.len, at_lane);
                             }
-                            if (next == 0) {      // the lengths changed under the call
-                                if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
-                                break;
-                            }
-                            at_lane = __ffs(next) - 1;
-                            u_tiles = __shfl_sync(~0u, tiles, at_lane);
-                            u_groups = __shfl_sync(~0u, groups, at_lane);
-                            u_first = __shfl_sync(~0u, first, at_lane);
-                            u.row0 = __shfl_sync(~0u, q.row0, at_lane);
-                            u.n = __shfl_sync(~0u, q.n, at_lane);
-                            u.len = __shfl_sync(~0u, q.len, at_lane);
                         }
                     }
+                    enter(ahead + b + 1);
                 }
             }
-            if (w + 1 < w1) page = fetch(s32 + at_lane, head, (u_first + tile) * kTile, u, &row);
-
-            wait_phase<false>(&s_empty[stage], parity, abort, status);
-            if (*abort) break;
-            uint8_t *dst = ring + (size_t)stage * Sh::kStage;
-            Meta *ms = &meta[stage];
-            const bool both = (got >> (lane & ~1) & 3u) == 3u;
-            if (my_page >= 0 && both)
-                tma_load_3d(smem_u32(dst) + kvl * Sh::kHalf + gl * R * D, &map, 0, my_row, my_page, &s_full[stage]);
-            if (mover) {
-                const int32_t e = my_page >= 0 && both ? exponent : 0;
-                for (int i = 0; i < R / 8; ++i) {
-                    const int g = gl * (R / 8) + i;
-                    if (kvl == 0) {
-                        ms->ks[g] = pow2(e);
+            ahead += count;
+            return count;
+        };
+        auto exponent_of = [&](Next &m) {
+            if (m.want && (m.page < 0 || m.page >= a.c.num_pages)) {
+                set_status(status, SLORA_DEV_BAD_PAGE);
+                m.want = false;
+            }
+            return m.want ? (int32_t)a.c.exps[m.page] : 0;
+        };
+        Next nx;
+        int n_next = describe(nx);
+        int32_t e_next = exponent_of(nx);
+        int64_t w = w0;
+        int stage = 0;
+        uint32_t parity = 1;
+        while (n_next > 0 && !*abort) {
+            const Next m = nx;
+            const int n_tiles = n_next;
+            const int32_t e_now = e_next;
+            n_next = describe(nx);
+            // a box needs both its keys and its values: bits 2 gl of `have`
+            unsigned have = __ballot_sync(~0u, m.want);
+            have &= have >> 1 & 0x55555555u;
+            if (lanes < 32) have = have >> (my_tile * lanes) & ((1u << lanes) - 1u);
+            const bool both = have >> (2 * gl) & 1u;
+            // bits 2 g spread over the 8-token groups of Meta.ok
+            uint32_t ok;
+            if (R == 16)
+                ok = (have & 1u) * 3u | (have >> 2 & 1u) * 12u | (have >> 4 & 1u) * 48u | (have >> 6 & 1u) * 192u;
+            else
+                ok = (have & 1u) | (have >> 1 & 2u) | (have >> 2 & 4u) | (have >> 3 & 8u) | (have >> 4 & 16u) |
+                     (have >> 5 & 32u) | (have >> 6 & 64u) | (have >> 7 & 128u);
+            const float e = (float)(both ? clamp_exponent(e_now) : 0);
+            for (int b = 0; b < n_tiles; ++b, ++w) {
+                wait_phase<false>(&s_empty[stage], parity, abort, status);
+                if (*abort) break;
+                if (b == my_tile) {
+                    uint8_t *dst = ring + (size_t)stage * Sh::kStage;
+                    Meta *ms = &meta[stage];
+                    if (both)
+                        tma_load_3d(smem_u32(dst) + kvl * Sh::kHalf + gl * R * D, &map, 0, m.row, m.page, &s_full[stage]);
+                    const float up = pow2((int)e), down = pow2(-(int)e);
+                    if (R == 16) {
+                        if (kvl == 0) {
+                            *reinterpret_cast<float2 *>(&ms->ks[2 * gl]) = make_float2(up, up);
+                        } else {
+                            *reinterpret_cast<float2 *>(&ms->lv[2 * gl]) = make_float2(e, e);
+                            *reinterpret_cast<float2 *>(&ms->li[2 * gl]) = make_float2(down, down);
+                        }
                     } else {
-                        ms->lv[g] = (float)e;
-                        ms->li[g] = pow2(-e);
+                        if (kvl == 0) {
+                            ms->ks[gl] = up;
+                        } else {
+                            ms->lv[gl] = e;
+                            ms->li[gl] = down;
+                        }
+                    }
+                    if (lane % lanes == 0) {
+                        int4 *mi = reinterpret_cast<int4 *>(&ms->plain);
+                        mi[0] = make_int4(m.m0.x && ok == 0xFFu, m.m0.y, m.m0.z, m.m0.w);
+                        mi[1] = m.m1;
+                        mi[2] = m.m2;
+                        ms->ok = ok;
                     }
                 }
+                __syncwarp();
+                if (lane == b * lanes) mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(ok) * 16u * D);
+                if (++stage == NS) {
+                    stage = 0;
+                    parity ^= 1;
+                }
             }
-            if (lane == 0) {
-                ms->ok = m.ok;
-                ms->plain = m.plain;
-                ms->first = m.first;
-                ms->last = m.last;
-                ms->whole = m.whole;
-                ms->j0 = m.j0;
-                ms->row0 = m.row0;
-                ms->n = m.n;
-                ms->len = m.len;
-                ms->head = m.head;
-                ms->r0 = m.r0;
-                ms->c0 = m.c0;
-                ms->c1 = m.c1;
-            }
-            __syncwarp();
-            if (lane == 0) mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(ok) * 16u * D);
-            if (++stage == NS) {
-                stage = 0;
-                parity ^= 1;
-            }
+            e_next = exponent_of(nx);
         }
         // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
         const int64_t issued = w - w0;
@@ -752,6 +804,7 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const CUtensorMap &map, in
     p.small_rows = small_rows;
     p.rows = (int64_t)a.b.max_q * a.group <= 8 ? 8 : 16;
     p.min_tiles = 2;
+    p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.part = static_cast<float *>(ws);
     p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kCtasPerSm * 2 * kPartStride);
     cudaError_t e = head_dim == 128 ? launch_d<128>(p, map, fmt, num_sms, stream)
