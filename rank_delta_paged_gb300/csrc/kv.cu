@@ -23,8 +23,7 @@ struct slora_kv {
     kv::Cache c = {};
     int64_t *launches = nullptr;
     void *ws = nullptr;        // the attention's partial results and counters
-    CUtensorMap map;           // pages as [num_pages][rows][head_dim] bytes
-    int box_rows = 0;
+    kv::PageMaps maps;
 };
 
 namespace {
@@ -33,9 +32,8 @@ using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
                                    CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
 
-// The pages as a 3-D tensor [num_pages][page_bytes / head_dim][head_dim] of bytes, boxes of box_rows rows
-// of one page, swizzled by the row's length.
-bool encode_map(slora_kv *k)
+// Boxes of whole rows, swizzled by the row's length.
+bool encode_maps(slora_kv *k)
 {
     void *fn = nullptr;
     cudaDriverEntryPointQueryResult q;
@@ -45,12 +43,17 @@ bool encode_map(slora_kv *k)
     const cuuint64_t d = (cuuint64_t)k->head_dim, pb = (cuuint64_t)k->c.page_bytes;
     const cuuint64_t dims[3] = {d, pb / d, (cuuint64_t)k->c.num_pages};
     const cuuint64_t strides[2] = {d, pb};
-    const cuuint32_t box[3] = {(cuuint32_t)d, (cuuint32_t)k->box_rows, 1};
     const cuuint32_t es[3] = {1, 1, 1};
-    return reinterpret_cast<EncodeTiledFn>(fn)(
-               &k->map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k->c.pool, dims, strides, box, es,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+    for (int i = 0; i < 3; ++i) {
+        const cuuint32_t box[3] = {(cuuint32_t)d, (k->c.bt % 16 == 0 ? 16u : 8u) << i, 1};
+        if (reinterpret_cast<EncodeTiledFn>(fn)(&k->maps.m[i], CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, k->c.pool, dims, strides,
+                                                box, es, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                                                d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) != CUDA_SUCCESS)
+            return false;
+    }
+    return true;
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
@@ -119,14 +122,13 @@ extern "C" slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, i
     k->c.n_kv = n_kv_heads;
     k->c.bt = bt;
     k->c.status = hp.pv.status;
-    k->box_rows = bt % 16 == 0 ? 16 : 8;
     const size_t ws = kv::decode_workspace_bytes(k->num_sms);
     if ((e = cudaMalloc(&k->c.exps, (size_t)hp.pv.num_pages)) == cudaSuccess &&
         (e = cudaMalloc(&k->ws, ws)) == cudaSuccess && (e = cudaMemset(k->c.exps, 0, (size_t)hp.pv.num_pages)) == cudaSuccess &&
         (e = cudaMemset(k->ws, 0, ws)) == cudaSuccess)
         e = cudaDeviceSynchronize();
     st = e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "kv_create: %s", cudaGetErrorString(e));
-    if (st == SLORA_OK && !encode_map(k))
+    if (st == SLORA_OK && !encode_maps(k))
         st = fail(SLORA_ERR_CUDA, "kv_create: no tensor map of the pool");
     if (st != SLORA_OK) {
         cudaFree(k->c.exps);
@@ -263,7 +265,7 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     cudaError_t e = dev_scope.error();
     int launches = 0;
     if (e == cudaSuccess)
-        e = kv::launch_attend_decode(a, k->map, k->box_rows, k->head_dim, k->format, INT_MAX, k->ws, k->num_sms,
+        e = kv::launch_attend_decode(a, k->maps, k->head_dim, k->format, INT_MAX, k->ws, k->num_sms,
                                      (cudaStream_t)stream, &launches);
     *k->launches += launches;
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));

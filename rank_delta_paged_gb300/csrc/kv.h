@@ -64,6 +64,12 @@ struct AttendArgs {
     int32_t causal, window;
 };
 
+// The pages as a tensor [num_pages][rows][head_dim] of bytes, in boxes of R, 2R and 4R rows of a
+// page (R = 16 if blocks are multiples of 16 tokens, else 8).
+struct PageMaps {
+    CUtensorMap m[3];
+};
+
 // One sequence of a batch as the attention kernels see it: its new rows, its keys, and
 // whether its sizes can be used.
 struct Seq {
@@ -178,7 +184,7 @@ cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sm
 // CTAs, and one arrival counter per CTA (zero between calls).
 size_t decode_workspace_bytes(int num_sms);
 // The rows of sequences with at most small_rows (new tokens * group) rows per KV head; INT32_MAX: all.
-cudaError_t launch_attend_decode(const AttendArgs &a, const CUtensorMap &map, int box_rows, int head_dim, int fmt,
+cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt,
                                  int32_t small_rows, void *ws, int num_sms, cudaStream_t stream, int *launches);
 
 }  // namespace kv

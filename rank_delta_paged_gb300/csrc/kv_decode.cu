@@ -16,13 +16,17 @@
 // sees the same load from every SM whatever the lengths.  A unit whose tiles fall into several
 // CTAs is joined by the last of them to finish, in the order of the list.
 //
-// Per CTA: one producer warp keeps a ring of tiles in flight by tensor-map copies (boxes of 16
-// rows, so a sequence's last page is not read past its last 16 tokens; the copy engine's swizzle spreads the rows
-// over the banks) and four consumer warps take 16 tokens of each tile: S^T = K Q^T and
-// O^T = V^T P^T with mma.sync m16n8k16, the tokens or the channels as the 16 rows and the
-// query rows as the 8 columns, so that a single row wastes 7 columns of a product that is far
-// from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers, two or one
-// instruction per pair.
+// Per CTA: one producer warp walks the list, writes a descriptor per tile (its unit, pages
+// and scales) into shared memory some tiles ahead, since a page id and then the exponent of its
+// page are two reads of a microsecond or two each under load, and copies the tiles into a ring by tensor
+// maps, in boxes of 64 rows down to 16 (8), so a sequence's last page is not read past its last 16
+// tokens; the copy engine's swizzle spreads the rows over the banks.  Four consumer warps take 16
+// tokens of each tile.  Copies by the consumers' lanes (cp.async) reached 4.4 TB/s on long
+// sequences, with the load path full.
+// S^T = K Q^T and O^T = V^T P^T run on mma.sync m16n8k16, the tokens or the channels as the
+// 16 rows and the query rows as the 8 columns: a single row wastes 7 columns of a product that
+// is far from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers,
+// half an instruction (e4m3) to one and a quarter (int8) per code.
 #include <cstddef>
 #include <mutex>
 
@@ -38,9 +42,10 @@ namespace {
 constexpr int kTile = 64;                       // tokens per tile
 constexpr int kConsumers = 4;                   // warps, 16 tokens of a tile each
 constexpr int kThreads = 32 * (kConsumers + 1);
-constexpr int kCtasPerSm = 2;
+constexpr int kMaxCtas = 3;                      // per SM, of any shape
 constexpr int kSeqChunks = 64;                  // partial sums of the tile counts
 constexpr int kMaxRows = 16;
+constexpr int kDescs = 32;                      // descriptors: 5 batches of 4 being prepared, 3 in use
 constexpr int kPartStride = 2 * kMaxRows + kMaxRows * 128;   // floats of one partial result: m, l, O
 
 struct Meta {
@@ -55,18 +60,22 @@ struct Meta {
     int32_t head;      // KV head
     int32_t r0;        // first row (token * group + head within the group)
     int32_t c0, c1;    // first and last CTA of the unit
-    uint32_t ok;       // bit g: tokens 8g .. 8g+7 of the tile were loaded
+    uint32_t ok;       // bit g: tokens 8g .. 8g+7 of the tile are loaded
     int32_t pad[3];
+    int32_t page[2][8];    // keys' and values' page of each box of 16 (8) rows
+    int32_t row[8];        // and its first row there
 };
 static_assert(sizeof(Meta) % 16 == 0 && offsetof(Meta, plain) % 16 == 0, "Meta");
 
 template <int D, int NT>
 struct Shape {
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 5 : 4) : (NT == 1 ? 10 : 8);
+    static constexpr int kCtas = NT == 1 ? 3 : 2;            // per SM
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 6 : 7);
     static constexpr int kHalf = kTile * D;                  // bytes of a tile's keys
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kMergeFloats = kConsumers * 8 * NT * (D + 2);
-    static constexpr size_t kSmem = 1024 + (size_t)kStages * kStage + kStages * sizeof(Meta) + kMergeFloats * 4 + 256;
+    static constexpr size_t kSmem =
+        1024 + (size_t)kStages * kStage + kDescs * sizeof(Meta) + kMergeFloats * 4;
 };
 
 __device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
@@ -89,13 +98,16 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int32_t c0, int32_t c1, int32_t c2,
-                                            uint64_t *bar)
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int32_t c1, int32_t c2, uint64_t *bar)
 {
     asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
                  "%3, %4}], [%5];" ::"r"(dst),
-                 "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+                 "l"(map), "r"(0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
                  : "memory");
+}
+__device__ __forceinline__ void lds128(uint32_t ad, uint32_t (&w)[4])
+{
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3]) : "r"(ad));
 }
 
 // Which token (of 8) is row m of an S^T tile.  The copy engine's swizzle moves 16-byte chunk
@@ -114,7 +126,8 @@ __device__ __forceinline__ int token_of_row(int m)
 
 struct DecodeParams {
     AttendArgs a;
-    int32_t box_rows, small_rows;
+    int32_t box_rows;      // 16 if blocks are multiples of 16 tokens, else 8
+    int32_t small_rows;
     int32_t rows;          // rows per unit: 8 * NT
     int32_t min_tiles;     // a CTA's run is at least this long
     uint32_t bt_inverse;   // ceil(2^32 / block tokens): a token's block, or one more
@@ -138,15 +151,15 @@ __device__ __forceinline__ void seq_tiles(const DecodeParams &p, const Seq &q, i
 }
 
 template <int D, int NT, int FMT>
-__global__ void __launch_bounds__(kThreads, kCtasPerSm)
-attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ CUtensorMap map)
+__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas)
+attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PageMaps maps)
 {
     using Sh = Shape<D, NT>;
     constexpr int NS = Sh::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
     Meta *meta = reinterpret_cast<Meta *>(ring + (size_t)NS * Sh::kStage);
-    float *merge = reinterpret_cast<float *>(meta + NS);
+    float *merge = reinterpret_cast<float *>(meta + kDescs);
     __shared__ uint64_t s_full[NS], s_empty[NS], s_merge[3];
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ int s_abort, s_last;
@@ -200,6 +213,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
     if (w0 >= w1) return;
     volatile int *abort = &s_abort;
+    const int R = p.box_rows;                  // rows of a tile that share a page
+    const int batch_log = R == 16 ? 2 : 1;     // tiles per batch of descriptors
+    const int n_batches = kDescs >> batch_log;
 
     if (warp == kConsumers) {
         // ---- producer ------------------------------------------------------------------
@@ -290,43 +306,58 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         };
         enter(w0);
 
-        // A batch of tiles at a time, `lanes` lanes each, one lane per box: their page ids and
-        // their exponents are read together, one batch ahead of the copies.
-        const int R = p.box_rows, boxes = kTile / R, lanes = 2 * boxes, per_batch = 32 / lanes;
+        // A batch of tiles at a time, `lanes` lanes each, one lane per box (R rows of keys or
+        // values): their page ids and their exponents are read together, one batch ahead.
+        const int boxes = kTile / R, lanes = 2 * boxes, per_batch = 32 / lanes;
         const int my_tile = lane / lanes, gl = (lane % lanes) >> 1, kvl = lane & 1;
         const int32_t table_step = a.c.n_kv * 2;
-        struct Next {
-            bool want;                  // this lane's box: whether any row of the sequence needs it,
+        struct Box {
+            bool want;                  // whether any row of the sequence needs it
             int32_t page, row;          // its page and first row there
-            int4 m0, m1, m2;            // the tile's Meta from `plain` on
         };
         int64_t ahead = w0;             // first tile of the list not yet described
         bool broken = false;
-        auto describe = [&](Next &m) {
+        // Batch of descriptors that the next call fills.  It was last used by the batch 8 (16 for
+        // R = 8) earlier, 4 (12) batches before the one being copied, whose tiles the consumers
+        // have left: the last copy waited for the tile NS before it.
+        int slot = 0;
+        // The tiles of the next batch: everything but pages and scales goes to the ring at once.
+        auto describe = [&](Box &m) {
             m.want = false;
             m.page = 0;
+            m.row = 0;
             int32_t count = w1 - ahead < per_batch ? (int32_t)(w1 - ahead) : per_batch;
-            if (broken) count = 0;
-            for (int b = 0; b < count; ++b) {
-                const int32_t j0 = (u_first + tile) * kTile;
-                if (b == my_tile) {
-                    const int32_t j = j0 + gl * R;
-                    m.want = j < un.hi && j + R > un.lo;
-                    if (m.want) {
-                        int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
-                        m.row = j - blk * a.c.bt;
-                        if (m.row < 0) {
-                            --blk;
-                            m.row += a.c.bt;
-                        }
-                        m.page = __ldg(un.table + (int64_t)blk * table_step + kvl);
+            if (broken || count <= 0) return 0;
+            Meta *ms = &meta[(slot << batch_log) + my_tile];
+            if (++slot == n_batches) slot = 0;
+            auto fill = [&](int32_t t, bool first, bool last) {    // this lane's tile is t of the unit
+                const int32_t j0 = (u_first + t) * kTile, j = j0 + gl * R;
+                m.want = j < un.hi && j + R > un.lo;
+                if (m.want) {
+                    int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
+                    m.row = j - blk * a.c.bt;
+                    if (m.row < 0) {
+                        --blk;
+                        m.row += a.c.bt;
                     }
-                    m.m0 = make_int4(j0 >= un.plain_lo && j0 + kTile <= un.plain_hi,
-                                     (b == 0 && ahead == w0) || tile == 0,
-                                     ahead + b == w1 - 1 || tile == u_tiles - 1, un.whole);
-                    m.m1 = make_int4(j0, u.row0, u.n, u.len);
-                    m.m2 = make_int4(head, un.r0, un.c0, un.c1);
+                    m.page = __ldg(un.table + (int64_t)blk * table_step + kvl);
                 }
+                if (lane % lanes == 0) {
+                    int4 *mi = reinterpret_cast<int4 *>(&ms->plain);
+                    mi[0] = make_int4(j0 >= un.plain_lo && j0 + kTile <= un.plain_hi, first || t == 0,
+                                      last || t == u_tiles - 1, un.whole);
+                    mi[1] = make_int4(j0, u.row0, u.n, u.len);
+                    mi[2] = make_int4(head, un.r0, un.c0, un.c1);
+                }
+            };
+            if (tile + per_batch < u_tiles && count == per_batch) {     // all within the unit, not at its end
+                fill(tile + my_tile, my_tile == 0 && ahead == w0, ahead + my_tile == w1 - 1);
+                tile += per_batch;
+                ahead += per_batch;
+                return count;
+            }
+            for (int b = 0; b < count; ++b) {
+                if (b == my_tile) fill(tile, b == 0 && ahead == w0, ahead + b == w1 - 1);
                 // step to the next tile
                 if (++tile == u_tiles) {
                     tile = 0;
@@ -363,26 +394,64 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             ahead += count;
             return count;
         };
-        auto exponent_of = [&](Next &m) {
+        auto exponent_of = [&](Box &m) {
             if (m.want && (m.page < 0 || m.page >= a.c.num_pages)) {
                 set_status(status, SLORA_DEV_BAD_PAGE);
                 m.want = false;
             }
             return m.want ? (int32_t)a.c.exps[m.page] : 0;
         };
-        Next nx;
-        int n_next = describe(nx);
-        int32_t e_next = exponent_of(nx);
-        int64_t w = w0;
-        int stage = 0;
+        // One lane: the copies of a tile.
+        auto copy_tile = [&](const Meta &m, int st) {
+            const uint32_t ok = m.ok, dst = smem_u32(ring) + st * Sh::kStage;
+            uint64_t *bar = &s_full[st];
+            auto copy = [&](int box, int level, int32_t row, int32_t kp, int32_t vp) {    // R << level rows
+                tma_load_3d(dst + box * R * D, &maps.m[level], row, kp, bar);
+                tma_load_3d(dst + box * R * D + Sh::kHalf, &maps.m[level], row, vp, bar);
+            };
+            if (R == 16) {
+                // the tile's four boxes as one, as two halves, or one by one: a box can be
+                // joined to the one before unless it starts a page
+                const int4 row = *reinterpret_cast<const int4 *>(m.row);
+                const int4 kp = *reinterpret_cast<const int4 *>(m.page[0]);
+                const int4 vp = *reinterpret_cast<const int4 *>(m.page[1]);
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
+                if (ok == 0xFFu && row.y && row.z && row.w) {
+                    copy(0, 2, row.x, kp.x, vp.x);
+                } else {
+                    if ((ok & 15u) == 15u && row.y) {
+                        copy(0, 1, row.x, kp.x, vp.x);
+                    } else {
+                        if (ok & 1u) copy(0, 0, row.x, kp.x, vp.x);
+                        if (ok & 4u) copy(1, 0, row.y, kp.y, vp.y);
+                    }
+                    if ((ok & 0xF0u) == 0xF0u && row.w) {
+                        copy(2, 1, row.z, kp.z, vp.z);
+                    } else {
+                        if (ok & 16u) copy(2, 0, row.z, kp.z, vp.z);
+                        if (ok & 64u) copy(3, 0, row.w, kp.w, vp.w);
+                    }
+                }
+            } else {
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
+                for (int x = 0; x < 8; ++x)
+                    if (ok >> x & 1u) copy(x, 0, m.row[x], m.page[0][x], m.page[1][x]);
+            }
+        };
+        // Two batches lie between the reading of a batch's page ids and of its exponents, and two more
+        // between those and their use: under load either read takes a microsecond or two.
+        Box b0, b1, b2, b3, b4;
+        int n0 = describe(b0), n1 = describe(b1);
+        int32_t e0 = exponent_of(b0), e1 = exponent_of(b1), e2;
+        int n2 = describe(b2), n3 = describe(b3), n4;
+        int batch = 0, stage = 0;
         uint32_t parity = 1;
-        while (n_next > 0 && !*abort) {
-            const Next m = nx;
-            const int n_tiles = n_next;
-            const int32_t e_now = e_next;
-            n_next = describe(nx);
+        int32_t issued = 0;
+        for (; n0 > 0 && !*abort; b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
+            e2 = exponent_of(b2);
+            n4 = describe(b4);
             // a box needs both its keys and its values: bits 2 gl of `have`
-            unsigned have = __ballot_sync(~0u, m.want);
+            unsigned have = __ballot_sync(~0u, b0.want);
             have &= have >> 1 & 0x55555555u;
             if (lanes < 32) have = have >> (my_tile * lanes) & ((1u << lanes) - 1u);
             const bool both = have >> (2 * gl) & 1u;
@@ -393,57 +462,53 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             else
                 ok = (have & 1u) | (have >> 1 & 2u) | (have >> 2 & 4u) | (have >> 3 & 8u) | (have >> 4 & 16u) |
                      (have >> 5 & 32u) | (have >> 6 & 64u) | (have >> 7 & 128u);
-            const float e = (float)(both ? clamp_exponent(e_now) : 0);
-            for (int b = 0; b < n_tiles; ++b, ++w) {
-                wait_phase<false>(&s_empty[stage], parity, abort, status);
-                if (*abort) break;
-                if (b == my_tile) {
-                    uint8_t *dst = ring + (size_t)stage * Sh::kStage;
-                    Meta *ms = &meta[stage];
-                    if (both)
-                        tma_load_3d(smem_u32(dst) + kvl * Sh::kHalf + gl * R * D, &map, 0, m.row, m.page, &s_full[stage]);
-                    const float up = pow2((int)e), down = pow2(-(int)e);
-                    if (R == 16) {
-                        if (kvl == 0) {
-                            *reinterpret_cast<float2 *>(&ms->ks[2 * gl]) = make_float2(up, up);
-                        } else {
-                            *reinterpret_cast<float2 *>(&ms->lv[2 * gl]) = make_float2(e, e);
-                            *reinterpret_cast<float2 *>(&ms->li[2 * gl]) = make_float2(down, down);
-                        }
+            if (my_tile < n0) {
+                const int e = both ? clamp_exponent(e0) : 0;
+                const float ef = (float)e, up = pow2(e), down = pow2(-e);
+                Meta *ms = &meta[(batch << batch_log) + my_tile];
+                ms->page[kvl][gl] = b0.page;
+                if (kvl == 0) ms->row[gl] = b0.row;
+                if (R == 16) {
+                    if (kvl == 0) {
+                        *reinterpret_cast<float2 *>(&ms->ks[2 * gl]) = make_float2(up, up);
                     } else {
-                        if (kvl == 0) {
-                            ms->ks[gl] = up;
-                        } else {
-                            ms->lv[gl] = e;
-                            ms->li[gl] = down;
-                        }
+                        *reinterpret_cast<float2 *>(&ms->lv[2 * gl]) = make_float2(ef, ef);
+                        *reinterpret_cast<float2 *>(&ms->li[2 * gl]) = make_float2(down, down);
                     }
-                    if (lane % lanes == 0) {
-                        int4 *mi = reinterpret_cast<int4 *>(&ms->plain);
-                        mi[0] = make_int4(m.m0.x && ok == 0xFFu, m.m0.y, m.m0.z, m.m0.w);
-                        mi[1] = m.m1;
-                        mi[2] = m.m2;
-                        ms->ok = ok;
+                } else {
+                    if (kvl == 0) {
+                        ms->ks[gl] = up;
+                    } else {
+                        ms->lv[gl] = ef;
+                        ms->li[gl] = down;
                     }
                 }
-                __syncwarp();
-                if (lane == b * lanes) mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(ok) * 16u * D);
+                if (lane % lanes == 0) {
+                    ms->ok = ok;
+                    if (ok != 0xFFu) ms->plain = 0;
+                }
+            }
+            __syncwarp();
+            for (int t = 0; t < n0; ++t, ++issued) {
+                wait_phase<false>(&s_empty[stage], parity, abort, status);
+                if (*abort) break;
+                if (lane == 0) copy_tile(meta[(batch << batch_log) + t], stage);
                 if (++stage == NS) {
                     stage = 0;
                     parity ^= 1;
                 }
             }
-            e_next = exponent_of(nx);
+            if (++batch == n_batches) batch = 0;
         }
         // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
-        const int64_t issued = w - w0;
         for (int i = 0; i < NS && i < issued; ++i) {
-            const int64_t t = issued - 1 - i;
+            const int t = issued - 1 - i;
             if (!mbar_wait_bounded(&s_full[t % NS], (uint32_t)(t / NS & 1), status)) break;
         }
         return;
     }
 
+    const int32_t total = (int32_t)(w1 - w0);
     // ---- consumers ---------------------------------------------------------------------
     const int g = lane >> 2, c = lane & 3;
     const int krow[2] = {token_of_row<D>(g), token_of_row<D>(g) + 8};
@@ -453,73 +518,107 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     constexpr int KS = D / 16;          // k steps of S^T, and 16-row tiles of O^T
     float o[NT][KS][4], mx[NT][2], sum[NT][2];
     uint32_t qf[NT][KS][2];
+    const uint32_t my_ring = smem_u32(ring) + warp * 16 * D;
     int stage = 0;
-    uint32_t parity = 0, mparity = 0, jparity = 0;
+    uint32_t parity = 0, mparity[2] = {0, 0}, jparity = 0, toggle = 0;
+    bool pending = false;      // the last unit's reads of the merge buffer may still be under way
+    auto meet = [&](int k) {
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&s_merge[k]);
+        wait_phase<false>(&s_merge[k], mparity[k], abort, status);
+        mparity[k] ^= 1;
+        return *abort == 0;
+    };
 
-    for (int64_t w = w0; w < w1; ++w) {
+    // This lane's share of the rows of m's unit: k step i holds channels 4 (i & 3) .. + 3 of
+    // chunk c + 4 (i >> 2).
+    auto load_q = [&](const Meta &m) {
+        const int32_t nrows = m.n * a.group - m.r0;
+#pragma unroll
+        for (int t = 0; t < NT; ++t) {
+            const int r = 8 * t + g;
+            const bool live = r < nrows;
+            const int tok = a.group == 1 ? m.r0 + r : (m.r0 + r) / a.group, hd = (m.r0 + r) - tok * a.group;
+            const __half *src = a.q + (int64_t)(m.row0 + tok) * a.q_stride + ((int64_t)m.head * a.group + hd) * D;
+#pragma unroll
+            for (int i = 0; i < KS; ++i) {
+                uint2 v = make_uint2(0, 0);
+                if (live) v = __ldg(reinterpret_cast<const uint2 *>(src + (c + 4 * (i >> 2)) * 16 + 4 * (i & 3)));
+                qf[t][i][0] = v.x;
+                qf[t][i][1] = v.y;
+            }
+        }
+    };
+    for (int32_t it = 0; it < total; ++it) {
         wait_phase<false>(&s_full[stage], parity, abort, status);
         if (*abort) break;
-        const Meta &m = meta[stage];
-        const uint32_t kbase = smem_u32(ring + (size_t)stage * Sh::kStage) + warp * 16 * D;
+        const Meta &m = meta[it % kDescs];
+        const int4 flags = *reinterpret_cast<const int4 *>(&m.plain);
+        const bool plain = flags.x != 0, last = flags.z != 0, whole = flags.w != 0;
+        const uint32_t kbase = my_ring + stage * Sh::kStage;
         const uint32_t vbase = kbase + Sh::kHalf;
         const int32_t nrows = m.n * a.group - m.r0;       // rows of this unit
-        if (m.first) {
+        if (flags.y) {
 #pragma unroll
             for (int t = 0; t < NT; ++t) {
                 mx[t][0] = mx[t][1] = -INFINITY;
                 sum[t][0] = sum[t][1] = 0.f;
 #pragma unroll
                 for (int i = 0; i < KS; ++i) o[t][i][0] = o[t][i][1] = o[t][i][2] = o[t][i][3] = 0.f;
-                const int r = 8 * t + g;
-                const bool live = r < nrows;
-                const int tok = (m.r0 + r) / a.group, hd = (m.r0 + r) - tok * a.group;
-                const __half *src = a.q + (int64_t)(m.row0 + tok) * a.q_stride + ((int64_t)m.head * a.group + hd) * D;
-#pragma unroll
-                for (int i = 0; i < KS; ++i) {
-                    // k step i holds this lane's channels 4 (i & 3) .. + 3 of chunk c + 4 (i >> 2)
-                    uint2 v = make_uint2(0, 0);
-                    if (live) v = *reinterpret_cast<const uint2 *>(src + (c + 4 * (i >> 2)) * 16 + 4 * (i & 3));
-                    qf[t][i][0] = v.x;
-                    qf[t][i][1] = v.y;
-                }
             }
+            if (it == 0) load_q(m);
         }
         // S^T: this warp's 16 tokens x the rows
-        float sc[NT][4];
+        float sc[NT][4], sd[NT][4];       // two chains of products, so that one hides the other's latency
 #pragma unroll
-        for (int t = 0; t < NT; ++t) sc[t][0] = sc[t][1] = sc[t][2] = sc[t][3] = 0.f;
+        for (int t = 0; t < NT; ++t)
+#pragma unroll
+            for (int x = 0; x < 4; ++x) sc[t][x] = sd[t][x] = 0.f;
 #pragma unroll
         for (int h = 0; h < D / 64; ++h) {
-            uint4 kw[2];
+            uint32_t kw[2][4];
 #pragma unroll
             for (int x = 0; x < 2; ++x) {
                 const int tok = krow[x];
-                const int chunk = D == 128 ? (c + 4 * h) ^ (tok & 7) : c ^ (tok >> 1 & 3);
-                const uint32_t ad = kbase + tok * D + chunk * 16;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(kw[x].x), "=r"(kw[x].y), "=r"(kw[x].z), "=r"(kw[x].w)
-                             : "r"(ad));
+                lds128(kbase + tok * D + (D == 128 ? (c + 4 * h) ^ (tok & 7) : c ^ (tok >> 1 & 3)) * 16, kw[x]);
             }
-            const uint32_t wa[4] = {kw[0].x, kw[0].y, kw[0].z, kw[0].w}, wb[4] = {kw[1].x, kw[1].y, kw[1].z, kw[1].w};
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 uint32_t a0, a1, a2, a3;
-                decode4<FMT>(wa[j], a0, a2);
-                decode4<FMT>(wb[j], a1, a3);
+                decode4<FMT>(kw[0][j], a0, a2);
+                decode4<FMT>(kw[1][j], a1, a3);
 #pragma unroll
                 for (int t = 0; t < NT; ++t)
-                    mma16816(sc[t], a0, a1, a2, a3, qf[t][4 * h + j][0], qf[t][4 * h + j][1]);
+                    mma16816(j & 1 ? sd[t] : sc[t], a0, a1, a2, a3, qf[t][4 * h + j][0], qf[t][4 * h + j][1]);
             }
+        }
+        // the values' codes, while the scores are worked on
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+            const int tok = vrow[x];
+            if constexpr (D == 128) {
+                lds128(vbase + tok * D + (g ^ (tok & 7)) * 16, vw[x]);
+            } else {
+                const uint32_t ad = vbase + tok * D + ((g >> 1) ^ (tok >> 1 & 3)) * 16 + (g & 1) * 8;
+                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(vw[x][0]), "=r"(vw[x][1]) : "r"(ad));
+            }
+        }
+        // the next unit's rows, while this one's last tile is finished
+        if (last && it + 1 < total) {
+            const bool wrap = stage + 1 == NS;
+            wait_phase<false>(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status);
+            if (*abort) break;
+            load_q(meta[(it + 1) % kDescs]);
         }
         const float f0 = m.ks[2 * warp] * a.scale_log2, f1 = m.ks[2 * warp + 1] * a.scale_log2;
         const float lv0 = m.lv[2 * warp], lv1 = m.lv[2 * warp + 1];
-        const bool plain = m.plain != 0;
 #pragma unroll
         for (int t = 0; t < NT; ++t) {
-            sc[t][0] = fmaf(sc[t][0], f0, lv0);
-            sc[t][1] = fmaf(sc[t][1], f0, lv0);
-            sc[t][2] = fmaf(sc[t][2], f1, lv1);
-            sc[t][3] = fmaf(sc[t][3], f1, lv1);
+            sc[t][0] = fmaf(sc[t][0] + sd[t][0], f0, lv0);
+            sc[t][1] = fmaf(sc[t][1] + sd[t][1], f0, lv0);
+            sc[t][2] = fmaf(sc[t][2] + sd[t][2], f1, lv1);
+            sc[t][3] = fmaf(sc[t][3] + sd[t][3], f1, lv1);
         }
         if (!plain) {
             Seq q;
@@ -581,26 +680,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             pf[t][1] = transpose8x8(*reinterpret_cast<uint32_t *>(&h1));
         }
         // O^T += V^T P^T
-        uint32_t vw[4][D / 32];
-#pragma unroll
-        for (int x = 0; x < 4; ++x) {
-            const int tok = vrow[x];
-            if (D == 128) {
-                const uint32_t ad = vbase + tok * D + (g ^ (tok & 7)) * 16;
-                asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(vw[x][0]), "=r"(vw[x][1]), "=r"(vw[x][D / 32 - 2]), "=r"(vw[x][D / 32 - 1])
-                             : "r"(ad));
-            } else {
-                const uint32_t ad = vbase + tok * D + ((g >> 1) ^ (tok >> 1 & 3)) * 16 + (g & 1) * 8;
-                asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(vw[x][0]), "=r"(vw[x][1]) : "r"(ad));
-            }
-        }
         if (!plain) {
-            // weights of unseen tokens are zero, but their codes may be NaN
-            Seq q;
-            q.row0 = m.row0;
-            q.n = m.n;
-            q.len = m.len;
+            // weights of unseen tokens are zero, but what lies in their place may be NaN
+            const Seq q = {m.row0, m.n, m.len};
             const int lo = first_key(a, q, 0), hi = end_key(a, q, m.n - 1);
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
@@ -624,8 +706,6 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 for (int t = 0; t < NT; ++t)
                     mma16816(o[t][2 * i + y], a0[y], a1[y], a2[y], a3[y], pf[t][0], pf[t][1]);
         }
-        const bool last = m.last != 0;
-        const bool whole = m.whole != 0;
         const int32_t row0 = m.row0, head = m.head, r0 = m.r0, c0 = m.c0, c1 = m.c1;
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_empty[stage]);
@@ -637,7 +717,15 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
 
         // ---- the unit's end: the four warps' results become one --------------------------
         const int live = nrows < 8 * NT ? nrows : 8 * NT;
-        float *mm = merge, *ml = merge + kConsumers * 8 * NT, *mo = merge + 2 * kConsumers * 8 * NT;
+        // with few rows the units take turns at the buffer's halves, and a unit's writes need not
+        // wait for the reads of the one before
+        const bool halves = live <= 4 * NT;
+        toggle ^= 1;
+        if (!halves && pending && !meet(1)) break;
+        pending = whole && halves;
+        const int mr = halves ? 4 * NT : 8 * NT;        // rows per warp
+        float *mm = merge + (halves && toggle ? kConsumers * 4 * NT * (D + 2) : 0);
+        float *ml = mm + kConsumers * mr, *mo = ml + kConsumers * mr;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
@@ -649,20 +737,17 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 const int r = 8 * t + 2 * c + x;
                 if (r < live) {
                     if (g == 0) {
-                        mm[warp * 8 * NT + r] = mx[t][x];
-                        ml[warp * 8 * NT + r] = l;
+                        mm[warp * mr + r] = mx[t][x];
+                        ml[warp * mr + r] = l;
                     }
                     // accumulators x, 2 + x: channels 2i, 2i + 1 of this lane's D / 8
 #pragma unroll
                     for (int i = 0; i < KS; ++i)
-                        *reinterpret_cast<float2 *>(&mo[(warp * 8 * NT + r) * D + g * (D / 8) + 2 * i]) =
+                        *reinterpret_cast<float2 *>(&mo[(warp * mr + r) * D + g * (D / 8) + 2 * i]) =
                             make_float2(o[t][i][x], o[t][i][2 + x]);
                 }
             }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&s_merge[0]);
-        wait_phase<false>(&s_merge[0], mparity, abort, status);
-        if (*abort) break;
+        if (!meet(0)) break;
         float *part = p.part + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kPartStride;
         auto emit = [&](int r, int d, float2 v, float M, float L) {
             const int tok = (r0 + r) / a.group, hd = (r0 + r) - tok * a.group;
@@ -678,15 +763,15 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
             float M = -INFINITY;
 #pragma unroll
-            for (int k = 0; k < kConsumers; ++k) M = fmaxf(M, mm[k * 8 * NT + r]);
+            for (int k = 0; k < kConsumers; ++k) M = fmaxf(M, mm[k * mr + r]);
             const float B = M == -INFINITY ? 0.f : M;
             float L = 0.f;
             float2 v = make_float2(0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kConsumers; ++k) {
-                const float e = ex2(mm[k * 8 * NT + r] - B);
-                const float2 x = *reinterpret_cast<const float2 *>(&mo[(k * 8 * NT + r) * D + d]);
-                L += ml[k * 8 * NT + r] * e;
+                const float e = ex2(mm[k * mr + r] - B);
+                const float2 x = *reinterpret_cast<const float2 *>(&mo[(k * mr + r) * D + d]);
+                L += ml[k * mr + r] * e;
                 v.x = fmaf(x.x, e, v.x);
                 v.y = fmaf(x.y, e, v.y);
             }
@@ -700,13 +785,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
             }
         }
+        if (pending) continue;
         if (!whole) {
             // the last CTA of the unit to arrive joins the parts in the order of the list
             __threadfence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_merge[1]);
-            wait_phase<false>(&s_merge[1], mparity, abort, status);
-            if (*abort) break;
+            if (!meet(1)) break;
             if (tid == 0) {
                 __threadfence();
                 s_last = atomicAdd(&p.count[c0], 1) == c1 - c0;
@@ -737,18 +820,14 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     emit(r, d, v, M, L);
                 }
             }
-        } else {
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_merge[1]);
-            wait_phase<false>(&s_merge[1], mparity, abort, status);
-            if (*abort) break;
+        } else if (!meet(1)) {
+            break;
         }
-        mparity ^= 1;
     }
 }
 
 template <int D, int NT, int FMT>
-cudaError_t launch(const DecodeParams &p, const CUtensorMap &map, int num_sms, cudaStream_t stream)
+cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cudaStream_t stream)
 {
     static std::mutex mu;
     static bool set[64] = {};
@@ -768,47 +847,47 @@ cudaError_t launch(const DecodeParams &p, const CUtensorMap &map, int num_sms, c
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms * kCtasPerSm);
+    cfg.gridDim = dim3(num_sms * Shape<D, NT>::kCtas);
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = Shape<D, NT>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<D, NT, FMT>, p, map);
+    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<D, NT, FMT>, p, maps);
 }
 
 template <int D>
-cudaError_t launch_d(const DecodeParams &p, const CUtensorMap &map, int fmt, int num_sms, cudaStream_t stream)
+cudaError_t launch_d(const DecodeParams &p, const PageMaps &maps, int fmt, int num_sms, cudaStream_t stream)
 {
     if (p.rows == 8)
-        return fmt == SLORA_KV_E4M3 ? launch<D, 1, SLORA_KV_E4M3>(p, map, num_sms, stream)
-                                    : launch<D, 1, SLORA_KV_INT8>(p, map, num_sms, stream);
-    return fmt == SLORA_KV_E4M3 ? launch<D, 2, SLORA_KV_E4M3>(p, map, num_sms, stream)
-                                : launch<D, 2, SLORA_KV_INT8>(p, map, num_sms, stream);
+        return fmt == SLORA_KV_E4M3 ? launch<D, 1, SLORA_KV_E4M3>(p, maps, num_sms, stream)
+                                    : launch<D, 1, SLORA_KV_INT8>(p, maps, num_sms, stream);
+    return fmt == SLORA_KV_E4M3 ? launch<D, 2, SLORA_KV_E4M3>(p, maps, num_sms, stream)
+                                : launch<D, 2, SLORA_KV_INT8>(p, maps, num_sms, stream);
 }
 
 }  // namespace
 
 size_t decode_workspace_bytes(int num_sms)
 {
-    const size_t ctas = (size_t)num_sms * kCtasPerSm;
+    const size_t ctas = (size_t)num_sms * kMaxCtas;
     return ctas * 2 * kPartStride * 4 + ctas * 4;
 }
 
-cudaError_t launch_attend_decode(const AttendArgs &a, const CUtensorMap &map, int box_rows, int head_dim, int fmt,
+cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt,
                                  int32_t small_rows, void *ws, int num_sms, cudaStream_t stream, int *launches)
 {
     DecodeParams p;
     p.a = a;
-    p.box_rows = box_rows;
+    p.box_rows = a.c.bt % 16 == 0 ? 16 : 8;
     p.small_rows = small_rows;
     p.rows = (int64_t)a.b.max_q * a.group <= 8 ? 8 : 16;
     p.min_tiles = 2;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.part = static_cast<float *>(ws);
-    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kCtasPerSm * 2 * kPartStride);
-    cudaError_t e = head_dim == 128 ? launch_d<128>(p, map, fmt, num_sms, stream)
-                                    : launch_d<64>(p, map, fmt, num_sms, stream);
+    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kMaxCtas * 2 * kPartStride);
+    cudaError_t e = head_dim == 128 ? launch_d<128>(p, maps, fmt, num_sms, stream)
+                                    : launch_d<64>(p, maps, fmt, num_sms, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
