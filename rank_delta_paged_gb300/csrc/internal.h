@@ -165,5 +165,9 @@ struct PoolHotPath {
     int64_t *launches;
 };
 slora_status pool_hot_path(slora_pool_t pool, PoolHotPath *out);
+// Device scratch of the KV attention, shared by the caches of a pool: allocated and set to zero by the
+// first call (with the pool's device current), freed with the pool.  Every call of a process
+// asks for the same size.
+slora_status pool_kv_scratch(slora_pool_t pool, size_t bytes, void **out);
 
 }  // namespace slora

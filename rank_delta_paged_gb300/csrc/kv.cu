@@ -1,6 +1,5 @@
 // Host side of the 8-bit paged KV cache: the cache's handle, the checks of arguments and the
 // choice of kernels.
-#include <climits>
 #include <cmath>
 #include <new>
 
@@ -22,11 +21,14 @@ struct slora_kv {
     int format = 0;
     kv::Cache c = {};
     int64_t *launches = nullptr;
-    void *ws = nullptr;        // the attention's partial results and counters
+    uint8_t *ws = nullptr;     // the attention's partial results and counters (the pool's)
     kv::PageMaps maps;
 };
 
 namespace {
+
+// Rows per KV head up to which the streaming kernel, 16 rows at a time, is the faster one.
+constexpr int32_t kSmallRows = 32;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -122,17 +124,21 @@ extern "C" slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, i
     k->c.n_kv = n_kv_heads;
     k->c.bt = bt;
     k->c.status = hp.pv.status;
-    const size_t ws = kv::decode_workspace_bytes(k->num_sms);
+    void *ws = nullptr;
+    st = pool_kv_scratch(pool, kv::decode_workspace_bytes(k->num_sms) + kv::prefill_workspace_bytes(k->num_sms), &ws);
+    if (st != SLORA_OK) {
+        delete k;
+        return st;
+    }
+    k->ws = static_cast<uint8_t *>(ws);
     if ((e = cudaMalloc(&k->c.exps, (size_t)hp.pv.num_pages)) == cudaSuccess &&
-        (e = cudaMalloc(&k->ws, ws)) == cudaSuccess && (e = cudaMemset(k->c.exps, 0, (size_t)hp.pv.num_pages)) == cudaSuccess &&
-        (e = cudaMemset(k->ws, 0, ws)) == cudaSuccess)
+        (e = cudaMemset(k->c.exps, 0, (size_t)hp.pv.num_pages)) == cudaSuccess)
         e = cudaDeviceSynchronize();
     st = e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "kv_create: %s", cudaGetErrorString(e));
     if (st == SLORA_OK && !encode_maps(k))
         st = fail(SLORA_ERR_CUDA, "kv_create: no tensor map of the pool");
     if (st != SLORA_OK) {
         cudaFree(k->c.exps);
-        cudaFree(k->ws);
         delete k;
         return st;
     }
@@ -147,7 +153,6 @@ extern "C" slora_status slora_kv_destroy(slora_kv_t k)
     DeviceScope dev_scope(k->device);
     cudaDeviceSynchronize();
     cudaFree(k->c.exps);
-    cudaFree(k->ws);
     delete k;
     return SLORA_OK;
 }
@@ -241,6 +246,9 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     if ((st = check_rows(fn, "q", q, q_stride, row)) != SLORA_OK ||
         (st = check_rows(fn, "out", out, out_stride, row)) != SLORA_OK)
         return st;
+    const int32_t group = n_q_heads / k->c.n_kv;
+    if ((int64_t)a.b.max_q * group > 1 << 30)
+        return fail(SLORA_ERR_UNSUPPORTED, "%s: %d new tokens of %d query heads per KV head", fn, a.b.max_q, group);
     if (out == q)
         return fail(SLORA_ERR_INVALID_ARG, "%s: out is q", fn);
     if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) || !std::isfinite(softmax_scale))
@@ -257,15 +265,25 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     a.q_stride = q_stride;
     a.out_stride = out_stride;
     a.n_q = n_q_heads;
-    a.group = n_q_heads / k->c.n_kv;
+    a.group = group;
     a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     a.causal = causal;
     a.window = window;
     DeviceScope dev_scope(k->device);
     cudaError_t e = dev_scope.error();
     int launches = 0;
-    if (e == cudaSuccess)
-        e = kv::launch_attend_decode(a, k->maps, k->head_dim, k->format, INT_MAX, k->ws, k->num_sms,
+    // Rows per KV head: few go to the streaming kernel, many to the tensor cores' one.  A batch whose sequences
+    // may be of both kinds runs both; where every sequence has nearly max_q new tokens, one
+    // kernel takes them all.
+    const int64_t most = (int64_t)a.b.max_q * a.group;
+    const bool big = most > kSmallRows;
+    const bool alike = (int64_t)a.b.T * 4 >= (int64_t)a.b.S * a.b.max_q * 3;
+    if (e == cudaSuccess && big)
+        e = kv::launch_attend_prefill(a, k->head_dim, k->format, alike ? 0 : kSmallRows,
+                                      k->ws + kv::decode_workspace_bytes(k->num_sms), k->num_sms, (cudaStream_t)stream,
+                                      &launches);
+    if (e == cudaSuccess && !(big && alike))
+        e = kv::launch_attend_decode(a, k->maps, k->head_dim, k->format, kSmallRows, k->ws, k->num_sms,
                                      (cudaStream_t)stream, &launches);
     *k->launches += launches;
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));

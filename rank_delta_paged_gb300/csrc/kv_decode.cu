@@ -871,7 +871,7 @@ cudaError_t launch_d(const DecodeParams &p, const PageMaps &maps, int fmt, int n
 size_t decode_workspace_bytes(int num_sms)
 {
     const size_t ctas = (size_t)num_sms * kMaxCtas;
-    return ctas * 2 * kPartStride * 4 + ctas * 4;
+    return (ctas * 2 * kPartStride * 4 + ctas * 4 + 255) / 256 * 256;
 }
 
 cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt,

@@ -1,0 +1,918 @@
+// Attention over the 8-bit paged KV cache for many rows per KV head (prompts and their chunks)
+// on the 5th-generation tensor cores.
+//
+// The mathematics is that of kv_decode.cu: scores in units of log2, the value pages'
+// exponents in the weights, one pass with a running maximum and sum.  A unit is 256 rows (new
+// token * group + query head of the group) of one sequence and KV head, as two tiles of 128:
+//     S_t = Q_t K^T      128 x 128 keys, fp32 in tensor memory
+//     P_t = 2^(S_t f + g - m)  in fp16, over S_t's own columns of tensor memory
+//     O_t += P_t V       fp32 in tensor memory
+// What bounds it: 4 D flops per row and key on the tensor cores; the codes are read once per 256
+// rows.  The tensor cores take fp16 from shared memory, so the codes of 128 keys and values are
+// converted once per unit and tile for both row tiles (a sixteenth of the exponentials' work).
+//
+// Per CTA (one per SM): warps 0-3 and 4-7 are the softmax of row tile 0 and 1, a row per
+// thread, so a row's maximum and sum need no exchange; warps 8-11 load codes, convert them and
+// write the swizzled operand tiles (K by rows, V as it stands: its channels run along N); one
+// thread of warp 12 issues the products in the order O_0 += P_0 V, S_0 = Q_0 K', O_1 += P_1 V,
+// S_1 = Q_1 K' so that one row tile's softmax runs under the other's products; warp 13 walks the
+// work list and looks up pages and exponents some tiles ahead.
+//
+// The key tiles of all units form one list, of which every CTA takes an equal run; a unit that
+// is cut between CTAs is joined by the last of them to finish, in the order of the list.
+#include <cstddef>
+#include <mutex>
+
+#include "host_common.h"
+#include "internal.h"
+#include "kv.h"
+#include "ptx.h"
+#include "tcgen05.h"
+
+namespace slora {
+namespace kv {
+namespace {
+
+constexpr int kTile = 128;                // keys per tile
+constexpr int kRows = 256;                // rows per unit
+constexpr int kThreads = 448;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kSeqChunks = 64;
+constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
+constexpr int kAhead = 4;
+
+enum : uint32_t {
+    kFirst = 1, kLast = 2, kWhole = 4, kPlain = 8,
+    kAct = 16,          // << t: row tile t sees keys of this tile
+    kFirstAct = 64,     // << t: the first such tile of the unit in this CTA
+    kLastAct = 256      // << t: the last
+};
+
+struct Desc {
+    int64_t off[2][16];     // keys and values: bytes from the pool's start to the first row of 8 tokens
+    float ks[16];           // 2^exponent of the key pages, per 8 tokens
+    float lv[16];           // exponent of the value pages
+    float li[16];           // 2^-exponent of the value pages
+    uint32_t flags;
+    int32_t j0;             // first key
+    int32_t lo, hi;         // keys that any of the unit's rows sees
+    int32_t row0, n, len, head;
+    int32_t r0, nrows;      // first row of the unit, and rows
+    int32_t c0, c1;         // first and last CTA of the unit
+    uint32_t ok;            // bit g: tokens 8g .. 8g+7 are there
+    int32_t pad[3];
+};
+static_assert(sizeof(Desc) % 16 == 0 && offsetof(Desc, flags) % 16 == 0, "Desc");
+
+template <int D>
+struct Shape {
+    static constexpr int kBlocks = D / 64;                   // 64-channel blocks of 128-byte rows
+    static constexpr int kQTile = 128 * D * 2;
+    static constexpr int kKVTile = kTile * D * 2;
+    static constexpr size_t kSmem = 1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kDescs * sizeof(Desc);
+    static constexpr int kPart = 2 * 128 + 128 * D;          // floats of a row tile's partial result: m, l, O
+};
+
+struct PrefillParams {
+    AttendArgs a;
+    int32_t small_rows;    // sequences with at most this many rows are another kernel's
+    int32_t min_tiles;
+    uint32_t bt_inverse;
+    uint32_t q_sign;       // the sign of the softmax scale, applied to Q, so that larger products are larger scores
+    float scale;           // its magnitude, times log2(e)
+    float *part;           // [CTAs][2][2] partial results
+    int32_t *count;        // [CTAs][2]
+};
+
+__device__ __forceinline__ float ex2(float x)
+{
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint4 ld_codes(const uint8_t *p)
+{
+    uint4 v;
+    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
+    return v;
+}
+__device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
+{
+    asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+
+struct Tiles {
+    int32_t lo, hi;        // key tiles [lo, hi) of a unit, one at least
+    int32_t k0, k1;        // keys
+    int32_t b[2], e[2];    // key tiles that row tile t sees
+};
+__device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, int32_t r0, int32_t r1, Tiles &t)
+{
+    t.k0 = first_key(a, q, r0 / a.group);
+    t.k1 = end_key(a, q, (r1 - 1) / a.group);
+    t.lo = t.k0 / kTile;
+    t.hi = (t.k1 + kTile - 1) / kTile;
+    if (t.hi <= t.lo) t.hi = t.lo + 1;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int32_t x0 = r0 + 128 * i, x1 = r1 < x0 + 128 ? r1 : x0 + 128;
+        t.b[i] = t.e[i] = 0;
+        if (x0 < x1) {
+            const int32_t k0 = first_key(a, q, x0 / a.group), k1 = end_key(a, q, (x1 - 1) / a.group);
+            if (k1 > k0) {
+                t.b[i] = k0 / kTile;
+                t.e[i] = (k1 + kTile - 1) / kTile;
+            }
+        }
+    }
+}
+__device__ __forceinline__ int32_t unit_count(const AttendArgs &a, const Seq &q, int32_t rows, int32_t rt)
+{
+    const int32_t r0 = rt * kRows, r1 = rows < r0 + kRows ? rows : r0 + kRows;
+    const int32_t lo = first_key(a, q, r0 / a.group) / kTile, hi = (end_key(a, q, (r1 - 1) / a.group) + kTile - 1) / kTile;
+    return hi > lo ? hi - lo : 1;
+}
+
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p)
+{
+    using Sh = Shape<D>;
+    constexpr int NB = Sh::kBlocks;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t q_sm = (smem_u32(smem_raw) + 1023) & ~1023u;      // two row tiles
+    const uint32_t k_sm = q_sm + 2 * Sh::kQTile, v_sm = k_sm + 2 * Sh::kKVTile;
+    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (v_sm + 2 * Sh::kKVTile - smem_u32(smem_raw)));
+    __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
+    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_fin;
+    __shared__ int64_t s_sum[kSeqChunks];
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_abort, s_last[2];
+
+    const AttendArgs &a = p.a;
+    int32_t *status = a.c.status;
+    const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+    if (tid == 0) {
+        for (int i = 0; i < kDescs; ++i) {
+            mbar_init(&s_tfull[i], 1);
+            mbar_init(&s_tempty[i], 13);         // 4 converting and 8 softmax warps, the issuing thread
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&s_kfull[i], 4);
+            mbar_init(&s_kempty[i], 1);
+            mbar_init(&s_vfull[i], 4);
+            mbar_init(&s_vempty[i], 1);
+            mbar_init(&s_sfull[i], 1);
+            mbar_init(&s_pfull[i], 4);
+            mbar_init(&s_odone[i], 1);
+            mbar_init(&s_ofree[i], 4);
+            mbar_init(&s_join[i], 4);
+            mbar_init(&s_said[i], 1);
+        }
+        mbar_init(&s_qfull, 4);
+        mbar_init(&s_qempty, 1);
+        mbar_init(&s_fin, 1);
+        fence_mbar_init();
+        s_abort = 0;
+    }
+    griddep_wait();
+    griddep_launch_dependents();
+
+    // Tiles of each run of `per` sequences; every CTA sums them for itself.
+    const int S = a.b.S;
+    const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
+    int32_t bad = 0;
+    for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
+        int64_t t = 0;
+        for (int64_t s = (int64_t)c * per; s < S && s < (int64_t)(c + 1) * per; s += 32) {
+            Seq q = {0, 0, 0};
+            if (s + lane < S) q = load_seq(a, (int32_t)s + lane, &bad);
+            const int64_t rows64 = (int64_t)q.n * a.group;
+            unsigned big = __ballot_sync(~0u, rows64 > p.small_rows && q.n > 0);
+            while (big) {
+                const int l = __ffs(big) - 1;
+                big &= big - 1;
+                Seq u;
+                u.row0 = __shfl_sync(~0u, q.row0, l);
+                u.n = __shfl_sync(~0u, q.n, l);
+                u.len = __shfl_sync(~0u, q.len, l);
+                const int32_t rows = u.n * a.group;
+                for (int32_t rt = lane; rt * kRows < rows; rt += 32) t += unit_count(a, u, rows, rt);
+            }
+        }
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+        if (lane == 0) s_sum[c] = t * a.c.n_kv;
+    }
+    if (bad && blockIdx.x == 0) set_status(status, bad);
+    __syncthreads();
+    int64_t v0 = s_sum[2 * lane], v1 = s_sum[2 * lane + 1], W = v0 + v1;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t u = __shfl_up_sync(~0u, W, o);
+        if (lane >= o) W += u;
+    }
+    const int64_t before = W - v0 - v1;
+    W = __shfl_sync(~0u, W, 31);
+    int64_t run = (W + gridDim.x - 1) / gridDim.x;
+    if (run < p.min_tiles) run = p.min_tiles;
+    const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
+    if (w0 >= w1) return;
+    const int32_t total = (int32_t)(w1 - w0);
+    volatile int *abort = &s_abort;
+
+    if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, 512);
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    const uint32_t tmem = s_tmem;
+    // columns: S_0, S_1 (P over them), O_0, O_1
+    const uint32_t tm_s = tmem, tm_o = tmem + 256;
+
+    if (warp == kPlanWarp) {
+        // ---- the work list -----------------------------------------------------------------
+        const unsigned hit = __ballot_sync(~0u, before <= w0);
+        const int at = 31 - __clz(hit);
+        int chunk = 2 * at;
+        int64_t base = __shfl_sync(~0u, before, at);
+        const int64_t half = __shfl_sync(~0u, v0, at);
+        if (base + half <= w0) {
+            base += half;
+            ++chunk;
+        }
+        // the 32 sequences that the lanes hold, and those of them with work
+        int32_t s32 = chunk * per, at_lane = -1;
+        Seq q, u = {0, 0, 0};
+        unsigned big = 0;
+        auto hold = [&]() {
+            q = Seq{0, 0, 0};
+            int32_t ignore;
+            if (s32 + lane < S) q = load_seq(a, s32 + lane, &ignore);
+            big = __ballot_sync(~0u, q.n > 0 && (int64_t)q.n * a.group > p.small_rows);
+        };
+        hold();
+        int32_t rows = 0, head = 0, rt = 0;
+        // the next sequence with work; false if there is none
+        auto next_seq = [&]() {
+            while (big == 0) {
+                s32 += 32;
+                if (s32 >= S) return false;
+                hold();
+            }
+            at_lane = __ffs(big) - 1;
+            big &= big - 1;
+            u.row0 = __shfl_sync(~0u, q.row0, at_lane);
+            u.n = __shfl_sync(~0u, q.n, at_lane);
+            u.len = __shfl_sync(~0u, q.len, at_lane);
+            rows = u.n * a.group;
+            head = rt = 0;
+            return true;
+        };
+        bool found = false;
+        while (next_seq()) {
+            int64_t t = 0;
+            for (int32_t i = lane; i * kRows < rows; i += 32) t += unit_count(a, u, rows, i);
+#pragma unroll
+            for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+            if (base + t * a.c.n_kv > w0) {
+                head = (int32_t)((w0 - base) / t);
+                base += head * t;
+                found = true;
+                break;
+            }
+            base += t * a.c.n_kv;
+        }
+        // the row tile of the head that holds w0
+        while (found) {
+            const int32_t i = rt + lane;
+            const int32_t mine = (int64_t)i * kRows < rows ? unit_count(a, u, rows, i) : 0;
+            int32_t sum = mine;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const int32_t v = __shfl_up_sync(~0u, sum, o);
+                if (lane >= o) sum += v;
+            }
+            const unsigned past = __ballot_sync(~0u, base + sum > w0);
+            if (past) {
+                const int l = __ffs(past) - 1;
+                rt += l;
+                base += __shfl_sync(~0u, sum - mine, l);
+                break;
+            }
+            base += __shfl_sync(~0u, sum, 31);
+            rt += 32;
+            if ((int64_t)rt * kRows >= rows) found = false;
+        }
+        if (!found && lane == 0) {        // the lengths changed under the call
+            set_status(status, SLORA_DEV_BAD_LENGTH);
+            s_abort = 1;
+        }
+        Tiles ut = {};
+        int32_t r0 = 0, r1 = 0, tile = 0, c0 = 0, c1 = 0;
+        bool whole = false;
+        int32_t ta = 0, tb = 0;                    // the unit's key tiles in this CTA
+        const int32_t *table = nullptr;
+        auto enter = [&](int64_t u0) {             // the unit starts at u0 of the list
+            r0 = rt * kRows;
+            r1 = rows < r0 + kRows ? rows : r0 + kRows;
+            unit_tiles(a, u, r0, r1, ut);
+            const int64_t u1 = u0 + ut.hi - ut.lo;
+            whole = u0 >= w0 && u1 <= w1;
+            c0 = c1 = 0;
+            if (!whole) {
+                c0 = (int32_t)(u0 / run);
+                c1 = (int32_t)((u1 - 1) / run);
+            }
+            ta = u0 >= w0 ? ut.lo : ut.lo + (int32_t)(w0 - u0);
+            tb = u1 <= w1 ? ut.hi : ut.hi - (int32_t)(u1 - w1);
+            tile = ta;
+            table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
+        };
+        int64_t u0 = base;
+        bool more = found;
+        if (found) enter(u0);
+        const int gl = lane >> 1, kvl = lane & 1;       // this lane's 8 tokens of a tile, and keys or values
+        struct Box {
+            bool want;
+            int32_t page, row;
+        };
+        int slot = 0;
+        uint32_t slot_parity = 1;
+        // The next tile: everything but pages and scales goes to its descriptor at once.
+        auto describe = [&](Box &x) {
+            x.want = false;
+            x.page = x.row = 0;
+            if (!more) return false;
+            wait_phase<false>(&s_tempty[slot], slot_parity, abort, status);
+            if (*abort) return false;
+            Desc &d = desc[slot];
+            if (++slot == kDescs) {
+                slot = 0;
+                slot_parity ^= 1;
+            }
+            const int32_t j0 = tile * kTile, j = j0 + 8 * gl;
+            x.want = j < ut.k1 && j + 8 > ut.k0;
+            if (x.want) {
+                int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
+                x.row = j - blk * a.c.bt;
+                if (x.row < 0) {
+                    --blk;
+                    x.row += a.c.bt;
+                }
+                x.page = __ldg(table + (int64_t)blk * a.c.n_kv * 2 + kvl);
+            }
+            if (lane == 0) {
+                uint32_t f = (tile == ta ? kFirst : 0) | (tile == tb - 1 ? kLast : 0) | (whole ? kWhole : 0);
+#pragma unroll
+                for (int t = 0; t < 2; ++t) {
+                    const int32_t b = ut.b[t] > ta ? ut.b[t] : ta, e = ut.e[t] < tb ? ut.e[t] : tb;
+                    if (tile >= b && tile < e)
+                        f |= (kAct << t) | (tile == b ? kFirstAct << t : 0) | (tile == e - 1 ? kLastAct << t : 0);
+                }
+                if (j0 >= first_key(a, u, (r1 - 1) / a.group) && j0 + kTile <= end_key(a, u, r0 / a.group)) f |= kPlain;
+                int4 *di = reinterpret_cast<int4 *>(&d.flags);
+                di[0] = make_int4((int)f, j0, ut.k0, ut.k1);
+                di[1] = make_int4(u.row0, u.n, u.len, head);
+                di[2] = make_int4(r0, r1 - r0, c0, c1);
+            }
+            if (++tile == tb) {
+                u0 += ut.hi - ut.lo;
+                if (u0 >= w1) {
+                    more = false;
+                } else {
+                    if ((int64_t)(++rt) * kRows >= rows) {
+                        rt = 0;
+                        if (++head == a.c.n_kv && !next_seq()) {      // the lengths changed under the call
+                            if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
+                            more = false;
+                        }
+                    }
+                    if (more) enter(u0);
+                }
+            }
+            return true;
+        };
+        auto exponent_of = [&](Box &x) {
+            if (x.want && (x.page < 0 || x.page >= a.c.num_pages)) {
+                set_status(status, SLORA_DEV_BAD_PAGE);
+                x.want = false;
+            }
+            return x.want ? (int32_t)a.c.exps[x.page] : 0;
+        };
+        // Two tiles lie between the reading of a tile's page ids and of its exponents, and two
+        // more between those and their use.
+        Box b0, b1, b2, b3, b4;
+        bool n0 = describe(b0), n1 = describe(b1);
+        int32_t e0 = exponent_of(b0), e1 = exponent_of(b1), e2;
+        bool n2 = describe(b2), n3 = describe(b3), n4;
+        int32_t i = 0;
+        for (; n0 && !*abort; ++i, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
+            e2 = exponent_of(b2);
+            n4 = describe(b4);
+            Desc &d = desc[i % kDescs];
+            unsigned have = __ballot_sync(~0u, b0.want);
+            have &= have >> 1 & 0x55555555u;               // a group needs both its keys and its values
+            const bool both = have >> (2 * gl) & 1u;
+            const int e = both ? clamp_exponent(e0) : 0;
+            d.off[kvl][gl] = both ? (int64_t)b0.page * a.c.page_bytes + b0.row * D : -1;
+            if (kvl == 0) {
+                d.ks[gl] = pow2(e);
+            } else {
+                d.lv[gl] = (float)e;
+                d.li[gl] = pow2(-e);
+            }
+            const unsigned ok = __ballot_sync(~0u, both && kvl == 0);      // bit 2g
+            if (lane == 0) {
+                uint32_t o = 0;
+                for (int k = 0; k < 16; ++k) o |= (ok >> (2 * k) & 1u) << k;
+                d.ok = o;
+                if (o != 0xFFFFu) d.flags &= ~kPlain;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_tfull[i % kDescs]);
+        }
+    } else if (warp == kMmaWarp) {
+        // ---- products --------------------------------------------------------------------
+        if (lane == 0) {
+            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kTile, 0, 0), id_o = tc::idesc_f16_f32(128, D, 0, 1);
+            uint32_t q_par = 0, p_par[2] = {0, 0}, of_par[2] = {1, 1};
+            auto flags_of = [&](int32_t i) {
+                wait_phase<false>(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
+                return *abort ? 0u : desc[i % kDescs].flags;
+            };
+            auto scores = [&](int t, int32_t i) {
+                const uint32_t qa = q_sm + t * Sh::kQTile, ka = k_sm + (i & 1) * Sh::kKVTile;
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t o = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
+                    tc::mma_f16(tm_s + 128 * t, tc::smem_desc_sw128(qa + o, 16, 1024),
+                                tc::smem_desc_sw128(ka + o, 16, 1024), id_s, kk != 0);
+                }
+                tc::commit(&s_sfull[t]);
+            };
+            auto values = [&](int t, int32_t i, bool first) {
+                const uint32_t va = v_sm + (i & 1) * Sh::kKVTile;
+#pragma unroll
+                for (int kk = 0; kk < kTile / 16; ++kk)
+                    tc::mma_f16_ts(tm_o + D * t, tm_s + 128 * t + kk * 8,
+                                   tc::smem_desc_sw128(va + kk * 2048, 128 * 128, 1024), id_o, !(first && kk == 0));
+            };
+            // what S of tile i needs: the keys and, for a new unit, its rows
+            auto before_scores = [&](int32_t i, uint32_t f) {
+                wait_phase<false>(&s_kfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
+                if (f & kFirst) {
+                    wait_phase<false>(&s_qfull, q_par, abort, status);
+                    q_par ^= 1;
+                }
+                tc::fence_after_sync();
+            };
+            auto after_scores = [&](int32_t i, uint32_t f) {
+                tc::commit(&s_kempty[i & 1]);
+                if (f & kLast) tc::commit(&s_qempty);
+            };
+            uint32_t f = flags_of(0);
+            if (!*abort) before_scores(0, f);
+            if (!*abort) {
+                for (int t = 0; t < 2; ++t)
+                    if (f & (kAct << t)) scores(t, 0);
+                after_scores(0, f);
+            }
+            for (int32_t i = 0; i < total && !*abort; ++i) {
+                uint32_t g = 0;
+                if (i + 1 < total) g = flags_of(i + 1);
+                if (*abort) break;
+                const bool same = i + 1 < total && !(g & kFirst);      // the next tile is of this unit
+                wait_phase<false>(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
+                bool ready = false;
+                for (int t = 0; t < 2 && !*abort; ++t) {
+                    if (f & (kAct << t)) {
+                        wait_phase<false>(&s_pfull[t], p_par[t], abort, status);
+                        p_par[t] ^= 1;
+                        if (f & (kFirstAct << t)) {
+                            wait_phase<false>(&s_ofree[t], of_par[t], abort, status);
+                            of_par[t] ^= 1;
+                        }
+                        if (*abort) break;
+                        tc::fence_after_sync();
+                        values(t, i, f & (kFirstAct << t));
+                        if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
+                    }
+                    if (same && (g & (kAct << t))) {
+                        if (!ready) before_scores(i + 1, g);
+                        ready = true;
+                        if (*abort) break;
+                        scores(t, i + 1);
+                    }
+                }
+                if (*abort) break;
+                tc::commit(&s_vempty[i & 1]);
+                mbar_arrive(&s_tempty[i % kDescs]);
+                if (i + 1 < total) {
+                    if (!ready) before_scores(i + 1, g);
+                    if (*abort) break;
+                    if (!same)
+                        for (int t = 0; t < 2; ++t)
+                            if (g & (kAct << t)) scores(t, i + 1);
+                    after_scores(i + 1, g);
+                }
+                f = g;
+            }
+            // every product issued has completed before tensor memory is released
+            tc::commit(&s_fin);
+            mbar_wait_bounded(&s_fin, 0, status);
+        }
+        __syncwarp();
+    } else if (warp >= kConvWarp) {
+        // ---- codes to fp16 operand tiles -----------------------------------------------------
+        const int ct = tid - kConvWarp * 32;                   // 0 .. 127
+        constexpr int NL = D == 128 ? 8 : 4;                   // 16-byte loads per thread and tile
+        // load x: chunk (ct & 3) + 4 (x & 1) of row (ct >> 2) + 32 (x >> 1)  (D = 128), or chunk ct & 3
+        // of row (ct >> 2) + 32 x: eight lanes then store to all banks
+        const int ch = ct & 3, rw = ct >> 2;
+        auto load = [&](const Desc &d, int kvl, uint4 (&r)[NL]) {
+            const bool plain = d.j0 >= d.lo && d.j0 + kTile <= d.hi;
+#pragma unroll
+            for (int x = 0; x < NL; ++x) {
+                const int row = rw + 32 * (D == 128 ? x >> 1 : x), c = D == 128 ? ch + 4 * (x & 1) : ch;
+                const int64_t off = d.off[kvl][row >> 3];
+                const int32_t j = d.j0 + row;
+                r[x] = make_uint4(0, 0, 0, 0);
+                if (off >= 0 && (plain || (j >= d.lo && j < d.hi)))
+                    r[x] = ld_codes(a.c.pool + off + (row & 7) * D + c * 16);
+            }
+        };
+        auto store = [&](uint32_t dst, const uint4 (&r)[NL]) {
+#pragma unroll
+            for (int x = 0; x < NL; ++x) {
+                const int row = rw + 32 * (D == 128 ? x >> 1 : x), blk = D == 128 ? x & 1 : 0;
+                const uint32_t at = dst + blk * (128 * 128) + row * 128;
+                uint32_t h[8];
+                decode4<FMT>(r[x].x, h[0], h[1]);
+                decode4<FMT>(r[x].y, h[2], h[3]);
+                decode4<FMT>(r[x].z, h[4], h[5]);
+                decode4<FMT>(r[x].w, h[6], h[7]);
+                sts128(at + (((2 * ch) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                sts128(at + (((2 * ch + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+            }
+        };
+        auto done = [&](uint64_t *bar) {
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(bar);
+        };
+        uint4 ra[NL], rb[NL];
+        uint32_t qe_par = 1;
+        wait_phase<false>(&s_tfull[0], 0, abort, status);
+        if (!*abort) load(desc[0], 0, ra);
+        for (int32_t i = 0; i < total && !*abort; ++i) {
+            const Desc &d = desc[i % kDescs];
+            load(d, 1, rb);
+            if (d.flags & kFirst) {
+                // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
+                wait_phase<false>(&s_qempty, qe_par, abort, status);
+                qe_par ^= 1;
+                if (*abort) break;
+                const int qc = ct & 7;
+                const int32_t nrows = d.nrows, steps = nrows > 128 ? 16 : 8;
+#pragma unroll 4
+                for (int s = 0; s < steps; ++s) {
+                    const int row = (ct >> 3) + 16 * s;
+                    const int32_t r = d.r0 + (row < nrows ? row : 0);
+                    const int32_t tok = a.group == 1 ? r : r / a.group;
+                    const __half *src = a.q + (int64_t)(d.row0 + tok) * a.q_stride +
+                                        ((int64_t)d.head * a.group + (r - tok * a.group)) * D + qc * 8;
+#pragma unroll
+                    for (int b = 0; b < NB; ++b) {
+                        uint4 v = make_uint4(0, 0, 0, 0);
+                        if (row < nrows) v = __ldg(reinterpret_cast<const uint4 *>(src + b * 64));
+                        sts128(q_sm + (row >> 7) * Sh::kQTile + b * (128 * 128) + (row & 127) * 128 + ((qc ^ (row & 7)) << 4),
+                               v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
+                    }
+                }
+                done(&s_qfull);
+            }
+            wait_phase<false>(&s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
+            if (*abort) break;
+            store(k_sm + (i & 1) * Sh::kKVTile, ra);
+            done(&s_kfull[i & 1]);
+            if (i + 1 < total) {
+                wait_phase<false>(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
+                if (*abort) break;
+                load(desc[(i + 1) % kDescs], 0, ra);
+            }
+            wait_phase<false>(&s_vempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
+            if (*abort) break;
+            store(v_sm + (i & 1) * Sh::kKVTile, rb);
+            done(&s_vfull[i & 1]);
+            if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
+        }
+    } else {
+        // ---- softmax: one row per thread -------------------------------------------------------
+        const int t = warp >> 2;                               // row tile
+        const uint32_t lane_base = (uint32_t)(warp & 3) << 21; // lane 32 (warp & 3) of tensor memory
+        const uint32_t ts = tm_s + 128 * t + lane_base, to = tm_o + D * t + lane_base;
+        const int row = tid & 127;
+        uint32_t s_par = 0, od_par = 0, j_par = 0;
+        float mx = -INFINITY, sum = 0.f;
+        bool any = false;
+        int32_t klo = 0, khi = 0;                              // keys that the row sees
+        for (int32_t i = 0; i < total; ++i) {
+            wait_phase<false>(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
+            if (*abort) break;
+            const Desc &d = desc[i % kDescs];
+            const uint32_t f = d.flags;
+            if (f & kFirst) {
+                mx = -INFINITY;
+                sum = 0.f;
+                any = false;
+                const Seq q = {d.row0, d.n, d.len};
+                const int32_t r = d.r0 + 128 * t + row, last = d.r0 + d.nrows - 1;
+                const int32_t tok = (r < last ? r : last) / a.group;
+                klo = first_key(a, q, tok);
+                khi = end_key(a, q, tok);
+            }
+            if (f & (kAct << t)) {
+                wait_phase<false>(&s_sfull[t], s_par, abort, status);
+                s_par ^= 1;
+                if (*abort) break;
+                tc::fence_after_sync();
+                const bool plain = f & kPlain;
+                const int32_t m0 = klo - d.j0;
+                const uint32_t mn = khi > klo ? (uint32_t)(khi - klo) : 0u;
+                const uint32_t ok = d.ok;
+                auto mask = [&](uint32_t (&x)[32], int h) {
+                    if (plain) return;
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) {
+                        const bool see = (uint32_t)(32 * h + k - m0) < mn && (ok >> (4 * h + k / 8) & 1u);
+                        if (!see) x[k] = 0xFF800000u;
+                    }
+                };
+                float top = -INFINITY;
+                uint32_t x[32];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    tc::ld_32x32b_x32(ts + 32 * h, x);
+                    tc::ld_wait();
+                    mask(x, h);
+                    const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
+                    const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
+                    const float kf[4] = {ks.x, ks.y, ks.z, ks.w}, lf[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        float m = __uint_as_float(x[8 * g]);
+#pragma unroll
+                        for (int k = 1; k < 8; ++k) m = fmaxf(m, __uint_as_float(x[8 * g + k]));
+                        top = fmaxf(top, fmaf(m, kf[g] * p.scale, lf[g]));
+                    }
+                }
+                // The running maximum follows only when a score passes it by 2^8, so that O is
+                // seldom rescaled; the weights stay below 2^8, far inside fp16.
+                const bool up = top > mx + 8.f;
+                if (__any_sync(~0u, up)) {
+                    const float nm = up ? top : mx;
+                    const float k = mx == -INFINITY ? 0.f : ex2(mx - nm);
+                    mx = nm;
+                    sum *= k;
+                    if (any) {
+                        const float kk = up ? k : 1.f;
+#pragma unroll
+                        for (int h = 0; h < D / 32; ++h) {
+                            tc::ld_32x32b_x32(to + 32 * h, x);
+                            tc::ld_wait();
+#pragma unroll
+                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * kk);
+                            tc::st_32x32b_x32(to + 32 * h, x);
+                        }
+                        tc::st_wait();
+                    }
+                }
+                any = true;
+                const float base = mx == -INFINITY ? 0.f : mx;
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    tc::ld_32x32b_x32(ts + 32 * h, x);
+                    tc::ld_wait();
+                    mask(x, h);
+                    const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
+                    const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
+                    const float4 li = *reinterpret_cast<const float4 *>(&d.li[4 * h]);
+                    const float kf[4] = {ks.x, ks.y, ks.z, ks.w}, lf[4] = {lv.x, lv.y, lv.z, lv.w};
+                    const float if_[4] = {li.x, li.y, li.z, li.w};
+                    uint32_t pk[16];
+#pragma unroll
+                    for (int g = 0; g < 4; ++g) {
+                        const float kx = kf[g] * p.scale, lx = lf[g] - base;
+                        float s = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float e0 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k]), kx, lx));
+                            const float e1 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k + 1]), kx, lx));
+                            s += e0 + e1;
+                            const __half2 hh = __floats2half2_rn(e0, e1);
+                            pk[4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                        }
+                        sum = fmaf(s, if_[g], sum);
+                    }
+                    // columns already read: 32 keys' weights take 16 of the 32 that their scores took
+                    tc::st_32x32b_x16(ts + 16 * h, pk);
+                }
+                tc::st_wait();
+                tc::fence_before_sync();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_pfull[t]);
+            }
+            const int32_t row0 = d.row0, head = d.head, r = d.r0 + 128 * t + row, c0 = d.c0, c1 = d.c1;
+            const bool live = 128 * t + row < d.nrows;
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
+            if (!(f & kLast)) continue;
+
+            // ---- the unit's end in this CTA ---------------------------------------------------
+            if (any) {
+                wait_phase<false>(&s_odone[t], od_par, abort, status);
+                od_par ^= 1;
+                if (*abort) break;
+                tc::fence_after_sync();
+            }
+            const int32_t tok = r / a.group;
+            const int64_t qh = (int64_t)head * a.group + (r - tok * a.group);
+            __half *out = a.out + (int64_t)(row0 + tok) * a.out_stride + qh * D;
+            auto put_lse = [&](float M, float L) {
+                if (a.lse)
+                    a.lse[(int64_t)(row0 + tok) * a.n_q + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            };
+            auto put = [&](int h, const float (&o)[32], float inv) {       // 32 channels
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint4 v;
+                    __half2 *hh = reinterpret_cast<__half2 *>(&v);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) hh[k] = __floats2half2_rn(o[8 * j + 2 * k] * inv, o[8 * j + 2 * k + 1] * inv);
+                    *reinterpret_cast<uint4 *>(out + 32 * h + 8 * j) = v;
+                }
+            };
+            float o[32];
+            auto own = [&](int h) {
+                uint32_t x[32];
+                if (any) {                                     // uniform over the warp
+                    tc::ld_32x32b_x32(to + 32 * h, x);
+                    tc::ld_wait();
+                }
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = any ? __uint_as_float(x[j]) : 0.f;
+            };
+            auto release = [&]() {
+                if (any) {
+                    tc::fence_before_sync();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_ofree[t]);
+                }
+            };
+            if (f & kWhole) {
+                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    own(h);
+                    if (live) put(h, o, inv);
+                }
+                release();
+                if (live) put_lse(mx, sum);
+                continue;
+            }
+            // a part of a unit: m and l of each row, and O by fours of channels, rows side by side
+            auto slot = [&](int32_t k) { return p.part + ((size_t)(2 * k + (k == c0 ? 1 : 0)) * 2 + t) * Sh::kPart; };
+            float *mine = slot((int32_t)blockIdx.x);
+            __stcg(mine + row, mx);
+            __stcg(mine + 128 + row, sum);
+            if (any) {
+#pragma unroll
+                for (int h = 0; h < D / 32; ++h) {
+                    own(h);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        __stcg(reinterpret_cast<float4 *>(mine + 256) + (8 * h + j) * 128 + row,
+                               make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
+                }
+            }
+            release();
+            __threadfence();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&s_join[t]);
+            wait_phase<false>(&s_join[t], j_par, abort, status);
+            if (*abort) break;
+            if (row == 0) {
+                __threadfence();
+                int32_t *cnt = p.count + 2 * c0 + t;
+                const int l = atomicAdd(cnt, 1) == c1 - c0;
+                if (l) *cnt = 0;
+                s_last[t] = l;
+                __threadfence();
+                mbar_arrive(&s_said[t]);
+            }
+            wait_phase<false>(&s_said[t], j_par, abort, status);
+            j_par ^= 1;
+            if (*abort) break;
+            if (!s_last[t] || !live) continue;
+            float M = -INFINITY;
+            for (int32_t k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + row));
+            const float B = M == -INFINITY ? 0.f : M;
+            float L = 0.f;
+            for (int32_t k = c0; k <= c1; ++k) L += __ldcg(slot(k) + 128 + row) * ex2(__ldcg(slot(k) + row) - B);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+#pragma unroll
+                for (int j = 0; j < 32; ++j) o[j] = 0.f;
+                for (int32_t k = c0; k <= c1; ++k) {
+                    const float *s = slot(k);
+                    const float m = __ldcg(s + row);
+                    if (m == -INFINITY) continue;              // nothing seen there: its O was not written
+                    const float e = ex2(m - B);
+#pragma unroll
+                    for (int j = 0; j < 8; ++j) {
+                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + 256) + (8 * h + j) * 128 + row);
+                        o[4 * j] = fmaf(v.x, e, o[4 * j]);
+                        o[4 * j + 1] = fmaf(v.y, e, o[4 * j + 1]);
+                        o[4 * j + 2] = fmaf(v.z, e, o[4 * j + 2]);
+                        o[4 * j + 3] = fmaf(v.w, e, o[4 * j + 3]);
+                    }
+                }
+                put(h, o, inv);
+            }
+            put_lse(M, L);
+        }
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    if (warp == kMmaWarp) {
+        tc::fence_after_sync();
+        tc::tmem_relinquish();
+        tc::tmem_dealloc(tmem, 512);
+    }
+}
+
+template <int D, int FMT>
+cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
+{
+    static std::mutex mu;
+    static bool set[64] = {};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    {
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 64 || !set[dev]) {
+            e = cudaFuncSetAttribute(attend_prefill_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                     (int)Shape<D>::kSmem);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) set[dev] = true;
+        }
+    }
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(num_sms);
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = Shape<D>::kSmem;
+    cfg.stream = stream;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p);
+}
+
+}  // namespace
+
+size_t prefill_workspace_bytes(int num_sms)
+{
+    return (size_t)num_sms * 4 * Shape<128>::kPart * 4 + (size_t)num_sms * 2 * 4;
+}
+
+cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
+                                  cudaStream_t stream, int *launches)
+{
+    PrefillParams p;
+    p.a = a;
+    p.small_rows = small_rows;
+    p.min_tiles = 2;
+    p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
+    p.q_sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
+    // masked scores are -infinity times this, so it may not be zero: at 2^-60 no score of fp16
+    // queries and 8-bit codes differs from zero
+    p.scale = a.scale_log2 < 0.f ? -a.scale_log2 : a.scale_log2;
+    if (p.scale < 0x1p-60f) p.scale = 0x1p-60f;
+    p.part = static_cast<float *>(ws);
+    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
+    cudaError_t e;
+    if (head_dim == 128)
+        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, num_sms, stream);
+    else
+        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, num_sms, stream);
+    if (e == cudaSuccess) ++*launches;
+    return e;
+}
+
+}  // namespace kv
+}  // namespace slora

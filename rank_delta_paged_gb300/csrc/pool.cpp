@@ -60,6 +60,7 @@ struct slora_pool {
 
 
     PlanScratch plan;
+    void *kv_scratch = nullptr;   // of the KV attention (pool_kv_scratch)
     std::vector<AdapterRec> adapters;
     int64_t launches = 0;  // kernels launched by this pool
     cudaEvent_t stage_event = nullptr;   // measurement hook: recorded between plan and delta
@@ -113,6 +114,7 @@ void free_pool_memory(slora_pool *p)
     if (p->dir_dev) cudaFree(p->dir_dev);
     if (p->status_dev) cudaFree(p->status_dev);
     if (p->plan.base) cudaFree(p->plan.base);
+    if (p->kv_scratch) cudaFree(p->kv_scratch);
     if (p->staging) cudaFree(p->staging);
     if (p->release_event) cudaEventDestroy(p->release_event);
     if (p->load_event) cudaEventDestroy(p->load_event);
@@ -1107,5 +1109,25 @@ slora_status slora::pool_hot_path(slora_pool_t p, PoolHotPath *out)
     out->num_sms = p->num_sms;
     out->max_rank = p->max_rank;
     out->launches = &p->launches;
+    return SLORA_OK;
+}
+
+slora_status slora::pool_kv_scratch(slora_pool_t p, size_t bytes, void **out)
+{
+    if (!p || !out)
+        return fail(SLORA_ERR_INVALID_ARG, "null pool");
+    if (!p->kv_scratch) {
+        void *m = nullptr;
+        CUDA_TRY(cudaMalloc(&m, bytes));
+        cudaError_t e = cudaMemset(m, 0, bytes);
+        if (e == cudaSuccess)
+            e = cudaDeviceSynchronize();
+        if (e != cudaSuccess) {
+            cudaFree(m);
+            return fail(SLORA_ERR_CUDA, "KV scratch: %s", cudaGetErrorString(e));
+        }
+        p->kv_scratch = m;
+    }
+    *out = p->kv_scratch;
     return SLORA_OK;
 }
