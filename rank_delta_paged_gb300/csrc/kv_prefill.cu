@@ -436,85 +436,77 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         // ---- products --------------------------------------------------------------------
         if (lane == 0) {
             constexpr uint32_t id_s = tc::idesc_f16_f32(128, kTile, 0, 0), id_o = tc::idesc_f16_f32(128, D, 0, 1);
-            uint32_t q_par = 0, p_par[2] = {0, 0}, of_par[2] = {1, 1};
-            auto flags_of = [&](int32_t i) {
-                wait_phase<false>(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
-                return *abort ? 0u : desc[i % kDescs].flags;
-            };
-            auto scores = [&](int t, int32_t i) {
-                const uint32_t qa = q_sm + t * Sh::kQTile, ka = k_sm + (i & 1) * Sh::kKVTile;
-#pragma unroll
-                for (int kk = 0; kk < D / 16; ++kk) {
-                    const uint32_t o = (kk >> 2) * (128 * 128) + (kk & 3) * 32;
-                    tc::mma_f16(tm_s + 128 * t, tc::smem_desc_sw128(qa + o, 16, 1024),
-                                tc::smem_desc_sw128(ka + o, 16, 1024), id_s, kk != 0);
-                }
-                tc::commit(&s_sfull[t]);
-            };
-            auto values = [&](int t, int32_t i, bool first) {
-                const uint32_t va = v_sm + (i & 1) * Sh::kKVTile;
-#pragma unroll
-                for (int kk = 0; kk < kTile / 16; ++kk)
-                    tc::mma_f16_ts(tm_o + D * t, tm_s + 128 * t + kk * 8,
-                                   tc::smem_desc_sw128(va + kk * 2048, 128 * 128, 1024), id_o, !(first && kk == 0));
-            };
-            // what S of tile i needs: the keys and, for a new unit, its rows
-            auto before_scores = [&](int32_t i, uint32_t f) {
-                wait_phase<false>(&s_kfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
-                if (f & kFirst) {
-                    wait_phase<false>(&s_qfull, q_par, abort, status);
-                    q_par ^= 1;
-                }
-                tc::fence_after_sync();
-            };
-            auto after_scores = [&](int32_t i, uint32_t f) {
-                tc::commit(&s_kempty[i & 1]);
-                if (f & kLast) tc::commit(&s_qempty);
-            };
-            uint32_t f = flags_of(0);
-            if (!*abort) before_scores(0, f);
-            if (!*abort) {
-                for (int t = 0; t < 2; ++t)
-                    if (f & (kAct << t)) scores(t, 0);
-                after_scores(0, f);
-            }
-            for (int32_t i = 0; i < total && !*abort; ++i) {
+            // Descriptors: 16 channels are 32 bytes of a swizzled row of Q and K, 64 a block of 128
+            // rows; 16 keys are 16 rows of V.  Only the low words differ.
+            const uint64_t dq = tc::smem_desc_sw128(q_sm, 16, 1024), dk = tc::smem_desc_sw128(k_sm, 16, 1024);
+            const uint64_t dv = tc::smem_desc_sw128(v_sm, 128 * 128, 1024);
+            uint32_t q_par = 0, p_par = 0, of_par = 3;           // bit t: row tile t
+            uint32_t f = 0;
+            // Tile i's weights times its values, and tile i + 1's scores: within a unit by turns, so that each
+            // row tile's softmax has the other's products to run under; at a unit's end the new
+            // unit's scores after both, since they wait for its rows.
+            for (int32_t i = -1; i < total && !*abort; ++i) {
                 uint32_t g = 0;
-                if (i + 1 < total) g = flags_of(i + 1);
-                if (*abort) break;
-                const bool same = i + 1 < total && !(g & kFirst);      // the next tile is of this unit
-                wait_phase<false>(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
+                const bool more = i + 1 < total;
+                if (more) {
+                    wait_phase<false>(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
+                    if (*abort) break;
+                    g = desc[(i + 1) % kDescs].flags;
+                }
+                const bool same = more && !(g & kFirst);
+                if (i >= 0) wait_phase<false>(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
                 bool ready = false;
-                for (int t = 0; t < 2 && !*abort; ++t) {
-                    if (f & (kAct << t)) {
-                        wait_phase<false>(&s_pfull[t], p_par[t], abort, status);
-                        p_par[t] ^= 1;
-                        if (f & (kFirstAct << t)) {
-                            wait_phase<false>(&s_ofree[t], of_par[t], abort, status);
-                            of_par[t] ^= 1;
+#pragma unroll 1
+                for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4) && !*abort; ++k) {
+                    const uint32_t t = k & 1;
+                    if (k < 2 && (f & (kAct << t))) {
+                        wait_phase<false>(&s_pfull[t], p_par >> t & 1u, abort, status);
+                        p_par ^= 1u << t;
+                        const bool first = f & (kFirstAct << t);
+                        if (first) {
+                            wait_phase<false>(&s_ofree[t], of_par >> t & 1u, abort, status);
+                            of_par ^= 1u << t;
                         }
                         if (*abort) break;
                         tc::fence_after_sync();
-                        values(t, i, f & (kFirstAct << t));
+                        const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
+                        const uint32_t o = tm_o + D * t, w = tm_s + 128 * t;
+                        tc::mma_f16_ts(o, w, d, id_o, !first);
+#pragma unroll
+                        for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
                         if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
                     }
-                    if (same && (g & (kAct << t))) {
-                        if (!ready) before_scores(i + 1, g);
-                        ready = true;
-                        if (*abort) break;
-                        scores(t, i + 1);
+                    if (more && (same || k >= 2)) {
+                        if (!ready) {
+                            ready = true;
+                            wait_phase<false>(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
+                            if (g & kFirst) {
+                                wait_phase<false>(&s_qfull, q_par, abort, status);
+                                q_par ^= 1;
+                            }
+                            if (*abort) break;
+                            tc::fence_after_sync();
+                        }
+                        if (g & (kAct << t)) {
+                            const uint64_t x = dq + t * (Sh::kQTile >> 4);
+                            const uint64_t y = dk + (uint32_t)(((i + 1) & 1) * (Sh::kKVTile >> 4));
+#pragma unroll
+                            for (int kk = 0; kk < D / 16; ++kk) {
+                                const uint32_t step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                                tc::mma_f16(tm_s + 128 * t, x + step, y + step, id_s, kk != 0);
+                            }
+                            tc::commit(&s_sfull[t]);
+                        }
                     }
                 }
                 if (*abort) break;
-                tc::commit(&s_vempty[i & 1]);
-                mbar_arrive(&s_tempty[i % kDescs]);
-                if (i + 1 < total) {
-                    if (!ready) before_scores(i + 1, g);
-                    if (*abort) break;
-                    if (!same)
-                        for (int t = 0; t < 2; ++t)
-                            if (g & (kAct << t)) scores(t, i + 1);
-                    after_scores(i + 1, g);
+                if (i >= 0) {
+                    tc::commit(&s_vempty[i & 1]);
+                    mbar_arrive(&s_tempty[i % kDescs]);
+                }
+                if (more) {
+                    tc::commit(&s_kempty[(i + 1) & 1]);
+                    if (g & kLast) tc::commit(&s_qempty);
                 }
                 f = g;
             }
@@ -542,7 +534,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     r[x] = ld_codes(a.c.pool + off + (row & 7) * D + c * 16);
             }
         };
-        auto store = [&](uint32_t dst, const uint4 (&r)[NL]) {
+        auto store = [&](uint32_t dst, uint4 (&r)[NL]) {
+            // the conversions stay behind the waits before this call: moved up to the loads, they
+            // would wait for them there
+#pragma unroll
+            for (int x = 0; x < NL; ++x) asm volatile("" : "+r"(r[x].x), "+r"(r[x].y), "+r"(r[x].z), "+r"(r[x].w));
 #pragma unroll
             for (int x = 0; x < NL; ++x) {
                 const int row = rw + 32 * (D == 128 ? x >> 1 : x), blk = D == 128 ? x & 1 : 0;
@@ -649,9 +645,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                         if (!see) x[k] = 0xFF800000u;
                     }
                 };
+                // The loops over a tile's columns stay rolled: unrolled, the roles' code does not fit the
+                // instruction caches (0.39 PFLOP/s on a long chunk).
                 float top = -INFINITY;
                 uint32_t x[32];
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     tc::ld_32x32b_x32(ts + 32 * h, x);
                     tc::ld_wait();
@@ -677,7 +675,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     sum *= k;
                     if (any) {
                         const float kk = up ? k : 1.f;
-#pragma unroll
+#pragma unroll 1
                         for (int h = 0; h < D / 32; ++h) {
                             tc::ld_32x32b_x32(to + 32 * h, x);
                             tc::ld_wait();
@@ -690,7 +688,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 }
                 any = true;
                 const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     tc::ld_32x32b_x32(ts + 32 * h, x);
                     tc::ld_wait();
@@ -772,7 +770,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             };
             if (f & kWhole) {
                 const float inv = sum == 0.f ? 0.f : 1.f / sum;
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < D / 32; ++h) {
                     own(h);
                     if (live) put(h, o, inv);
@@ -787,7 +785,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             __stcg(mine + row, mx);
             __stcg(mine + 128 + row, sum);
             if (any) {
-#pragma unroll
+#pragma unroll 1
                 for (int h = 0; h < D / 32; ++h) {
                     own(h);
 #pragma unroll
