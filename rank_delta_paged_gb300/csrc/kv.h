@@ -8,6 +8,7 @@
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
+#include "ptx.h"
 #include "slora.h"
 
 namespace slora {
@@ -60,6 +61,7 @@ struct AttendArgs {
     float *lse;
     int64_t q_stride, out_stride;
     int32_t n_q, group;
+    uint32_t group_inverse;             // ceil(2^32 / group), 0 for 1
     float scale_log2;                   // softmax scale * log2(e)
     int32_t causal, window;
 };
@@ -95,6 +97,20 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs &a, int32_t s, int32_t 
     return q;
 }
 
+// r / group, 0 <= r < 2^31: the product with the inverse is the quotient or one more.
+__device__ __forceinline__ int32_t div_group(const AttendArgs &a, int32_t r)
+{
+    if (a.group_inverse == 0) return r;
+    const int32_t q = (int32_t)__umulhi((uint32_t)r, a.group_inverse);
+    return q * a.group > r ? q - 1 : q;
+}
+
+// 64-bit quotients are long code; none is on a path that matters.
+static __device__ __noinline__ int32_t div_list(int64_t x, int64_t y)
+{
+    return (int32_t)(x / y);
+}
+
 // First key that any of the rows [r0, r1) of new tokens sees, and one past the last; tokens
 // counted from the sequence's first new one.
 __device__ __forceinline__ int32_t first_key(const AttendArgs &a, const Seq &q, int32_t tok)
@@ -108,6 +124,28 @@ __device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, in
     if (!a.causal) return q.len;
     const int32_t p = q.len - q.n + tok + 1;
     return p > 0 ? p : 0;
+}
+
+// Bounded wait on an mbarrier phase, as wait_phase of ptx.h: after the first timeout in the CTA
+// (*abort, SLORA_DEV_TIMEOUT) every wait returns at once.  Its loop stays rolled: these kernels
+// have some thirty waits, and unrolled ones made 250 KB of code, fetched from L2 again and again
+// (a long chunk of a prompt took 1.5 times as long).
+__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
+{
+    if (mbar_try_wait(bar, parity)) return;
+    uint64_t t0 = 0;
+#pragma unroll 1
+    for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
+        if ((it & 63u) != 0) continue;
+        if (*abort) return;
+        const uint64_t now = global_timer_ns();
+        if (t0 == 0) t0 = now;
+        if (now - t0 > kWaitLimitNs) {
+            set_status(status, SLORA_DEV_TIMEOUT);
+            *abort = 1;
+            return;
+        }
+    }
 }
 
 // ---- codes ---------------------------------------------------------------------------
@@ -189,7 +227,7 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
 
 // The rows of sequences with more than small_rows rows per KV head.
 size_t prefill_workspace_bytes(int num_sms);
-cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
+cudaError_t launch_attend_prefill(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
                                   cudaStream_t stream, int *launches);
 
 }  // namespace kv

@@ -205,6 +205,7 @@ __device__ __forceinline__ void few_rows(const AppendArgs &a, int32_t u0, int32_
                 e = old;
             } else {
                 const float unit = pow2(old - e);
+#pragma unroll 1
                 for (int r = 0; r < held; ++r) {
                     uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
                     *w = rescale8<FMT>(*w, unit);
@@ -382,6 +383,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
                 e = old;
             } else {
                 const float unit = pow2(old - e);
+#pragma unroll 1
                 for (int r = grp; r < held; r += GROUPS) {
                     uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
                     *w = rescale8<FMT>(*w, unit);

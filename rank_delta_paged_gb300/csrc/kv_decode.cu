@@ -146,7 +146,7 @@ __device__ __forceinline__ void seq_tiles(const DecodeParams &p, const Seq &q, i
     if (q.n == 0 || rows > p.small_rows) return;
     const int32_t lo = first_key(p.a, q, 0) / kTile, hi = (end_key(p.a, q, q.n - 1) + kTile - 1) / kTile;
     *tiles = hi > lo ? hi - lo : 1;     // a row that sees nothing still writes zeros
-    *groups = (int32_t)((rows + p.rows - 1) / p.rows);
+    *groups = (int32_t)((rows + p.rows - 1) >> (p.rows == 8 ? 3 : 4));
     *first = lo;
 }
 
@@ -186,8 +186,10 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     const int S = a.b.S;
     const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
     int32_t bad = 0;
+#pragma unroll 1
     for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
         int64_t t = 0;
+#pragma unroll 1
         for (int64_t s = (int64_t)c * per + lane; s < S && s < (int64_t)(c + 1) * per; s += 32) {
             int32_t tiles, groups, first;
             seq_tiles(p, load_seq(a, (int32_t)s, &bad), &tiles, &groups, &first);
@@ -208,7 +210,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
     const int64_t before = W - v0 - v1;          // tiles before chunk 2 * lane
     W = __shfl_sync(~0u, W, 31);
-    int64_t run = (W + gridDim.x - 1) / gridDim.x;
+    int64_t run = div_list(W + gridDim.x - 1, gridDim.x);
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
     if (w0 >= w1) return;
@@ -241,9 +243,10 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 seq_tiles(p, q, &tiles, &groups, &first);
             }
         };
-        hold(s32);
         int at_lane = 0;
-        for (;; hold(s32 += 32)) {
+#pragma unroll 1
+        for (;; s32 += 32) {
+            hold(s32);
             if (s32 >= S) {       // the lengths changed under the call: nothing to copy
                 if (lane == 0) {
                     set_status(status, SLORA_DEV_BAD_LENGTH);
@@ -269,9 +272,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         int32_t u_tiles = __shfl_sync(~0u, tiles, at_lane), u_groups = __shfl_sync(~0u, groups, at_lane);
         int32_t u_first = __shfl_sync(~0u, first, at_lane);
         int64_t in_seq = w0 - base;
-        int32_t head = (int32_t)(in_seq / ((int64_t)u_tiles * u_groups));
+        int32_t head = div_list(in_seq, (int64_t)u_tiles * u_groups);
         in_seq -= (int64_t)head * u_tiles * u_groups;
-        int32_t grp = (int32_t)(in_seq / u_tiles), tile = (int32_t)(in_seq - (int64_t)grp * u_tiles);
+        int32_t grp = div_list(in_seq, u_tiles), tile = (int32_t)(in_seq - (int64_t)grp * u_tiles);
         Seq u;
         u.row0 = __shfl_sync(~0u, q.row0, at_lane);
         u.n = __shfl_sync(~0u, q.n, at_lane);
@@ -289,8 +292,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             un.whole = u0 >= w0 && u1 <= w1;
             un.c0 = un.c1 = 0;
             if (!un.whole) {
-                un.c0 = (int32_t)(u0 / run);
-                un.c1 = (int32_t)((u1 - 1) / run);
+                un.c0 = div_list(u0, run);
+                un.c1 = div_list(u1 - 1, run);
             }
             un.r0 = grp * p.rows;
             const int32_t rows = u.n * a.group, r1 = un.r0 + p.rows < rows ? un.r0 + p.rows : rows;
@@ -299,12 +302,12 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             un.plain_lo = un.lo;
             un.plain_hi = un.hi;
             if (u.n > 1) {
-                un.plain_lo = first_key(a, u, (r1 - 1) / a.group);
-                un.plain_hi = end_key(a, u, un.r0 / a.group);
+                un.plain_lo = first_key(a, u, div_group(a, r1 - 1));
+                un.plain_hi = end_key(a, u, div_group(a, un.r0));
             }
             un.table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
         };
-        enter(w0);
+        bool fresh = true;              // the unit has yet to be entered
 
         // A batch of tiles at a time, `lanes` lanes each, one lane per box (R rows of keys or
         // values): their page ids and their exponents are read together, one batch ahead.
@@ -350,13 +353,18 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     mi[2] = make_int4(head, un.r0, un.c0, un.c1);
                 }
             };
-            if (tile + per_batch < u_tiles && count == per_batch) {     // all within the unit, not at its end
+            if (!fresh && tile + per_batch < u_tiles && count == per_batch) {     // all within the unit, not at its end
                 fill(tile + my_tile, my_tile == 0 && ahead == w0, ahead + my_tile == w1 - 1);
                 tile += per_batch;
                 ahead += per_batch;
                 return count;
             }
+#pragma unroll 1
             for (int b = 0; b < count; ++b) {
+                if (fresh) {
+                    enter(ahead + b);
+                    fresh = false;
+                }
                 if (b == my_tile) fill(tile, b == 0 && ahead == w0, ahead + b == w1 - 1);
                 // step to the next tile
                 if (++tile == u_tiles) {
@@ -367,6 +375,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                             head = 0;
                             if (ahead + b + 1 < w1) {
                                 unsigned next;
+#pragma unroll 1
                                 while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
                                     s32 += 32;
                                     at_lane = -1;
@@ -388,7 +397,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                             }
                         }
                     }
-                    enter(ahead + b + 1);
+                    fresh = true;
                 }
             }
             ahead += count;
@@ -434,22 +443,27 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
             } else {
                 mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
+#pragma unroll 1
                 for (int x = 0; x < 8; ++x)
                     if (ok >> x & 1u) copy(x, 0, m.row[x], m.page[0][x], m.page[1][x]);
             }
         };
         // Two batches lie between the reading of a batch's page ids and of its exponents, and two more
         // between those and their use: under load either read takes a microsecond or two.
-        Box b0, b1, b2, b3, b4;
-        int n0 = describe(b0), n1 = describe(b1);
-        int32_t e0 = exponent_of(b0), e1 = exponent_of(b1), e2;
-        int n2 = describe(b2), n3 = describe(b3), n4;
+        const Box none = {false, 0, 0};
+        Box b0 = none, b1 = none, b2 = none, b3 = none, b4;
+        int n0 = 0, n1 = 0, n2 = 0, n3 = 0, n4;
+        int32_t e0 = 0, e1 = 0, e2;
         int batch = 0, stage = 0;
         uint32_t parity = 1;
         int32_t issued = 0;
-        for (; n0 > 0 && !*abort; b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
+#pragma unroll 1
+        for (int step = 0;;
+             ++step, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
             e2 = exponent_of(b2);
             n4 = describe(b4);
+            if (step < 4) continue;
+            if (n0 == 0 || *abort) break;
             // a box needs both its keys and its values: bits 2 gl of `have`
             unsigned have = __ballot_sync(~0u, b0.want);
             have &= have >> 1 & 0x55555555u;
@@ -489,8 +503,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
             }
             __syncwarp();
+#pragma unroll 1
             for (int t = 0; t < n0; ++t, ++issued) {
-                wait_phase<false>(&s_empty[stage], parity, abort, status);
+                wait_bar(&s_empty[stage], parity, abort, status);
                 if (*abort) break;
                 if (lane == 0) copy_tile(meta[(batch << batch_log) + t], stage);
                 if (++stage == NS) {
@@ -501,9 +516,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (++batch == n_batches) batch = 0;
         }
         // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
-        for (int i = 0; i < NS && i < issued; ++i) {
+        volatile int gone = 0;
+#pragma unroll 1
+        for (int i = 0; i < NS && i < issued && !gone; ++i) {
             const int t = issued - 1 - i;
-            if (!mbar_wait_bounded(&s_full[t % NS], (uint32_t)(t / NS & 1), status)) break;
+            wait_bar(&s_full[t % NS], (uint32_t)(t / NS & 1), &gone, status);
         }
         return;
     }
@@ -525,7 +542,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     auto meet = [&](int k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_merge[k]);
-        wait_phase<false>(&s_merge[k], mparity[k], abort, status);
+        wait_bar(&s_merge[k], mparity[k], abort, status);
         mparity[k] ^= 1;
         return *abort == 0;
     };
@@ -538,7 +555,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         for (int t = 0; t < NT; ++t) {
             const int r = 8 * t + g;
             const bool live = r < nrows;
-            const int tok = a.group == 1 ? m.r0 + r : (m.r0 + r) / a.group, hd = (m.r0 + r) - tok * a.group;
+            const int tok = div_group(a, m.r0 + r), hd = (m.r0 + r) - tok * a.group;
             const __half *src = a.q + (int64_t)(m.row0 + tok) * a.q_stride + ((int64_t)m.head * a.group + hd) * D;
 #pragma unroll
             for (int i = 0; i < KS; ++i) {
@@ -550,7 +567,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         }
     };
     for (int32_t it = 0; it < total; ++it) {
-        wait_phase<false>(&s_full[stage], parity, abort, status);
+        wait_bar(&s_full[stage], parity, abort, status);
         if (*abort) break;
         const Meta &m = meta[it % kDescs];
         const int4 flags = *reinterpret_cast<const int4 *>(&m.plain);
@@ -607,7 +624,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         // the next unit's rows, while this one's last tile is finished
         if (last && it + 1 < total) {
             const bool wrap = stage + 1 == NS;
-            wait_phase<false>(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status);
+            wait_bar(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status);
             if (*abort) break;
             load_q(meta[(it + 1) % kDescs]);
         }
@@ -632,7 +649,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
 #pragma unroll
                 for (int x = 0; x < 2; ++x) {
                     const int r = 8 * t + 2 * c + x;
-                    const int tok = (m.r0 + (r < nrows ? r : 0)) / a.group;
+                    const int tok = div_group(a, m.r0 + (r < nrows ? r : 0));
                     const int lo = first_key(a, q, tok), hi = end_key(a, q, tok);
                     if (!(ok0 && j0 >= lo && j0 < hi)) sc[t][x] = -INFINITY;
                     if (!(ok1 && j1 >= lo && j1 < hi)) sc[t][2 + x] = -INFINITY;
@@ -750,7 +767,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         if (!meet(0)) break;
         float *part = p.part + (size_t)(2 * blockIdx.x + ((int)blockIdx.x == c0 ? 1 : 0)) * kPartStride;
         auto emit = [&](int r, int d, float2 v, float M, float L) {
-            const int tok = (r0 + r) / a.group, hd = (r0 + r) - tok * a.group;
+            const int tok = div_group(a, r0 + r), hd = (r0 + r) - tok * a.group;
             const int64_t qh = (int64_t)head * a.group + hd;
             const float inv = L == 0.f ? 0.f : 1.f / L;
             __half2 h = __floats2half2_rn(v.x * inv, v.y * inv);
@@ -759,6 +776,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 a.lse[(int64_t)(row0 + tok) * a.n_q + qh] =
                     L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
         };
+#pragma unroll 1
         for (int i = tid; i < live * (D / 2); i += 32 * kConsumers) {
             const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
             float M = -INFINITY;
@@ -797,10 +815,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 __threadfence();
                 mbar_arrive(&s_merge[2]);
             }
-            wait_phase<false>(&s_merge[2], jparity, abort, status);
+            wait_bar(&s_merge[2], jparity, abort, status);
             if (*abort) break;
             jparity ^= 1;
             if (s_last) {
+#pragma unroll 1
                 for (int i = tid; i < live * (D / 2); i += 32 * kConsumers) {
                     const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
                     auto slot = [&](int k) { return p.part + (size_t)(2 * k + (k == c0 ? 1 : 0)) * kPartStride; };

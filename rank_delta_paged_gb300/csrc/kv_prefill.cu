@@ -12,11 +12,13 @@
 // converted once per unit and tile for both row tiles (a sixteenth of the exponentials' work).
 //
 // Per CTA (one per SM): warps 0-3 and 4-7 are the softmax of row tile 0 and 1, a row per
-// thread, so a row's maximum and sum need no exchange; warps 8-11 load codes, convert them and
-// write the swizzled operand tiles (K by rows, V as it stands: its channels run along N); one
-// thread of warp 12 issues the products in the order O_0 += P_0 V, S_0 = Q_0 K', O_1 += P_1 V,
-// S_1 = Q_1 K' so that one row tile's softmax runs under the other's products; warp 13 walks the
-// work list and looks up pages and exponents some tiles ahead.
+// thread, so a row's maximum and sum need no exchange; warp 13 walks the work list, looks up
+// pages and exponents some tiles ahead and copies the codes by tensor maps into a ring of pieces
+// of 64 tokens; warps 8-11 convert them into the swizzled operand tiles (K by rows, V as it
+// stands: its channels run along N); one thread of warp 12 issues the products in the order
+// O_0 += P_0 V, S_0 = Q_0 K', O_1 += P_1 V, S_1 = Q_1 K' so that one row tile's softmax runs
+// under the other's products.  The roles' inner loops are kept short: with 14 warps in four
+// programs, straight-line code is fetched again for every tile, and the warps wait for that.
 //
 // The key tiles of all units form one list, of which every CTA takes an equal run; a unit that
 // is cut between CTAs is joined by the last of them to finish, in the order of the list.
@@ -39,7 +41,6 @@ constexpr int kThreads = 448;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
 constexpr int kSeqChunks = 64;
 constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
-constexpr int kAhead = 4;
 
 enum : uint32_t {
     kFirst = 1, kLast = 2, kWhole = 4, kPlain = 8,
@@ -49,7 +50,8 @@ enum : uint32_t {
 };
 
 struct Desc {
-    int64_t off[2][16];     // keys and values: bytes from the pool's start to the first row of 8 tokens
+    int32_t page[2][16];    // keys' and values' page of 8 tokens
+    int32_t row[16];        // and the first row there of their box of 16 (8) tokens
     float ks[16];           // 2^exponent of the key pages, per 8 tokens
     float lv[16];           // exponent of the value pages
     float li[16];           // 2^-exponent of the value pages
@@ -69,13 +71,17 @@ struct Shape {
     static constexpr int kBlocks = D / 64;                   // 64-channel blocks of 128-byte rows
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kKVTile = kTile * D * 2;
-    static constexpr size_t kSmem = 1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kDescs * sizeof(Desc);
+    static constexpr int kPiece = 64 * D;                    // codes of 64 tokens, keys or values
+    static constexpr int kPieces = D == 128 ? 3 : 6;
+    static constexpr size_t kSmem =
+        1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kPieces * kPiece + kDescs * sizeof(Desc);
     static constexpr int kPart = 2 * 128 + 128 * D;          // floats of a row tile's partial result: m, l, O
 };
 
 struct PrefillParams {
     AttendArgs a;
     int32_t small_rows;    // sequences with at most this many rows are another kernel's
+    int32_t box_rows;      // 16 if blocks are multiples of 16 tokens, else 8
     int32_t min_tiles;
     uint32_t bt_inverse;
     uint32_t q_sign;       // the sign of the softmax scale, applied to Q, so that larger products are larger scores
@@ -90,12 +96,36 @@ __device__ __forceinline__ float ex2(float x)
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-__device__ __forceinline__ uint4 ld_codes(const uint8_t *p)
+// Two fp32 numbers at a time.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int32_t c1, int32_t c2, uint64_t *bar)
+{
+    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
+                 "%3, %4}], [%5];" ::"r"(dst),
+                 "l"(map), "r"(0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
+                 : "memory");
+}
+__device__ __forceinline__ uint4 lds128(uint32_t ad)
 {
     uint4 v;
-    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.b32 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
-                 : "l"(p));
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ad));
     return v;
 }
 __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -110,8 +140,8 @@ struct Tiles {
 };
 __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, int32_t r0, int32_t r1, Tiles &t)
 {
-    t.k0 = first_key(a, q, r0 / a.group);
-    t.k1 = end_key(a, q, (r1 - 1) / a.group);
+    t.k0 = first_key(a, q, div_group(a, r0));
+    t.k1 = end_key(a, q, div_group(a, r1 - 1));
     t.lo = t.k0 / kTile;
     t.hi = (t.k1 + kTile - 1) / kTile;
     if (t.hi <= t.lo) t.hi = t.lo + 1;
@@ -120,7 +150,7 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, in
         const int32_t x0 = r0 + 128 * i, x1 = r1 < x0 + 128 ? r1 : x0 + 128;
         t.b[i] = t.e[i] = 0;
         if (x0 < x1) {
-            const int32_t k0 = first_key(a, q, x0 / a.group), k1 = end_key(a, q, (x1 - 1) / a.group);
+            const int32_t k0 = first_key(a, q, div_group(a, x0)), k1 = end_key(a, q, div_group(a, x1 - 1));
             if (k1 > k0) {
                 t.b[i] = k0 / kTile;
                 t.e[i] = (k1 + kTile - 1) / kTile;
@@ -131,20 +161,23 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, in
 __device__ __forceinline__ int32_t unit_count(const AttendArgs &a, const Seq &q, int32_t rows, int32_t rt)
 {
     const int32_t r0 = rt * kRows, r1 = rows < r0 + kRows ? rows : r0 + kRows;
-    const int32_t lo = first_key(a, q, r0 / a.group) / kTile, hi = (end_key(a, q, (r1 - 1) / a.group) + kTile - 1) / kTile;
+    const int32_t lo = first_key(a, q, div_group(a, r0)) / kTile, hi = (end_key(a, q, div_group(a, r1 - 1)) + kTile - 1) / kTile;
     return hi > lo ? hi - lo : 1;
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p)
+__global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p,
+                                                                     const __grid_constant__ PageMaps maps)
 {
     using Sh = Shape<D>;
     constexpr int NB = Sh::kBlocks;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t q_sm = (smem_u32(smem_raw) + 1023) & ~1023u;      // two row tiles
     const uint32_t k_sm = q_sm + 2 * Sh::kQTile, v_sm = k_sm + 2 * Sh::kKVTile;
-    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (v_sm + 2 * Sh::kKVTile - smem_u32(smem_raw)));
+    const uint32_t raw_sm = v_sm + 2 * Sh::kKVTile;
+    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (raw_sm + Sh::kPieces * Sh::kPiece - smem_u32(smem_raw)));
     __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
+    __shared__ uint64_t s_rfull[Sh::kPieces], s_rempty[Sh::kPieces];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_fin;
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
@@ -170,6 +203,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             mbar_init(&s_join[i], 4);
             mbar_init(&s_said[i], 1);
         }
+        for (int i = 0; i < Sh::kPieces; ++i) {
+            mbar_init(&s_rfull[i], 1);
+            mbar_init(&s_rempty[i], 4);
+        }
         mbar_init(&s_qfull, 4);
         mbar_init(&s_qempty, 1);
         mbar_init(&s_fin, 1);
@@ -183,13 +220,16 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     const int S = a.b.S;
     const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
     int32_t bad = 0;
+#pragma unroll 1
     for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
         int64_t t = 0;
+#pragma unroll 1
         for (int64_t s = (int64_t)c * per; s < S && s < (int64_t)(c + 1) * per; s += 32) {
             Seq q = {0, 0, 0};
             if (s + lane < S) q = load_seq(a, (int32_t)s + lane, &bad);
             const int64_t rows64 = (int64_t)q.n * a.group;
             unsigned big = __ballot_sync(~0u, rows64 > p.small_rows && q.n > 0);
+#pragma unroll 1
             while (big) {
                 const int l = __ffs(big) - 1;
                 big &= big - 1;
@@ -198,6 +238,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 u.n = __shfl_sync(~0u, q.n, l);
                 u.len = __shfl_sync(~0u, q.len, l);
                 const int32_t rows = u.n * a.group;
+#pragma unroll 1
                 for (int32_t rt = lane; rt * kRows < rows; rt += 32) t += unit_count(a, u, rows, rt);
             }
         }
@@ -215,7 +256,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     }
     const int64_t before = W - v0 - v1;
     W = __shfl_sync(~0u, W, 31);
-    int64_t run = (W + gridDim.x - 1) / gridDim.x;
+    int64_t run = div_list(W + gridDim.x - 1, gridDim.x);
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
     if (w0 >= w1) return;
@@ -245,20 +286,18 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         int32_t s32 = chunk * per, at_lane = -1;
         Seq q, u = {0, 0, 0};
         unsigned big = 0;
-        auto hold = [&]() {
-            q = Seq{0, 0, 0};
-            int32_t ignore;
-            if (s32 + lane < S) q = load_seq(a, s32 + lane, &ignore);
-            big = __ballot_sync(~0u, q.n > 0 && (int64_t)q.n * a.group > p.small_rows);
-        };
-        hold();
+        s32 -= 32;
         int32_t rows = 0, head = 0, rt = 0;
         // the next sequence with work; false if there is none
         auto next_seq = [&]() {
+#pragma unroll 1
             while (big == 0) {
                 s32 += 32;
                 if (s32 >= S) return false;
-                hold();
+                q = Seq{0, 0, 0};
+                int32_t ignore;
+                if (s32 + lane < S) q = load_seq(a, s32 + lane, &ignore);
+                big = __ballot_sync(~0u, q.n > 0 && (int64_t)q.n * a.group > p.small_rows);
             }
             at_lane = __ffs(big) - 1;
             big &= big - 1;
@@ -270,13 +309,15 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             return true;
         };
         bool found = false;
+#pragma unroll 1
         while (next_seq()) {
             int64_t t = 0;
+#pragma unroll 1
             for (int32_t i = lane; i * kRows < rows; i += 32) t += unit_count(a, u, rows, i);
 #pragma unroll
             for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
             if (base + t * a.c.n_kv > w0) {
-                head = (int32_t)((w0 - base) / t);
+                head = div_list(w0 - base, t);
                 base += head * t;
                 found = true;
                 break;
@@ -284,6 +325,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             base += t * a.c.n_kv;
         }
         // the row tile of the head that holds w0
+#pragma unroll 1
         while (found) {
             const int32_t i = rt + lane;
             const int32_t mine = (int64_t)i * kRows < rows ? unit_count(a, u, rows, i) : 0;
@@ -321,8 +363,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             whole = u0 >= w0 && u1 <= w1;
             c0 = c1 = 0;
             if (!whole) {
-                c0 = (int32_t)(u0 / run);
-                c1 = (int32_t)((u1 - 1) / run);
+                c0 = div_list(u0, run);
+                c1 = div_list(u1 - 1, run);
             }
             ta = u0 >= w0 ? ut.lo : ut.lo + (int32_t)(w0 - u0);
             tb = u1 <= w1 ? ut.hi : ut.hi - (int32_t)(u1 - w1);
@@ -331,8 +373,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         };
         int64_t u0 = base;
         bool more = found;
-        if (found) enter(u0);
+        bool fresh = true;                              // the unit has yet to be entered
         const int gl = lane >> 1, kvl = lane & 1;       // this lane's 8 tokens of a tile, and keys or values
+        const int R = p.box_rows;                       // tokens that share a page: 16, or 8
         struct Box {
             bool want;
             int32_t page, row;
@@ -344,15 +387,19 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             x.want = false;
             x.page = x.row = 0;
             if (!more) return false;
-            wait_phase<false>(&s_tempty[slot], slot_parity, abort, status);
+            if (fresh) {
+                enter(u0);
+                fresh = false;
+            }
+            wait_bar(&s_tempty[slot], slot_parity, abort, status);
             if (*abort) return false;
             Desc &d = desc[slot];
             if (++slot == kDescs) {
                 slot = 0;
                 slot_parity ^= 1;
             }
-            const int32_t j0 = tile * kTile, j = j0 + 8 * gl;
-            x.want = j < ut.k1 && j + 8 > ut.k0;
+            const int32_t j0 = tile * kTile, j = j0 + (8 * gl & -R);      // first token of the box
+            x.want = j < ut.k1 && j + R > ut.k0;
             if (x.want) {
                 int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
                 x.row = j - blk * a.c.bt;
@@ -370,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (tile >= b && tile < e)
                         f |= (kAct << t) | (tile == b ? kFirstAct << t : 0) | (tile == e - 1 ? kLastAct << t : 0);
                 }
-                if (j0 >= first_key(a, u, (r1 - 1) / a.group) && j0 + kTile <= end_key(a, u, r0 / a.group)) f |= kPlain;
+                if (j0 >= first_key(a, u, div_group(a, r1 - 1)) && j0 + kTile <= end_key(a, u, div_group(a, r0))) f |= kPlain;
                 int4 *di = reinterpret_cast<int4 *>(&d.flags);
                 di[0] = make_int4((int)f, j0, ut.k0, ut.k1);
                 di[1] = make_int4(u.row0, u.n, u.len, head);
@@ -388,7 +435,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                             more = false;
                         }
                     }
-                    if (more) enter(u0);
+                    fresh = true;
                 }
             }
             return true;
@@ -402,21 +449,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         };
         // Two tiles lie between the reading of a tile's page ids and of its exponents, and two
         // more between those and their use.
-        Box b0, b1, b2, b3, b4;
-        bool n0 = describe(b0), n1 = describe(b1);
-        int32_t e0 = exponent_of(b0), e1 = exponent_of(b1), e2;
-        bool n2 = describe(b2), n3 = describe(b3), n4;
-        int32_t i = 0;
-        for (; n0 && !*abort; ++i, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
+        const Box none = {false, 0, 0};
+        Box b0 = none, b1 = none, b2 = none, b3 = none, b4;
+        bool n0 = false, n1 = false, n2 = false, n3 = false, n4;
+        int32_t e0 = 0, e1 = 0, e2;
+        int piece = 0;
+        uint32_t piece_parity = 1;
+        int32_t issued = 0;
+#pragma unroll 1
+        for (int32_t i = -4;;
+             ++i, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
             e2 = exponent_of(b2);
             n4 = describe(b4);
+            if (i < 0) continue;
+            if (!n0 || *abort) break;
             Desc &d = desc[i % kDescs];
             unsigned have = __ballot_sync(~0u, b0.want);
             have &= have >> 1 & 0x55555555u;               // a group needs both its keys and its values
             const bool both = have >> (2 * gl) & 1u;
             const int e = both ? clamp_exponent(e0) : 0;
-            d.off[kvl][gl] = both ? (int64_t)b0.page * a.c.page_bytes + b0.row * D : -1;
+            d.page[kvl][gl] = b0.page;
             if (kvl == 0) {
+                d.row[gl] = b0.row;
                 d.ks[gl] = pow2(e);
             } else {
                 d.lv[gl] = (float)e;
@@ -431,6 +485,39 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_tfull[i % kDescs]);
+            // the tile's pieces: keys 0-63, 64-127, values 0-63, 64-127
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                wait_bar(&s_rempty[piece], piece_parity, abort, status);
+                if (*abort) break;
+                if (lane == 0) {
+                    const int g0 = 8 * (k & 1);
+                    const uint32_t o = d.ok >> g0 & 255u, dst = raw_sm + piece * Sh::kPiece;
+                    const int32_t *pg = &d.page[k >> 1][g0], *rw = &d.row[g0];
+                    uint64_t *bar = &s_rfull[piece];
+                    mbar_arrive_expect_tx(bar, (uint32_t)__popc(o) * 8u * D);
+                    // as one box if no block starts within, else in boxes of R rows
+                    if (R == 16 && o == 255u && rw[2] && rw[4] && rw[6]) {
+                        tma_load_3d(dst, &maps.m[2], rw[0], pg[0], bar);
+                    } else {
+#pragma unroll 1
+                        for (int x = 0; x < 8; x += R / 8)
+                            if (o >> x & 1u) tma_load_3d(dst + x * 8 * D, &maps.m[0], rw[x], pg[x], bar);
+                    }
+                }
+                ++issued;
+                if (++piece == Sh::kPieces) {
+                    piece = 0;
+                    piece_parity ^= 1;
+                }
+            }
+        }
+        // no copy outlives the CTA
+        volatile int gone = 0;
+#pragma unroll 1
+        for (int k = 0; k < Sh::kPieces && k < issued && !gone; ++k) {
+            const int32_t n = issued - 1 - k;
+            wait_bar(&s_rfull[n % Sh::kPieces], (uint32_t)(n / Sh::kPieces) & 1u, &gone, status);
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------------
@@ -449,22 +536,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 uint32_t g = 0;
                 const bool more = i + 1 < total;
                 if (more) {
-                    wait_phase<false>(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
+                    wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
                     if (*abort) break;
                     g = desc[(i + 1) % kDescs].flags;
                 }
                 const bool same = more && !(g & kFirst);
-                if (i >= 0) wait_phase<false>(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
+                if (i >= 0) wait_bar(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
                 bool ready = false;
 #pragma unroll 1
                 for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4) && !*abort; ++k) {
                     const uint32_t t = k & 1;
                     if (k < 2 && (f & (kAct << t))) {
-                        wait_phase<false>(&s_pfull[t], p_par >> t & 1u, abort, status);
+                        wait_bar(&s_pfull[t], p_par >> t & 1u, abort, status);
                         p_par ^= 1u << t;
                         const bool first = f & (kFirstAct << t);
                         if (first) {
-                            wait_phase<false>(&s_ofree[t], of_par >> t & 1u, abort, status);
+                            wait_bar(&s_ofree[t], of_par >> t & 1u, abort, status);
                             of_par ^= 1u << t;
                         }
                         if (*abort) break;
@@ -479,9 +566,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (more && (same || k >= 2)) {
                         if (!ready) {
                             ready = true;
-                            wait_phase<false>(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
+                            wait_bar(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
                             if (g & kFirst) {
-                                wait_phase<false>(&s_qfull, q_par, abort, status);
+                                wait_bar(&s_qfull, q_par, abort, status);
                                 q_par ^= 1;
                             }
                             if (*abort) break;
@@ -512,61 +599,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             // every product issued has completed before tensor memory is released
             tc::commit(&s_fin);
-            mbar_wait_bounded(&s_fin, 0, status);
+            volatile int gone = 0;
+            wait_bar(&s_fin, 0, &gone, status);
         }
         __syncwarp();
-    } else if (warp >= kConvWarp) {
+    } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ---- codes to fp16 operand tiles -----------------------------------------------------
         const int ct = tid - kConvWarp * 32;                   // 0 .. 127
-        constexpr int NL = D == 128 ? 8 : 4;                   // 16-byte loads per thread and tile
-        // load x: chunk (ct & 3) + 4 (x & 1) of row (ct >> 2) + 32 (x >> 1)  (D = 128), or chunk ct & 3
-        // of row (ct >> 2) + 32 x: eight lanes then store to all banks
         const int ch = ct & 3, rw = ct >> 2;
-        auto load = [&](const Desc &d, int kvl, uint4 (&r)[NL]) {
-            const bool plain = d.j0 >= d.lo && d.j0 + kTile <= d.hi;
-#pragma unroll
-            for (int x = 0; x < NL; ++x) {
-                const int row = rw + 32 * (D == 128 ? x >> 1 : x), c = D == 128 ? ch + 4 * (x & 1) : ch;
-                const int64_t off = d.off[kvl][row >> 3];
-                const int32_t j = d.j0 + row;
-                r[x] = make_uint4(0, 0, 0, 0);
-                if (off >= 0 && (plain || (j >= d.lo && j < d.hi)))
-                    r[x] = ld_codes(a.c.pool + off + (row & 7) * D + c * 16);
-            }
-        };
-        auto store = [&](uint32_t dst, uint4 (&r)[NL]) {
-            // the conversions stay behind the waits before this call: moved up to the loads, they
-            // would wait for them there
-#pragma unroll
-            for (int x = 0; x < NL; ++x) asm volatile("" : "+r"(r[x].x), "+r"(r[x].y), "+r"(r[x].z), "+r"(r[x].w));
-#pragma unroll
-            for (int x = 0; x < NL; ++x) {
-                const int row = rw + 32 * (D == 128 ? x >> 1 : x), blk = D == 128 ? x & 1 : 0;
-                const uint32_t at = dst + blk * (128 * 128) + row * 128;
-                uint32_t h[8];
-                decode4<FMT>(r[x].x, h[0], h[1]);
-                decode4<FMT>(r[x].y, h[2], h[3]);
-                decode4<FMT>(r[x].z, h[4], h[5]);
-                decode4<FMT>(r[x].w, h[6], h[7]);
-                sts128(at + (((2 * ch) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                sts128(at + (((2 * ch + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
-            }
-        };
         auto done = [&](uint64_t *bar) {
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        uint4 ra[NL], rb[NL];
-        uint32_t qe_par = 1;
-        wait_phase<false>(&s_tfull[0], 0, abort, status);
-        if (!*abort) load(desc[0], 0, ra);
+        uint32_t qe_par = 1, r_par = 0;
+        int piece = 0;
         for (int32_t i = 0; i < total && !*abort; ++i) {
+            wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
+            if (*abort) break;
             const Desc &d = desc[i % kDescs];
-            load(d, 1, rb);
             if (d.flags & kFirst) {
                 // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
-                wait_phase<false>(&s_qempty, qe_par, abort, status);
+                wait_bar(&s_qempty, qe_par, abort, status);
                 qe_par ^= 1;
                 if (*abort) break;
                 const int qc = ct & 7;
@@ -575,7 +629,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 for (int s = 0; s < steps; ++s) {
                     const int row = (ct >> 3) + 16 * s;
                     const int32_t r = d.r0 + (row < nrows ? row : 0);
-                    const int32_t tok = a.group == 1 ? r : r / a.group;
+                    const int32_t tok = div_group(a, r);
                     const __half *src = a.q + (int64_t)(d.row0 + tok) * a.q_stride +
                                         ((int64_t)d.head * a.group + (r - tok * a.group)) * D + qc * 8;
 #pragma unroll
@@ -588,22 +642,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 }
                 done(&s_qfull);
             }
-            wait_phase<false>(&s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
-            if (*abort) break;
-            store(k_sm + (i & 1) * Sh::kKVTile, ra);
-            done(&s_kfull[i & 1]);
-            if (i + 1 < total) {
-                wait_phase<false>(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
+            // rows that are not seen hold anything in the ring, and zeros in the operands
+            const bool all = d.ok == 0xFFFFu && d.j0 >= d.lo && d.j0 + kTile <= d.hi;
+#pragma unroll 1
+            for (int k = 0; k < 4; ++k) {
+                if ((k & 1) == 0) {
+                    wait_bar(k ? &s_vempty[i & 1] : &s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
+                    if (*abort) break;
+                }
+                wait_bar(&s_rfull[piece], r_par, abort, status);
                 if (*abort) break;
-                load(desc[(i + 1) % kDescs], 0, ra);
+                const uint32_t src = raw_sm + piece * Sh::kPiece;
+                const uint32_t dst = (k >> 1 ? v_sm : k_sm) + (i & 1) * Sh::kKVTile + (k & 1) * 64 * 128;
+                // Step x: chunk ch + 4 ((x ^ row) & 1) of row rw + 32 (x >> 1)  (D = 128), or chunk ch of row
+                // rw + 32 x: eight lanes read from, and write to, all banks.
+                constexpr int NL = D / 32;
+                uint4 r[NL];
+#pragma unroll
+                for (int x = 0; x < NL; ++x) {
+                    const int row = rw + 32 * (D == 128 ? x >> 1 : x);
+                    const int c = D == 128 ? (ch + 4 * ((x ^ rw) & 1)) ^ (row & 7) : ch ^ (row >> 1 & 3);
+                    r[x] = lds128(src + row * D + c * 16);
+                }
+                if (!all) {
+#pragma unroll
+                    for (int x = 0; x < NL; ++x) {
+                        const int row = rw + 32 * (D == 128 ? x >> 1 : x) + 64 * (k & 1);
+                        const int32_t j = d.j0 + row;
+                        if (!((d.ok >> (row >> 3) & 1u) && j >= d.lo && j < d.hi)) r[x] = make_uint4(0, 0, 0, 0);
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < NL; ++x) {
+                    const int row = rw + 32 * (D == 128 ? x >> 1 : x);
+                    const uint32_t at = dst + (D == 128 ? ((x ^ rw) & 1) * (128 * 128) : 0) + row * 128;
+                    uint32_t h[8];
+                    decode4<FMT>(r[x].x, h[0], h[1]);
+                    decode4<FMT>(r[x].y, h[2], h[3]);
+                    decode4<FMT>(r[x].z, h[4], h[5]);
+                    decode4<FMT>(r[x].w, h[6], h[7]);
+                    sts128(at + (((2 * ch) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
+                    sts128(at + (((2 * ch + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_rempty[piece]);
+                if (++piece == Sh::kPieces) {
+                    piece = 0;
+                    r_par ^= 1;
+                }
+                if (k & 1) done(k >> 1 ? &s_vfull[i & 1] : &s_kfull[i & 1]);
             }
-            wait_phase<false>(&s_vempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
-            if (*abort) break;
-            store(v_sm + (i & 1) * Sh::kKVTile, rb);
-            done(&s_vfull[i & 1]);
             if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
         }
-    } else {
+    } else if (warp < kConvWarp) {
         // ---- softmax: one row per thread -------------------------------------------------------
         const int t = warp >> 2;                               // row tile
         const uint32_t lane_base = (uint32_t)(warp & 3) << 21; // lane 32 (warp & 3) of tensor memory
@@ -612,9 +703,21 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         uint32_t s_par = 0, od_par = 0, j_par = 0;
         float mx = -INFINITY, sum = 0.f;
         bool any = false;
+        // The largest score of 32 keys.
+        auto top_of = [&](const Desc &d, const uint32_t (&x)[32], int h) {
+            float top = -INFINITY;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                float m = __uint_as_float(x[8 * g]);
+#pragma unroll
+                for (int k = 1; k < 8; ++k) m = fmaxf(m, __uint_as_float(x[8 * g + k]));
+                top = fmaxf(top, fmaf(m, d.ks[4 * h + g] * p.scale, d.lv[4 * h + g]));
+            }
+            return top;
+        };
         int32_t klo = 0, khi = 0;                              // keys that the row sees
         for (int32_t i = 0; i < total; ++i) {
-            wait_phase<false>(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
+            wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
             if (*abort) break;
             const Desc &d = desc[i % kDescs];
             const uint32_t f = d.flags;
@@ -624,12 +727,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 any = false;
                 const Seq q = {d.row0, d.n, d.len};
                 const int32_t r = d.r0 + 128 * t + row, last = d.r0 + d.nrows - 1;
-                const int32_t tok = (r < last ? r : last) / a.group;
+                const int32_t tok = div_group(a, r < last ? r : last);
                 klo = first_key(a, q, tok);
                 khi = end_key(a, q, tok);
             }
             if (f & (kAct << t)) {
-                wait_phase<false>(&s_sfull[t], s_par, abort, status);
+                wait_bar(&s_sfull[t], s_par, abort, status);
                 s_par ^= 1;
                 if (*abort) break;
                 tc::fence_after_sync();
@@ -646,76 +749,102 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     }
                 };
                 // The loops over a tile's columns stay rolled: unrolled, the roles' code does not fit the
-                // instruction caches (0.39 PFLOP/s on a long chunk).
-                float top = -INFINITY;
+                // instruction caches (0.39 PFLOP/s on a long chunk, 0.52 rolled).
                 uint32_t x[32];
+                if (__any_sync(~0u, mx == -INFINITY)) {
+                    // rows that have seen nothing yet start from this tile's maximum
+                    float top = -INFINITY;
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        tc::ld_32x32b_x32(ts + 32 * h, x);
+                        tc::ld_wait(x);
+                        mask(x, h);
+                        top = fmaxf(top, top_of(d, x, h));
+                    }
+                    if (mx == -INFINITY) mx = ceilf(top);
+                }
+                // The weights, 32 keys at a time, by the running maximum as it stands: an integer, so that
+                // following it is exact.  It follows only when a weight passes 2^8, far inside fp16, and
+                // then what was made with the old one is divided by a power of two.
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     tc::ld_32x32b_x32(ts + 32 * h, x);
-                    tc::ld_wait();
-                    mask(x, h);
-                    const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
-                    const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
-                    const float kf[4] = {ks.x, ks.y, ks.z, ks.w}, lf[4] = {lv.x, lv.y, lv.z, lv.w};
-#pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        float m = __uint_as_float(x[8 * g]);
-#pragma unroll
-                        for (int k = 1; k < 8; ++k) m = fmaxf(m, __uint_as_float(x[8 * g + k]));
-                        top = fmaxf(top, fmaf(m, kf[g] * p.scale, lf[g]));
-                    }
-                }
-                // The running maximum follows only when a score passes it by 2^8, so that O is
-                // seldom rescaled; the weights stay below 2^8, far inside fp16.
-                const bool up = top > mx + 8.f;
-                if (__any_sync(~0u, up)) {
-                    const float nm = up ? top : mx;
-                    const float k = mx == -INFINITY ? 0.f : ex2(mx - nm);
-                    mx = nm;
-                    sum *= k;
-                    if (any) {
-                        const float kk = up ? k : 1.f;
-#pragma unroll 1
-                        for (int h = 0; h < D / 32; ++h) {
-                            tc::ld_32x32b_x32(to + 32 * h, x);
-                            tc::ld_wait();
-#pragma unroll
-                            for (int j = 0; j < 32; ++j) x[j] = __float_as_uint(__uint_as_float(x[j]) * kk);
-                            tc::st_32x32b_x32(to + 32 * h, x);
-                        }
-                        tc::st_wait();
-                    }
-                }
-                any = true;
-                const float base = mx == -INFINITY ? 0.f : mx;
-#pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
-                    tc::ld_32x32b_x32(ts + 32 * h, x);
-                    tc::ld_wait();
+                    tc::ld_wait(x);
                     mask(x, h);
                     const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
                     const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
                     const float4 li = *reinterpret_cast<const float4 *>(&d.li[4 * h]);
-                    const float kf[4] = {ks.x, ks.y, ks.z, ks.w}, lf[4] = {lv.x, lv.y, lv.z, lv.w};
-                    const float if_[4] = {li.x, li.y, li.z, li.w};
+                    const float base = mx == -INFINITY ? 0.f : mx;
+                    float kx[4] = {ks.x * p.scale, ks.y * p.scale, ks.z * p.scale, ks.w * p.scale};
+                    float lx[4] = {lv.x - base, lv.y - base, lv.z - base, lv.w - base};
+                    const float il[4] = {li.x, li.y, li.z, li.w};
                     uint32_t pk[16];
+                    float add;
+                    for (int turn = 0;; ++turn) {
+                        __half2 hm = __float2half2_rn(0.f);
+                        add = 0.f;
 #pragma unroll
-                    for (int g = 0; g < 4; ++g) {
-                        const float kx = kf[g] * p.scale, lx = lf[g] - base;
-                        float s = 0.f;
+                        for (int g = 0; g < 4; ++g) {
+                            uint64_t s2 = 0;
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            const float e0 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k]), kx, lx));
-                            const float e1 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k + 1]), kx, lx));
-                            s += e0 + e1;
-                            const __half2 hh = __floats2half2_rn(e0, e1);
-                            pk[4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                            for (int k = 0; k < 4; ++k) {
+                                const float e0 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k]), kx[g], lx[g]));
+                                const float e1 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k + 1]), kx[g], lx[g]));
+                                s2 = add2(s2, pair(e0, e1));
+                                const __half2 hh = __floats2half2_rn(e0, e1);
+                                hm = __hmax2(hm, hh);
+                                pk[4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                            }
+                            const float2 sg = unpair(s2);
+                            add = fmaf(sg.x + sg.y, il[g], add);
                         }
-                        sum = fmaf(s, if_[g], sum);
+                        const bool up = __hgt(__hmax(__low2half(hm), __high2half(hm)), __float2half(256.f));
+                        if (turn == 1 || !__any_sync(~0u, up)) break;
+                        const float nm = up ? ceilf(top_of(d, x, h)) : mx;
+                        const float k = mx == nm ? 1.f : ex2(mx - nm);
+                        mx = nm;
+                        // The second turn takes scores rounded as the maximum was, so that no weight is above 1
+                        // however large they are.
+                        const float nb = mx == -INFINITY ? 0.f : mx;
+                        const float kv[4] = {ks.x, ks.y, ks.z, ks.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w};
+#pragma unroll
+                        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+                            for (int j = 0; j < 8; ++j)
+                                x[8 * g + j] = __float_as_uint(fmaf(__uint_as_float(x[8 * g + j]), kv[g] * p.scale, lw[g]) - nb);
+                            kx[g] = 1.f;
+                            lx[g] = 0.f;
+                        }
+                        sum *= k;
+                        uint32_t y[16];
+                        if (any)
+#pragma unroll 1
+                            for (int c = 0; c < D / 16; ++c) {
+                                tc::ld_32x32b_x16(to + 16 * c, y);
+                                tc::ld_wait(y);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * k);
+                                tc::st_32x32b_x16(to + 16 * c, y);
+                            }
+                        const __half2 kh = __float2half2_rn(k);
+#pragma unroll 1
+                        for (int c = 0; c < h; ++c) {
+                            tc::ld_32x32b_x16(ts + 16 * c, y);
+                            tc::ld_wait(y);
+#pragma unroll
+                            for (int j = 0; j < 16; ++j) {
+                                __half2 w = __hmul2(*reinterpret_cast<__half2 *>(&y[j]), kh);
+                                y[j] = *reinterpret_cast<uint32_t *>(&w);
+                            }
+                            tc::st_32x32b_x16(ts + 16 * c, y);
+                        }
+                        tc::st_wait();
                     }
+                    sum += add;
                     // columns already read: 32 keys' weights take 16 of the 32 that their scores took
                     tc::st_32x32b_x16(ts + 16 * h, pk);
                 }
+                any = true;
                 tc::st_wait();
                 tc::fence_before_sync();
                 __syncwarp();
@@ -729,12 +858,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 
             // ---- the unit's end in this CTA ---------------------------------------------------
             if (any) {
-                wait_phase<false>(&s_odone[t], od_par, abort, status);
+                wait_bar(&s_odone[t], od_par, abort, status);
                 od_par ^= 1;
                 if (*abort) break;
                 tc::fence_after_sync();
             }
-            const int32_t tok = r / a.group;
+            const int32_t tok = div_group(a, r);
             const int64_t qh = (int64_t)head * a.group + (r - tok * a.group);
             __half *out = a.out + (int64_t)(row0 + tok) * a.out_stride + qh * D;
             auto put_lse = [&](float M, float L) {
@@ -756,7 +885,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 uint32_t x[32];
                 if (any) {                                     // uniform over the warp
                     tc::ld_32x32b_x32(to + 32 * h, x);
-                    tc::ld_wait();
+                    tc::ld_wait(x);
                 }
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = any ? __uint_as_float(x[j]) : 0.f;
@@ -798,7 +927,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             __threadfence();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_join[t]);
-            wait_phase<false>(&s_join[t], j_par, abort, status);
+            wait_bar(&s_join[t], j_par, abort, status);
             if (*abort) break;
             if (row == 0) {
                 __threadfence();
@@ -809,20 +938,23 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 __threadfence();
                 mbar_arrive(&s_said[t]);
             }
-            wait_phase<false>(&s_said[t], j_par, abort, status);
+            wait_bar(&s_said[t], j_par, abort, status);
             j_par ^= 1;
             if (*abort) break;
             if (!s_last[t] || !live) continue;
             float M = -INFINITY;
+#pragma unroll 1
             for (int32_t k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + row));
             const float B = M == -INFINITY ? 0.f : M;
             float L = 0.f;
+#pragma unroll 1
             for (int32_t k = c0; k <= c1; ++k) L += __ldcg(slot(k) + 128 + row) * ex2(__ldcg(slot(k) + row) - B);
             const float inv = L == 0.f ? 0.f : 1.f / L;
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
 #pragma unroll
                 for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
                 for (int32_t k = c0; k <= c1; ++k) {
                     const float *s = slot(k);
                     const float m = __ldcg(s + row);
@@ -852,7 +984,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 }
 
 template <int D, int FMT>
-cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
+cudaError_t launch(const PrefillParams &p, const PageMaps &maps, int num_sms, cudaStream_t stream)
 {
     static std::mutex mu;
     static bool set[64] = {};
@@ -878,7 +1010,7 @@ cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p);
+    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p, maps);
 }
 
 }  // namespace
@@ -888,12 +1020,13 @@ size_t prefill_workspace_bytes(int num_sms)
     return (size_t)num_sms * 4 * Shape<128>::kPart * 4 + (size_t)num_sms * 2 * 4;
 }
 
-cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
+cudaError_t launch_attend_prefill(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
                                   cudaStream_t stream, int *launches)
 {
     PrefillParams p;
     p.a = a;
     p.small_rows = small_rows;
+    p.box_rows = a.c.bt % 16 == 0 ? 16 : 8;
     p.min_tiles = 2;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.q_sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
@@ -905,9 +1038,9 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, in
     p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
     cudaError_t e;
     if (head_dim == 128)
-        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, num_sms, stream);
+        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, maps, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, maps, num_sms, stream);
     else
-        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, num_sms, stream);
+        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, maps, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, maps, num_sms, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -191,6 +191,28 @@ def test_attend_large_scores():
     Case([(1, 500), (3, 333), (130, 400)], hq=4, hkv=2, seed=10).check(scale=4.0)
 
 
+@pytest.mark.parametrize("scale", [3e4, -3e4, 1e30, -1e30, 0.0])
+@pytest.mark.parametrize("n", [1, 140])
+def test_attend_scores_beyond_fp32s_fractions(scale, n):
+    """Scores so large that fp32 holds no fraction of them (and past its range at 1e30, and all equal at 0):
+    the rows stay within the values they average, or are NaN where a score is infinite."""
+    c = Case([(n, 400)], hq=4, hkv=2, seed=33, stale=False)
+    out, lse = c.attend(scale=scale)
+    assert c.s.device_status() == 0
+    val, exps = c.values()
+    for h in range(2):
+        pages = c.table[0, :-(-400 // c.bt), h, 1]
+        top = np.abs(val[pages] * 2.0 ** exps[pages][:, None, None]).max()
+        got = out[:, 2 * h:2 * h + 2]
+        if abs(scale) < 1e20:
+            assert np.isfinite(got).all() and np.abs(got).max() <= top * 1.001
+        else:
+            assert (np.isnan(got) | (np.abs(got) <= top * 1.001)).all()
+    if scale == 0:
+        for t in range(n):
+            assert np.allclose(lse[t], np.log(400 - n + 1 + t), atol=1e-5)
+
+
 def test_attend_rising_scores():
     """Every tile's scores pass the ones before by more than the rescaling threshold."""
     c = Case([(1, 1000), (130, 1000)], hq=2, hkv=1, seed=11, stale=False)
