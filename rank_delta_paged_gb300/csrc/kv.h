@@ -126,26 +126,31 @@ __device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, in
     return p > 0 ? p : 0;
 }
 
-// Bounded wait on an mbarrier phase, as wait_phase of ptx.h: after the first timeout in the CTA
-// (*abort, SLORA_DEV_TIMEOUT) every wait returns at once.  Its loop stays rolled: these kernels
-// have some thirty waits, and unrolled ones made 250 KB of code, fetched from L2 again and again
-// (a long chunk of a prompt took 1.5 times as long).
-__device__ __forceinline__ void wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
+// Bounded wait on an mbarrier phase, as wait_phase of ptx.h: true once the phase has completed;
+// false after the first timeout in the CTA (*abort, SLORA_DEV_TIMEOUT), from when on every wait that
+// would have to wait gives up soon.  One try, which the hardware holds for up to 20 us, stands
+// in line and the rest in a function: these kernels have some thirty waits, and with whole
+// loops at each the code is fetched from L2 again and again.
+static __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
 {
-    if (mbar_try_wait(bar, parity)) return;
     uint64_t t0 = 0;
 #pragma unroll 1
     for (uint32_t it = 1; !mbar_try_wait(bar, parity); ++it) {
         if ((it & 63u) != 0) continue;
-        if (*abort) return;
+        if (*abort) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
         if (now - t0 > kWaitLimitNs) {
             set_status(status, SLORA_DEV_TIMEOUT);
             *abort = 1;
-            return;
+            return false;
         }
     }
+    return true;
+}
+__device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
+{
+    return mbar_try_wait(bar, parity) || wait_more(bar, parity, abort, status);
 }
 
 // ---- codes ---------------------------------------------------------------------------

@@ -505,8 +505,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             __syncwarp();
 #pragma unroll 1
             for (int t = 0; t < n0; ++t, ++issued) {
-                wait_bar(&s_empty[stage], parity, abort, status);
-                if (*abort) break;
+                if (!wait_bar(&s_empty[stage], parity, abort, status)) break;
                 if (lane == 0) copy_tile(meta[(batch << batch_log) + t], stage);
                 if (++stage == NS) {
                     stage = 0;
@@ -542,9 +541,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     auto meet = [&](int k) {
         __syncwarp();
         if (lane == 0) mbar_arrive(&s_merge[k]);
-        wait_bar(&s_merge[k], mparity[k], abort, status);
+        const bool fine = wait_bar(&s_merge[k], mparity[k], abort, status);
         mparity[k] ^= 1;
-        return *abort == 0;
+        return fine;
     };
 
     // This lane's share of the rows of m's unit: k step i holds channels 4 (i & 3) .. + 3 of
@@ -567,8 +566,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         }
     };
     for (int32_t it = 0; it < total; ++it) {
-        wait_bar(&s_full[stage], parity, abort, status);
-        if (*abort) break;
+        if (!wait_bar(&s_full[stage], parity, abort, status)) break;
         const Meta &m = meta[it % kDescs];
         const int4 flags = *reinterpret_cast<const int4 *>(&m.plain);
         const bool plain = flags.x != 0, last = flags.z != 0, whole = flags.w != 0;
@@ -624,8 +622,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         // the next unit's rows, while this one's last tile is finished
         if (last && it + 1 < total) {
             const bool wrap = stage + 1 == NS;
-            wait_bar(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status);
-            if (*abort) break;
+            if (!wait_bar(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status)) break;
             load_q(meta[(it + 1) % kDescs]);
         }
         const float f0 = m.ks[2 * warp] * a.scale_log2, f1 = m.ks[2 * warp + 1] * a.scale_log2;
@@ -815,8 +812,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 __threadfence();
                 mbar_arrive(&s_merge[2]);
             }
-            wait_bar(&s_merge[2], jparity, abort, status);
-            if (*abort) break;
+            if (!wait_bar(&s_merge[2], jparity, abort, status)) break;
             jparity ^= 1;
             if (s_last) {
 #pragma unroll 1

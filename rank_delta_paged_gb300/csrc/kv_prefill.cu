@@ -391,8 +391,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 enter(u0);
                 fresh = false;
             }
-            wait_bar(&s_tempty[slot], slot_parity, abort, status);
-            if (*abort) return false;
+            if (!wait_bar(&s_tempty[slot], slot_parity, abort, status)) return false;
             Desc &d = desc[slot];
             if (++slot == kDescs) {
                 slot = 0;
@@ -488,8 +487,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             // the tile's pieces: keys 0-63, 64-127, values 0-63, 64-127
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
-                wait_bar(&s_rempty[piece], piece_parity, abort, status);
-                if (*abort) break;
+                if (!wait_bar(&s_rempty[piece], piece_parity, abort, status)) break;
                 if (lane == 0) {
                     const int g0 = 8 * (k & 1);
                     const uint32_t o = d.ok >> g0 & 255u, dst = raw_sm + piece * Sh::kPiece;
@@ -532,29 +530,30 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             // Tile i's weights times its values, and tile i + 1's scores: within a unit by turns, so that each
             // row tile's softmax has the other's products to run under; at a unit's end the new
             // unit's scores after both, since they wait for its rows.
-            for (int32_t i = -1; i < total && !*abort; ++i) {
+            bool fine = true;
+#pragma unroll 1
+            for (int32_t i = -1; i < total && fine; ++i) {
                 uint32_t g = 0;
                 const bool more = i + 1 < total;
                 if (more) {
-                    wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status);
-                    if (*abort) break;
+                    if (!wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status)) break;
                     g = desc[(i + 1) % kDescs].flags;
                 }
                 const bool same = more && !(g & kFirst);
-                if (i >= 0) wait_bar(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
+                if (i >= 0) fine = wait_bar(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
                 bool ready = false;
 #pragma unroll 1
-                for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4) && !*abort; ++k) {
+                for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4) && fine; ++k) {
                     const uint32_t t = k & 1;
                     if (k < 2 && (f & (kAct << t))) {
-                        wait_bar(&s_pfull[t], p_par >> t & 1u, abort, status);
+                        fine = wait_bar(&s_pfull[t], p_par >> t & 1u, abort, status);
                         p_par ^= 1u << t;
                         const bool first = f & (kFirstAct << t);
                         if (first) {
-                            wait_bar(&s_ofree[t], of_par >> t & 1u, abort, status);
+                            fine = fine && wait_bar(&s_ofree[t], of_par >> t & 1u, abort, status);
                             of_par ^= 1u << t;
                         }
-                        if (*abort) break;
+                        if (!fine) break;
                         tc::fence_after_sync();
                         const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
                         const uint32_t o = tm_o + D * t, w = tm_s + 128 * t;
@@ -566,12 +565,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (more && (same || k >= 2)) {
                         if (!ready) {
                             ready = true;
-                            wait_bar(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
+                            fine = wait_bar(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
                             if (g & kFirst) {
-                                wait_bar(&s_qfull, q_par, abort, status);
+                                fine = fine && wait_bar(&s_qfull, q_par, abort, status);
                                 q_par ^= 1;
                             }
-                            if (*abort) break;
+                            if (!fine) break;
                             tc::fence_after_sync();
                         }
                         if (g & (kAct << t)) {
@@ -586,7 +585,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                         }
                     }
                 }
-                if (*abort) break;
+                if (!fine) break;
                 if (i >= 0) {
                     tc::commit(&s_vempty[i & 1]);
                     mbar_arrive(&s_tempty[i % kDescs]);
@@ -615,14 +614,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         uint32_t qe_par = 1, r_par = 0;
         int piece = 0;
         for (int32_t i = 0; i < total && !*abort; ++i) {
-            wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
-            if (*abort) break;
+            if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
             const Desc &d = desc[i % kDescs];
             if (d.flags & kFirst) {
                 // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
-                wait_bar(&s_qempty, qe_par, abort, status);
+                if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                 qe_par ^= 1;
-                if (*abort) break;
                 const int qc = ct & 7;
                 const int32_t nrows = d.nrows, steps = nrows > 128 ? 16 : 8;
 #pragma unroll 4
@@ -647,11 +644,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 #pragma unroll 1
             for (int k = 0; k < 4; ++k) {
                 if ((k & 1) == 0) {
-                    wait_bar(k ? &s_vempty[i & 1] : &s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status);
-                    if (*abort) break;
+                    if (!wait_bar(k ? &s_vempty[i & 1] : &s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
                 }
-                wait_bar(&s_rfull[piece], r_par, abort, status);
-                if (*abort) break;
+                if (!wait_bar(&s_rfull[piece], r_par, abort, status)) break;
                 const uint32_t src = raw_sm + piece * Sh::kPiece;
                 const uint32_t dst = (k >> 1 ? v_sm : k_sm) + (i & 1) * Sh::kKVTile + (k & 1) * 64 * 128;
                 // Step x: chunk ch + 4 ((x ^ row) & 1) of row rw + 32 (x >> 1)  (D = 128), or chunk ch of row
@@ -717,8 +712,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         };
         int32_t klo = 0, khi = 0;                              // keys that the row sees
         for (int32_t i = 0; i < total; ++i) {
-            wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status);
-            if (*abort) break;
+            if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
             const Desc &d = desc[i % kDescs];
             const uint32_t f = d.flags;
             if (f & kFirst) {
@@ -732,9 +726,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 khi = end_key(a, q, tok);
             }
             if (f & (kAct << t)) {
-                wait_bar(&s_sfull[t], s_par, abort, status);
+                if (!wait_bar(&s_sfull[t], s_par, abort, status)) break;
                 s_par ^= 1;
-                if (*abort) break;
                 tc::fence_after_sync();
                 const bool plain = f & kPlain;
                 const int32_t m0 = klo - d.j0;
@@ -858,9 +851,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 
             // ---- the unit's end in this CTA ---------------------------------------------------
             if (any) {
-                wait_bar(&s_odone[t], od_par, abort, status);
+                if (!wait_bar(&s_odone[t], od_par, abort, status)) break;
                 od_par ^= 1;
-                if (*abort) break;
                 tc::fence_after_sync();
             }
             const int32_t tok = div_group(a, r);
@@ -927,8 +919,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             __threadfence();
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_join[t]);
-            wait_bar(&s_join[t], j_par, abort, status);
-            if (*abort) break;
+            if (!wait_bar(&s_join[t], j_par, abort, status)) break;
             if (row == 0) {
                 __threadfence();
                 int32_t *cnt = p.count + 2 * c0 + t;
@@ -938,9 +929,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 __threadfence();
                 mbar_arrive(&s_said[t]);
             }
-            wait_bar(&s_said[t], j_par, abort, status);
+            if (!wait_bar(&s_said[t], j_par, abort, status)) break;
             j_par ^= 1;
-            if (*abort) break;
             if (!s_last[t] || !live) continue;
             float M = -INFINITY;
 #pragma unroll 1
