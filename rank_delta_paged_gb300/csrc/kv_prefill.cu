@@ -133,6 +133,13 @@ __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 struct Tiles {
     int32_t lo, hi;        // key tiles [lo, hi) of a unit, one at least
     int32_t k0, k1;        // keys
@@ -519,73 +526,83 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         }
     } else if (warp == kMmaWarp) {
         // ---- products --------------------------------------------------------------------
-        if (lane == 0) {
-            constexpr uint32_t id_s = tc::idesc_f16_f32(128, kTile, 0, 0), id_o = tc::idesc_f16_f32(128, D, 0, 1);
-            // Descriptors: 16 channels are 32 bytes of a swizzled row of Q and K, 64 a block of 128
-            // rows; 16 keys are 16 rows of V.  Only the low words differ.
-            const uint64_t dq = tc::smem_desc_sw128(q_sm, 16, 1024), dk = tc::smem_desc_sw128(k_sm, 16, 1024);
-            const uint64_t dv = tc::smem_desc_sw128(v_sm, 128 * 128, 1024);
-            uint32_t q_par = 0, p_par = 0, of_par = 3;           // bit t: row tile t
-            uint32_t f = 0;
-            // Tile i's weights times its values, and tile i + 1's scores: within a unit by turns, so that each
-            // row tile's softmax has the other's products to run under; at a unit's end the new
-            // unit's scores after both, since they wait for its rows.
-            bool fine = true;
+        // The whole warp walks the tiles, by values that are the same in every lane, so that
+        // the descriptors stay in uniform registers; one lane issues.
+        constexpr uint32_t id_s = tc::idesc_f16_f32(128, kTile, 0, 0), id_o = tc::idesc_f16_f32(128, D, 0, 1);
+        // Descriptors: 16 channels are 32 bytes of a swizzled row of Q and K, 64 a block of 128
+        // rows; 16 keys are 16 rows of V.  Only the low words differ.
+        const uint64_t dq = tc::smem_desc_sw128(q_sm, 16, 1024), dk = tc::smem_desc_sw128(k_sm, 16, 1024);
+        const uint64_t dv = tc::smem_desc_sw128(v_sm, 128 * 128, 1024);
+        const uint32_t ut = __shfl_sync(~0u, tmem, 0);
+        const bool leader = elect_one();
+        uint32_t q_par = 0, p_par = 0, of_par = 3;           // bit t: row tile t
+        uint32_t f = 0;
+        bool fine = true;
+        auto wait = [&](uint64_t *bar, uint32_t parity) {
+            fine = __all_sync(~0u, wait_bar(bar, parity, abort, status));
+            return fine;
+        };
+        // Tile i's weights times its values, and tile i + 1's scores: within a unit by turns, so that each
+        // row tile's softmax has the other's products to run under; at a unit's end the new
+        // unit's scores after both, since they wait for its rows.
 #pragma unroll 1
-            for (int32_t i = -1; i < total && fine; ++i) {
-                uint32_t g = 0;
-                const bool more = i + 1 < total;
-                if (more) {
-                    if (!wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status)) break;
-                    g = desc[(i + 1) % kDescs].flags;
-                }
-                const bool same = more && !(g & kFirst);
-                if (i >= 0) fine = wait_bar(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u, abort, status);
-                bool ready = false;
+        for (int32_t i = -1; i < total; ++i) {
+            uint32_t g = 0;
+            const bool more = i + 1 < total;
+            if (more) {
+                if (!wait(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u)) break;
+                g = __shfl_sync(~0u, desc[(i + 1) % kDescs].flags, 0);
+            }
+            const bool same = more && !(g & kFirst);
+            if (i >= 0 && !wait(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+            bool ready = false;
 #pragma unroll 1
-                for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4) && fine; ++k) {
-                    const uint32_t t = k & 1;
-                    if (k < 2 && (f & (kAct << t))) {
-                        fine = wait_bar(&s_pfull[t], p_par >> t & 1u, abort, status);
-                        p_par ^= 1u << t;
-                        const bool first = f & (kFirstAct << t);
-                        if (first) {
-                            fine = fine && wait_bar(&s_ofree[t], of_par >> t & 1u, abort, status);
-                            of_par ^= 1u << t;
-                        }
-                        if (!fine) break;
-                        tc::fence_after_sync();
-                        const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
-                        const uint32_t o = tm_o + D * t, w = tm_s + 128 * t;
+            for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4); ++k) {
+                const uint32_t t = k & 1;
+                if (k < 2 && (f & (kAct << t))) {
+                    if (!wait(&s_pfull[t], p_par >> t & 1u)) break;
+                    p_par ^= 1u << t;
+                    const bool first = f & (kFirstAct << t);
+                    if (first) {
+                        if (!wait(&s_ofree[t], of_par >> t & 1u)) break;
+                        of_par ^= 1u << t;
+                    }
+                    tc::fence_after_sync();
+                    const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
+                    const uint32_t o = ut + 256 + D * t, w = ut + 128 * t;
+                    if (leader) {
                         tc::mma_f16_ts(o, w, d, id_o, !first);
 #pragma unroll
                         for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
                         if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
                     }
-                    if (more && (same || k >= 2)) {
-                        if (!ready) {
-                            ready = true;
-                            fine = wait_bar(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u, abort, status);
-                            if (g & kFirst) {
-                                fine = fine && wait_bar(&s_qfull, q_par, abort, status);
-                                q_par ^= 1;
-                            }
-                            if (!fine) break;
-                            tc::fence_after_sync();
+                }
+                if (more && (same || k >= 2)) {
+                    if (!ready) {
+                        ready = true;
+                        if (!wait(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
+                        if (g & kFirst) {
+                            if (!wait(&s_qfull, q_par)) break;
+                            q_par ^= 1;
                         }
-                        if (g & (kAct << t)) {
-                            const uint64_t x = dq + t * (Sh::kQTile >> 4);
-                            const uint64_t y = dk + (uint32_t)(((i + 1) & 1) * (Sh::kKVTile >> 4));
+                        tc::fence_after_sync();
+                    }
+                    if (g & (kAct << t)) {
+                        const uint64_t x = dq + t * (Sh::kQTile >> 4);
+                        const uint64_t y = dk + (uint32_t)(((i + 1) & 1) * (Sh::kKVTile >> 4));
+                        if (leader) {
 #pragma unroll
                             for (int kk = 0; kk < D / 16; ++kk) {
                                 const uint32_t step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-                                tc::mma_f16(tm_s + 128 * t, x + step, y + step, id_s, kk != 0);
+                                tc::mma_f16(ut + 128 * t, x + step, y + step, id_s, kk != 0);
                             }
                             tc::commit(&s_sfull[t]);
                         }
                     }
                 }
-                if (!fine) break;
+            }
+            if (!fine) break;
+            if (leader) {
                 if (i >= 0) {
                     tc::commit(&s_vempty[i & 1]);
                     mbar_arrive(&s_tempty[i % kDescs]);
@@ -594,13 +611,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     tc::commit(&s_kempty[(i + 1) & 1]);
                     if (g & kLast) tc::commit(&s_qempty);
                 }
-                f = g;
             }
-            // every product issued has completed before tensor memory is released
-            tc::commit(&s_fin);
-            volatile int gone = 0;
-            wait_bar(&s_fin, 0, &gone, status);
+            f = g;
         }
+        // every product issued has completed before tensor memory is released
+        if (leader) tc::commit(&s_fin);
+        volatile int gone = 0;
+        wait_bar(&s_fin, 0, &gone, status);
         __syncwarp();
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ---- codes to fp16 operand tiles -----------------------------------------------------
