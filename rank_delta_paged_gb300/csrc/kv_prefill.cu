@@ -15,10 +15,11 @@
 // thread, so a row's maximum and sum need no exchange; warp 13 walks the work list, looks up
 // pages and exponents some tiles ahead and copies the codes by tensor maps into a ring of pieces
 // of 64 tokens; warps 8-11 convert them into the swizzled operand tiles (K by rows, V as it
-// stands: its channels run along N); one thread of warp 12 issues the products in the order
-// O_0 += P_0 V, S_0 = Q_0 K', O_1 += P_1 V, S_1 = Q_1 K' so that one row tile's softmax runs
-// under the other's products.  The roles' inner loops are kept short: with 14 warps in four
-// programs, straight-line code is fetched again for every tile, and the warps wait for that.
+// stands: its channels run along N); warps 12 and 14 issue the products of row tile 0 and 1,
+// O_t += P_t V and S_t = Q_t K' by turns, so that one row tile's softmax runs under the other's
+// products (one warp for both was the bound: an issue costs it some 60 cycles, of 64 that a product takes).
+// The roles' inner loops are kept short: with 15 warps in four programs, straight-line code is
+// fetched again for every tile, and the warps wait for that.
 //
 // The key tiles of all units form one list, of which every CTA takes an equal run; a unit that
 // is cut between CTAs is joined by the last of them to finish, in the order of the list.
@@ -37,8 +38,8 @@ namespace {
 
 constexpr int kTile = 128;                // keys per tile
 constexpr int kRows = 256;                // rows per unit
-constexpr int kThreads = 448;
-constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13;
+constexpr int kThreads = 480;
+constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kMmaWarp1 = 14;
 constexpr int kSeqChunks = 64;
 constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
 
@@ -107,6 +108,12 @@ __device__ __forceinline__ float2 unpair(uint64_t v)
 {
     float2 r;
     asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c)
+{
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
     return r;
 }
 __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
@@ -185,7 +192,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     Desc *desc = reinterpret_cast<Desc *>(smem_raw + (raw_sm + Sh::kPieces * Sh::kPiece - smem_u32(smem_raw)));
     __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
     __shared__ uint64_t s_rfull[Sh::kPieces], s_rempty[Sh::kPieces];
-    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_fin;
+    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin;
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
@@ -196,27 +203,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     if (tid == 0) {
         for (int i = 0; i < kDescs; ++i) {
             mbar_init(&s_tfull[i], 1);
-            mbar_init(&s_tempty[i], 13);         // 4 converting and 8 softmax warps, the issuing thread
+            mbar_init(&s_tempty[i], 14);         // 4 converting, 8 softmax and 2 issuing warps
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&s_kfull[i], 4);
-            mbar_init(&s_kempty[i], 1);
+            mbar_init(&s_kempty[i], 2);
             mbar_init(&s_vfull[i], 4);
-            mbar_init(&s_vempty[i], 1);
+            mbar_init(&s_vempty[i], 2);
             mbar_init(&s_sfull[i], 1);
             mbar_init(&s_pfull[i], 4);
             mbar_init(&s_odone[i], 1);
             mbar_init(&s_ofree[i], 4);
             mbar_init(&s_join[i], 4);
             mbar_init(&s_said[i], 1);
+            mbar_init(&s_turn[i], 1);
         }
         for (int i = 0; i < Sh::kPieces; ++i) {
             mbar_init(&s_rfull[i], 1);
             mbar_init(&s_rempty[i], 4);
         }
         mbar_init(&s_qfull, 4);
-        mbar_init(&s_qempty, 1);
-        mbar_init(&s_fin, 1);
+        mbar_init(&s_qempty, 2);
+        mbar_init(&s_fin, 2);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -361,6 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         int32_t r0 = 0, r1 = 0, tile = 0, c0 = 0, c1 = 0;
         bool whole = false;
         int32_t ta = 0, tb = 0;                    // the unit's key tiles in this CTA
+        int32_t plain_lo = 0, plain_hi = 0;        // keys that all of its rows see
         const int32_t *table = nullptr;
         auto enter = [&](int64_t u0) {             // the unit starts at u0 of the list
             r0 = rt * kRows;
@@ -376,6 +385,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             ta = u0 >= w0 ? ut.lo : ut.lo + (int32_t)(w0 - u0);
             tb = u1 <= w1 ? ut.hi : ut.hi - (int32_t)(u1 - w1);
             tile = ta;
+            plain_lo = first_key(a, u, div_group(a, r1 - 1));
+            plain_hi = end_key(a, u, div_group(a, r0));
             table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
         };
         int64_t u0 = base;
@@ -423,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (tile >= b && tile < e)
                         f |= (kAct << t) | (tile == b ? kFirstAct << t : 0) | (tile == e - 1 ? kLastAct << t : 0);
                 }
-                if (j0 >= first_key(a, u, div_group(a, r1 - 1)) && j0 + kTile <= end_key(a, u, div_group(a, r0))) f |= kPlain;
+                if (j0 >= plain_lo && j0 + kTile <= plain_hi) f |= kPlain;
                 int4 *di = reinterpret_cast<int4 *>(&d.flags);
                 di[0] = make_int4((int)f, j0, ut.k0, ut.k1);
                 di[1] = make_int4(u.row0, u.n, u.len, head);
@@ -524,93 +535,82 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             const int32_t n = issued - 1 - k;
             wait_bar(&s_rfull[n % Sh::kPieces], (uint32_t)(n / Sh::kPieces) & 1u, &gone, status);
         }
-    } else if (warp == kMmaWarp) {
-        // ---- products --------------------------------------------------------------------
+    } else if (warp == kMmaWarp || warp == kMmaWarp1) {
+        // ---- products of one row tile -------------------------------------------------------
         // The whole warp walks the tiles, by values that are the same in every lane, so that
         // the descriptors stay in uniform registers; one lane issues.
         constexpr uint32_t id_s = tc::idesc_f16_f32(128, kTile, 0, 0), id_o = tc::idesc_f16_f32(128, D, 0, 1);
+        const uint32_t t = __shfl_sync(~0u, warp == kMmaWarp1 ? 1u : 0u, 0);
         // Descriptors: 16 channels are 32 bytes of a swizzled row of Q and K, 64 a block of 128
         // rows; 16 keys are 16 rows of V.  Only the low words differ.
-        const uint64_t dq = tc::smem_desc_sw128(q_sm, 16, 1024), dk = tc::smem_desc_sw128(k_sm, 16, 1024);
+        const uint64_t dq = tc::smem_desc_sw128(q_sm + t * Sh::kQTile, 16, 1024), dk = tc::smem_desc_sw128(k_sm, 16, 1024);
         const uint64_t dv = tc::smem_desc_sw128(v_sm, 128 * 128, 1024);
-        const uint32_t ut = __shfl_sync(~0u, tmem, 0);
+        const uint32_t ut = __shfl_sync(~0u, tmem, 0), o = ut + 256 + D * t, w = ut + 128 * t;
         const bool leader = elect_one();
-        uint32_t q_par = 0, p_par = 0, of_par = 3;           // bit t: row tile t
-        uint32_t f = 0;
-        bool fine = true;
-        auto wait = [&](uint64_t *bar, uint32_t parity) {
-            fine = __all_sync(~0u, wait_bar(bar, parity, abort, status));
-            return fine;
+        uint32_t q_par = 0, p_par = 0, of_par = 1, turn = t ^ 1u, f = 0;
+        auto wait = [&](uint64_t *bar, uint32_t parity) { return __all_sync(~0u, wait_bar(bar, parity, abort, status)) != 0; };
+        auto scores = [&](int32_t j) {
+            const uint64_t y = dk + (uint32_t)((j & 1) * (Sh::kKVTile >> 4));
+            if (leader) {
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
+                    tc::mma_f16(w, dq + step, y + step, id_s, kk != 0);
+                }
+                tc::commit(&s_sfull[t]);
+            }
         };
-        // Tile i's weights times its values, and tile i + 1's scores: within a unit by turns, so that each
-        // row tile's softmax has the other's products to run under; at a unit's end the new
-        // unit's scores after both, since they wait for its rows.
+        // Tile i's weights times its values, then tile i + 1's scores, in turn with the other row tile's
+        // warp: products of both at once would end together, and the two softmaxes would run
+        // side by side instead of each under the other's products.
 #pragma unroll 1
         for (int32_t i = -1; i < total; ++i) {
+            const int32_t j = i + 1;
             uint32_t g = 0;
-            const bool more = i + 1 < total;
-            if (more) {
-                if (!wait(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u)) break;
-                g = __shfl_sync(~0u, desc[(i + 1) % kDescs].flags, 0);
+            if (j < total) {
+                if (!wait(&s_tfull[j % kDescs], (uint32_t)(j / kDescs) & 1u)) break;
+                g = __shfl_sync(~0u, desc[j % kDescs].flags, 0);
+                if (!wait(&s_kfull[j & 1], (uint32_t)(j >> 1) & 1u)) break;
             }
-            const bool same = more && !(g & kFirst);
-            if (i >= 0 && !wait(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u)) break;
-            bool ready = false;
-#pragma unroll 1
-            for (int k = i < 0 ? 2 : 0; k < (same ? 2 : 4); ++k) {
-                const uint32_t t = k & 1;
-                if (k < 2 && (f & (kAct << t))) {
-                    if (!wait(&s_pfull[t], p_par >> t & 1u)) break;
-                    p_par ^= 1u << t;
-                    const bool first = f & (kFirstAct << t);
+            const bool fresh = g & kFirst;           // tile j is another unit's: its rows are still to come
+            if (i >= 0) {
+                const bool act = f & (kAct << t), first = f & (kFirstAct << t);
+                if (!wait(&s_vfull[i & 1], (uint32_t)(i >> 1) & 1u)) break;
+                if (act) {
+                    if (!wait(&s_pfull[t], p_par)) break;
+                    p_par ^= 1u;
                     if (first) {
-                        if (!wait(&s_ofree[t], of_par >> t & 1u)) break;
-                        of_par ^= 1u << t;
+                        if (!wait(&s_ofree[t], of_par)) break;
+                        of_par ^= 1u;
                     }
-                    tc::fence_after_sync();
+                }
+                if (!wait(&s_turn[t], turn)) break;
+                turn ^= 1u;
+                tc::fence_after_sync();
+                if (act && leader) {
                     const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
-                    const uint32_t o = ut + 256 + D * t, w = ut + 128 * t;
-                    if (leader) {
-                        tc::mma_f16_ts(o, w, d, id_o, !first);
+                    tc::mma_f16_ts(o, w, d, id_o, !first);
 #pragma unroll
-                        for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
-                        if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
-                    }
+                    for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
+                    if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
                 }
-                if (more && (same || k >= 2)) {
-                    if (!ready) {
-                        ready = true;
-                        if (!wait(&s_kfull[(i + 1) & 1], (uint32_t)((i + 1) >> 1) & 1u)) break;
-                        if (g & kFirst) {
-                            if (!wait(&s_qfull, q_par)) break;
-                            q_par ^= 1;
-                        }
-                        tc::fence_after_sync();
-                    }
-                    if (g & (kAct << t)) {
-                        const uint64_t x = dq + t * (Sh::kQTile >> 4);
-                        const uint64_t y = dk + (uint32_t)(((i + 1) & 1) * (Sh::kKVTile >> 4));
-                        if (leader) {
-#pragma unroll
-                            for (int kk = 0; kk < D / 16; ++kk) {
-                                const uint32_t step = ((kk >> 2) * (128 * 128) + (kk & 3) * 32) >> 4;
-                                tc::mma_f16(ut + 128 * t, x + step, y + step, id_s, kk != 0);
-                            }
-                            tc::commit(&s_sfull[t]);
-                        }
-                    }
-                }
-            }
-            if (!fine) break;
-            if (leader) {
-                if (i >= 0) {
+                if (j < total && !fresh && (g & (kAct << t))) scores(j);
+                if (leader) {
+                    mbar_arrive(&s_turn[t ^ 1u]);
                     tc::commit(&s_vempty[i & 1]);
                     mbar_arrive(&s_tempty[i % kDescs]);
                 }
-                if (more) {
-                    tc::commit(&s_kempty[(i + 1) & 1]);
-                    if (g & kLast) tc::commit(&s_qempty);
-                }
+            }
+            if (j == total) break;
+            if (fresh) {
+                if (!wait(&s_qfull, q_par)) break;
+                q_par ^= 1;
+                tc::fence_after_sync();
+                if (g & (kAct << t)) scores(j);
+            }
+            if (leader) {
+                tc::commit(&s_kempty[j & 1]);
+                if (g & kLast) tc::commit(&s_qempty);
             }
             f = g;
         }
@@ -633,7 +633,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         for (int32_t i = 0; i < total && !*abort; ++i) {
             if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
             const Desc &d = desc[i % kDescs];
-            if (d.flags & kFirst) {
+            if (__builtin_expect(d.flags & kFirst, 0)) {
                 // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
                 if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                 qe_par ^= 1;
@@ -676,7 +676,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     const int c = D == 128 ? (ch + 4 * ((x ^ rw) & 1)) ^ (row & 7) : ch ^ (row >> 1 & 3);
                     r[x] = lds128(src + row * D + c * 16);
                 }
-                if (!all) {
+                if (__builtin_expect(!all, 0)) {
 #pragma unroll
                     for (int x = 0; x < NL; ++x) {
                         const int row = rw + 32 * (D == 128 ? x >> 1 : x) + 64 * (k & 1);
@@ -750,37 +750,42 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 const int32_t m0 = klo - d.j0;
                 const uint32_t mn = khi > klo ? (uint32_t)(khi - klo) : 0u;
                 const uint32_t ok = d.ok;
-                auto mask = [&](uint32_t (&x)[32], int h) {
-                    if (plain) return;
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const bool see = (uint32_t)(32 * h + k - m0) < mn && (ok >> (4 * h + k / 8) & 1u);
-                        if (!see) x[k] = 0xFF800000u;
-                    }
-                };
-                // The loops over a tile's columns stay rolled: unrolled, the roles' code does not fit the
-                // instruction caches (0.39 PFLOP/s on a long chunk, 0.52 rolled).
+                // The loops over a tile's columns stay rolled and what is rare stays out of them: the
+                // roles' code has to fit the instruction caches.
                 uint32_t x[32];
-                if (__any_sync(~0u, mx == -INFINITY)) {
+                if (__builtin_expect(!plain, 0)) {
+                    // scores of unseen keys, in place
+#pragma unroll 1
+                    for (int h = 0; h < 4; ++h) {
+                        tc::ld_32x32b_x32(ts + 32 * h, x);
+                        tc::ld_wait(x);
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) {
+                            const bool see = (uint32_t)(32 * h + k - m0) < mn && (ok >> (4 * h + k / 8) & 1u);
+                            if (!see) x[k] = 0xFF800000u;
+                        }
+                        tc::st_32x32b_x32(ts + 32 * h, x);
+                    }
+                    tc::st_wait();
+                }
+                if (__builtin_expect(__any_sync(~0u, mx == -INFINITY), 0)) {
                     // rows that have seen nothing yet start from this tile's maximum
                     float top = -INFINITY;
 #pragma unroll 1
                     for (int h = 0; h < 4; ++h) {
                         tc::ld_32x32b_x32(ts + 32 * h, x);
                         tc::ld_wait(x);
-                        mask(x, h);
                         top = fmaxf(top, top_of(d, x, h));
                     }
                     if (mx == -INFINITY) mx = ceilf(top);
                 }
                 // The weights, 32 keys at a time, by the running maximum as it stands: an integer, so that
-                // following it is exact.  It follows only when a weight passes 2^8, far inside fp16, and
-                // then what was made with the old one is divided by a power of two.
+                // following it is exact.  It follows only when the 32 weights' sum passes 2^8 (fp16
+                // ends at 2^16), and then what was made with the old one is divided by a power of two.
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
                     tc::ld_32x32b_x32(ts + 32 * h, x);
                     tc::ld_wait(x);
-                    mask(x, h);
                     const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
                     const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
                     const float4 li = *reinterpret_cast<const float4 *>(&d.li[4 * h]);
@@ -791,25 +796,27 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     uint32_t pk[16];
                     float add;
                     for (int turn = 0;; ++turn) {
-                        __half2 hm = __float2half2_rn(0.f);
+                        float all = 0.f;
                         add = 0.f;
 #pragma unroll
                         for (int g = 0; g < 4; ++g) {
+                            const uint64_t k2 = pair(kx[g], kx[g]), l2 = pair(lx[g], lx[g]);
                             uint64_t s2 = 0;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) {
-                                const float e0 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k]), kx[g], lx[g]));
-                                const float e1 = ex2(fmaf(__uint_as_float(x[8 * g + 2 * k + 1]), kx[g], lx[g]));
+                                const float2 z = unpair(fma2(pair(__uint_as_float(x[8 * g + 2 * k]),
+                                                                  __uint_as_float(x[8 * g + 2 * k + 1])), k2, l2));
+                                const float e0 = ex2(z.x), e1 = ex2(z.y);
                                 s2 = add2(s2, pair(e0, e1));
                                 const __half2 hh = __floats2half2_rn(e0, e1);
-                                hm = __hmax2(hm, hh);
                                 pk[4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
                             }
                             const float2 sg = unpair(s2);
+                            all += sg.x + sg.y;
                             add = fmaf(sg.x + sg.y, il[g], add);
                         }
-                        const bool up = __hgt(__hmax(__low2half(hm), __high2half(hm)), __float2half(256.f));
-                        if (turn == 1 || !__any_sync(~0u, up)) break;
+                        const bool up = all > 256.f;
+                        if (__builtin_expect(turn == 1 || !__any_sync(~0u, up), 1)) break;
                         const float nm = up ? ceilf(top_of(d, x, h)) : mx;
                         const float k = mx == nm ? 1.f : ex2(mx - nm);
                         mx = nm;
