@@ -280,7 +280,7 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     const bool big = most > kSmallRows;
     const bool alike = (int64_t)a.b.T * 4 >= (int64_t)a.b.S * a.b.max_q * 3;
     if (e == cudaSuccess && big)
-        e = kv::launch_attend_prefill(a, k->maps, k->head_dim, k->format, alike ? 0 : kSmallRows,
+        e = kv::launch_attend_prefill(a, k->head_dim, k->format, alike ? 0 : kSmallRows,
                                       k->ws + kv::decode_workspace_bytes(k->num_sms), k->num_sms, (cudaStream_t)stream,
                                       &launches);
     if (e == cudaSuccess && !(big && alike))

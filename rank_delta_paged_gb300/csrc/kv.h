@@ -232,7 +232,7 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
 
 // The rows of sequences with more than small_rows rows per KV head.
 size_t prefill_workspace_bytes(int num_sms);
-cudaError_t launch_attend_prefill(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
+cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
                                   cudaStream_t stream, int *launches);
 
 }  // namespace kv

@@ -12,10 +12,11 @@
 // converted once per unit and tile for both row tiles (a sixteenth of the exponentials' work).
 //
 // Per CTA (one per SM): warps 0-3 and 4-7 are the softmax of row tile 0 and 1, a row per
-// thread, so a row's maximum and sum need no exchange; warp 13 walks the work list, looks up
-// pages and exponents some tiles ahead and copies the codes by tensor maps into a ring of pieces
-// of 64 tokens; warps 8-11 convert them into the swizzled operand tiles (K by rows, V as it
-// stands: its channels run along N); warps 12 and 14 issue the products of row tile 0 and 1,
+// thread, so a row's maximum and sum need no exchange; warp 13 walks the work list and looks up
+// pages and exponents some tiles ahead; warps 8-11 read the codes, a tile ahead in registers,
+// and convert them into the swizzled operand tiles (K by rows, V as it stands: its channels run
+// along N; tensor-map copies into a ring of raw pieces cost these warps more in waits than the
+// loads do); warps 12 and 14 issue the products of row tile 0 and 1,
 // O_t += P_t V and S_t = Q_t K' by turns, so that one row tile's softmax runs under the other's
 // products (one warp for both was the bound: an issue costs it some 60 cycles, of 64 that a product takes).
 // The roles' inner loops are kept short: with 15 warps in four programs, straight-line code is
@@ -51,8 +52,7 @@ enum : uint32_t {
 };
 
 struct Desc {
-    int32_t page[2][16];    // keys' and values' page of 8 tokens
-    int32_t row[16];        // and the first row there of their box of 16 (8) tokens
+    int64_t off[2][16];     // keys and values: bytes from the pool's start to the first row of 8 tokens
     float ks[16];           // 2^exponent of the key pages, per 8 tokens
     float lv[16];           // exponent of the value pages
     float li[16];           // 2^-exponent of the value pages
@@ -72,10 +72,7 @@ struct Shape {
     static constexpr int kBlocks = D / 64;                   // 64-channel blocks of 128-byte rows
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kKVTile = kTile * D * 2;
-    static constexpr int kPiece = 64 * D;                    // codes of 64 tokens, keys or values
-    static constexpr int kPieces = D == 128 ? 3 : 6;
-    static constexpr size_t kSmem =
-        1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kPieces * kPiece + kDescs * sizeof(Desc);
+    static constexpr size_t kSmem = 1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kDescs * sizeof(Desc);
     static constexpr int kPart = 2 * 128 + 128 * D;          // floats of a row tile's partial result: m, l, O
 };
 
@@ -122,17 +119,12 @@ __device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
     asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
     return r;
 }
-__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void *map, int32_t c1, int32_t c2, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, "
-                 "%3, %4}], [%5];" ::"r"(dst),
-                 "l"(map), "r"(0), "r"(c1), "r"(c2), "r"(smem_u32(bar))
-                 : "memory");
-}
-__device__ __forceinline__ uint4 lds128(uint32_t ad)
+__device__ __forceinline__ uint4 ld_codes(const uint8_t *p)
 {
     uint4 v;
-    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ad));
+    asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.b32 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
+                 : "l"(p));
     return v;
 }
 __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
@@ -180,18 +172,15 @@ __device__ __forceinline__ int32_t unit_count(const AttendArgs &a, const Seq &q,
 }
 
 template <int D, int FMT>
-__global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p,
-                                                                     const __grid_constant__ PageMaps maps)
+__global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using Sh = Shape<D>;
     constexpr int NB = Sh::kBlocks;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t q_sm = (smem_u32(smem_raw) + 1023) & ~1023u;      // two row tiles
     const uint32_t k_sm = q_sm + 2 * Sh::kQTile, v_sm = k_sm + 2 * Sh::kKVTile;
-    const uint32_t raw_sm = v_sm + 2 * Sh::kKVTile;
-    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (raw_sm + Sh::kPieces * Sh::kPiece - smem_u32(smem_raw)));
+    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (v_sm + 2 * Sh::kKVTile - smem_u32(smem_raw)));
     __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
-    __shared__ uint64_t s_rfull[Sh::kPieces], s_rempty[Sh::kPieces];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin;
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
@@ -217,10 +206,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             mbar_init(&s_join[i], 4);
             mbar_init(&s_said[i], 1);
             mbar_init(&s_turn[i], 1);
-        }
-        for (int i = 0; i < Sh::kPieces; ++i) {
-            mbar_init(&s_rfull[i], 1);
-            mbar_init(&s_rempty[i], 4);
         }
         mbar_init(&s_qfull, 4);
         mbar_init(&s_qempty, 2);
@@ -470,9 +455,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         Box b0 = none, b1 = none, b2 = none, b3 = none, b4;
         bool n0 = false, n1 = false, n2 = false, n3 = false, n4;
         int32_t e0 = 0, e1 = 0, e2;
-        int piece = 0;
-        uint32_t piece_parity = 1;
-        int32_t issued = 0;
 #pragma unroll 1
         for (int32_t i = -4;;
              ++i, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
@@ -485,9 +467,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             have &= have >> 1 & 0x55555555u;               // a group needs both its keys and its values
             const bool both = have >> (2 * gl) & 1u;
             const int e = both ? clamp_exponent(e0) : 0;
-            d.page[kvl][gl] = b0.page;
+            d.off[kvl][gl] = both ? (int64_t)b0.page * a.c.page_bytes + (b0.row + (8 * gl & (R - 1))) * D : 0;
             if (kvl == 0) {
-                d.row[gl] = b0.row;
                 d.ks[gl] = pow2(e);
             } else {
                 d.lv[gl] = (float)e;
@@ -502,38 +483,6 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_tfull[i % kDescs]);
-            // the tile's pieces: keys 0-63, 64-127, values 0-63, 64-127
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                if (!wait_bar(&s_rempty[piece], piece_parity, abort, status)) break;
-                if (lane == 0) {
-                    const int g0 = 8 * (k & 1);
-                    const uint32_t o = d.ok >> g0 & 255u, dst = raw_sm + piece * Sh::kPiece;
-                    const int32_t *pg = &d.page[k >> 1][g0], *rw = &d.row[g0];
-                    uint64_t *bar = &s_rfull[piece];
-                    mbar_arrive_expect_tx(bar, (uint32_t)__popc(o) * 8u * D);
-                    // as one box if no block starts within, else in boxes of R rows
-                    if (R == 16 && o == 255u && rw[2] && rw[4] && rw[6]) {
-                        tma_load_3d(dst, &maps.m[2], rw[0], pg[0], bar);
-                    } else {
-#pragma unroll 1
-                        for (int x = 0; x < 8; x += R / 8)
-                            if (o >> x & 1u) tma_load_3d(dst + x * 8 * D, &maps.m[0], rw[x], pg[x], bar);
-                    }
-                }
-                ++issued;
-                if (++piece == Sh::kPieces) {
-                    piece = 0;
-                    piece_parity ^= 1;
-                }
-            }
-        }
-        // no copy outlives the CTA
-        volatile int gone = 0;
-#pragma unroll 1
-        for (int k = 0; k < Sh::kPieces && k < issued && !gone; ++k) {
-            const int32_t n = issued - 1 - k;
-            wait_bar(&s_rfull[n % Sh::kPieces], (uint32_t)(n / Sh::kPieces) & 1u, &gone, status);
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
         // ---- products of one row tile -------------------------------------------------------
@@ -622,17 +571,64 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ---- codes to fp16 operand tiles -----------------------------------------------------
         const int ct = tid - kConvWarp * 32;                   // 0 .. 127
-        const int ch = ct & 3, rw = ct >> 2;
+        // Warp w of the four has rows 32 w .. + 31: a lane loads chunks ch (and ch + 4 if D = 128) of rows rw,
+        // rw + 8, rw + 16, rw + 24, so that eight lanes store to all banks.
+        constexpr int NC = D / 64, NL = 4 * NC;
+        const int ch = lane & 3, r0 = (warp - kConvWarp) * 32, rw = lane >> 2;
+        const uint8_t *codes = a.c.pool + rw * D + ch * 16;
+        const uint32_t put = (r0 + rw) * 128 + (((2 * ch) ^ rw) << 4);
+        auto load = [&](const Desc &d, int kvl, uint4 (&r)[NL]) {
+            const longlong2 *o = reinterpret_cast<const longlong2 *>(&d.off[kvl][r0 / 8]);
+            const longlong2 o0 = o[0], o1 = o[1];
+            const int64_t at[4] = {o0.x, o0.y, o1.x, o1.y};
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) r[x * NC + c] = ld_codes(codes + at[x] + 64 * c);
+        };
+        auto store = [&](const Desc &d, uint32_t dst, uint4 (&r)[NL]) {
+            // the conversions stay behind the waits before this call: moved up to the loads, they
+            // would wait for them there
+#pragma unroll
+            for (int x = 0; x < NL; ++x) asm volatile("" : "+r"(r[x].x), "+r"(r[x].y), "+r"(r[x].z), "+r"(r[x].w));
+            if (__builtin_expect(!(d.ok == 0xFFFFu && d.j0 >= d.lo && d.j0 + kTile <= d.hi), 0)) {
+                // rows that are not seen may hold anything: zeros
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                    const int row = r0 + rw + 8 * x;
+                    const int32_t j = d.j0 + row;
+                    if (!((d.ok >> (row >> 3) & 1u) && j >= d.lo && j < d.hi))
+#pragma unroll
+                        for (int c = 0; c < NC; ++c) r[x * NC + c] = make_uint4(0, 0, 0, 0);
+                }
+            }
+#pragma unroll
+            for (int x = 0; x < 4; ++x)
+#pragma unroll
+                for (int c = 0; c < NC; ++c) {
+                    const uint4 v = r[x * NC + c];
+                    const uint32_t at = dst + put + x * 8 * 128 + c * (128 * 128);
+                    uint32_t h[8];
+                    decode4<FMT>(v.x, h[0], h[1]);
+                    decode4<FMT>(v.y, h[2], h[3]);
+                    decode4<FMT>(v.z, h[4], h[5]);
+                    decode4<FMT>(v.w, h[6], h[7]);
+                    sts128(at, h[0], h[1], h[2], h[3]);
+                    sts128(at ^ 16u, h[4], h[5], h[6], h[7]);
+                }
+        };
         auto done = [&](uint64_t *bar) {
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        uint32_t qe_par = 1, r_par = 0;
-        int piece = 0;
+        uint4 rk[NL], rv[NL];
+        uint32_t qe_par = 1;
+        if (wait_bar(&s_tfull[0], 0, abort, status)) load(desc[0], 0, rk);
+#pragma unroll 1
         for (int32_t i = 0; i < total && !*abort; ++i) {
-            if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
             const Desc &d = desc[i % kDescs];
+            load(d, 1, rv);
             if (__builtin_expect(d.flags & kFirst, 0)) {
                 // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
                 if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
@@ -656,54 +652,17 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 }
                 done(&s_qfull);
             }
-            // rows that are not seen hold anything in the ring, and zeros in the operands
-            const bool all = d.ok == 0xFFFFu && d.j0 >= d.lo && d.j0 + kTile <= d.hi;
-#pragma unroll 1
-            for (int k = 0; k < 4; ++k) {
-                if ((k & 1) == 0) {
-                    if (!wait_bar(k ? &s_vempty[i & 1] : &s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
-                }
-                if (!wait_bar(&s_rfull[piece], r_par, abort, status)) break;
-                const uint32_t src = raw_sm + piece * Sh::kPiece;
-                const uint32_t dst = (k >> 1 ? v_sm : k_sm) + (i & 1) * Sh::kKVTile + (k & 1) * 64 * 128;
-                // Step x: chunk ch + 4 ((x ^ row) & 1) of row rw + 32 (x >> 1)  (D = 128), or chunk ch of row
-                // rw + 32 x: eight lanes read from, and write to, all banks.
-                constexpr int NL = D / 32;
-                uint4 r[NL];
-#pragma unroll
-                for (int x = 0; x < NL; ++x) {
-                    const int row = rw + 32 * (D == 128 ? x >> 1 : x);
-                    const int c = D == 128 ? (ch + 4 * ((x ^ rw) & 1)) ^ (row & 7) : ch ^ (row >> 1 & 3);
-                    r[x] = lds128(src + row * D + c * 16);
-                }
-                if (__builtin_expect(!all, 0)) {
-#pragma unroll
-                    for (int x = 0; x < NL; ++x) {
-                        const int row = rw + 32 * (D == 128 ? x >> 1 : x) + 64 * (k & 1);
-                        const int32_t j = d.j0 + row;
-                        if (!((d.ok >> (row >> 3) & 1u) && j >= d.lo && j < d.hi)) r[x] = make_uint4(0, 0, 0, 0);
-                    }
-                }
-#pragma unroll
-                for (int x = 0; x < NL; ++x) {
-                    const int row = rw + 32 * (D == 128 ? x >> 1 : x);
-                    const uint32_t at = dst + (D == 128 ? ((x ^ rw) & 1) * (128 * 128) : 0) + row * 128;
-                    uint32_t h[8];
-                    decode4<FMT>(r[x].x, h[0], h[1]);
-                    decode4<FMT>(r[x].y, h[2], h[3]);
-                    decode4<FMT>(r[x].z, h[4], h[5]);
-                    decode4<FMT>(r[x].w, h[6], h[7]);
-                    sts128(at + (((2 * ch) ^ (row & 7)) << 4), h[0], h[1], h[2], h[3]);
-                    sts128(at + (((2 * ch + 1) ^ (row & 7)) << 4), h[4], h[5], h[6], h[7]);
-                }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&s_rempty[piece]);
-                if (++piece == Sh::kPieces) {
-                    piece = 0;
-                    r_par ^= 1;
-                }
-                if (k & 1) done(k >> 1 ? &s_vfull[i & 1] : &s_kfull[i & 1]);
+            const uint32_t par = ((uint32_t)(i >> 1) & 1u) ^ 1u;
+            if (!wait_bar(&s_kempty[i & 1], par, abort, status)) break;
+            store(d, k_sm + (i & 1) * Sh::kKVTile, rk);
+            done(&s_kfull[i & 1]);
+            if (i + 1 < total) {
+                if (!wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status)) break;
+                load(desc[(i + 1) % kDescs], 0, rk);
             }
+            if (!wait_bar(&s_vempty[i & 1], par, abort, status)) break;
+            store(d, v_sm + (i & 1) * Sh::kKVTile, rv);
+            done(&s_vfull[i & 1]);
             if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
         }
     } else if (warp < kConvWarp) {
@@ -998,7 +957,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 }
 
 template <int D, int FMT>
-cudaError_t launch(const PrefillParams &p, const PageMaps &maps, int num_sms, cudaStream_t stream)
+cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
 {
     static std::mutex mu;
     static bool set[64] = {};
@@ -1024,7 +983,7 @@ cudaError_t launch(const PrefillParams &p, const PageMaps &maps, int num_sms, cu
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p, maps);
+    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p);
 }
 
 }  // namespace
@@ -1034,7 +993,7 @@ size_t prefill_workspace_bytes(int num_sms)
     return (size_t)num_sms * 4 * Shape<128>::kPart * 4 + (size_t)num_sms * 2 * 4;
 }
 
-cudaError_t launch_attend_prefill(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
+cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
                                   cudaStream_t stream, int *launches)
 {
     PrefillParams p;
@@ -1052,9 +1011,9 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, const PageMaps &maps, int
     p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
     cudaError_t e;
     if (head_dim == 128)
-        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, maps, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, maps, num_sms, stream);
+        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, num_sms, stream);
     else
-        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, maps, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, maps, num_sms, stream);
+        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, num_sms, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
