@@ -622,48 +622,59 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
+        // The rows of a unit, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s.
+        auto load_rows = [&](const Desc &e) {
+            const int qc = ct & 7;
+            const int32_t nrows = e.nrows, steps = nrows > 128 ? 16 : 8;
+#pragma unroll 4
+            for (int s = 0; s < steps; ++s) {
+                const int row = (ct >> 3) + 16 * s;
+                const int32_t r = e.r0 + (row < nrows ? row : 0);
+                const int32_t tok = div_group(a, r);
+                const __half *src = a.q + (int64_t)(e.row0 + tok) * a.q_stride +
+                                    ((int64_t)e.head * a.group + (r - tok * a.group)) * D + qc * 8;
+#pragma unroll
+                for (int b = 0; b < NB; ++b) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (row < nrows) v = __ldg(reinterpret_cast<const uint4 *>(src + b * 64));
+                    sts128(q_sm + (row >> 7) * Sh::kQTile + b * (128 * 128) + (row & 127) * 128 + ((qc ^ (row & 7)) << 4),
+                           v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
+                }
+            }
+            done(&s_qfull);
+        };
+        // Keys run a tile ahead of values: K_0, K_1, V_0, K_2, V_1, ..
         uint4 rk[NL], rv[NL];
         uint32_t qe_par = 1;
-        if (wait_bar(&s_tfull[0], 0, abort, status)) load(desc[0], 0, rk);
 #pragma unroll 1
-        for (int32_t i = 0; i < total && !*abort; ++i) {
-            const Desc &d = desc[i % kDescs];
-            load(d, 1, rv);
-            if (__builtin_expect(d.flags & kFirst, 0)) {
-                // the unit's rows, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s
+        for (int32_t i = -1; i < total && !*abort; ++i) {
+            const int32_t j = i + 1;
+            if (i < 0) {
+                if (!wait_bar(&s_tfull[0], 0, abort, status)) break;
+                load(desc[0], 0, rk);
+            } else {
+                load(desc[i % kDescs], 1, rv);
+            }
+            if (j < total) {
+                if (!wait_bar(&s_kempty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, status)) break;
+                store(desc[j % kDescs], k_sm + (j & 1) * Sh::kKVTile, rk);
+                done(&s_kfull[j & 1]);
+                if (j + 1 < total) {
+                    if (!wait_bar(&s_tfull[(j + 1) % kDescs], (uint32_t)((j + 1) / kDescs) & 1u, abort, status)) break;
+                    load(desc[(j + 1) % kDescs], 0, rk);
+                }
+            }
+            if (i >= 0) {
+                if (!wait_bar(&s_vempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
+                store(desc[i % kDescs], v_sm + (i & 1) * Sh::kKVTile, rv);
+                done(&s_vfull[i & 1]);
+                if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
+            }
+            if (j < total && __builtin_expect(desc[j % kDescs].flags & kFirst, 0)) {
                 if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                 qe_par ^= 1;
-                const int qc = ct & 7;
-                const int32_t nrows = d.nrows, steps = nrows > 128 ? 16 : 8;
-#pragma unroll 4
-                for (int s = 0; s < steps; ++s) {
-                    const int row = (ct >> 3) + 16 * s;
-                    const int32_t r = d.r0 + (row < nrows ? row : 0);
-                    const int32_t tok = div_group(a, r);
-                    const __half *src = a.q + (int64_t)(d.row0 + tok) * a.q_stride +
-                                        ((int64_t)d.head * a.group + (r - tok * a.group)) * D + qc * 8;
-#pragma unroll
-                    for (int b = 0; b < NB; ++b) {
-                        uint4 v = make_uint4(0, 0, 0, 0);
-                        if (row < nrows) v = __ldg(reinterpret_cast<const uint4 *>(src + b * 64));
-                        sts128(q_sm + (row >> 7) * Sh::kQTile + b * (128 * 128) + (row & 127) * 128 + ((qc ^ (row & 7)) << 4),
-                               v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
-                    }
-                }
-                done(&s_qfull);
+                load_rows(desc[j % kDescs]);
             }
-            const uint32_t par = ((uint32_t)(i >> 1) & 1u) ^ 1u;
-            if (!wait_bar(&s_kempty[i & 1], par, abort, status)) break;
-            store(d, k_sm + (i & 1) * Sh::kKVTile, rk);
-            done(&s_kfull[i & 1]);
-            if (i + 1 < total) {
-                if (!wait_bar(&s_tfull[(i + 1) % kDescs], (uint32_t)((i + 1) / kDescs) & 1u, abort, status)) break;
-                load(desc[(i + 1) % kDescs], 0, rk);
-            }
-            if (!wait_bar(&s_vempty[i & 1], par, abort, status)) break;
-            store(d, v_sm + (i & 1) * Sh::kKVTile, rv);
-            done(&s_vfull[i & 1]);
-            if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
         }
     } else if (warp < kConvWarp) {
         // ---- softmax: one row per thread -------------------------------------------------------
@@ -741,56 +752,50 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 // The weights, 32 keys at a time, by the running maximum as it stands: an integer, so that
                 // following it is exact.  It follows only when the 32 weights' sum passes 2^8 (fp16
                 // ends at 2^16), and then what was made with the old one is divided by a power of two.
+                uint32_t xa[16], xb[16], pk[16];
+                float raw, add, base = mx == -INFINITY ? 0.f : mx;
+                // 16 scores into pk[at ..], their sums plain and without the value pages' scales
+                auto weigh = [&](const uint32_t (&v)[16], int c, int at) {
+                    const float2 ks = *reinterpret_cast<const float2 *>(&d.ks[2 * c]);
+                    const float2 lv = *reinterpret_cast<const float2 *>(&d.lv[2 * c]);
+                    const float2 li = *reinterpret_cast<const float2 *>(&d.li[2 * c]);
+#pragma unroll
+                    for (int g = 0; g < 2; ++g) {
+                        const float kx = (g ? ks.y : ks.x) * p.scale, lx = (g ? lv.y : lv.x) - base;
+                        const uint64_t k2 = pair(kx, kx), l2 = pair(lx, lx);
+                        uint64_t s2 = 0;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 z = unpair(fma2(pair(__uint_as_float(v[8 * g + 2 * k]),
+                                                              __uint_as_float(v[8 * g + 2 * k + 1])), k2, l2));
+                            const float e0 = ex2(z.x), e1 = ex2(z.y);
+                            s2 = add2(s2, pair(e0, e1));
+                            const __half2 hh = __floats2half2_rn(e0, e1);
+                            pk[at + 4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
+                        }
+                        const float2 sg = unpair(s2);
+                        raw += sg.x + sg.y;
+                        add = fmaf(sg.x + sg.y, g ? li.y : li.x, add);
+                    }
+                };
+                tc::ld_32x32b_x16(ts, xa);
 #pragma unroll 1
                 for (int h = 0; h < 4; ++h) {
-                    tc::ld_32x32b_x32(ts + 32 * h, x);
-                    tc::ld_wait(x);
-                    const float4 ks = *reinterpret_cast<const float4 *>(&d.ks[4 * h]);
-                    const float4 lv = *reinterpret_cast<const float4 *>(&d.lv[4 * h]);
-                    const float4 li = *reinterpret_cast<const float4 *>(&d.li[4 * h]);
-                    const float base = mx == -INFINITY ? 0.f : mx;
-                    float kx[4] = {ks.x * p.scale, ks.y * p.scale, ks.z * p.scale, ks.w * p.scale};
-                    float lx[4] = {lv.x - base, lv.y - base, lv.z - base, lv.w - base};
-                    const float il[4] = {li.x, li.y, li.z, li.w};
-                    uint32_t pk[16];
-                    float add;
-                    for (int turn = 0;; ++turn) {
-                        float all = 0.f;
-                        add = 0.f;
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-                            const uint64_t k2 = pair(kx[g], kx[g]), l2 = pair(lx[g], lx[g]);
-                            uint64_t s2 = 0;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                const float2 z = unpair(fma2(pair(__uint_as_float(x[8 * g + 2 * k]),
-                                                                  __uint_as_float(x[8 * g + 2 * k + 1])), k2, l2));
-                                const float e0 = ex2(z.x), e1 = ex2(z.y);
-                                s2 = add2(s2, pair(e0, e1));
-                                const __half2 hh = __floats2half2_rn(e0, e1);
-                                pk[4 * g + k] = *reinterpret_cast<const uint32_t *>(&hh);
-                            }
-                            const float2 sg = unpair(s2);
-                            all += sg.x + sg.y;
-                            add = fmaf(sg.x + sg.y, il[g], add);
-                        }
-                        const bool up = all > 256.f;
-                        if (__builtin_expect(turn == 1 || !__any_sync(~0u, up), 1)) break;
+                    raw = add = 0.f;
+                    tc::ld_wait(xa);
+                    tc::ld_32x32b_x16(ts + 32 * h + 16, xb);
+                    weigh(xa, 2 * h, 0);
+                    tc::ld_wait(xb);
+                    tc::ld_32x32b_x16(ts + (32 * (h + 1) & 127), xa);      // (not used after the last)
+                    weigh(xb, 2 * h + 1, 8);
+                    const bool up = raw > 256.f;
+                    if (__builtin_expect(__any_sync(~0u, up), 0)) {
+                        tc::ld_32x32b_x32(ts + 32 * h, x);
+                        tc::ld_wait(x);
                         const float nm = up ? ceilf(top_of(d, x, h)) : mx;
                         const float k = mx == nm ? 1.f : ex2(mx - nm);
                         mx = nm;
-                        // The second turn takes scores rounded as the maximum was, so that no weight is above 1
-                        // however large they are.
-                        const float nb = mx == -INFINITY ? 0.f : mx;
-                        const float kv[4] = {ks.x, ks.y, ks.z, ks.w}, lw[4] = {lv.x, lv.y, lv.z, lv.w};
-#pragma unroll
-                        for (int g = 0; g < 4; ++g) {
-#pragma unroll
-                            for (int j = 0; j < 8; ++j)
-                                x[8 * g + j] = __float_as_uint(fmaf(__uint_as_float(x[8 * g + j]), kv[g] * p.scale, lw[g]) - nb);
-                            kx[g] = 1.f;
-                            lx[g] = 0.f;
-                        }
+                        base = mx == -INFINITY ? 0.f : mx;
                         sum *= k;
                         uint32_t y[16];
                         if (any)
@@ -815,11 +820,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                             tc::st_32x32b_x16(ts + 16 * c, y);
                         }
                         tc::st_wait();
+                        // these 32 again, from scores rounded as the maximum was, so that no weight
+                        // is above 1 however large they are
+                        add = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 32; j += 2) {
+                            const float kv = d.ks[4 * h + j / 8] * p.scale, l = d.lv[4 * h + j / 8];
+                            const float e0 = ex2(fmaf(__uint_as_float(x[j]), kv, l) - base);
+                            const float e1 = ex2(fmaf(__uint_as_float(x[j + 1]), kv, l) - base);
+                            add = fmaf(e0 + e1, d.li[4 * h + j / 8], add);
+                            const __half2 hh = __floats2half2_rn(e0, e1);
+                            pk[j / 2] = *reinterpret_cast<const uint32_t *>(&hh);
+                        }
                     }
                     sum += add;
                     // columns already read: 32 keys' weights take 16 of the 32 that their scores took
                     tc::st_32x32b_x16(ts + 16 * h, pk);
                 }
+                tc::ld_wait(xa);
                 any = true;
                 tc::st_wait();
                 tc::fence_before_sync();
