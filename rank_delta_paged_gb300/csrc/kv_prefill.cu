@@ -82,8 +82,8 @@ struct PrefillParams {
     int32_t box_rows;      // 16 if blocks are multiples of 16 tokens, else 8
     int32_t min_tiles;
     uint32_t bt_inverse;
-    uint32_t q_sign;       // the sign of the softmax scale, applied to Q, so that larger products are larger scores
-    float scale;           // its magnitude, times log2(e)
+    float scale;           // softmax scale * log2(e), not zero
+    uint32_t unseen;       // what a product must be for a score of -infinity
     float *part;           // [CTAs][2][2] partial results
     int32_t *count;        // [CTAs][2]
 };
@@ -126,6 +126,10 @@ __device__ __forceinline__ uint4 ld_codes(const uint8_t *p)
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
     return v;
+}
+__device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t src_bytes)
+{
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(src_bytes) : "memory");
 }
 __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint32_t c, uint32_t d)
 {
@@ -622,30 +626,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             __syncwarp();
             if (lane == 0) mbar_arrive(bar);
         };
-        // The rows of a unit, 16 bytes per thread and step: chunk ct & 7 of row (ct >> 3) + 16 s.
+        // The rows of a unit by asynchronous copies of 16 bytes, zeros past the last: chunk ct & 7 of row
+        // (ct >> 3) + 16 s of each 64-channel block.
         auto load_rows = [&](const Desc &e) {
             const int qc = ct & 7;
             const int32_t nrows = e.nrows, steps = nrows > 128 ? 16 : 8;
-#pragma unroll 4
+            const __half *src0 = a.q + (int64_t)e.row0 * a.q_stride + (int64_t)e.head * a.group * D + qc * 8;
+#pragma unroll 2
             for (int s = 0; s < steps; ++s) {
                 const int row = (ct >> 3) + 16 * s;
                 const int32_t r = e.r0 + (row < nrows ? row : 0);
                 const int32_t tok = div_group(a, r);
-                const __half *src = a.q + (int64_t)(e.row0 + tok) * a.q_stride +
-                                    ((int64_t)e.head * a.group + (r - tok * a.group)) * D + qc * 8;
+                const __half *src = src0 + (int64_t)tok * a.q_stride + (r - tok * a.group) * D;
+                const uint32_t at = q_sm + (row >> 7) * Sh::kQTile + (row & 127) * 128 + ((qc ^ (row & 7)) << 4);
 #pragma unroll
-                for (int b = 0; b < NB; ++b) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (row < nrows) v = __ldg(reinterpret_cast<const uint4 *>(src + b * 64));
-                    sts128(q_sm + (row >> 7) * Sh::kQTile + b * (128 * 128) + (row & 127) * 128 + ((qc ^ (row & 7)) << 4),
-                           v.x ^ p.q_sign, v.y ^ p.q_sign, v.z ^ p.q_sign, v.w ^ p.q_sign);
-                }
+                for (int b = 0; b < NB; ++b) copy16(at + b * (128 * 128), src + b * 64, row < nrows ? 16u : 0u);
             }
-            done(&s_qfull);
+            cp_async_commit();
         };
         // Keys run a tile ahead of values: K_0, K_1, V_0, K_2, V_1, ..
         uint4 rk[NL], rv[NL];
         uint32_t qe_par = 1;
+        bool rows_under_way = false;
 #pragma unroll 1
         for (int32_t i = -1; i < total && !*abort; ++i) {
             const int32_t j = i + 1;
@@ -664,6 +666,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     load(desc[(j + 1) % kDescs], 0, rk);
                 }
             }
+            if (rows_under_way) {
+                cp_async_wait<0>();
+                done(&s_qfull);
+                rows_under_way = false;
+            }
             if (i >= 0) {
                 if (!wait_bar(&s_vempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
                 store(desc[i % kDescs], v_sm + (i & 1) * Sh::kKVTile, rv);
@@ -674,8 +681,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                 qe_par ^= 1;
                 load_rows(desc[j % kDescs]);
+                rows_under_way = true;
             }
         }
+        cp_async_wait<0>();
     } else if (warp < kConvWarp) {
         // ---- softmax: one row per thread -------------------------------------------------------
         const int t = warp >> 2;                               // row tile
@@ -690,10 +699,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             float top = -INFINITY;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                float m = __uint_as_float(x[8 * g]);
+                const float kx = d.ks[4 * h + g] * p.scale, lv = d.lv[4 * h + g];
 #pragma unroll
-                for (int k = 1; k < 8; ++k) m = fmaxf(m, __uint_as_float(x[8 * g + k]));
-                top = fmaxf(top, fmaf(m, d.ks[4 * h + g] * p.scale, d.lv[4 * h + g]));
+                for (int k = 0; k < 8; ++k) top = fmaxf(top, fmaf(__uint_as_float(x[8 * g + k]), kx, lv));
             }
             return top;
         };
@@ -732,7 +740,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
                             const bool see = (uint32_t)(32 * h + k - m0) < mn && (ok >> (4 * h + k / 8) & 1u);
-                            if (!see) x[k] = 0xFF800000u;
+                            if (!see) x[k] = p.unseen;
                         }
                         tc::st_32x32b_x32(ts + 32 * h, x);
                     }
@@ -1020,11 +1028,11 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, in
     p.box_rows = a.c.bt % 16 == 0 ? 16 : 8;
     p.min_tiles = 2;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
-    p.q_sign = a.scale_log2 < 0.f ? 0x80008000u : 0u;
-    // masked scores are -infinity times this, so it may not be zero: at 2^-60 no score of fp16
+    // unseen products are an infinity times this, so it may not be zero: at 2^-60 no score of fp16
     // queries and 8-bit codes differs from zero
-    p.scale = a.scale_log2 < 0.f ? -a.scale_log2 : a.scale_log2;
-    if (p.scale < 0x1p-60f) p.scale = 0x1p-60f;
+    p.scale = a.scale_log2;
+    if (p.scale < 0x1p-60f && p.scale > -0x1p-60f) p.scale = 0x1p-60f;
+    p.unseen = p.scale < 0.f ? 0x7F800000u : 0xFF800000u;
     p.part = static_cast<float *>(ws);
     p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
     cudaError_t e;
