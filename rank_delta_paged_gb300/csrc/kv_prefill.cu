@@ -731,15 +731,22 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 // The loops over a tile's columns stay rolled and what is rare stays out of them: the
                 // roles' code has to fit the instruction caches.
                 uint32_t x[32];
+                int hn = 4;                                    // some row of the warp sees keys 32 (hn - 1) .. + 31, none later ones
                 if (__builtin_expect(!plain, 0)) {
-                    // scores of unseen keys, in place
+                    // the scores of unseen keys, in place, where some rows see some of 32 keys
+                    const int32_t v0 = m0 < 0 ? 0 : m0, v1 = m0 + (int32_t)mn;
+                    const int32_t a1 = __reduce_max_sync(~0u, v0);
+                    const int32_t z0 = __reduce_min_sync(~0u, v1), z1 = __reduce_max_sync(~0u, v1);
+                    while (hn > 0 && (z1 <= 32 * hn - 32 || (ok >> (4 * hn - 4) & 15u) == 0)) --hn;
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
+                    for (int h = 0; h < hn; ++h) {
+                        const uint32_t okh = ok >> (4 * h) & 15u;
+                        if (a1 <= 32 * h && z0 >= 32 * h + 32 && okh == 15u) continue;
                         tc::ld_32x32b_x32(ts + 32 * h, x);
                         tc::ld_wait(x);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            const bool see = (uint32_t)(32 * h + k - m0) < mn && (ok >> (4 * h + k / 8) & 1u);
+                            const bool see = (uint32_t)(32 * h + k - m0) < mn && (okh >> (k / 8) & 1u);
                             if (!see) x[k] = p.unseen;
                         }
                         tc::st_32x32b_x32(ts + 32 * h, x);
@@ -750,7 +757,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     // rows that have seen nothing yet start from this tile's maximum
                     float top = -INFINITY;
 #pragma unroll 1
-                    for (int h = 0; h < 4; ++h) {
+                    for (int h = 0; h < hn; ++h) {
                         tc::ld_32x32b_x32(ts + 32 * h, x);
                         tc::ld_wait(x);
                         top = fmaxf(top, top_of(d, x, h));
@@ -788,7 +795,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 };
                 tc::ld_32x32b_x16(ts, xa);
 #pragma unroll 1
-                for (int h = 0; h < 4; ++h) {
+                for (int h = 0; h < hn; ++h) {
                     raw = add = 0.f;
                     tc::ld_wait(xa);
                     tc::ld_32x32b_x16(ts + 32 * h + 16, xb);
@@ -846,6 +853,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     tc::st_32x32b_x16(ts + 16 * h, pk);
                 }
                 tc::ld_wait(xa);
+                if (__builtin_expect(hn < 4, 0)) {
+#pragma unroll
+                    for (int k = 0; k < 16; ++k) pk[k] = 0;
+                    for (int h = hn; h < 4; ++h) tc::st_32x32b_x16(ts + 16 * h, pk);
+                }
                 any = true;
                 tc::st_wait();
                 tc::fence_before_sync();
