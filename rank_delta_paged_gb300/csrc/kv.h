@@ -193,9 +193,11 @@ __device__ __forceinline__ uint32_t encode2(float x, float y)
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(y), "f"(x));
         return r;
     }
-    const int a = x != x ? 0 : __float2int_rn(fminf(fmaxf(x, -127.f), 127.f));
-    const int b = y != y ? 0 : __float2int_rn(fminf(fmaxf(y, -127.f), 127.f));
-    return (uint32_t)(a & 255) | (uint32_t)(b & 255) << 8;
+    // the conversion saturates to -128 .. 127 and takes NaN to 0
+    int32_t a, b;
+    asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(a) : "f"(fmaxf(x, -127.f)));
+    asm("cvt.rni.sat.s8.f32 %0, %1;" : "=r"(b) : "f"(fmaxf(y, -127.f)));
+    return __byte_perm((uint32_t)(x != x ? 0 : a), (uint32_t)(y != y ? 0 : b), 0x7740) & 0xFFFFu;
 }
 
 // Four codes -> fp16 pairs (bytes 0, 1) and (bytes 2, 3); exact in both formats.

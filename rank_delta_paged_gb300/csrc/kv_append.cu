@@ -6,14 +6,19 @@
 //     code = round(x 2^-e)
 //
 // What bounds it: reading the fp16 keys, values and queries once and writing the codes and the
-// rotated queries once.  The scale of a block needs the largest value of all its new tokens
-// before the first code can be written, so a block's tokens stay in registers between the
-// two.  The work is cut by (block of the cache, run of its pages): a CTA finds its block by a binary
-// search of the token offsets, in which block `slot` of the batch is
-// counted as if every sequence before it had touched floor(tokens / block) + 2 blocks
-// (at least as many as it can), so no prefix sum over the sequences has to be made first.
-// Blocks with at most kFew new tokens (every decode token) go to groups of head_dim / 8 lanes,
-// one page each, with no barrier; fuller blocks to the whole CTA, page after page.
+// rotated queries once; for a few tokens, the chain of dependent reads (offsets, page ids and rows,
+// angles and exponents).  The scale of a block needs the largest value of all its new tokens
+// before the first code can be written, so a block's tokens stay in registers between the two.
+//
+// Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
+// values and queries alike; a row is a group of head_dim / 8 lanes, which holds two of them at a
+// time, and all of its reads that do not depend on others go first.
+// Other sequences (append_kernel): a CTA takes a run of one block's pages, page after page, with the next
+// page's rows under way; blocks with at most kFew new tokens go to groups of lanes, a page each,
+// which read their few rows twice.  It finds its block by a search of the token offsets, in which
+// block `slot` of the batch is counted as if every sequence before it had touched
+// floor(tokens / block) + 2 blocks (at least as many as it can), so no prefix sum over the
+// sequences has to be made first.  Their queries are a kernel of their own (rotate_kernel).
 #include "host_common.h"
 #include "internal.h"
 #include "kv.h"
@@ -24,17 +29,17 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kFew = 4;
+constexpr int kBlockThreads = 512;  // append_kernel: two rows of 64 per group of 16 lanes
+constexpr int kFew = 8;
 constexpr int kMaxUnits = 128;     // pages per CTA at most
 constexpr int kQHeads = 4;         // query heads per group and step
 
 struct Params {
     AppendArgs a;
-    int32_t slots;       // blocks of the cache, counted as above
-    int32_t per_seq;     // slots per sequence besides its tokens / block: 2, or 1 and no search if max_q is 1
+    int32_t slots;       // blocks of the cache, counted as above (single tokens: sequences)
     int32_t splits;      // CTAs per slot
     int32_t units;       // pages per CTA
-    int64_t kv_ctas;     // slots * splits; later CTAs rotate queries
+    int32_t q_rows;      // single tokens: query heads that go with the keys and values
 };
 
 struct Rot {
@@ -67,6 +72,9 @@ __device__ __forceinline__ void load_rot(const AppendArgs &a, int32_t pos, int c
             r.c[4 * i] = c.x, r.c[4 * i + 1] = c.y, r.c[4 * i + 2] = c.z, r.c[4 * i + 3] = c.w;
             r.s[4 * i] = s.x, r.s[4 * i + 1] = s.y, r.s[4 * i + 2] = s.z, r.s[4 * i + 3] = s.w;
         }
+        if (ch * 8 < half)      // a cos + b (-sin)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) r.s[i] = -r.s[i];
     }
 }
 
@@ -88,15 +96,11 @@ __device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch
         return;
     }
     const int m = a.rot / 16;            // chunks of half the rotated channels
-    const bool low = ch < m;
-    const int from = low ? ch + m : (ch < 2 * m ? ch - m : ch);
+    const int from = ch < m ? ch + m : (ch < 2 * m ? ch - m : ch);
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const float y = __shfl_sync(~0u, x[i], from, LPR);
-        if (r.on) {
-            const float p = __fmul_rn(x[i], r.c[i]), q = __fmul_rn(y, r.s[i]);
-            x[i] = low ? __fsub_rn(p, q) : __fadd_rn(p, q);
-        }
+        if (r.on) x[i] = __fadd_rn(__fmul_rn(x[i], r.c[i]), __fmul_rn(y, r.s[i]));
     }
 }
 
@@ -111,15 +115,25 @@ __device__ __forceinline__ void unpack(uint4 v, float (&x)[8])
     }
 }
 
+// The largest finite magnitude.
 __device__ __forceinline__ float size_of(const float (&x)[8])
 {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const uint32_t u = __float_as_uint(x[i]) & 0x7FFFFFFFu;
-        if (u < 0x7F800000u) m = fmaxf(m, __uint_as_float(u));
+    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));      // passes over NaN
+    if (__builtin_expect(m == INFINITY, 0)) {
+        m = 0.f;
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (fabsf(x[i]) < INFINITY) m = fmaxf(m, fabsf(x[i]));
     }
     return m;
+}
+
+// The largest of the lanes' values, none negative: their bit patterns are in the same order.
+__device__ __forceinline__ float max_of(unsigned lanes, float m)
+{
+    return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(m)));
 }
 
 template <int FMT>
@@ -154,150 +168,245 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
 }
 
 // A block's nt <= kFew new rows of the pages [u0, u1): one page per group of lanes and step.
-// The rows' loads do not need the pages and go first; for a single token the next step's are
-// under way while one is written.
+// The rows are read once for their largest value and again, from the caches, for the codes.
 template <int D, int FMT>
 __device__ __forceinline__ void few_rows(const AppendArgs &a, int32_t u0, int32_t u1, int32_t nt, int32_t held,
                                          int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp)
 {
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 8, GROUPS = kBlockThreads / LPR;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
-    auto row_of = [&](int32_t u, int i) {
-        const __half *src = u & 1 ? a.v : a.k;
-        const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
-        return *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + i) * stride + (int64_t)(u >> 1) * D + ch * 8);
-    };
-    const uint4 zero = make_uint4(0, 0, 0, 0);
-    uint4 next = u0 + grp < u1 ? row_of(u0 + grp, 0) : zero;
-    Rot rot0;
-    rot0.on = false;
-    load_rot(a, position(a, row0, from), ch, rot0);
-    __syncthreads();
+    const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
+#pragma unroll 1
     for (int32_t ub = u0; ub < u1; ub += GROUPS) {
         const int32_t u = ub + grp;
         const bool val = u & 1;
         const int32_t page = u < u1 ? s_page[u - u0] : -1;
-        uint4 raw[kFew];
-        raw[0] = next;
-#pragma unroll
-        for (int i = 1; i < kFew; ++i) raw[i] = i < nt && page >= 0 ? row_of(u, i) : zero;
-        next = u + GROUPS < u1 ? row_of(u + GROUPS, 0) : zero;
-        float x[kFew][8];
-        float m = 0.f;
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-            if (i >= nt) break;
-            unpack(raw[i], x[i]);
-            Rot r = rot0;
-            if (i > 0 && !val && page >= 0) load_rot(a, position(a, row0 + i, from + i), ch, r);
-            r.on = r.on && !val;
-            rotate<LPR>(a, r, ch, x[i]);
-            m = fmaxf(m, size_of(x[i]));
-        }
-#pragma unroll
-        for (int o = 1; o < LPR; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        if (page < 0) continue;
-        int e = fit_exponent<FMT>(m);
-        uint8_t *dst = a.c.pool + page * a.c.page_bytes;
-        if (held) {
-            const int old = s_exp[u - u0];
-            if (old >= e) {
-                e = old;
-            } else {
-                const float unit = pow2(old - e);
+        const __half *src = (val ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
+        const int64_t stride = val ? a.v_stride : a.k_stride;
+        auto row = [&](int32_t i, float (&x)[8]) {
+            uint4 raw = make_uint4(0, 0, 0, 0);
+            if (page >= 0) raw = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + i) * stride);
+            Rot r;
+            r.on = false;
+            if (page >= 0 && !val) load_rot(a, position(a, row0 + i, from + i), ch, r);
+            unpack(raw, x);
+            rotate<LPR>(a, r, ch, x);
+        };
+        float x[8], m = 0.f;
 #pragma unroll 1
-                for (int r = 0; r < held; ++r) {
-                    uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
-                    *w = rescale8<FMT>(*w, unit);
+        for (int32_t i = 0; i < nt; ++i) {
+            row(i, x);
+            m = fmaxf(m, size_of(x));
+        }
+        m = max_of(row_lanes, m);
+        int e = fit_exponent<FMT>(m);
+        uint8_t *dst = a.c.pool + (int64_t)page * a.c.page_bytes + ch * 8;
+        if (page >= 0) {
+            if (held) {
+                const int old = s_exp[u - u0];
+                if (old >= e) {
+                    e = old;
+                } else {
+                    const float unit = pow2(old - e);
+#pragma unroll 1
+                    for (int r = 0; r < held; ++r) {
+                        uint2 *w = reinterpret_cast<uint2 *>(dst + r * D);
+                        *w = rescale8<FMT>(*w, unit);
+                    }
                 }
             }
+            if (ch == 0) a.c.exps[page] = (int8_t)e;
         }
-        if (ch == 0) a.c.exps[page] = (int8_t)e;
         const float unit = pow2(-e);
-#pragma unroll
-        for (int i = 0; i < kFew; ++i) {
-            if (i >= nt) break;
-            *reinterpret_cast<uint2 *>(dst + (held + i) * D + ch * 8) = encode8<FMT>(x[i], unit);
+#pragma unroll 1
+        for (int32_t i = 0; i < nt; ++i) {
+            if (nt > 1) row(i, x);
+            if (page >= 0) *reinterpret_cast<uint2 *>(dst + (held + i) * D) = encode8<FMT>(x, unit);
         }
     }
 }
 
-template <int D, int FMT, int PASSES>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ Params p)
+// Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
+// have rows of one kind and those of values do not rotate.
+template <int D, int FMT>
+__global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_constant__ Params p)
 {
-    constexpr int LPR = D / 8;                 // lanes per row
-    constexpr int GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 8, GROUPS = kThreads / LPR, ILP = 2;
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
-    __shared__ float s_max[2][kThreads / 32];
-    __shared__ int32_t s_page[kMaxUnits];
-    __shared__ int8_t s_exp[kMaxUnits];
-
+    const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
     griddep_wait();
     griddep_launch_dependents();
-
-    if (blockIdx.x >= p.kv_ctas) {
-        // ---- queries: kQHeads heads of one token per group --------------------------------
-        const int32_t per = (a.n_q + kQHeads - 1) / kQHeads;
-        const int64_t total = (int64_t)a.b.T * per;
-        const int64_t step = (int64_t)(gridDim.x - p.kv_ctas) * GROUPS;
-        for (int64_t i0 = (blockIdx.x - p.kv_ctas) * GROUPS; i0 < total; i0 += step) {
-            const int64_t i = i0 + grp;
-            const bool live = i < total;
-            const int32_t t = live ? (int32_t)(i / per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
-            bool mine = live;
-            int32_t pos = 0;
-            if (a.positions) {
-                if (live) pos = a.positions[t];
-            } else {
-                int32_t lo = 0, hi = a.b.S - 1;      // last sequence that starts at or before t
-                while (lo < hi) {
-                    const int32_t mid = (lo + hi + 1) / 2;
-                    if (a.b.indptr[mid] <= t) lo = mid; else hi = mid - 1;
-                }
-                const int32_t end = a.b.indptr[lo + 1];
-                mine = live && a.b.indptr[lo] <= t && t < end;
-                if (mine) pos = a.b.kv_len[lo] - end + t;
+    const int32_t s = (int32_t)(blockIdx.x / (unsigned)p.splits), part = (int32_t)(blockIdx.x - (unsigned)s * p.splits);
+    const int32_t t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s];
+    int32_t bad = 0;
+    if (t0 < 0 || t1 < t0 || t1 > a.b.T || t1 - t0 > a.b.max_q)
+        bad = SLORA_DEV_BAD_SEGMENT;
+    else if (len < t1 - t0 || (int64_t)len > (int64_t)a.b.max_blocks * a.c.bt)
+        bad = SLORA_DEV_BAD_LENGTH;
+    if (bad) {
+        if (tid == 0) set_status(a.c.status, bad);
+        return;
+    }
+    if (t1 - t0 != 1) return;
+    const int32_t kv = 2 * a.c.n_kv, all = kv + p.q_rows;
+    const int32_t u0 = part * p.units, u1 = u0 + p.units < all ? u0 + p.units : all;
+    const int32_t blk = (len - 1) / a.c.bt, held = len - 1 - blk * a.c.bt;
+    const int32_t *table = a.b.table + ((int64_t)s * a.b.max_blocks + blk) * kv;
+    const int32_t pos = a.rot ? (a.positions ? a.positions[t0] : len - 1) : 0;
+    Rot rot;
+    rot.on = false;
+#pragma unroll 1
+    for (int32_t ub = u0; ub < u1; ub += ILP * GROUPS) {
+        uint4 raw[ILP];
+        int32_t page[ILP], old[ILP];
+#pragma unroll
+        for (int i = 0; i < ILP; ++i) {
+            const int32_t u = ub + i * GROUPS + grp;
+            raw[i] = make_uint4(0, 0, 0, 0);
+            page[i] = -1;
+            old[i] = kMinExponent;
+            if (u < u1) {
+                const bool val = u >= a.c.n_kv;
+                const int32_t h = val ? u - a.c.n_kv : u;
+                const __half *src = u >= kv ? a.q + t0 * a.q_stride + (int64_t)(u - kv) * D
+                                   : val    ? a.v + t0 * a.v_stride + (int64_t)h * D
+                                            : a.k + t0 * a.k_stride + (int64_t)h * D;
+                raw[i] = *reinterpret_cast<const uint4 *>(src + ch * 8);
+                if (u < kv) page[i] = table[2 * h + val];
             }
-            uint4 v[kQHeads];
+        }
+        if (ub == u0) load_rot(a, pos, ch, rot);
 #pragma unroll
-            for (int k = 0; k < kQHeads; ++k)
-                if (mine && h0 + k < a.n_q)
-                    v[k] = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D + ch * 8);
-            Rot r;
-            r.on = false;
-            if (mine) load_rot(a, pos, ch, r);
+        for (int i = 0; i < ILP; ++i) {
+            const int32_t u = ub + i * GROUPS + grp;
+            if (u < u1 && u < kv) {
+                if (page[i] < 0 || page[i] >= a.c.num_pages) {
+                    if (ch == 0) set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+                    page[i] = -1;
+                } else if (held && ch == 0) {
+                    old[i] = clamp_exponent(a.c.exps[page[i]]);    // by the lane that writes it
+                }
+            }
+        }
 #pragma unroll
-            for (int k = 0; k < kQHeads; ++k) {
-                float x[8];
-                if (!(mine && h0 + k < a.n_q)) v[k] = make_uint4(0, 0, 0, 0);
-                unpack(v[k], x);
+        for (int i = 0; i < ILP; ++i) {
+            const int32_t u = ub + i * GROUPS + grp;
+            float x[8];
+            unpack(raw[i], x);
+            const bool turns = u < a.c.n_kv || u >= kv;
+            if (__any_sync(~0u, turns)) {
+                Rot r = rot;
+                r.on = rot.on && turns;
                 rotate<LPR>(a, r, ch, x);
+            }
+            float m = size_of(x);
+            m = max_of(row_lanes, m);
+            const int was = __shfl_sync(~0u, old[i], 0, LPR);
+            if (u >= kv && u < u1) {
                 uint4 w;
                 __half2 *h = reinterpret_cast<__half2 *>(&w);
 #pragma unroll
                 for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-                if (mine && h0 + k < a.n_q)
-                    *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)(h0 + k) * D + ch * 8) = w;
+                *reinterpret_cast<uint4 *>(a.q_out + t0 * a.q_out_stride + (int64_t)(u - kv) * D + ch * 8) = w;
             }
+            if (page[i] < 0) continue;
+            const int fit = fit_exponent<FMT>(m), e = held && was > fit ? was : fit;
+            uint8_t *dst = a.c.pool + page[i] * a.c.page_bytes + ch * 8;
+            if (held && was < e) {
+                const float unit = pow2(was - e);
+#pragma unroll 1
+                for (int k = 0; k < held; ++k) {
+                    uint2 *w = reinterpret_cast<uint2 *>(dst + k * D);
+                    *w = rescale8<FMT>(*w, unit);
+                }
+            }
+            if (ch == 0) a.c.exps[page[i]] = (int8_t)e;
+            *reinterpret_cast<uint2 *>(dst + held * D) = encode8<FMT>(x, pow2(-e));
         }
-        return;
     }
+}
+
+// The queries of a batch: kQHeads heads of one token per group of lanes and step.
+template <int D>
+__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ Params p)
+{
+    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    const AppendArgs &a = p.a;
+    const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
+    // as append_kernel
+    griddep_launch_dependents();
+    const int32_t per = (a.n_q + kQHeads - 1) / kQHeads;
+    const int64_t total = (int64_t)a.b.T * per;
+    const int64_t step = (int64_t)gridDim.x * GROUPS;
+#pragma unroll 1
+    for (int64_t i0 = (int64_t)blockIdx.x * GROUPS; i0 < total; i0 += step) {
+        const int64_t i = i0 + grp;
+        const bool live = i < total;
+        const int32_t t = live ? (int32_t)(i / per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
+        bool mine = live;
+        int32_t pos = 0;
+        if (a.positions) {
+            if (live) pos = a.positions[t];
+        } else {
+            int32_t lo = 0, hi = a.b.S - 1;      // last sequence that starts at or before t
+            while (lo < hi) {
+                const int32_t mid = (lo + hi + 1) / 2;
+                if (a.b.indptr[mid] <= t) lo = mid; else hi = mid - 1;
+            }
+            const int32_t end = a.b.indptr[lo + 1];
+            mine = live && a.b.indptr[lo] <= t && t < end;
+            if (mine) pos = a.b.kv_len[lo] - end + t;
+        }
+        uint4 v[kQHeads];
+#pragma unroll
+        for (int k = 0; k < kQHeads; ++k)
+            if (mine && h0 + k < a.n_q)
+                v[k] = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D + ch * 8);
+        Rot r;
+        r.on = false;
+        if (mine) load_rot(a, pos, ch, r);
+#pragma unroll
+        for (int k = 0; k < kQHeads; ++k) {
+            float x[8];
+            if (!(mine && h0 + k < a.n_q)) v[k] = make_uint4(0, 0, 0, 0);
+            unpack(v[k], x);
+            rotate<LPR>(a, r, ch, x);
+            uint4 w;
+            __half2 *h = reinterpret_cast<__half2 *>(&w);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
+            if (mine && h0 + k < a.n_q)
+                *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)(h0 + k) * D + ch * 8) = w;
+        }
+    }
+    griddep_wait();
+}
+
+template <int D, int FMT, int PASSES>
+__device__ __forceinline__ void append_blocks(const Params &p)
+{
+    constexpr int LPR = D / 8;                 // lanes per row
+    constexpr int GROUPS = kBlockThreads / LPR;
+    const AppendArgs &a = p.a;
+    const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
+    __shared__ uint32_t s_max[3];
+    if (tid == 0) s_max[0] = 0;
+    __shared__ int32_t s_page[kMaxUnits];
+    __shared__ int8_t s_exp[kMaxUnits];
+
 
     // ---- keys and values of one block of the cache ------------------------------------------
     const int32_t slot = (int32_t)(blockIdx.x / p.splits), part = (int32_t)(blockIdx.x - (int64_t)slot * p.splits);
     const int32_t bt = a.c.bt;
-    int32_t lo = slot;
-    if (p.per_seq == 2) {
-        // last sequence whose slots start at or before this one, 32 at a time; every warp for itself
-        lo = 0;
-        for (int32_t n = a.b.S; n > 1;) {
-            const int32_t step = (n + 31) / 32, at = lo + (tid & 31) * step;
-            const bool le = at < lo + n && (int64_t)(a.b.indptr[at] / bt) + 2ll * at <= slot;
-            const int k = 31 - __clz(__ballot_sync(~0u, le) | 1u);
-            n = n - k * step < step ? n - k * step : step;
-            lo += k * step;
-        }
+    // last sequence whose slots start at or before this one, 32 at a time; every warp for itself
+    int32_t lo = 0;
+    for (int32_t n = a.b.S; n > 1;) {
+        const int32_t step = (n + 31) / 32, at = lo + (tid & 31) * step;
+        const bool le = at < lo + n && (int64_t)(a.b.indptr[at] / bt) + 2ll * at <= slot;
+        const int k = 31 - __clz(__ballot_sync(~0u, le) | 1u);
+        n = n - k * step < step ? n - k * step : step;
+        lo += k * step;
     }
     const int32_t s = lo, t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s];
     const int32_t n = t1 - t0;
@@ -310,9 +419,9 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         if (tid == 0) set_status(a.c.status, bad);
         return;
     }
-    if (n == 0) return;
+    if (n <= 1) return;                                           // one: append_one_kernel's
     const int32_t p0 = len - n;                                   // position of the first new token
-    const int64_t nth = p.per_seq == 2 ? slot - ((int64_t)(t0 / bt) + 2ll * s) : 0;    // nth touched block of the sequence
+    const int64_t nth = slot - ((int64_t)(t0 / bt) + 2ll * s);    // nth touched block of the sequence
     if (nth < 0 || p0 / bt + nth > (len - 1) / bt) return;
     const int32_t blk = p0 / bt + (int32_t)nth;
     const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
@@ -331,36 +440,44 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         s_exp[tid] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
     }
 
+    __syncthreads();
+    // unit: KV head * 2 + (0 keys, 1 values)
     if (nt <= kFew) {
-        // one page per group and step; unit: KV head * 2 + (0 keys, 1 values)
         few_rows<D, FMT>(a, u0, u1, nt, held, row0, from, s_page, s_exp);
         return;
     }
-    __syncthreads();
 
-    int turn = 0;        // s_max alternates, so one barrier per page is enough
-    for (int32_t u = u0; u < u1; ++u) {
-        const int32_t head = u >> 1;
-        const bool val = u & 1;
-        const int32_t page = s_page[u - u0];
-        if (page < 0) continue;             // the whole CTA
-        const __half *src = (val ? a.v : a.k) + (int64_t)head * D + ch * 8;
-        const int64_t stride = val ? a.v_stride : a.k_stride;
-        const int old = s_exp[u - u0];
-        uint4 raw[PASSES];
+    int turn = 0;
+    uint4 raw[PASSES];
+    auto read = [&](int32_t u) {
+        const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
+        const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int r = i * GROUPS + grp;
             raw[i] = make_uint4(0, 0, 0, 0);
             if (r < nt) raw[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + r) * stride);
         }
+    };
+    read(u0);
+#pragma unroll 1
+    for (int32_t u = u0; u < u1; ++u) {
+        const bool val = u & 1;
+        const int32_t page = s_page[u - u0];
+        const int old = s_exp[u - u0];
         float x[PASSES][8];
         float m = 0.f;
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             if (i * GROUPS >= nt) break;
-            const int r = i * GROUPS + grp;
             unpack(raw[i], x[i]);
+        }
+        if (u + 1 < u1) read(u + 1);
+        if (page < 0) continue;             // the whole CTA
+#pragma unroll
+        for (int i = 0; i < PASSES; ++i) {
+            if (i * GROUPS >= nt) break;
+            const int r = i * GROUPS + grp;
             if (!val) {
                 Rot rt;
                 rt.on = false;
@@ -369,13 +486,13 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
             }
             m = fmaxf(m, size_of(x[i]));
         }
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-        float *sm = s_max[turn ^= 1];
-        if ((tid & 31) == 0) sm[tid >> 5] = m;
+        // the page's maximum, by turns in three words: one is added to, one read, one cleared
+        m = max_of(~0u, m);
+        if ((tid & 31) == 0) atomicMax(&s_max[turn], __float_as_uint(m));
+        if (tid == 0) s_max[turn == 2 ? 0 : turn + 1] = 0;
         __syncthreads();
-#pragma unroll
-        for (int i = 0; i < kThreads / 32; ++i) m = fmaxf(m, sm[i]);
+        m = __uint_as_float(s_max[turn]);
+        turn = turn == 2 ? 0 : turn + 1;
         int e = fit_exponent<FMT>(m);
         uint8_t *dst = a.c.pool + page * a.c.page_bytes;
         if (held) {
@@ -400,60 +517,89 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
 }
 
-template <int D>
-cudaError_t launch_d(const Params &p, int fmt, unsigned grid, cudaStream_t stream)
+template <int D, int FMT, int PASSES>
+__global__ void __launch_bounds__(kBlockThreads, PASSES <= 3 ? 2 : 1) append_kernel(const __grid_constant__ Params p)
 {
+    // append_one_kernel, the one before, has waited for what came before it, and nothing here depends on
+    // its results; the kernel after this one waits for what this one has waited for
+    griddep_launch_dependents();
+    append_blocks<D, FMT, PASSES>(p);
+    griddep_wait();
+}
+
+template <class... Args>
+cudaError_t start(void (*kernel)(Args...), const Params &p, int64_t ctas, cudaStream_t stream, int threads = kThreads)
+{
+    if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(grid);
-    cfg.blockDim = dim3(kThreads);
+    cfg.gridDim = dim3((unsigned)ctas);
+    cfg.blockDim = dim3(threads);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // rows of a block over the CTA's groups: the registers for 4, 5 or 8 of them per lane (a
-    // page of up to 8192, 10240 or 16384 bytes)
-    const int passes = (p.a.c.bt + kThreads / (D / 8) - 1) / (kThreads / (D / 8));
-    auto go = [&](auto e4m3, auto int8) {
-        return cudaLaunchKernelEx(&cfg, fmt == SLORA_KV_E4M3 ? e4m3 : int8, p);
-    };
-    if (passes <= 4) return go(append_kernel<D, SLORA_KV_E4M3, 4>, append_kernel<D, SLORA_KV_INT8, 4>);
-    if (passes <= 5) return go(append_kernel<D, SLORA_KV_E4M3, 5>, append_kernel<D, SLORA_KV_INT8, 5>);
-    return go(append_kernel<D, SLORA_KV_E4M3, 8>, append_kernel<D, SLORA_KV_INT8, 8>);
+    return cudaLaunchKernelEx(&cfg, kernel, p);
+}
+
+template <int D>
+cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *launches)
+{
+    constexpr int groups = kThreads / (D / 8);
+    const AppendArgs &a = p.a;
+    const bool e4m3 = fmt == SLORA_KV_E4M3;
+    cudaError_t e;
+    {
+        // two rows per group of lanes and CTA
+        p.q_rows = a.b.max_q == 1 ? a.n_q : 0;
+        const int32_t all = 2 * a.c.n_kv + p.q_rows;
+        p.slots = a.b.S;
+        p.splits = (all + 2 * groups - 1) / (2 * groups);
+        p.units = (all + p.splits - 1) / p.splits;
+        e = start(e4m3 ? append_one_kernel<D, SLORA_KV_E4M3> : append_one_kernel<D, SLORA_KV_INT8>, p,
+                  (int64_t)p.slots * p.splits, stream);
+        *launches += e == cudaSuccess;
+        if (e != cudaSuccess || a.b.max_q == 1) return e;
+    }
+    // A block's pages over several CTAs where the batch has few blocks; runs of at least four
+    // pages otherwise, so that a page's reads go under the page before.
+    const int32_t all = 2 * a.c.n_kv;
+    p.slots = a.b.T / a.c.bt + 2 * a.b.S;
+    int64_t splits = (8ll * num_sms + p.slots - 1) / p.slots;
+    if (splits > all) splits = all;
+    if (splits * kMaxUnits < all) splits = (all + kMaxUnits - 1) / kMaxUnits;
+    p.units = (int32_t)((all + splits - 1) / splits);
+    p.splits = (all + p.units - 1) / p.units;
+    const int64_t ctas = (int64_t)p.slots * p.splits;
+    // rows of a block over the CTA's groups: the registers for 2, 3 or 4 of them per lane (a
+    // page of up to 8192, 12288 or 16384 bytes)
+    constexpr int block_groups = kBlockThreads / (D / 8);
+    const int passes = (a.c.bt + block_groups - 1) / block_groups;
+    if (passes <= 2)
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 2> : append_kernel<D, SLORA_KV_INT8, 2>, p, ctas, stream, kBlockThreads);
+    else if (passes <= 3)
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 3> : append_kernel<D, SLORA_KV_INT8, 3>, p, ctas, stream, kBlockThreads);
+    else
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 4> : append_kernel<D, SLORA_KV_INT8, 4>, p, ctas, stream, kBlockThreads);
+    *launches += e == cudaSuccess;
+    if (e != cudaSuccess || !a.q) return e;
+    const int64_t items = (int64_t)a.b.T * ((a.n_q + kQHeads - 1) / kQHeads);
+    int64_t q_ctas = (items + groups - 1) / groups;
+    if (q_ctas > 32ll * num_sms) q_ctas = 32ll * num_sms;
+    e = start(rotate_kernel<D>, p, q_ctas, stream);
+    *launches += e == cudaSuccess;
+    return e;
 }
 
 }  // namespace
 
 cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream, int *launches)
 {
-    Params p;
+    Params p = {};
     p.a = a;
-    const int groups = kThreads / (head_dim / 8);
-    const int32_t all = 2 * a.c.n_kv;
-    p.per_seq = a.b.max_q == 1 ? 1 : 2;
-    p.slots = p.per_seq == 1 ? a.b.S : a.b.T / a.c.bt + 2 * a.b.S;
-    // Pages of one slot over several CTAs where the batch has few slots; a CTA's groups need
-    // a page each when the blocks gain a token or so each.
-    const int64_t want = 8ll * num_sms;
-    int64_t splits = (want + p.slots - 1) / p.slots;
-    const int64_t most = a.b.max_q <= kFew ? (all + groups - 1) / groups : all;
-    if (splits > most) splits = most;
-    if (splits * kMaxUnits < all) splits = (all + kMaxUnits - 1) / kMaxUnits;
-    p.units = (int32_t)((all + splits - 1) / splits);
-    p.splits = (all + p.units - 1) / p.units;
-    p.kv_ctas = (int64_t)p.slots * p.splits;
-    int64_t q_ctas = 0;
-    if (a.q) {
-        const int64_t items = (int64_t)a.b.T * ((a.n_q + kQHeads - 1) / kQHeads);
-        q_ctas = (items + groups - 1) / groups;
-        if (q_ctas > 16ll * num_sms) q_ctas = 16ll * num_sms;
-    }
-    if (p.kv_ctas + q_ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
-    const unsigned grid = (unsigned)(p.kv_ctas + q_ctas);
-    cudaError_t e = head_dim == 128 ? launch_d<128>(p, fmt, grid, stream) : launch_d<64>(p, fmt, grid, stream);
-    if (e == cudaSuccess) ++*launches;
-    return e;
+    return head_dim == 128 ? launch_d<128>(p, fmt, num_sms, stream, launches)
+                           : launch_d<64>(p, fmt, num_sms, stream, launches);
 }
 
 }  // namespace kv
