@@ -108,6 +108,7 @@ __device__ __forceinline__ int32_t div_group(const AttendArgs &a, int32_t r)
 // 64-bit quotients are long code; none is on a path that matters.
 static __device__ __noinline__ int32_t div_list(int64_t x, int64_t y)
 {
+    if (((uint64_t)x | (uint64_t)y) >> 32 == 0) return (int32_t)((uint32_t)x / (uint32_t)y);
     return (int32_t)(x / y);
 }
 

@@ -45,7 +45,7 @@ constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxCtas = 3;                      // per SM, of any shape
 constexpr int kSeqChunks = 64;                  // partial sums of the tile counts
 constexpr int kMaxRows = 16;
-constexpr int kDescs = 32;                      // descriptors: 5 batches of 4 being prepared, 3 in use
+constexpr int kDescs = 32;                      // descriptors: 4 batches of 4 being prepared, 4 in use
 constexpr int kPartStride = 2 * kMaxRows + kMaxRows * 128;   // floats of one partial result: m, l, O
 
 struct Meta {
@@ -163,6 +163,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     __shared__ uint64_t s_full[NS], s_empty[NS], s_merge[3];
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ int s_abort, s_last;
+    __shared__ float s_row[2][kMaxRows];
 
     const AttendArgs &a = p.a;
     int32_t *status = a.c.status;
@@ -185,9 +186,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     // than a launch.
     const int S = a.b.S;
     const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
+    const int chunks = (S + per - 1) / per;
+    if (tid >= chunks && tid < kSeqChunks) s_sum[tid] = 0;
     int32_t bad = 0;
 #pragma unroll 1
-    for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
+    for (int c = warp; c < chunks; c += kThreads / 32) {
         int64_t t = 0;
 #pragma unroll 1
         for (int64_t s = (int64_t)c * per + lane; s < S && s < (int64_t)(c + 1) * per; s += 32) {
@@ -317,11 +320,12 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         struct Box {
             bool want;                  // whether any row of the sequence needs it
             int32_t page, row;          // its page and first row there
+            int32_t e;                  // and its exponent
         };
         int64_t ahead = w0;             // first tile of the list not yet described
         bool broken = false;
         // Batch of descriptors that the next call fills.  It was last used by the batch 8 (16 for
-        // R = 8) earlier, 4 (12) batches before the one being copied, whose tiles the consumers
+        // R = 8) earlier, 4 (12) batches before the last one copied, whose tiles the consumers
         // have left: the last copy waited for the tile NS before it.
         int slot = 0;
         // The tiles of the next batch: everything but pages and scales goes to the ring at once.
@@ -403,12 +407,35 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             ahead += count;
             return count;
         };
-        auto exponent_of = [&](Box &m) {
+        // The batch's page ids are there: into the descriptors with them, and on to the exponents.
+        auto settle = [&](Box &m, int n, int at) {
             if (m.want && (m.page < 0 || m.page >= a.c.num_pages)) {
                 set_status(status, SLORA_DEV_BAD_PAGE);
                 m.want = false;
             }
-            return m.want ? (int32_t)a.c.exps[m.page] : 0;
+            // a box needs both its keys and its values: bits 2 gl of `have`
+            unsigned have = __ballot_sync(~0u, m.want);
+            have &= have >> 1 & 0x55555555u;
+            if (lanes < 32) have = have >> (my_tile * lanes) & ((1u << lanes) - 1u);
+            m.want = have >> (2 * gl) & 1u;
+            m.e = m.want ? (int32_t)a.c.exps[m.page] : 0;
+            // bits 2 g spread over the 8-token groups of Meta.ok
+            uint32_t ok;
+            if (R == 16)
+                ok = (have & 1u) * 3u | (have >> 2 & 1u) * 12u | (have >> 4 & 1u) * 48u | (have >> 6 & 1u) * 192u;
+            else
+                ok = (have & 1u) | (have >> 1 & 2u) | (have >> 2 & 4u) | (have >> 3 & 8u) | (have >> 4 & 16u) |
+                     (have >> 5 & 32u) | (have >> 6 & 64u) | (have >> 7 & 128u);
+            if (my_tile < n) {
+                Meta *ms = &meta[(at << batch_log) + my_tile];
+                ms->page[kvl][gl] = m.page;
+                if (kvl == 0) ms->row[gl] = m.row;
+                if (lane % lanes == 0) {
+                    ms->ok = ok;
+                    if (ok != 0xFFu) ms->plain = 0;
+                }
+            }
+            __syncwarp();
         };
         // One lane: the copies of a tile.
         auto copy_tile = [&](const Meta &m, int st) {
@@ -424,7 +451,6 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 const int4 row = *reinterpret_cast<const int4 *>(m.row);
                 const int4 kp = *reinterpret_cast<const int4 *>(m.page[0]);
                 const int4 vp = *reinterpret_cast<const int4 *>(m.page[1]);
-                mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
                 if (ok == 0xFFu && row.y && row.z && row.w) {
                     copy(0, 2, row.x, kp.x, vp.x);
                 } else {
@@ -442,46 +468,38 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     }
                 }
             } else {
-                mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
 #pragma unroll 1
                 for (int x = 0; x < 8; ++x)
                     if (ok >> x & 1u) copy(x, 0, m.row[x], m.page[0][x], m.page[1][x]);
             }
         };
-        // Two batches lie between the reading of a batch's page ids and of its exponents, and two more
-        // between those and their use: under load either read takes a microsecond or two.
-        const Box none = {false, 0, 0};
-        Box b0 = none, b1 = none, b2 = none, b3 = none, b4;
-        int n0 = 0, n1 = 0, n2 = 0, n3 = 0, n4;
-        int32_t e0 = 0, e1 = 0, e2;
+        // Two batches lie between the reading of a batch's page ids and of its exponents, and one more
+        // between those and their use: under load either read takes a microsecond or two.  The first
+        // tiles' copies start as soon as their pages are known, and the first batch waits for nothing else.
+        const Box none = {false, 0, 0, 0};
+        Box b0 = none, b1 = none, b2 = none, b3;
+        int n0 = 0, n1 = 0, n2 = 0, n3;
         int batch = 0, stage = 0;
         uint32_t parity = 1;
         int32_t issued = 0;
+        int early = 0;
 #pragma unroll 1
-        for (int step = 0;;
-             ++step, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
-            e2 = exponent_of(b2);
-            n4 = describe(b4);
-            if (step < 4) continue;
+        for (int step = 0;; ++step, b0 = b1, b1 = b2, b2 = b3, n0 = n1, n1 = n2, n2 = n3) {
+            n3 = describe(b3);
+            if (step == 0) {
+                settle(b3, n3, 0);
+                early = n3 < NS ? n3 : NS;
+                if (lane == 0)
+#pragma unroll 1
+                    for (int t = 0; t < early; ++t) copy_tile(meta[t], t);
+            }
+            if (step < 3) continue;
             if (n0 == 0 || *abort) break;
-            // a box needs both its keys and its values: bits 2 gl of `have`
-            unsigned have = __ballot_sync(~0u, b0.want);
-            have &= have >> 1 & 0x55555555u;
-            if (lanes < 32) have = have >> (my_tile * lanes) & ((1u << lanes) - 1u);
-            const bool both = have >> (2 * gl) & 1u;
-            // bits 2 g spread over the 8-token groups of Meta.ok
-            uint32_t ok;
-            if (R == 16)
-                ok = (have & 1u) * 3u | (have >> 2 & 1u) * 12u | (have >> 4 & 1u) * 48u | (have >> 6 & 1u) * 192u;
-            else
-                ok = (have & 1u) | (have >> 1 & 2u) | (have >> 2 & 4u) | (have >> 3 & 8u) | (have >> 4 & 16u) |
-                     (have >> 5 & 32u) | (have >> 6 & 64u) | (have >> 7 & 128u);
+            if (step > 3) settle(b1, n1, (step - 2) % n_batches);
             if (my_tile < n0) {
-                const int e = both ? clamp_exponent(e0) : 0;
+                const int e = b0.want ? clamp_exponent(b0.e) : 0;
                 const float ef = (float)e, up = pow2(e), down = pow2(-e);
                 Meta *ms = &meta[(batch << batch_log) + my_tile];
-                ms->page[kvl][gl] = b0.page;
-                if (kvl == 0) ms->row[gl] = b0.row;
                 if (R == 16) {
                     if (kvl == 0) {
                         *reinterpret_cast<float2 *>(&ms->ks[2 * gl]) = make_float2(up, up);
@@ -497,22 +515,23 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                         ms->li[gl] = down;
                     }
                 }
-                if (lane % lanes == 0) {
-                    ms->ok = ok;
-                    if (ok != 0xFFu) ms->plain = 0;
-                }
             }
             __syncwarp();
 #pragma unroll 1
             for (int t = 0; t < n0; ++t, ++issued) {
                 if (!wait_bar(&s_empty[stage], parity, abort, status)) break;
-                if (lane == 0) copy_tile(meta[(batch << batch_log) + t], stage);
+                if (lane == 0) {
+                    const Meta &m = meta[(batch << batch_log) + t];
+                    mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(m.ok) * 16u * D);
+                    if (issued >= early) copy_tile(m, stage);
+                }
                 if (++stage == NS) {
                     stage = 0;
                     parity ^= 1;
                 }
             }
             if (++batch == n_batches) batch = 0;
+            if (step == 3) settle(b1, n1, 1);
         }
         // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
         volatile int gone = 0;
@@ -815,24 +834,44 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (!wait_bar(&s_merge[2], jparity, abort, status)) break;
             jparity ^= 1;
             if (s_last) {
+                auto slot = [&](int k) { return p.part + (size_t)(2 * k + (k == c0 ? 1 : 0)) * kPartStride; };
+                // each row's maximum and sum by eight lanes
+                const int r8 = tid >> 3, j8 = tid & 7;
+                float M = -INFINITY, L = 0.f;
+                if (r8 < live)
+#pragma unroll 4
+                    for (int k = c0 + j8; k <= c1; k += 8) M = fmaxf(M, __ldcg(slot(k) + r8));
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) M = fmaxf(M, __shfl_xor_sync(~0u, M, o));
+                const float B = M == -INFINITY ? 0.f : M;
+                if (r8 < live)
+#pragma unroll 4
+                    for (int k = c0 + j8; k <= c1; k += 8)
+                        L = fmaf(__ldcg(slot(k) + kMaxRows + r8), ex2(__ldcg(slot(k) + r8) - B), L);
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1) L += __shfl_xor_sync(~0u, L, o);
+                if (j8 == 0) {
+                    s_row[0][r8] = M;
+                    s_row[1][r8] = L;
+                }
+                if (!meet(1)) break;
 #pragma unroll 1
-                for (int i = tid; i < live * (D / 2); i += 32 * kConsumers) {
-                    const int r = i / (D / 2), d = (i - r * (D / 2)) * 2;
-                    auto slot = [&](int k) { return p.part + (size_t)(2 * k + (k == c0 ? 1 : 0)) * kPartStride; };
-                    float M = -INFINITY;
-                    for (int k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + r));
-                    const float B = M == -INFINITY ? 0.f : M;
-                    float L = 0.f;
-                    float2 v = make_float2(0.f, 0.f);
+                for (int i = tid; i < live * (D / 4); i += 32 * kConsumers) {
+                    const int r = i / (D / 4), d = (i - r * (D / 4)) * 4;
+                    const float Mr = s_row[0][r], Lr = s_row[1][r], Br = Mr == -INFINITY ? 0.f : Mr;
+                    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
                     for (int k = c0; k <= c1; ++k) {
                         const float *sl = slot(k);
-                        const float e = ex2(__ldcg(sl + r) - B);
-                        const float2 x = __ldcg(reinterpret_cast<const float2 *>(sl + 2 * kMaxRows + r * D + d));
-                        L += __ldcg(sl + kMaxRows + r) * e;
+                        const float e = ex2(__ldcg(sl + r) - Br);
+                        const float4 x = __ldcg(reinterpret_cast<const float4 *>(sl + 2 * kMaxRows + r * D + d));
                         v.x = fmaf(x.x, e, v.x);
                         v.y = fmaf(x.y, e, v.y);
+                        v.z = fmaf(x.z, e, v.z);
+                        v.w = fmaf(x.w, e, v.w);
                     }
-                    emit(r, d, v, M, L);
+                    emit(r, d, make_float2(v.x, v.y), Mr, Lr);
+                    emit(r, d + 2, make_float2(v.z, v.w), Mr, Lr);
                 }
             }
         } else if (!meet(1)) {

@@ -223,9 +223,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     // Tiles of each run of `per` sequences; every CTA sums them for itself.
     const int S = a.b.S;
     const int per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32;
+    const int chunks = (S + per - 1) / per;
+    if (tid >= chunks && tid < kSeqChunks) s_sum[tid] = 0;
     int32_t bad = 0;
 #pragma unroll 1
-    for (int c = warp; c < kSeqChunks; c += kThreads / 32) {
+    for (int c = warp; c < chunks; c += kThreads / 32) {
         int64_t t = 0;
 #pragma unroll 1
         for (int64_t s = (int64_t)c * per; s < S && s < (int64_t)(c + 1) * per; s += 32) {
