@@ -935,7 +935,10 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
     p.a = a;
     p.box_rows = a.c.bt % 16 == 0 ? 16 : 8;
     p.small_rows = small_rows;
-    p.rows = (int64_t)a.b.max_q * a.group <= 8 ? 8 : 16;
+    // Rows per unit by the batch's most common kind: every sequence's, or, where longer ones are the
+    // other kernel's, the single tokens' (16 prompt-free rows beside prompts cost 1.4 times 8).
+    const int64_t most = (int64_t)a.b.max_q * a.group;
+    p.rows = (most <= small_rows ? most : a.group) <= 8 ? 8 : 16;
     p.min_tiles = 2;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.part = static_cast<float *>(ws);

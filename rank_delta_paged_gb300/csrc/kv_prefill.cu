@@ -72,7 +72,9 @@ struct Shape {
     static constexpr int kBlocks = D / 64;                   // 64-channel blocks of 128-byte rows
     static constexpr int kQTile = 128 * D * 2;
     static constexpr int kKVTile = kTile * D * 2;
-    static constexpr size_t kSmem = 1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + kDescs * sizeof(Desc);
+    static constexpr int kStage = 32 * 64;                   // a warp's 32 rows of 32 channels on their way out
+    static constexpr size_t kSmem =
+        1024 + 2 * (size_t)kQTile + 4 * (size_t)kKVTile + 8 * (size_t)kStage + kDescs * sizeof(Desc);
     static constexpr int kPart = 2 * 128 + 128 * D;          // floats of a row tile's partial result: m, l, O
 };
 
@@ -125,6 +127,12 @@ __device__ __forceinline__ uint4 ld_codes(const uint8_t *p)
     asm volatile("ld.global.nc.L1::no_allocate.L2::128B.v4.b32 {%0,%1,%2,%3}, [%4];"
                  : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w)
                  : "l"(p));
+    return v;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t ad)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(ad));
     return v;
 }
 __device__ __forceinline__ void copy16(uint32_t dst, const void *src, uint32_t src_bytes)
@@ -183,7 +191,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     extern __shared__ uint8_t smem_raw[];
     const uint32_t q_sm = (smem_u32(smem_raw) + 1023) & ~1023u;      // two row tiles
     const uint32_t k_sm = q_sm + 2 * Sh::kQTile, v_sm = k_sm + 2 * Sh::kKVTile;
-    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (v_sm + 2 * Sh::kKVTile - smem_u32(smem_raw)));
+    const uint32_t stage_sm = v_sm + 2 * Sh::kKVTile;
+    Desc *desc = reinterpret_cast<Desc *>(smem_raw + (stage_sm + 8 * Sh::kStage - smem_u32(smem_raw)));
     __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin;
     __shared__ int64_t s_sum[kSeqChunks];
@@ -866,7 +875,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&s_pfull[t]);
             }
-            const int32_t row0 = d.row0, head = d.head, r = d.r0 + 128 * t + row, c0 = d.c0, c1 = d.c1;
+            const int32_t row0 = d.row0, head = d.head, r = d.r0 + 128 * t + row, rend = d.r0 + d.nrows, c0 = d.c0, c1 = d.c1;
             const bool live = 128 * t + row < d.nrows;
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
@@ -878,32 +887,20 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 od_par ^= 1;
                 tc::fence_after_sync();
             }
-            const int32_t tok = div_group(a, r);
-            const int64_t qh = (int64_t)head * a.group + (r - tok * a.group);
-            __half *out = a.out + (int64_t)(row0 + tok) * a.out_stride + qh * D;
-            auto put_lse = [&](float M, float L) {
-                if (a.lse)
-                    a.lse[(int64_t)(row0 + tok) * a.n_q + qh] = L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
-            };
-            auto put = [&](int h, const float (&o)[32], float inv) {       // 32 channels
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint4 v;
-                    __half2 *hh = reinterpret_cast<__half2 *>(&v);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) hh[k] = __floats2half2_rn(o[8 * j + 2 * k] * inv, o[8 * j + 2 * k + 1] * inv);
-                    *reinterpret_cast<uint4 *>(out + 32 * h + 8 * j) = v;
-                }
-            };
-            float o[32];
+            const bool whole = f & kWhole;
+            float M = mx, L = sum, B = 0.f, o[32];
+            // a part of a unit: m and l of each row, and O by fours of channels, rows side by side
+            auto slot = [&](int32_t k) { return p.part + ((size_t)(2 * k + (k == c0 ? 1 : 0)) * 2 + t) * Sh::kPart; };
             auto own = [&](int h) {
-                uint32_t x[32];
+                uint32_t y[32];
+#pragma unroll
+                for (int j = 0; j < 32; ++j) y[j] = 0;
                 if (any) {                                     // uniform over the warp
-                    tc::ld_32x32b_x32(to + 32 * h, x);
-                    tc::ld_wait(x);
+                    tc::ld_32x32b_x32(to + 32 * h, y);
+                    tc::ld_wait(y);
                 }
 #pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = any ? __uint_as_float(x[j]) : 0.f;
+                for (int j = 0; j < 32; ++j) o[j] = __uint_as_float(y[j]);
             };
             auto release = [&]() {
                 if (any) {
@@ -912,79 +909,105 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (lane == 0) mbar_arrive(&s_ofree[t]);
                 }
             };
-            if (f & kWhole) {
-                const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            if (!whole) {
+                float *mine = slot((int32_t)blockIdx.x);
+                __stcg(mine + row, mx);
+                __stcg(mine + 128 + row, sum);
+                if (any) {
 #pragma unroll 1
-                for (int h = 0; h < D / 32; ++h) {
-                    own(h);
-                    if (live) put(h, o, inv);
-                }
-                release();
-                if (live) put_lse(mx, sum);
-                continue;
-            }
-            // a part of a unit: m and l of each row, and O by fours of channels, rows side by side
-            auto slot = [&](int32_t k) { return p.part + ((size_t)(2 * k + (k == c0 ? 1 : 0)) * 2 + t) * Sh::kPart; };
-            float *mine = slot((int32_t)blockIdx.x);
-            __stcg(mine + row, mx);
-            __stcg(mine + 128 + row, sum);
-            if (any) {
-#pragma unroll 1
-                for (int h = 0; h < D / 32; ++h) {
-                    own(h);
+                    for (int h = 0; h < D / 32; ++h) {
+                        own(h);
 #pragma unroll
-                    for (int j = 0; j < 8; ++j)
-                        __stcg(reinterpret_cast<float4 *>(mine + 256) + (8 * h + j) * 128 + row,
-                               make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
-                }
-            }
-            release();
-            __threadfence();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&s_join[t]);
-            if (!wait_bar(&s_join[t], j_par, abort, status)) break;
-            if (row == 0) {
-                __threadfence();
-                int32_t *cnt = p.count + 2 * c0 + t;
-                const int l = atomicAdd(cnt, 1) == c1 - c0;
-                if (l) *cnt = 0;
-                s_last[t] = l;
-                __threadfence();
-                mbar_arrive(&s_said[t]);
-            }
-            if (!wait_bar(&s_said[t], j_par, abort, status)) break;
-            j_par ^= 1;
-            if (!s_last[t] || !live) continue;
-            float M = -INFINITY;
-#pragma unroll 1
-            for (int32_t k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + row));
-            const float B = M == -INFINITY ? 0.f : M;
-            float L = 0.f;
-#pragma unroll 1
-            for (int32_t k = c0; k <= c1; ++k) L += __ldcg(slot(k) + 128 + row) * ex2(__ldcg(slot(k) + row) - B);
-            const float inv = L == 0.f ? 0.f : 1.f / L;
-#pragma unroll 1
-            for (int h = 0; h < D / 32; ++h) {
-#pragma unroll
-                for (int j = 0; j < 32; ++j) o[j] = 0.f;
-#pragma unroll 1
-                for (int32_t k = c0; k <= c1; ++k) {
-                    const float *s = slot(k);
-                    const float m = __ldcg(s + row);
-                    if (m == -INFINITY) continue;              // nothing seen there: its O was not written
-                    const float e = ex2(m - B);
-#pragma unroll
-                    for (int j = 0; j < 8; ++j) {
-                        const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + 256) + (8 * h + j) * 128 + row);
-                        o[4 * j] = fmaf(v.x, e, o[4 * j]);
-                        o[4 * j + 1] = fmaf(v.y, e, o[4 * j + 1]);
-                        o[4 * j + 2] = fmaf(v.z, e, o[4 * j + 2]);
-                        o[4 * j + 3] = fmaf(v.w, e, o[4 * j + 3]);
+                        for (int j = 0; j < 8; ++j)
+                            __stcg(reinterpret_cast<float4 *>(mine + 256) + (8 * h + j) * 128 + row,
+                                   make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]));
                     }
                 }
-                put(h, o, inv);
+                release();
+                __threadfence();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&s_join[t]);
+                if (!wait_bar(&s_join[t], j_par, abort, status)) break;
+                if (row == 0) {
+                    __threadfence();
+                    int32_t *cnt = p.count + 2 * c0 + t;
+                    const int l = atomicAdd(cnt, 1) == c1 - c0;
+                    if (l) *cnt = 0;
+                    s_last[t] = l;
+                    __threadfence();
+                    mbar_arrive(&s_said[t]);
+                }
+                if (!wait_bar(&s_said[t], j_par, abort, status)) break;
+                j_par ^= 1;
+                if (!s_last[t]) continue;
+                M = -INFINITY;
+                L = 0.f;
+#pragma unroll 1
+                for (int32_t k = c0; k <= c1; ++k) M = fmaxf(M, __ldcg(slot(k) + row));
+                B = M == -INFINITY ? 0.f : M;
+#pragma unroll 1
+                for (int32_t k = c0; k <= c1; ++k) L += __ldcg(slot(k) + 128 + row) * ex2(__ldcg(slot(k) + row) - B);
             }
-            put_lse(M, L);
+            const float inv = L == 0.f ? 0.f : 1.f / L;
+            // The rows' outputs, turned in shared memory 32 channels at a time so that four lanes
+            // write 64 bytes of a row: this lane's rows, then, are (lane >> 2) + 8 j of the warp's.
+            const uint32_t turn = stage_sm + warp * Sh::kStage;
+            auto place = [&](int32_t rr) {
+                const int32_t tk = div_group(a, rr);
+                return (int64_t)(row0 + tk) * a.out_stride + ((int64_t)head * a.group + (rr - tk * a.group)) * D;
+            };
+            const int32_t rw = r - lane + (lane >> 2);
+            int64_t at[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) at[j] = place(rw + 8 * j);
+#pragma unroll 1
+            for (int h = 0; h < D / 32; ++h) {
+                if (whole) {
+                    own(h);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) o[j] = 0.f;
+#pragma unroll 1
+                    for (int32_t k = c0; k <= c1; ++k) {
+                        const float *s = slot(k);
+                        const float m = __ldcg(s + row);
+                        if (m == -INFINITY) continue;          // nothing seen there: its O was not written
+                        const float e = ex2(m - B);
+#pragma unroll
+                        for (int j = 0; j < 8; ++j) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(s + 256) + (8 * h + j) * 128 + row);
+                            o[4 * j] = fmaf(v.x, e, o[4 * j]);
+                            o[4 * j + 1] = fmaf(v.y, e, o[4 * j + 1]);
+                            o[4 * j + 2] = fmaf(v.z, e, o[4 * j + 2]);
+                            o[4 * j + 3] = fmaf(v.w, e, o[4 * j + 3]);
+                        }
+                    }
+                }
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const __half2 hh = __floats2half2_rn(o[8 * j + 2 * k] * inv, o[8 * j + 2 * k + 1] * inv);
+                        w[k] = *reinterpret_cast<const uint32_t *>(&hh);
+                    }
+                    sts128(turn + lane * 64 + ((j ^ (lane >> 1 & 3)) << 4), w[0], w[1], w[2], w[3]);
+                }
+                __syncwarp();
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int y = (lane >> 2) + 8 * j, c = lane & 3;
+                    const uint4 v = lds128(turn + y * 64 + ((c ^ (y >> 1 & 3)) << 4));
+                    if (rw + 8 * j < rend) *reinterpret_cast<uint4 *>(a.out + at[j] + 32 * h + 8 * c) = v;
+                }
+                __syncwarp();
+            }
+            if (whole) release();
+            if (live && a.lse) {
+                const int32_t tok = div_group(a, r);
+                a.lse[(int64_t)(row0 + tok) * a.n_q + (int64_t)head * a.group + (r - tok * a.group)] =
+                    L == 0.f ? -INFINITY : (M + log2f(L)) * 0.6931471805599453f;
+            }
         }
     }
     tc::fence_before_sync();
