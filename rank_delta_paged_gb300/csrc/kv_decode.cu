@@ -43,6 +43,9 @@ constexpr int kTile = 64;                       // tokens per tile
 constexpr int kConsumers = 4;                   // warps, 16 tokens of a tile each
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxCtas = 3;                      // per SM, of any shape
+// What a unit costs besides its tiles, in tiles: starting and joining its four warps' results.  With
+// runs of equal tiles alone, the CTAs of a ragged 13B decode batch took 250 to 620 us.
+constexpr int kUnitCost = 2;
 constexpr int kSeqChunks = 64;                  // partial sums of the tile counts
 constexpr int kMaxRows = 16;
 constexpr int kDescs = 32;                      // descriptors: 4 batches of 4 being prepared, 4 in use
@@ -196,7 +199,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         for (int64_t s = (int64_t)c * per + lane; s < S && s < (int64_t)(c + 1) * per; s += 32) {
             int32_t tiles, groups, first;
             seq_tiles(p, load_seq(a, (int32_t)s, &bad), &tiles, &groups, &first);
-            t += (int64_t)tiles * groups;
+            t += (int64_t)(tiles + kUnitCost) * groups;
         }
 #pragma unroll
         for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
@@ -204,7 +207,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
     if (bad && blockIdx.x == 0) set_status(status, bad);
     __syncthreads();
-    // This CTA's run [w0, w1) of the W tiles.
+    // This CTA's run [w0, w1) of the list's W places: a unit's tiles, then kUnitCost empty ones.
     int64_t v0 = s_sum[2 * lane], v1 = s_sum[2 * lane + 1], W = v0 + v1;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
@@ -216,7 +219,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     int64_t run = div_list(W + gridDim.x - 1, gridDim.x);
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
-    if (w0 >= w1) return;
+    if (w0 >= W - kUnitCost) return;
     volatile int *abort = &s_abort;
     const int R = p.box_rows;                  // rows of a tile that share a page
     const int batch_log = R == 16 ? 2 : 1;     // tiles per batch of descriptors
@@ -257,7 +260,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
                 return;
             }
-            int64_t mine = (int64_t)tiles * groups * a.c.n_kv, sum = mine;
+            int64_t mine = (int64_t)(tiles + kUnitCost) * groups * a.c.n_kv, sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
                 const int64_t u = __shfl_up_sync(~0u, sum, o);
@@ -275,9 +278,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         int32_t u_tiles = __shfl_sync(~0u, tiles, at_lane), u_groups = __shfl_sync(~0u, groups, at_lane);
         int32_t u_first = __shfl_sync(~0u, first, at_lane);
         int64_t in_seq = w0 - base;
-        int32_t head = div_list(in_seq, (int64_t)u_tiles * u_groups);
-        in_seq -= (int64_t)head * u_tiles * u_groups;
-        int32_t grp = div_list(in_seq, u_tiles), tile = (int32_t)(in_seq - (int64_t)grp * u_tiles);
+        int32_t head = div_list(in_seq, (int64_t)(u_tiles + kUnitCost) * u_groups);
+        in_seq -= (int64_t)head * (u_tiles + kUnitCost) * u_groups;
+        int32_t grp = div_list(in_seq, u_tiles + kUnitCost), tile = (int32_t)(in_seq - (int64_t)grp * (u_tiles + kUnitCost));
         Seq u;
         u.row0 = __shfl_sync(~0u, q.row0, at_lane);
         u.n = __shfl_sync(~0u, q.n, at_lane);
@@ -322,8 +325,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             int32_t page, row;          // its page and first row there
             int32_t e;                  // and its exponent
         };
-        int64_t ahead = w0;             // first tile of the list not yet described
-        bool broken = false;
+        int64_t ahead = w0;             // place of `tile` in the list, the first not yet described
+        bool begun = false;
         // Batch of descriptors that the next call fills.  It was last used by the batch 8 (16 for
         // R = 8) earlier, 4 (12) batches before the last one copied, whose tiles the consumers
         // have left: the last copy waited for the tile NS before it.
@@ -333,11 +336,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             m.want = false;
             m.page = 0;
             m.row = 0;
-            int32_t count = w1 - ahead < per_batch ? (int32_t)(w1 - ahead) : per_batch;
-            if (broken || count <= 0) return 0;
             Meta *ms = &meta[(slot << batch_log) + my_tile];
-            if (++slot == n_batches) slot = 0;
-            auto fill = [&](int32_t t, bool first, bool last) {    // this lane's tile is t of the unit
+            // this lane's tile is t of the unit, at `at` in the list
+            auto fill = [&](int32_t t, int64_t at, bool first) {
                 const int32_t j0 = (u_first + t) * kTile, j = j0 + gl * R;
                 m.want = j < un.hi && j + R > un.lo;
                 if (m.want) {
@@ -351,33 +352,31 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
                 if (lane % lanes == 0) {
                     int4 *mi = reinterpret_cast<int4 *>(&ms->plain);
+                    const bool end = t == u_tiles - 1, last = end || at == w1 - 1;
+                    const bool run_end = at + 1 + (end ? kUnitCost : 0) >= w1;
                     mi[0] = make_int4(j0 >= un.plain_lo && j0 + kTile <= un.plain_hi, first || t == 0,
-                                      last || t == u_tiles - 1, un.whole);
+                                      (last ? 1 : 0) | (run_end ? 2 : 0), un.whole);
                     mi[1] = make_int4(j0, u.row0, u.n, u.len);
                     mi[2] = make_int4(head, un.r0, un.c0, un.c1);
                 }
             };
-            if (!fresh && tile + per_batch < u_tiles && count == per_batch) {     // all within the unit, not at its end
-                fill(tile + my_tile, my_tile == 0 && ahead == w0, ahead + my_tile == w1 - 1);
+            int count = 0;
+            if (!fresh && tile + per_batch < u_tiles && ahead + per_batch < w1) {     // all within the unit
+                fill(tile + my_tile, ahead + my_tile, !begun && my_tile == 0);
                 tile += per_batch;
                 ahead += per_batch;
-                return count;
-            }
+                count = per_batch;
+            } else {
 #pragma unroll 1
-            for (int b = 0; b < count; ++b) {
-                if (fresh) {
-                    enter(ahead + b);
-                    fresh = false;
-                }
-                if (b == my_tile) fill(tile, b == 0 && ahead == w0, ahead + b == w1 - 1);
-                // step to the next tile
-                if (++tile == u_tiles) {
-                    tile = 0;
-                    if (++grp == u_groups) {
-                        grp = 0;
-                        if (++head == a.c.n_kv) {
-                            head = 0;
-                            if (ahead + b + 1 < w1) {
+                for (; count < per_batch; ++count) {
+                    if (tile >= u_tiles) {
+                        // the next unit
+                        ahead += u_tiles + kUnitCost - tile;
+                        if (ahead >= w1) break;
+                        if (++grp == u_groups) {
+                            grp = 0;
+                            if (++head == a.c.n_kv) {
+                                head = 0;
                                 unsigned next;
 #pragma unroll 1
                                 while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
@@ -387,8 +386,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                                 }
                                 if (next == 0) {      // the lengths changed under the call
                                     if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
-                                    broken = true;
-                                    count = b + 1;
+                                    ahead = w1;
                                     break;
                                 }
                                 at_lane = __ffs(next) - 1;
@@ -400,11 +398,22 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                                 u.len = __shfl_sync(~0u, q.len, at_lane);
                             }
                         }
+                        tile = 0;
+                        fresh = true;
                     }
-                    fresh = true;
+                    if (ahead >= w1) break;
+                    if (fresh) {
+                        enter(ahead);
+                        fresh = false;
+                    }
+                    if (count == my_tile) fill(tile, ahead, !begun && count == 0);
+                    ++tile;
+                    ++ahead;
                 }
             }
-            ahead += count;
+            if (count == 0) return 0;
+            begun = true;
+            if (++slot == n_batches) slot = 0;
             return count;
         };
         // The batch's page ids are there: into the descriptors with them, and on to the exponents.
@@ -543,7 +552,6 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         return;
     }
 
-    const int32_t total = (int32_t)(w1 - w0);
     // ---- consumers ---------------------------------------------------------------------
     const int g = lane >> 2, c = lane & 3;
     const int krow[2] = {token_of_row<D>(g), token_of_row<D>(g) + 8};
@@ -584,11 +592,13 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             }
         }
     };
-    for (int32_t it = 0; it < total; ++it) {
+    bool more = true;
+    for (int32_t it = 0; more; ++it) {
         if (!wait_bar(&s_full[stage], parity, abort, status)) break;
         const Meta &m = meta[it % kDescs];
         const int4 flags = *reinterpret_cast<const int4 *>(&m.plain);
-        const bool plain = flags.x != 0, last = flags.z != 0, whole = flags.w != 0;
+        const bool plain = flags.x != 0, last = flags.z & 1, whole = flags.w != 0;
+        more = (flags.z & 2) == 0;
         const uint32_t kbase = my_ring + stage * Sh::kStage;
         const uint32_t vbase = kbase + Sh::kHalf;
         const int32_t nrows = m.n * a.group - m.r0;       // rows of this unit
@@ -639,7 +649,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             }
         }
         // the next unit's rows, while this one's last tile is finished
-        if (last && it + 1 < total) {
+        if (last && more) {
             const bool wrap = stage + 1 == NS;
             if (!wait_bar(&s_full[wrap ? 0 : stage + 1], parity ^ (wrap ? 1u : 0u), abort, status)) break;
             load_q(meta[(it + 1) % kDescs]);
@@ -939,7 +949,7 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
     // other kernel's, the single tokens' (16 prompt-free rows beside prompts cost 1.4 times 8).
     const int64_t most = (int64_t)a.b.max_q * a.group;
     p.rows = (most <= small_rows ? most : a.group) <= 8 ? 8 : 16;
-    p.min_tiles = 2;
+    p.min_tiles = 1 + kUnitCost;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.part = static_cast<float *>(ws);
     p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kMaxCtas * 2 * kPartStride);
