@@ -41,6 +41,8 @@ constexpr int kTile = 128;                // keys per tile
 constexpr int kRows = 256;                // rows per unit
 constexpr int kThreads = 480;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kMmaWarp1 = 14;
+// What a unit costs besides its tiles, in tiles: its rows' loads, the first tile's maxima, the outputs.
+constexpr int kUnitCost = 3;
 constexpr int kSeqChunks = 64;
 constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
 
@@ -48,7 +50,8 @@ enum : uint32_t {
     kFirst = 1, kLast = 2, kWhole = 4, kPlain = 8,
     kAct = 16,          // << t: row tile t sees keys of this tile
     kFirstAct = 64,     // << t: the first such tile of the unit in this CTA
-    kLastAct = 256      // << t: the last
+    kLastAct = 256,     // << t: the last
+    kEnd = 1024         // the CTA's last tile
 };
 
 struct Desc {
@@ -176,11 +179,12 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, in
         }
     }
 }
+// Its places in the list: the tiles, then kUnitCost empty ones.
 __device__ __forceinline__ int32_t unit_count(const AttendArgs &a, const Seq &q, int32_t rows, int32_t rt)
 {
     const int32_t r0 = rt * kRows, r1 = rows < r0 + kRows ? rows : r0 + kRows;
     const int32_t lo = first_key(a, q, div_group(a, r0)) / kTile, hi = (end_key(a, q, div_group(a, r1 - 1)) + kTile - 1) / kTile;
-    return hi > lo ? hi - lo : 1;
+    return (hi > lo ? hi - lo : 1) + kUnitCost;
 }
 
 template <int D, int FMT>
@@ -274,8 +278,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     int64_t run = div_list(W + gridDim.x - 1, gridDim.x);
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
-    if (w0 >= w1) return;
-    const int32_t total = (int32_t)(w1 - w0);
+    if (w0 >= W - kUnitCost) return;
     volatile int *abort = &s_abort;
 
     if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, 512);
@@ -382,7 +385,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 c0 = div_list(u0, run);
                 c1 = div_list(u1 - 1, run);
             }
-            ta = u0 >= w0 ? ut.lo : ut.lo + (int32_t)(w0 - u0);
+            ta = u0 >= w0 ? ut.lo : w0 - u0 < ut.hi - ut.lo ? ut.lo + (int32_t)(w0 - u0) : ut.hi;
             tb = u1 <= w1 ? ut.hi : ut.hi - (int32_t)(u1 - w1);
             tile = ta;
             plain_lo = first_key(a, u, div_group(a, r1 - 1));
@@ -404,11 +407,26 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         auto describe = [&](Box &x) {
             x.want = false;
             x.page = x.row = 0;
-            if (!more) return false;
-            if (fresh) {
-                enter(u0);
+            while (more && (fresh || tile >= tb)) {
+                if (!fresh) {
+                    u0 += ut.hi - ut.lo + kUnitCost;
+                    if (u0 >= w1) {
+                        more = false;
+                        break;
+                    }
+                    if ((int64_t)(++rt) * kRows >= rows) {
+                        rt = 0;
+                        if (++head == a.c.n_kv && !next_seq()) {      // the lengths changed under the call
+                            if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
+                            more = false;
+                            break;
+                        }
+                    }
+                }
+                enter(u0);          // (nothing of it is left if w0 is among its empty places)
                 fresh = false;
             }
+            if (!more) return false;
             if (!wait_bar(&s_tempty[slot], slot_parity, abort, status)) return false;
             Desc &d = desc[slot];
             if (++slot == kDescs) {
@@ -428,6 +446,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             if (lane == 0) {
                 uint32_t f = (tile == ta ? kFirst : 0) | (tile == tb - 1 ? kLast : 0) | (whole ? kWhole : 0);
+                if (tile == tb - 1 && (tb < ut.hi || u0 + ut.hi - ut.lo + kUnitCost >= w1)) f |= kEnd;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
                     const int32_t b = ut.b[t] > ta ? ut.b[t] : ta, e = ut.e[t] < tb ? ut.e[t] : tb;
@@ -440,21 +459,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 di[1] = make_int4(u.row0, u.n, u.len, head);
                 di[2] = make_int4(r0, r1 - r0, c0, c1);
             }
-            if (++tile == tb) {
-                u0 += ut.hi - ut.lo;
-                if (u0 >= w1) {
-                    more = false;
-                } else {
-                    if ((int64_t)(++rt) * kRows >= rows) {
-                        rt = 0;
-                        if (++head == a.c.n_kv && !next_seq()) {      // the lengths changed under the call
-                            if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
-                            more = false;
-                        }
-                    }
-                    fresh = true;
-                }
-            }
+            ++tile;
             return true;
         };
         auto exponent_of = [&](Box &x) {
@@ -528,10 +533,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         // warp: products of both at once would end together, and the two softmaxes would run
         // side by side instead of each under the other's products.
 #pragma unroll 1
-        for (int32_t i = -1; i < total; ++i) {
+        for (int32_t i = -1;; ++i) {
             const int32_t j = i + 1;
+            const bool more = (f & kEnd) == 0;
             uint32_t g = 0;
-            if (j < total) {
+            if (more) {
                 if (!wait(&s_tfull[j % kDescs], (uint32_t)(j / kDescs) & 1u)) break;
                 g = __shfl_sync(~0u, desc[j % kDescs].flags, 0);
                 if (!wait(&s_kfull[j & 1], (uint32_t)(j >> 1) & 1u)) break;
@@ -558,14 +564,14 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
                     if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
                 }
-                if (j < total && !fresh && (g & (kAct << t))) scores(j);
+                if (more && !fresh && (g & (kAct << t))) scores(j);
                 if (leader) {
                     mbar_arrive(&s_turn[t ^ 1u]);
                     tc::commit(&s_vempty[i & 1]);
                     mbar_arrive(&s_tempty[i % kDescs]);
                 }
             }
-            if (j == total) break;
+            if (!more) break;
             if (fresh) {
                 if (!wait(&s_qfull, q_par)) break;
                 q_par ^= 1;
@@ -659,8 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         uint4 rk[NL], rv[NL];
         uint32_t qe_par = 1;
         bool rows_under_way = false;
+        bool more = true;                                      // there is a tile i + 1
 #pragma unroll 1
-        for (int32_t i = -1; i < total && !*abort; ++i) {
+        for (int32_t i = -1; !*abort; ++i) {
             const int32_t j = i + 1;
             if (i < 0) {
                 if (!wait_bar(&s_tfull[0], 0, abort, status)) break;
@@ -668,11 +675,13 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             } else {
                 load(desc[i % kDescs], 1, rv);
             }
-            if (j < total) {
+            bool after = false;                                // and a tile i + 2
+            if (more) {
                 if (!wait_bar(&s_kempty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, status)) break;
                 store(desc[j % kDescs], k_sm + (j & 1) * Sh::kKVTile, rk);
                 done(&s_kfull[j & 1]);
-                if (j + 1 < total) {
+                after = (desc[j % kDescs].flags & kEnd) == 0;
+                if (after) {
                     if (!wait_bar(&s_tfull[(j + 1) % kDescs], (uint32_t)((j + 1) / kDescs) & 1u, abort, status)) break;
                     load(desc[(j + 1) % kDescs], 0, rk);
                 }
@@ -688,7 +697,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 done(&s_vfull[i & 1]);
                 if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
             }
-            if (j < total && __builtin_expect(desc[j % kDescs].flags & kFirst, 0)) {
+            if (!more) break;
+            more = after;
+            if (__builtin_expect(desc[j % kDescs].flags & kFirst, 0)) {
                 if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                 qe_par ^= 1;
                 load_rows(desc[j % kDescs]);
@@ -717,10 +728,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             return top;
         };
         int32_t klo = 0, khi = 0;                              // keys that the row sees
-        for (int32_t i = 0; i < total; ++i) {
+        uint32_t f = 0;
+        for (int32_t i = 0; (f & kEnd) == 0; ++i) {
             if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
             const Desc &d = desc[i % kDescs];
-            const uint32_t f = d.flags;
+            f = d.flags;
             if (f & kFirst) {
                 mx = -INFINITY;
                 sum = 0.f;
@@ -1063,7 +1075,7 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, in
     p.a = a;
     p.small_rows = small_rows;
     p.box_rows = a.c.bt % 16 == 0 ? 16 : 8;
-    p.min_tiles = 2;
+    p.min_tiles = 1 + kUnitCost;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     // unseen products are an infinity times this, so it may not be zero: at 2^-60 no score of fp16
     // queries and 8-bit codes differs from zero
