@@ -661,49 +661,56 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             cp_async_commit();
         };
-        // Keys run a tile ahead of values: K_0, K_1, V_0, K_2, V_1, ..
-        uint4 rk[NL], rv[NL];
+        // Keys run a tile ahead of values: K_0, K_1, V_0, K_2, V_1, ..  One loop for both, with the next half
+        // tile's codes on their way in rb, keeps the code short; the moves at its end cost less than a second copy.
+        uint4 ra[NL], rb[NL];
         uint32_t qe_par = 1;
         bool rows_under_way = false;
-        bool more = true;                                      // there is a tile i + 1
+        int32_t i = 0, last = 0x7FFFFFFF;                      // the tile, and the last of the run once known
+        int kv = 0;
+        if (wait_bar(&s_tfull[0], 0, abort, status)) {
+            load(desc[0], 0, ra);
 #pragma unroll 1
-        for (int32_t i = -1; !*abort; ++i) {
-            const int32_t j = i + 1;
-            if (i < 0) {
-                if (!wait_bar(&s_tfull[0], 0, abort, status)) break;
-                load(desc[0], 0, rk);
-            } else {
-                load(desc[i % kDescs], 1, rv);
-            }
-            bool after = false;                                // and a tile i + 2
-            if (more) {
-                if (!wait_bar(&s_kempty[j & 1], ((uint32_t)(j >> 1) & 1u) ^ 1u, abort, status)) break;
-                store(desc[j % kDescs], k_sm + (j & 1) * Sh::kKVTile, rk);
-                done(&s_kfull[j & 1]);
-                after = (desc[j % kDescs].flags & kEnd) == 0;
-                if (after) {
-                    if (!wait_bar(&s_tfull[(j + 1) % kDescs], (uint32_t)((j + 1) / kDescs) & 1u, abort, status)) break;
-                    load(desc[(j + 1) % kDescs], 0, rk);
+            for (;;) {
+                const Desc &d = desc[i % kDescs];
+                if (kv == 0 && (d.flags & kEnd)) last = i;
+                // the half tile after this one
+                int nk = 1;
+                int32_t ni = i - 1;
+                if (kv == 1) {
+                    nk = i + 2 <= last ? 0 : 1;
+                    ni = i + 2 <= last ? i + 2 : i + 1;
+                } else if (i == 0) {
+                    nk = last > 0 ? 0 : 1;
+                    ni = last > 0 ? 1 : 0;
                 }
-            }
-            if (rows_under_way) {
-                cp_async_wait<0>();
-                done(&s_qfull);
-                rows_under_way = false;
-            }
-            if (i >= 0) {
-                if (!wait_bar(&s_vempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
-                store(desc[i % kDescs], v_sm + (i & 1) * Sh::kKVTile, rv);
-                done(&s_vfull[i & 1]);
-                if (lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
-            }
-            if (!more) break;
-            more = after;
-            if (__builtin_expect(desc[j % kDescs].flags & kFirst, 0)) {
-                if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
-                qe_par ^= 1;
-                load_rows(desc[j % kDescs]);
-                rows_under_way = true;
+                const bool more = ni <= last;
+                if (more) {
+                    if (nk == 0 && !wait_bar(&s_tfull[ni % kDescs], (uint32_t)(ni / kDescs) & 1u, abort, status)) break;
+                    load(desc[ni % kDescs], nk, rb);
+                }
+                if (!wait_bar(kv ? &s_vempty[i & 1] : &s_kempty[i & 1], ((uint32_t)(i >> 1) & 1u) ^ 1u, abort, status)) break;
+                store(d, (kv ? v_sm : k_sm) + (i & 1) * Sh::kKVTile, ra);
+                done(kv ? &s_vfull[i & 1] : &s_kfull[i & 1]);
+                if (__builtin_expect(rows_under_way, 0)) {
+                    cp_async_wait<0>();
+                    done(&s_qfull);
+                    rows_under_way = false;
+                }
+                if (kv && lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
+                // the rows of a unit that starts with the next tile
+                const int32_t u = kv ? i + 1 : 0;
+                if ((kv || i == 0) && u <= last && __builtin_expect(desc[u % kDescs].flags & kFirst, 0)) {
+                    if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
+                    qe_par ^= 1;
+                    load_rows(desc[u % kDescs]);
+                    rows_under_way = true;
+                }
+                if (!more) break;
+#pragma unroll
+                for (int x = 0; x < NL; ++x) ra[x] = rb[x];
+                kv = nk;
+                i = ni;
             }
         }
         cp_async_wait<0>();
