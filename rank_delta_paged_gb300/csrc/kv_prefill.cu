@@ -388,6 +388,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             ta = u0 >= w0 ? ut.lo : w0 - u0 < ut.hi - ut.lo ? ut.lo + (int32_t)(w0 - u0) : ut.hi;
             tb = u1 <= w1 ? ut.hi : ut.hi - (int32_t)(u1 - w1);
             tile = ta;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (ut.b[t] < ta) ut.b[t] = ta;
+                if (ut.e[t] > tb) ut.e[t] = tb;
+            }
             plain_lo = first_key(a, u, div_group(a, r1 - 1));
             plain_hi = end_key(a, u, div_group(a, r0));
             table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
@@ -395,7 +400,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         int64_t u0 = base;
         bool more = found;
         bool fresh = true;                              // the unit has yet to be entered
-        const int gl = lane >> 1, kvl = lane & 1;       // this lane's 8 tokens of a tile, and keys or values
+        const int gl = lane & 15, kvl = lane >> 4;      // this lane's 8 tokens of a tile, and keys or values
         const int R = p.box_rows;                       // tokens that share a page: 16, or 8
         struct Box {
             bool want;
@@ -449,9 +454,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (tile == tb - 1 && (tb < ut.hi || u0 + ut.hi - ut.lo + kUnitCost >= w1)) f |= kEnd;
 #pragma unroll
                 for (int t = 0; t < 2; ++t) {
-                    const int32_t b = ut.b[t] > ta ? ut.b[t] : ta, e = ut.e[t] < tb ? ut.e[t] : tb;
-                    if (tile >= b && tile < e)
-                        f |= (kAct << t) | (tile == b ? kFirstAct << t : 0) | (tile == e - 1 ? kLastAct << t : 0);
+                    if (tile >= ut.b[t] && tile < ut.e[t])
+                        f |= (kAct << t) | (tile == ut.b[t] ? kFirstAct << t : 0) | (tile == ut.e[t] - 1 ? kLastAct << t : 0);
                 }
                 if (j0 >= plain_lo && j0 + kTile <= plain_hi) f |= kPlain;
                 int4 *di = reinterpret_cast<int4 *>(&d.flags);
@@ -483,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             if (i < 0) continue;
             if (!n0 || *abort) break;
             Desc &d = desc[i % kDescs];
-            unsigned have = __ballot_sync(~0u, b0.want);
-            have &= have >> 1 & 0x55555555u;               // a group needs both its keys and its values
-            const bool both = have >> (2 * gl) & 1u;
+            // a group needs both its keys and its values
+            const unsigned have = __ballot_sync(~0u, b0.want), ok = have & have >> 16 & 0xFFFFu;
+            const bool both = ok >> gl & 1u;
             const int e = both ? clamp_exponent(e0) : 0;
             d.off[kvl][gl] = both ? (int64_t)b0.page * a.c.page_bytes + (b0.row + (8 * gl & (R - 1))) * D : 0;
             if (kvl == 0) {
@@ -494,12 +498,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 d.lv[gl] = (float)e;
                 d.li[gl] = pow2(-e);
             }
-            const unsigned ok = __ballot_sync(~0u, both && kvl == 0);      // bit 2g
             if (lane == 0) {
-                uint32_t o = 0;
-                for (int k = 0; k < 16; ++k) o |= (ok >> (2 * k) & 1u) << k;
-                d.ok = o;
-                if (o != 0xFFFFu) d.flags &= ~kPlain;
+                d.ok = ok;
+                if (ok != 0xFFFFu) d.flags &= ~kPlain;
             }
             __syncwarp();
             if (lane == 0) mbar_arrive(&s_tfull[i % kDescs]);
@@ -560,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (act && leader) {
                     const uint64_t d = dv + (uint32_t)((i & 1) * (Sh::kKVTile >> 4));
                     tc::mma_f16_ts(o, w, d, id_o, !first);
-#pragma unroll
+#pragma unroll 1
                     for (int kk = 1; kk < kTile / 16; ++kk) tc::mma_f16_ts(o, w + kk * 8, d + kk * (2048 >> 4), id_o, 1);
                     if (f & (kLastAct << t)) tc::commit(&s_odone[t]);
                 }
