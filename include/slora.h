@@ -475,10 +475,12 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * slora_kv_create(): the cache of one layer's (or any) KV heads over `pool`'s pages.
  *   n_kv_heads  1 .. 1024;  head_dim  64 or 128 (a page must hold 8 rows of it)
  *   format      SLORA_KV_E4M3 or SLORA_KV_INT8
- *   Allocates num_pages bytes for the exponents (set to 0) and the attention's workspace.  The pages stay
- *   the pool's: the caller takes and returns them, and may use several caches over one pool
- *   (each with exponents of its own).  Destroy a pool's caches before the pool;
- *   slora_kv_destroy waits for the device, and NULL is a no-op.
+ *   Allocates num_pages bytes for the exponents (set to 0) and, with a pool's first cache,
+ *   the attention's workspace (about 48 MB on 152 SMs), which is the pool's and shared by
+ *   all its caches.  The pages stay the pool's: the caller takes and returns them.  One
+ *   cache can serve several layers, each with pages of its own in a block table of its own;
+ *   a pool may also have several caches, each with its own exponents.  Destroy a pool's
+ *   caches before the pool; slora_kv_destroy waits for the device, and NULL is a no-op.
  * slora_kv_block_tokens(), slora_kv_exponents(): block_tokens, and the device address of the
  *   exponents (for saving, moving or filling pages; a page's bytes are at slora_pool_base).
  *
@@ -496,17 +498,20 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *                positions kv_len[s] - n .. kv_len[s] - 1 of the cache
  *   block_table  device int32 [S][max_blocks][n_kv_heads][2]: the pages of the keys (0) and
  *                the values (1) of each block and head.  Entries of blocks that a call does not
- *                touch are not read (they may be -1).  Sequences may share pages that
- *                are only read.
+ *                touch are not read (they may be -1).  Sequences may share pages that are
+ *                only read.
+ * Tokens of rows outside every sequence, and of a sequence that is skipped, are not computed:
+ * their rows of q_out, out and lse are unspecified.
  *
- * slora_kv_append(): writes the new tokens' keys and values to the cache, rotating queries and keys by their
- * positions on the way.  Scales: a block's exponent is the smallest e >= -40 for which every
- * finite |value| of its new tokens is at most 448 * 2^e (127 * 2^e for INT8); if the block
- * already holds tokens of the sequence (its first new token is not the block's first row), the larger of
- * that and its present exponent, and if that grew, the rows before it are rescaled.  Codes are
- * value * 2^-e rounded to nearest even; infinities become the largest code, NaN the format's
- * NaN (INT8: 0).  The rotation and the codes are computed from fp32, each product and sum
- * rounded once.  A page may be written for one sequence only within a call.
+ * slora_kv_append(): writes the new tokens' keys and values to the cache, rotating queries
+ * and keys by their positions on the way.  Scales: a block's exponent is the smallest
+ * e >= -40 for which every finite |value| of its new tokens is at most 448 * 2^e (127 * 2^e
+ * for INT8); if the block already holds tokens of the sequence (its first new token is not
+ * the block's first row), the larger of that and its present exponent, and if that grew, the
+ * rows before it are rescaled.  Codes are value * 2^-e rounded to nearest even; infinities
+ * become the largest code, NaN the format's NaN (INT8: 0).  The rotation and the codes are
+ * computed from fp32, each product and sum rounded once.  A page may be written for one
+ * sequence only within a call.
  *   k, v         device fp16 [T][n_kv_heads][head_dim]; row t starts at t * k_stride
  *                (v_stride) elements, so the three can be parts of one buffer
  *   q, q_out     device fp16 [T][n_q_heads][head_dim] with strides alike, or both NULL: q_out
@@ -527,20 +532,25 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   lse          device float [T][n_q_heads], or NULL: natural log of the softmax's denominator
  *   causal       1: the token at position p sees positions <= p;  0: the whole sequence
  *   window       0, or with causal 1: it sees positions p - window + 1 .. p only
- * A token that sees nothing gets zeros and lse -inf.  Cache rows that no query sees may hold
- * anything (their codes are never used, and pages wholly outside are not read).  Scores, the softmax's maxima
- * and sums and the output sums are fp32; the weights are rounded to fp16 once
- * for the product with the values, the output once.  Results of one call are deterministic for
- * given sizes; the order of the partial sums depends on the batch and the number of SMs.
- * Attends of one cache share its workspace: issue them on one stream, or order the streams.
+ * A token that sees nothing gets zeros and lse -inf.  Cache rows that no new token of the
+ * sequence sees may hold anything (their codes are never used, and pages wholly outside are
+ * not read).  A NaN among the values that one new token sees can reach the sequence's other
+ * new tokens of the call, whose weight for it is 0.  Scores, the softmax's maxima and sums
+ * and the output sums are fp32; the weights are rounded to fp16 once for the product with
+ * the values, the output once.  Results are the same from call to call; the order of the
+ * partial sums depends on the batch and the number of SMs.
+ * Attends over one pool, of whichever cache, share its workspace: issue them on one stream,
+ * or order the streams.
  *
- * Both: strides are multiples of 8 elements and at least a row; pointers 16-byte aligned.  Errors:
- * SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is launched),
- * SLORA_ERR_UNSUPPORTED (head_dim or a page too small).  On the device a bad page id
- * (SLORA_DEV_BAD_PAGE: that block is not written, or not seen), a kv_len below the number of new
- * tokens (append) or beyond the block table (SLORA_DEV_BAD_LENGTH) and a tok_indptr that decreases or leaves
+ * Both: strides are multiples of 8 elements and at least a row; pointers 16-byte aligned.
+ * Errors: SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is
+ * launched), SLORA_ERR_UNSUPPORTED (head_dim or a page too small; or max_q times the query
+ * heads per KV head above 2^30).  On the device a bad page id (SLORA_DEV_BAD_PAGE: that
+ * block is not written, or not seen), a kv_len below the number of new tokens (append) or
+ * beyond the block table (SLORA_DEV_BAD_LENGTH) and a tok_indptr that decreases or leaves
  * [0, T] (SLORA_DEV_BAD_SEGMENT) set the pool's status word and skip that work; an attend
- * with kv_len < n sees no key for its first n - kv_len tokens.  Enqueued on `stream`; nothing waits or allocates.
+ * with kv_len < n sees no key for its first n - kv_len tokens.  Enqueued on `stream`;
+ * nothing waits or allocates.
  * ------------------------------------------------------------------------- */
 typedef struct slora_kv *slora_kv_t;
 enum { SLORA_KV_E4M3 = 0, SLORA_KV_INT8 = 1 };

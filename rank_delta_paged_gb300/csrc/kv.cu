@@ -14,7 +14,6 @@
 using namespace slora;
 
 struct slora_kv {
-    slora_pool_t pool = nullptr;
     int device = 0;
     int num_sms = 0;
     int head_dim = 0;
@@ -27,7 +26,13 @@ struct slora_kv {
 
 namespace {
 
-// Rows per KV head up to which the streaming kernel, 16 rows at a time, is the faster one.
+// Rows per KV head (new tokens x query heads of the group) up to which a sequence is the streaming
+// kernel's, 16 rows at a time; the rest is the tensor cores' kernel's, 256 at a time.  Sequences of 500
+// to 8000 tokens, 8 KV heads, streaming and the other in us:
+//     rows    4 sequences    24 sequences    96 sequences
+//      16      50     65      92     132      229     379
+//      32      55     65     140     136      426     389
+//      64      69     66     245     140      809     398
 constexpr int32_t kSmallRows = 32;
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
@@ -112,7 +117,6 @@ extern "C" slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, i
     slora_kv *k = new (std::nothrow) slora_kv();
     if (!k)
         return fail(SLORA_ERR_HOST_ALLOC, "kv_create");
-    k->pool = pool;
     k->device = hp.device;
     k->num_sms = hp.num_sms > 0 ? hp.num_sms : 1;
     k->head_dim = head_dim;
@@ -273,12 +277,16 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     DeviceScope dev_scope(k->device);
     cudaError_t e = dev_scope.error();
     int launches = 0;
-    // Rows per KV head: few go to the streaming kernel, many to the tensor cores' one.  A batch whose sequences
-    // may be of both kinds runs both; where every sequence has nearly max_q new tokens, one
-    // kernel takes them all.
+    // A batch whose sequences may be of both kinds runs both kernels.  One takes them all where the mean
+    // is near max_q, or where the sequences that may have few rows (all but those that T needs, at max_q
+    // new tokens each) add at most a unit per SM: the second launch costs 2 to 8 us (16 prompts 120 us
+    // by one, 123 by two), and few rows gain little by it (24 sequences of 8 to 24 drafted tokens, 4 rows
+    // each: 138 us by one, 163 by two; of 2 to 60: 150 and 172).  Single tokens in number are
+    // dear beside prompts: 8 prompts and 64 of them take 346 us by one, 228 by two.
     const int64_t most = (int64_t)a.b.max_q * a.group;
     const bool big = most > kSmallRows;
-    const bool alike = (int64_t)a.b.T * 4 >= (int64_t)a.b.S * a.b.max_q * 3;
+    const int64_t others = a.b.max_q > 1 ? a.b.S - ((int64_t)a.b.T - a.b.S) / (a.b.max_q - 1) : 0;
+    const bool alike = (int64_t)a.b.T * 4 >= (int64_t)a.b.S * a.b.max_q * 3 || others * k->c.n_kv <= k->num_sms;
     if (e == cudaSuccess && big)
         e = kv::launch_attend_prefill(a, k->head_dim, k->format, alike ? 0 : kSmallRows,
                                       k->ws + kv::decode_workspace_bytes(k->num_sms), k->num_sms, (cudaStream_t)stream,

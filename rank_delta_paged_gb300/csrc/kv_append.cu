@@ -30,7 +30,9 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlockThreads = 512;  // append_kernel: two rows of 64 per group of 16 lanes
-constexpr int kFew = 8;
+// New tokens of a block up to which its pages go to groups of lanes.  64 sequences of 2, 32 KV heads:
+// 33 us so, 45 by whole pages; of 3: 37 and 43; but with 8 KV heads, of 3: 34 and 29, of 8: 46 and 31.
+constexpr int kFew = 2;
 constexpr int kMaxUnits = 128;     // pages per CTA at most
 constexpr int kQHeads = 4;         // query heads per group and step
 
