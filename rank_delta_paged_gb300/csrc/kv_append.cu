@@ -13,12 +13,15 @@
 // Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
 // values and queries alike; a row is a group of head_dim / 8 lanes, which holds two of them at a
 // time, and all of its reads that do not depend on others go first.
-// Other sequences (append_kernel): a CTA takes a run of one block's pages, page after page, with the next
-// page's rows under way; blocks with at most kFew new tokens go to groups of lanes, a page each,
-// which read their few rows twice.  It finds its block by a search of the token offsets, in which
-// block `slot` of the batch is counted as if every sequence before it had touched
-// floor(tokens / block) + 2 blocks (at least as many as it can), so no prefix sum over the
-// sequences has to be made first.  Their queries are a kernel of their own (rotate_kernel).
+// Other sequences (append_kernel): the pages of all blocks that they touch form one list, of which
+// every CTA takes an equal run, page after page by the whole CTA with the next page's rows under
+// way.  Their queries are a kernel of their own (rotate_kernel).
+//
+// Measured: 512 single tokens of 40 heads 14 us; 5400 tokens, of which 384 are single, of 32 heads 65 us
+// (3.2 TB/s); 16381 tokens of 8 heads of 64 51 us (3.7 TB/s).  The instructions between the reads and
+// the writes (some 180 per warp and 16 bytes a lane) and the waits for a page's reads take the time.
+// With two CTAs' worth of pages per block and CTAs found by a search of the token offsets, the
+// 5400 tokens took 93 us: half the SMs had twice the work of the others.
 #include "host_common.h"
 #include "internal.h"
 #include "kv.h"
@@ -30,19 +33,35 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kBlockThreads = 512;  // append_kernel: two rows of 64 per group of 16 lanes
-// New tokens of a block up to which its pages go to groups of lanes.  64 sequences of 2, 32 KV heads:
-// 33 us so, 45 by whole pages; of 3: 37 and 43; but with 8 KV heads, of 3: 34 and 29, of 8: 46 and 31.
-constexpr int kFew = 2;
-constexpr int kMaxUnits = 128;     // pages per CTA at most
+constexpr int kMaxUnits = 128;     // pages of a block at a time, at most
+constexpr int kSeqChunks = 64;
+// append_kernel's CTAs per SM: those that fit.  4 and 8 cost 1 to 8 us more for their starts.
+constexpr int kBlockCtas = 2;
 constexpr int kQHeads = 4;         // query heads per group and step
 
 struct Params {
     AppendArgs a;
-    int32_t slots;       // blocks of the cache, counted as above (single tokens: sequences)
-    int32_t splits;      // CTAs per slot
-    int32_t units;       // pages per CTA
-    int32_t q_rows;      // single tokens: query heads that go with the keys and values
+    // append_one_kernel:
+    int32_t splits;      // CTAs per sequence
+    int32_t units;       // rows per CTA
+    int32_t q_rows;      // query heads that go with the keys and values
 };
+
+// append_kernel's place in its run: what is left, and the part at hand.
+struct Walk {
+    int64_t left;                       // pages
+    int32_t s, skip, unit;              // sequence, block from its first, page of the block
+    int32_t u0, u1;                     // pages of the part at hand
+    int32_t held, nt, row0, from;       // rows already there, new rows, first of them, its position
+};
+
+// threadIdx.x, read anew: what is made from it is not kept across a loop around its use.
+__device__ __forceinline__ int fresh_tid()
+{
+    int t;
+    asm volatile("mov.u32 %0, %%tid.x;" : "=r"(t));
+    return t;
+}
 
 struct Rot {
     float c[8], s[8];
@@ -167,65 +186,6 @@ __device__ __forceinline__ uint2 rescale8(uint2 v, float unit)
 __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int32_t in_cache)
 {
     return a.positions ? a.positions[t] : in_cache;
-}
-
-// A block's nt <= kFew new rows of the pages [u0, u1): one page per group of lanes and step.
-// The rows are read once for their largest value and again, from the caches, for the codes.
-template <int D, int FMT>
-__device__ __forceinline__ void few_rows(const AppendArgs &a, int32_t u0, int32_t u1, int32_t nt, int32_t held,
-                                         int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp)
-{
-    constexpr int LPR = D / 8, GROUPS = kBlockThreads / LPR;
-    const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
-    const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
-#pragma unroll 1
-    for (int32_t ub = u0; ub < u1; ub += GROUPS) {
-        const int32_t u = ub + grp;
-        const bool val = u & 1;
-        const int32_t page = u < u1 ? s_page[u - u0] : -1;
-        const __half *src = (val ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
-        const int64_t stride = val ? a.v_stride : a.k_stride;
-        auto row = [&](int32_t i, float (&x)[8]) {
-            uint4 raw = make_uint4(0, 0, 0, 0);
-            if (page >= 0) raw = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + i) * stride);
-            Rot r;
-            r.on = false;
-            if (page >= 0 && !val) load_rot(a, position(a, row0 + i, from + i), ch, r);
-            unpack(raw, x);
-            rotate<LPR>(a, r, ch, x);
-        };
-        float x[8], m = 0.f;
-#pragma unroll 1
-        for (int32_t i = 0; i < nt; ++i) {
-            row(i, x);
-            m = fmaxf(m, size_of(x));
-        }
-        m = max_of(row_lanes, m);
-        int e = fit_exponent<FMT>(m);
-        uint8_t *dst = a.c.pool + (int64_t)page * a.c.page_bytes + ch * 8;
-        if (page >= 0) {
-            if (held) {
-                const int old = s_exp[u - u0];
-                if (old >= e) {
-                    e = old;
-                } else {
-                    const float unit = pow2(old - e);
-#pragma unroll 1
-                    for (int r = 0; r < held; ++r) {
-                        uint2 *w = reinterpret_cast<uint2 *>(dst + r * D);
-                        *w = rescale8<FMT>(*w, unit);
-                    }
-                }
-            }
-            if (ch == 0) a.c.exps[page] = (int8_t)e;
-        }
-        const float unit = pow2(-e);
-#pragma unroll 1
-        for (int32_t i = 0; i < nt; ++i) {
-            if (nt > 1) row(i, x);
-            if (page >= 0) *reinterpret_cast<uint2 *>(dst + (held + i) * D) = encode8<FMT>(x, unit);
-        }
-    }
 }
 
 // Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
@@ -385,71 +345,14 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     griddep_wait();
 }
 
+// A block's nt new rows of the pages [u0, u1), page after page by the whole CTA.
 template <int D, int FMT, int PASSES>
-__device__ __forceinline__ void append_blocks(const Params &p)
+__device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32_t u1, int32_t nt, int32_t held,
+                                          int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp,
+                                          uint32_t *s_max, int &turn)
 {
-    constexpr int LPR = D / 8;                 // lanes per row
-    constexpr int GROUPS = kBlockThreads / LPR;
-    const AppendArgs &a = p.a;
-    const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
-    __shared__ uint32_t s_max[3];
-    if (tid == 0) s_max[0] = 0;
-    __shared__ int32_t s_page[kMaxUnits];
-    __shared__ int8_t s_exp[kMaxUnits];
-
-
-    // ---- keys and values of one block of the cache ------------------------------------------
-    const int32_t slot = (int32_t)(blockIdx.x / p.splits), part = (int32_t)(blockIdx.x - (int64_t)slot * p.splits);
-    const int32_t bt = a.c.bt;
-    // last sequence whose slots start at or before this one, 32 at a time; every warp for itself
-    int32_t lo = 0;
-    for (int32_t n = a.b.S; n > 1;) {
-        const int32_t step = (n + 31) / 32, at = lo + (tid & 31) * step;
-        const bool le = at < lo + n && (int64_t)(a.b.indptr[at] / bt) + 2ll * at <= slot;
-        const int k = 31 - __clz(__ballot_sync(~0u, le) | 1u);
-        n = n - k * step < step ? n - k * step : step;
-        lo += k * step;
-    }
-    const int32_t s = lo, t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s];
-    const int32_t n = t1 - t0;
-    int32_t bad = 0;
-    if (t0 < 0 || t1 < t0 || t1 > a.b.T || n > a.b.max_q)
-        bad = SLORA_DEV_BAD_SEGMENT;
-    else if (len < n || (int64_t)len > (int64_t)a.b.max_blocks * bt)
-        bad = SLORA_DEV_BAD_LENGTH;
-    if (bad) {
-        if (tid == 0) set_status(a.c.status, bad);
-        return;
-    }
-    if (n <= 1) return;                                           // one: append_one_kernel's
-    const int32_t p0 = len - n;                                   // position of the first new token
-    const int64_t nth = slot - ((int64_t)(t0 / bt) + 2ll * s);    // nth touched block of the sequence
-    if (nth < 0 || p0 / bt + nth > (len - 1) / bt) return;
-    const int32_t blk = p0 / bt + (int32_t)nth;
-    const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
-    const int32_t held = from - blk * bt, nt = to - from;         // rows already there, new rows
-    const int32_t row0 = t0 + from - p0;                          // first of the new tokens' rows
-    const int32_t all = 2 * a.c.n_kv;
-    const int32_t u0 = part * p.units, u1 = u0 + p.units < all ? u0 + p.units : all;
-    // the CTA's pages and, for a block that holds tokens, their exponents
-    if (tid < u1 - u0) {
-        int32_t page = a.b.table[((int64_t)s * a.b.max_blocks + blk) * all + u0 + tid];
-        if (page < 0 || page >= a.c.num_pages) {
-            set_status(a.c.status, SLORA_DEV_BAD_PAGE);
-            page = -1;
-        }
-        s_page[tid] = page;
-        s_exp[tid] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
-    }
-
-    __syncthreads();
-    // unit: KV head * 2 + (0 keys, 1 values)
-    if (nt <= kFew) {
-        few_rows<D, FMT>(a, u0, u1, nt, held, row0, from, s_page, s_exp);
-        return;
-    }
-
-    int turn = 0;
+    constexpr int LPR = D / 8, GROUPS = kBlockThreads / LPR;
+    const int tid = fresh_tid(), ch = tid % LPR, grp = tid / LPR;
     uint4 raw[PASSES];
     auto read = [&](int32_t u) {
         const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
@@ -519,6 +422,149 @@ __device__ __forceinline__ void append_blocks(const Params &p)
     }
 }
 
+// The blocks that sequence s writes in append_kernel: none if it is skipped or has one new token or
+// none (append_one_kernel's, which reports what is wrong).
+__device__ __forceinline__ int32_t blocks_of(const AppendArgs &a, int64_t s)
+{
+    if (s >= a.b.S) return 0;
+    const int32_t t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s], n = t1 - t0, bt = a.c.bt;
+    if (t0 < 0 || t1 < t0 || t1 > a.b.T || n > a.b.max_q || n <= 1 || len < n ||
+        (int64_t)len > (int64_t)a.b.max_blocks * bt)
+        return 0;
+    return (len - 1) / bt - (len - n) / bt + 1;
+}
+
+// The next part of a CTA's run, by one warp: pages of one block.  A function of its own, so that what it
+// knows takes no registers while rows are in them.
+__device__ __noinline__ void next_part(const Params &p, Walk &w, int32_t *s_page, int8_t *s_exp)
+{
+    const AppendArgs &a = p.a;
+    const int32_t lane = threadIdx.x & 31, bt = a.c.bt, all = 2 * a.c.n_kv, S = a.b.S;
+                int64_t left = w.left;
+                int32_t q = w.s, skip = w.skip;
+                // the first sequence at or behind q that has block `skip`, counted from q
+                bool found = false;
+    #pragma unroll 1
+                while (left > 0 && !found && q < S) {
+                    const int32_t nb = blocks_of(a, (int64_t)q + lane);
+                    int32_t sum = nb;
+    #pragma unroll
+                    for (int o = 1; o < 32; o <<= 1) {
+                        const int32_t x = __shfl_up_sync(~0u, sum, o);
+                        if (lane >= o) sum += x;
+                    }
+                    const unsigned beyond = __ballot_sync(~0u, sum > skip);
+                    found = beyond != 0;
+                    const int l = found ? __ffs(beyond) - 1 : 31;
+                    skip -= __shfl_sync(~0u, found ? sum - nb : sum, l);
+                    q += found ? l : 32;
+                }
+                int32_t u0 = 0, u1 = 0;
+                if (found) {
+                    const int32_t t0 = a.b.indptr[q], n = a.b.indptr[q + 1] - t0, len = a.b.kv_len[q];
+                    const int32_t p0 = len - n;                                   // position of the first new token
+                    const int32_t blk = p0 / bt + skip;
+                    const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
+                    const int32_t held = from - blk * bt;
+                    u0 = w.unit;
+                    u1 = left < all - u0 ? u0 + (int32_t)left : all;
+                    if (u1 > u0 + kMaxUnits) u1 = u0 + kMaxUnits;
+                    // the block's pages of this CTA and, if it holds tokens, their exponents
+    #pragma unroll 1
+                    for (int32_t u = u0 + lane; u < u1; u += 32) {
+                        int32_t page = a.b.table[((int64_t)q * a.b.max_blocks + blk) * all + u];
+                        if (page < 0 || page >= a.c.num_pages) {
+                            set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+                            page = -1;
+                        }
+                        s_page[u - u0] = page;
+                        s_exp[u - u0] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
+                    }
+                    __syncwarp();                       // w.unit has been read
+                    if (lane == 0) {
+                        w.held = held;
+                        w.nt = to - from;
+                        w.row0 = t0 + from - p0;
+                        w.from = from;
+                        w.left = left - (u1 - u0);
+                        w.s = q;
+                        w.skip = u1 == all ? skip + 1 : skip;
+                        w.unit = u1 == all ? 0 : u1;
+                    }
+                }
+                if (lane == 0) {
+                    w.u0 = u0;
+                    w.u1 = u1;
+                }
+}
+
+template <int D, int FMT, int PASSES>
+__device__ __forceinline__ void append_blocks(const Params &p)
+{
+    const AppendArgs &a = p.a;
+    const int tid = threadIdx.x;
+    __shared__ uint32_t s_max[3];
+    __shared__ int32_t s_page[kMaxUnits];
+    __shared__ int8_t s_exp[kMaxUnits];
+    __shared__ int64_t s_sum[kSeqChunks];
+    __shared__ Walk s_walk;
+    const int lane = tid & 31;
+    const int32_t bt = a.c.bt, all = 2 * a.c.n_kv, S = a.b.S;
+    // ---- the list of blocks; every CTA sums it for itself ------------------------------------
+    const int32_t per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32, chunks = (S + per - 1) / per;
+    if (tid == 0) s_max[0] = 0;
+    if (tid >= chunks && tid < kSeqChunks) s_sum[tid] = 0;
+#pragma unroll 1
+    for (int c = tid >> 5; c < chunks; c += kBlockThreads / 32) {
+        int64_t t = 0;
+#pragma unroll 1
+        for (int64_t q = (int64_t)c * per + lane; q < (int64_t)(c + 1) * per; q += 32) t += blocks_of(a, q);
+#pragma unroll
+        for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
+        if (lane == 0) s_sum[c] = t;
+    }
+    __syncthreads();
+    // Warp 0 walks the list; what it knows stands in shared memory between its steps, since the rows
+    // of a page take all the registers there are.
+    if (tid < 32) {
+        const int64_t v0 = s_sum[2 * lane], v1 = s_sum[2 * lane + 1];
+        int64_t W = v0 + v1;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(~0u, W, o);
+            if (lane >= o) W += x;
+        }
+        const int64_t before = W - v0 - v1;
+        W = __shfl_sync(~0u, W, 31) * all;
+        // an equal run of pages per CTA
+        const int64_t run = (W + gridDim.x - 1) / gridDim.x, w0 = blockIdx.x * run;
+        int64_t skip = w0 / all;                   // blocks before this CTA's first
+        const int32_t unit = (int32_t)(w0 - skip * all);
+        const int at = 31 - __clz(__ballot_sync(~0u, before <= skip));
+        skip -= __shfl_sync(~0u, before, at);
+        const int64_t first = __shfl_sync(~0u, v0, at);
+        if (lane == 0) {
+            s_walk.left = w0 + run < W ? run : W - w0;
+            s_walk.s = 2 * at * per + (skip >= first ? per : 0);
+            s_walk.skip = (int32_t)(skip >= first ? skip - first : skip);
+            s_walk.unit = unit;
+        }
+        __syncwarp();
+    }
+    int turn = 0;
+#pragma unroll 1
+    for (;;) {
+        if (tid < 32) next_part(p, s_walk, s_page, s_exp);
+        __syncthreads();
+        const int32_t u0 = s_walk.u0, u1 = s_walk.u1, nt = s_walk.nt, held = s_walk.held, row0 = s_walk.row0,
+                      from = s_walk.from;
+        if (u1 == 0) return;
+        // unit: KV head * 2 + (0 keys, 1 values)
+        full_rows<D, FMT, PASSES>(a, u0, u1, nt, held, row0, from, s_page, s_exp, s_max, turn);
+        __syncthreads();                           // s_walk, s_page and s_exp have been read
+    }
+}
+
 template <int D, int FMT, int PASSES>
 __global__ void __launch_bounds__(kBlockThreads, PASSES <= 3 ? 2 : 1) append_kernel(const __grid_constant__ Params p)
 {
@@ -556,24 +602,14 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
         // two rows per group of lanes and CTA
         p.q_rows = a.b.max_q == 1 ? a.n_q : 0;
         const int32_t all = 2 * a.c.n_kv + p.q_rows;
-        p.slots = a.b.S;
         p.splits = (all + 2 * groups - 1) / (2 * groups);
         p.units = (all + p.splits - 1) / p.splits;
         e = start(e4m3 ? append_one_kernel<D, SLORA_KV_E4M3> : append_one_kernel<D, SLORA_KV_INT8>, p,
-                  (int64_t)p.slots * p.splits, stream);
+                  (int64_t)a.b.S * p.splits, stream);
         *launches += e == cudaSuccess;
         if (e != cudaSuccess || a.b.max_q == 1) return e;
     }
-    // A block's pages over several CTAs where the batch has few blocks; runs of at least four
-    // pages otherwise, so that a page's reads go under the page before.
-    const int32_t all = 2 * a.c.n_kv;
-    p.slots = a.b.T / a.c.bt + 2 * a.b.S;
-    int64_t splits = (8ll * num_sms + p.slots - 1) / p.slots;
-    if (splits > all) splits = all;
-    if (splits * kMaxUnits < all) splits = (all + kMaxUnits - 1) / kMaxUnits;
-    p.units = (int32_t)((all + splits - 1) / splits);
-    p.splits = (all + p.units - 1) / p.units;
-    const int64_t ctas = (int64_t)p.slots * p.splits;
+    const int64_t ctas = (int64_t)kBlockCtas * num_sms;
     // rows of a block over the CTA's groups: the registers for 2, 3 or 4 of them per lane (a
     // page of up to 8192, 12288 or 16384 bytes)
     constexpr int block_groups = kBlockThreads / (D / 8);
