@@ -77,7 +77,7 @@ typedef enum slora_status {
 #define SLORA_DEV_BAD_PAGE 3      /* page-table entry outside [0, num_pages) */
 #define SLORA_DEV_BAD_SEGMENT 4   /* segment tokens disagree on their adapter, or bad bounds */
 #define SLORA_DEV_TIMEOUT 5       /* a bounded wait inside a kernel gave up */
-#define SLORA_DEV_BAD_LENGTH 6    /* KV length below the new tokens or beyond the block table */
+#define SLORA_DEV_BAD_LENGTH 6    /* KV length below the new tokens, beyond the block table or above 2^30 */
 #define SLORA_DEV_BAD_POSITION 7  /* token position outside the rotation table */
 
 const char *slora_status_str(slora_status s);
@@ -546,8 +546,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * Errors: SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is
  * launched), SLORA_ERR_UNSUPPORTED (head_dim or a page too small; or max_q times the query
  * heads per KV head above 2^30).  On the device a bad page id (SLORA_DEV_BAD_PAGE: that
- * block is not written, or not seen), a kv_len below the number of new tokens (append) or
- * beyond the block table (SLORA_DEV_BAD_LENGTH) and a tok_indptr that decreases or leaves
+ * block is not written, or not seen), a kv_len below the number of new tokens (append),
+ * beyond the block table or above 2^30 (SLORA_DEV_BAD_LENGTH) and a tok_indptr that decreases or leaves
  * [0, T] (SLORA_DEV_BAD_SEGMENT) set the pool's status word and skip that work; an attend
  * with kv_len < n sees no key for its first n - kv_len tokens.  Enqueued on `stream`;
  * nothing waits or allocates.

@@ -72,6 +72,12 @@ struct PageMaps {
     CUtensorMap m[3];
 };
 
+// Lengths beyond the block table; and above 2^30 tokens positions would leave 32 bits at the end of a tile.
+__device__ __forceinline__ bool too_long(const Cache &c, const Batch &b, int32_t len)
+{
+    return len > 1 << 30 || (int64_t)len > (int64_t)b.max_blocks * c.bt;
+}
+
 // One sequence of a batch as the attention kernels see it: its new rows, its keys, and
 // whether its sizes can be used.
 struct Seq {
@@ -90,7 +96,7 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs &a, int32_t s, int32_t 
     if (t0 < 0 || t1 < t0 || t1 > a.b.T || q.n > a.b.max_q) {
         *bad = SLORA_DEV_BAD_SEGMENT;
         q.n = 0;
-    } else if (q.len < 0 || (int64_t)q.len > (int64_t)a.b.max_blocks * a.c.bt) {
+    } else if (q.len < 0 || too_long(a.c, a.b, q.len)) {
         *bad = SLORA_DEV_BAD_LENGTH;
         q.n = 0;
     }

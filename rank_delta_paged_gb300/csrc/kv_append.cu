@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
     int32_t bad = 0;
     if (t0 < 0 || t1 < t0 || t1 > a.b.T || t1 - t0 > a.b.max_q)
         bad = SLORA_DEV_BAD_SEGMENT;
-    else if (len < t1 - t0 || (int64_t)len > (int64_t)a.b.max_blocks * a.c.bt)
+    else if (len < t1 - t0 || too_long(a.c, a.b, len))
         bad = SLORA_DEV_BAD_LENGTH;
     if (bad) {
         if (tid == 0) set_status(a.c.status, bad);
@@ -428,8 +428,7 @@ __device__ __forceinline__ int32_t blocks_of(const AppendArgs &a, int64_t s)
 {
     if (s >= a.b.S) return 0;
     const int32_t t0 = a.b.indptr[s], t1 = a.b.indptr[s + 1], len = a.b.kv_len[s], n = t1 - t0, bt = a.c.bt;
-    if (t0 < 0 || t1 < t0 || t1 > a.b.T || n > a.b.max_q || n <= 1 || len < n ||
-        (int64_t)len > (int64_t)a.b.max_blocks * bt)
+    if (t0 < 0 || t1 < t0 || t1 > a.b.T || n > a.b.max_q || n <= 1 || len < n || too_long(a.c, a.b, len))
         return 0;
     return (len - 1) / bt - (len - n) / bt + 1;
 }

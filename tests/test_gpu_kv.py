@@ -558,3 +558,25 @@ def test_append_device_checks():
     assert c.s.device_status() == 6
     same = (c.s.pages == before).all(dim=1).cpu().numpy()
     assert same[c.table[1, 0].ravel()].all() and not same[c.table[0, 1].ravel()].all()
+
+
+def test_lengths_past_the_positions_are_refused():
+    # a block table wide enough by its own account, of which nothing may be read
+    c = Case([(2, 70), (1, 30)], hq=4, hkv=2, seed=32)
+    want, _ = c.attend()
+    c.kv_len[0] = (1 << 30) + 1
+    c.d_len = dev(c.kv_len)
+    wide = (1 << 24) + 1
+    b = rdp.KVBatch(c.T, 1, 2, wide, c.d_indptr, c.d_len, c.d_table)
+    out = torch.full((c.T, 512), 7.0, dtype=torch.float16, device="cuda")
+    rdp.slora_kv_attend(c.s.kv, b, half(c.q).view(-1, 512), 512, 4, out, 512)
+    assert c.s.device_status() == 6
+    assert (out == 7).all()
+    before = c.s.pages.clone()
+    k = torch.ones((c.T, 256), dtype=torch.float16, device="cuda")
+    rdp.slora_kv_append(c.s.kv, b, k, 256, k, 256)
+    assert c.s.device_status() == 6
+    assert torch.equal(before, c.s.pages)
+    c.kv_len[0] = 70
+    c.push()
+    assert np.array_equal(c.attend()[0], want)
