@@ -368,56 +368,52 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
             };
             int count = 0;
-            if (!fresh && tile + per_batch < u_tiles && ahead + per_batch < w1) {     // all within the unit
-                fill(tile + my_tile, ahead + my_tile, !begun && my_tile == 0);
-                tile += per_batch;
-                ahead += per_batch;
-                count = per_batch;
-            } else {
-#pragma unroll 1
-                for (; count < per_batch; ++count) {
-                    if (tile >= u_tiles) {
-                        // the next unit
-                        ahead += u_tiles + kUnitCost - tile;
-                        if (ahead >= w1) break;
-                        if (++grp == u_groups) {
-                            grp = 0;
-                            if (++head == a.c.n_kv) {
-                                head = 0;
-                                unsigned next;
-#pragma unroll 1
-                                while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
-                                    s32 += 32;
-                                    at_lane = -1;
-                                    hold(s32);
-                                }
-                                if (next == 0) {      // the lengths changed under the call
-                                    if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
-                                    ahead = w1;
-                                    break;
-                                }
-                                at_lane = __ffs(next) - 1;
-                                u_tiles = __shfl_sync(~0u, tiles, at_lane);
-                                u_groups = __shfl_sync(~0u, groups, at_lane);
-                                u_first = __shfl_sync(~0u, first, at_lane);
-                                u.row0 = __shfl_sync(~0u, q.row0, at_lane);
-                                u.n = __shfl_sync(~0u, q.n, at_lane);
-                                u.len = __shfl_sync(~0u, q.len, at_lane);
-                            }
-                        }
-                        tile = 0;
-                        fresh = true;
-                    }
+            do {                        // the part of the batch that lies in one unit
+                if (tile >= u_tiles) {
+                    // the next unit
+                    ahead += u_tiles + kUnitCost - tile;
                     if (ahead >= w1) break;
-                    if (fresh) {
-                        enter(ahead);
-                        fresh = false;
+                    if (++grp == u_groups) {
+                        grp = 0;
+                        if (++head == a.c.n_kv) {
+                            head = 0;
+                            unsigned next;
+#pragma unroll 1
+                            while ((next = __ballot_sync(~0u, tiles > 0 && lane > at_lane)) == 0 && s32 + 32 < S) {
+                                s32 += 32;
+                                at_lane = -1;
+                                hold(s32);
+                            }
+                            if (next == 0) {      // the lengths changed under the call
+                                if (lane == 0) set_status(status, SLORA_DEV_BAD_LENGTH);
+                                ahead = w1;
+                                break;
+                            }
+                            at_lane = __ffs(next) - 1;
+                            u_tiles = __shfl_sync(~0u, tiles, at_lane);
+                            u_groups = __shfl_sync(~0u, groups, at_lane);
+                            u_first = __shfl_sync(~0u, first, at_lane);
+                            u.row0 = __shfl_sync(~0u, q.row0, at_lane);
+                            u.n = __shfl_sync(~0u, q.n, at_lane);
+                            u.len = __shfl_sync(~0u, q.len, at_lane);
+                        }
                     }
-                    if (count == my_tile) fill(tile, ahead, !begun && count == 0);
-                    ++tile;
-                    ++ahead;
+                    tile = 0;
+                    fresh = true;
                 }
-            }
+                if (ahead >= w1) break;
+                if (fresh) {
+                    enter(ahead);
+                    fresh = false;
+                }
+                int32_t n = per_batch - count < u_tiles - tile ? per_batch - count : u_tiles - tile;
+                if (w1 - ahead < n) n = (int32_t)(w1 - ahead);
+                const int32_t t = my_tile - count;
+                if (t >= 0 && t < n) fill(tile + t, ahead + t, !begun && my_tile == 0);
+                tile += n;
+                ahead += n;
+                count += n;
+            } while (count < per_batch);
             if (count == 0) return 0;
             begun = true;
             if (++slot == n_batches) slot = 0;
