@@ -508,7 +508,7 @@ __device__ __forceinline__ void append_blocks(const Params &p)
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ Walk s_walk;
     const int lane = tid & 31;
-    const int32_t bt = a.c.bt, all = 2 * a.c.n_kv, S = a.b.S;
+    const int32_t all = 2 * a.c.n_kv, S = a.b.S;
     // ---- the list of blocks; every CTA sums it for itself ------------------------------------
     const int32_t per = ((S + kSeqChunks - 1) / kSeqChunks + 31) / 32 * 32, chunks = (S + per - 1) / per;
     if (tid == 0) s_max[0] = 0;
