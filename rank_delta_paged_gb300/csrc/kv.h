@@ -111,6 +111,14 @@ __device__ __forceinline__ int32_t div_group(const AttendArgs &a, int32_t r)
     return q * a.group > r ? q - 1 : q;
 }
 
+// The same lane of the warp every time, and one that the compiler knows to be one.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r != 0;
+}
+
 // 64-bit quotients are long code; none is on a path that matters.
 static __device__ __noinline__ int32_t div_list(int64_t x, int64_t y)
 {

@@ -58,6 +58,16 @@ constexpr int kMaxRows = 16;
 constexpr int kDescs = 32;                      // descriptors: 4 batches of 4 being prepared, 4 in use
 constexpr int kPartStride = 2 * kMaxRows + kMaxRows * 128;   // floats of one partial result: m, l, O
 
+template <class T>
+__device__ __forceinline__ T uniform(T x)
+{
+    return __shfl_sync(~0u, x, 0);
+}
+__device__ __forceinline__ int4 uniform(int4 v)
+{
+    return make_int4(uniform(v.x), uniform(v.y), uniform(v.z), uniform(v.w));
+}
+
 struct Meta {
     float ks[8];       // 2^exponent of the key pages, per 8 tokens of the tile
     float lv[8];       // exponent of the value pages
@@ -235,6 +245,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     if (warp == kConsumers) {
         // ---- producer ------------------------------------------------------------------
         // the sequence that holds tile w0: its chunk, then 32 sequences at a time
+        const bool leader = elect_one();
         const unsigned hit = __ballot_sync(~0u, before <= w0);
         const int at = 31 - __clz(hit);
         int chunk = 2 * at;
@@ -449,20 +460,25 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             }
             __syncwarp();
         };
-        // One lane: the copies of a tile.
-        auto copy_tile = [&](const Meta &m, int st) {
-            const uint32_t ok = m.ok, dst = smem_u32(ring) + st * Sh::kStage;
+        // The copies of a tile.  The whole warp goes through it by values that are the same in every lane, and one
+        // elected lane issues: a lane's own values would be turned into uniform ones for every copy.
+        auto copy_tile = [&](const Meta &m, int st, bool arrive, bool issue) {
+            const uint32_t ok = uniform(m.ok), dst = uniform(smem_u32(ring) + st * Sh::kStage);
             uint64_t *bar = &s_full[st];
+            if (arrive && leader) mbar_arrive_expect_tx(bar, (uint32_t)__popc(ok) * 16u * D);
+            if (!issue) return;
             auto copy = [&](int box, int level, int32_t row, int32_t kp, int32_t vp) {    // R << level rows
-                tma_load_3d(dst + box * R * D, &maps.m[level], row, kp, bar);
-                tma_load_3d(dst + box * R * D + Sh::kHalf, &maps.m[level], row, vp, bar);
+                if (leader) {
+                    tma_load_3d(dst + box * R * D, &maps.m[level], row, kp, bar);
+                    tma_load_3d(dst + box * R * D + Sh::kHalf, &maps.m[level], row, vp, bar);
+                }
             };
             if (R == 16) {
                 // the tile's four boxes as one, as two halves, or one by one: a box can be
                 // joined to the one before unless it starts a page
-                const int4 row = *reinterpret_cast<const int4 *>(m.row);
-                const int4 kp = *reinterpret_cast<const int4 *>(m.page[0]);
-                const int4 vp = *reinterpret_cast<const int4 *>(m.page[1]);
+                const int4 row = uniform(*reinterpret_cast<const int4 *>(m.row));
+                const int4 kp = uniform(*reinterpret_cast<const int4 *>(m.page[0]));
+                const int4 vp = uniform(*reinterpret_cast<const int4 *>(m.page[1]));
                 if (ok == 0xFFu && row.y && row.z && row.w) {
                     copy(0, 2, row.x, kp.x, vp.x);
                 } else {
@@ -482,7 +498,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             } else {
 #pragma unroll 1
                 for (int x = 0; x < 8; ++x)
-                    if (ok >> x & 1u) copy(x, 0, m.row[x], m.page[0][x], m.page[1][x]);
+                    if (ok >> x & 1u) copy(x, 0, uniform(m.row[x]), uniform(m.page[0][x]), uniform(m.page[1][x]));
             }
         };
         // Two batches lie between the reading of a batch's page ids and of its exponents, and one more
@@ -501,9 +517,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (step == 0) {
                 settle(b3, n3, 0);
                 early = n3 < NS ? n3 : NS;
-                if (lane == 0)
 #pragma unroll 1
-                    for (int t = 0; t < early; ++t) copy_tile(meta[t], t);
+                for (int t = 0; t < early; ++t) copy_tile(meta[t], t, false, true);
             }
             if (step < 3) continue;
             if (n0 == 0 || *abort) break;
@@ -532,11 +547,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
 #pragma unroll 1
             for (int t = 0; t < n0; ++t, ++issued) {
                 if (!wait_bar(&s_empty[stage], parity, abort, status)) break;
-                if (lane == 0) {
-                    const Meta &m = meta[(batch << batch_log) + t];
-                    mbar_arrive_expect_tx(&s_full[stage], (uint32_t)__popc(m.ok) * 16u * D);
-                    if (issued >= early) copy_tile(m, stage);
-                }
+                copy_tile(meta[(batch << batch_log) + t], stage, true, issued >= early);
                 if (++stage == NS) {
                     stage = 0;
                     parity ^= 1;

@@ -154,13 +154,6 @@ __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t r;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
-    return r != 0;
-}
-
 struct Tiles {
     int32_t lo, hi;        // key tiles [lo, hi) of a unit, one at least
     int32_t k0, k1;        // keys
