@@ -51,7 +51,7 @@ constexpr int kConvWarp = 8, kMmaWarp = 12, kPlanWarp = 13, kMmaWarp1 = 14;
 // of 2 to 60 drafted tokens 493 and 507; 16 equal prompts the same by either.
 constexpr int kUnitCost = 3;
 constexpr int kSeqChunks = 64;
-constexpr int kDescs = 8;                 // tile descriptors: 5 being prepared, 3 in use
+constexpr int kDescs = 8;                 // tile descriptors: 3 being prepared, the others in use
 
 enum : uint32_t {
     kFirst = 1, kLast = 2, kWhole = 4, kPlain = 8,
@@ -198,7 +198,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     const uint32_t stage_sm = v_sm + 2 * Sh::kKVTile;
     Desc *desc = reinterpret_cast<Desc *>(smem_raw + (stage_sm + 8 * Sh::kStage - smem_u32(smem_raw)));
     __shared__ uint64_t s_tfull[kDescs], s_tempty[kDescs], s_kfull[2], s_kempty[2], s_vfull[2], s_vempty[2];
-    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin;
+    __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin, s_unit;
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
     __shared__ int s_abort, s_last[2];
@@ -227,6 +227,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         mbar_init(&s_qfull, 4);
         mbar_init(&s_qempty, 2);
         mbar_init(&s_fin, 2);
+        mbar_init(&s_unit, 1);
         fence_mbar_init();
         s_abort = 0;
     }
@@ -473,20 +474,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             return x.want ? (int32_t)a.c.exps[x.page] : 0;
         };
-        // Two tiles lie between the reading of a tile's page ids and of its exponents, and two
-        // more between those and their use.
+        // A tile lies between the reading of a tile's page ids and of its exponents, and one more between
+        // those and their use; but the first tile goes out as soon as it can.
         const Box none = {false, 0, 0};
-        Box b0 = none, b1 = none, b2 = none, b3 = none, b4;
-        bool n0 = false, n1 = false, n2 = false, n3 = false, n4;
-        int32_t e0 = 0, e1 = 0, e2;
+        Box b0 = none, b1 = none, b2;
+        bool n0 = false, n1 = false, n2;
+        int32_t e0 = 0, e1;
 #pragma unroll 1
-        for (int32_t i = -4;;
-             ++i, b0 = b1, b1 = b2, b2 = b3, b3 = b4, n0 = n1, n1 = n2, n2 = n3, n3 = n4, e0 = e1, e1 = e2) {
-            e2 = exponent_of(b2);
-            n4 = describe(b4);
-            if (i < 0) continue;
+        for (int32_t i = -2;; ++i, b0 = b1, b1 = b2, n0 = n1, n1 = n2, e0 = e1) {
+            e1 = exponent_of(b1);
+            n2 = describe(b2);
+            if (i == -2) {
+                __syncwarp();
+                if (lane == 0 && n2) mbar_arrive(&s_unit);       // the first unit is known
+                b0 = b2;
+                n0 = n2;
+                e0 = exponent_of(b2);
+            } else if (i < 0) {
+                continue;
+            }
             if (!n0 || *abort) break;
-            Desc &d = desc[i % kDescs];
+            if (i == 0) continue;
+            Desc &d = desc[i < 0 ? 0 : i % kDescs];
             // a group needs both its keys and its values
             const unsigned have = __ballot_sync(~0u, b0.want), ok = have & have >> 16 & 0xFFFFu;
             const bool both = ok >> gl & 1u;
@@ -503,7 +512,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (ok != 0xFFFFu) d.flags &= ~kPlain;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_tfull[i % kDescs]);
+            if (lane == 0) mbar_arrive(&s_tfull[i < 0 ? 0 : i % kDescs]);
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
         // ---- products of one row tile -------------------------------------------------------
@@ -665,10 +674,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         // Keys run a tile ahead of values: K_0, K_1, V_0, K_2, V_1, ..  One loop for both, with the next half
         // tile's codes on their way in rb, keeps the code short; the moves at its end cost less than a second copy.
         uint4 ra[NL], rb[NL];
-        uint32_t qe_par = 1;
-        bool rows_under_way = false;
+        uint32_t qe_par = 0;
+        bool rows_under_way = true;
         int32_t i = 0, last = 0x7FFFFFFF;                      // the tile, and the last of the run once known
         int kv = 0;
+        // the first unit's rows, under way while its pages are looked up
+        if (wait_bar(&s_unit, 0, abort, status)) load_rows(desc[0]);
         if (wait_bar(&s_tfull[0], 0, abort, status)) {
             load(desc[0], 0, ra);
 #pragma unroll 1
@@ -700,11 +711,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 }
                 if (kv && lane == 0) mbar_arrive(&s_tempty[i % kDescs]);
                 // the rows of a unit that starts with the next tile
-                const int32_t u = kv ? i + 1 : 0;
-                if ((kv || i == 0) && u <= last && __builtin_expect(desc[u % kDescs].flags & kFirst, 0)) {
+                if (kv && i < last && __builtin_expect(desc[(i + 1) % kDescs].flags & kFirst, 0)) {
                     if (!wait_bar(&s_qempty, qe_par, abort, status)) break;
                     qe_par ^= 1;
-                    load_rows(desc[u % kDescs]);
+                    load_rows(desc[(i + 1) % kDescs]);
                     rows_under_way = true;
                 }
                 if (!more) break;
