@@ -30,8 +30,8 @@ namespace {
 // kernel's, 16 rows at a time; the rest is the tensor cores' kernel's, 256 at a time.  Sequences of 500
 // to 8000 tokens, 8 KV heads, streaming and the other in us:
 //     rows    4 sequences    24 sequences    96 sequences
-//      16      50     65      92     132      229     379
-//      32      55     65     140     136      426     389
+//      16      50     65      91     132      224     379
+//      32      54     65     138     136      420     389
 //      64      69     66     245     140      809     398
 constexpr int32_t kSmallRows = 32;
 

@@ -28,11 +28,13 @@
 // is far from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers,
 // half an instruction (e4m3) to one and a quarter (int8) per code.
 //
-// Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 557 us, 4.9 TB/s; 4 over 60000 to 131000
-// keys: 116 us, 5.5 TB/s; one over 700: 12 us, of which the launch and the chain of dependent reads (lengths,
-// page id, exponent, codes, parts) is nearly all.  Short sequences are held up by what a unit
-// costs besides its tiles (its rows' reads, the join of its four warps), long ones by
-// the start and the join of the parts.
+// Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 477 us, 5.7 TB/s; 4 over 60000 to 131000
+// keys: 116 us, 5.5 TB/s; one over 700: 11.5 us, of which the launch and the chain of dependent reads (lengths,
+// page id, exponent, codes, parts) is nearly all.  Short sequences are held up by their last tiles, which
+// cost the consumers as much as full ones, by the join of a unit's four warps, and by SMs that memory
+// serves a tenth slower than others; long ones by the start and the join of the parts.  The producer
+// is as busy as the consumers: a copy issued by one lane of a branch cost 340 cycles, by an elected
+// lane from values that are uniform over the warp half of that (520 to 485 us).
 #include <cstddef>
 #include <mutex>
 
@@ -50,8 +52,8 @@ constexpr int kConsumers = 4;                   // warps, 16 tokens of a tile ea
 constexpr int kThreads = 32 * (kConsumers + 1);
 constexpr int kMaxCtas = 3;                      // per SM, of any shape
 // What a unit costs besides its tiles, in tiles: starting and joining its four warps' results.  With
-// runs of equal tiles alone, the CTAs of 512 single tokens over 30 to 1000 keys took 250 to 620 us and the
-// kernel 600; so 557.
+// runs of equal tiles alone, the CTAs of 512 single tokens over 30 to 1000 keys took 250 to 620 us; the
+// kernel took 600 by 0 and 557 by 2.
 constexpr int kUnitCost = 2;
 constexpr int kSeqChunks = 64;                  // partial sums of the tile counts
 constexpr int kMaxRows = 16;
@@ -961,9 +963,9 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
     p.small_rows = small_rows;
     // Rows per unit by the batch's most common kind: every sequence's, or, where longer ones are the
     // other kernel's, the single tokens'.  8 rows have the registers for 3 CTAs per SM, 16 for 2, but
-    // read the keys half as often.  24 sequences of 500 to 8000 keys, by 8 and by 16 in us: 8 rows 72
-    // and 84, 16 rows 96 and 92, 32 rows 153 and 140; 512 single tokens of one row 557 and 760; 384
-    // of them beside 8 prompts 456 and 654 with the prompts.
+    // read the keys half as often.  24 sequences of 500 to 8000 keys, by 8 and by 16 in us: 8 rows 70
+    // and 81, 16 rows 94 and 91, 32 rows 147 and 138; 96 of 16 rows 280 and 224, 4 of 16 rows 41 and
+    // 50; 512 single tokens of one row 500 and 696.
     const int64_t most = (int64_t)a.b.max_q * a.group;
     p.rows = (most <= small_rows ? most : a.group) <= 8 ? 8 : 16;
     p.min_tiles = 1 + kUnitCost;
