@@ -387,6 +387,21 @@ def test_append_head_layouts_and_layouts_of_rows(hq, hkv):
     check_append(Case([(1, 33), (1, 100), (20, 70)], hq=hq, hkv=hkv, seed=24), with_q=False)
 
 
+def test_append_many_sequences():
+    """Blocks are found through long stretches of sequences that have none."""
+    rng = np.random.default_rng(3)
+    few = [(int(rng.choice([0, 1, 1, 1, 2, 9])), int(rng.integers(9, 60))) for _ in range(2200)]
+    seqs = [(0, 5)] * 70 + few + [(200, 333)] + [(1, 7)] * 400 + [(0, 0)] * 40 + [(33, 90), (1, 1)]
+    check_append(Case(seqs, hq=2, hkv=1, d=64, hidden=512, seed=33), rot=64)
+    check_append(Case([(1, 9)] * 2100 + [(2, 9)], hq=2, hkv=1, d=64, hidden=512, seed=34), rot=64)
+
+
+def test_append_more_pages_than_a_cta_lists():
+    """A CTA's run is longer than the pages it looks up at a time, and a block has more pages than that."""
+    check_append(Case([(330, 400), (1, 5), (310, 310)], hq=512, hkv=512, d=64, hidden=512, seed=35, stale=False), rot=64,
+                 with_q=False)
+
+
 def test_append_given_positions():
     check_append(Case([(1, 33), (5, 100), (20, 70)], hq=4, hkv=2, seed=25), positions=lambda p: p[::-1] + 3)
 
