@@ -487,9 +487,9 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             if (i == -2) {
                 __syncwarp();
                 if (lane == 0 && n2) mbar_arrive(&s_unit);       // the first unit is known
+                e0 = exponent_of(b2);                            // checks its pages, before anything is made of them
                 b0 = b2;
                 n0 = n2;
-                e0 = exponent_of(b2);
             } else if (i < 0) {
                 continue;
             }

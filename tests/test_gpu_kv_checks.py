@@ -1,0 +1,178 @@
+"""GPU checks of what the 8-bit KV cache does with entries that it must not use: page ids, lengths and
+token offsets out of range reach a status word, never memory, and every other block, head and
+sequence of the call keeps its result bit for bit."""
+import numpy as np
+import pytest
+import torch
+
+import kv_reference as R
+import rank_delta_paged_gb300 as rdp
+from test_gpu_kv import Case, dev, half
+
+pytestmark = pytest.mark.gpu
+
+BAD_PAGE, BAD_SEGMENT, TIMEOUT, BAD_LENGTH, BAD_POSITION = 3, 4, 5, 6, 7
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _built():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    rdp.build.build()
+    rdp.lib()
+
+
+def masked_attend(c, s, h, missing, scale):
+    """fp64 causal attention of sequence s, KV head h, with the blocks `missing` not seen: (out, tolerance), the
+    tolerance by the same account as kv_reference.attend."""
+    val, exps = c.values()
+    n, L = c.seqs[s]
+    t0, g, bt = c.indptr[s], c.hq // c.hkv, c.bt
+    nb = -(-L // bt)
+    ok = np.repeat([b not in missing for b in range(nb)], bt)[:L]
+    rows = []
+    for w in (0, 1):
+        rows.append(np.concatenate([np.zeros((bt, c.d)) if b in missing else
+                                    val[c.table[s, b, h, w]] * 2.0 ** float(exps[c.table[s, b, h, w]])
+                                    for b in range(nb)])[:L])
+    see = (np.arange(L)[None] <= (L - n + np.arange(n))[:, None]) & ok[None]
+    out, tol = np.zeros((n, g, c.d)), np.zeros((n, g, c.d))
+    for j in range(g):
+        q = c.q[t0:t0 + n, h * g + j].astype(np.float64)
+        z = np.where(see, q @ rows[0].T * scale, -np.inf)
+        m = z.max(1)
+        p = np.exp(z - np.where(np.isinf(m), 0.0, m)[:, None])
+        w = p / np.maximum(p.sum(1), 1e-300)[:, None]
+        out[:, j] = w @ rows[1]
+        ds = np.where(see, np.abs(q) @ np.abs(rows[0]).T, 0).max(1) * scale * (c.d + 8) * 2.0 ** -24 + 2.0 ** -21 + L * 2.0 ** -24
+        tol[:, j] = (2.0 ** -11 * 1.01 + 2 * ds[:, None]) * (w @ np.abs(rows[1])) + 2.0 ** -11 * np.abs(out[:, j]) + 2.0 ** -24
+    return out, tol
+
+
+# new tokens of each sequence: of single tokens the streaming kernel's, else the prompt kernel's (its rows per KV
+# head are new tokens x 4), in one call or beside each other
+PROMPTS = [(70, 200), (40, 40), (130, 333)]
+STREAM = [(1, 200), (2, 40), (4, 333)]
+MIXED = [(130, 333)] + [(1, 90)] * 200
+
+
+@pytest.mark.parametrize("seqs", [PROMPTS, STREAM, MIXED], ids=["prompts", "stream", "mixed"])
+@pytest.mark.parametrize("d,hidden", [(128, 4096), (64, 256)])
+@pytest.mark.parametrize("block", [0, 1])
+@pytest.mark.parametrize("which", [0, 1])
+def test_bad_pages_are_not_seen(seqs, d, hidden, block, which):
+    """A page id below 0, the first past the pool and one far past it, of keys and of values, in the first block of
+    a call's first tile and in a later one."""
+    c = Case(seqs, hq=8, hkv=2, d=d, hidden=hidden, seed=40)
+    scale = 0.5 / np.sqrt(d)
+    want, wl = c.attend()
+    num = len(c.pages)
+    for s, h in ((0, 0), (len(seqs) - 1, 1)):
+        if block >= -(-seqs[s][1] // c.bt):
+            continue
+        keep = c.table[s, block, h, which]
+        good, tol = masked_attend(c, s, h, {block}, scale)
+        for page in (-1, -(1 << 31), num, (1 << 31) - 1):
+            c.table[s, block, h, which] = page
+            c.d_table = dev(c.table)
+            out, lse = c.attend()
+            assert c.s.device_status() == BAD_PAGE
+            mine = np.zeros(out.shape[:2], bool)
+            mine[c.indptr[s]:c.indptr[s + 1], 4 * h:4 * h + 4] = True
+            assert np.array_equal(out[~mine], want[~mine]) and np.array_equal(lse[~mine], wl[~mine])
+            got = out[c.indptr[s]:c.indptr[s + 1], 4 * h:4 * h + 4]
+            assert (np.abs(got - good) <= tol).all()
+        c.table[s, block, h, which] = keep
+    c.d_table = dev(c.table)
+    out, lse = c.attend()
+    assert np.array_equal(out, want) and np.array_equal(lse, wl) and c.s.device_status() == 0
+
+
+@pytest.mark.parametrize("seqs", [PROMPTS, STREAM], ids=["prompts", "stream"])
+def test_every_page_bad(seqs):
+    c = Case(seqs, hq=8, hkv=2, seed=41)
+    c.table[:] = -1
+    c.d_table = dev(c.table)
+    out, lse = c.attend()
+    assert c.s.device_status() == BAD_PAGE
+    assert (out == 0).all() and (lse == -np.inf).all()
+
+
+def test_bad_lengths_and_offsets_of_prompts():
+    """The prompt kernel skips the sequence and reports it; the others keep their results."""
+    c = Case(PROMPTS, hq=8, hkv=2, seed=42)
+    want, _ = c.attend()
+    t0, t1 = c.indptr[1], c.indptr[2]
+    rest = np.r_[0:t0, t1:c.T]
+    for length in (-1, c.max_blocks * c.bt + 1, (1 << 30) + 1, -(1 << 31)):
+        keep = c.kv_len[1]
+        c.kv_len[1] = length
+        c.d_len = dev(c.kv_len)
+        out, _ = c.attend()
+        assert c.s.device_status() == BAD_LENGTH
+        assert np.array_equal(out[rest], want[rest]) and (out[t0:t1] == 7).all()
+        c.kv_len[1] = keep
+    c.d_len = dev(c.kv_len)
+    for indptr, kept in (([0, 70, c.T + 1, c.T + 1], np.r_[0:70]), ([0, 70, 60, 60], np.r_[0:70]), ([-1, 70, 70, 70], np.r_[0:0])):
+        c.d_indptr = dev(np.array(indptr, np.int32))
+        out, _ = c.attend()
+        assert c.s.device_status() == BAD_SEGMENT
+        other = np.setdiff1d(np.arange(c.T), kept)
+        assert np.array_equal(out[kept], want[kept]) and (out[other] == 7).all()
+    c.d_indptr = dev(c.indptr)
+    out, _ = c.attend(max_q=70)                     # a sequence with more new tokens than max_q
+    assert c.s.device_status() == BAD_SEGMENT
+    assert np.array_equal(out[:110], want[:110]) and (out[110:] == 7).all()
+
+
+def append_ones(c, batch=None):
+    k = torch.ones((c.T, c.hkv * c.d), dtype=torch.float16, device="cuda")
+    rdp.slora_kv_append(c.s.kv, batch or c.batch(), k, c.hkv * c.d, k, c.hkv * c.d)
+    status = c.s.device_status()
+    return status, c.s.pages.cpu().numpy(), c.s.exponents.cpu().numpy()
+
+
+@pytest.mark.parametrize("seqs", [[(1, 70), (1, 40), (1, 130)], [(9, 70), (30, 40), (130, 200)]], ids=["single", "several"])
+def test_append_skips_bad_pages(seqs):
+    """The page is not written, every other page is written as without the bad entry."""
+    c = Case(seqs, hq=4, hkv=2, seed=43)
+    _, want, we = append_ones(c)
+    for s, h, which in ((0, 0, 0), (1, 1, 1), (2, 0, 1)):
+        blk = (seqs[s][1] - 1) // c.bt
+        page = c.table[s, blk, h, which]
+        for bad in (-1, -(1 << 31), len(c.pages), (1 << 31) - 1):
+            c.push()
+            t = c.table.copy()
+            t[s, blk, h, which] = bad
+            c.d_table = dev(t)
+            status, got, ge = append_ones(c)
+            assert status == BAD_PAGE
+            others = np.arange(len(got)) != page
+            assert np.array_equal(got[others], want[others]) and np.array_equal(ge[others], we[others])
+            assert np.array_equal(got[page], c.pages[page]) and ge[page] == c.exps[page]
+
+
+@pytest.mark.parametrize("seqs", [[(1, 70), (1, 40), (1, 130)], [(9, 70), (30, 40), (130, 200)]], ids=["single", "several"])
+def test_append_leaves_skipped_sequences_alone(seqs):
+    """A sequence with an unusable length or offsets: none of its pages and exponents change."""
+    c = Case(seqs, hq=4, hkv=2, seed=44)
+    _, want, we = append_ones(c)
+    mine = np.zeros(len(c.pages), bool)
+    mine[c.table[1][c.table[1] >= 0]] = True
+    for length in (-1, seqs[1][0] - 1, c.max_blocks * c.bt + 1, (1 << 30) + 1):
+        c.push()
+        lens = c.kv_len.copy()
+        lens[1] = length
+        c.d_len = dev(lens)
+        status, got, ge = append_ones(c)
+        assert status == BAD_LENGTH
+        assert np.array_equal(got[mine], c.pages[mine]) and np.array_equal(ge[mine], c.exps[mine])
+        assert np.array_equal(got[~mine], want[~mine]) and np.array_equal(ge[~mine], we[~mine])
+    c.push()
+    c.d_indptr = dev(np.array([0, seqs[0][0], c.T + 1, c.T + 1], np.int32))
+    status, got, ge = append_ones(c)
+    assert status == BAD_SEGMENT
+    first = np.zeros(len(c.pages), bool)
+    first[c.table[0][c.table[0] >= 0]] = True
+    assert np.array_equal(got[first], want[first]) and np.array_equal(got[~first], c.pages[~first])
+    assert np.array_equal(ge[~first], c.exps[~first])
