@@ -642,6 +642,12 @@ slora_status slora_debug_set_prefill_split(int32_t on);
 enum { SLORA_FAULT_NONE = 0, SLORA_FAULT_COPY = 1, SLORA_FAULT_SCATTER = 2, SLORA_FAULT_DIRECTORY = 3,
        SLORA_FAULT_STAGING = 4, SLORA_FAULT_ARENA = 5 };
 slora_status slora_debug_inject_load_fault(int32_t kind, int32_t nth);
+/* Test hook: in every later slora_kv_attend of the process, CTA number `cta` of each kernel (grids are
+ * 1 to 3 CTAs per SM) behaves as if a wait inside it had run out: it sets SLORA_DEV_TIMEOUT, leaves its
+ * work undone and ends.  Rows whose keys it was to take are unspecified; later calls are not affected.
+ * -1 (the default): none; below that SLORA_ERR_INVALID_ARG.  The S-LoRA pages have no counterpart
+ * for it. */
+slora_status slora_debug_kv_give_up(int32_t cta);
 
 #ifdef __cplusplus
 }

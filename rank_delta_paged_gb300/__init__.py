@@ -45,7 +45,7 @@ __all__ = [
     "slora_bmm_workspace_bytes", "slora_lora_apply_bmm",
     "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope",
     "slora_kv_create", "slora_kv_destroy", "slora_kv_block_tokens", "slora_kv_exponents",
-    "slora_kv_append", "slora_kv_attend",
+    "slora_kv_append", "slora_kv_attend", "slora_debug_kv_give_up",
 ]
 
 _I32, _I64, _U64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -113,6 +113,7 @@ _SIGS = {
     "slora_kv_exponents": [_P, _PP],
     "slora_kv_append": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P],
     "slora_kv_attend": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
+    "slora_debug_kv_give_up": [_I32],
 }
 _RESTYPE = {"slora_status_str": ctypes.c_char_p, "slora_last_error": ctypes.c_char_p,
             "slora_version": _I32}
@@ -521,6 +522,11 @@ SLORA_FAULT_DIRECTORY, SLORA_FAULT_STAGING, SLORA_FAULT_ARENA = 3, 4, 5
 def slora_debug_inject_load_fault(kind: int, nth: int) -> None:
     """Make the nth later load-path operation of `kind` fail on the host (test hook)."""
     _call("slora_debug_inject_load_fault", int(kind), int(nth))
+
+
+def slora_debug_kv_give_up(cta: int) -> None:
+    """Test hook: makes one CTA of every later attention kernel give up; -1 clears it."""
+    _call("slora_debug_kv_give_up", int(cta))
 
 
 def slora_debug_set_prefill_cluster(ctas: int) -> None:

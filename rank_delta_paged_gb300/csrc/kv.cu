@@ -1,5 +1,6 @@
 // Host side of the 8-bit paged KV cache: the cache's handle, the checks of arguments and the
 // choice of kernels.
+#include <atomic>
 #include <cmath>
 #include <new>
 
@@ -34,6 +35,8 @@ namespace {
 //      32      54     65     138     136      420     389
 //      64      69     66     245     140      809     398
 constexpr int32_t kSmallRows = 32;
+
+std::atomic<int32_t> g_give_up{-1};     // slora_debug_kv_give_up
 
 using EncodeTiledFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
                                    const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
@@ -274,6 +277,7 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     a.causal = causal;
     a.window = window;
+    a.give_up = g_give_up.load();
     DeviceScope dev_scope(k->device);
     cudaError_t e = dev_scope.error();
     int launches = 0;
@@ -296,4 +300,12 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
                                      (cudaStream_t)stream, &launches);
     *k->launches += launches;
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+extern "C" slora_status slora_debug_kv_give_up(int32_t cta)
+{
+    if (cta < -1)
+        return fail(SLORA_ERR_INVALID_ARG, "debug_kv_give_up: cta=%d", cta);
+    g_give_up.store(cta);
+    return SLORA_OK;
 }

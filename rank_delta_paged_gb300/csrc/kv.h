@@ -64,6 +64,7 @@ struct AttendArgs {
     uint32_t group_inverse;             // ceil(2^32 / group), 0 for 1
     float scale_log2;                   // softmax scale * log2(e)
     int32_t causal, window;
+    int32_t give_up;                    // test hook: this CTA gives up at its start; -1: none
 };
 
 // The pages as a tensor [num_pages][rows][head_dim] of bytes, in boxes of R, 2R and 4R rows of a

@@ -203,6 +203,10 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
     griddep_wait();
     griddep_launch_dependents();
+    if (tid == 0 && (int32_t)blockIdx.x == a.give_up) {
+        set_status(status, SLORA_DEV_TIMEOUT);
+        s_abort = 1;
+    }
 
     // Tiles of each run of `per` sequences; every CTA sums them for itself, which costs less
     // than a launch.
@@ -558,11 +562,16 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (++batch == n_batches) batch = 0;
             if (step == 3) settle(b1, n1, 1);
         }
-        // no copy outlives the CTA: wait for the last ones issued, whatever the consumers do
+        // No copy outlives the CTA: wait for the last ones, whatever the consumers do.  If the CTA gave up,
+        // some of the early ones may not have been handed on yet, and their barriers know nothing of them.
+#pragma unroll 1
+        for (int t = issued; t < early; ++t)
+            if (leader) mbar_arrive_expect_tx(&s_full[t], (uint32_t)__popc(meta[t].ok) * 16u * D);
+        const int32_t copied = issued > early ? issued : early;
         volatile int gone = 0;
 #pragma unroll 1
-        for (int i = 0; i < NS && i < issued && !gone; ++i) {
-            const int t = issued - 1 - i;
+        for (int i = 0; i < NS && i < copied && !gone; ++i) {
+            const int t = copied - 1 - i;
             wait_bar(&s_full[t % NS], (uint32_t)(t / NS & 1), &gone, status);
         }
         return;

@@ -233,6 +233,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     }
     griddep_wait();
     griddep_launch_dependents();
+    if (tid == 0 && (int32_t)blockIdx.x == a.give_up) {
+        set_status(status, SLORA_DEV_TIMEOUT);
+        s_abort = 1;
+    }
 
     // Tiles of each run of `per` sequences; every CTA sums them for itself.
     const int S = a.b.S;

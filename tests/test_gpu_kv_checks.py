@@ -176,3 +176,40 @@ def test_append_leaves_skipped_sequences_alone(seqs):
     first[c.table[0][c.table[0] >= 0]] = True
     assert np.array_equal(got[first], want[first]) and np.array_equal(got[~first], c.pages[~first])
     assert np.array_equal(ge[~first], c.exps[~first])
+
+
+@pytest.fixture
+def give_up():
+    yield rdp.slora_debug_kv_give_up
+    rdp.slora_debug_kv_give_up(-1)
+
+
+WHOLE = {"stream": ([(1, 60)] * 40, 8, 2), "stream16": ([(3, 60)] * 40, 8, 2), "prompts": ([(60, 60)] * 30, 8, 2)}
+
+
+@pytest.mark.parametrize("kind", WHOLE)
+@pytest.mark.parametrize("hidden,d", [(4096, 128), (256, 64)])
+def test_a_cta_that_gives_up_ends_and_reports_it(give_up, kind, hidden, d):
+    """Units of one tile, a CTA each: the one that gives up (with its first copies under way) leaves its rows, the
+    others and the calls after it are as ever."""
+    seqs, hq, hkv = WHOLE[kind]
+    c = Case(seqs, hq=hq, hkv=hkv, d=d, hidden=hidden, seed=45)
+    want, wl = c.attend()
+    for cta in (0, 7, 33):
+        give_up(cta)
+        out, _ = c.attend()
+        assert c.s.device_status() == TIMEOUT
+        # a CTA's run holds one unit here: one sequence and KV head
+        s, h = divmod(cta, hkv)
+        mine = np.zeros(out.shape[:2], bool)
+        mine[c.indptr[s]:c.indptr[s + 1], h * 4:h * 4 + 4] = True
+        assert np.array_equal(out[~mine], want[~mine])
+        give_up(-1)
+        out, lse = c.attend()
+        assert c.s.device_status() == 0
+        assert np.array_equal(out, want) and np.array_equal(lse, wl)
+    give_up(1 << 20)                                    # no such CTA
+    out, _ = c.attend()
+    assert np.array_equal(out, want) and c.s.device_status() == 0
+    with pytest.raises(rdp.SloraError):
+        give_up(-2)
