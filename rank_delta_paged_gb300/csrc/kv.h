@@ -169,6 +169,28 @@ __device__ __forceinline__ bool wait_bar(uint64_t *bar, uint32_t parity, volatil
     return mbar_try_wait(bar, parity) || wait_more(bar, parity, abort, status);
 }
 
+// ---- joins ---------------------------------------------------------------------------
+// A unit that is cut between CTAs is joined by the last of them to arrive.  The words that count the arrivals
+// outlive a call, and a CTA that gave up never arrives; so a count belongs to its launch, and whatever
+// an earlier one left is below it.  The launches are numbered on the device, for a graph that is
+// replayed passes the same arguments each time: n threads of a launch add to `started` when they start, all
+// but one of them 1 and that one what makes 2^16, so the number stands above 16 bits of it, for arrivals.
+struct Joins {
+    unsigned long long *started;
+    unsigned long long *word;
+};
+__device__ __forceinline__ uint64_t start_launch(const Joins &j, bool first, uint32_t n)
+{
+    return atomicAdd(j.started, first ? 0x10000ull - (n - 1) : 1ull);
+}
+// Whether this is the last of a unit's n arrivals in the launch.
+__device__ __forceinline__ bool arrive_last(unsigned long long *word, uint64_t started, int32_t n)
+{
+    const unsigned long long none = started & ~0xFFFFull;
+    atomicMax(word, none);              // without a result, and before the addition at the same address
+    return atomicAdd(word, 1ull) == none + (unsigned)(n - 1);
+}
+
 // ---- codes ---------------------------------------------------------------------------
 template <int FMT>
 __device__ __forceinline__ constexpr float code_limit()
@@ -241,8 +263,8 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t &lo, uint32_t &hi)
 cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream,
                           int *launches);
 
-// The attention's workspace: partial results of rows whose keys are split over several
-// CTAs, and one arrival counter per CTA (zero between calls).
+// The attention's workspace: partial results of rows whose keys are split over several CTAs, and
+// the words of their joins (zero at first).
 size_t decode_workspace_bytes(int num_sms);
 // The rows of sequences with at most small_rows (new tokens * group) rows per KV head; INT32_MAX: all.
 cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt,

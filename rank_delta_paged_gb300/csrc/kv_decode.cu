@@ -154,7 +154,7 @@ struct DecodeParams {
     int32_t min_tiles;     // a CTA's run is at least this long
     uint32_t bt_inverse;   // ceil(2^32 / block tokens): a token's block, or one more
     float *part;           // [CTAs][2] partial results
-    int32_t *count;        // [CTAs] arrivals at units that start in the CTA, zero between calls
+    Joins joins;           // a word per CTA: the unit that starts there and goes on in others
 };
 
 // Tiles of sequence s: tiles per unit, units per KV head.
@@ -185,6 +185,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     __shared__ uint64_t s_full[NS], s_empty[NS], s_merge[3];
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ int s_abort, s_last;
+    __shared__ uint64_t s_launch;               // tid 0's
     __shared__ float s_row[2][kMaxRows];
 
     const AttendArgs &a = p.a;
@@ -203,9 +204,13 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
     griddep_wait();
     griddep_launch_dependents();
-    if (tid == 0 && (int32_t)blockIdx.x == a.give_up) {
-        set_status(status, SLORA_DEV_TIMEOUT);
-        s_abort = 1;
+    uint64_t started = 0;
+    if (tid == 0) {
+        started = start_launch(p.joins, blockIdx.x == 0, gridDim.x);
+        if ((int32_t)blockIdx.x == a.give_up) {
+            set_status(status, SLORA_DEV_TIMEOUT);
+            s_abort = 1;
+        }
     }
 
     // Tiles of each run of `per` sequences; every CTA sums them for itself, which costs less
@@ -578,6 +583,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
 
     // ---- consumers ---------------------------------------------------------------------
+    if (tid == 0) s_launch = started;
     const int g = lane >> 2, c = lane & 3;
     const int krow[2] = {token_of_row<D>(g), token_of_row<D>(g) + 8};
     // the tokens of this lane's two rows of V^T P^T's inner index, in both halves of the 16
@@ -861,8 +867,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (!meet(1)) break;
             if (tid == 0) {
                 __threadfence();
-                s_last = atomicAdd(&p.count[c0], 1) == c1 - c0;
-                if (s_last) p.count[c0] = 0;
+                s_last = arrive_last(p.joins.word + c0, s_launch, c1 - c0 + 1);
                 __threadfence();
                 mbar_arrive(&s_merge[2]);
             }
@@ -960,7 +965,7 @@ cudaError_t launch_d(const DecodeParams &p, const PageMaps &maps, int fmt, int n
 size_t decode_workspace_bytes(int num_sms)
 {
     const size_t ctas = (size_t)num_sms * kMaxCtas;
-    return (ctas * 2 * kPartStride * 4 + ctas * 4 + 255) / 256 * 256;
+    return (ctas * 2 * kPartStride * 4 + (ctas + 1) * 8 + 255) / 256 * 256;
 }
 
 cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int head_dim, int fmt,
@@ -980,7 +985,8 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
     p.min_tiles = 1 + kUnitCost;
     p.bt_inverse = (uint32_t)(((1ull << 32) + a.c.bt - 1) / a.c.bt);
     p.part = static_cast<float *>(ws);
-    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * kMaxCtas * 2 * kPartStride);
+    p.joins.started = reinterpret_cast<unsigned long long *>(p.part + (size_t)num_sms * kMaxCtas * 2 * kPartStride);
+    p.joins.word = p.joins.started + 1;
     cudaError_t e = head_dim == 128 ? launch_d<128>(p, maps, fmt, num_sms, stream)
                                     : launch_d<64>(p, maps, fmt, num_sms, stream);
     if (e == cudaSuccess) ++*launches;

@@ -97,7 +97,7 @@ struct PrefillParams {
     float scale;           // softmax scale * log2(e), not zero
     uint32_t unseen;       // what a product must be for a score of -infinity
     float *part;           // [CTAs][2][2] partial results
-    int32_t *count;        // [CTAs][2]
+    Joins joins;           // a word per CTA and row tile
 };
 
 __device__ __forceinline__ float ex2(float x)
@@ -201,6 +201,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     __shared__ uint64_t s_qfull, s_qempty, s_sfull[2], s_pfull[2], s_odone[2], s_ofree[2], s_join[2], s_said[2], s_turn[2], s_fin, s_unit;
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
+    __shared__ uint64_t s_launch;
     __shared__ int s_abort, s_last[2];
 
     const AttendArgs &a = p.a;
@@ -233,6 +234,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     }
     griddep_wait();
     griddep_launch_dependents();
+    uint64_t started = 0;
+    if (tid == 32 * kPlanWarp) started = start_launch(p.joins, blockIdx.x == 0, gridDim.x);
     if (tid == 0 && (int32_t)blockIdx.x == a.give_up) {
         set_status(status, SLORA_DEV_TIMEOUT);
         s_abort = 1;
@@ -516,7 +519,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (ok != 0xFFFFu) d.flags &= ~kPlain;
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&s_tfull[i < 0 ? 0 : i % kDescs]);
+            if (lane == 0) {
+                if (i < 0) s_launch = started;          // with the first tile
+                mbar_arrive(&s_tfull[i < 0 ? 0 : i % kDescs]);
+            }
         }
     } else if (warp == kMmaWarp || warp == kMmaWarp1) {
         // ---- products of one row tile -------------------------------------------------------
@@ -966,10 +972,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (!wait_bar(&s_join[t], j_par, abort, status)) break;
                 if (row == 0) {
                     __threadfence();
-                    int32_t *cnt = p.count + 2 * c0 + t;
-                    const int l = atomicAdd(cnt, 1) == c1 - c0;
-                    if (l) *cnt = 0;
-                    s_last[t] = l;
+                    s_last[t] = arrive_last(p.joins.word + 2 * c0 + t, s_launch, c1 - c0 + 1);
                     __threadfence();
                     mbar_arrive(&s_said[t]);
                 }
@@ -1089,7 +1092,7 @@ cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
 
 size_t prefill_workspace_bytes(int num_sms)
 {
-    return (size_t)num_sms * 4 * Shape<128>::kPart * 4 + (size_t)num_sms * 2 * 4;
+    return (size_t)num_sms * 4 * Shape<128>::kPart * 4 + ((size_t)num_sms * 2 + 1) * 8;
 }
 
 cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, int32_t small_rows, void *ws, int num_sms,
@@ -1107,7 +1110,8 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, in
     if (p.scale < 0x1p-60f && p.scale > -0x1p-60f) p.scale = 0x1p-60f;
     p.unseen = p.scale < 0.f ? 0x7F800000u : 0xFF800000u;
     p.part = static_cast<float *>(ws);
-    p.count = reinterpret_cast<int32_t *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
+    p.joins.started = reinterpret_cast<unsigned long long *>(p.part + (size_t)num_sms * 4 * Shape<128>::kPart);
+    p.joins.word = p.joins.started + 1;
     cudaError_t e;
     if (head_dim == 128)
         e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, num_sms, stream);

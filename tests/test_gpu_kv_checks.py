@@ -213,3 +213,55 @@ def test_a_cta_that_gives_up_ends_and_reports_it(give_up, kind, hidden, d):
     assert np.array_equal(out, want) and c.s.device_status() == 0
     with pytest.raises(rdp.SloraError):
         give_up(-2)
+
+
+SPLIT = {"stream": [(1, 100011), (1, 3), (1, 40001)], "stream16": [(3, 100011), (2, 60345)], "prompts": [(140, 9001), (1, 3), (200, 6000)]}
+
+
+@pytest.mark.parametrize("kind", SPLIT)
+@pytest.mark.parametrize("graph", [False, True])
+def test_calls_after_a_cta_gave_up_join_their_parts_as_ever(give_up, kind, graph):
+    """Units cut between many CTAs.  One that gives up never arrives at its unit's join; what it leaves there does not
+    reach a later call, eager or replayed from a graph, with other queries or lengths and so another split."""
+    c = Case(SPLIT[kind], hq=4, hkv=1, seed=46)
+    row = c.hq * c.d
+    longer = c.batch()                                    # what gives up: the full lengths
+    c.kv_len = np.array([n if n < 1000 else n * 5 // 8 for n in c.kv_len], np.int32)
+    c.d_len = dev(c.kv_len)
+    qs, wants = [], []
+    for _ in range(4):
+        c.q = c.rng.normal(0, 1, c.q.shape).astype(np.float16)
+        qs.append(half(c.q).view(-1, row))
+        wants.append(c.attend())
+    q, b = torch.zeros_like(qs[0]), c.batch()
+    out, lse = torch.zeros((c.T, row), dtype=torch.float16, device="cuda"), torch.zeros((c.T, c.hq), device="cuda")
+    st = torch.cuda.Stream()
+
+    def calls(batch):
+        """What runs one call: the call itself, or a graph of it."""
+        run = lambda: rdp.slora_kv_attend(c.s.kv, batch, q, row, c.hq, out, row, lse, 0.5 / np.sqrt(c.d), True, 0, st)  # noqa: E731
+        if not graph:
+            return run
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g, stream=st):
+            run()
+        return g.replay
+
+    good, n = calls(b), 0
+    for cta in (0, 1, 50, 149, 303):
+        for batch in (longer, b):
+            give_up(cta)
+            calls(batch)()
+            torch.cuda.synchronize()
+            give_up(-1)
+            c.s.device_status()                           # TIMEOUT where a grid has this CTA
+            for _ in range(4):
+                n += 1
+                q.copy_(qs[n % 4])
+                out.fill_(7)
+                torch.cuda.synchronize()
+                good()
+                torch.cuda.synchronize()
+                assert np.array_equal(out.float().cpu().numpy().reshape(c.q.shape), wants[n % 4][0])
+                assert np.array_equal(lse.cpu().numpy(), wants[n % 4][1])
+            assert c.s.device_status() == 0
