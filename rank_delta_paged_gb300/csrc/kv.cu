@@ -84,9 +84,10 @@ slora_status check_batch(const char *fn, slora_kv_t k, const slora_kv_batch *b, 
     return SLORA_OK;
 }
 
-slora_status check_rows(const char *fn, const char *what, const void *p, int64_t stride, int64_t row)
+// `none`: the call has no rows, and the pointer (that of an empty tensor is null) is not looked at.
+slora_status check_rows(const char *fn, const char *what, const void *p, int64_t stride, int64_t row, bool none)
 {
-    if (!p || !aligned16(p) || stride % 8 != 0 || stride < row)
+    if ((!none && (!p || !aligned16(p))) || stride % 8 != 0 || stride < row)
         return fail(SLORA_ERR_INVALID_ARG, "%s: %s is null or misaligned, or its stride %lld is below %lld or no multiple of 8",
                     fn, what, (long long)stride, (long long)row);
     return SLORA_OK;
@@ -190,18 +191,19 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
     slora_status st = check_batch(fn, k, batch, &a.b);
     if (st != SLORA_OK)
         return st;
+    const bool none = a.b.T == 0 || a.b.S == 0;
     const int64_t row = (int64_t)k->c.n_kv * k->head_dim;
-    if ((st = check_rows(fn, "k", kk, k_stride, row)) != SLORA_OK ||
-        (st = check_rows(fn, "v", v, v_stride, row)) != SLORA_OK)
+    if ((st = check_rows(fn, "k", kk, k_stride, row, none)) != SLORA_OK ||
+        (st = check_rows(fn, "v", v, v_stride, row, none)) != SLORA_OK)
         return st;
-    if ((q == nullptr) != (q_out == nullptr) || (q && !rope))
+    if ((!none && (q == nullptr) != (q_out == nullptr)) || (q && !rope))
         return fail(SLORA_ERR_INVALID_ARG, "%s: q needs q_out and rope", fn);
     if (q) {
         if (n_q_heads < 1 || n_q_heads > 8192)
             return fail(SLORA_ERR_INVALID_ARG, "%s: n_q_heads=%d", fn, n_q_heads);
         const int64_t qrow = (int64_t)n_q_heads * k->head_dim;
-        if ((st = check_rows(fn, "q", q, q_stride, qrow)) != SLORA_OK ||
-            (st = check_rows(fn, "q_out", q_out, q_out_stride, qrow)) != SLORA_OK)
+        if ((st = check_rows(fn, "q", q, q_stride, qrow, none)) != SLORA_OK ||
+            (st = check_rows(fn, "q_out", q_out, q_out_stride, qrow, none)) != SLORA_OK)
             return st;
         a.q = static_cast<const __half *>(q);
         a.q_out = static_cast<__half *>(q_out);
@@ -222,7 +224,7 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
         a.sin = rope->sin;
         a.positions = rope->positions;
     }
-    if (a.b.T == 0 || a.b.S == 0)
+    if (none)
         return SLORA_OK;
     a.c = k->c;
     a.k = static_cast<const __half *>(kk);
@@ -249,21 +251,22 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
         return st;
     if (n_q_heads < 1 || n_q_heads > 8192 || n_q_heads % k->c.n_kv != 0)
         return fail(SLORA_ERR_INVALID_ARG, "%s: n_q_heads=%d is no multiple of the cache's %d", fn, n_q_heads, k->c.n_kv);
+    const bool none = a.b.T == 0 || a.b.S == 0;
     const int64_t row = (int64_t)n_q_heads * k->head_dim;
-    if ((st = check_rows(fn, "q", q, q_stride, row)) != SLORA_OK ||
-        (st = check_rows(fn, "out", out, out_stride, row)) != SLORA_OK)
+    if ((st = check_rows(fn, "q", q, q_stride, row, none)) != SLORA_OK ||
+        (st = check_rows(fn, "out", out, out_stride, row, none)) != SLORA_OK)
         return st;
     const int32_t group = n_q_heads / k->c.n_kv;
     if ((int64_t)a.b.max_q * group > 1 << 30)
         return fail(SLORA_ERR_UNSUPPORTED, "%s: %d new tokens of %d query heads per KV head", fn, a.b.max_q, group);
-    if (out == q)
+    if (!none && out == q)
         return fail(SLORA_ERR_INVALID_ARG, "%s: out is q", fn);
     if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) || !std::isfinite(softmax_scale))
         return fail(SLORA_ERR_INVALID_ARG, "%s: causal=%d window=%d softmax_scale=%g", fn, causal, window,
                     (double)softmax_scale);
     if (((uintptr_t)lse & 3) != 0)
         return fail(SLORA_ERR_INVALID_ARG, "%s: lse is misaligned", fn);
-    if (a.b.T == 0 || a.b.S == 0)
+    if (none)
         return SLORA_OK;
     a.c = k->c;
     a.q = static_cast<const __half *>(q);

@@ -265,3 +265,31 @@ def test_calls_after_a_cta_gave_up_join_their_parts_as_ever(give_up, kind, graph
                 assert np.array_equal(out.float().cpu().numpy().reshape(c.q.shape), wants[n % 4][0])
                 assert np.array_equal(lse.cpu().numpy(), wants[n % 4][1])
             assert c.s.device_status() == 0
+
+
+def test_a_batch_without_tokens_or_sequences_needs_no_rows():
+    """An empty tensor has no address; the scalar arguments are still checked."""
+    c = Case([(1, 10), (2, 20)], hq=4, hkv=2, seed=48)
+    z = lambda *shape: torch.empty(shape, dtype=torch.float16, device="cuda")  # noqa: E731
+    zi = lambda *shape: torch.empty(shape, dtype=torch.int32, device="cuda")  # noqa: E731
+    q, k, tab = z(0, 512), z(0, 256), torch.zeros((32, 64), device="cuda")
+    assert q.data_ptr() == 0
+    before = c.s.pages.clone()
+    for b in (rdp.KVBatch(0, 0, 1, 1, zi(0), zi(0), zi(0, 1, 2, 2)), rdp.KVBatch(0, 2, 3, c.max_blocks, c.d_indptr, c.d_len, c.d_table),
+              rdp.KVBatch(3, 0, 1, 1, None, None, None)):
+        for lse in (None, torch.empty((0, 4), device="cuda")):
+            rdp.slora_kv_attend(c.s.kv, b, q, 512, 4, q, 512, lse)
+        rdp.slora_kv_append(c.s.kv, b, k, 256, k, 256)
+        for q_out in (q, z(4, 512)):
+            for pos in (None, zi(0)):
+                rdp.slora_kv_append(c.s.kv, b, k, 256, k, 256, q, 512, q_out, 512, 4, rdp.KVRope(128, 0, 32, tab, tab, pos))
+        for bad in (dict(hq=3), dict(qs=504), dict(os=516), dict(window=-1)):
+            a = dict(hq=4, qs=512, os=512, window=0)
+            a.update(bad)
+            with pytest.raises(rdp.SloraError) as e:
+                rdp.slora_kv_attend(c.s.kv, b, q, a["qs"], a["hq"], q, a["os"], window=a["window"])
+            assert e.value.status == 1
+        with pytest.raises(rdp.SloraError) as e:
+            rdp.slora_kv_append(c.s.kv, b, k, 248, k, 256)
+        assert e.value.status == 1
+    assert torch.equal(before, c.s.pages) and c.s.device_status() == 0
