@@ -500,8 +500,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *                the values (1) of each block and head.  Entries of blocks that a call does not
  *                touch are not read (they may be -1).  Sequences may share pages that are
  *                only read.
- * Tokens of rows outside every sequence, and of a sequence that is skipped, are not computed:
- * their rows of q_out, out and lse are unspecified.
+ * Tokens of rows outside every sequence, and of a sequence that is skipped, are not computed: their
+ * rows of q_out, out and lse are not written, and their positions (below) may be anything.
  *
  * slora_kv_append(): writes the new tokens' keys and values to the cache, rotating queries
  * and keys by their positions on the way.  Scales: a block's exponent is the smallest

@@ -296,6 +296,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
+    const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
     // as append_kernel
     griddep_launch_dependents();
     const int32_t per = (a.n_q + kQHeads - 1) / kQHeads;
@@ -306,25 +307,26 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
         const int64_t i = i0 + grp;
         const bool live = i < total;
         const int32_t t = live ? (int32_t)(i / per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
-        bool mine = live;
-        int32_t pos = 0;
-        if (a.positions) {
-            if (live) pos = a.positions[t];
-        } else {
-            int32_t lo = 0, hi = a.b.S - 1;      // last sequence that starts at or before t
-            while (lo < hi) {
-                const int32_t mid = (lo + hi + 1) / 2;
-                if (a.b.indptr[mid] <= t) lo = mid; else hi = mid - 1;
-            }
-            const int32_t end = a.b.indptr[lo + 1];
-            mine = live && a.b.indptr[lo] <= t && t < end;
-            if (mine) pos = a.b.kv_len[lo] - end + t;
-        }
         uint4 v[kQHeads];
 #pragma unroll
         for (int k = 0; k < kQHeads; ++k)
-            if (mine && h0 + k < a.n_q)
+            if (live && h0 + k < a.n_q)
                 v[k] = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D + ch * 8);
+        int32_t pos = a.positions && live ? a.positions[t] : 0;
+        // rows outside every sequence, and those of a sequence that is skipped, are left alone
+        int32_t lo = 0, n = a.b.S;               // the last of n from lo that starts at or before t, a lane per part of them
+#pragma unroll 1
+        while (__any_sync(~0u, n > 1)) {
+            const int32_t step = (n + LPR - 1) / LPR;
+            const bool before = ch * step < n && a.b.indptr[lo + ch * step] <= t;
+            const int k = __popc(__ballot_sync(~0u, before) & row_lanes);
+            if (k > 1) lo += (k - 1) * step, n -= (k - 1) * step;
+            if (n > step) n = step;
+        }
+        const int32_t begin = a.b.indptr[lo], end = a.b.indptr[lo + 1], len = a.b.kv_len[lo];
+        const bool mine = live && begin >= 0 && begin <= t && t < end && end <= a.b.T && end - begin <= a.b.max_q &&
+                          len >= end - begin && !too_long(a.c, a.b, len);
+        if (mine && !a.positions) pos = len - end + t;
         Rot r;
         r.on = false;
         if (mine) load_rot(a, pos, ch, r);

@@ -293,3 +293,58 @@ def test_a_batch_without_tokens_or_sequences_needs_no_rows():
             rdp.slora_kv_append(c.s.kv, b, k, 248, k, 256)
         assert e.value.status == 1
     assert torch.equal(before, c.s.pages) and c.s.device_status() == 0
+
+
+def rotate_with_padding(seqs, pad, in_place, given, bad=None, max_q=None):
+    """Appends with `pad` spare rows before and behind the sequences' rows; returns the case, q, q_out, the rows that
+    the sequences have, and the status."""
+    c = Case(seqs, hq=6, hkv=2, seed=49)
+    T = c.T + 2 * pad
+    rng = np.random.default_rng(5)
+    q = rng.normal(0, 1, (T, 6 * 128)).astype(np.float16)
+    k = torch.from_numpy(rng.normal(0, 1, (T, 256)).astype(np.float16)).cuda()
+    n_pos = int(c.kv_len.max()) + 1
+    angle = np.arange(n_pos)[:, None] * 10000.0 ** (-np.arange(0, 128, 2) / 128)
+    cos, sin = np.cos(angle).astype(np.float32), np.sin(angle).astype(np.float32)
+    pos = np.full(T, -1, np.int32)
+    rows = pad + np.arange(c.T)
+    pos[rows] = np.concatenate([np.arange(n - m, n) for m, n in seqs])
+    if bad is not None:                                  # a skipped sequence: its positions are nobody's
+        mine = rows[c.indptr[bad]:c.indptr[bad + 1]]
+        c.kv_len[bad] = c.max_blocks * c.bt + 1
+        c.d_len = dev(c.kv_len)
+        pos[mine] = 1 << 30
+        rows = np.setdiff1d(rows, mine)
+    dq = torch.from_numpy(q).cuda()
+    out = dq if in_place else torch.full_like(dq, 7.0)
+    kept = out.cpu().numpy().copy()
+    b = rdp.KVBatch(T, len(seqs), max_q or max(m for m, _ in seqs), c.max_blocks, dev(c.indptr + pad), c.d_len, c.d_table)
+    rope = rdp.KVRope(128, False, n_pos, dev(cos), dev(sin), dev(pos) if given else None)
+    rdp.slora_kv_append(c.s.kv, b, k, 256, k, 256, dq, 768, out, 768, 6, rope)
+    status = c.s.device_status()
+    got = out.cpu().numpy()
+    want = R.rotate(q.reshape(T, 6, 128)[rows], cos[pos[rows]], sin[pos[rows]], False, np.float32).astype(np.float16)
+    assert np.array_equal(got[rows].reshape(want.shape).view(np.uint16), want.view(np.uint16))
+    other = np.setdiff1d(np.arange(T), rows)
+    assert np.array_equal(got[other].view(np.uint16), kept[other].view(np.uint16))
+    return status
+
+
+SINGLE, SEVERAL = [(1, 30), (0, 9), (1, 65), (1, 1)], [(5, 30), (0, 9), (1, 65), (70, 70), (0, 0)]
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("seqs", [SINGLE, SEVERAL, SEVERAL * 90], ids=["single", "several", "many"])
+def test_rows_outside_every_sequence_are_left_alone(seqs, in_place, given):
+    """A padded batch: spare rows before and behind the sequences, whose positions are -1."""
+    assert rotate_with_padding(seqs, 11, in_place, given) == 0
+    assert rotate_with_padding(seqs, 0, in_place, given) == 0
+    assert rotate_with_padding(seqs, 3, in_place, given, max_q=1 << 20) == 0
+
+
+@pytest.mark.parametrize("given", [False, True])
+@pytest.mark.parametrize("seqs", [SINGLE, SEVERAL], ids=["single", "several"])
+def test_rows_of_a_skipped_sequence_are_left_alone(seqs, given):
+    assert rotate_with_padding(seqs, 2, False, given, bad=0) == BAD_LENGTH
+    assert rotate_with_padding(seqs, 2, True, given, bad=3) == BAD_LENGTH
