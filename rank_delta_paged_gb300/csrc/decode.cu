@@ -894,8 +894,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_kernel(const __grid_constan
     // waits later (see DeltaArgs::plan_ready)
     const bool lead_early = a.plan_ready != 0 && warp == kWarpLead;
     const bool copy_early = a.plan_ready != 0 && warp >= kWarpCopy0 && warp < kWarpCopy0 + kCopyWarps;
-    if (!lead_early && !copy_early) griddep_wait();
-    griddep_launch_dependents();
+    // Only warps that have waited let the next kernel start: the segment kernel reads x without a wait of its
+    // own (see its top), and what wrote x, the kernel before this one, may have let this one start early.
+    if (!lead_early && !copy_early) {
+        griddep_wait();
+        griddep_launch_dependents();
+    }
     const int n_units = __ldcg(&a.L.hdr->n_units);
 
     // read record k's header (every reader walks the records in order); false at the end
