@@ -713,13 +713,14 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 }
         }
         // A row's maximum is taken up only when a score passes it by 2^8 (the first one always does):
-        // the weights stay below 2^8, far inside fp16, and the rescaling of O is rare.
+        // the weights stay below 2^8, far inside fp16, and the rescaling of O is rare.  The difference of the
+        // two is exact where it decides; a sum with 2^8's exponent need not be.
         bool up = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                up |= fmaxf(sc[t][x], sc[t][2 + x]) > mx[t][x] + 8.f;
+                up |= fmaxf(sc[t][x], sc[t][2 + x]) - mx[t][x] > 8.f;
         if (__any_sync(~0u, up)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)

@@ -348,3 +348,26 @@ def test_rows_outside_every_sequence_are_left_alone(seqs, in_place, given):
 def test_rows_of_a_skipped_sequence_are_left_alone(seqs, given):
     assert rotate_with_padding(seqs, 2, False, given, bad=0) == BAD_LENGTH
     assert rotate_with_padding(seqs, 2, True, given, bad=3) == BAD_LENGTH
+
+
+@pytest.mark.parametrize("n,group", [(1, 1), (3, 4), (140, 2)])
+@pytest.mark.parametrize("power", range(8, 16))
+def test_attend_scores_whose_steps_are_the_rescaling_s(n, group, power):
+    """Scores of 2^(power + 15) and their neighbours in fp32, 2^(power - 8) apart, each block one step above the last:
+    no weight passes fp16's range whatever the rounding of the sums that decide about it."""
+    c = Case([(n, 900)], hq=2 * group, hkv=2, seed=52, stale=False)
+    c.q[:] = 0
+    c.q[:, :, 0], c.q[:, :, 1] = 2.0 ** 15, 2.0 ** -8
+    steps = torch.arange(1, 17).float().to(torch.float8_e4m3fn).view(torch.uint8).numpy()
+    for b in range(-(-900 // c.bt)):
+        for h in range(2):
+            kp, vp = c.table[0, b, h]
+            k, v = (c.pages[p, :c.bt * c.d].reshape(c.bt, c.d) for p in (kp, vp))
+            k[:] = 0
+            k[:, 0], k[:, 1] = 0x38, steps[b]                      # 1, and the step
+            v[:] = 0x7E                                            # 448
+            c.exps[kp] = c.exps[vp] = 0
+    c.push()
+    out, lse = c.attend(scale=float(2.0 ** power * np.log(2)))
+    assert c.s.device_status() == 0
+    assert np.abs(out - 448).max() <= 0.5 and np.isfinite(lse).all()
