@@ -24,6 +24,14 @@ constexpr int kMinExponent = -40;
 // ratio of two scales.
 constexpr int kExpLimit = 60;
 
+// The softmax's weights are rounded to fp16 for the product with the values, so they stand high in its range: a
+// reference m is taken kHeadRoom below the largest score, and kept until weights would pass
+// 2^kMaxWeight (fp16 ends at 2^16).  A weight keeps its 11 bits down to 2^-21 of the largest and is lost below
+// 2^-32 of it; with m at the largest score itself those were 2^-14 and 2^-25, and a key that held
+// most of the softmax made the rest's weights coarse (errors of 1 part in 100 in their sum).
+constexpr float kHeadRoom = 7.f;
+constexpr float kMaxWeight = 15.f;
+
 struct Cache {
     uint8_t *pool;          // page p starts at pool + p * page_bytes
     int8_t *exps;           // [num_pages]

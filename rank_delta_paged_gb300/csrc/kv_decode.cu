@@ -712,15 +712,14 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     if (!(ok1 && j1 >= lo && j1 < hi)) sc[t][2 + x] = -INFINITY;
                 }
         }
-        // A row's maximum is taken up only when a score passes it by 2^8 (the first one always does):
-        // the weights stay below 2^8, far inside fp16, and the rescaling of O is rare.  The difference of the
-        // two is exact where it decides; a sum with 2^8's exponent need not be.
+        // A row's reference is taken up only when a score passes it by kMaxWeight (the first one always
+        // does), so the rescaling of O is rare.  The difference of the two is exact where it decides.
         bool up = false;
 #pragma unroll
         for (int t = 0; t < NT; ++t)
 #pragma unroll
             for (int x = 0; x < 2; ++x)
-                up |= fmaxf(sc[t][x], sc[t][2 + x]) - mx[t][x] > 8.f;
+                up |= fmaxf(sc[t][x], sc[t][2 + x]) - mx[t][x] > kMaxWeight;
         if (__any_sync(~0u, up)) {
 #pragma unroll
             for (int t = 0; t < NT; ++t)
@@ -730,7 +729,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 4));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 8));
                     v = fmaxf(v, __shfl_xor_sync(~0u, v, 16));
-                    v = fmaxf(v, mx[t][x]);
+                    v = fmaxf(v - kHeadRoom, mx[t][x]);
                     const float k = mx[t][x] == -INFINITY ? 0.f : ex2(mx[t][x] - v);
                     mx[t][x] = v;
                     sum[t][x] *= k;

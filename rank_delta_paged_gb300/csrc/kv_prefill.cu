@@ -813,12 +813,12 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                         tc::ld_wait(x);
                         top = fmaxf(top, top_of(d, x, h));
                     }
-                    if (mx == -INFINITY) mx = top;
+                    if (mx == -INFINITY) mx = top - kHeadRoom;
                 }
                 // The weights, 32 keys at a time, by the running maximum as it stands.  It follows only when the
-                // 32 weights' sum passes 2^8 (fp16 ends at 2^16), to the largest score itself: a key
-                // that outweighs all others then has the weight 1, which fp16 holds exactly (an integer above
-                // it made the outputs' error 2.9e-4 of their norm instead of 2.3e-4).  What this tile's
+                // 32 weights' sum passes 2^kMaxWeight, to kHeadRoom below the largest score itself: a key
+                // that outweighs all others then has the weight 2^7, which fp16 holds exactly (an integer above
+                // its score made the outputs' error 2.9e-4 of their norm instead of 2.3e-4).  What this tile's
                 // earlier keys made with the old one is rounded a second time.
                 uint32_t xa[16], xb[16], pk[16];
                 float raw, add, base = mx == -INFINITY ? 0.f : mx;
@@ -856,11 +856,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     tc::ld_wait(xb);
                     tc::ld_32x32b_x16(ts + (32 * (h + 1) & 127), xa);      // (not used after the last)
                     weigh(xb, 2 * h + 1, 8);
-                    const bool up = raw > 256.f;
+                    const bool up = raw > 32768.f;
                     if (__builtin_expect(__any_sync(~0u, up), 0)) {
                         tc::ld_32x32b_x32(ts + 32 * h, x);
                         tc::ld_wait(x);
-                        const float nm = up ? top_of(d, x, h) : mx;
+                        const float nm = up ? top_of(d, x, h) - kHeadRoom : mx;
                         const float k = mx == nm ? 1.f : ex2(mx - nm);
                         mx = nm;
                         base = mx == -INFINITY ? 0.f : mx;
@@ -875,21 +875,28 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                                 for (int j = 0; j < 16; ++j) y[j] = __float_as_uint(__uint_as_float(y[j]) * k);
                                 tc::st_32x32b_x16(to + 16 * c, y);
                             }
-                        const __half2 kh = __float2half2_rn(k);
+                        // in two steps where k is so small that fp16 has few bits of it
+                        float part = fmaxf(k, 0x1p-13f);
 #pragma unroll 1
-                        for (int c = 0; c < h; ++c) {
-                            tc::ld_32x32b_x16(ts + 16 * c, y);
-                            tc::ld_wait(y);
+                        for (int e = 0; e < 2; ++e) {
+                            const __half2 kh = __float2half2_rn(part);
+#pragma unroll 1
+                            for (int c = 0; c < h; ++c) {
+                                tc::ld_32x32b_x16(ts + 16 * c, y);
+                                tc::ld_wait(y);
 #pragma unroll
-                            for (int j = 0; j < 16; ++j) {
-                                __half2 w = __hmul2(*reinterpret_cast<__half2 *>(&y[j]), kh);
-                                y[j] = *reinterpret_cast<uint32_t *>(&w);
+                                for (int j = 0; j < 16; ++j) {
+                                    __half2 w = __hmul2(*reinterpret_cast<__half2 *>(&y[j]), kh);
+                                    y[j] = *reinterpret_cast<uint32_t *>(&w);
+                                }
+                                tc::st_32x32b_x16(ts + 16 * c, y);
                             }
-                            tc::st_32x32b_x16(ts + 16 * c, y);
+                            tc::st_wait();
+                            if (__all_sync(~0u, k >= 0x1p-13f)) break;
+                            part = fminf(k * 0x1p13f, 1.f);
                         }
-                        tc::st_wait();
                         // these 32 again, from scores rounded as the maximum was, so that no weight
-                        // is above 1 however large they are
+                        // is above 2^8 however large they are
                         add = 0.f;
 #pragma unroll
                         for (int j = 0; j < 32; j += 2) {

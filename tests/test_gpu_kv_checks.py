@@ -350,6 +350,45 @@ def test_rows_of_a_skipped_sequence_are_left_alone(seqs, given):
     assert rotate_with_padding(seqs, 2, True, given, bad=3) == BAD_LENGTH
 
 
+def dominated(n, length, at, below, fmt, page_exponent, hkv, group):
+    """A cache whose key at position `at` outweighs every other by 2^(below - 1) to 2^below and has the value 0, so that the
+    outputs are made of the others alone; its value page's scale is 2^page_exponent of the others'."""
+    c = Case([(n, length)], hq=hkv * group, hkv=hkv, fmt=fmt, seed=51)
+    sixteen = {"e4m3": 0x58, "int8": 16}[fmt]
+    small = np.array([0, 8, 12, 16])                       # 0 to 1 in units of 2^-4
+    codes = np.array([0, 0x50, 0x54, 0x58] if fmt == "e4m3" else small, np.uint8)
+    c.q[:] = 0
+    c.q[:, :, 0], c.q[:, :, 1] = 1, below
+    for b in range(-(-length // c.bt)):
+        for h in range(hkv):
+            kp, vp = c.table[0, b, h]
+            k, v = (c.pages[p, :c.bt * c.d].reshape(c.bt, c.d) for p in (kp, vp))
+            k[:] = 0
+            k[:, 0] = codes[c.rng.integers(0, 4, c.bt)]
+            c.exps[kp], c.exps[vp] = -4, 0
+            if b == at // c.bt:
+                k[at % c.bt, :2] = 0, sixteen
+                c.exps[vp] = page_exponent
+                v[:] = 0
+                if at == 0:                                # one for each warp of the streaming kernel
+                    k[16:64:16] = k[0]
+            else:                                          # of one sign, so that errors add up
+                v[:] = v & 0x7F if fmt == "e4m3" else np.abs(v.view(np.int8)).view(np.uint8)
+                v[v == 0x7F] = 0x7E
+    c.push()
+    return c
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("n,group", [(1, 1), (3, 4), (140, 2)])
+@pytest.mark.parametrize("at", [0, 700, 1300])
+@pytest.mark.parametrize("below,page_exponent", [(4, 0), (11.3, 0), (15.3, 0), (20.3, 0), (9.3, 11), (20.3, -9)])
+def test_attend_keys_beside_one_that_outweighs_them(fmt, n, group, at, below, page_exponent):
+    """The rest of the softmax keeps its bits: each key's weight is within fp16's rounding of its value, although it is
+    2^-20 of the largest."""
+    dominated(n, 1500, at, below, fmt, page_exponent, 2, group).check(scale=float(np.log(2)))
+
+
 @pytest.mark.parametrize("n,group", [(1, 1), (3, 4), (140, 2)])
 @pytest.mark.parametrize("power", range(8, 16))
 def test_attend_scores_whose_steps_are_the_rescaling_s(n, group, power):
