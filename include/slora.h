@@ -493,7 +493,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *                it is skipped)
  *   max_blocks   width of the block table, 1 or more
  *   tok_indptr   device int32 [S + 1]: sequence s's new tokens are rows
- *                tok_indptr[s] .. tok_indptr[s+1]-1, in order (none: the sequence is skipped)
+ *                tok_indptr[s] .. tok_indptr[s+1]-1, in order (none: the sequence is skipped,
+ *                whatever its length and block table hold)
  *   kv_len       device int32 [S]: the sequence's length with its new tokens; they stand at
  *                positions kv_len[s] - n .. kv_len[s] - 1 of the cache
  *   block_table  device int32 [S][max_blocks][n_kv_heads][2]: the pages of the keys (0) and

@@ -105,7 +105,7 @@ __device__ __forceinline__ Seq load_seq(const AttendArgs &a, int32_t s, int32_t 
     if (t0 < 0 || t1 < t0 || t1 > a.b.T || q.n > a.b.max_q) {
         *bad = SLORA_DEV_BAD_SEGMENT;
         q.n = 0;
-    } else if (q.len < 0 || too_long(a.c, a.b, q.len)) {
+    } else if (q.n > 0 && (q.len < 0 || too_long(a.c, a.b, q.len))) {
         *bad = SLORA_DEV_BAD_LENGTH;
         q.n = 0;
     }

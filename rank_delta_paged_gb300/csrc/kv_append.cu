@@ -204,7 +204,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
     int32_t bad = 0;
     if (t0 < 0 || t1 < t0 || t1 > a.b.T || t1 - t0 > a.b.max_q)
         bad = SLORA_DEV_BAD_SEGMENT;
-    else if (len < t1 - t0 || too_long(a.c, a.b, len))
+    else if (t1 > t0 && (len < t1 - t0 || too_long(a.c, a.b, len)))
         bad = SLORA_DEV_BAD_LENGTH;
     if (bad) {
         if (tid == 0) set_status(a.c.status, bad);

@@ -410,3 +410,22 @@ def test_attend_scores_whose_steps_are_the_rescaling_s(n, group, power):
     out, lse = c.attend(scale=float(2.0 ** power * np.log(2)))
     assert c.s.device_status() == 0
     assert np.abs(out - 448).max() <= 0.5 and np.isfinite(lse).all()
+
+
+@pytest.mark.parametrize("seqs", [[(1, 70), (0, 40), (1, 9), (0, 5)], [(0, 9), (9, 70), (0, 40), (130, 200), (1, 7), (0, 0)]],
+                         ids=["single", "several"])
+def test_sequences_without_new_tokens_may_hold_anything(seqs):
+    """Spare places of a padded batch: their lengths and pages are not looked at."""
+    c = Case(seqs, hq=8, hkv=2, seed=53)
+    want, wl = c.attend()
+    _, pages, exps = append_ones(c)
+    spare = [s for s, (n, _) in enumerate(seqs) if n == 0]
+    for length in (-1, -(1 << 31), (1 << 31) - 1, c.max_blocks * c.bt + 1):
+        c.kv_len[spare] = length
+        c.table[spare] = 1 << 30
+        c.push()
+        out, lse = c.attend()
+        assert c.s.device_status() == 0
+        assert np.array_equal(out, want) and np.array_equal(lse, wl)
+        status, got, ge = append_ones(c)
+        assert status == 0 and np.array_equal(got, pages) and np.array_equal(ge, exps)
