@@ -535,8 +535,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   window       0, or with causal 1: it sees positions p - window + 1 .. p only
  * A token that sees nothing gets zeros and lse -inf.  Cache rows that no new token of the
  * sequence sees may hold anything (their codes are never used, and pages wholly outside are
- * not read).  A NaN among the values that one new token sees can reach the sequence's other
- * new tokens of the call, whose weight for it is 0.  Scores, the softmax's maxima and sums
+ * not read).  A NaN among the values reaches, in its channel, the tokens that see it and no others.
+ * Scores, the softmax's maxima and sums
  * and the output sums are fp32; the weights are rounded to fp16 once for the product with
  * the values, the output once.  Results are the same from call to call; the order of the
  * partial sums depends on the batch and the number of SMs.

@@ -267,6 +267,12 @@ __device__ __forceinline__ void decode4(uint32_t w, uint32_t &lo, uint32_t &hi)
     }
 }
 
+// The bytes of four codes that are NaN, as their top bits (E4M3 without the sign: 127; INT8 has none).
+__device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
+{
+    return ((w & 0x7F7F7F7Fu) + 0x01010101u) & 0x80808080u;
+}
+
 // ---- launchers -------------------------------------------------------------------------
 cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream,
                           int *launches);

@@ -765,6 +765,42 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) vw[x][i] = ok ? vw[x][i] : 0u;
             }
+            if (FMT == SLORA_KV_E4M3 && m.n > 1) {
+                // A NaN reaches the rows that see its token, and by the product, as 0 times NaN, the others too:
+                // it is taken out of that and put into those rows' sums.
+                uint32_t odd = 0;
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int i = 0; i < D / 32; ++i) odd |= nan_bytes(vw[x][i]);
+                if (__builtin_expect(__any_sync(~0u, odd != 0), 0)) {
+                    uint64_t mine = 0;       // 16 bits per token x: its channels of this lane's D / 8
+#pragma unroll
+                    for (int x = 0; x < 4; ++x)
+#pragma unroll
+                        for (int i = 0; i < D / 32; ++i) {
+                            const uint32_t b = nan_bytes(vw[x][i]) >> 7;
+                            vw[x][i] &= ~(b * 0xFFu);
+                            mine |= (uint64_t)((b * 0x10204080u) >> 28) << (16 * x + 4 * i);
+                        }
+#pragma unroll 1
+                    for (int k = 0; k < 16; ++k) {
+                        const uint32_t set = (uint32_t)(__shfl_sync(~0u, mine, (lane & ~3) + (k >> 2)) >> (16 * (k & 3))) & 0xFFFFu;
+                        const int j = m.j0 + warp * 16 + token_of_row<D>(2 * (k >> 2) + (k & 1)) + 8 * (k >> 1 & 1);
+#pragma unroll
+                        for (int t = 0; t < NT; ++t)
+#pragma unroll
+                            for (int x = 0; x < 2; ++x) {
+                                const int r = 8 * t + 2 * c + x;
+                                const int tok = div_group(a, m.r0 + (r < nrows ? r : 0));
+                                const uint32_t see = j >= first_key(a, q, tok) && j < end_key(a, q, tok) ? set : 0u;
+#pragma unroll
+                                for (int h = 0; h < D / 8; ++h)
+                                    if (see >> h & 1u) o[t][h >> 1][x + 2 * (h & 1)] = __int_as_float(0x7FFFFFFF);
+                            }
+                    }
+                }
+            }
         }
 #pragma unroll
         for (int i = 0; i < D / 32; ++i) {

@@ -154,6 +154,79 @@ __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
+// The product takes a NaN value to every row of the unit, as 0 times NaN to those that do not see its key. Row r
+// (of the unit that ends before rend, of the sequence whose new tokens start at row0) sums those
+// channels of its output that are NaN once more, key by key over the keys that it sees, by the maximum and the
+// sum that the softmax has found.  Rare, and slow: a row's thread reads its keys alone.
+template <int D, int FMT>
+static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t row0, int32_t head, int32_t r, float base, float inv)
+{
+    const AttendArgs &a = p.a;
+    int32_t s = 0;
+    for (int32_t hi = a.b.S - 1; s < hi;) {              // the last sequence that starts at or before row0
+        const int32_t mid = (s + hi + 1) / 2;
+        if (a.b.indptr[mid] <= row0) s = mid; else hi = mid - 1;
+    }
+    if (a.b.indptr[s] != row0)                           // offsets that decrease elsewhere
+        for (s = 0; s < a.b.S - 1 && !(a.b.indptr[s] == row0 && a.b.indptr[s + 1] > row0);) ++s;
+    int32_t bad = 0;
+    const Seq q = load_seq(a, s, &bad);
+    const int32_t tok = div_group(a, r), qh = head * a.group + (r - tok * a.group);
+    if (tok >= q.n) return;                              // offsets changed under the call
+    const int32_t k0 = first_key(a, q, tok), k1 = end_key(a, q, tok);
+    const uint4 *query = reinterpret_cast<const uint4 *>(a.q + (int64_t)(q.row0 + tok) * a.q_stride + (int64_t)qh * D);
+    __half *out = a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)qh * D;
+    const int32_t *table = a.b.table + ((int64_t)s * a.b.max_blocks * a.c.n_kv + head) * 2;
+#pragma unroll 1
+    for (int c = 0; c < D; c += 4) {
+        const uint2 was = __ldcg(reinterpret_cast<const uint2 *>(out + c));
+        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&was.x));
+        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&was.y));
+        if (x.x == x.x && x.y == x.y && y.x == y.x && y.y == y.y) continue;
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 1
+        for (int32_t k = k0; k < k1; ++k) {
+            const int32_t blk = k / a.c.bt, row = k - blk * a.c.bt;
+            const int32_t *pages = table + (int64_t)blk * a.c.n_kv * 2;
+            const int32_t kp = pages[0], vp = pages[1];
+            if (kp < 0 || kp >= a.c.num_pages || vp < 0 || vp >= a.c.num_pages) continue;      // not seen
+            const uint4 *key = reinterpret_cast<const uint4 *>(a.c.pool + kp * a.c.page_bytes + row * D);
+            float dot = 0.f;
+#pragma unroll 1
+            for (int i = 0; i < D / 16; ++i) {
+                const uint4 w = key[i], q0 = query[2 * i], q1 = query[2 * i + 1];
+                const uint32_t kw[4] = {w.x, w.y, w.z, w.w}, qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    uint32_t h[2];
+                    decode4<FMT>(kw[j], h[0], h[1]);
+#pragma unroll
+                    for (int l = 0; l < 2; ++l) {
+                        const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&h[l]));
+                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&qw[2 * j + l]));
+                        dot = fmaf(u.x, v.x, dot);
+                        dot = fmaf(u.y, v.y, dot);
+                    }
+                }
+            }
+            const float kx = pow2(clamp_exponent(a.c.exps[kp])) * p.scale;
+            const float e = ex2(fmaf(dot, kx, (float)clamp_exponent(a.c.exps[vp])) - base);
+            uint32_t h[2];
+            decode4<FMT>(*reinterpret_cast<const uint32_t *>(a.c.pool + vp * a.c.page_bytes + row * D + c), h[0], h[1]);
+#pragma unroll
+            for (int l = 0; l < 2; ++l) {
+                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[l]));
+                o[2 * l] = fmaf(e, v.x, o[2 * l]);
+                o[2 * l + 1] = fmaf(e, v.y, o[2 * l + 1]);
+            }
+        }
+        const float was4[4] = {x.x, x.y, y.x, y.y};
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (was4[j] != was4[j]) out[c + j] = __float2half_rn(o[j] * inv);
+    }
+}
+
 struct Tiles {
     int32_t lo, hi;        // key tiles [lo, hi) of a unit, one at least
     int32_t k0, k1;        // keys
@@ -1006,6 +1079,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             int64_t at[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) at[j] = place(rw + 8 * j);
+            __half2 probe = __float2half2_rn(0.f);             // NaN if an output that this lane writes is (or infinite)
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
                 if (whole) {
@@ -1044,11 +1118,24 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 for (int j = 0; j < 4; ++j) {
                     const int y = (lane >> 2) + 8 * j, c = lane & 3;
                     const uint4 v = lds128(turn + y * 64 + ((c ^ (y >> 1 & 3)) << 4));
+                    if (FMT == SLORA_KV_E4M3) {
+                        const __half2 *x = reinterpret_cast<const __half2 *>(&v);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) probe = __hfma2(x[k], __float2half2_rn(0.f), probe);
+                    }
                     if (rw + 8 * j < rend) *reinterpret_cast<uint4 *>(a.out + at[j] + 32 * h + 8 * c) = v;
                 }
                 __syncwarp();
             }
             if (whole) release();
+            if (FMT == SLORA_KV_E4M3) {
+                const float2 x = __half22float2(probe);
+                if (__builtin_expect(__any_sync(~0u, !(x.x == x.x && x.y == x.y)), 0)) {
+                    // (the row's outputs were written by other lanes, behind the loop's __syncwarp)
+                    if (live && M < INFINITY && L < INFINITY) sum_again<D, FMT>(p, row0, head, r, M == -INFINITY ? 0.f : M, inv);
+                    __syncwarp();
+                }
+            }
             if (live && a.lse) {
                 const int32_t tok = div_group(a, r);
                 a.lse[(int64_t)(row0 + tok) * a.n_q + (int64_t)head * a.group + (r - tok * a.group)] =

@@ -429,3 +429,65 @@ def test_sequences_without_new_tokens_may_hold_anything(seqs):
         assert np.array_equal(out, want) and np.array_equal(lse, wl)
         status, got, ge = append_ones(c)
         assert status == 0 and np.array_equal(got, pages) and np.array_equal(ge, exps)
+
+
+NAN_CASES = {
+    "drafts": ([(4, 70), (1, 33), (7, 150), (3, 3)], 8, 2, 128, 4096),
+    "drafts, 64-wide": ([(4, 70), (1, 33), (7, 150), (3, 3)], 4, 4, 64, 256),
+    "drafts, 16 rows": ([(4, 200), (5, 64)], 6, 2, 128, 5120),
+    "drafts beyond the cache": ([(6, 4), (5, 200)], 4, 2, 128, 4096),
+    "prompts": ([(130, 333), (70, 70), (1, 9), (300, 300)], 4, 2, 128, 4096),
+    "prompts beyond the cache": ([(150, 90), (70, 70)], 4, 2, 128, 4096),
+    "prompts, 64-wide": ([(130, 333), (70, 70)], 3, 1, 64, 640),
+    "prompts beside tokens": ([(150, 200)] + [(1, 40)] * 200, 4, 2, 128, 4096),
+    "split prompts": ([(280, 9001)], 2, 1, 128, 4096),
+}
+
+
+@pytest.mark.parametrize("kind", NAN_CASES)
+@pytest.mark.parametrize("window", [0, 50])
+def test_a_nan_value_reaches_the_tokens_that_see_it_only(kind, window):
+    """NaN codes among the values, at new tokens, at the window's edge and deep in the cache: the outputs of the tokens
+    that see one are NaN in its channel; all else, the log-sum-exp too, is as with 0 in its place."""
+    seqs, hq, hkv, d, hidden = NAN_CASES[kind]
+    c = Case(seqs, hq=hq, hkv=hkv, d=d, hidden=hidden, seed=54)
+    g = hq // hkv
+    spots = []
+    for s, (n, length) in enumerate(seqs[:4]):
+        for p in {length - 1, length - n, length - n + 1, length - 1 - n // 2, max(0, length - n - 49), length // 3, 0}:
+            if 0 <= p < length:
+                spots.append((s, p, int(c.rng.integers(hkv)), int(c.rng.integers(d)), int(c.rng.choice([0x7F, 0xFF]))))
+    codes = c.pages.reshape(len(c.pages), -1)
+
+    def put(nan):
+        for s, p, h, ch, code in spots:
+            codes[c.table[s, p // c.bt, h, 1], (p % c.bt) * d + ch] = code if nan else 0
+        c.push()
+
+    put(False)
+    clean, cl = c.attend(window=window)
+    put(True)
+    out, lse = c.attend(window=window)
+    assert c.s.device_status() == 0
+    want = clean.copy()
+    for s, p, h, ch, _ in spots:
+        n, length = seqs[s]
+        pos = length - n + np.arange(n)
+        see = (p <= pos) & ((p > pos - window) if window else True)
+        want[c.indptr[s] + np.nonzero(see)[0], h * g:(h + 1) * g, ch] = np.nan
+    assert np.isnan(want).any() and not np.isnan(want).all()
+    assert np.array_equal(np.isnan(out), np.isnan(want)) and np.array_equal(lse, cl)
+    # the prompt kernel sums such a channel of a token that sees no NaN once more, by fp32 weights: within the
+    # tolerance of the definition; every other channel bit for bit
+    val, exps = c.values()
+    ref, _, tol, _ = R.attend(np.nan_to_num(val), exps, c.table, c.indptr, c.kv_len, c.q, c.bt, 0.5 / np.sqrt(d), True, window)
+    touched = np.zeros(out.shape, bool)
+    for s, p, h, ch, _ in spots:
+        touched[c.indptr[s]:c.indptr[s + 1], h * g:(h + 1) * g, ch] = True
+    ok = ~np.isnan(want)
+    assert np.array_equal(out[ok & ~touched], want[ok & ~touched])
+    assert (np.abs(out - ref) <= tol)[ok].all()
+    a, la = c.attend(causal=False)                        # every token sees every key
+    for s, p, h, ch, _ in spots:
+        n, length = seqs[s]
+        assert np.isnan(a[c.indptr[s]:c.indptr[s + 1], h * g:(h + 1) * g, ch]).all()
