@@ -465,6 +465,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * hidden 4096 and head_dim 128).  Bytes past the rows are not used.  One power-of-two scale
  * per page, i.e. per block of tokens and head, for keys and values apart:
  *     value = code * 2^exponent[page],   int8 exponent[num_pages], device memory of the cache
+ * with exponents of -60 to 60: one that the caller wrote beyond them is read as the nearest of the
+ * two (scores and sums are fp32).  append writes -40 to 11 by itself.
  * The format is that of the codes:
  *     SLORA_KV_E4M3  8-bit floats (4 exponent bits, 3 mantissa bits, largest value 448)
  *     SLORA_KV_INT8  integers -127 .. 127

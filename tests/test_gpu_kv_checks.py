@@ -491,3 +491,23 @@ def test_a_nan_value_reaches_the_tokens_that_see_it_only(kind, window):
     for s, p, h, ch, _ in spots:
         n, length = seqs[s]
         assert np.isnan(a[c.indptr[s]:c.indptr[s + 1], h * g:(h + 1) * g, ch]).all()
+
+
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+@pytest.mark.parametrize("seqs", [[(1, 100), (3, 70)], [(70, 130), (40, 40)]], ids=["stream", "prompts"])
+def test_exponents_beyond_sixty_are_read_as_sixty(seqs, fmt):
+    """As the header says, by attend and, for the rows that a block holds, by append."""
+    c = Case(seqs, hq=8, hkv=2, fmt=fmt, seed=55, stale=False)
+    for sign in (1, -1):
+        got = []
+        for e in (60, 61, 100, 127):
+            c.exps[:] = sign * e
+            c.exps[::3] = sign * 60
+            c.push()
+            out, lse = c.attend(scale=2.0 ** (-58 * sign))
+            assert np.isfinite(lse).all()
+            got.append((out, lse) + append_ones(c))
+        for g in got[1:]:
+            assert np.array_equal(g[0], got[0][0], equal_nan=True) and np.array_equal(g[1], got[0][1])
+            touched = np.unique(np.concatenate([c.table[s, (n - m) // c.bt:-(-n // c.bt)].ravel() for s, (m, n) in enumerate(seqs)]))
+            assert g[2] == got[0][2] == 0 and np.array_equal(g[3], got[0][3]) and np.array_equal(g[4][touched], got[0][4][touched])
