@@ -545,8 +545,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * Attends over one pool, of whichever cache, share its workspace: issue them on one stream,
  * or order the streams.
  *
- * Both: strides are multiples of 8 elements and at least a row; pointers 16-byte aligned.  With
- * n_tokens or n_seqs 0 nothing is read, written or launched and the pointers may be NULL.
+ * Both: strides are multiples of 8 elements and at least a row; pointers of rows, cos and sin 16-byte
+ * aligned, of int32 and lse 4-byte aligned.  With n_tokens or n_seqs 0 nothing is read, written or launched and the pointers may be NULL.
  * Errors: SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is
  * launched), SLORA_ERR_UNSUPPORTED (head_dim or a page too small; or max_q times the query
  * heads per KV head above 2^30).  On the device a bad page id (SLORA_DEV_BAD_PAGE: that

@@ -67,6 +67,7 @@ bool encode_maps(slora_kv *k)
 }
 
 bool aligned16(const void *p) { return ((uintptr_t)p & 15) == 0; }
+bool aligned4(const void *p) { return ((uintptr_t)p & 3) == 0; }
 
 // The checks that append and attend share.
 slora_status check_batch(const char *fn, slora_kv_t k, const slora_kv_batch *b, kv::Batch *out)
@@ -79,6 +80,8 @@ slora_status check_batch(const char *fn, slora_kv_t k, const slora_kv_batch *b, 
                     b->n_seqs, b->max_q, b->max_blocks);
     if (b->n_tokens > 0 && b->n_seqs > 0 && (!b->tok_indptr || !b->kv_len || !b->block_table))
         return fail(SLORA_ERR_INVALID_ARG, "%s: null tok_indptr, kv_len or block_table", fn);
+    if (!aligned4(b->tok_indptr) || !aligned4(b->kv_len) || !aligned4(b->block_table))
+        return fail(SLORA_ERR_INVALID_ARG, "%s: misaligned tok_indptr, kv_len or block_table", fn);
     *out = kv::Batch{b->n_tokens, b->n_seqs, b->max_q < b->n_tokens ? b->max_q : b->n_tokens, b->max_blocks,
                      b->tok_indptr, b->kv_len, b->block_table};
     return SLORA_OK;
@@ -214,7 +217,7 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
     if (rope) {
         if (rope->rot_dim < 16 || rope->rot_dim > k->head_dim || rope->rot_dim % 16 != 0 ||
             (rope->interleaved != 0 && rope->interleaved != 1) || rope->n_positions < 1 || !rope->cos || !rope->sin ||
-            !aligned16(rope->cos) || !aligned16(rope->sin))
+            !aligned16(rope->cos) || !aligned16(rope->sin) || !aligned4(rope->positions))
             return fail(SLORA_ERR_INVALID_ARG, "%s: rope with rot_dim=%d interleaved=%d n_positions=%d, or its tables", fn,
                         rope->rot_dim, rope->interleaved, rope->n_positions);
         a.rot = rope->rot_dim;
@@ -264,7 +267,7 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     if ((causal != 0 && causal != 1) || window < 0 || (window > 0 && !causal) || !std::isfinite(softmax_scale))
         return fail(SLORA_ERR_INVALID_ARG, "%s: causal=%d window=%d softmax_scale=%g", fn, causal, window,
                     (double)softmax_scale);
-    if (((uintptr_t)lse & 3) != 0)
+    if (!aligned4(lse))
         return fail(SLORA_ERR_INVALID_ARG, "%s: lse is misaligned", fn);
     if (none)
         return SLORA_OK;

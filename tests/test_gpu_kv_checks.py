@@ -511,3 +511,30 @@ def test_exponents_beyond_sixty_are_read_as_sixty(seqs, fmt):
             assert np.array_equal(g[0], got[0][0], equal_nan=True) and np.array_equal(g[1], got[0][1])
             touched = np.unique(np.concatenate([c.table[s, (n - m) // c.bt:-(-n // c.bt)].ravel() for s, (m, n) in enumerate(seqs)]))
             assert g[2] == got[0][2] == 0 and np.array_equal(g[3], got[0][3]) and np.array_equal(g[4][touched], got[0][4][touched])
+
+
+def test_misaligned_arrays_of_integers_are_refused():
+    c = Case([(1, 10), (2, 20)], hq=4, hkv=2, seed=56)
+    q, k = torch.zeros((c.T, 512), dtype=torch.float16, device="cuda"), torch.zeros((c.T, 256), dtype=torch.float16, device="cuda")
+    out, tab = torch.zeros_like(q), torch.zeros((32, 64), device="cuda")
+
+    def attend(b):
+        rdp.slora_kv_attend(c.s.kv, b, q, 512, 4, out, 512)
+
+    def append(b, pos=None):
+        rdp.slora_kv_append(c.s.kv, b, k, 256, k, 256, rope=rdp.KVRope(128, False, 32, tab, tab, pos))
+
+    def refused(fn, *args):
+        with pytest.raises(rdp.SloraError) as e:
+            fn(*args)
+        assert e.value.status == 1
+
+    for field in ("tok_indptr", "kv_len", "block_table"):
+        for off in (1, 2, 3):
+            b = c.batch()
+            setattr(b, field, getattr(b, field) + off)
+            refused(attend, b)
+            refused(append, b)
+    for off in (1, 2, 3):
+        refused(append, c.batch(), torch.zeros(8, dtype=torch.int32, device="cuda").data_ptr() + off)
+    assert (out == 0).all() and c.s.device_status() == 0
