@@ -154,7 +154,9 @@ __device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, in
 // false after the first timeout in the CTA (*abort, SLORA_DEV_TIMEOUT), from when on every wait that
 // would have to wait gives up soon.  One try, which the hardware holds for up to 20 us, stands
 // in line and the rest in a function: these kernels have some thirty waits, and with whole
-// loops at each the code is fetched from L2 again and again.
+// loops at each the code is fetched from L2 again and again.  A warp at long work puts the time into
+// abort[1], and the limit counts from then.
+__device__ __forceinline__ uint32_t work_clock(uint64_t ns) { return (uint32_t)(ns >> 20); }
 static __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
 {
     uint64_t t0 = 0;
@@ -164,7 +166,7 @@ static __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, vo
         if (*abort) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs) {
+        if (now - t0 > kWaitLimitNs && work_clock(now) - (uint32_t)abort[1] > work_clock(kWaitLimitNs)) {
             set_status(status, SLORA_DEV_TIMEOUT);
             *abort = 1;
             return false;

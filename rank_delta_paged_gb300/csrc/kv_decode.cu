@@ -184,7 +184,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     float *merge = reinterpret_cast<float *>(meta + kDescs);
     __shared__ uint64_t s_full[NS], s_empty[NS], s_merge[3];
     __shared__ int64_t s_sum[kSeqChunks];
-    __shared__ int s_abort, s_last;
+    __shared__ int s_abort[2], s_last;
     __shared__ uint64_t s_launch;               // tid 0's
     __shared__ float s_row[2][kMaxRows];
 
@@ -200,7 +200,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         mbar_init(&s_merge[1], kConsumers);
         mbar_init(&s_merge[2], 1);
         fence_mbar_init();
-        s_abort = 0;
+        s_abort[0] = s_abort[1] = 0;
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -209,7 +209,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         started = start_launch(p.joins, blockIdx.x == 0, gridDim.x);
         if ((int32_t)blockIdx.x == a.give_up) {
             set_status(status, SLORA_DEV_TIMEOUT);
-            s_abort = 1;
+            s_abort[0] = 1;
         }
     }
 
@@ -248,7 +248,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
     if (w0 >= W - kUnitCost) return;
-    volatile int *abort = &s_abort;
+    volatile int *abort = s_abort;
     const int R = p.box_rows;                  // rows of a tile that share a page
     const int batch_log = R == 16 ? 2 : 1;     // tiles per batch of descriptors
     const int n_batches = kDescs >> batch_log;
@@ -285,7 +285,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             if (s32 >= S) {       // the lengths changed under the call: nothing to copy
                 if (lane == 0) {
                     set_status(status, SLORA_DEV_BAD_LENGTH);
-                    s_abort = 1;
+                    s_abort[0] = 1;
                 }
                 return;
             }
@@ -573,11 +573,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         for (int t = issued; t < early; ++t)
             if (leader) mbar_arrive_expect_tx(&s_full[t], (uint32_t)__popc(meta[t].ok) * 16u * D);
         const int32_t copied = issued > early ? issued : early;
-        volatile int gone = 0;
+        volatile int gone[2] = {0, 0};
 #pragma unroll 1
-        for (int i = 0; i < NS && i < copied && !gone; ++i) {
+        for (int i = 0; i < NS && i < copied && !gone[0]; ++i) {
             const int t = copied - 1 - i;
-            wait_bar(&s_full[t % NS], (uint32_t)(t / NS & 1), &gone, status);
+            wait_bar(&s_full[t % NS], (uint32_t)(t / NS & 1), gone, status);
         }
         return;
     }

@@ -154,14 +154,18 @@ __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(ad), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
 }
 
-// The product takes a NaN value to every row of the unit, as 0 times NaN to those that do not see its key. Row r
-// (of the unit that ends before rend, of the sequence whose new tokens start at row0) sums those
-// channels of its output that are NaN once more, key by key over the keys that it sees, by the maximum and the
-// sum that the softmax has found.  Rare, and slow: a row's thread reads its keys alone.
+// The product takes a NaN value to every row of the unit, as 0 times NaN to those that do not see its key. A warp
+// goes through its rows: where an output is NaN in a channel in which one of the unit's keys that
+// the row does not see is NaN, it sums the channel again over the keys that it sees, by the reference and the sum that the
+// softmax has found (inv < 0: not this row).  (Channels that are NaN by a key which every row sees are right as they are.)  Rare, and
+// slow: abort[1] tells the waits of the CTA's other warps that it goes on.
 template <int D, int FMT>
-static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t row0, int32_t head, int32_t r, float base, float inv)
+static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t row0, int32_t head, int32_t r, int32_t rend, float base,
+                                              float inv, volatile int *abort)
 {
     const AttendArgs &a = p.a;
+    const int lane = threadIdx.x & 31;
+    constexpr int CL = D / 32;                           // channels of a lane
     int32_t s = 0;
     for (int32_t hi = a.b.S - 1; s < hi;) {              // the last sequence that starts at or before row0
         const int32_t mid = (s + hi + 1) / 2;
@@ -171,59 +175,98 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
         for (s = 0; s < a.b.S - 1 && !(a.b.indptr[s] == row0 && a.b.indptr[s + 1] > row0);) ++s;
     int32_t bad = 0;
     const Seq q = load_seq(a, s, &bad);
-    const int32_t tok = div_group(a, r), qh = head * a.group + (r - tok * a.group);
-    if (tok >= q.n) return;                              // offsets changed under the call
-    const int32_t k0 = first_key(a, q, tok), k1 = end_key(a, q, tok);
-    const uint4 *query = reinterpret_cast<const uint4 *>(a.q + (int64_t)(q.row0 + tok) * a.q_stride + (int64_t)qh * D);
-    __half *out = a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)qh * D;
+    if ((int64_t)q.n * a.group < rend) return;           // offsets changed under the call
+    const int32_t first = first_key(a, q, div_group(a, r & -kRows)), end = end_key(a, q, div_group(a, rend - 1));
     const int32_t *table = a.b.table + ((int64_t)s * a.b.max_blocks * a.c.n_kv + head) * 2;
+    // the pages' rows of key k; false if it is not seen by any row
+    auto place = [&](int32_t k, int32_t &kp, int32_t &vp, int32_t &row) {
+        const int32_t blk = k / a.c.bt;
+        row = (k - blk * a.c.bt) * D;
+        kp = table[(int64_t)blk * a.c.n_kv * 2];
+        vp = table[(int64_t)blk * a.c.n_kv * 2 + 1];
+        return kp >= 0 && kp < a.c.num_pages && vp >= 0 && vp < a.c.num_pages;
+    };
+    // this lane's channels of a row of codes, the first in the low byte
+    auto codes = [&](int64_t at) -> uint32_t {
+        const uint8_t *c = a.c.pool + at + CL * lane;
+        return CL == 4 ? *reinterpret_cast<const uint32_t *>(c) : *reinterpret_cast<const uint16_t *>(c);
+    };
 #pragma unroll 1
-    for (int c = 0; c < D; c += 4) {
-        const uint2 was = __ldcg(reinterpret_cast<const uint2 *>(out + c));
-        const float2 x = __half22float2(*reinterpret_cast<const __half2 *>(&was.x));
-        const float2 y = __half22float2(*reinterpret_cast<const __half2 *>(&was.y));
-        if (x.x == x.x && x.y == x.y && y.x == y.x && y.y == y.y) continue;
+    for (unsigned rows = __ballot_sync(~0u, inv >= 0.f); rows; rows &= rows - 1) {
+        const int l = __ffs(rows) - 1;
+        const int32_t rr = __shfl_sync(~0u, r, l);
+        const float m = __shfl_sync(~0u, base, l), iv = __shfl_sync(~0u, inv, l);
+        const int32_t tok = div_group(a, rr), qh = head * a.group + (rr - tok * a.group);
+        const int32_t k0 = first_key(a, q, tok), k1 = end_key(a, q, tok);
+        __half *out = a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)qh * D + CL * lane;
+        uint32_t odd = 0;                                // channels: bit 8 c + 7, as nan_bytes has them
+#pragma unroll
+        for (int c = 0; c < CL; ++c)
+            if ((__ldcg(reinterpret_cast<const unsigned short *>(out) + c) & 0x7FFFu) > 0x7C00u) odd |= 0x80u << (8 * c);
+        if (!__any_sync(~0u, odd != 0)) continue;
+        uint32_t unseen = 0;
+#pragma unroll 1
+        for (int32_t k = first; k < end; ++k) {
+            if (k >= k0 && k < k1) {
+                k = k1 - 1;
+                continue;
+            }
+            int32_t kp, vp, row;
+            if (place(k, kp, vp, row)) unseen |= nan_bytes(codes(vp * a.c.page_bytes + row));
+        }
+        odd &= unseen;
+        if (!__any_sync(~0u, odd != 0)) continue;
+        const uint4 *query = reinterpret_cast<const uint4 *>(a.q + (int64_t)(q.row0 + tok) * a.q_stride + (int64_t)qh * D);
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int32_t k = k0; k < k1; ++k) {
-            const int32_t blk = k / a.c.bt, row = k - blk * a.c.bt;
-            const int32_t *pages = table + (int64_t)blk * a.c.n_kv * 2;
-            const int32_t kp = pages[0], vp = pages[1];
-            if (kp < 0 || kp >= a.c.num_pages || vp < 0 || vp >= a.c.num_pages) continue;      // not seen
-            const uint4 *key = reinterpret_cast<const uint4 *>(a.c.pool + kp * a.c.page_bytes + row * D);
-            float dot = 0.f;
+        for (int32_t kb = k0; kb < k1; kb += 32) {
+            if (lane == 0) abort[1] = (int)work_clock(global_timer_ns());
+            // a key per lane, then a channel per lane
+            int32_t kp, vp, row;
+            float e = 0.f;
+            int64_t at = -1;
+            if (kb + lane < k1 && place(kb + lane, kp, vp, row)) {
+                at = vp * a.c.page_bytes + row;
+                const uint4 *key = reinterpret_cast<const uint4 *>(a.c.pool + kp * a.c.page_bytes + row);
+                float dot = 0.f;
 #pragma unroll 1
-            for (int i = 0; i < D / 16; ++i) {
-                const uint4 w = key[i], q0 = query[2 * i], q1 = query[2 * i + 1];
-                const uint32_t kw[4] = {w.x, w.y, w.z, w.w}, qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
+                for (int i = 0; i < D / 16; ++i) {
+                    const uint4 w = key[i], q0 = query[2 * i], q1 = query[2 * i + 1];
+                    const uint32_t kw[4] = {w.x, w.y, w.z, w.w}, qw[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
 #pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    uint32_t h[2];
-                    decode4<FMT>(kw[j], h[0], h[1]);
+                    for (int j = 0; j < 4; ++j) {
+                        uint32_t h[2];
+                        decode4<FMT>(kw[j], h[0], h[1]);
 #pragma unroll
-                    for (int l = 0; l < 2; ++l) {
-                        const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&h[l]));
-                        const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&qw[2 * j + l]));
-                        dot = fmaf(u.x, v.x, dot);
-                        dot = fmaf(u.y, v.y, dot);
+                        for (int x = 0; x < 2; ++x) {
+                            const float2 u = __half22float2(*reinterpret_cast<const __half2 *>(&h[x]));
+                            const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&qw[2 * j + x]));
+                            dot = fmaf(u.x, v.x, dot);
+                            dot = fmaf(u.y, v.y, dot);
+                        }
                     }
                 }
+                const float kx = pow2(clamp_exponent(a.c.exps[kp])) * p.scale;
+                e = ex2(fmaf(dot, kx, (float)clamp_exponent(a.c.exps[vp])) - m);
             }
-            const float kx = pow2(clamp_exponent(a.c.exps[kp])) * p.scale;
-            const float e = ex2(fmaf(dot, kx, (float)clamp_exponent(a.c.exps[vp])) - base);
-            uint32_t h[2];
-            decode4<FMT>(*reinterpret_cast<const uint32_t *>(a.c.pool + vp * a.c.page_bytes + row * D + c), h[0], h[1]);
+            __syncwarp();
+#pragma unroll 4
+            for (int j = 0; j < 32; ++j) {
+                const float ej = __shfl_sync(~0u, e, j);
+                const int64_t aj = __shfl_sync(~0u, at, j);
+                uint32_t h[2] = {0u, 0u};
+                if (aj >= 0) decode4<FMT>(codes(aj), h[0], h[1]);
 #pragma unroll
-            for (int l = 0; l < 2; ++l) {
-                const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[l]));
-                o[2 * l] = fmaf(e, v.x, o[2 * l]);
-                o[2 * l + 1] = fmaf(e, v.y, o[2 * l + 1]);
+                for (int x = 0; x < CL / 2; ++x) {
+                    const float2 v = __half22float2(*reinterpret_cast<const __half2 *>(&h[x]));
+                    o[2 * x] = fmaf(ej, v.x, o[2 * x]);
+                    o[2 * x + 1] = fmaf(ej, v.y, o[2 * x + 1]);
+                }
             }
         }
-        const float was4[4] = {x.x, x.y, y.x, y.y};
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-            if (was4[j] != was4[j]) out[c + j] = __float2half_rn(o[j] * inv);
+        for (int c = 0; c < CL; ++c)
+            if (odd >> (8 * c + 7) & 1u) out[c] = __float2half_rn(o[c] * iv);
     }
 }
 
@@ -275,7 +318,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     __shared__ int64_t s_sum[kSeqChunks];
     __shared__ uint32_t s_tmem;
     __shared__ uint64_t s_launch;
-    __shared__ int s_abort, s_last[2];
+    __shared__ int s_abort[2], s_last[2];
 
     const AttendArgs &a = p.a;
     int32_t *status = a.c.status;
@@ -303,7 +346,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         mbar_init(&s_fin, 2);
         mbar_init(&s_unit, 1);
         fence_mbar_init();
-        s_abort = 0;
+        s_abort[0] = s_abort[1] = 0;
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -311,7 +354,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     if (tid == 32 * kPlanWarp) started = start_launch(p.joins, blockIdx.x == 0, gridDim.x);
     if (tid == 0 && (int32_t)blockIdx.x == a.give_up) {
         set_status(status, SLORA_DEV_TIMEOUT);
-        s_abort = 1;
+        s_abort[0] = 1;
     }
 
     // Tiles of each run of `per` sequences; every CTA sums them for itself.
@@ -360,7 +403,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     if (run < p.min_tiles) run = p.min_tiles;
     const int64_t w0 = (int64_t)blockIdx.x * run, w1 = w0 + run < W ? w0 + run : W;
     if (w0 >= W - kUnitCost) return;
-    volatile int *abort = &s_abort;
+    volatile int *abort = s_abort;
 
     if (warp == kMmaWarp) tc::tmem_alloc(&s_tmem, 512);
     tc::fence_before_sync();
@@ -447,7 +490,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         }
         if (!found && lane == 0) {        // the lengths changed under the call
             set_status(status, SLORA_DEV_BAD_LENGTH);
-            s_abort = 1;
+            s_abort[0] = 1;
         }
         Tiles ut = {};
         int32_t r0 = 0, r1 = 0, tile = 0, c0 = 0, c1 = 0;
@@ -679,8 +722,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         }
         // every product issued has completed before tensor memory is released
         if (leader) tc::commit(&s_fin);
-        volatile int gone = 0;
-        wait_bar(&s_fin, 0, &gone, status);
+        volatile int gone[2] = {0, 0};
+        wait_bar(&s_fin, 0, gone, status);
         __syncwarp();
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
         // ---- codes to fp16 operand tiles -----------------------------------------------------
@@ -1079,7 +1122,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             int64_t at[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) at[j] = place(rw + 8 * j);
-            __half2 probe = __float2half2_rn(0.f);             // NaN if an output that this lane writes is (or infinite)
+            __half2 probe = __float2half2_rn(0.f);             // the largest output that this lane writes, NaN if one is
 #pragma unroll 1
             for (int h = 0; h < D / 32; ++h) {
                 if (whole) {
@@ -1121,7 +1164,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (FMT == SLORA_KV_E4M3) {
                         const __half2 *x = reinterpret_cast<const __half2 *>(&v);
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) probe = __hfma2(x[k], __float2half2_rn(0.f), probe);
+                        for (int k = 0; k < 4; ++k) probe = __hmax2_nan(probe, __habs2(x[k]));
                     }
                     if (rw + 8 * j < rend) *reinterpret_cast<uint4 *>(a.out + at[j] + 32 * h + 8 * c) = v;
                 }
@@ -1132,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 const float2 x = __half22float2(probe);
                 if (__builtin_expect(__any_sync(~0u, !(x.x == x.x && x.y == x.y)), 0)) {
                     // (the row's outputs were written by other lanes, behind the loop's __syncwarp)
-                    if (live && M < INFINITY && L < INFINITY) sum_again<D, FMT>(p, row0, head, r, M == -INFINITY ? 0.f : M, inv);
+                    sum_again<D, FMT>(p, row0, head, r, rend, M == -INFINITY ? 0.f : M, live && M < INFINITY && L < INFINITY ? inv : -1.f, abort);
                     __syncwarp();
                 }
             }

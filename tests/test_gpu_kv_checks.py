@@ -538,3 +538,34 @@ def test_misaligned_arrays_of_integers_are_refused():
     for off in (1, 2, 3):
         refused(append, c.batch(), torch.zeros(8, dtype=torch.int32, device="cuda").data_ptr() + off)
     assert (out == 0).all() and c.s.device_status() == 0
+
+
+@pytest.mark.parametrize("seqs,hq,hkv,d", [([(280, 30001), (40, 40)], 2, 1, 128), ([(100, 5000), (90, 90), (200, 333)], 8, 2, 64)])
+@pytest.mark.parametrize("window", [0, 300])
+def test_whole_rows_of_nan_values(seqs, hq, hkv, d, window):
+    """Tokens whose values are all NaN, as a bad one leaves them: new ones and cached ones, over long contexts."""
+    c = Case(seqs, hq=hq, hkv=hkv, d=d, seed=57)
+    rows = []
+    for s, (n, length) in enumerate(seqs):
+        rows += [(s, length - 3), (s, length - n // 2)]
+        if window or s == len(seqs) - 1:
+            rows += [(s, 5), (s, max(0, length - n - 290))]
+    for value in (0, 0x7F):
+        for s, p in rows:
+            for h in range(hkv):
+                at = p % c.bt * d
+                c.pages[c.table[s, p // c.bt, h, 1], at:at + d] = value
+        c.push()
+        if value == 0:
+            clean, cl = c.attend(window=window)
+    out, lse = c.attend(window=window)
+    assert c.s.device_status() == 0 and np.array_equal(lse, cl)
+    val, exps = c.values()
+    ref, _, tol, _ = R.attend(np.nan_to_num(val), exps, c.table, c.indptr, c.kv_len, c.q, c.bt, 0.5 / np.sqrt(d), True, window)
+    hit = np.zeros(c.T, bool)
+    for s, p in rows:
+        n, length = seqs[s]
+        pos = length - n + np.arange(n)
+        hit[c.indptr[s]:c.indptr[s + 1]] |= (p <= pos) & ((p > pos - window) if window else True)
+    assert np.isnan(out[hit]).all() and np.isfinite(out[~hit]).all() and (~hit).sum() > 30
+    assert (np.abs(out - ref) <= tol)[~hit].all()
