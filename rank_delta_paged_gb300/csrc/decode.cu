@@ -706,6 +706,7 @@ struct DeltaArgs {
     // before; the lead waits before it claims any unit, a copy warp before its first token
     // stage (x or y0, which the kernel before may still be writing).
     int32_t plan_ready;
+    int32_t segments_next;      // the segment kernel may be the next in the stream
 };
 
 // A unit as the lead warp hands it to the other warps: the descriptor, the token ids of
@@ -894,12 +895,12 @@ __global__ void __launch_bounds__(kThreads, 1) delta_kernel(const __grid_constan
     // waits later (see DeltaArgs::plan_ready)
     const bool lead_early = a.plan_ready != 0 && warp == kWarpLead;
     const bool copy_early = a.plan_ready != 0 && warp >= kWarpCopy0 && warp < kWarpCopy0 + kCopyWarps;
-    // Only warps that have waited let the next kernel start: the segment kernel reads x without a wait of its
+    // Where the segment kernel follows, only warps that have waited let it start: it reads x without a wait of its
     // own (see its top), and what wrote x, the kernel before this one, may have let this one start early.
-    if (!lead_early && !copy_early) {
-        griddep_wait();
-        griddep_launch_dependents();
-    }
+    // Every other kernel waits for itself.
+    const bool early = lead_early || copy_early;
+    if (!early) griddep_wait();
+    if (!early || !a.segments_next) griddep_launch_dependents();
     const int n_units = __ldcg(&a.L.hdr->n_units);
 
     // read record k's header (every reader walks the records in order); false at the end
@@ -1786,6 +1787,7 @@ static cudaError_t launch_batch(const PoolView &pv, const ProjList *pl, int32_t 
         da.tag = tag;
         for (int j = 0; j < pl->n; ++j) da.proj[j] = pl->proj[j];
         da.plan_ready = plan_ready && !make_plans ? 1 : 0;
+        da.segments_next = n_seg > 0 ? 1 : 0;
         e = cudaLaunchKernelEx(&cfg2, delta_kernel, da);
         if (e != cudaSuccess) return e;
         *launches += 1;
