@@ -17,11 +17,18 @@
 // every CTA takes an equal run, page after page by the whole CTA with the next page's rows under
 // way.  Their queries are a kernel of their own (rotate_kernel).
 //
-// Measured: 512 single tokens of 40 heads 14 us; 5400 tokens, of which 384 are single, of 32 heads 65 us
+// Measured: 512 single tokens of 40 heads 15 us; 5046 tokens, of which 384 are single, of 32 heads 65 us
 // (3.2 TB/s); 16381 tokens of 8 heads of 64 51 us (3.7 TB/s).  The instructions between the reads and
 // the writes (some 180 per warp and 16 bytes a lane) and the waits for a page's reads take the time.
 // With two CTAs' worth of pages per block and CTAs found by a search of the token offsets, the
-// 5400 tokens took 93 us: half the SMs had twice the work of the others.
+// 5046 tokens took 93 us: half the SMs had twice the work of the others.
+// These times are of tokens that no block's exponent grows for.  Where it does, the group of lanes that has the
+// page's token rescales the rows before it one after another: the 512 single tokens, from a cold cache
+// and with the launch, take 23 us without, 58 with 681 of their 40960 pages growing and 136 with 9841 (INT8 66
+// and 160); the 5046 tokens 71, then 91 with 4379 pages growing.
+// Pages above 8192 bytes have more rows per lane: 4096 tokens in prompts, cold, 57 us at 8192 bytes and 32
+// heads (3.0 TB/s), 98 at 10240 and 40 (2.2 TB/s: the registers for 3 rows at two CTAs per SM spill), 111
+// at 16384 and 64 (3.0 TB/s).
 #include "host_common.h"
 #include "internal.h"
 #include "kv.h"
@@ -35,7 +42,8 @@ constexpr int kThreads = 256;
 constexpr int kBlockThreads = 512;  // append_kernel: two rows of 64 per group of 16 lanes
 constexpr int kMaxUnits = 128;     // pages of a block at a time, at most
 constexpr int kSeqChunks = 64;
-// append_kernel's CTAs per SM: those that fit.  4 and 8 cost 1 to 8 us more for their starts.
+// append_kernel's CTAs per SM: those that fit with 2 or 3 rows per lane (with 4 one fits, and the other half of
+// the grid follows it).  4 and 8 cost 1 to 8 us more for their starts.
 constexpr int kBlockCtas = 2;
 constexpr int kQHeads = 4;         // query heads per group and step
 
@@ -441,62 +449,62 @@ __device__ __noinline__ void next_part(const Params &p, Walk &w, int32_t *s_page
 {
     const AppendArgs &a = p.a;
     const int32_t lane = threadIdx.x & 31, bt = a.c.bt, all = 2 * a.c.n_kv, S = a.b.S;
-                int64_t left = w.left;
-                int32_t q = w.s, skip = w.skip;
-                // the first sequence at or behind q that has block `skip`, counted from q
-                bool found = false;
-    #pragma unroll 1
-                while (left > 0 && !found && q < S) {
-                    const int32_t nb = blocks_of(a, (int64_t)q + lane);
-                    int32_t sum = nb;
-    #pragma unroll
-                    for (int o = 1; o < 32; o <<= 1) {
-                        const int32_t x = __shfl_up_sync(~0u, sum, o);
-                        if (lane >= o) sum += x;
-                    }
-                    const unsigned beyond = __ballot_sync(~0u, sum > skip);
-                    found = beyond != 0;
-                    const int l = found ? __ffs(beyond) - 1 : 31;
-                    skip -= __shfl_sync(~0u, found ? sum - nb : sum, l);
-                    q += found ? l : 32;
-                }
-                int32_t u0 = 0, u1 = 0;
-                if (found) {
-                    const int32_t t0 = a.b.indptr[q], n = a.b.indptr[q + 1] - t0, len = a.b.kv_len[q];
-                    const int32_t p0 = len - n;                                   // position of the first new token
-                    const int32_t blk = p0 / bt + skip;
-                    const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
-                    const int32_t held = from - blk * bt;
-                    u0 = w.unit;
-                    u1 = left < all - u0 ? u0 + (int32_t)left : all;
-                    if (u1 > u0 + kMaxUnits) u1 = u0 + kMaxUnits;
-                    // the block's pages of this CTA and, if it holds tokens, their exponents
-    #pragma unroll 1
-                    for (int32_t u = u0 + lane; u < u1; u += 32) {
-                        int32_t page = a.b.table[((int64_t)q * a.b.max_blocks + blk) * all + u];
-                        if (page < 0 || page >= a.c.num_pages) {
-                            set_status(a.c.status, SLORA_DEV_BAD_PAGE);
-                            page = -1;
-                        }
-                        s_page[u - u0] = page;
-                        s_exp[u - u0] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
-                    }
-                    __syncwarp();                       // w.unit has been read
-                    if (lane == 0) {
-                        w.held = held;
-                        w.nt = to - from;
-                        w.row0 = t0 + from - p0;
-                        w.from = from;
-                        w.left = left - (u1 - u0);
-                        w.s = q;
-                        w.skip = u1 == all ? skip + 1 : skip;
-                        w.unit = u1 == all ? 0 : u1;
-                    }
-                }
-                if (lane == 0) {
-                    w.u0 = u0;
-                    w.u1 = u1;
-                }
+    int64_t left = w.left;
+    int32_t q = w.s, skip = w.skip;
+    // the first sequence at or behind q that has block `skip`, counted from q
+    bool found = false;
+#pragma unroll 1
+    while (left > 0 && !found && q < S) {
+        const int32_t nb = blocks_of(a, (int64_t)q + lane);
+        int32_t sum = nb;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int32_t x = __shfl_up_sync(~0u, sum, o);
+            if (lane >= o) sum += x;
+        }
+        const unsigned beyond = __ballot_sync(~0u, sum > skip);
+        found = beyond != 0;
+        const int l = found ? __ffs(beyond) - 1 : 31;
+        skip -= __shfl_sync(~0u, found ? sum - nb : sum, l);
+        q += found ? l : 32;
+    }
+    int32_t u0 = 0, u1 = 0;
+    if (found) {
+        const int32_t t0 = a.b.indptr[q], n = a.b.indptr[q + 1] - t0, len = a.b.kv_len[q];
+        const int32_t p0 = len - n;                                   // position of the first new token
+        const int32_t blk = p0 / bt + skip;
+        const int32_t from = blk * bt > p0 ? blk * bt : p0, to = (blk + 1) * bt < len ? (blk + 1) * bt : len;
+        const int32_t held = from - blk * bt;
+        u0 = w.unit;
+        u1 = left < all - u0 ? u0 + (int32_t)left : all;
+        if (u1 > u0 + kMaxUnits) u1 = u0 + kMaxUnits;
+        // the block's pages of this CTA and, if it holds tokens, their exponents
+#pragma unroll 1
+        for (int32_t u = u0 + lane; u < u1; u += 32) {
+            int32_t page = a.b.table[((int64_t)q * a.b.max_blocks + blk) * all + u];
+            if (page < 0 || page >= a.c.num_pages) {
+                set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+                page = -1;
+            }
+            s_page[u - u0] = page;
+            s_exp[u - u0] = (int8_t)(held && page >= 0 ? clamp_exponent(a.c.exps[page]) : 0);
+        }
+        __syncwarp();                       // w.unit has been read
+        if (lane == 0) {
+            w.held = held;
+            w.nt = to - from;
+            w.row0 = t0 + from - p0;
+            w.from = from;
+            w.left = left - (u1 - u0);
+            w.s = q;
+            w.skip = u1 == all ? skip + 1 : skip;
+            w.unit = u1 == all ? 0 : u1;
+        }
+    }
+    if (lane == 0) {
+        w.u0 = u0;
+        w.u1 = u1;
+    }
 }
 
 template <int D, int FMT, int PASSES>

@@ -3,7 +3,7 @@
 //
 // For a row (new token t, query head j) with keys k_i = c_i 2^e, values v_i = d_i 2^f (codes
 // c, d; exponents e, f of the key's pages):
-//     s_i = q . c_i * 2^e * scale * log2(e)        m = max_i (s_i + f)
+//     s_i = q . c_i * 2^e * scale * log2(e)        m = max_i (s_i + f) - 7, or up to 8 less
 //     w_i = 2^(s_i + f - m)                        out = sum_i w_i d_i / sum_i w_i 2^-f
 // The exponent of the value page goes into the weight, so that values enter the product as
 // plain codes, exact in fp16, and the weights of all pages share one scale; the sum of the
@@ -28,8 +28,8 @@
 // is far from being the bound, and not 15 rows of registers.  The codes go to fp16 in registers,
 // half an instruction (e4m3) to one and a quarter (int8) per code.
 //
-// Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 477 us, 5.7 TB/s; 4 over 60000 to 131000
-// keys: 116 us, 5.5 TB/s; one over 700: 11.5 us, of which the launch and the chain of dependent reads (lengths,
+// Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 476 us, 5.7 TB/s; 4 over 60000 to 131000
+// keys: 116 us, 5.5 TB/s; one over 700: 11.7 us, of which the launch and the chain of dependent reads (lengths,
 // page id, exponent, codes, parts) is nearly all.  Short sequences are held up by their last tiles, which
 // cost the consumers as much as full ones, by the join of a unit's four warps, and by SMs that memory
 // serves a tenth slower than others; long ones by the start and the join of the parts.  The producer
