@@ -537,11 +537,12 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   window       0, or with causal 1: it sees positions p - window + 1 .. p only
  * A token that sees nothing gets zeros and lse -inf.  Cache rows that no new token of the
  * sequence sees may hold anything (their codes are never used, and pages wholly outside are
- * not read).  A NaN among the values reaches, in its channel, the tokens that see it and no others.
- * Scores, the softmax's maxima and sums
- * and the output sums are fp32; the weights are rounded to fp16 once for the product with
- * the values, the output once.  Results are the same from call to call; the order of the
- * partial sums depends on the batch and the number of SMs.
+ * not read).  A NaN among the values reaches, in its channel, the tokens that see it and no
+ * others.  Scores, the softmax's maxima and sums and the output sums are fp32; the weights are
+ * rounded to fp16 for the product with the values (a prompt's weights of the last 128 keys again,
+ * where a much larger score follows), the output once.  Weights below 2^-32 of a token's
+ * largest, each times its value page's scale, count as 0.  Results are the same from call to
+ * call; the order of the partial sums depends on the batch and the number of SMs.
  * Attends over one pool, of whichever cache, share its workspace: issue them on one stream,
  * or order the streams.
  *
