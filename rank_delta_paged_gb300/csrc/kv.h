@@ -150,13 +150,15 @@ __device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, in
     return p > 0 ? p : 0;
 }
 
+// Milliseconds or so, to be compared by differences.
+__device__ __forceinline__ int32_t work_clock(uint64_t ns) { return (int32_t)(uint32_t)(ns >> 20); }
+
 // Bounded wait on an mbarrier phase, as wait_phase of ptx.h: true once the phase has completed;
 // false after the first timeout in the CTA (*abort, SLORA_DEV_TIMEOUT), from when on every wait that
 // would have to wait gives up soon.  One try, which the hardware holds for up to 20 us, stands
 // in line and the rest in a function: these kernels have some thirty waits, and with whole
-// loops at each the code is fetched from L2 again and again.  A warp at long work puts the time into
-// abort[1], and the limit counts from then.
-__device__ __forceinline__ uint32_t work_clock(uint64_t ns) { return (uint32_t)(ns >> 20); }
+// loops at each the code is fetched from L2 again and again.  The limit also counts from the work_clock() in
+// abort[1], which is that of the start until a warp at long work renews it.
 static __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, volatile int *abort, int32_t *status)
 {
     uint64_t t0 = 0;
@@ -166,7 +168,8 @@ static __device__ __noinline__ bool wait_more(uint64_t *bar, uint32_t parity, vo
         if (*abort) return false;
         const uint64_t now = global_timer_ns();
         if (t0 == 0) t0 = now;
-        if (now - t0 > kWaitLimitNs && work_clock(now) - (uint32_t)abort[1] > work_clock(kWaitLimitNs)) {
+        // (the other warp's clock may have been read after this one's)
+        if (now - t0 > kWaitLimitNs && (int32_t)((uint32_t)work_clock(now) - (uint32_t)abort[1]) > work_clock(kWaitLimitNs)) {
             set_status(status, SLORA_DEV_TIMEOUT);
             *abort = 1;
             return false;

@@ -200,7 +200,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         mbar_init(&s_merge[1], kConsumers);
         mbar_init(&s_merge[2], 1);
         fence_mbar_init();
-        s_abort[0] = s_abort[1] = 0;
+        s_abort[0] = 0;
+        s_abort[1] = work_clock(global_timer_ns());
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -573,7 +574,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         for (int t = issued; t < early; ++t)
             if (leader) mbar_arrive_expect_tx(&s_full[t], (uint32_t)__popc(meta[t].ok) * 16u * D);
         const int32_t copied = issued > early ? issued : early;
-        volatile int gone[2] = {0, 0};
+        volatile int gone[2] = {0, abort[1]};
 #pragma unroll 1
         for (int i = 0; i < NS && i < copied && !gone[0]; ++i) {
             const int t = copied - 1 - i;

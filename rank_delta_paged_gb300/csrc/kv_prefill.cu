@@ -26,7 +26,7 @@
 // is cut between CTAs is joined by the last of them to finish, in the order of the list.
 //
 // Measured: 2048 tokens x 32 heads over 30001 keys of 8 KV heads: 0.93 ms, 1.12 PFLOP/s, 58% of what a library
-// product reaches; 16 prompts of 512, 32 heads: 107 us (E4M3; 104 without the look for NaN outputs).  A tile takes 2.3 us where its products need
+// product reaches; 16 prompts of 512, 32 heads: 108 us (E4M3; 105 without the look for NaN outputs).  A tile takes 2.3 us where its products need
 // 1.3: the warps' instruction fetch and the softmax's waits for tensor memory.  Prompts this
 // short are held up by a unit's start and end, about three tiles' time for two to four tiles.
 #include <cstddef>
@@ -220,7 +220,7 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
         for (int32_t kb = k0; kb < k1; kb += 32) {
-            if (lane == 0) abort[1] = (int)work_clock(global_timer_ns());
+            if (lane == 0) abort[1] = work_clock(global_timer_ns());
             // a key per lane, then a channel per lane
             int32_t kp, vp, row;
             float e = 0.f;
@@ -346,7 +346,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         mbar_init(&s_fin, 2);
         mbar_init(&s_unit, 1);
         fence_mbar_init();
-        s_abort[0] = s_abort[1] = 0;
+        s_abort[0] = 0;
+        s_abort[1] = work_clock(global_timer_ns());
     }
     griddep_wait();
     griddep_launch_dependents();
@@ -722,7 +723,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         }
         // every product issued has completed before tensor memory is released
         if (leader) tc::commit(&s_fin);
-        volatile int gone[2] = {0, 0};
+        volatile int gone[2] = {0, abort[1]};
         wait_bar(&s_fin, 0, gone, status);
         __syncwarp();
     } else if (warp >= kConvWarp && warp < kMmaWarp) {
