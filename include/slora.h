@@ -527,6 +527,20 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *                  position outside [0, n_positions) leaves that token unrotated and sets
  *                  SLORA_DEV_BAD_POSITION.
  *
+ * slora_kv_append_norm(): append for models that normalise queries and keys per head before the rotation.
+ * Each row x of head_dim channels of k and q becomes, before anything above is done with it,
+ *     y = (x - m) / sqrt(mean((x - m)^2) + eps) * w      m = 0, or the mean of x with `centered`
+ * in fp32 (the reciprocal square root to 2^-22 of its value, every other step rounded once, the sums in an
+ * order that depends on head_dim alone, so that a token's codes depend on neither the batch nor the
+ * kernel); values are not normalised.  A row with an infinity or a NaN becomes what the formula gives for it.
+ * rope may be NULL here, with q too.
+ *   norm
+ *     centered     0: root mean square;  1: the mean is taken out first
+ *     eps          finite, 0 or more
+ *     q_weight, k_weight   device float [head_dim], 16-byte aligned, or NULL: ones
+ *     q_weight_stride, k_weight_stride   floats from one head's weights to the next head's, a multiple of 4 and at
+ *                  least head_dim; 0: all heads have the same ones
+ *
  * slora_kv_attend(): out = softmax(softmax_scale * q K^T) V of every new token over its
  * sequence's cache, written to out; keys and values of the new tokens themselves must be in
  * the cache already (append first).  Query heads are grouped: head j reads KV head
@@ -577,6 +591,14 @@ typedef struct slora_kv_rope {
     const float *sin;
     const int32_t *positions;
 } slora_kv_rope;
+typedef struct slora_kv_norm {
+    int32_t centered;
+    float eps;
+    const float *q_weight;
+    int64_t q_weight_stride;
+    const float *k_weight;
+    int64_t k_weight_stride;
+} slora_kv_norm;
 slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, int32_t head_dim, int32_t format,
                              slora_kv_t *out);
 slora_status slora_kv_destroy(slora_kv_t kv);
@@ -586,6 +608,10 @@ slora_status slora_kv_append(slora_kv_t kv, const slora_kv_batch *batch /*host*/
                              const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
                              int64_t q_out_stride, int32_t n_q_heads, const slora_kv_rope *rope /*host*/,
                              slora_stream_t stream);
+slora_status slora_kv_append_norm(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *k, int64_t k_stride,
+                                  const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                  int64_t q_out_stride, int32_t n_q_heads, const slora_kv_norm *norm /*host*/,
+                                  const slora_kv_rope *rope /*host*/, slora_stream_t stream);
 slora_status slora_kv_attend(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *q, int64_t q_stride,
                              int32_t n_q_heads, void *out, int64_t out_stride, float *lse, float softmax_scale,
                              int32_t causal, int32_t window, slora_stream_t stream);

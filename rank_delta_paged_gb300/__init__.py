@@ -43,9 +43,9 @@ __all__ = [
     "slora_lru_pin", "slora_lru_unpin", "slora_lru_victims",
     "slora_adapters_acquire", "slora_adapters_release", "slora_pages_alloc_evict", "slora_pool_get_stats",
     "slora_bmm_workspace_bytes", "slora_lora_apply_bmm",
-    "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope",
+    "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope", "KVNorm",
     "slora_kv_create", "slora_kv_destroy", "slora_kv_block_tokens", "slora_kv_exponents",
-    "slora_kv_append", "slora_kv_attend", "slora_debug_kv_give_up",
+    "slora_kv_append", "slora_kv_append_norm", "slora_kv_attend", "slora_debug_kv_give_up",
 ]
 
 _I32, _I64, _U64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -112,6 +112,7 @@ _SIGS = {
     "slora_kv_block_tokens": [_P, _P],
     "slora_kv_exponents": [_P, _PP],
     "slora_kv_append": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P],
+    "slora_kv_append_norm": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _P],
     "slora_kv_attend": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
     "slora_debug_kv_give_up": [_I32],
 }
@@ -453,6 +454,18 @@ class KVRope(ctypes.Structure):
         self.ref = ctypes.addressof(self)
 
 
+class KVNorm(ctypes.Structure):
+    """slora_kv_norm: the norm of queries and keys per head.  The device arrays are kept alive by it."""
+    _fields_ = [("centered", _I32), ("eps", _F32), ("q_weight", _P), ("q_weight_stride", _I64),
+                ("k_weight", _P), ("k_weight_stride", _I64)]
+
+    def __init__(self, eps: float, centered: bool = False, q_weight=None, q_weight_stride: int = 0, k_weight=None,
+                 k_weight_stride: int = 0):
+        super().__init__(int(centered), eps, _ptr(q_weight), q_weight_stride, _ptr(k_weight), k_weight_stride)
+        self._keep = (q_weight, k_weight)
+        self.ref = ctypes.addressof(self)
+
+
 def slora_kv_create(pool: int, n_kv_heads: int, head_dim: int, format: int = SLORA_KV_E4M3) -> int:
     h = ctypes.c_void_p()
     _call("slora_kv_create", pool, n_kv_heads, head_dim, format, ctypes.byref(h))
@@ -481,6 +494,13 @@ def slora_kv_append(kv: int, batch: KVBatch, k, k_stride: int, v, v_stride: int,
                     stream=None) -> None:
     _call("slora_kv_append", kv, batch.ref, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride, _ptr(q_out),
           q_out_stride, n_q_heads, None if rope is None else rope.ref, _stream(stream))
+
+
+def slora_kv_append_norm(kv: int, batch: KVBatch, k, k_stride: int, v, v_stride: int, q=None, q_stride: int = 0,
+                         q_out=None, q_out_stride: int = 0, n_q_heads: int = 0, norm: Optional[KVNorm] = None,
+                         rope: Optional[KVRope] = None, stream=None) -> None:
+    _call("slora_kv_append_norm", kv, batch.ref, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride, _ptr(q_out),
+          q_out_stride, n_q_heads, None if norm is None else norm.ref, None if rope is None else rope.ref, _stream(stream))
 
 
 def slora_kv_attend(kv: int, batch: KVBatch, q, q_stride: int, n_q_heads: int, out, out_stride: int, lse=None,

@@ -184,12 +184,13 @@ extern "C" slora_status slora_kv_exponents(slora_kv_t k, int8_t **out)
     return SLORA_OK;
 }
 
-extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batch, const void *kk, int64_t k_stride,
-                                        const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
-                                        int64_t q_out_stride, int32_t n_q_heads, const slora_kv_rope *rope,
-                                        slora_stream_t stream)
+namespace {
+
+// Append, with the norm of keys and queries if there is one.
+slora_status append(const char *fn, slora_kv_t k, const slora_kv_batch *batch, const void *kk, int64_t k_stride,
+                    const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out, int64_t q_out_stride,
+                    int32_t n_q_heads, const slora_kv_norm *norm, const slora_kv_rope *rope, slora_stream_t stream)
 {
-    const char *fn = "kv_append";
     kv::AppendArgs a = {};
     slora_status st = check_batch(fn, k, batch, &a.b);
     if (st != SLORA_OK)
@@ -199,8 +200,8 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
     if ((st = check_rows(fn, "k", kk, k_stride, row, none)) != SLORA_OK ||
         (st = check_rows(fn, "v", v, v_stride, row, none)) != SLORA_OK)
         return st;
-    if ((!none && (q == nullptr) != (q_out == nullptr)) || (q && !rope))
-        return fail(SLORA_ERR_INVALID_ARG, "%s: q needs q_out and rope", fn);
+    if ((!none && (q == nullptr) != (q_out == nullptr)) || (q && !rope && !norm))
+        return fail(SLORA_ERR_INVALID_ARG, "%s: q needs q_out, and rope or a norm", fn);
     if (q) {
         if (n_q_heads < 1 || n_q_heads > 8192)
             return fail(SLORA_ERR_INVALID_ARG, "%s: n_q_heads=%d", fn, n_q_heads);
@@ -227,6 +228,21 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
         a.sin = rope->sin;
         a.positions = rope->positions;
     }
+    if (norm) {
+        auto weight = [&](const float *w, int64_t stride) {
+            return aligned16(w) && (stride == 0 || (stride >= k->head_dim && stride % 4 == 0));
+        };
+        if ((norm->centered != 0 && norm->centered != 1) || !(norm->eps >= 0.f) || !std::isfinite(norm->eps) ||
+            !weight(norm->q_weight, norm->q_weight_stride) || !weight(norm->k_weight, norm->k_weight_stride))
+            return fail(SLORA_ERR_INVALID_ARG, "%s: norm with centered=%d eps=%g, or its weights", fn, norm->centered,
+                        (double)norm->eps);
+        a.q_weight = norm->q_weight;
+        a.k_weight = norm->k_weight;
+        a.q_weight_stride = norm->q_weight_stride;
+        a.k_weight_stride = norm->k_weight_stride;
+        a.eps = norm->eps;
+        a.centered = norm->centered;
+    }
     if (none)
         return SLORA_OK;
     a.c = k->c;
@@ -238,9 +254,31 @@ extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batc
     cudaError_t e = dev_scope.error();
     int launches = 0;
     if (e == cudaSuccess)
-        e = kv::launch_append(a, k->head_dim, k->format, k->num_sms, (cudaStream_t)stream, &launches);
+        e = kv::launch_append(a, norm != nullptr, k->head_dim, k->format, k->num_sms, (cudaStream_t)stream, &launches);
     *k->launches += launches;
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" slora_status slora_kv_append(slora_kv_t k, const slora_kv_batch *batch, const void *kk, int64_t k_stride,
+                                        const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                        int64_t q_out_stride, int32_t n_q_heads, const slora_kv_rope *rope,
+                                        slora_stream_t stream)
+{
+    return append("kv_append", k, batch, kk, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, n_q_heads, nullptr,
+                  rope, stream);
+}
+
+extern "C" slora_status slora_kv_append_norm(slora_kv_t k, const slora_kv_batch *batch, const void *kk, int64_t k_stride,
+                                             const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
+                                             int64_t q_out_stride, int32_t n_q_heads, const slora_kv_norm *norm,
+                                             const slora_kv_rope *rope, slora_stream_t stream)
+{
+    const char *fn = "kv_append_norm";
+    if (!norm)
+        return fail(SLORA_ERR_INVALID_ARG, "%s: null norm", fn);
+    return append(fn, k, batch, kk, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, n_q_heads, norm, rope, stream);
 }
 
 extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batch, const void *q, int64_t q_stride,

@@ -59,6 +59,11 @@ struct AppendArgs {
     int32_t rot, interleaved, n_pos;    // rot 0: no rotation
     const float *cos, *sin;
     const int32_t *positions;           // nullptr: positions in the cache
+    // The norm of keys and queries per head (kernels with NORM); weights nullptr: ones.
+    const float *q_weight, *k_weight;
+    int64_t q_weight_stride, k_weight_stride;   // from one head's weights to the next, 0: the same ones
+    float eps;
+    int32_t centered;
 };
 
 struct AttendArgs {
@@ -279,7 +284,7 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
 }
 
 // ---- launchers -------------------------------------------------------------------------
-cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream,
+cudaError_t launch_append(const AppendArgs &a, bool norm, int head_dim, int fmt, int num_sms, cudaStream_t stream,
                           int *launches);
 
 // The attention's workspace: partial results of rows whose keys are split over several CTAs, and

@@ -133,6 +133,55 @@ __device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch
     }
 }
 
+// The sum over a row's channels of its LPR lanes' eight each, in an order that every kernel shares: the even and
+// the odd channels of a lane, one after another, then the lanes by twos.  No product is contracted into it.
+template <int LPR>
+__device__ __forceinline__ float row_sum(const float (&x)[8], bool squares)
+{
+    float e = 0.f, o = 0.f;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const float a = squares ? __fmul_rn(x[2 * i], x[2 * i]) : x[2 * i];
+        const float b = squares ? __fmul_rn(x[2 * i + 1], x[2 * i + 1]) : x[2 * i + 1];
+        e = i ? __fadd_rn(e, a) : a;
+        o = i ? __fadd_rn(o, b) : b;
+    }
+    float s = __fadd_rn(e, o);
+#pragma unroll
+    for (int k = 1; k < LPR; k *= 2) s = __fadd_rn(s, __shfl_xor_sync(~0u, s, k));
+    return s;
+}
+
+// This lane's eight weights of head h.
+__device__ __forceinline__ void load_weight(const float *w, int64_t stride, int32_t h, int ch, float (&x)[8])
+{
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = 1.f;
+    if (w == nullptr) return;
+    const float4 *p = reinterpret_cast<const float4 *>(w + h * stride) + 2 * ch;
+    const float4 a = __ldg(p), b = __ldg(p + 1);
+    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
+    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
+}
+
+// The norm of a row: x <- (x - mean) / sqrt(mean of squares + eps) * w, the mean taken out if `centered`.  Every lane of
+// the warp calls it; rows that are not `on` keep their values.  The mean is the sum times a power of two.
+template <int LPR>
+__device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const float (&w)[8], float (&x)[8])
+{
+    constexpr float each = 1.f / (8 * LPR);
+    if (a.centered) {
+        const float m = row_sum<LPR>(x, false) * each;
+        if (on)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], m);
+    }
+    const float r = rsqrtf(__fadd_rn(row_sum<LPR>(x, true) * each, a.eps));
+    if (on)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+}
+
 __device__ __forceinline__ void unpack(uint4 v, float (&x)[8])
 {
     const __half2 *h = reinterpret_cast<const __half2 *>(&v);
@@ -198,7 +247,7 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
 
 // Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
 // have rows of one kind and those of values do not rotate.
-template <int D, int FMT>
+template <int D, int FMT, bool NORM>
 __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR, ILP = 2;
@@ -230,6 +279,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
     for (int32_t ub = u0; ub < u1; ub += ILP * GROUPS) {
         uint4 raw[ILP];
         int32_t page[ILP], old[ILP];
+        float weight[NORM ? ILP : 1][8];
 #pragma unroll
         for (int i = 0; i < ILP; ++i) {
             const int32_t u = ub + i * GROUPS + grp;
@@ -244,6 +294,11 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
                                             : a.k + t0 * a.k_stride + (int64_t)h * D;
                 raw[i] = *reinterpret_cast<const uint4 *>(src + ch * 8);
                 if (u < kv) page[i] = table[2 * h + val];
+            }
+            if (NORM) {
+                const bool q = u >= kv;
+                load_weight(u < u1 && (q || u < a.c.n_kv) ? (q ? a.q_weight : a.k_weight) : nullptr,
+                            q ? a.q_weight_stride : a.k_weight_stride, q ? u - kv : u, ch, weight[i]);
             }
         }
         if (ub == u0) load_rot(a, pos, ch, rot);
@@ -266,6 +321,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
             unpack(raw[i], x);
             const bool turns = u < a.c.n_kv || u >= kv;
             if (__any_sync(~0u, turns)) {
+                if (NORM) normalise<LPR>(a, turns, weight[i], x);
                 Rot r = rot;
                 r.on = rot.on && turns;
                 rotate<LPR>(a, r, ch, x);
@@ -298,7 +354,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
 }
 
 // The queries of a batch: kQHeads heads of one token per group of lanes and step.
-template <int D>
+template <int D, bool NORM>
 __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
@@ -343,6 +399,11 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
             float x[8];
             if (!(mine && h0 + k < a.n_q)) v[k] = make_uint4(0, 0, 0, 0);
             unpack(v[k], x);
+            if (NORM) {
+                float weight[8];
+                load_weight(mine && h0 + k < a.n_q ? a.q_weight : nullptr, a.q_weight_stride, h0 + k, ch, weight);
+                normalise<LPR>(a, true, weight, x);
+            }
             rotate<LPR>(a, r, ch, x);
             uint4 w;
             __half2 *h = reinterpret_cast<__half2 *>(&w);
@@ -356,7 +417,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
 }
 
 // A block's nt new rows of the pages [u0, u1), page after page by the whole CTA.
-template <int D, int FMT, int PASSES>
+template <int D, int FMT, int PASSES, bool NORM>
 __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32_t u1, int32_t nt, int32_t held,
                                           int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp,
                                           uint32_t *s_max, int &turn)
@@ -396,6 +457,11 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
             if (!val) {
                 Rot rt;
                 rt.on = false;
+                if (NORM) {
+                    float weight[8];
+                    load_weight(a.k_weight, a.k_weight_stride, u >> 1, ch, weight);
+                    normalise<LPR>(a, r < nt, weight, x[i]);
+                }
                 if (r < nt) load_rot(a, position(a, row0 + r, from + r), ch, rt);
                 rotate<LPR>(a, rt, ch, x[i]);
             }
@@ -507,7 +573,7 @@ __device__ __noinline__ void next_part(const Params &p, Walk &w, int32_t *s_page
     }
 }
 
-template <int D, int FMT, int PASSES>
+template <int D, int FMT, int PASSES, bool NORM>
 __device__ __forceinline__ void append_blocks(const Params &p)
 {
     const AppendArgs &a = p.a;
@@ -569,18 +635,18 @@ __device__ __forceinline__ void append_blocks(const Params &p)
                       from = s_walk.from;
         if (u1 == 0) return;
         // unit: KV head * 2 + (0 keys, 1 values)
-        full_rows<D, FMT, PASSES>(a, u0, u1, nt, held, row0, from, s_page, s_exp, s_max, turn);
+        full_rows<D, FMT, PASSES, NORM>(a, u0, u1, nt, held, row0, from, s_page, s_exp, s_max, turn);
         __syncthreads();                           // s_walk, s_page and s_exp have been read
     }
 }
 
-template <int D, int FMT, int PASSES>
+template <int D, int FMT, int PASSES, bool NORM>
 __global__ void __launch_bounds__(kBlockThreads, PASSES <= 3 ? 2 : 1) append_kernel(const __grid_constant__ Params p)
 {
     // append_one_kernel, the one before, has waited for what came before it, and nothing here depends on
     // its results; the kernel after this one waits for what this one has waited for
     griddep_launch_dependents();
-    append_blocks<D, FMT, PASSES>(p);
+    append_blocks<D, FMT, PASSES, NORM>(p);
     griddep_wait();
 }
 
@@ -600,7 +666,7 @@ cudaError_t start(void (*kernel)(Args...), const Params &p, int64_t ctas, cudaSt
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
-template <int D>
+template <int D, bool NORM>
 cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *launches)
 {
     constexpr int groups = kThreads / (D / 8);
@@ -613,7 +679,7 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
         const int32_t all = 2 * a.c.n_kv + p.q_rows;
         p.splits = (all + 2 * groups - 1) / (2 * groups);
         p.units = (all + p.splits - 1) / p.splits;
-        e = start(e4m3 ? append_one_kernel<D, SLORA_KV_E4M3> : append_one_kernel<D, SLORA_KV_INT8>, p,
+        e = start(e4m3 ? append_one_kernel<D, SLORA_KV_E4M3, NORM> : append_one_kernel<D, SLORA_KV_INT8, NORM>, p,
                   (int64_t)a.b.S * p.splits, stream);
         *launches += e == cudaSuccess;
         if (e != cudaSuccess || a.b.max_q == 1) return e;
@@ -624,29 +690,36 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
     constexpr int block_groups = kBlockThreads / (D / 8);
     const int passes = (a.c.bt + block_groups - 1) / block_groups;
     if (passes <= 2)
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 2> : append_kernel<D, SLORA_KV_INT8, 2>, p, ctas, stream, kBlockThreads);
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 2, NORM> : append_kernel<D, SLORA_KV_INT8, 2, NORM>, p, ctas, stream,
+                  kBlockThreads);
     else if (passes <= 3)
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 3> : append_kernel<D, SLORA_KV_INT8, 3>, p, ctas, stream, kBlockThreads);
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 3, NORM> : append_kernel<D, SLORA_KV_INT8, 3, NORM>, p, ctas, stream,
+                  kBlockThreads);
     else
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 4> : append_kernel<D, SLORA_KV_INT8, 4>, p, ctas, stream, kBlockThreads);
+        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 4, NORM> : append_kernel<D, SLORA_KV_INT8, 4, NORM>, p, ctas, stream,
+                  kBlockThreads);
     *launches += e == cudaSuccess;
     if (e != cudaSuccess || !a.q) return e;
     const int64_t items = (int64_t)a.b.T * ((a.n_q + kQHeads - 1) / kQHeads);
     int64_t q_ctas = (items + groups - 1) / groups;
     if (q_ctas > 32ll * num_sms) q_ctas = 32ll * num_sms;
-    e = start(rotate_kernel<D>, p, q_ctas, stream);
+    e = start(rotate_kernel<D, NORM>, p, q_ctas, stream);
     *launches += e == cudaSuccess;
     return e;
 }
 
 }  // namespace
 
-cudaError_t launch_append(const AppendArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream, int *launches)
+cudaError_t launch_append(const AppendArgs &a, bool norm, int head_dim, int fmt, int num_sms, cudaStream_t stream,
+                          int *launches)
 {
     Params p = {};
     p.a = a;
-    return head_dim == 128 ? launch_d<128>(p, fmt, num_sms, stream, launches)
-                           : launch_d<64>(p, fmt, num_sms, stream, launches);
+    if (head_dim == 128)
+        return norm ? launch_d<128, true>(p, fmt, num_sms, stream, launches)
+                    : launch_d<128, false>(p, fmt, num_sms, stream, launches);
+    return norm ? launch_d<64, true>(p, fmt, num_sms, stream, launches)
+                : launch_d<64, false>(p, fmt, num_sms, stream, launches);
 }
 
 }  // namespace kv
