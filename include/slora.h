@@ -78,7 +78,7 @@ typedef enum slora_status {
 #define SLORA_DEV_BAD_SEGMENT 4   /* segment tokens disagree on their adapter, or bad bounds */
 #define SLORA_DEV_TIMEOUT 5       /* a bounded wait inside a kernel gave up */
 #define SLORA_DEV_BAD_LENGTH 6    /* KV length below the new tokens, beyond the block table or above 2^30 */
-#define SLORA_DEV_BAD_POSITION 7  /* token position outside the rotation table */
+#define SLORA_DEV_BAD_POSITION 7  /* token position outside the rotation table, or a kept one out of order or range */
 
 const char *slora_status_str(slora_status s);
 /* Message of the calling thread's last failed call ("" if none).  Valid until the
@@ -99,12 +99,16 @@ int32_t slora_version(void);
  * alloc() pops n pages or fails with SLORA_ERR_POOL_FULL and allocates nothing.
  * free() returns pages; a page that is out of range or not allocated fails the whole
  * call with SLORA_ERR_INVALID_ARG before any page is returned.
+ * share() adds a holder to each listed page (a page listed twice gets two); every holder frees the page
+ * once, and the last one's free returns it.  A page that is out of range or not allocated fails the whole
+ * call before anything is shared.
  * ------------------------------------------------------------------------- */
 slora_status slora_pagealloc_create(int64_t num_pages, uint64_t shuffle_seed,
                                     slora_pagealloc_t *out);
 slora_status slora_pagealloc_destroy(slora_pagealloc_t a);
 slora_status slora_pagealloc_alloc(slora_pagealloc_t a, int64_t n, int32_t *out_pages /*host [n]*/);
 slora_status slora_pagealloc_free(slora_pagealloc_t a, int64_t n, const int32_t *pages /*host [n]*/);
+slora_status slora_pagealloc_share(slora_pagealloc_t a, int64_t n, const int32_t *pages /*host [n]*/);
 slora_status slora_pagealloc_num_free(slora_pagealloc_t a, int64_t *out);
 
 /* ---------------------------------------------------------------------------
@@ -156,10 +160,14 @@ slora_status slora_pool_base(slora_pool_t pool, void **out);
 /* KV side of the unified allocator.  pages_alloc pops n slots from the same free list
  * adapters use and writes them to out_pages (host).  pages_free returns KV slots; it
  * records an event on `stream` after which the slots may be rewritten by adapter
- * loads, so work already enqueued on `stream` may still read them. */
+ * loads, so work already enqueued on `stream` may still read them.
+ * pages_share adds a holder to pages that pages_alloc gave out (sequences that share a prefix): each holder frees
+ * them once, and a slot returns to the list with its last holder's pages_free.  Holders free on one
+ * stream or on ordered streams: the event is that of the last free. */
 slora_status slora_pages_alloc(slora_pool_t pool, int64_t n, int32_t *out_pages);
 slora_status slora_pages_free(slora_pool_t pool, int64_t n, const int32_t *pages,
                               slora_stream_t stream);
+slora_status slora_pages_share(slora_pool_t pool, int64_t n, const int32_t *pages);
 
 /* ---------------------------------------------------------------------------
  * Host adapter store (explainer, "The mechanism": all adapters live in host memory and
@@ -560,6 +568,45 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * Attends over one pool, of whichever cache, share its workspace: issue them on one stream,
  * or order the streams.
  *
+ * slora_kv_copy(): copies pages of the cache, rows and exponents, within the pool: a forked sequence gets its own
+ * copy of the block that both would go on to write, and shares the others (slora_pages_share).
+ *   n            pages, 0 <= n < 2^31
+ *   src, dst     device int32 [n]: page dst[i] gets page src[i]'s first rows and its exponent; the rows behind
+ *                them stay as they were.  A page may be the source of several; one that is written is listed
+ *                once, and is no source (src[i] == dst[i]: nothing to do).
+ *   rows         device int32 [n], 0 .. block_tokens (0: nothing is copied), or NULL: all of them
+ * A page id out of range (SLORA_DEV_BAD_PAGE) or a number of rows (SLORA_DEV_BAD_LENGTH) skips that page.
+ *
+ * slora_kv_compact(): moves the kept tokens of each sequence to the front, in place or into other pages: the
+ * accepted branch of drafted tokens, or what is left of a long sequence when tokens are evicted.  The kept
+ * tokens of sequence s, in order, become its tokens first[s], first[s] + 1, ..; the tokens before first[s] stay.
+ *   n_seqs       S, 0 <= S <= 1 << 20
+ *   n_kept       K, 0 <= K <= 1 << 30: entries of a list of kept tokens
+ *   max_kept     the most kept tokens of a sequence; one with more is the caller's error (SLORA_DEV_BAD_SEGMENT)
+ *   max_blocks, dst_blocks   widths of the block tables, 1 or more (dst_blocks is not looked at in place)
+ *   kept_indptr  device int32 [S + 1]: sequence s has entries kept_indptr[s] .. kept_indptr[s+1]-1
+ *   kept         device int32 [K]: the positions that are kept, ascending within a sequence, none below the one
+ *                that it goes to
+ *   kept_head_stride   entries from one KV head's list to the next head's, K or more; 0: one list for all heads
+ *   first        device int32 [S], or NULL: 0
+ *   kv_len       device int32 [S]: the sequences' lengths before
+ *   block_table  device int32 [S][max_blocks][n_kv_heads][2], as in slora_kv_batch
+ *   dst_table    device int32 [S][dst_blocks][n_kv_heads][2]: where the blocks from first[s] on go, or NULL: in place.
+ *                Only entries of written blocks are read.  A page that is written is none that the call
+ *                reads, but that the block of first[s] may keep its page (or its page may be shared with the
+ *                source table).  In that block the tokens before first[s] are written too.
+ *   new_len      device int32 [S] that gets first[s] + the kept tokens, or NULL
+ * Scales: the exponent of every block that gets a token is the smallest e >= -40 for which every finite value of its
+ * rows fits (as in append, with no regard for what it was): a row's codes are multiplied by a power
+ * of two, exact where they grow, rounded to nearest even where they shrink; NaN stays.  Rows of a written
+ * block behind the last kept token are unspecified.  In place a page belongs to one sequence of the call;
+ * with dst_table the sequences may share pages that are only read.
+ * A position that is out of order, below its destination or not below kv_len (SLORA_DEV_BAD_POSITION) or a bad page id
+ * (SLORA_DEV_BAD_PAGE) leaves the block and head that it is for unwritten, a destination beyond its table
+ * (SLORA_DEV_BAD_LENGTH) the block; a kv_len that is negative, beyond the block table or above 2^30, a first
+ * outside [0, kv_len] or more kept tokens than there are from it on (SLORA_DEV_BAD_LENGTH), and offsets that decrease
+ * or leave [0, K] (SLORA_DEV_BAD_SEGMENT), leave the sequence and its new_len as they were.
+ *
  * Both: strides are multiples of 8 elements and at least a row; pointers of rows, cos and sin 16-byte
  * aligned, of int32 and lse 4-byte aligned.  With n_tokens or n_seqs 0 nothing is read, written or launched and the pointers may be NULL.
  * Errors: SLORA_ERR_INVALID_ARG (null, misaligned or out-of-range arguments; nothing is
@@ -599,6 +646,22 @@ typedef struct slora_kv_norm {
     const float *k_weight;
     int64_t k_weight_stride;
 } slora_kv_norm;
+typedef struct slora_kv_keep {
+    int32_t n_seqs;
+    int32_t n_kept;
+    int32_t max_kept;
+    int32_t max_blocks;
+    int32_t dst_blocks;
+    int32_t reserved; /* 0 */
+    const int32_t *kept_indptr;
+    const int32_t *kept;
+    int64_t kept_head_stride;
+    const int32_t *first;
+    const int32_t *kv_len;
+    const int32_t *block_table;
+    const int32_t *dst_table;
+    int32_t *new_len;
+} slora_kv_keep;
 slora_status slora_kv_create(slora_pool_t pool, int32_t n_kv_heads, int32_t head_dim, int32_t format,
                              slora_kv_t *out);
 slora_status slora_kv_destroy(slora_kv_t kv);
@@ -612,6 +675,9 @@ slora_status slora_kv_append_norm(slora_kv_t kv, const slora_kv_batch *batch /*h
                                   const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
                                   int64_t q_out_stride, int32_t n_q_heads, const slora_kv_norm *norm /*host*/,
                                   const slora_kv_rope *rope /*host*/, slora_stream_t stream);
+slora_status slora_kv_copy(slora_kv_t kv, int64_t n, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                           slora_stream_t stream);
+slora_status slora_kv_compact(slora_kv_t kv, const slora_kv_keep *keep /*host*/, slora_stream_t stream);
 slora_status slora_kv_attend(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *q, int64_t q_stride,
                              int32_t n_q_heads, void *out, int64_t out_stride, float *lse, float softmax_scale,
                              int32_t causal, int32_t window, slora_stream_t stream);

@@ -21,9 +21,9 @@ __all__ = [
     "SloraError", "lib", "library_path",
     "slora_status_str", "slora_last_error", "slora_version",
     "slora_pagealloc_create", "slora_pagealloc_destroy", "slora_pagealloc_alloc",
-    "slora_pagealloc_free", "slora_pagealloc_num_free",
+    "slora_pagealloc_free", "slora_pagealloc_share", "slora_pagealloc_num_free",
     "slora_pool_create", "slora_pool_destroy", "slora_pool_num_free", "slora_pool_base",
-    "slora_pages_alloc", "slora_pages_free",
+    "slora_pages_alloc", "slora_pages_free", "slora_pages_share",
     "slora_adapter_register", "slora_adapter_unregister",
     "slora_adapter_load", "slora_adapters_load", "slora_adapter_evict", "slora_adapter_is_resident",
     "slora_lora_apply", "slora_lora_apply_noalloc",
@@ -43,9 +43,9 @@ __all__ = [
     "slora_lru_pin", "slora_lru_unpin", "slora_lru_victims",
     "slora_adapters_acquire", "slora_adapters_release", "slora_pages_alloc_evict", "slora_pool_get_stats",
     "slora_bmm_workspace_bytes", "slora_lora_apply_bmm",
-    "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope", "KVNorm",
+    "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope", "KVNorm", "KVKeep",
     "slora_kv_create", "slora_kv_destroy", "slora_kv_block_tokens", "slora_kv_exponents",
-    "slora_kv_append", "slora_kv_append_norm", "slora_kv_attend", "slora_debug_kv_give_up",
+    "slora_kv_append", "slora_kv_append_norm", "slora_kv_copy", "slora_kv_compact", "slora_kv_attend", "slora_debug_kv_give_up",
 ]
 
 _I32, _I64, _U64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -60,6 +60,7 @@ _SIGS = {
     "slora_pagealloc_destroy": [_P],
     "slora_pagealloc_alloc": [_P, _I64, _P],
     "slora_pagealloc_free": [_P, _I64, _P],
+    "slora_pagealloc_share": [_P, _I64, _P],
     "slora_pagealloc_num_free": [_P, _P],
     "slora_pool_create": [ctypes.c_int, _I32, _I64, _I32, _I32, _U64, _PP],
     "slora_pool_destroy": [_P],
@@ -67,6 +68,7 @@ _SIGS = {
     "slora_pool_base": [_P, _PP],
     "slora_pages_alloc": [_P, _I64, _P],
     "slora_pages_free": [_P, _I64, _P, _P],
+    "slora_pages_share": [_P, _I64, _P],
     "slora_adapter_register": [_P, _I32, _I32, _F32, _P, _P],
     "slora_adapter_unregister": [_P, _I32, _P],
     "slora_adapter_load": [_P, _I32, _P],
@@ -113,6 +115,8 @@ _SIGS = {
     "slora_kv_exponents": [_P, _PP],
     "slora_kv_append": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P],
     "slora_kv_append_norm": [_P, _P, _P, _I64, _P, _I64, _P, _I64, _P, _I64, _I32, _P, _P, _P],
+    "slora_kv_copy": [_P, _I64, _P, _P, _P, _P],
+    "slora_kv_compact": [_P, _P, _P],
     "slora_kv_attend": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
     "slora_debug_kv_give_up": [_I32],
 }
@@ -209,6 +213,10 @@ def slora_pagealloc_free(a: int, n: int, pages) -> None:
     _call("slora_pagealloc_free", a, n, _ptr(pages))
 
 
+def slora_pagealloc_share(a: int, n: int, pages) -> None:
+    _call("slora_pagealloc_share", a, n, _ptr(pages))
+
+
 def slora_pagealloc_num_free(a: int) -> int:
     v = ctypes.c_int64()
     _call("slora_pagealloc_num_free", a, ctypes.byref(v))
@@ -246,6 +254,10 @@ def slora_pages_alloc(pool: int, n: int, out_pages) -> None:
 
 def slora_pages_free(pool: int, n: int, pages, stream=None) -> None:
     _call("slora_pages_free", pool, n, _ptr(pages), _stream(stream))
+
+
+def slora_pages_share(pool: int, n: int, pages) -> None:
+    _call("slora_pages_share", pool, n, _ptr(pages))
 
 
 def slora_adapter_register(pool: int, adapter_id: int, rank: int, scaling: float, At_host,
@@ -466,6 +478,20 @@ class KVNorm(ctypes.Structure):
         self.ref = ctypes.addressof(self)
 
 
+class KVKeep(ctypes.Structure):
+    """slora_kv_keep: the kept tokens of a compaction.  The device arrays are kept alive by it."""
+    _fields_ = [("n_seqs", _I32), ("n_kept", _I32), ("max_kept", _I32), ("max_blocks", _I32), ("dst_blocks", _I32),
+                ("reserved", _I32), ("kept_indptr", _P), ("kept", _P), ("kept_head_stride", _I64), ("first", _P),
+                ("kv_len", _P), ("block_table", _P), ("dst_table", _P), ("new_len", _P)]
+
+    def __init__(self, n_seqs: int, n_kept: int, max_kept: int, max_blocks: int, kept_indptr, kept, first, kv_len,
+                 block_table, dst_blocks: int = 0, dst_table=None, head_stride: int = 0, new_len=None):
+        super().__init__(n_seqs, n_kept, max_kept, max_blocks, dst_blocks, 0, _ptr(kept_indptr), _ptr(kept), head_stride,
+                         _ptr(first), _ptr(kv_len), _ptr(block_table), _ptr(dst_table), _ptr(new_len))
+        self._keep = (kept_indptr, kept, first, kv_len, block_table, dst_table, new_len)
+        self.ref = ctypes.addressof(self)
+
+
 def slora_kv_create(pool: int, n_kv_heads: int, head_dim: int, format: int = SLORA_KV_E4M3) -> int:
     h = ctypes.c_void_p()
     _call("slora_kv_create", pool, n_kv_heads, head_dim, format, ctypes.byref(h))
@@ -501,6 +527,14 @@ def slora_kv_append_norm(kv: int, batch: KVBatch, k, k_stride: int, v, v_stride:
                          rope: Optional[KVRope] = None, stream=None) -> None:
     _call("slora_kv_append_norm", kv, batch.ref, _ptr(k), k_stride, _ptr(v), v_stride, _ptr(q), q_stride, _ptr(q_out),
           q_out_stride, n_q_heads, None if norm is None else norm.ref, None if rope is None else rope.ref, _stream(stream))
+
+
+def slora_kv_copy(kv: int, n: int, src, dst, rows=None, stream=None) -> None:
+    _call("slora_kv_copy", kv, n, _ptr(src), _ptr(dst), _ptr(rows), _stream(stream))
+
+
+def slora_kv_compact(kv: int, keep: KVKeep, stream=None) -> None:
+    _call("slora_kv_compact", kv, keep.ref, _stream(stream))
 
 
 def slora_kv_attend(kv: int, batch: KVBatch, q, q_stride: int, n_q_heads: int, out, out_stride: int, lse=None,

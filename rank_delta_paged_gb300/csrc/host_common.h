@@ -17,14 +17,17 @@ extern thread_local std::string g_last_error;
 slora_status fail(slora_status s, const char *fmt, ...);
 uint64_t splitmix64(uint64_t &state);
 
-// Free list of pool slots.  allocated[p]: 0 free, 1 in use.
+// Free list of pool slots.  allocated[p]: 0 free, 1 in use.  A page in use has one holder and extra[p] more
+// (empty until a page is shared); it goes back to the list when its last holder releases it.
 struct PageAlloc {
     int64_t num_pages = 0;
     std::vector<int32_t> free_stack;
     std::vector<uint8_t> allocated;
+    std::vector<int32_t> extra;
     void init(int64_t n, uint64_t seed);
     slora_status alloc(int64_t n, int32_t *out);
     slora_status release(int64_t n, const int32_t *pages);
+    slora_status share(int64_t n, const int32_t *pages);
     int64_t num_free() const { return (int64_t)free_stack.size(); }
 };
 

@@ -346,6 +346,69 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
 }
 
+extern "C" slora_status slora_kv_copy(slora_kv_t k, int64_t n, const int32_t *src, const int32_t *dst, const int32_t *rows,
+                                      slora_stream_t stream)
+{
+    if (!k)
+        return fail(SLORA_ERR_INVALID_ARG, "kv_copy: null cache");
+    if (n < 0 || n > INT32_MAX || (n > 0 && (!src || !dst)) || !aligned4(src) || !aligned4(dst) || !aligned4(rows))
+        return fail(SLORA_ERR_INVALID_ARG, "kv_copy: n=%lld, or a list is null or misaligned", (long long)n);
+    if (n == 0)
+        return SLORA_OK;
+    const kv::CopyArgs a = {k->c, (int32_t)n, src, dst, rows, k->head_dim};
+    DeviceScope dev_scope(k->device);
+    cudaError_t e = dev_scope.error();
+    int launches = 0;
+    if (e == cudaSuccess)
+        e = kv::launch_copy(a, k->num_sms, (cudaStream_t)stream, &launches);
+    *k->launches += launches;
+    return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "kv_copy: %s", cudaGetErrorString(e));
+}
+
+extern "C" slora_status slora_kv_compact(slora_kv_t k, const slora_kv_keep *keep, slora_stream_t stream)
+{
+    const char *fn = "kv_compact";
+    if (!k || !keep)
+        return fail(SLORA_ERR_INVALID_ARG, "%s: null cache or lists", fn);
+    if (keep->n_seqs < 0 || keep->n_seqs > (1 << 20) || keep->n_kept < 0 || keep->n_kept > (1 << 30) || keep->max_kept < 0 ||
+        keep->max_kept > (1 << 30) || keep->max_blocks < 1 || (keep->dst_table && keep->dst_blocks < 1) ||
+        (keep->kept_head_stride != 0 && keep->kept_head_stride < keep->n_kept))
+        return fail(SLORA_ERR_INVALID_ARG, "%s: n_seqs=%d n_kept=%d max_kept=%d max_blocks=%d dst_blocks=%d kept_head_stride=%lld", fn,
+                    keep->n_seqs, keep->n_kept, keep->max_kept, keep->max_blocks, keep->dst_blocks,
+                    (long long)keep->kept_head_stride);
+    if (keep->n_seqs > 0 && (!keep->kept_indptr || !keep->kv_len || !keep->block_table || (keep->n_kept > 0 && !keep->kept)))
+        return fail(SLORA_ERR_INVALID_ARG, "%s: null kept_indptr, kept, kv_len or block_table", fn);
+    for (const void *p : {(const void *)keep->kept_indptr, (const void *)keep->kept, (const void *)keep->first,
+                          (const void *)keep->kv_len, (const void *)keep->block_table, (const void *)keep->dst_table,
+                          (const void *)keep->new_len})
+        if (!aligned4(p))
+            return fail(SLORA_ERR_INVALID_ARG, "%s: a misaligned array", fn);
+    if (keep->n_seqs == 0)
+        return SLORA_OK;
+    kv::CompactArgs a = {};
+    a.c = k->c;
+    a.S = keep->n_seqs;
+    a.n_kept = keep->n_kept;
+    a.max_kept = keep->max_kept < keep->n_kept ? keep->max_kept : keep->n_kept;
+    a.max_blocks = keep->max_blocks;
+    a.dst_blocks = keep->dst_table ? keep->dst_blocks : keep->max_blocks;
+    a.indptr = keep->kept_indptr;
+    a.kept = keep->kept;
+    a.first = keep->first;
+    a.kv_len = keep->kv_len;
+    a.table = keep->block_table;
+    a.dst_table = keep->dst_table;
+    a.head_stride = keep->kept_head_stride;
+    a.new_len = keep->new_len;
+    DeviceScope dev_scope(k->device);
+    cudaError_t e = dev_scope.error();
+    int launches = 0;
+    if (e == cudaSuccess)
+        e = kv::launch_compact(a, k->head_dim, k->format, k->num_sms, (cudaStream_t)stream, &launches);
+    *k->launches += launches;
+    return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
 extern "C" slora_status slora_debug_kv_give_up(int32_t cta)
 {
     if (cta < -1)

@@ -287,6 +287,23 @@ __device__ __forceinline__ uint32_t nan_bytes(uint32_t w)
 cudaError_t launch_append(const AppendArgs &a, bool norm, int head_dim, int fmt, int num_sms, cudaStream_t stream,
                           int *launches);
 
+struct CopyArgs {
+    Cache c;
+    int32_t n;
+    const int32_t *src, *dst, *rows;    // rows nullptr: whole blocks
+    int32_t row_bytes;
+};
+cudaError_t launch_copy(const CopyArgs &a, int num_sms, cudaStream_t stream, int *launches);
+
+struct CompactArgs {
+    Cache c;
+    int32_t S, n_kept, max_kept, max_blocks, dst_blocks;
+    const int32_t *indptr, *kept, *first, *kv_len, *table, *dst_table;     // dst_table nullptr: in place; first nullptr: 0
+    int64_t head_stride;
+    int32_t *new_len;
+};
+cudaError_t launch_compact(const CompactArgs &a, int head_dim, int fmt, int num_sms, cudaStream_t stream, int *launches);
+
 // The attention's workspace: partial results of rows whose keys are split over several CTAs, and
 // the words of their joins (zero at first).
 size_t decode_workspace_bytes(int num_sms);

@@ -95,8 +95,38 @@ slora_status PageAlloc::release(int64_t n, const int32_t *pages)
         seen.push_back(p);
     }
     for (int32_t p : seen) {
+        if (!extra.empty() && extra[(size_t)p] > 0) {
+            --extra[(size_t)p];
+            allocated[(size_t)p] = 1;
+            continue;
+        }
         allocated[(size_t)p] = 0;
         free_stack.push_back(p);
+    }
+    return SLORA_OK;
+}
+
+slora_status PageAlloc::share(int64_t n, const int32_t *pages)
+{
+    if (n < 0 || (n > 0 && pages == nullptr))
+        return fail(SLORA_ERR_INVALID_ARG, "page share: n=%lld", (long long)n);
+    for (int64_t i = 0; i < n; ++i)
+        if (pages[i] < 0 || pages[i] >= num_pages || !allocated[(size_t)pages[i]])
+            return fail(SLORA_ERR_INVALID_ARG, "page share: page %d is out of range or not allocated", pages[i]);
+    if (n > 0 && extra.empty()) {
+        try {
+            extra.assign((size_t)num_pages, 0);
+        } catch (...) {
+            return fail(SLORA_ERR_HOST_ALLOC, "page share: %lld pages", (long long)num_pages);
+        }
+    }
+    for (int64_t i = 0; i < n; ++i) {
+        if (extra[(size_t)pages[i]] == INT32_MAX) {
+            while (i-- > 0)
+                --extra[(size_t)pages[i]];
+            return fail(SLORA_ERR_INVALID_ARG, "page share: too many holders of a page");
+        }
+        ++extra[(size_t)pages[i]];
     }
     return SLORA_OK;
 }
@@ -211,6 +241,13 @@ slora_status slora_pagealloc_free(slora_pagealloc_t a, int64_t n, const int32_t 
     if (!a)
         return fail(SLORA_ERR_INVALID_ARG, "pagealloc_free: null allocator");
     return a->a.release(n, pages);
+}
+
+slora_status slora_pagealloc_share(slora_pagealloc_t a, int64_t n, const int32_t *pages)
+{
+    if (!a)
+        return fail(SLORA_ERR_INVALID_ARG, "pagealloc_share: null allocator");
+    return a->a.share(n, pages);
 }
 
 slora_status slora_pagealloc_num_free(slora_pagealloc_t a, int64_t *out)

@@ -260,6 +260,13 @@ slora_status slora_pages_free(slora_pool_t p, int64_t n, const int32_t *pages, s
     return SLORA_OK;
 }
 
+slora_status slora_pages_share(slora_pool_t p, int64_t n, const int32_t *pages)
+{
+    if (!p)
+        return fail(SLORA_ERR_INVALID_ARG, "pages_share: null pool");
+    return p->pages.share(n, pages);
+}
+
 slora_status slora_adapter_register(slora_pool_t p, int32_t id, int32_t rank, float scaling,
                                     const uint16_t *At_host, const uint16_t *B_host)
 {
