@@ -568,6 +568,12 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * Attends over one pool, of whichever cache, share its workspace: issue them on one stream,
  * or order the streams.
  *
+ * slora_kv_attend_sinks(): causal attention in a window with the sequence's first tokens, the sinks, still visible: the
+ * token at position p sees the positions p - window + 1 .. p and those below n_sinks (up to p), each once.
+ * window is 1 or more, n_sinks 0 .. 2^30 (0: slora_kv_attend with that window); the other arguments, and what is said of
+ * them, are those of slora_kv_attend.  Blocks wholly between the sinks and the windows are not read: their pages can
+ * be given back and their entries of the block table be -1, as in a stream that never ends.
+ *
  * slora_kv_copy(): copies pages of the cache, rows and exponents, within the pool: a forked sequence gets its own
  * copy of the block that both would go on to write, and shares the others (slora_pages_share).
  *   n            pages, 0 <= n < 2^31
@@ -675,6 +681,9 @@ slora_status slora_kv_append_norm(slora_kv_t kv, const slora_kv_batch *batch /*h
                                   const void *v, int64_t v_stride, const void *q, int64_t q_stride, void *q_out,
                                   int64_t q_out_stride, int32_t n_q_heads, const slora_kv_norm *norm /*host*/,
                                   const slora_kv_rope *rope /*host*/, slora_stream_t stream);
+slora_status slora_kv_attend_sinks(slora_kv_t kv, const slora_kv_batch *batch /*host*/, const void *q, int64_t q_stride,
+                                   int32_t n_q_heads, void *out, int64_t out_stride, float *lse, float softmax_scale,
+                                   int32_t window, int32_t n_sinks, slora_stream_t stream);
 slora_status slora_kv_copy(slora_kv_t kv, int64_t n, const int32_t *src, const int32_t *dst, const int32_t *rows,
                            slora_stream_t stream);
 slora_status slora_kv_compact(slora_kv_t kv, const slora_kv_keep *keep /*host*/, slora_stream_t stream);

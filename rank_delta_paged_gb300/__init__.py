@@ -45,7 +45,7 @@ __all__ = [
     "slora_bmm_workspace_bytes", "slora_lora_apply_bmm",
     "SLORA_KV_E4M3", "SLORA_KV_INT8", "KVBatch", "KVRope", "KVNorm", "KVKeep",
     "slora_kv_create", "slora_kv_destroy", "slora_kv_block_tokens", "slora_kv_exponents",
-    "slora_kv_append", "slora_kv_append_norm", "slora_kv_copy", "slora_kv_compact", "slora_kv_attend", "slora_debug_kv_give_up",
+    "slora_kv_append", "slora_kv_append_norm", "slora_kv_copy", "slora_kv_compact", "slora_kv_attend", "slora_kv_attend_sinks", "slora_debug_kv_give_up",
 ]
 
 _I32, _I64, _U64, _F32, _P = ctypes.c_int32, ctypes.c_int64, ctypes.c_uint64, ctypes.c_float, ctypes.c_void_p
@@ -118,6 +118,7 @@ _SIGS = {
     "slora_kv_copy": [_P, _I64, _P, _P, _P, _P],
     "slora_kv_compact": [_P, _P, _P],
     "slora_kv_attend": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
+    "slora_kv_attend_sinks": [_P, _P, _P, _I64, _I32, _P, _I64, _P, _F32, _I32, _I32, _P],
     "slora_debug_kv_give_up": [_I32],
 }
 _RESTYPE = {"slora_status_str": ctypes.c_char_p, "slora_last_error": ctypes.c_char_p,
@@ -541,6 +542,12 @@ def slora_kv_attend(kv: int, batch: KVBatch, q, q_stride: int, n_q_heads: int, o
                     softmax_scale: float = 1.0, causal: bool = True, window: int = 0, stream=None) -> None:
     _call("slora_kv_attend", kv, batch.ref, _ptr(q), q_stride, n_q_heads, _ptr(out), out_stride, _ptr(lse),
           softmax_scale, int(causal), window, _stream(stream))
+
+
+def slora_kv_attend_sinks(kv: int, batch: KVBatch, q, q_stride: int, n_q_heads: int, out, out_stride: int, lse=None,
+                          softmax_scale: float = 1.0, window: int = 0, n_sinks: int = 0, stream=None) -> None:
+    _call("slora_kv_attend_sinks", kv, batch.ref, _ptr(q), q_stride, n_q_heads, _ptr(out), out_stride, _ptr(lse),
+          softmax_scale, window, n_sinks, _stream(stream))
 
 
 def slora_adapter_pages(pool: int, adapter_id: int, proj: int, out) -> None:

@@ -281,11 +281,12 @@ extern "C" slora_status slora_kv_append_norm(slora_kv_t k, const slora_kv_batch 
     return append(fn, k, batch, kk, k_stride, v, v_stride, q, q_stride, q_out, q_out_stride, n_q_heads, norm, rope, stream);
 }
 
-extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batch, const void *q, int64_t q_stride,
-                                        int32_t n_q_heads, void *out, int64_t out_stride, float *lse,
-                                        float softmax_scale, int32_t causal, int32_t window, slora_stream_t stream)
+namespace {
+
+slora_status attend(const char *fn, slora_kv_t k, const slora_kv_batch *batch, const void *q, int64_t q_stride,
+                    int32_t n_q_heads, void *out, int64_t out_stride, float *lse, float softmax_scale, int32_t causal,
+                    int32_t window, int32_t sinks, slora_stream_t stream)
 {
-    const char *fn = "kv_attend";
     kv::AttendArgs a = {};
     slora_status st = check_batch(fn, k, batch, &a.b);
     if (st != SLORA_OK)
@@ -321,6 +322,7 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
     a.scale_log2 = (float)((double)softmax_scale * 1.4426950408889634);
     a.causal = causal;
     a.window = window;
+    a.sinks = sinks;
     a.give_up = g_give_up.load();
     DeviceScope dev_scope(k->device);
     cudaError_t e = dev_scope.error();
@@ -344,6 +346,25 @@ extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batc
                                      (cudaStream_t)stream, &launches);
     *k->launches += launches;
     return e == cudaSuccess ? SLORA_OK : fail(SLORA_ERR_CUDA, "%s: %s", fn, cudaGetErrorString(e));
+}
+
+}  // namespace
+
+extern "C" slora_status slora_kv_attend(slora_kv_t k, const slora_kv_batch *batch, const void *q, int64_t q_stride,
+                                        int32_t n_q_heads, void *out, int64_t out_stride, float *lse,
+                                        float softmax_scale, int32_t causal, int32_t window, slora_stream_t stream)
+{
+    return attend("kv_attend", k, batch, q, q_stride, n_q_heads, out, out_stride, lse, softmax_scale, causal, window, 0, stream);
+}
+
+extern "C" slora_status slora_kv_attend_sinks(slora_kv_t k, const slora_kv_batch *batch, const void *q, int64_t q_stride,
+                                              int32_t n_q_heads, void *out, int64_t out_stride, float *lse,
+                                              float softmax_scale, int32_t window, int32_t n_sinks, slora_stream_t stream)
+{
+    const char *fn = "kv_attend_sinks";
+    if (n_sinks < 0 || n_sinks > (1 << 30) || window < 1)
+        return fail(SLORA_ERR_INVALID_ARG, "%s: window=%d n_sinks=%d", fn, window, n_sinks);
+    return attend(fn, k, batch, q, q_stride, n_q_heads, out, out_stride, lse, softmax_scale, 1, window, n_sinks, stream);
 }
 
 extern "C" slora_status slora_kv_copy(slora_kv_t k, int64_t n, const int32_t *src, const int32_t *dst, const int32_t *rows,

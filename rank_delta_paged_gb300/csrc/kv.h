@@ -77,6 +77,7 @@ struct AttendArgs {
     uint32_t group_inverse;             // ceil(2^32 / group), 0 for 1
     float scale_log2;                   // softmax scale * log2(e)
     int32_t causal, window;
+    int32_t sinks;                      // with a window: the first tokens, which stay visible
     int32_t give_up;                    // test hook: this CTA gives up at its start; -1: none
 };
 
@@ -153,6 +154,18 @@ __device__ __forceinline__ int32_t end_key(const AttendArgs &a, const Seq &q, in
     if (!a.causal) return q.len;
     const int32_t p = q.len - q.n + tok + 1;
     return p > 0 ? p : 0;
+}
+
+// With sinks a row sees the keys [0, sinks) as well as its window's.  Where the windows of some rows have left R tokens or
+// more between the two, the rows' keys are numbered anew without them, so that the sinks take no tile of their own:
+// number v below `sinks` rounded up to R is key v, a later one key v + shift.  What is made of a sequence's length
+// (first_key, end_key) is in the new numbers once the length is shorter by the shift, which is returned; `first` is the
+// first key in any of the rows' windows.
+__device__ __forceinline__ int32_t sinks_end(const AttendArgs &a, int32_t R) { return (a.sinks + R - 1) & -R; }
+__device__ __forceinline__ int32_t key_shift(const AttendArgs &a, int32_t first, int32_t R)
+{
+    const int32_t gap = (first & -R) - sinks_end(a, R);
+    return gap > 0 ? gap : 0;
 }
 
 // Milliseconds or so, to be compared by differences.

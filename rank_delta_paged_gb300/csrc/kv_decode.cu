@@ -157,22 +157,29 @@ struct DecodeParams {
     Joins joins;           // a word per CTA: the unit that starts there and goes on in others
 };
 
-// Tiles of sequence s: tiles per unit, units per KV head.
-__device__ __forceinline__ void seq_tiles(const DecodeParams &p, const Seq &q, int32_t *tiles, int32_t *groups,
-                                          int32_t *first)
+// Tiles of sequence s: tiles per unit, units per KV head.  With sinks its length becomes one of the numbers that
+// key_shift gives its keys.
+template <bool SINKS>
+__device__ __forceinline__ void seq_tiles(const DecodeParams &p, Seq &q, int32_t *tiles, int32_t *groups,
+                                          int32_t *first, int32_t *shift)
 {
     *tiles = 0;
     *groups = 0;
     *first = 0;
+    *shift = 0;
     const int64_t rows = (int64_t)q.n * p.a.group;
     if (q.n == 0 || rows > p.small_rows) return;
-    const int32_t lo = first_key(p.a, q, 0) / kTile, hi = (end_key(p.a, q, q.n - 1) + kTile - 1) / kTile;
+    if (SINKS) {
+        *shift = key_shift(p.a, first_key(p.a, q, 0), p.box_rows);
+        q.len -= *shift;
+    }
+    const int32_t lo = SINKS ? 0 : first_key(p.a, q, 0) / kTile, hi = (end_key(p.a, q, q.n - 1) + kTile - 1) / kTile;
     *tiles = hi > lo ? hi - lo : 1;     // a row that sees nothing still writes zeros
     *groups = (int32_t)((rows + p.rows - 1) >> (p.rows == 8 ? 3 : 4));
     *first = lo;
 }
 
-template <int D, int NT, int FMT>
+template <int D, int NT, int FMT, bool SINKS>
 __global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas)
 attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PageMaps maps)
 {
@@ -226,8 +233,9 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         int64_t t = 0;
 #pragma unroll 1
         for (int64_t s = (int64_t)c * per + lane; s < S && s < (int64_t)(c + 1) * per; s += 32) {
-            int32_t tiles, groups, first;
-            seq_tiles(p, load_seq(a, (int32_t)s, &bad), &tiles, &groups, &first);
+            int32_t tiles, groups, first, shift;
+            Seq q = load_seq(a, (int32_t)s, &bad);
+            seq_tiles<SINKS>(p, q, &tiles, &groups, &first, &shift);
             t += (int64_t)(tiles + kUnitCost) * groups;
         }
 #pragma unroll
@@ -269,14 +277,14 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         }
         int32_t s32 = chunk * per;               // first of the 32 sequences that the lanes hold
         Seq q;
-        int32_t tiles, groups, first;
+        int32_t tiles, groups, first, shift;
         auto hold = [&](int32_t s) {
             q.n = 0;
-            tiles = groups = first = 0;
+            tiles = groups = first = shift = 0;
             int32_t ignore;
             if (s + lane < S) {
                 q = load_seq(a, s + lane, &ignore);
-                seq_tiles(p, q, &tiles, &groups, &first);
+                seq_tiles<SINKS>(p, q, &tiles, &groups, &first, &shift);
             }
         };
         int at_lane = 0;
@@ -306,7 +314,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
         }
         // position in the list: sequence, KV head, row group, tile
         int32_t u_tiles = __shfl_sync(~0u, tiles, at_lane), u_groups = __shfl_sync(~0u, groups, at_lane);
-        int32_t u_first = __shfl_sync(~0u, first, at_lane);
+        int32_t u_first = __shfl_sync(~0u, first, at_lane), u_shift = SINKS ? __shfl_sync(~0u, shift, at_lane) : 0;
         int64_t in_seq = w0 - base;
         int32_t head = div_list(in_seq, (int64_t)(u_tiles + kUnitCost) * u_groups);
         in_seq -= (int64_t)head * (u_tiles + kUnitCost) * u_groups;
@@ -341,6 +349,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 un.plain_lo = first_key(a, u, div_group(a, r1 - 1));
                 un.plain_hi = end_key(a, u, div_group(a, un.r0));
             }
+            if (SINKS && un.plain_lo <= a.sinks) un.plain_lo = 0;
             un.table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
         };
         bool fresh = true;              // the unit has yet to be entered
@@ -370,10 +379,11 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
             // this lane's tile is t of the unit, at `at` in the list
             auto fill = [&](int32_t t, int64_t at, bool first) {
                 const int32_t j0 = (u_first + t) * kTile, j = j0 + gl * R;
-                m.want = j < un.hi && j + R > un.lo;
+                m.want = j < un.hi && (j + R > un.lo || (SINKS && j < a.sinks));
                 if (m.want) {
-                    int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
-                    m.row = j - blk * a.c.bt;
+                    const int32_t key = SINKS && j >= sinks_end(a, R) ? j + u_shift : j;
+                    int32_t blk = (int32_t)__umulhi((uint32_t)key, p.bt_inverse);
+                    m.row = key - blk * a.c.bt;
                     if (m.row < 0) {
                         --blk;
                         m.row += a.c.bt;
@@ -384,7 +394,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     int4 *mi = reinterpret_cast<int4 *>(&ms->plain);
                     const bool end = t == u_tiles - 1, last = end || at == w1 - 1;
                     const bool run_end = at + 1 + (end ? kUnitCost : 0) >= w1;
-                    mi[0] = make_int4(j0 >= un.plain_lo && j0 + kTile <= un.plain_hi, first || t == 0,
+                    mi[0] = make_int4((j0 >= un.plain_lo || (SINKS && j0 + kTile <= a.sinks)) && j0 + kTile <= un.plain_hi,
+                                      first || t == 0,
                                       (last ? 1 : 0) | (run_end ? 2 : 0), un.whole);
                     mi[1] = make_int4(j0, u.row0, u.n, u.len);
                     mi[2] = make_int4(head, un.r0, un.c0, un.c1);
@@ -416,6 +427,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                             u_tiles = __shfl_sync(~0u, tiles, at_lane);
                             u_groups = __shfl_sync(~0u, groups, at_lane);
                             u_first = __shfl_sync(~0u, first, at_lane);
+                            if (SINKS) u_shift = __shfl_sync(~0u, shift, at_lane);
                             u.row0 = __shfl_sync(~0u, q.row0, at_lane);
                             u.n = __shfl_sync(~0u, q.n, at_lane);
                             u.len = __shfl_sync(~0u, q.len, at_lane);
@@ -491,16 +503,21 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                 const int4 row = uniform(*reinterpret_cast<const int4 *>(m.row));
                 const int4 kp = uniform(*reinterpret_cast<const int4 *>(m.page[0]));
                 const int4 vp = uniform(*reinterpret_cast<const int4 *>(m.page[1]));
-                if (ok == 0xFFu && row.y && row.z && row.w) {
+                // (with sinks: unless it does not follow it there)
+                auto joined = [&](int32_t r0, int32_t r1, int32_t k0, int32_t k1, int32_t v0, int32_t v1) {
+                    return SINKS ? r1 == r0 + 16 && k1 == k0 && v1 == v0 : r1 != 0;
+                };
+                const bool xy = joined(row.x, row.y, kp.x, kp.y, vp.x, vp.y), zw = joined(row.z, row.w, kp.z, kp.w, vp.z, vp.w);
+                if (ok == 0xFFu && xy && zw && joined(row.y, row.z, kp.y, kp.z, vp.y, vp.z)) {
                     copy(0, 2, row.x, kp.x, vp.x);
                 } else {
-                    if ((ok & 15u) == 15u && row.y) {
+                    if ((ok & 15u) == 15u && xy) {
                         copy(0, 1, row.x, kp.x, vp.x);
                     } else {
                         if (ok & 1u) copy(0, 0, row.x, kp.x, vp.x);
                         if (ok & 4u) copy(1, 0, row.y, kp.y, vp.y);
                     }
-                    if ((ok & 0xF0u) == 0xF0u && row.w) {
+                    if ((ok & 0xF0u) == 0xF0u && zw) {
                         copy(2, 1, row.z, kp.z, vp.z);
                     } else {
                         if (ok & 16u) copy(2, 0, row.z, kp.z, vp.z);
@@ -709,8 +726,8 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                     const int r = 8 * t + 2 * c + x;
                     const int tok = div_group(a, m.r0 + (r < nrows ? r : 0));
                     const int lo = first_key(a, q, tok), hi = end_key(a, q, tok);
-                    if (!(ok0 && j0 >= lo && j0 < hi)) sc[t][x] = -INFINITY;
-                    if (!(ok1 && j1 >= lo && j1 < hi)) sc[t][2 + x] = -INFINITY;
+                    if (!(ok0 && (j0 >= lo || (SINKS && j0 < a.sinks)) && j0 < hi)) sc[t][x] = -INFINITY;
+                    if (!(ok1 && (j1 >= lo || (SINKS && j1 < a.sinks)) && j1 < hi)) sc[t][2 + x] = -INFINITY;
                 }
         }
         // A row's reference is taken up only when a score passes it by kMaxWeight (the first one always
@@ -762,7 +779,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
 #pragma unroll
             for (int x = 0; x < 4; ++x) {
                 const int j = m.j0 + warp * 16 + vrow[x];
-                const bool ok = (m.ok >> (2 * warp + (x >> 1)) & 1) && j >= lo && j < hi;
+                const bool ok = (m.ok >> (2 * warp + (x >> 1)) & 1) && (j >= lo || (SINKS && j < a.sinks)) && j < hi;
 #pragma unroll
                 for (int i = 0; i < D / 32; ++i) vw[x][i] = ok ? vw[x][i] : 0u;
             }
@@ -794,7 +811,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
                             for (int x = 0; x < 2; ++x) {
                                 const int r = 8 * t + 2 * c + x;
                                 const int tok = div_group(a, m.r0 + (r < nrows ? r : 0));
-                                const uint32_t see = j >= first_key(a, q, tok) && j < end_key(a, q, tok) ? set : 0u;
+                                const uint32_t see = (j >= first_key(a, q, tok) || (SINKS && j < a.sinks)) && j < end_key(a, q, tok) ? set : 0u;
 #pragma unroll
                                 for (int h = 0; h < D / 8; ++h)
                                     if (see >> h & 1u) o[t][h >> 1][x + 2 * (h & 1)] = __int_as_float(0x7FFFFFFF);
@@ -957,7 +974,7 @@ attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_consta
     }
 }
 
-template <int D, int NT, int FMT>
+template <int D, int NT, int FMT, bool SINKS>
 cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cudaStream_t stream)
 {
     static std::mutex mu;
@@ -968,7 +985,7 @@ cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cud
     {
         std::lock_guard<std::mutex> lk(mu);
         if (dev >= 64 || !set[dev]) {
-            e = cudaFuncSetAttribute(attend_decode_kernel<D, NT, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(attend_decode_kernel<D, NT, FMT, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)Shape<D, NT>::kSmem);
             if (e != cudaSuccess) return e;
             if (dev < 64) set[dev] = true;
@@ -984,17 +1001,17 @@ cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cud
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<D, NT, FMT>, p, maps);
+    return cudaLaunchKernelEx(&cfg, attend_decode_kernel<D, NT, FMT, SINKS>, p, maps);
 }
 
-template <int D>
+template <int D, bool SINKS>
 cudaError_t launch_d(const DecodeParams &p, const PageMaps &maps, int fmt, int num_sms, cudaStream_t stream)
 {
     if (p.rows == 8)
-        return fmt == SLORA_KV_E4M3 ? launch<D, 1, SLORA_KV_E4M3>(p, maps, num_sms, stream)
-                                    : launch<D, 1, SLORA_KV_INT8>(p, maps, num_sms, stream);
-    return fmt == SLORA_KV_E4M3 ? launch<D, 2, SLORA_KV_E4M3>(p, maps, num_sms, stream)
-                                : launch<D, 2, SLORA_KV_INT8>(p, maps, num_sms, stream);
+        return fmt == SLORA_KV_E4M3 ? launch<D, 1, SLORA_KV_E4M3, SINKS>(p, maps, num_sms, stream)
+                                    : launch<D, 1, SLORA_KV_INT8, SINKS>(p, maps, num_sms, stream);
+    return fmt == SLORA_KV_E4M3 ? launch<D, 2, SLORA_KV_E4M3, SINKS>(p, maps, num_sms, stream)
+                                : launch<D, 2, SLORA_KV_INT8, SINKS>(p, maps, num_sms, stream);
 }
 
 }  // namespace
@@ -1024,8 +1041,11 @@ cudaError_t launch_attend_decode(const AttendArgs &a, const PageMaps &maps, int 
     p.part = static_cast<float *>(ws);
     p.joins.started = reinterpret_cast<unsigned long long *>(p.part + (size_t)num_sms * kMaxCtas * 2 * kPartStride);
     p.joins.word = p.joins.started + 1;
-    cudaError_t e = head_dim == 128 ? launch_d<128>(p, maps, fmt, num_sms, stream)
-                                    : launch_d<64>(p, maps, fmt, num_sms, stream);
+    cudaError_t e;
+    if (head_dim == 128)
+        e = a.sinks > 0 ? launch_d<128, true>(p, maps, fmt, num_sms, stream) : launch_d<128, false>(p, maps, fmt, num_sms, stream);
+    else
+        e = a.sinks > 0 ? launch_d<64, true>(p, maps, fmt, num_sms, stream) : launch_d<64, false>(p, maps, fmt, num_sms, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }

@@ -159,7 +159,7 @@ __device__ __forceinline__ void sts128(uint32_t ad, uint32_t a, uint32_t b, uint
 // the row does not see is NaN, it sums the channel again over the keys that it sees, by the reference and the sum that the
 // softmax has found (inv < 0: not this row).  (Channels that are NaN by a key which every row sees are right as they are.)  Rare, and
 // slow: abort[1] tells the waits of the CTA's other warps that it goes on.
-template <int D, int FMT>
+template <int D, int FMT, bool SINKS>
 static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t row0, int32_t head, int32_t r, int32_t rend, float base,
                                               float inv, volatile int *abort)
 {
@@ -198,6 +198,7 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
         const float m = __shfl_sync(~0u, base, l), iv = __shfl_sync(~0u, inv, l);
         const int32_t tok = div_group(a, rr), qh = head * a.group + (rr - tok * a.group);
         const int32_t k0 = first_key(a, q, tok), k1 = end_key(a, q, tok);
+        const int32_t before = !SINKS ? 0 : a.sinks < k0 ? a.sinks : k0;       // sinks in front of the window
         __half *out = a.out + (int64_t)(q.row0 + tok) * a.out_stride + (int64_t)qh * D + CL * lane;
         uint32_t odd = 0;                                // channels: bit 8 c + 7, as nan_bytes has them
 #pragma unroll
@@ -206,10 +207,17 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
         if (!__any_sync(~0u, odd != 0)) continue;
         uint32_t unseen = 0;
 #pragma unroll 1
-        for (int32_t k = first; k < end; ++k) {
+        for (int32_t k = SINKS ? 0 : first; k < end; ++k) {
             if (k >= k0 && k < k1) {
                 k = k1 - 1;
                 continue;
+            }
+            if (SINKS) {
+                if (k < a.sinks && k < k1) continue;
+                if (k >= a.sinks && k < first) {
+                    k = first - 1;
+                    continue;
+                }
             }
             int32_t kp, vp, row;
             if (place(k, kp, vp, row)) unseen |= nan_bytes(codes(vp * a.c.page_bytes + row));
@@ -219,13 +227,14 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
         const uint4 *query = reinterpret_cast<const uint4 *>(a.q + (int64_t)(q.row0 + tok) * a.q_stride + (int64_t)qh * D);
         float o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll 1
-        for (int32_t kb = k0; kb < k1; kb += 32) {
+        for (int32_t kb = k0 - before; kb < k1; kb += 32) {
             if (lane == 0) abort[1] = work_clock(global_timer_ns());
             // a key per lane, then a channel per lane
             int32_t kp, vp, row;
             float e = 0.f;
             int64_t at = -1;
-            if (kb + lane < k1 && place(kb + lane, kp, vp, row)) {
+            const int32_t key = kb + lane < k0 ? kb + lane - (k0 - before) : kb + lane;
+            if (kb + lane < k1 && place(key, kp, vp, row)) {
                 at = vp * a.c.page_bytes + row;
                 const uint4 *key = reinterpret_cast<const uint4 *>(a.c.pool + kp * a.c.page_bytes + row);
                 float dot = 0.f;
@@ -272,14 +281,21 @@ static __device__ __noinline__ void sum_again(const PrefillParams &p, int32_t ro
 
 struct Tiles {
     int32_t lo, hi;        // key tiles [lo, hi) of a unit, one at least
+    int32_t shift;         // with sinks: key_shift of its rows, and what follows is in those numbers
     int32_t k0, k1;        // keys
     int32_t b[2], e[2];    // key tiles that row tile t sees
 };
-__device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, int32_t r0, int32_t r1, Tiles &t)
+template <bool SINKS>
+__device__ __forceinline__ void unit_tiles(const AttendArgs &a, Seq q, int32_t r0, int32_t r1, int32_t R, Tiles &t)
 {
+    t.shift = 0;
+    if (SINKS) {
+        t.shift = key_shift(a, first_key(a, q, div_group(a, r0)), R);
+        q.len -= t.shift;
+    }
     t.k0 = first_key(a, q, div_group(a, r0));
     t.k1 = end_key(a, q, div_group(a, r1 - 1));
-    t.lo = t.k0 / kTile;
+    t.lo = SINKS ? 0 : t.k0 / kTile;
     t.hi = (t.k1 + kTile - 1) / kTile;
     if (t.hi <= t.lo) t.hi = t.lo + 1;
 #pragma unroll
@@ -289,21 +305,23 @@ __device__ __forceinline__ void unit_tiles(const AttendArgs &a, const Seq &q, in
         if (x0 < x1) {
             const int32_t k0 = first_key(a, q, div_group(a, x0)), k1 = end_key(a, q, div_group(a, x1 - 1));
             if (k1 > k0) {
-                t.b[i] = k0 / kTile;
+                t.b[i] = SINKS ? 0 : k0 / kTile;      // (at most two tiles lie between the sinks and row tile 1's window)
                 t.e[i] = (k1 + kTile - 1) / kTile;
             }
         }
     }
 }
 // Its places in the list: the tiles, then kUnitCost empty ones.
-__device__ __forceinline__ int32_t unit_count(const AttendArgs &a, const Seq &q, int32_t rows, int32_t rt)
+template <bool SINKS>
+__device__ __forceinline__ int32_t unit_count(const AttendArgs &a, Seq q, int32_t rows, int32_t rt, int32_t R)
 {
     const int32_t r0 = rt * kRows, r1 = rows < r0 + kRows ? rows : r0 + kRows;
-    const int32_t lo = first_key(a, q, div_group(a, r0)) / kTile, hi = (end_key(a, q, div_group(a, r1 - 1)) + kTile - 1) / kTile;
+    if (SINKS) q.len -= key_shift(a, first_key(a, q, div_group(a, r0)), R);
+    const int32_t lo = SINKS ? 0 : first_key(a, q, div_group(a, r0)) / kTile, hi = (end_key(a, q, div_group(a, r1 - 1)) + kTile - 1) / kTile;
     return (hi > lo ? hi - lo : 1) + kUnitCost;
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool SINKS>
 __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __grid_constant__ PrefillParams p)
 {
     using Sh = Shape<D>;
@@ -383,7 +401,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 u.len = __shfl_sync(~0u, q.len, l);
                 const int32_t rows = u.n * a.group;
 #pragma unroll 1
-                for (int32_t rt = lane; rt * kRows < rows; rt += 32) t += unit_count(a, u, rows, rt);
+                for (int32_t rt = lane; rt * kRows < rows; rt += 32) t += unit_count<SINKS>(a, u, rows, rt, p.box_rows);
             }
         }
 #pragma unroll
@@ -456,7 +474,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         while (next_seq()) {
             int64_t t = 0;
 #pragma unroll 1
-            for (int32_t i = lane; i * kRows < rows; i += 32) t += unit_count(a, u, rows, i);
+            for (int32_t i = lane; i * kRows < rows; i += 32) t += unit_count<SINKS>(a, u, rows, i, p.box_rows);
 #pragma unroll
             for (int o = 16; o; o >>= 1) t += __shfl_xor_sync(~0u, t, o);
             if (base + t * a.c.n_kv > w0) {
@@ -471,7 +489,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
 #pragma unroll 1
         while (found) {
             const int32_t i = rt + lane;
-            const int32_t mine = (int64_t)i * kRows < rows ? unit_count(a, u, rows, i) : 0;
+            const int32_t mine = (int64_t)i * kRows < rows ? unit_count<SINKS>(a, u, rows, i, p.box_rows) : 0;
             int32_t sum = mine;
 #pragma unroll
             for (int o = 1; o < 32; o <<= 1) {
@@ -502,7 +520,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
         auto enter = [&](int64_t u0) {             // the unit starts at u0 of the list
             r0 = rt * kRows;
             r1 = rows < r0 + kRows ? rows : r0 + kRows;
-            unit_tiles(a, u, r0, r1, ut);
+            unit_tiles<SINKS>(a, u, r0, r1, p.box_rows, ut);
             const int64_t u1 = u0 + ut.hi - ut.lo;
             whole = u0 >= w0 && u1 <= w1;
             c0 = c1 = 0;
@@ -518,8 +536,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 if (ut.b[t] < ta) ut.b[t] = ta;
                 if (ut.e[t] > tb) ut.e[t] = tb;
             }
-            plain_lo = first_key(a, u, div_group(a, r1 - 1));
-            plain_hi = end_key(a, u, div_group(a, r0));
+            const Seq v = {u.row0, u.n, u.len - ut.shift};
+            plain_lo = first_key(a, v, div_group(a, r1 - 1));
+            plain_hi = end_key(a, v, div_group(a, r0));
+            if (SINKS && plain_lo <= a.sinks) plain_lo = 0;
             table = a.b.table + ((int64_t)(s32 + at_lane) * a.b.max_blocks * a.c.n_kv + head) * 2;
         };
         int64_t u0 = base;
@@ -564,10 +584,11 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 slot_parity ^= 1;
             }
             const int32_t j0 = tile * kTile, j = j0 + (8 * gl & -R);      // first token of the box
-            x.want = j < ut.k1 && j + R > ut.k0;
+            x.want = j < ut.k1 && (j + R > ut.k0 || (SINKS && j < a.sinks));
             if (x.want) {
-                int32_t blk = (int32_t)__umulhi((uint32_t)j, p.bt_inverse);
-                x.row = j - blk * a.c.bt;
+                const int32_t key = SINKS && j >= sinks_end(a, R) ? j + ut.shift : j;
+                int32_t blk = (int32_t)__umulhi((uint32_t)key, p.bt_inverse);
+                x.row = key - blk * a.c.bt;
                 if (x.row < 0) {
                     --blk;
                     x.row += a.c.bt;
@@ -582,10 +603,10 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                     if (tile >= ut.b[t] && tile < ut.e[t])
                         f |= (kAct << t) | (tile == ut.b[t] ? kFirstAct << t : 0) | (tile == ut.e[t] - 1 ? kLastAct << t : 0);
                 }
-                if (j0 >= plain_lo && j0 + kTile <= plain_hi) f |= kPlain;
+                if ((j0 >= plain_lo || (SINKS && j0 + kTile <= a.sinks)) && j0 + kTile <= plain_hi) f |= kPlain;
                 int4 *di = reinterpret_cast<int4 *>(&d.flags);
                 di[0] = make_int4((int)f, j0, ut.k0, ut.k1);
-                di[1] = make_int4(u.row0, u.n, u.len, head);
+                di[1] = make_int4(u.row0, u.n, u.len - ut.shift, head);
                 di[2] = make_int4(r0, r1 - r0, c0, c1);
             }
             ++tile;
@@ -755,7 +776,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 for (int x = 0; x < 4; ++x) {
                     const int row = r0 + rw + 8 * x;
                     const int32_t j = d.j0 + row;
-                    if (!((d.ok >> (row >> 3) & 1u) && j >= d.lo && j < d.hi))
+                    if (!((d.ok >> (row >> 3) & 1u) && (j >= d.lo || (SINKS && j < a.sinks)) && j < d.hi))
 #pragma unroll
                         for (int c = 0; c < NC; ++c) r[x * NC + c] = make_uint4(0, 0, 0, 0);
                 }
@@ -872,7 +893,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
             }
             return top;
         };
-        int32_t klo = 0, khi = 0;                              // keys that the row sees
+        int32_t klo = 0, khi = 0;                              // keys that the row sees, sinks apart
         uint32_t f = 0;
         for (int32_t i = 0; (f & kEnd) == 0; ++i) {
             if (!wait_bar(&s_tfull[i % kDescs], (uint32_t)(i / kDescs) & 1u, abort, status)) break;
@@ -895,6 +916,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 const bool plain = f & kPlain;
                 const int32_t m0 = klo - d.j0;
                 const uint32_t mn = khi > klo ? (uint32_t)(khi - klo) : 0u;
+                const int32_t sk = (a.sinks < khi ? a.sinks : khi) - d.j0;     // end of the sinks
                 const uint32_t ok = d.ok;
                 // The loops over a tile's columns stay rolled and what is rare stays out of them: the
                 // roles' code has to fit the instruction caches.
@@ -914,7 +936,8 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                         tc::ld_wait(x);
 #pragma unroll
                         for (int k = 0; k < 32; ++k) {
-                            const bool see = (uint32_t)(32 * h + k - m0) < mn && (okh >> (k / 8) & 1u);
+                            const bool in = (uint32_t)(32 * h + k - m0) < mn || (SINKS && 32 * h + k < sk);
+                            const bool see = in && (okh >> (k / 8) & 1u);
                             if (!see) x[k] = p.unseen;
                         }
                         tc::st_32x32b_x32(ts + 32 * h, x);
@@ -1176,7 +1199,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
                 const float2 x = __half22float2(probe);
                 if (__builtin_expect(__any_sync(~0u, !(x.x == x.x && x.y == x.y)), 0)) {
                     // (the row's outputs were written by other lanes, behind the loop's __syncwarp)
-                    sum_again<D, FMT>(p, row0, head, r, rend, M == -INFINITY ? 0.f : M, live && M < INFINITY && L < INFINITY ? inv : -1.f, abort);
+                    sum_again<D, FMT, SINKS>(p, row0, head, r, rend, M == -INFINITY ? 0.f : M, live && M < INFINITY && L < INFINITY ? inv : -1.f, abort);
                     __syncwarp();
                 }
             }
@@ -1196,7 +1219,7 @@ __global__ void __launch_bounds__(kThreads, 1) attend_prefill_kernel(const __gri
     }
 }
 
-template <int D, int FMT>
+template <int D, int FMT, bool SINKS>
 cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
 {
     static std::mutex mu;
@@ -1207,7 +1230,7 @@ cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
     {
         std::lock_guard<std::mutex> lk(mu);
         if (dev >= 64 || !set[dev]) {
-            e = cudaFuncSetAttribute(attend_prefill_kernel<D, FMT>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+            e = cudaFuncSetAttribute(attend_prefill_kernel<D, FMT, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                                      (int)Shape<D>::kSmem);
             if (e != cudaSuccess) return e;
             if (dev < 64) set[dev] = true;
@@ -1223,7 +1246,14 @@ cudaError_t launch(const PrefillParams &p, int num_sms, cudaStream_t stream)
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT>, p);
+    return cudaLaunchKernelEx(&cfg, attend_prefill_kernel<D, FMT, SINKS>, p);
+}
+
+template <int D, bool SINKS>
+cudaError_t launch_d(const PrefillParams &p, int fmt, int num_sms, cudaStream_t stream)
+{
+    return fmt == SLORA_KV_E4M3 ? launch<D, SLORA_KV_E4M3, SINKS>(p, num_sms, stream)
+                                : launch<D, SLORA_KV_INT8, SINKS>(p, num_sms, stream);
 }
 
 }  // namespace
@@ -1252,9 +1282,9 @@ cudaError_t launch_attend_prefill(const AttendArgs &a, int head_dim, int fmt, in
     p.joins.word = p.joins.started + 1;
     cudaError_t e;
     if (head_dim == 128)
-        e = fmt == SLORA_KV_E4M3 ? launch<128, SLORA_KV_E4M3>(p, num_sms, stream) : launch<128, SLORA_KV_INT8>(p, num_sms, stream);
+        e = a.sinks > 0 ? launch_d<128, true>(p, fmt, num_sms, stream) : launch_d<128, false>(p, fmt, num_sms, stream);
     else
-        e = fmt == SLORA_KV_E4M3 ? launch<64, SLORA_KV_E4M3>(p, num_sms, stream) : launch<64, SLORA_KV_INT8>(p, num_sms, stream);
+        e = a.sinks > 0 ? launch_d<64, true>(p, fmt, num_sms, stream) : launch_d<64, false>(p, fmt, num_sms, stream);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
