@@ -158,12 +158,13 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(a) -> Optional[int]:
     """Data pointer of a torch tensor / numpy array / int / None."""
-    if a is None:
-        return None
+    if a is None or type(a) is int:
+        return a
+    address = getattr(a, "data_ptr", None)
+    if address is not None:
+        return address()
     if isinstance(a, int):
         return a
-    if hasattr(a, "data_ptr"):
-        return int(a.data_ptr())
     if hasattr(a, "ctypes"):
         return int(a.ctypes.data)
     raise TypeError(f"cannot take a pointer of {type(a)}")
@@ -178,7 +179,7 @@ def _stream(s) -> Optional[int]:
 
 
 def _call(name: str, *args) -> None:
-    st = getattr(lib(), name)(*args)
+    st = getattr(_lib or lib(), name)(*args)
     if st != 0:
         raise SloraError(name, st, slora_last_error())
 

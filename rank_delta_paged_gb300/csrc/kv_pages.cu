@@ -49,32 +49,52 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 //     e = the smallest exponent that max |code 2^e_row| fits        code <- round(code 2^(e_row - e))
 // What bounds it: the kept rows are read and written once; for few of them the chain of dependent reads (offsets,
 // kept positions, pages, exponents, rows).
-constexpr int kCompactThreads = 128;
-constexpr int kMaxBlock = 256;     // rows of the largest page
-constexpr int kCompactCtas = 12;   // per SM
+constexpr int kFill = 1280;      // threads per SM that the registers are to allow
+constexpr int64_t kCompactCtas = 1 << 20;     // of a grid, at most: the hardware deals them out as SMs become free
 
-// The largest finite magnitude of 16 codes, as a code without its sign.
+// The largest finite magnitude of 16 codes.
 template <int FMT>
-__device__ __forceinline__ uint32_t top_code(uint4 v)
+__device__ __forceinline__ float top_code(uint4 v)
 {
-    auto one = [](uint32_t w) {
-        if (FMT == SLORA_KV_INT8) return __vabsss4(w);
-        w &= 0x7F7F7F7Fu;
-        return w & ~__vcmpeq4(w, 0x7F7F7F7Fu);
-    };
-    uint32_t m = __vmaxu4(__vmaxu4(one(v.x), one(v.y)), __vmaxu4(one(v.z), one(v.w)));
-    m = __vmaxu4(m, m >> 16);
-    return __vmaxu4(m, m >> 8) & 0xFFu;
+    __half2 m = __float2half2_rn(0.f);
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        uint32_t lo, hi;
+        decode4<FMT>(w[i], lo, hi);
+        m = __hmax2(m, __habs2(*reinterpret_cast<__half2 *>(&lo)));     // passes over NaN
+        m = __hmax2(m, __habs2(*reinterpret_cast<__half2 *>(&hi)));
+    }
+    return fmaxf(__low2float(m), __high2float(m));
 }
 
-// Four codes times a power of two.
+// Four codes times a power of two, -infinity < shift <= 15, rounded to nearest even.  fp16 loses nothing that counts: an
+// E4M3 product of 2^-11 or more has its last bit at 2^-14 or above, a smaller one is 0 as a code; an INT8
+// product and 1536, whose sum has its last bit at 1, are rounded together, and its low byte is the code.
 template <int FMT>
-__device__ __forceinline__ uint32_t rescale4(uint32_t w, float unit)
+__device__ __forceinline__ uint32_t rescale4(uint32_t w, __half2 unit)
 {
     uint32_t lo, hi;
     decode4<FMT>(w, lo, hi);
-    const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-    return encode2<FMT>(a.x * unit, a.y * unit) | encode2<FMT>(b.x * unit, b.y * unit) << 16;
+    const __half2 a = *reinterpret_cast<__half2 *>(&lo), b = *reinterpret_cast<__half2 *>(&hi);
+    if (FMT == SLORA_KV_E4M3) {
+        const __half2 x = __hmul2(a, unit), y = __hmul2(b, unit);
+        uint32_t r;
+        asm("{\n\t.reg .b16 l, h;\n\tcvt.rn.satfinite.e4m3x2.f16x2 l, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 h, %2;\n\t"
+            "mov.b32 %0, {l, h};\n\t}"
+            : "=r"(r)
+            : "r"(*reinterpret_cast<const uint32_t *>(&x)), "r"(*reinterpret_cast<const uint32_t *>(&y)));
+        return r;
+    }
+    const __half2 off = __float2half2_rn(1536.f);
+    const __half2 x = __hfma2(a, unit, off), y = __hfma2(b, unit, off);
+    return __byte_perm(*reinterpret_cast<const uint32_t *>(&x), *reinterpret_cast<const uint32_t *>(&y), 0x6420);
+}
+template <int FMT>
+__device__ __forceinline__ uint4 rescale16(uint4 v, int shift)
+{
+    const __half2 unit = __float2half2_rn(pow2(shift < 15 ? shift : 15));
+    return make_uint4(rescale4<FMT>(v.x, unit), rescale4<FMT>(v.y, unit), rescale4<FMT>(v.z, unit), rescale4<FMT>(v.w, unit));
 }
 
 struct Span {
@@ -96,130 +116,157 @@ __device__ __forceinline__ int32_t load_span(const CompactArgs &a, int32_t s, Sp
     return 0;
 }
 
-// PASSES: 16-byte pieces of a page per thread.
-template <int D, int FMT, int PASSES>
-__global__ void __launch_bounds__(kCompactThreads) compact_kernel(const __grid_constant__ CompactArgs a, int32_t nb, int64_t items)
+// A CTA takes one block of one head, keys and values: two pages, each by half of its threads, with its rows in shared
+// memory between the reads and the writes, where a thread finds what it has copied itself.  PT threads per page: 64,
+// or 128 for pages above 8192 bytes.
+// In place a CTA goes through a sequence's blocks from the first: a block takes rows from itself and later ones only,
+// so none is written before it has been read.  Where the next block's rows come from is looked up under this one's reads.
+template <int D, int FMT, int PT>
+__global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const __grid_constant__ CompactArgs a, int32_t nb, int64_t items)
 {
-    constexpr int LPR = D / 16;
-    __shared__ int64_t s_from[kMaxBlock];
-    __shared__ int8_t s_exp[kMaxBlock];
-    __shared__ uint32_t s_max[kCompactThreads / 32];
+    constexpr int LPR = D / 16, kRows = 8 * PT / LPR;
+    constexpr uint32_t kBad = ~0u;
+    __shared__ uint4 s_code[2][kRows * LPR];
+    __shared__ int32_t s_page[2][2][kRows], s_row[2][kRows];
+    __shared__ float s_unit[2][kRows];              // 2^exponent of the rows' pages
+    __shared__ uint32_t s_max[2 * PT / 32];
     griddep_wait();
     griddep_launch_dependents();
-    const int tid = threadIdx.x;
-    const int32_t units = 2 * a.c.n_kv, bt = a.c.bt;
+    const int tid = threadIdx.x, w = tid / PT, pt = tid % PT;
+    const int32_t n_kv = a.c.n_kv, bt = a.c.bt;
     const bool in_place = a.dst_table == nullptr;
+    uint4 *codes = s_code[w];
 #pragma unroll 1
     for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-        // (sequence, block, page of the block), or in place (sequence, page of its blocks)
-        const int64_t at = it / units;
-        const int32_t u = (int32_t)(it - at * units), s = (int32_t)(in_place ? at : at / nb);
+        // (sequence, block, head), or in place (sequence, head)
+        const int64_t at = it / n_kv;
+        const int32_t h = (int32_t)(it - at * n_kv), s = (int32_t)(in_place ? at : at / nb);
         const int32_t b = in_place ? 0 : (int32_t)(at - (int64_t)s * nb);
         Span q;
-        const int32_t bad = load_span(a, s, q);
-        if (bad) {
-            if (tid == 0 && u == 0 && b == 0) set_status(a.c.status, bad);
+        const int32_t unfit = load_span(a, s, q);
+        const bool tells = tid == 0 && h == 0 && b == 0;
+        if (unfit) {
+            if (tells) set_status(a.c.status, unfit);
             continue;
         }
-        if (tid == 0 && u == 0 && b == 0 && a.new_len) a.new_len[s] = q.first + q.n;
+        if (tells && a.new_len) a.new_len[s] = q.first + q.n;
         if (q.n == 0) continue;
-        const int32_t *kept = a.kept + (u >> 1) * a.head_stride + q.t0;
-        const int32_t *table = a.table + (int64_t)s * a.max_blocks * units + u;
-        const int32_t *dst_table = in_place ? table : a.dst_table + (int64_t)s * a.dst_blocks * units + u;
+        const int32_t *kept = a.kept + h * a.head_stride + q.t0;
+        const int32_t *table = a.table + ((int64_t)s * a.max_blocks * n_kv + h) * 2 + w;
+        const int32_t *dst_table = in_place ? table : a.dst_table + ((int64_t)s * a.dst_blocks * n_kv + h) * 2 + w;
         const int32_t end = q.first + q.n, last = (end - 1) / bt;
         const int32_t b0 = q.first / bt + b, b1 = in_place ? last : (b0 < last ? b0 : last);
-#pragma unroll 1
-        for (int32_t blk = b0; blk <= b1; ++blk) {
+        // the pages and rows of a block's kept tokens; false if this thread found one that cannot be used
+        auto look_up = [&](int32_t blk, int buf) {
             const int32_t to0 = blk * bt, rows = end - to0 < bt ? end - to0 : bt;
-            int32_t wrong = 0;
+            bool good = true;
 #pragma unroll 1
-            for (int32_t r = tid; r < rows; r += kCompactThreads) {
+            for (int32_t r = pt; r < rows; r += PT) {
                 const int32_t to = to0 + r, i = to - q.first;
-                int32_t p = to;
+                int32_t p = to, page = -1;
+                bool fine = true;
                 if (i >= 0) {
-                    p = kept[i];
-                    if (p < to || p >= q.len || (i > 0 && kept[i - 1] >= p)) {
-                        wrong = SLORA_DEV_BAD_POSITION;
-                        continue;
+                    p = __ldg(kept + i);
+                    fine = p >= to && p < q.len && (i == 0 || __ldg(kept + i - 1) < p);
+                    if (!fine) set_status(a.c.status, SLORA_DEV_BAD_POSITION);
+                }
+                if (fine) {
+                    const int32_t sb = p / bt;
+                    page = __ldg(table + (int64_t)sb * n_kv * 2);
+                    if (page < 0 || page >= a.c.num_pages) {
+                        set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+                        page = -1;
                     }
+                    s_row[buf][r] = p - sb * bt;    // (the same by either half)
                 }
-                const int32_t sb = p / bt, page = table[(int64_t)sb * units];
-                if (page < 0 || page >= a.c.num_pages) {
-                    wrong = SLORA_DEV_BAD_PAGE;
-                    continue;
-                }
-                s_from[r] = page * a.c.page_bytes + (p - sb * bt) * D;
-                s_exp[r] = (int8_t)clamp_exponent(a.c.exps[page]);
+                s_page[buf][w][r] = page;
+                good &= page >= 0;
             }
-            int32_t dst = -1;
-            if (blk >= a.dst_blocks) {
-                wrong = SLORA_DEV_BAD_LENGTH;
-            } else {
-                dst = dst_table[(int64_t)blk * units];
-                if (dst < 0 || dst >= a.c.num_pages) wrong = SLORA_DEV_BAD_PAGE;
+            return good;
+        };
+        auto to_page = [&](int32_t blk) { return blk < a.dst_blocks ? __ldg(dst_table + (int64_t)blk * n_kv * 2) : -1; };
+        int buf = 0;
+        bool next_good = look_up(b0, 0);
+        int32_t next_dst = to_page(b0);
+#pragma unroll 1
+        for (int32_t blk = b0; blk <= b1; ++blk, buf ^= 1) {
+            const int32_t rows = end - blk * bt < bt ? end - blk * bt : bt;
+            bool bad = !next_good;
+            const int32_t dst = next_dst;
+            __syncthreads();
+            const int32_t pieces = rows * LPR;
+#pragma unroll 4
+            for (int32_t x = pt; x < pieces; x += PT) {
+                const int32_t r = x / LPR, page = s_page[buf][w][r];
+                if (page >= 0)
+                    cp_async16(&codes[x], a.c.pool + page * a.c.page_bytes + (s_row[buf][r] * D + x % LPR * 16), 16);
             }
-            if (wrong) set_status(a.c.status, wrong);
-            if (__syncthreads_or(wrong)) continue;      // (nothing of shared memory has been read)
-            uint4 v[PASSES];
+            cp_async_commit();
+            // the exponents, while the rows are on their way
+#pragma unroll 1
+            for (int32_t r = pt; r < rows; r += PT) {
+                const int32_t page = s_page[buf][w][r];
+                s_unit[w][r] = page >= 0 ? pow2(clamp_exponent(a.c.exps[page])) : 0.f;
+            }
+            if (dst < 0 || dst >= a.c.num_pages) {
+                if (pt == 0) set_status(a.c.status, blk < a.dst_blocks ? SLORA_DEV_BAD_PAGE : SLORA_DEV_BAD_LENGTH);
+                bad = true;
+            }
+            if (blk < b1) {
+                next_good = look_up(blk + 1, buf ^ 1);
+                next_dst = to_page(blk + 1);
+            }
+            cp_async_wait<0>();
+            __syncthreads();
             float m = 0.f;
-#pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                const int32_t x = k * kCompactThreads + tid, r = x / LPR;
-                v[k] = make_uint4(0, 0, 0, 0);
-                if (r < rows) v[k] = *reinterpret_cast<const uint4 *>(a.c.pool + s_from[r] + x % LPR * 16);
-            }
-#pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                const int32_t r = (k * kCompactThreads + tid) / LPR;
-                if (r >= rows) continue;
-                uint32_t lo, hi;
-                decode4<FMT>(top_code<FMT>(v[k]), lo, hi);
-                m = fmaxf(m, __low2float(*reinterpret_cast<__half2 *>(&lo)) * pow2(s_exp[r]));
-            }
-            const uint32_t w = __reduce_max_sync(~0u, __float_as_uint(m));
-            if ((tid & 31) == 0) s_max[tid >> 5] = w;
+#pragma unroll 2
+            for (int32_t x = pt; x < pieces; x += PT)
+                if (s_page[buf][w][x / LPR] >= 0) m = fmaxf(m, top_code<FMT>(codes[x]) * s_unit[w][x / LPR]);
+            const uint32_t mine = __reduce_max_sync(~0u, bad ? kBad : __float_as_uint(m));
+            if ((tid & 31) == 0) s_max[tid >> 5] = mine;
             __syncthreads();
-            uint32_t top = s_max[0];
+            uint32_t top = 0;
 #pragma unroll
-            for (int k = 1; k < kCompactThreads / 32; ++k) top = top > s_max[k] ? top : s_max[k];
-            const int e = fit_exponent<FMT>(__uint_as_float(top));
-            uint8_t *page = a.c.pool + dst * a.c.page_bytes;
-#pragma unroll
-            for (int k = 0; k < PASSES; ++k) {
-                const int32_t x = k * kCompactThreads + tid, r = x / LPR;
-                if (r >= rows) continue;
-                const int shift = s_exp[r] - e;
-                if (shift != 0) {
-                    const float unit = pow2(shift);
-                    v[k] = make_uint4(rescale4<FMT>(v[k].x, unit), rescale4<FMT>(v[k].y, unit), rescale4<FMT>(v[k].z, unit),
-                                      rescale4<FMT>(v[k].w, unit));
+            for (int k = 0; k < PT / 32; ++k) {
+                const uint32_t y = s_max[w * (PT / 32) + k];
+                top = top > y ? top : y;
+            }
+            if (top != kBad) {
+                const int e = fit_exponent<FMT>(__uint_as_float(top));
+                uint4 *page = reinterpret_cast<uint4 *>(a.c.pool + dst * a.c.page_bytes);
+#pragma unroll 2
+                for (int32_t x = pt; x < pieces; x += PT) {
+                    const int shift = (int)(__float_as_uint(s_unit[w][x / LPR]) >> 23) - 127 - e;
+                    uint4 v = codes[x];
+                    if (shift != 0) v = rescale16<FMT>(v, shift);
+                    if (FMT == SLORA_KV_E4M3 && shift > 15) v = rescale16<FMT>(v, shift - 15);
+                    page[x] = v;
                 }
-                *reinterpret_cast<uint4 *>(page + x * 16) = v[k];
+                if (pt == 0) a.c.exps[dst] = (int8_t)e;
             }
-            if (tid == 0) a.c.exps[dst] = (int8_t)e;
-            __syncthreads();
         }
+        if (it + gridDim.x < items) __syncthreads();
     }
 }
 
 template <int D, int FMT>
 cudaError_t launch_compact_d(const CompactArgs &a, int num_sms, cudaStream_t stream)
 {
+    const int pt = a.c.bt * D <= 8192 ? 64 : 128;
     // the blocks that a sequence's kept tokens touch, at most
     const int32_t nb = a.dst_table ? (a.max_kept + a.c.bt - 1) / a.c.bt + 1 : 1;
-    const int64_t items = (int64_t)a.S * nb * 2 * a.c.n_kv, ctas = (int64_t)num_sms * kCompactCtas;
+    const int64_t items = (int64_t)a.S * nb * a.c.n_kv;
     cudaLaunchAttribute attr[1];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items < ctas ? items : ctas));
-    cfg.blockDim = dim3(kCompactThreads);
+    cfg.gridDim = dim3((unsigned)(items < kCompactCtas ? items : kCompactCtas));
+    cfg.blockDim = dim3(2 * pt);
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    // pages of up to 8192 and up to 16384 bytes
-    return a.c.bt * D <= 4 * 16 * kCompactThreads ? cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 4>, a, nb, items)
-                                                  : cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 8>, a, nb, items);
+    return pt == 64 ? cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 64>, a, nb, items)
+                    : cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 128>, a, nb, items);
 }
 
 }  // namespace
