@@ -404,6 +404,14 @@ extern "C" slora_status slora_kv_compact(slora_kv_t k, const slora_kv_keep *keep
                           (const void *)keep->new_len})
         if (!aligned4(p))
             return fail(SLORA_ERR_INVALID_ARG, "%s: a misaligned array", fn);
+    // a sequence's arrays are read by CTAs that start after another has written its new length
+    auto apart = [&](const int32_t *p, int64_t n) {
+        const uintptr_t x = (uintptr_t)keep->new_len, y = (uintptr_t)p;
+        return !p || !keep->new_len || x + 4 * (uintptr_t)keep->n_seqs <= y || y + 4 * (uintptr_t)n <= x;
+    };
+    if (!apart(keep->kept_indptr, (int64_t)keep->n_seqs + 1) || !apart(keep->first, keep->n_seqs) ||
+        !apart(keep->kv_len, keep->n_seqs))
+        return fail(SLORA_ERR_INVALID_ARG, "%s: new_len overlaps kept_indptr, first or kv_len", fn);
     if (keep->n_seqs == 0)
         return SLORA_OK;
     kv::CompactArgs a = {};

@@ -49,6 +49,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 //     e = the smallest exponent that max |code 2^e_row| fits        code <- round(code 2^(e_row - e))
 // What bounds it: the kept rows are read and written once; for few of them the chain of dependent reads (offsets,
 // kept positions, pages, exponents, rows).
+constexpr int kMaxCluster = 8;
 constexpr int kFill = 1280;      // threads per SM that the registers are to allow
 constexpr int64_t kCompactCtas = 1 << 20;     // of a grid, at most: the hardware deals them out as SMs become free
 
@@ -119,8 +120,9 @@ __device__ __forceinline__ int32_t load_span(const CompactArgs &a, int32_t s, Sp
 // A CTA takes one block of one head, keys and values: two pages, each by half of its threads, with its rows in shared
 // memory between the reads and the writes, where a thread finds what it has copied itself.  PT threads per page: 64,
 // or 128 for pages above 8192 bytes.
-// In place a CTA goes through a sequence's blocks from the first: a block takes rows from itself and later ones only,
-// so none is written before it has been read.  Where the next block's rows come from is looked up under this one's reads.
+// In place a cluster of CTAs goes through a sequence's blocks from the first, a block each at a time: a block takes rows
+// from itself and later ones only, so what a round writes no later one reads, and within a round all have read
+// before one writes.  Where the next round's rows come from is looked up under this one's reads.
 template <int D, int FMT, int PT>
 __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const __grid_constant__ CompactArgs a, int32_t nb, int64_t items)
 {
@@ -135,13 +137,14 @@ __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const
     const int tid = threadIdx.x, w = tid / PT, pt = tid % PT;
     const int32_t n_kv = a.c.n_kv, bt = a.c.bt;
     const bool in_place = a.dst_table == nullptr;
+    const int32_t ctas = (int32_t)cluster_nctarank();    // more than one in place only, and then one item per cluster
     uint4 *codes = s_code[w];
 #pragma unroll 1
-    for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    for (int64_t it = blockIdx.x / (unsigned)ctas; it < items; it += gridDim.x) {
         // (sequence, block, head), or in place (sequence, head)
         const int64_t at = it / n_kv;
         const int32_t h = (int32_t)(it - at * n_kv), s = (int32_t)(in_place ? at : at / nb);
-        const int32_t b = in_place ? 0 : (int32_t)(at - (int64_t)s * nb);
+        const int32_t b = in_place ? (int32_t)(blockIdx.x % (unsigned)ctas) : (int32_t)(at - (int64_t)s * nb);
         Span q;
         const int32_t unfit = load_span(a, s, q);
         const bool tells = tid == 0 && h == 0 && b == 0;
@@ -155,7 +158,7 @@ __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const
         const int32_t *table = a.table + ((int64_t)s * a.max_blocks * n_kv + h) * 2 + w;
         const int32_t *dst_table = in_place ? table : a.dst_table + ((int64_t)s * a.dst_blocks * n_kv + h) * 2 + w;
         const int32_t end = q.first + q.n, last = (end - 1) / bt;
-        const int32_t b0 = q.first / bt + b, b1 = in_place ? last : (b0 < last ? b0 : last);
+        const int32_t b0 = q.first / bt + b, b1 = in_place || b0 > last ? last : b0;
         // the pages and rows of a block's kept tokens; false if this thread found one that cannot be used
         auto look_up = [&](int32_t blk, int buf) {
             const int32_t to0 = blk * bt, rows = end - to0 < bt ? end - to0 : bt;
@@ -186,11 +189,12 @@ __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const
         };
         auto to_page = [&](int32_t blk) { return blk < a.dst_blocks ? __ldg(dst_table + (int64_t)blk * n_kv * 2) : -1; };
         int buf = 0;
-        bool next_good = look_up(b0, 0);
-        int32_t next_dst = to_page(b0);
+        bool next_good = b0 > b1 || look_up(b0, 0);
+        int32_t next_dst = b0 > b1 ? 0 : to_page(b0);
+        // (a cluster's CTAs go through as many rounds as its first one)
 #pragma unroll 1
-        for (int32_t blk = b0; blk <= b1; ++blk, buf ^= 1) {
-            const int32_t rows = end - blk * bt < bt ? end - blk * bt : bt;
+        for (int32_t blk = b0; blk - b <= b1 - (in_place ? 0 : b); blk += ctas, buf ^= 1) {
+            const int32_t rows = blk > b1 ? 0 : end - blk * bt < bt ? end - blk * bt : bt;
             bool bad = !next_good;
             const int32_t dst = next_dst;
             __syncthreads();
@@ -212,12 +216,18 @@ __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const
                 if (pt == 0) set_status(a.c.status, blk < a.dst_blocks ? SLORA_DEV_BAD_PAGE : SLORA_DEV_BAD_LENGTH);
                 bad = true;
             }
-            if (blk < b1) {
-                next_good = look_up(blk + 1, buf ^ 1);
-                next_dst = to_page(blk + 1);
+            if (b1 - blk >= ctas) {
+                next_good = look_up(blk + ctas, buf ^ 1);
+                next_dst = to_page(blk + ctas);
             }
             cp_async_wait<0>();
-            __syncthreads();
+            if (ctas > 1) {
+                __syncwarp();
+                cluster_sync_all();
+            } else {
+                __syncthreads();
+            }
+            if (rows == 0) break;                   // the cluster's last round
             float m = 0.f;
 #pragma unroll 2
             for (int32_t x = pt; x < pieces; x += PT)
@@ -256,15 +266,24 @@ cudaError_t launch_compact_d(const CompactArgs &a, int num_sms, cudaStream_t str
     // the blocks that a sequence's kept tokens touch, at most
     const int32_t nb = a.dst_table ? (a.max_kept + a.c.bt - 1) / a.c.bt + 1 : 1;
     const int64_t items = (int64_t)a.S * nb * a.c.n_kv;
-    cudaLaunchAttribute attr[1];
+    // In place, the most CTAs per cluster that find blocks and room.  By 1, 2, 4 and 8, in us:
+    // a sequence of 8 heads that keeps 8000 tokens 364, 223, 115, 60 (10 into pages of their own); 8 sequences that
+    // keep 2000 to 8000 each 370, 216, 119, 72 (36); 64 that keep 500 40, 34, 34, 34 (31).
+    int cluster = 1;
+    if (!a.dst_table)
+        while (cluster < kMaxCluster && cluster * 2 <= (a.max_kept + a.c.bt - 1) / a.c.bt && items * cluster * 2 <= 8ll * num_sms) cluster *= 2;
+    cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = cluster;
+    attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items < kCompactCtas ? items : kCompactCtas));
+    cfg.gridDim = dim3((unsigned)(items < kCompactCtas ? items : kCompactCtas) * cluster);
     cfg.blockDim = dim3(2 * pt);
     cfg.stream = stream;
     cfg.attrs = attr;
-    cfg.numAttrs = 1;
+    cfg.numAttrs = cluster > 1 ? 2 : 1;
     return pt == 64 ? cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 64>, a, nb, items)
                     : cudaLaunchKernelEx(&cfg, compact_kernel<D, FMT, 128>, a, nb, items);
 }

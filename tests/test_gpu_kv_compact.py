@@ -180,6 +180,18 @@ def test_compact_long_sequences(in_place):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
+def test_compact_by_several_ctas_in_turn(in_place):
+    """Few sequences and many blocks: in place their blocks are dealt out to 2, 4 and 8 CTAs, with rounds that are full,
+    and with one to all but one of a round's blocks missing."""
+    for d, hidden, fmt in ((64, 256, "e4m3"), (128, 640, "int8"), (64, 8192, "e4m3")):
+        bt = hidden * 2 // d // 8 * 8
+        for blocks in (2, 3, 5, 7, 8, 9, 15, 16, 17, 31):
+            n = blocks * bt
+            Moves([4 * n + 5, n + 40, 30], [7, 0, 3], [n - 9, n, 20], d=d, hidden=hidden, fmt=fmt, seed=217, in_place=in_place).check()
+            Moves([n + 3], [0], [n + 2], d=d, hidden=hidden, fmt=fmt, seed=218, in_place=in_place, hkv=3, per_head=True).check()
+
+
+@pytest.mark.parametrize("in_place", [False, True])
 def test_compact_many_sequences_and_heads(in_place):
     rng = np.random.default_rng(7)
     n = rng.integers(0, 40, 1500)
@@ -369,6 +381,9 @@ def test_compact_refusals():
     k = m.lists()
     for f in ("kept_indptr", "kept", "first", "kv_len", "block_table", "dst_table", "new_len"):
         refused(**{f: getattr(k, f) + 2})
+    for f in ("kept_indptr", "first", "kv_len"):
+        refused(keep=k, new_len=getattr(k, f))
+        refused(keep=k, new_len=getattr(k, f) + 4)
     with pytest.raises(rdp.SloraError):
         rdp._call("slora_kv_compact", m.c.s.kv, None, None)
     for empty in (dict(n_seqs=0), dict(n_seqs=0, n_kept=0, max_kept=0, kept=None, kept_indptr=None, kv_len=None, block_table=None)):
