@@ -133,20 +133,39 @@ __device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch
     }
 }
 
+// Two fp32 numbers at a time, each rounded as by itself.
+__device__ __forceinline__ uint64_t pair(float x, float y)
+{
+    uint64_t r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 unpair(uint64_t v)
+{
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
+{
+    uint64_t r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+
 // The sum over a row's channels of its LPR lanes' eight each, in an order that every kernel shares: the even and
 // the odd channels of a lane, one after another, then the lanes by twos.  No product is contracted into it.
 template <int LPR>
-__device__ __forceinline__ float row_sum(const float (&x)[8], bool squares)
+__device__ __forceinline__ float row_sum(const uint64_t (&x)[4])
 {
-    float e = 0.f, o = 0.f;
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float a = squares ? __fmul_rn(x[2 * i], x[2 * i]) : x[2 * i];
-        const float b = squares ? __fmul_rn(x[2 * i + 1], x[2 * i + 1]) : x[2 * i + 1];
-        e = i ? __fadd_rn(e, a) : a;
-        o = i ? __fadd_rn(o, b) : b;
-    }
-    float s = __fadd_rn(e, o);
+    const float2 t = unpair(add2(add2(add2(x[0], x[1]), x[2]), x[3]));
+    float s = __fadd_rn(t.x, t.y);
 #pragma unroll
     for (int k = 1; k < LPR; k *= 2) s = __fadd_rn(s, __shfl_xor_sync(~0u, s, k));
     return s;
@@ -165,21 +184,31 @@ __device__ __forceinline__ void load_weight(const float *w, int64_t stride, int3
 }
 
 // The norm of a row: x <- (x - mean) / sqrt(mean of squares + eps) * w, the mean taken out if `centered`.  Every lane of
-// the warp calls it; rows that are not `on` keep their values.  The mean is the sum times a power of two.
-template <int LPR>
+// the warp calls it; with SOME, rows that are not `on` keep their values.  The mean is the sum times a power of two.
+template <int LPR, bool SOME>
 __device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const float (&w)[8], float (&x)[8])
 {
     constexpr float each = 1.f / (8 * LPR);
+    uint64_t y[4], z[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) y[i] = pair(x[2 * i], x[2 * i + 1]);
     if (a.centered) {
-        const float m = row_sum<LPR>(x, false) * each;
-        if (on)
+        const float m = -(row_sum<LPR>(y) * each);
+        const uint64_t mm = pair(m, m);
 #pragma unroll
-            for (int i = 0; i < 8; ++i) x[i] = __fsub_rn(x[i], m);
+        for (int i = 0; i < 4; ++i) y[i] = add2(y[i], mm);
     }
-    const float r = rsqrtf(__fadd_rn(row_sum<LPR>(x, true) * each, a.eps));
-    if (on)
 #pragma unroll
-        for (int i = 0; i < 8; ++i) x[i] = __fmul_rn(__fmul_rn(x[i], r), w[i]);
+    for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], y[i]);
+    const float r = rsqrtf(__fadd_rn(row_sum<LPR>(z) * each, a.eps));
+    const uint64_t rr = pair(r, r);
+    if (!SOME || on)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 t = unpair(mul2(mul2(y[i], rr), pair(w[2 * i], w[2 * i + 1])));
+            x[2 * i] = t.x;
+            x[2 * i + 1] = t.y;
+        }
 }
 
 __device__ __forceinline__ void unpack(uint4 v, float (&x)[8])
@@ -215,12 +244,25 @@ __device__ __forceinline__ float max_of(unsigned lanes, float m)
 }
 
 template <int FMT>
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, float unit)
+{
+    if (FMT == SLORA_KV_INT8) {
+        // The last bit of 1.5 2^23 + 128 is 1, so the sum's low byte is the code + 128, rounded to nearest even; the
+        // bytes above are the same for -127 .. 127, which leaves infinities and NaN to the conversions, whose
+        // pipe takes a quarter of the numbers per cycle.
+        const float magic = 12583040.f;
+        const uint32_t u = __float_as_uint(__fmaf_rn(a, unit, magic)), v = __float_as_uint(__fmaf_rn(b, unit, magic));
+        const uint32_t w = __float_as_uint(__fmaf_rn(c, unit, magic)), x = __float_as_uint(__fmaf_rn(d, unit, magic));
+        const uint32_t k = 0x4B400000u;
+        if (__builtin_expect(((u ^ k) | (v ^ k) | (w ^ k) | (x ^ k)) < 256u, 1))
+            return __byte_perm(__byte_perm(u, v, 0x0040), __byte_perm(w, x, 0x0040), 0x5410) ^ 0x80808080u;
+    }
+    return encode2<FMT>(a * unit, b * unit) | encode2<FMT>(c * unit, d * unit) << 16;
+}
+template <int FMT>
 __device__ __forceinline__ uint2 encode8(const float (&x)[8], float unit)
 {
-    uint2 r;
-    r.x = encode2<FMT>(x[0] * unit, x[1] * unit) | encode2<FMT>(x[2] * unit, x[3] * unit) << 16;
-    r.y = encode2<FMT>(x[4] * unit, x[5] * unit) | encode2<FMT>(x[6] * unit, x[7] * unit) << 16;
-    return r;
+    return make_uint2(encode4<FMT>(x[0], x[1], x[2], x[3], unit), encode4<FMT>(x[4], x[5], x[6], x[7], unit));
 }
 
 // Eight codes divided by a power of two (unit < 1).
@@ -248,7 +290,7 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
 // Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
 // have rows of one kind and those of values do not rotate.
 template <int D, int FMT, bool NORM>
-__global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) append_one_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR, ILP = 2;
     const AppendArgs &a = p.a;
@@ -321,7 +363,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
             unpack(raw[i], x);
             const bool turns = u < a.c.n_kv || u >= kv;
             if (__any_sync(~0u, turns)) {
-                if (NORM) normalise<LPR>(a, turns, weight[i], x);
+                if (NORM) normalise<LPR, true>(a, turns, weight[i], x);
                 Rot r = rot;
                 r.on = rot.on && turns;
                 rotate<LPR>(a, r, ch, x);
@@ -355,7 +397,7 @@ __global__ void __launch_bounds__(kThreads) append_one_kernel(const __grid_const
 
 // The queries of a batch: kQHeads heads of one token per group of lanes and step.
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) rotate_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
     const AppendArgs &a = p.a;
@@ -402,7 +444,7 @@ __global__ void __launch_bounds__(kThreads) rotate_kernel(const __grid_constant_
             if (NORM) {
                 float weight[8];
                 load_weight(mine && h0 + k < a.n_q ? a.q_weight : nullptr, a.q_weight_stride, h0 + k, ch, weight);
-                normalise<LPR>(a, true, weight, x);
+                normalise<LPR, false>(a, true, weight, x);
             }
             rotate<LPR>(a, r, ch, x);
             uint4 w;
@@ -460,7 +502,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
                 if (NORM) {
                     float weight[8];
                     load_weight(a.k_weight, a.k_weight_stride, u >> 1, ch, weight);
-                    normalise<LPR>(a, r < nt, weight, x[i]);
+                    normalise<LPR, false>(a, true, weight, x[i]);
                 }
                 if (r < nt) load_rot(a, position(a, row0 + r, from + r), ch, rt);
                 rotate<LPR>(a, rt, ch, x[i]);
