@@ -29,6 +29,8 @@
 // Pages above 8192 bytes have more rows per lane: 4096 tokens in prompts, cold, 57 us at 8192 bytes and 32
 // heads (3.0 TB/s), 98 at 10240 and 40 (2.2 TB/s: the registers for 3 rows at two CTAs per SM spill), 111
 // at 16384 and 64 (3.0 TB/s).
+#include <mutex>
+
 #include "host_common.h"
 #include "internal.h"
 #include "kv.h"
@@ -45,7 +47,8 @@ constexpr int kSeqChunks = 64;
 // append_kernel's CTAs per SM: those that fit with 2 or 3 rows per lane (with 4 one fits, and the other half of
 // the grid follows it).  4 and 8 cost 1 to 8 us more for their starts.
 constexpr int kBlockCtas = 2;
-constexpr int kQHeads = 4;         // query heads per group and step
+constexpr int kStages = 3;         // append_kernel: a page's rows and those of the next two
+constexpr int kQHeads = 2;         // query heads per group and step
 
 struct Params {
     AppendArgs a;
@@ -71,65 +74,100 @@ __device__ __forceinline__ int fresh_tid()
     return t;
 }
 
+// A lane has 16 channels of a row: chunk ch of 8 in either half.  With the whole row rotated in halves a channel's partner
+// is then its own, and both turn by the same angle.
 struct Rot {
     float c[8], s[8];
+    int32_t pos;
     bool on;
 };
 
-// The angles of the 8 channels that this lane holds (chunk ch of the row).
+// The angles of this lane's channels: of chunk ch and its partner where rows turn in halves, or (the first four, then the
+// last four) of its adjacent pairs.  Where more than half a row turns, but not all, rotate() looks them up.
+template <int D>
 __device__ __forceinline__ void load_rot(const AppendArgs &a, int32_t pos, int ch, Rot &r)
 {
-    r.on = a.rot != 0 && ch * 8 < a.rot;
+    r.on = a.rot != 0;
+    r.pos = pos;
     if (r.on && (pos < 0 || pos >= a.n_pos)) {
         set_status(a.c.status, SLORA_DEV_BAD_POSITION);
         r.on = false;
     }
     if (!r.on) return;
-    const int half = a.rot / 2;
-    const int64_t row = (int64_t)pos * half;
-    if (a.interleaved) {
-        const float4 c = __ldg(reinterpret_cast<const float4 *>(a.cos + row) + ch);
-        const float4 s = __ldg(reinterpret_cast<const float4 *>(a.sin + row) + ch);
-        r.c[0] = c.x, r.c[1] = c.y, r.c[2] = c.z, r.c[3] = c.w;
-        r.s[0] = s.x, r.s[1] = s.y, r.s[2] = s.z, r.s[3] = s.w;
-    } else {
-        const int k = ch * 8 < half ? ch : ch - half / 8;
+    const int64_t row = (int64_t)pos * (a.rot / 2);
+    const float4 *cos = reinterpret_cast<const float4 *>(a.cos + row), *sin = reinterpret_cast<const float4 *>(a.sin + row);
+    const bool halves = !a.interleaved;
+    const int m = a.rot / 16;            // chunks of half the rotated channels
+    if (halves && 2 * m > D / 16 && a.rot != D) return;
 #pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const float4 c = __ldg(reinterpret_cast<const float4 *>(a.cos + row) + 2 * k + i);
-            const float4 s = __ldg(reinterpret_cast<const float4 *>(a.sin + row) + 2 * k + i);
-            r.c[4 * i] = c.x, r.c[4 * i + 1] = c.y, r.c[4 * i + 2] = c.z, r.c[4 * i + 3] = c.w;
-            r.s[4 * i] = s.x, r.s[4 * i + 1] = s.y, r.s[4 * i + 2] = s.z, r.s[4 * i + 3] = s.w;
-        }
-        if (ch * 8 < half)      // a cos + b (-sin)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) r.s[i] = -r.s[i];
+    for (int i = 0; i < 2; ++i) {
+        const int k = halves ? 2 * (ch < m ? ch : ch - m) + i : ch + i * (D / 16);
+        const bool turns = halves ? ch < 2 * m : ch * 8 + i * (D / 2) < a.rot;
+        const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), none = make_float4(0.f, 0.f, 0.f, 0.f);
+        const float4 c = turns ? __ldg(cos + k) : one, s = turns ? __ldg(sin + k) : none;
+        r.c[4 * i] = c.x, r.c[4 * i + 1] = c.y, r.c[4 * i + 2] = c.z, r.c[4 * i + 3] = c.w;
+        r.s[4 * i] = s.x, r.s[4 * i + 1] = s.y, r.s[4 * i + 2] = s.z, r.s[4 * i + 3] = s.w;
     }
 }
 
-// Rotates the 8 channels of chunk ch; every lane of the row's group (LPR lanes) calls it.  Products and sums are
-// rounded one by one, so the codes do not depend on contraction.
-template <int LPR>
-__device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch, float (&x)[8])
+// Rotates this lane's channels; every lane of the warp calls it.  Products and sums are rounded one by one, so the codes
+// do not depend on contraction.
+template <int D>
+__device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch, float (&x)[16])
 {
     if (a.rot == 0) return;
     if (a.interleaved) {
-        if (r.on) {
+        if (r.on)
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
+            for (int i = 0; i < 8; ++i) {
                 const float u = x[2 * i], w = x[2 * i + 1];
-                x[2 * i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
-                x[2 * i + 1] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
+                if (ch * 8 + (i >> 2) * (D / 2) < a.rot) {
+                    x[2 * i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
+                    x[2 * i + 1] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
+                }
+            }
+    } else if (a.rot == D) {
+        if (r.on)
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float u = x[i], w = x[8 + i];
+                x[i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
+                x[8 + i] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
+            }
+    } else {
+        // a part of the row in halves: the partners are other lanes', all of the first half's chunks if at most that turns
+        constexpr int LPR = D / 16;
+        const int m = a.rot / 16;
+        auto partner = [&](int k) { return k < m ? k + m : k < 2 * m ? k - m : k; };
+        if (2 * m <= LPR) {
+            const bool turns = r.on && ch < 2 * m;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float y = __shfl_sync(~0u, x[i], partner(ch), LPR);
+                if (turns) x[i] = __fadd_rn(__fmul_rn(x[i], r.c[i]), __fmul_rn(y, ch < m ? -r.s[i] : r.s[i]));
+            }
+            return;
+        }
+        const int64_t row = (int64_t)r.pos * (a.rot / 2);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            float y[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int from = partner(ch + h * LPR);
+                const float u = __shfl_sync(~0u, x[i], from % LPR, LPR), w = __shfl_sync(~0u, x[8 + i], from % LPR, LPR);
+                y[h] = from < LPR ? u : w;
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int k = ch + h * LPR;
+                if (r.on && k < 2 * m) {
+                    const int64_t at = row + 8 * (k < m ? k : k - m) + i;
+                    const float sn = __ldg(a.sin + at);
+                    x[8 * h + i] = __fadd_rn(__fmul_rn(x[8 * h + i], __ldg(a.cos + at)), __fmul_rn(y[h], k < m ? -sn : sn));
+                }
             }
         }
-        return;
-    }
-    const int m = a.rot / 16;            // chunks of half the rotated channels
-    const int from = ch < m ? ch + m : (ch < 2 * m ? ch - m : ch);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const float y = __shfl_sync(~0u, x[i], from, LPR);
-        if (r.on) x[i] = __fadd_rn(__fmul_rn(x[i], r.c[i]), __fmul_rn(y, r.s[i]));
     }
 }
 
@@ -159,79 +197,104 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
     return r;
 }
 
-// The sum over a row's channels of its LPR lanes' eight each, in an order that every kernel shares: the even and
-// the odd channels of a lane, one after another, then the lanes by twos.  No product is contracted into it.
-template <int LPR>
-__device__ __forceinline__ float row_sum(const uint64_t (&x)[4])
+// The sum over a row's channels in an order that depends on D alone: the even and the odd channels of each 8, one after
+// another, then the eights by twos.  No product is contracted into it.
+template <int D>
+__device__ __forceinline__ float row_sum(const uint64_t (&x)[8])
 {
-    const float2 t = unpair(add2(add2(add2(x[0], x[1]), x[2]), x[3]));
-    float s = __fadd_rn(t.x, t.y);
+    const float2 t = unpair(add2(add2(add2(x[0], x[1]), x[2]), x[3])), u = unpair(add2(add2(add2(x[4], x[5]), x[6]), x[7]));
+    float a = __fadd_rn(t.x, t.y), b = __fadd_rn(u.x, u.y);
 #pragma unroll
-    for (int k = 1; k < LPR; k *= 2) s = __fadd_rn(s, __shfl_xor_sync(~0u, s, k));
-    return s;
+    for (int k = 1; k < D / 16; k *= 2) {
+        a = __fadd_rn(a, __shfl_xor_sync(~0u, a, k));
+        b = __fadd_rn(b, __shfl_xor_sync(~0u, b, k));
+    }
+    return __fadd_rn(a, b);
 }
 
-// This lane's eight weights of head h.
-__device__ __forceinline__ void load_weight(const float *w, int64_t stride, int32_t h, int ch, float (&x)[8])
+// The norm of a row: x <- (x - mean) / sqrt(mean of squares + eps) * w, the mean taken out if `centered`, the head's weights
+// from w on (nullptr: ones).  Every lane of the warp calls it; with SOME, rows that are not `on` keep their values.
+// The mean is the sum times a power of two.
+template <int D, bool SOME>
+__device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const float *w, int ch, float (&x)[16])
 {
+    uint64_t y[8], z[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) x[i] = 1.f;
-    if (w == nullptr) return;
-    const float4 *p = reinterpret_cast<const float4 *>(w + h * stride) + 2 * ch;
-    const float4 a = __ldg(p), b = __ldg(p + 1);
-    x[0] = a.x, x[1] = a.y, x[2] = a.z, x[3] = a.w;
-    x[4] = b.x, x[5] = b.y, x[6] = b.z, x[7] = b.w;
-}
-
-// The norm of a row: x <- (x - mean) / sqrt(mean of squares + eps) * w, the mean taken out if `centered`.  Every lane of
-// the warp calls it; with SOME, rows that are not `on` keep their values.  The mean is the sum times a power of two.
-template <int LPR, bool SOME>
-__device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const float (&w)[8], float (&x)[8])
-{
-    constexpr float each = 1.f / (8 * LPR);
-    uint64_t y[4], z[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) y[i] = pair(x[2 * i], x[2 * i + 1]);
+    for (int i = 0; i < 8; ++i) y[i] = pair(x[2 * i], x[2 * i + 1]);
     if (a.centered) {
-        const float m = -(row_sum<LPR>(y) * each);
+        const float m = -(row_sum<D>(y) * (1.f / D));
         const uint64_t mm = pair(m, m);
 #pragma unroll
-        for (int i = 0; i < 4; ++i) y[i] = add2(y[i], mm);
+        for (int i = 0; i < 8; ++i) y[i] = add2(y[i], mm);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) z[i] = mul2(y[i], y[i]);
-    const float r = rsqrtf(__fadd_rn(row_sum<LPR>(z) * each, a.eps));
+    for (int i = 0; i < 8; ++i) z[i] = mul2(y[i], y[i]);
+    const float r = rsqrtf(__fadd_rn(row_sum<D>(z) * (1.f / D), a.eps));
     const uint64_t rr = pair(r, r);
-    if (!SOME || on)
+#pragma unroll
+    for (int i = 0; i < 8; ++i) y[i] = mul2(y[i], rr);
+    if (w != nullptr) {
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float2 t = unpair(mul2(mul2(y[i], rr), pair(w[2 * i], w[2 * i + 1])));
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (i >> 1) * (D / 2)) + 2 * ch + (i & 1));
+            y[2 * i] = mul2(y[2 * i], pair(v.x, v.y));
+            y[2 * i + 1] = mul2(y[2 * i + 1], pair(v.z, v.w));
+        }
+    }
+    if (!SOME || on)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const float2 t = unpair(y[i]);
             x[2 * i] = t.x;
             x[2 * i + 1] = t.y;
         }
 }
 
-__device__ __forceinline__ void unpack(uint4 v, float (&x)[8])
+// A row's two pieces of this lane.
+struct Raw {
+    uint4 a, b;
+};
+template <int D>
+__device__ __forceinline__ Raw read_row(const __half *row, int ch)
 {
-    const __half2 *h = reinterpret_cast<const __half2 *>(&v);
+    return {*reinterpret_cast<const uint4 *>(row + ch * 8), *reinterpret_cast<const uint4 *>(row + D / 2 + ch * 8)};
+}
+
+__device__ __forceinline__ void unpack(const Raw &v, float (&x)[16])
+{
+    const uint32_t w[8] = {v.a.x, v.a.y, v.a.z, v.a.w, v.b.x, v.b.y, v.b.z, v.b.w};
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(h[i]);
+    for (int i = 0; i < 8; ++i) {
+        const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&w[i]));
         x[2 * i] = f.x;
         x[2 * i + 1] = f.y;
     }
 }
 
+// The rotated query of this lane in fp16.
+template <int D>
+__device__ __forceinline__ void write_query(__half *row, int ch, const float (&x)[16])
+{
+    uint32_t w[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
+        w[i] = *reinterpret_cast<const uint32_t *>(&h);
+    }
+    *reinterpret_cast<uint4 *>(row + ch * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(row + D / 2 + ch * 8) = make_uint4(w[4], w[5], w[6], w[7]);
+}
+
 // The largest finite magnitude.
-__device__ __forceinline__ float size_of(const float (&x)[8])
+__device__ __forceinline__ float size_of(const float (&x)[16])
 {
     float m = 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(x[i]));      // passes over NaN
+    for (int i = 0; i < 16; ++i) m = fmaxf(m, fabsf(x[i]));      // passes over NaN
     if (__builtin_expect(m == INFINITY, 0)) {
         m = 0.f;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
+        for (int i = 0; i < 16; ++i)
             if (fabsf(x[i]) < INFINITY) m = fmaxf(m, fabsf(x[i]));
     }
     return m;
@@ -241,6 +304,12 @@ __device__ __forceinline__ float size_of(const float (&x)[8])
 __device__ __forceinline__ float max_of(unsigned lanes, float m)
 {
     return __uint_as_float(__reduce_max_sync(lanes, __float_as_uint(m)));
+}
+
+// INT8 codes with an infinity or a NaN among them: out of line, for its registers.
+static __device__ __noinline__ uint32_t encode4_odd(float a, float b, float c, float d)
+{
+    return encode2<SLORA_KV_INT8>(a, b) | encode2<SLORA_KV_INT8>(c, d) << 16;
 }
 
 template <int FMT>
@@ -256,30 +325,35 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
         const uint32_t k = 0x4B400000u;
         if (__builtin_expect(((u ^ k) | (v ^ k) | (w ^ k) | (x ^ k)) < 256u, 1))
             return __byte_perm(__byte_perm(u, v, 0x0040), __byte_perm(w, x, 0x0040), 0x5410) ^ 0x80808080u;
+        return encode4_odd(a * unit, b * unit, c * unit, d * unit);
     }
     return encode2<FMT>(a * unit, b * unit) | encode2<FMT>(c * unit, d * unit) << 16;
 }
-template <int FMT>
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float unit)
+// This lane's codes to a row.
+template <int D, int FMT>
+__device__ __forceinline__ void write_codes(uint8_t *row, int ch, const float (&x)[16], float unit)
 {
-    return make_uint2(encode4<FMT>(x[0], x[1], x[2], x[3], unit), encode4<FMT>(x[4], x[5], x[6], x[7], unit));
+#pragma unroll
+    for (int h = 0; h < 2; ++h)
+        *reinterpret_cast<uint2 *>(row + h * (D / 2) + ch * 8) =
+            make_uint2(encode4<FMT>(x[8 * h], x[8 * h + 1], x[8 * h + 2], x[8 * h + 3], unit),
+                       encode4<FMT>(x[8 * h + 4], x[8 * h + 5], x[8 * h + 6], x[8 * h + 7], unit));
 }
 
-// Eight codes divided by a power of two (unit < 1).
+// Sixteen codes of a row divided by a power of two (unit < 1).
 template <int FMT>
-__device__ __forceinline__ uint2 rescale8(uint2 v, float unit)
+__device__ __forceinline__ void rescale16(uint4 *at, float unit)
 {
-    float x[8];
-    uint32_t h[4];
-    decode4<FMT>(v.x, h[0], h[1]);
-    decode4<FMT>(v.y, h[2], h[3]);
+    const uint4 v = *at;
+    uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
-        const float2 f = __half22float2(*reinterpret_cast<__half2 *>(&h[i]));
-        x[2 * i] = f.x;
-        x[2 * i + 1] = f.y;
+        uint32_t lo, hi;
+        decode4<FMT>(w[i], lo, hi);
+        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
+        w[i] = encode4<FMT>(a.x, a.y, b.x, b.y, unit);
     }
-    return encode8<FMT>(x, unit);
+    *at = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int32_t in_cache)
@@ -290,9 +364,9 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
 // Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
 // have rows of one kind and those of values do not rotate.
 template <int D, int FMT, bool NORM>
-__global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) append_one_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(const __grid_constant__ Params p)
 {
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR, ILP = 2;
+    constexpr int LPR = D / 16;
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
     const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
@@ -310,96 +384,60 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) append_one_kernel(cons
         return;
     }
     if (t1 - t0 != 1) return;
-    const int32_t kv = 2 * a.c.n_kv, all = kv + p.q_rows;
-    const int32_t u0 = part * p.units, u1 = u0 + p.units < all ? u0 + p.units : all;
+    const int32_t n_kv = a.c.n_kv, kv = 2 * n_kv, all = kv + p.q_rows;
+    const int32_t u = part * p.units + grp;         // this group's row
+    const bool live = grp < p.units && u < all, query = u >= kv, val = u >= n_kv && !query;
+    const int32_t h = query ? u - kv : val ? u - n_kv : u;
     const int32_t blk = (len - 1) / a.c.bt, held = len - 1 - blk * a.c.bt;
-    const int32_t *table = a.b.table + ((int64_t)s * a.b.max_blocks + blk) * kv;
-    const int32_t pos = a.rot ? (a.positions ? a.positions[t0] : len - 1) : 0;
+    Raw raw = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+    int32_t page = -1, old = kMinExponent;
+    if (live) {
+        const __half *src = query ? a.q + t0 * a.q_stride : val ? a.v + t0 * a.v_stride : a.k + t0 * a.k_stride;
+        raw = read_row<D>(src + (int64_t)h * D, ch);
+        if (!query) page = a.b.table[((int64_t)s * a.b.max_blocks + blk) * kv + 2 * h + val];
+    }
+    const bool turns = live && !val;
     Rot rot;
     rot.on = false;
-#pragma unroll 1
-    for (int32_t ub = u0; ub < u1; ub += ILP * GROUPS) {
-        uint4 raw[ILP];
-        int32_t page[ILP], old[ILP];
-        float weight[NORM ? ILP : 1][8];
-#pragma unroll
-        for (int i = 0; i < ILP; ++i) {
-            const int32_t u = ub + i * GROUPS + grp;
-            raw[i] = make_uint4(0, 0, 0, 0);
-            page[i] = -1;
-            old[i] = kMinExponent;
-            if (u < u1) {
-                const bool val = u >= a.c.n_kv;
-                const int32_t h = val ? u - a.c.n_kv : u;
-                const __half *src = u >= kv ? a.q + t0 * a.q_stride + (int64_t)(u - kv) * D
-                                   : val    ? a.v + t0 * a.v_stride + (int64_t)h * D
-                                            : a.k + t0 * a.k_stride + (int64_t)h * D;
-                raw[i] = *reinterpret_cast<const uint4 *>(src + ch * 8);
-                if (u < kv) page[i] = table[2 * h + val];
-            }
-            if (NORM) {
-                const bool q = u >= kv;
-                load_weight(u < u1 && (q || u < a.c.n_kv) ? (q ? a.q_weight : a.k_weight) : nullptr,
-                            q ? a.q_weight_stride : a.k_weight_stride, q ? u - kv : u, ch, weight[i]);
-            }
-        }
-        if (ub == u0) load_rot(a, pos, ch, rot);
-#pragma unroll
-        for (int i = 0; i < ILP; ++i) {
-            const int32_t u = ub + i * GROUPS + grp;
-            if (u < u1 && u < kv) {
-                if (page[i] < 0 || page[i] >= a.c.num_pages) {
-                    if (ch == 0) set_status(a.c.status, SLORA_DEV_BAD_PAGE);
-                    page[i] = -1;
-                } else if (held && ch == 0) {
-                    old[i] = clamp_exponent(a.c.exps[page[i]]);    // by the lane that writes it
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < ILP; ++i) {
-            const int32_t u = ub + i * GROUPS + grp;
-            float x[8];
-            unpack(raw[i], x);
-            const bool turns = u < a.c.n_kv || u >= kv;
-            if (__any_sync(~0u, turns)) {
-                if (NORM) normalise<LPR, true>(a, turns, weight[i], x);
-                Rot r = rot;
-                r.on = rot.on && turns;
-                rotate<LPR>(a, r, ch, x);
-            }
-            float m = size_of(x);
-            m = max_of(row_lanes, m);
-            const int was = __shfl_sync(~0u, old[i], 0, LPR);
-            if (u >= kv && u < u1) {
-                uint4 w;
-                __half2 *h = reinterpret_cast<__half2 *>(&w);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-                *reinterpret_cast<uint4 *>(a.q_out + t0 * a.q_out_stride + (int64_t)(u - kv) * D + ch * 8) = w;
-            }
-            if (page[i] < 0) continue;
-            const int fit = fit_exponent<FMT>(m), e = held && was > fit ? was : fit;
-            uint8_t *dst = a.c.pool + page[i] * a.c.page_bytes + ch * 8;
-            if (held && was < e) {
-                const float unit = pow2(was - e);
-#pragma unroll 1
-                for (int k = 0; k < held; ++k) {
-                    uint2 *w = reinterpret_cast<uint2 *>(dst + k * D);
-                    *w = rescale8<FMT>(*w, unit);
-                }
-            }
-            if (ch == 0) a.c.exps[page[i]] = (int8_t)e;
-            *reinterpret_cast<uint2 *>(dst + held * D) = encode8<FMT>(x, pow2(-e));
+    if (turns) load_rot<D>(a, a.rot ? (a.positions ? a.positions[t0] : len - 1) : 0, ch, rot);
+    if (live && !query) {
+        if (page < 0 || page >= a.c.num_pages) {
+            if (ch == 0) set_status(a.c.status, SLORA_DEV_BAD_PAGE);
+            page = -1;
+        } else if (held && ch == 0) {
+            old = clamp_exponent(a.c.exps[page]);   // by the lane that writes it
         }
     }
+    float x[16];
+    unpack(raw, x);
+    if (__any_sync(~0u, turns)) {
+        if (NORM) {
+            const float *w = query ? a.q_weight : a.k_weight;
+            if (w != nullptr) w = turns ? w + h * (query ? a.q_weight_stride : a.k_weight_stride) : nullptr;
+            normalise<D, true>(a, turns, w, ch, x);
+        }
+        rotate<D>(a, rot, ch, x);
+    }
+    const float m = max_of(row_lanes, size_of(x));
+    const int was = __shfl_sync(~0u, old, 0, LPR);
+    if (live && query) write_query<D>(a.q_out + t0 * a.q_out_stride + (int64_t)h * D, ch, x);
+    if (page < 0) return;
+    const int fit = fit_exponent<FMT>(m), e = held && was > fit ? was : fit;
+    uint8_t *dst = a.c.pool + page * a.c.page_bytes;
+    if (held && was < e) {
+        const float unit = pow2(was - e);
+#pragma unroll 1
+        for (int k = 0; k < held; ++k) rescale16<FMT>(reinterpret_cast<uint4 *>(dst + k * D + ch * 16), unit);
+    }
+    if (ch == 0) a.c.exps[page] = (int8_t)e;
+    write_codes<D, FMT>(dst + held * D, ch, x, pow2(-e));
 }
 
 // The queries of a batch: kQHeads heads of one token per group of lanes and step.
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) rotate_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_constant__ Params p)
 {
-    constexpr int LPR = D / 8, GROUPS = kThreads / LPR;
+    constexpr int LPR = D / 16, GROUPS = kThreads / LPR;
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
     const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
@@ -412,12 +450,12 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) rotate_kernel(const __
     for (int64_t i0 = (int64_t)blockIdx.x * GROUPS; i0 < total; i0 += step) {
         const int64_t i = i0 + grp;
         const bool live = i < total;
-        const int32_t t = live ? (int32_t)(i / per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
-        uint4 v[kQHeads];
+        // (at most 2^20 tokens and 2^11 groups of heads)
+        const int32_t t = live ? (int32_t)((uint32_t)i / (uint32_t)per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
+        Raw v[kQHeads];
 #pragma unroll
         for (int k = 0; k < kQHeads; ++k)
-            if (live && h0 + k < a.n_q)
-                v[k] = *reinterpret_cast<const uint4 *>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D + ch * 8);
+            if (live && h0 + k < a.n_q) v[k] = read_row<D>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D, ch);
         int32_t pos = a.positions && live ? a.positions[t] : 0;
         // rows outside every sequence, and those of a sequence that is skipped, are left alone
         int32_t lo = 0, n = a.b.S;               // the last of n from lo that starts at or before t, a lane per part of them
@@ -435,24 +473,16 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 0) rotate_kernel(const __
         if (mine && !a.positions) pos = len - end + t;
         Rot r;
         r.on = false;
-        if (mine) load_rot(a, pos, ch, r);
+        if (mine) load_rot<D>(a, pos, ch, r);
 #pragma unroll
         for (int k = 0; k < kQHeads; ++k) {
-            float x[8];
-            if (!(mine && h0 + k < a.n_q)) v[k] = make_uint4(0, 0, 0, 0);
+            const bool some = mine && h0 + k < a.n_q;
+            float x[16];
+            if (!some) v[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
             unpack(v[k], x);
-            if (NORM) {
-                float weight[8];
-                load_weight(mine && h0 + k < a.n_q ? a.q_weight : nullptr, a.q_weight_stride, h0 + k, ch, weight);
-                normalise<LPR, false>(a, true, weight, x);
-            }
-            rotate<LPR>(a, r, ch, x);
-            uint4 w;
-            __half2 *h = reinterpret_cast<__half2 *>(&w);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) h[j] = __floats2half2_rn(x[2 * j], x[2 * j + 1]);
-            if (mine && h0 + k < a.n_q)
-                *reinterpret_cast<uint4 *>(a.q_out + t * a.q_out_stride + (int64_t)(h0 + k) * D + ch * 8) = w;
+            if (NORM) normalise<D, false>(a, true, some && a.q_weight ? a.q_weight + (h0 + k) * a.q_weight_stride : nullptr, ch, x);
+            rotate<D>(a, r, ch, x);
+            if (some) write_query<D>(a.q_out + t * a.q_out_stride + (int64_t)(h0 + k) * D, ch, x);
         }
     }
     griddep_wait();
@@ -464,48 +494,81 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
                                           int32_t row0, int32_t from, const int32_t *s_page, const int8_t *s_exp,
                                           uint32_t *s_max, int &turn)
 {
-    constexpr int LPR = D / 8, GROUPS = kBlockThreads / LPR;
+    constexpr int LPR = D / 16, GROUPS = kBlockThreads / LPR;
     const int tid = fresh_tid(), ch = tid % LPR, grp = tid / LPR;
-    uint4 raw[PASSES];
-    auto read = [&](int32_t u) {
-        const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
-        const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
+    // Shared memory of which every thread has pieces of its own: the rows of this page and the next ones, and the angles.
+    extern __shared__ uint4 s_own[];
+    uint4 *ring = s_own + tid;
+    float4 *s_rot = reinterpret_cast<float4 *>(s_own + kStages * PASSES * 2 * kBlockThreads) + tid;
+    auto piece = [&](int slot, int i, int h) { return ring + ((slot * PASSES + i) * 2 + h) * kBlockThreads; };
+    auto read = [&](int32_t u, int slot) {
+        if (u < u1) {
+            const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
+            const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
 #pragma unroll
-        for (int i = 0; i < PASSES; ++i) {
-            const int r = i * GROUPS + grp;
-            raw[i] = make_uint4(0, 0, 0, 0);
-            if (r < nt) raw[i] = *reinterpret_cast<const uint4 *>(src + (int64_t)(row0 + r) * stride);
+            for (int i = 0; i < PASSES; ++i) {
+                const int r = i * GROUPS + grp;
+                if (r >= nt) break;
+                const __half *row = src + (int64_t)(row0 + r) * stride;
+                cp_async16(piece(slot, i, 0), row, 16);
+                cp_async16(piece(slot, i, 1), row + D / 2, 16);
+            }
         }
+        cp_async_commit();
     };
-    read(u0);
+#pragma unroll
+    for (int k = 0; k < kStages - 1; ++k) read(u0 + k, k);
+    // a row's angles are those of all heads: a thread keeps its own in shared memory
+    int32_t at[PASSES];                     // position, -1: not rotated
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) {
+        const int r = i * GROUPS + grp;
+        at[i] = -1;
+        if (a.rot == 0 || r >= nt) continue;
+        Rot rt;
+        load_rot<D>(a, position(a, row0 + r, from + r), ch, rt);
+        if (!rt.on) continue;
+        at[i] = rt.pos;
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float *v = j < 2 ? rt.c + 4 * j : rt.s + 4 * (j - 2);
+            s_rot[(4 * i + j) * kBlockThreads] = make_float4(v[0], v[1], v[2], v[3]);
+        }
+    }
+    int slot = 0;
 #pragma unroll 1
-    for (int32_t u = u0; u < u1; ++u) {
+    for (int32_t u = u0; u < u1; ++u, slot = slot == kStages - 1 ? 0 : slot + 1) {
         const bool val = u & 1;
         const int32_t page = s_page[u - u0];
         const int old = s_exp[u - u0];
-        float x[PASSES][8];
+        float x[PASSES][16];
         float m = 0.f;
+        read(u + kStages - 1, slot == 0 ? kStages - 1 : slot - 1);
+        cp_async_wait<kStages - 1>();
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            if (i * GROUPS >= nt) break;
-            unpack(raw[i], x[i]);
+            Raw raw = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+            if (i * GROUPS + grp < nt) raw = {*piece(slot, i, 0), *piece(slot, i, 1)};
+            unpack(raw, x[i]);
         }
-        if (u + 1 < u1) read(u + 1);
         if (page < 0) continue;             // the whole CTA
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
-            if (i * GROUPS >= nt) break;
             const int r = i * GROUPS + grp;
+            if (__all_sync(~0u, r >= nt)) break;
             if (!val) {
+                if (NORM) normalise<D, false>(a, true, a.k_weight ? a.k_weight + (u >> 1) * a.k_weight_stride : nullptr, ch, x[i]);
                 Rot rt;
-                rt.on = false;
-                if (NORM) {
-                    float weight[8];
-                    load_weight(a.k_weight, a.k_weight_stride, u >> 1, ch, weight);
-                    normalise<LPR, false>(a, true, weight, x[i]);
-                }
-                if (r < nt) load_rot(a, position(a, row0 + r, from + r), ch, rt);
-                rotate<LPR>(a, rt, ch, x[i]);
+                rt.pos = at[i];
+                rt.on = at[i] >= 0;
+                if (rt.on)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float4 v = s_rot[(4 * i + j) * kBlockThreads];
+                        float *w = j < 2 ? rt.c + 4 * j : rt.s + 4 * (j - 2);
+                        w[0] = v.x, w[1] = v.y, w[2] = v.z, w[3] = v.w;
+                    }
+                rotate<D>(a, rt, ch, x[i]);
             }
             m = fmaxf(m, size_of(x[i]));
         }
@@ -524,10 +587,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
             } else {
                 const float unit = pow2(old - e);
 #pragma unroll 1
-                for (int r = grp; r < held; r += GROUPS) {
-                    uint2 *w = reinterpret_cast<uint2 *>(dst + r * D + ch * 8);
-                    *w = rescale8<FMT>(*w, unit);
-                }
+                for (int r = grp; r < held; r += GROUPS) rescale16<FMT>(reinterpret_cast<uint4 *>(dst + r * D + ch * 16), unit);
             }
         }
         if (tid == 0) a.c.exps[page] = (int8_t)e;
@@ -535,7 +595,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int r = i * GROUPS + grp;
-            if (r < nt) *reinterpret_cast<uint2 *>(dst + (held + r) * D + ch * 8) = encode8<FMT>(x[i], unit);
+            if (r < nt) write_codes<D, FMT>(dst + (held + r) * D, ch, x[i], unit);
         }
     }
 }
@@ -683,7 +743,7 @@ __device__ __forceinline__ void append_blocks(const Params &p)
 }
 
 template <int D, int FMT, int PASSES, bool NORM>
-__global__ void __launch_bounds__(kBlockThreads, PASSES <= 3 ? 2 : 1) append_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kBlockThreads, PASSES == 1 ? 2 : 1) append_kernel(const __grid_constant__ Params p)
 {
     // append_one_kernel, the one before, has waited for what came before it, and nothing here depends on
     // its results; the kernel after this one waits for what this one has waited for
@@ -693,7 +753,8 @@ __global__ void __launch_bounds__(kBlockThreads, PASSES <= 3 ? 2 : 1) append_ker
 }
 
 template <class... Args>
-cudaError_t start(void (*kernel)(Args...), const Params &p, int64_t ctas, cudaStream_t stream, int threads = kThreads)
+cudaError_t start(void (*kernel)(Args...), const Params &p, int64_t ctas, cudaStream_t stream, int threads = kThreads,
+                  size_t smem = 0)
 {
     if (ctas > 0x7FFFFFFFll) return cudaErrorInvalidConfiguration;
     cudaLaunchAttribute attr[1];
@@ -702,24 +763,45 @@ cudaError_t start(void (*kernel)(Args...), const Params &p, int64_t ctas, cudaSt
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)ctas);
     cfg.blockDim = dim3(threads);
+    cfg.dynamicSmemBytes = smem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     return cudaLaunchKernelEx(&cfg, kernel, p);
 }
 
+template <int D, int FMT, int PASSES, bool NORM>
+cudaError_t start_blocks(const Params &p, int64_t ctas, cudaStream_t stream)
+{
+    constexpr size_t smem = (size_t)PASSES * (2 * kStages + 4) * kBlockThreads * 16;
+    {
+        static std::mutex mu;
+        static bool set[64] = {};
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        std::lock_guard<std::mutex> lk(mu);
+        if (dev >= 64 || !set[dev]) {
+            e = cudaFuncSetAttribute(append_kernel<D, FMT, PASSES, NORM>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+            if (e != cudaSuccess) return e;
+            if (dev < 64) set[dev] = true;
+        }
+    }
+    return start(append_kernel<D, FMT, PASSES, NORM>, p, ctas, stream, kBlockThreads, smem);
+}
+
 template <int D, bool NORM>
 cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *launches)
 {
-    constexpr int groups = kThreads / (D / 8);
+    constexpr int groups = kThreads / (D / 16);
     const AppendArgs &a = p.a;
     const bool e4m3 = fmt == SLORA_KV_E4M3;
     cudaError_t e;
     {
-        // two rows per group of lanes and CTA
+        // a row per group of lanes
         p.q_rows = a.b.max_q == 1 ? a.n_q : 0;
         const int32_t all = 2 * a.c.n_kv + p.q_rows;
-        p.splits = (all + 2 * groups - 1) / (2 * groups);
+        p.splits = (all + groups - 1) / groups;
         p.units = (all + p.splits - 1) / p.splits;
         e = start(e4m3 ? append_one_kernel<D, SLORA_KV_E4M3, NORM> : append_one_kernel<D, SLORA_KV_INT8, NORM>, p,
                   (int64_t)a.b.S * p.splits, stream);
@@ -727,19 +809,12 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
         if (e != cudaSuccess || a.b.max_q == 1) return e;
     }
     const int64_t ctas = (int64_t)kBlockCtas * num_sms;
-    // rows of a block over the CTA's groups: the registers for 2, 3 or 4 of them per lane (a
-    // page of up to 8192, 12288 or 16384 bytes)
-    constexpr int block_groups = kBlockThreads / (D / 8);
-    const int passes = (a.c.bt + block_groups - 1) / block_groups;
-    if (passes <= 2)
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 2, NORM> : append_kernel<D, SLORA_KV_INT8, 2, NORM>, p, ctas, stream,
-                  kBlockThreads);
-    else if (passes <= 3)
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 3, NORM> : append_kernel<D, SLORA_KV_INT8, 3, NORM>, p, ctas, stream,
-                  kBlockThreads);
+    // rows of a block over the CTA's groups: one or two per lane (a page of up to 8192 or 16384 bytes)
+    constexpr int block_groups = kBlockThreads / (D / 16);
+    if (a.c.bt <= block_groups)
+        e = e4m3 ? start_blocks<D, SLORA_KV_E4M3, 1, NORM>(p, ctas, stream) : start_blocks<D, SLORA_KV_INT8, 1, NORM>(p, ctas, stream);
     else
-        e = start(e4m3 ? append_kernel<D, SLORA_KV_E4M3, 4, NORM> : append_kernel<D, SLORA_KV_INT8, 4, NORM>, p, ctas, stream,
-                  kBlockThreads);
+        e = e4m3 ? start_blocks<D, SLORA_KV_E4M3, 2, NORM>(p, ctas, stream) : start_blocks<D, SLORA_KV_INT8, 2, NORM>(p, ctas, stream);
     *launches += e == cudaSuccess;
     if (e != cudaSuccess || !a.q) return e;
     const int64_t items = (int64_t)a.b.T * ((a.n_q + kQHeads - 1) / kQHeads);
