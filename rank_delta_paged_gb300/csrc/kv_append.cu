@@ -227,8 +227,12 @@ __device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const fl
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = add2(y[i], mm);
     }
+    // (the squares one by one: the compiler makes one rounding of a packed product and its sum)
 #pragma unroll
-    for (int i = 0; i < 8; ++i) z[i] = mul2(y[i], y[i]);
+    for (int i = 0; i < 8; ++i) {
+        const float2 t = unpair(y[i]);
+        z[i] = pair(__fmul_rn(t.x, t.x), __fmul_rn(t.y, t.y));
+    }
     const float r = rsqrtf(__fadd_rn(row_sum<D>(z) * (1.f / D), a.eps));
     const uint64_t rr = pair(r, r);
 #pragma unroll

@@ -18,29 +18,37 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
     griddep_wait();
     griddep_launch_dependents();
     const int tid = threadIdx.x;
+    int32_t i = (int32_t)blockIdx.x;
+    auto rows_of = [&](int32_t k) { return a.rows ? __ldg(a.rows + k) : a.c.bt; };
+    int32_t s = __ldg(a.src + i), d = __ldg(a.dst + i), rows = rows_of(i);
 #pragma unroll 1
-    for (int64_t i = blockIdx.x; i < a.n; i += gridDim.x) {
-        const int32_t s = a.src[i], d = a.dst[i], rows = a.rows ? a.rows[i] : a.c.bt;
+    for (;;) {
+        // the next page's entries, while this one's rows are on their way
+        const int32_t next = a.n - i > (int32_t)gridDim.x ? i + (int32_t)gridDim.x : -1;
+        int32_t ns = 0, nd = 0, nrows = 0;
+        if (next >= 0) ns = __ldg(a.src + next), nd = __ldg(a.dst + next), nrows = rows_of(next);
         if (s < 0 || s >= a.c.num_pages || d < 0 || d >= a.c.num_pages || rows < 0 || rows > a.c.bt) {
             if (tid == 0)
                 set_status(a.c.status, rows < 0 || rows > a.c.bt ? SLORA_DEV_BAD_LENGTH : SLORA_DEV_BAD_PAGE);
-            continue;
-        }
-        if (s == d || rows == 0) continue;
-        const uint4 *from = reinterpret_cast<const uint4 *>(a.c.pool + s * a.c.page_bytes);
-        uint4 *to = reinterpret_cast<uint4 *>(a.c.pool + d * a.c.page_bytes);
-        const int32_t chunks = rows * a.row_bytes / 16;
+        } else if (s != d && rows > 0) {
+            const uint4 *from = reinterpret_cast<const uint4 *>(a.c.pool + s * a.c.page_bytes);
+            uint4 *to = reinterpret_cast<uint4 *>(a.c.pool + d * a.c.page_bytes);
+            const int32_t chunks = rows * a.row_bytes / 16;
+            const int8_t e = tid == 0 ? a.c.exps[s] : 0;
 #pragma unroll 1
-        for (int32_t k = tid; k < chunks; k += 4 * kCopyThreads) {
-            uint4 v[4];
+            for (int32_t k = tid; k < chunks; k += 4 * kCopyThreads) {
+                uint4 v[4];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (k + j * kCopyThreads < chunks) v[j] = from[k + j * kCopyThreads];
+                for (int j = 0; j < 4; ++j)
+                    if (k + j * kCopyThreads < chunks) v[j] = from[k + j * kCopyThreads];
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                if (k + j * kCopyThreads < chunks) to[k + j * kCopyThreads] = v[j];
+                for (int j = 0; j < 4; ++j)
+                    if (k + j * kCopyThreads < chunks) to[k + j * kCopyThreads] = v[j];
+            }
+            if (tid == 0) a.c.exps[d] = e;
         }
-        if (tid == 0) a.c.exps[d] = a.c.exps[s];
+        if (next < 0) return;
+        i = next, s = ns, d = nd, rows = nrows;
     }
 }
 

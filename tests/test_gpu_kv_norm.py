@@ -227,6 +227,35 @@ def test_norm_does_not_depend_on_the_kernel(d, centered):
                 assert np.array_equal(va[pa, 0], vb[pb, t % 8])
 
 
+def step_by_step(x, w, eps, centered):
+    """The norm in fp32, each step rounded once: the even and the odd channels of each 8 summed one after another, then
+    the eights by twos; the reciprocal root is CUDA's."""
+    def mean(y):
+        y = y.reshape(*y.shape[:-1], -1, 4, 2)
+        y = ((y[..., 0, :] + y[..., 1, :]) + y[..., 2, :]) + y[..., 3, :]
+        y = y[..., 0] + y[..., 1]
+        while y.shape[-1] > 1:
+            y = y[..., 0::2] + y[..., 1::2]
+        return y * np.float32(1.0 / x.shape[-1])
+    x = x.astype(np.float32)
+    if centered:
+        x = x - mean(x)
+    r = torch.rsqrt(dev(mean(x * x) + np.float32(eps))).cpu().numpy()
+    return (x * r) * w
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("centered", [False, True])
+@pytest.mark.parametrize("seqs", [[(1, 70)] * 300, [(300, 400)]], ids=["single", "prompt"])
+def test_norm_rounds_every_step_by_itself(d, centered, seqs):
+    """No product is contracted into a sum, in either kernel: the queries bit for bit."""
+    c = Case(seqs, hq=8, hkv=2, d=d, seed=82)
+    x = Call(c, rot=0, centered=centered, weights="heads", eps=1e-5)
+    _, _, out = x.check()
+    want = step_by_step(x.q, x.qw[:, :d], 1e-5, centered).astype(np.float16).reshape(c.T, -1)
+    assert np.array_equal(out[:c.T, :8 * d].view(np.uint16), want.view(np.uint16))
+
+
 def test_norm_in_a_graph_on_another_stream_then_attention():
     """A graph of an append with norms and the attention over it, replayed with other tokens, against eager calls."""
     seqs = [(1, 70), (1, 200), (130, 300), (2, 65), (9, 70)]
