@@ -84,11 +84,13 @@ const char *slora_status_str(slora_status s);
 /* Message of the calling thread's last failed call ("" if none).  Valid until the
  * thread's next failing call. */
 const char *slora_last_error(void);
-/* Library version as major * 10000 + minor * 100 + patch: 300 (0.3.0).  0.2.0 added
+/* Library version as major * 10000 + minor * 100 + patch: 400 (0.4.0).  0.2.0 added
  * slora_lora_apply_multi, residency under pool pressure (slora_adapters_acquire /
  * release, slora_pages_alloc_evict, slora_pool_get_stats, slora_lru_*) and the padded
- * batched-GEMM comparison path (slora_lora_apply_bmm); 0.3.0 adds the 8-bit KV cache in
- * the pool's pages (slora_kv_*). */
+ * batched-GEMM comparison path (slora_lora_apply_bmm); 0.3.0 added the 8-bit KV cache in
+ * the pool's pages (slora_kv_*); 0.4.0 adds to it appends with norms (slora_kv_append_norm),
+ * attention with sinks (slora_kv_attend_sinks), copies and shared holders of pages
+ * (slora_kv_copy, slora_pages_share) and compaction (slora_kv_compact). */
 int32_t slora_version(void);
 
 /* ---------------------------------------------------------------------------
@@ -100,7 +102,7 @@ int32_t slora_version(void);
  * free() returns pages; a page that is out of range or not allocated fails the whole
  * call with SLORA_ERR_INVALID_ARG before any page is returned.
  * share() adds a holder to each listed page (a page listed twice gets two); every holder frees the page
- * once, and the last one's free returns it.  A page that is out of range or not allocated fails the whole
+ * once, in a call of its own, and the last one's free returns it.  A page that is out of range or not allocated fails the whole
  * call before anything is shared.
  * ------------------------------------------------------------------------- */
 slora_status slora_pagealloc_create(int64_t num_pages, uint64_t shuffle_seed,
@@ -541,6 +543,7 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * in fp32 (the reciprocal square root to 2^-22 of its value, every other step rounded once, the sums in an
  * order that depends on head_dim alone, so that a token's codes depend on neither the batch nor the
  * kernel); values are not normalised.  A row with an infinity or a NaN becomes what the formula gives for it.
+ * Exponents end at 60 here, whatever the weights: keys beyond that become the largest code.
  * rope may be NULL here, with q too.
  *   norm
  *     centered     0: root mean square;  1: the mean is taken out first

@@ -333,6 +333,14 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
     }
     return encode2<FMT>(a * unit, b * unit) | encode2<FMT>(c * unit, d * unit) << 16;
 }
+// The exponent of new values: with weights it may be any, and what is read back ends at kExpLimit.
+template <int FMT, bool NORM>
+__device__ __forceinline__ int new_exponent(float m)
+{
+    const int e = fit_exponent<FMT>(m);
+    return NORM && e > kExpLimit ? kExpLimit : e;
+}
+
 // This lane's codes to a row.
 template <int D, int FMT>
 __device__ __forceinline__ void write_codes(uint8_t *row, int ch, const float (&x)[16], float unit)
@@ -426,7 +434,7 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     const int was = __shfl_sync(~0u, old, 0, LPR);
     if (live && query) write_query<D>(a.q_out + t0 * a.q_out_stride + (int64_t)h * D, ch, x);
     if (page < 0) return;
-    const int fit = fit_exponent<FMT>(m), e = held && was > fit ? was : fit;
+    const int fit = new_exponent<FMT, NORM>(m), e = held && was > fit ? was : fit;
     uint8_t *dst = a.c.pool + page * a.c.page_bytes;
     if (held && was < e) {
         const float unit = pow2(was - e);
@@ -583,7 +591,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
         __syncthreads();
         m = __uint_as_float(s_max[turn]);
         turn = turn == 2 ? 0 : turn + 1;
-        int e = fit_exponent<FMT>(m);
+        int e = new_exponent<FMT, NORM>(m);
         uint8_t *dst = a.c.pool + page * a.c.page_bytes;
         if (held) {
             if (old >= e) {

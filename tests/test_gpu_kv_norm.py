@@ -286,6 +286,30 @@ def test_norm_in_a_graph_on_another_stream_then_attention():
     assert c.s.device_status() == 0
 
 
+@pytest.mark.parametrize("fmt", ["e4m3", "int8"])
+def test_norm_with_weights_past_the_exponents(fmt):
+    """Keys beyond the largest scale become the largest code, and the block's other rows stay what they were."""
+    for seqs in ([(1, 70)] * 3, [(5, 70)]):
+        c = Case(seqs, hq=4, hkv=2, fmt=fmt, seed=83)
+        x = Call(c, rot=0, weights="heads")
+        x.norm = rdp.KVNorm(1e-6, False, None, 0, torch.full((128,), 1e30, device="cuda"), 0)
+        before, exps = c.values()
+        x.run()
+        got, ge = c.values()
+        assert c.s.device_status() == 0
+        for s, (n, length) in enumerate(seqs):
+            for h in range(2):
+                p = c.table[s, 1, h, 0]
+                held = length - n - c.bt
+                assert ge[p] == 60
+                new = got[p, held:held + n]
+                k = x.k[c.indptr[s]:c.indptr[s] + n, h].astype(np.float64)
+                r = 1 / np.sqrt((k ** 2).mean(-1, keepdims=True) + 1e-6)
+                large = np.abs(k * r) > 1e-8                   # 1e22 and more, of 5e20
+                assert np.array_equal(new[large], (R.LIMIT[fmt] * np.sign(k))[large])
+                assert np.array_equal(got[p, :held], R.nearest(before[p, :held] * 2.0 ** (int(exps[p]) - 60), fmt))
+
+
 def test_norm_in_place_and_rows_of_nobody():
     """q_out is q; rows outside every sequence are left as they were."""
     c = Case([(1, 33), (6, 20)], hq=4, hkv=2, seed=80)
