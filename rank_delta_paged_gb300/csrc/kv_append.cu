@@ -352,20 +352,32 @@ __device__ __forceinline__ void write_codes(uint8_t *row, int ch, const float (&
                        encode4<FMT>(x[8 * h + 4], x[8 * h + 5], x[8 * h + 6], x[8 * h + 7], unit));
 }
 
-// Sixteen codes of a row divided by a power of two (unit < 1).
-template <int FMT>
-__device__ __forceinline__ void rescale16(uint4 *at, float unit)
+// This lane's sixteen codes of the rows r0, r0 + step, .. below `held` of a page divided by a power of two (unit < 1),
+// N rows' reads at a time.
+template <int D, int FMT, int N>
+__device__ __forceinline__ void rescale_rows(uint8_t *page, int ch, int r0, int step, int held, float unit)
 {
-    const uint4 v = *at;
-    uint32_t w[4] = {v.x, v.y, v.z, v.w};
+    uint4 *at = reinterpret_cast<uint4 *>(page + ch * 16);
+#pragma unroll 1
+    for (int k = r0; k < held; k += N * step) {
+        uint4 v[N];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        uint32_t lo, hi;
-        decode4<FMT>(w[i], lo, hi);
-        const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
-        w[i] = encode4<FMT>(a.x, a.y, b.x, b.y, unit);
+        for (int j = 0; j < N; ++j)
+            if (k + j * step < held) v[j] = at[(k + j * step) * (D / 16)];
+#pragma unroll
+        for (int j = 0; j < N; ++j) {
+            if (k + j * step >= held) break;
+            uint32_t w[4] = {v[j].x, v[j].y, v[j].z, v[j].w};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t lo, hi;
+                decode4<FMT>(w[i], lo, hi);
+                const float2 a = __half22float2(*reinterpret_cast<__half2 *>(&lo)), b = __half22float2(*reinterpret_cast<__half2 *>(&hi));
+                w[i] = encode4<FMT>(a.x, a.y, b.x, b.y, unit);
+            }
+            at[(k + j * step) * (D / 16)] = make_uint4(w[0], w[1], w[2], w[3]);
+        }
     }
-    *at = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int32_t in_cache)
@@ -436,13 +448,9 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     if (page < 0) return;
     const int fit = new_exponent<FMT, NORM>(m), e = held && was > fit ? was : fit;
     uint8_t *dst = a.c.pool + page * a.c.page_bytes;
-    if (held && was < e) {
-        const float unit = pow2(was - e);
-#pragma unroll 1
-        for (int k = 0; k < held; ++k) rescale16<FMT>(reinterpret_cast<uint4 *>(dst + k * D + ch * 16), unit);
-    }
     if (ch == 0) a.c.exps[page] = (int8_t)e;
     write_codes<D, FMT>(dst + held * D, ch, x, pow2(-e));
+    if (held && was < e) rescale_rows<D, FMT, 8>(dst, ch, 0, 1, held, pow2(was - e));
 }
 
 // The queries of a batch: kQHeads heads of one token per group of lanes and step.
@@ -593,15 +601,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
         turn = turn == 2 ? 0 : turn + 1;
         int e = new_exponent<FMT, NORM>(m);
         uint8_t *dst = a.c.pool + page * a.c.page_bytes;
-        if (held) {
-            if (old >= e) {
-                e = old;
-            } else {
-                const float unit = pow2(old - e);
-#pragma unroll 1
-                for (int r = grp; r < held; r += GROUPS) rescale16<FMT>(reinterpret_cast<uint4 *>(dst + r * D + ch * 16), unit);
-            }
-        }
+        if (held && old > e) e = old;
         if (tid == 0) a.c.exps[page] = (int8_t)e;
         const float unit = pow2(-e);
 #pragma unroll
@@ -609,6 +609,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
             const int r = i * GROUPS + grp;
             if (r < nt) write_codes<D, FMT>(dst + (held + r) * D, ch, x[i], unit);
         }
+        if (held && old < e) rescale_rows<D, FMT, 1>(dst, ch, grp, GROUPS, held, pow2(old - e));
     }
 }
 
