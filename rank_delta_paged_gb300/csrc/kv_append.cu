@@ -1,6 +1,8 @@
 // Append to the 8-bit paged KV cache: the new tokens' keys, rotated by their positions, and
-// values become codes with one power-of-two scale per page; queries are rotated beside them.
+// values become codes with one power-of-two scale per page; queries are rotated beside them.  With
+// NORM, queries and keys are normalised per head before that.
 //
+//     y = (x - m) / sqrt(mean((x - m)^2) + eps) w        m = 0 or the mean of x (NORM)
 //     (a, b) -> (a cos - b sin, b cos + a sin)      per pair of channels
 //     e = max(e of the block if it holds tokens, smallest e with max |x| <= limit 2^e)
 //     code = round(x 2^-e)
@@ -10,25 +12,33 @@
 // angles and exponents).  The scale of a block needs the largest value of all its new tokens
 // before the first code can be written, so a block's tokens stay in registers between the two.
 //
-// Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
-// values and queries alike; a row is a group of head_dim / 8 lanes, which holds two of them at a
-// time, and all of its reads that do not depend on others go first.
-// Other sequences (append_kernel): the pages of all blocks that they touch form one list, of which
-// every CTA takes an equal run, page after page by the whole CTA with the next page's rows under
-// way.  Their queries are a kernel of their own (rotate_kernel).
+// A lane holds 16 channels of a row, chunk ch of 8 of either half: where the whole row turns in halves,
+// partners and their angle are in one lane, and what a row costs besides its channels (page ids,
+// exponents, addresses) is shared by twice as many of them.  With 8 channels a lane and shuffles between partners
+// 512 single tokens of 40 heads took 15.3 us instead of 10.5, 5046 tokens 65 instead of 54.
 //
-// Measured: 512 single tokens of 40 heads 15 us; 5046 tokens, of which 384 are single, of 32 heads 65 us
-// (3.2 TB/s); 16381 tokens of 8 heads of 64 51 us (3.7 TB/s).  The instructions between the reads and
-// the writes (some 180 per warp and 16 bytes a lane) and the waits for a page's reads take the time.
+// Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
+// values and queries alike; a row is a group of head_dim / 16 lanes, and all of its reads that do not
+// depend on others go first.  (A CTA that goes on to other tokens with their offsets read ahead: no gain without
+// norms, 21.9 us instead of 16.4 with them, for its registers.)
+// Other sequences (append_kernel): the pages of all blocks that they touch form one list, of which
+// every CTA takes an equal run, page after page by the whole CTA.  Shared memory, of which every thread
+// reads what it has written itself, holds the rows of the page and the next two (asynchronous copies) and
+// the rows' angles, which are the same for all heads of the block.  Their queries are a kernel of their own (rotate_kernel).
+//
+// Measured: 512 single tokens of 40 heads 10.5 us, with norms 14; 5046 tokens, of which 384 are single, of 32
+// heads 54 us (3.9 TB/s), with the mean taken out and a weight for each head 75; 16381 tokens of 8 heads of 64 49 us
+// (3.9 TB/s).  The instructions between the reads and the writes, the barrier of a page's maximum and the waits for
+// exponents take the time.
 // With two CTAs' worth of pages per block and CTAs found by a search of the token offsets, the
 // 5046 tokens took 93 us: half the SMs had twice the work of the others.
 // These times are of tokens that no block's exponent grows for.  Where it does, the group of lanes that has the
-// page's token rescales the rows before it one after another: the 512 single tokens, from a cold cache
-// and with the launch, take 23 us without, 58 with 681 of their 40960 pages growing and 136 with 9841 (INT8 66
-// and 160); the 5046 tokens 71, then 91 with 4379 pages growing.
-// Pages above 8192 bytes have more rows per lane: 4096 tokens in prompts, cold, 57 us at 8192 bytes and 32
-// heads (3.0 TB/s), 98 at 10240 and 40 (2.2 TB/s: the registers for 3 rows at two CTAs per SM spill), 111
-// at 16384 and 64 (3.0 TB/s).
+// page's token rescales the rows before it, eight at a time: the 512 single tokens, from a cold cache
+// and with the call, take 26 us without, 45 with 215 of their 40960 pages growing and 55 with 9632 (INT8 25, 51 with
+// 246, 87 with 11157); row by row before the new codes were written it was 71 and 100.  The 5046 tokens 67, then 87 with
+// 10720 pages growing.
+// Pages above 8192 bytes have two rows per lane and one CTA per SM: 4096 tokens in prompts, cold, 56 us at 8192 bytes and
+// 32 heads (3.0 TB/s), 73 at 10240 and 40 (2.9 TB/s), 97 at 16384 and 64 (3.5 TB/s).
 #include <mutex>
 
 #include "host_common.h"
@@ -41,14 +51,14 @@ namespace kv {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kBlockThreads = 512;  // append_kernel: two rows of 64 per group of 16 lanes
+constexpr int kBlockThreads = 512;  // append_kernel: 64 rows of 128 channels, or 128 of 64
 constexpr int kMaxUnits = 128;     // pages of a block at a time, at most
 constexpr int kSeqChunks = 64;
-// append_kernel's CTAs per SM: those that fit with 2 or 3 rows per lane (with 4 one fits, and the other half of
+// append_kernel's CTAs per SM: those that fit with a row per lane (with 2 one fits, and the other half of
 // the grid follows it).  4 and 8 cost 1 to 8 us more for their starts.
 constexpr int kBlockCtas = 2;
 constexpr int kStages = 3;         // append_kernel: a page's rows and those of the next two
-constexpr int kQHeads = 2;         // query heads per group and step
+constexpr int kQHeads = 2;         // query heads per group and step; by 4 the 5046 tokens with norms took 80 us, by 2 78
 
 struct Params {
     AppendArgs a;
@@ -387,6 +397,7 @@ __device__ __forceinline__ int32_t position(const AppendArgs &a, int32_t t, int3
 
 // Single tokens.  Row u of a token: keys, then values, of the KV heads, then query heads, so that most warps
 // have rows of one kind and those of values do not rotate.
+// CTAs per SM: with norms by 3, 4 (a few spills) 15.2 and 13.8 us for the 512 tokens; without, 5 fit.
 template <int D, int FMT, bool NORM>
 __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(const __grid_constant__ Params p)
 {

@@ -1,6 +1,9 @@
 // Pages of the 8-bit KV cache moved about: copies of pages, and the compaction of sequences to their kept tokens.
 //
-// What bounds a copy: its rows are read and written once.
+// What bounds a copy: its rows are read and written once.  A CTA takes a page at a time, 16 bytes a lane and up to
+// four pieces a lane under way, with the next page's entries read meanwhile.
+// Measured: 30011 pages of 10 KB 98 us, 6.3 TB/s, 93 % of a plain copy's rate (106 without the reads ahead; by 512 threads and 4
+// CTAs per SM 125, by 128 and 16 98); 16 pages 1.8 us on the GPU.
 #include "host_common.h"
 #include "internal.h"
 #include "kv.h"
@@ -57,8 +60,13 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const __grid_constan
 //     e = the smallest exponent that max |code 2^e_row| fits        code <- round(code 2^(e_row - e))
 // What bounds it: the kept rows are read and written once; for few of them the chain of dependent reads (offsets,
 // kept positions, pages, exponents, rows).
+// Measured: 30 thousand kept tokens of six sequences, 8 heads, into pages of their own 29 us, 4.3 TB/s of rows of 128 bytes;
+// 29 thousand of a choice for each head, rows of 64 bytes, 24 us (2.6 TB/s; memory moves 1.7 times as much for such rows);
+// 24 drafted branches in place 5 us on the GPU.  At 68 % issue the instructions are the bound, some 180 per lane and 16
+// bytes.  With the rows in registers instead of shared memory 36 us (the decoded codes of the maximum were kept, and
+// spilled), with codes rescaled in fp32 51; the maximum over the codes as integers 30.
 constexpr int kMaxCluster = 8;
-constexpr int kFill = 1280;      // threads per SM that the registers are to allow
+constexpr int kFill = 1280;      // threads per SM that the registers are to allow (1024 and 1536: within 3 %)
 constexpr int64_t kCompactCtas = 1 << 20;     // of a grid, at most: the hardware deals them out as SMs become free
 
 // The largest finite magnitude of 16 codes.

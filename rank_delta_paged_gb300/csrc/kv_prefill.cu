@@ -25,6 +25,11 @@
 // The key tiles of all units form one list, of which every CTA takes an equal run; a unit that
 // is cut between CTAs is joined by the last of them to finish, in the order of the list.
 //
+// With SINKS a unit's keys are numbered without those between the sequence's first tokens and the first of its rows' windows
+// (kv.h, key_shift), so the sinks fill up the window's first tile.  Eight chunks of 1500 to 2048 tokens x 32 heads over windows
+// of 2048 and 128 sinks: 660 to 690 us, 0.74 PFLOP/s (623 us without the sinks): a unit has 18 tiles of 2.2 us and pays
+// some 15 us for its start, its end and the masks of the tiles at either end of the window.
+//
 // Measured: 2048 tokens x 32 heads over 30001 keys of 8 KV heads: 0.93 ms, 1.12 PFLOP/s, 58% of what a library
 // product reaches; 16 prompts of 512, 32 heads: 108 us (E4M3; 105 without the look for NaN outputs).  A tile takes 2.3 us where its products need
 // 1.3: the warps' instruction fetch and the softmax's waits for tensor memory.  Prompts this
