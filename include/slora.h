@@ -600,8 +600,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   first        device int32 [S], or NULL: 0
  *   kv_len       device int32 [S]: the sequences' lengths before
  *   block_table  device int32 [S][max_blocks][n_kv_heads][2], as in slora_kv_batch
- *   dst_table    device int32 [S][dst_blocks][n_kv_heads][2]: where the blocks from first[s] on go, or NULL: in place.
- *                Only entries of written blocks are read.  A page that is written is none that the call
+ *   dst_table    device int32 [S][dst_blocks][n_kv_heads][2]: where the blocks from first[s] on go; NULL, or block_table
+ *                itself: in place.  Only entries of written blocks are read.  A page that is written is none that the call
  *                reads, but that the block of first[s] may keep its page (or its page may be shared with the
  *                source table).  In that block the tokens before first[s] are written too.
  *   new_len      device int32 [S] that gets first[s] + the kept tokens, or NULL; none of the other arrays

@@ -391,8 +391,9 @@ extern "C" slora_status slora_kv_compact(slora_kv_t k, const slora_kv_keep *keep
     const char *fn = "kv_compact";
     if (!k || !keep)
         return fail(SLORA_ERR_INVALID_ARG, "%s: null cache or lists", fn);
+    const int32_t *dst_table = keep->dst_table == keep->block_table ? nullptr : keep->dst_table;
     if (keep->n_seqs < 0 || keep->n_seqs > (1 << 20) || keep->n_kept < 0 || keep->n_kept > (1 << 30) || keep->max_kept < 0 ||
-        keep->max_kept > (1 << 30) || keep->max_blocks < 1 || (keep->dst_table && keep->dst_blocks < 1) ||
+        keep->max_kept > (1 << 30) || keep->max_blocks < 1 || (dst_table && keep->dst_blocks < 1) ||
         (keep->kept_head_stride != 0 && keep->kept_head_stride < keep->n_kept))
         return fail(SLORA_ERR_INVALID_ARG, "%s: n_seqs=%d n_kept=%d max_kept=%d max_blocks=%d dst_blocks=%d kept_head_stride=%lld", fn,
                     keep->n_seqs, keep->n_kept, keep->max_kept, keep->max_blocks, keep->dst_blocks,
@@ -420,13 +421,13 @@ extern "C" slora_status slora_kv_compact(slora_kv_t k, const slora_kv_keep *keep
     a.n_kept = keep->n_kept;
     a.max_kept = keep->max_kept < keep->n_kept ? keep->max_kept : keep->n_kept;
     a.max_blocks = keep->max_blocks;
-    a.dst_blocks = keep->dst_table ? keep->dst_blocks : keep->max_blocks;
+    a.dst_blocks = dst_table ? keep->dst_blocks : keep->max_blocks;
     a.indptr = keep->kept_indptr;
     a.kept = keep->kept;
     a.first = keep->first;
     a.kv_len = keep->kv_len;
     a.table = keep->block_table;
-    a.dst_table = keep->dst_table;
+    a.dst_table = dst_table;
     a.head_stride = keep->kept_head_stride;
     a.new_len = keep->new_len;
     DeviceScope dev_scope(k->device);

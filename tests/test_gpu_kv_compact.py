@@ -231,6 +231,19 @@ def test_compact_without_optional_arrays():
     assert (m.new_len == -5).all() and m.c.s.device_status() == 0
 
 
+def test_compact_into_the_same_table_is_in_place():
+    """The block table as dst_table, of whatever width it says."""
+    for n in ([300, 200], [9000]):
+        a, b = (Moves(n, [0] * len(n), [100] * (len(n) - 1) + [n[-1] - 50], seed=219) for _ in range(2))
+        a.check()
+        k = b.lists()
+        k.dst_table, k.dst_blocks = k.block_table, 1
+        rdp.slora_kv_compact(b.c.s.kv, k)
+        torch.cuda.synchronize()
+        assert torch.equal(a.c.s.pages, b.c.s.pages) and torch.equal(a.c.s.exponents, b.c.s.exponents)
+        assert b.c.s.device_status() == 0
+
+
 def test_compact_does_not_depend_on_max_kept():
     for in_place in (False, True):
         m = Moves([300, 200], [10, 0], [100, 50], seed=212, in_place=in_place)
