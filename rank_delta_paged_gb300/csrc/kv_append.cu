@@ -58,7 +58,8 @@ constexpr int kSeqChunks = 64;
 // the grid follows it).  4 and 8 cost 1 to 8 us more for their starts.
 constexpr int kBlockCtas = 2;
 constexpr int kStages = 3;         // append_kernel: a page's rows and those of the next two
-constexpr int kQHeads = 2;         // query heads per group and step; by 4 the 5046 tokens with norms took 80 us, by 2 78
+constexpr int kQHeads = 2;         // rotate_kernel: query heads at a time, and CTAs per SM.  1 and 4: 3 to 6 % slower
+constexpr int kQCtas = 3;
 
 struct Params {
     AppendArgs a;
@@ -66,6 +67,7 @@ struct Params {
     int32_t splits;      // CTAs per sequence
     int32_t units;       // rows per CTA
     int32_t q_rows;      // query heads that go with the keys and values
+    int32_t q_run;       // rotate_kernel: heads per group of lanes
 };
 
 // append_kernel's place in its run: what is left, and the part at hand.
@@ -464,9 +466,9 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     if (held && was < e) rescale_rows<D, FMT, 8>(dst, ch, 0, 1, held, pow2(was - e));
 }
 
-// The queries of a batch: kQHeads heads of one token per group of lanes and step.
+// The queries of a batch: q_run heads of one token per group of lanes, kQHeads at a time with the next ones on their way.
 template <int D, bool NORM>
-__global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_constant__ Params p)
+__global__ void __launch_bounds__(kThreads, kQCtas) rotate_kernel(const __grid_constant__ Params p)
 {
     constexpr int LPR = D / 16, GROUPS = kThreads / LPR;
     const AppendArgs &a = p.a;
@@ -474,19 +476,26 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_consta
     const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
     // as append_kernel
     griddep_launch_dependents();
-    const int32_t per = (a.n_q + kQHeads - 1) / kQHeads;
+    const int32_t per = (a.n_q + p.q_run - 1) / p.q_run;
     const int64_t total = (int64_t)a.b.T * per;
     const int64_t step = (int64_t)gridDim.x * GROUPS;
 #pragma unroll 1
     for (int64_t i0 = (int64_t)blockIdx.x * GROUPS; i0 < total; i0 += step) {
         const int64_t i = i0 + grp;
         const bool live = i < total;
-        // (at most 2^20 tokens and 2^11 groups of heads)
-        const int32_t t = live ? (int32_t)((uint32_t)i / (uint32_t)per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * kQHeads : 0;
+        // (at most 2^20 tokens and 2^12 runs of heads)
+        const int32_t t = live ? (int32_t)((uint32_t)i / (uint32_t)per) : 0, h0 = live ? (int32_t)(i - (int64_t)t * per) * p.q_run : a.n_q;
+        const int32_t hend = h0 + p.q_run < a.n_q ? h0 + p.q_run : a.n_q;
+        const __half *src = a.q + t * a.q_stride;
         Raw v[kQHeads];
+        auto read = [&](int32_t h) {
 #pragma unroll
-        for (int k = 0; k < kQHeads; ++k)
-            if (live && h0 + k < a.n_q) v[k] = read_row<D>(a.q + t * a.q_stride + (int64_t)(h0 + k) * D, ch);
+            for (int k = 0; k < kQHeads; ++k) {
+                v[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
+                if (h + k < hend) v[k] = read_row<D>(src + (int64_t)(h + k) * D, ch);
+            }
+        };
+        read(h0);
         int32_t pos = a.positions && live ? a.positions[t] : 0;
         // rows outside every sequence, and those of a sequence that is skipped, are left alone
         int32_t lo = 0, n = a.b.S;               // the last of n from lo that starts at or before t, a lane per part of them
@@ -505,15 +514,23 @@ __global__ void __launch_bounds__(kThreads, 3) rotate_kernel(const __grid_consta
         Rot r;
         r.on = false;
         if (mine) load_rot<D>(a, pos, ch, r);
+        __half *dst = a.q_out + t * a.q_out_stride;
+#pragma unroll 1
+        for (int32_t h = 0; h < p.q_run; h += kQHeads) {
+            Raw w[kQHeads];
 #pragma unroll
-        for (int k = 0; k < kQHeads; ++k) {
-            const bool some = mine && h0 + k < a.n_q;
-            float x[16];
-            if (!some) v[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-            unpack(v[k], x);
-            if (NORM) normalise<D, false>(a, true, some && a.q_weight ? a.q_weight + (h0 + k) * a.q_weight_stride : nullptr, ch, x);
-            rotate<D>(a, r, ch, x);
-            if (some) write_query<D>(a.q_out + t * a.q_out_stride + (int64_t)(h0 + k) * D, ch, x);
+            for (int k = 0; k < kQHeads; ++k) w[k] = v[k];
+            if (h + kQHeads < p.q_run) read(h0 + h + kQHeads);
+#pragma unroll
+            for (int k = 0; k < kQHeads; ++k) {
+                const int32_t head = h0 + h + k;
+                const bool some = mine && head < hend;
+                float x[16];
+                unpack(w[k], x);
+                if (NORM) normalise<D, false>(a, true, some && a.q_weight ? a.q_weight + head * a.q_weight_stride : nullptr, ch, x);
+                rotate<D>(a, r, ch, x);
+                if (some) write_query<D>(dst + (int64_t)head * D, ch, x);
+            }
         }
     }
     griddep_wait();
@@ -841,7 +858,12 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
         e = e4m3 ? start_blocks<D, SLORA_KV_E4M3, 2, NORM>(p, ctas, stream) : start_blocks<D, SLORA_KV_INT8, 2, NORM>(p, ctas, stream);
     *launches += e == cudaSuccess;
     if (e != cudaSuccess || !a.q) return e;
-    const int64_t items = (int64_t)a.b.T * ((a.n_q + kQHeads - 1) / kQHeads);
+    // Heads per group of lanes: a run of them shares the search for its token's sequence and the angles, and the next
+    // ones' reads are under way; as long as the runs fill the SMs.  By 2, 4, 8 and 16: 5046 tokens of 32 heads 55.7, 50.1,
+    // 47.7 and 46.3 us, with norms 79, 73, 71 and 74; 16381 of 32 heads of 64 channels 52.1, 44.7, 42.2 and 43.2.
+    for (p.q_run = 8; p.q_run > 2; p.q_run /= 2)
+        if ((int64_t)a.b.T * ((a.n_q + p.q_run - 1) / p.q_run) >= (int64_t)kQCtas * num_sms * groups) break;
+    const int64_t items = (int64_t)a.b.T * ((a.n_q + p.q_run - 1) / p.q_run);
     int64_t q_ctas = (items + groups - 1) / groups;
     if (q_ctas > 32ll * num_sms) q_ctas = 32ll * num_sms;
     e = start(rotate_kernel<D, NORM>, p, q_ctas, stream);

@@ -14,7 +14,7 @@ import torch
 
 import kv_reference as R
 import rank_delta_paged_gb300 as rdp
-from test_gpu_kv import Case, dev, half
+from test_gpu_kv import Case, check_append, dev, half
 
 pytestmark = pytest.mark.gpu
 U = 2.0 ** -24
@@ -254,6 +254,30 @@ def test_norm_rounds_every_step_by_itself(d, centered, seqs):
     _, _, out = x.check()
     want = step_by_step(x.q, x.qw[:, :d], 1e-5, centered).astype(np.float16).reshape(c.T, -1)
     assert np.array_equal(out[:c.T, :8 * d].view(np.uint16), want.view(np.uint16))
+
+
+@pytest.mark.parametrize("d", [64, 128])
+@pytest.mark.parametrize("hq", [64, 67, 71])
+def test_queries_in_runs_of_heads(d, hq):
+    """Batches so large that a group of lanes takes 8 heads of a token (128 channels) or 4 (64), the last run short, with
+    rows of skipped sequences between; with norms and without, and in place."""
+    seqs = [(1000, 1003), (0, 9), (3, 7), (1, 40), (1150, 1150)]
+    Call(Case(seqs, hq=hq, hkv=1, d=d, seed=84), rot=d, weights="heads", centered=True).check()
+    check_append(Case(seqs, hq=hq, hkv=1, d=d, seed=85), rot=d)
+    check_append(Case(seqs, hq=hq, hkv=1, d=d, seed=86), rot=d // 2, interleaved=hq == 67)
+    c = Case(seqs, hq=hq, hkv=1, d=d, seed=87)
+    x = Call(c, rot=d)
+    x.run()
+    want = x.q_out[:, :hq * d].clone()
+    q = x.buf[:, :hq * d].contiguous()
+    pad = torch.full((7, hq * d), 3.0, dtype=torch.float16, device="cuda")
+    q = torch.cat([pad, q, pad])
+    k = torch.zeros((len(q), d), dtype=torch.float16, device="cuda")
+    b = rdp.KVBatch(len(q), len(seqs), 1150, c.max_blocks, dev(c.indptr + 7), c.d_len, c.d_table)
+    rdp.slora_kv_append_norm(c.s.kv, b, k, d, k, d, q, hq * d, q, hq * d, hq, x.norm, x.rope)
+    torch.cuda.synchronize()
+    assert torch.equal(q[7:-7].view(torch.int16), want.view(torch.int16))
+    assert (q[:7] == 3).all() and (q[-7:] == 3).all() and c.s.device_status() == 0
 
 
 def test_norm_in_a_graph_on_another_stream_then_attention():
