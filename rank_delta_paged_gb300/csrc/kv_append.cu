@@ -15,7 +15,7 @@
 // A lane holds 16 channels of a row, chunk ch of 8 of either half: where the whole row turns in halves,
 // partners and their angle are in one lane, and what a row costs besides its channels (page ids,
 // exponents, addresses) is shared by twice as many of them.  With 8 channels a lane and shuffles between partners
-// 512 single tokens of 40 heads took 15.3 us instead of 10.5, 5046 tokens 65 instead of 54.
+// 512 single tokens of 40 heads took 15.3 us instead of 10.5, 5046 tokens 65 instead of 54 (their queries two heads at a time).
 //
 // Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
 // values and queries alike; a row is a group of head_dim / 16 lanes, and all of its reads that do not
@@ -27,18 +27,19 @@
 // the rows' angles, which are the same for all heads of the block.  Their queries are a kernel of their own (rotate_kernel).
 //
 // Measured: 512 single tokens of 40 heads 10.5 us, with norms 14; 5046 tokens, of which 384 are single, of 32
-// heads 54 us (3.9 TB/s), with the mean taken out and a weight for each head 75; 16381 tokens of 8 heads of 64 49 us
-// (3.9 TB/s).  The instructions between the reads and the writes, the barrier of a page's maximum and the waits for
+// heads 47.5 us (4.4 TB/s), with the mean taken out and a weight for each head 71; 16381 tokens of 8 heads of 64 42 us
+// (4.5 TB/s).  The instructions between the reads and the writes, the barrier of a page's maximum and the waits for
 // exponents take the time.
 // With two CTAs' worth of pages per block and CTAs found by a search of the token offsets, the
 // 5046 tokens took 93 us: half the SMs had twice the work of the others.
 // These times are of tokens that no block's exponent grows for.  Where it does, the group of lanes that has the
 // page's token rescales the rows before it, eight at a time: the 512 single tokens, from a cold cache
 // and with the call, take 26 us without, 45 with 215 of their 40960 pages growing and 55 with 9632 (INT8 25, 51 with
-// 246, 87 with 11157); row by row before the new codes were written it was 71 and 100.  The 5046 tokens 67, then 87 with
-// 10720 pages growing.
-// Pages above 8192 bytes have two rows per lane and one CTA per SM: 4096 tokens in prompts, cold, 56 us at 8192 bytes and
-// 32 heads (3.0 TB/s), 73 at 10240 and 40 (2.9 TB/s), 97 at 16384 and 64 (3.5 TB/s).
+// 246, 87 with 11157); row by row before the new codes were written it was 71 and 100.  The 5046 tokens some 60, then 80 with
+// 10720 pages growing.  Four rows per group of lanes, all their reads first: 9.3 us for the 512 tokens, 14.1 with norms, and 5.4 us
+// instead of 2.9 for one token.
+// Pages above 8192 bytes have two rows per lane and one CTA per SM: 4096 tokens in prompts, cold, 52 us at 8192 bytes and
+// 32 heads (3.3 TB/s), 70 at 10240 and 40 (3.1 TB/s), 91 at 16384 and 64 (3.7 TB/s).
 #include <mutex>
 
 #include "host_common.h"

@@ -31,7 +31,7 @@
 // With SINKS the keys between a sequence's first tokens and its window are left out of the numbering of its tiles
 // (kv.h, key_shift), box by box of 16 (8) rows, so the sinks share the window's first tile.  256 single tokens over windows of
 // 4096 and 64 sinks: 341 us, 6.1 TB/s, 90 % of a plain copy's rate (322 without the sinks); one over 1020 and 4: 12.9; 48
-// sequences of 3 to 8 drafted tokens, 64 channels, over 1000 and 4: 45 us (the same without the sinks).
+// sequences of 3 to 8 drafted tokens, 64 channels, over 1000 and 4: 42 us (43 without the sinks, by two CTAs per SM).
 //
 // Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 476 us, 5.7 TB/s; 4 over 60000 to 131000
 // keys: 116 us, 5.5 TB/s; one over 700: 11.7 us, of which the launch and the chain of dependent reads (lengths,
@@ -94,10 +94,14 @@ struct Meta {
 };
 static_assert(sizeof(Meta) % 16 == 0 && offsetof(Meta, plain) % 16 == 0, "Meta");
 
-template <int D, int NT>
+// CTAs per SM and stages of the ring.  Two groups of 8 rows of 64 channels by three CTAs and 5 stages instead of two and 7:
+// 48 sequences of 3 to 8 drafted tokens over windows of 1000 with sinks 42.6 us instead of 45.6 (the parts of the plain kernel's
+// results stay as they are).
+template <int D, int NT, bool SINKS>
 struct Shape {
-    static constexpr int kCtas = NT == 1 ? 3 : 2;            // per SM
-    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 6 : 7);
+    static constexpr bool kThree = NT == 1 || (SINKS && D == 64);
+    static constexpr int kCtas = kThree ? 3 : 2;
+    static constexpr int kStages = D == 128 ? (NT == 1 ? 3 : 4) : (NT == 1 ? 6 : kThree ? 5 : 7);
     static constexpr int kHalf = kTile * D;                  // bytes of a tile's keys
     static constexpr int kStage = 2 * kHalf;
     static constexpr int kMergeFloats = kConsumers * 8 * NT * (D + 2);
@@ -185,10 +189,10 @@ __device__ __forceinline__ void seq_tiles(const DecodeParams &p, Seq &q, int32_t
 }
 
 template <int D, int NT, int FMT, bool SINKS>
-__global__ void __launch_bounds__(kThreads, Shape<D, NT>::kCtas)
+__global__ void __launch_bounds__(kThreads, Shape<D, NT, SINKS>::kCtas)
 attend_decode_kernel(const __grid_constant__ DecodeParams p, const __grid_constant__ PageMaps maps)
 {
-    using Sh = Shape<D, NT>;
+    using Sh = Shape<D, NT, SINKS>;
     constexpr int NS = Sh::kStages;
     extern __shared__ uint8_t smem_raw[];
     uint8_t *ring = smem_raw + (1024 - (smem_u32(smem_raw) & 1023)) % 1024;
@@ -991,7 +995,7 @@ cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cud
         std::lock_guard<std::mutex> lk(mu);
         if (dev >= 64 || !set[dev]) {
             e = cudaFuncSetAttribute(attend_decode_kernel<D, NT, FMT, SINKS>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                     (int)Shape<D, NT>::kSmem);
+                                     (int)Shape<D, NT, SINKS>::kSmem);
             if (e != cudaSuccess) return e;
             if (dev < 64) set[dev] = true;
         }
@@ -1000,9 +1004,9 @@ cudaError_t launch(const DecodeParams &p, const PageMaps &maps, int num_sms, cud
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(num_sms * Shape<D, NT>::kCtas);
+    cfg.gridDim = dim3(num_sms * Shape<D, NT, SINKS>::kCtas);
     cfg.blockDim = dim3(kThreads);
-    cfg.dynamicSmemBytes = Shape<D, NT>::kSmem;
+    cfg.dynamicSmemBytes = Shape<D, NT, SINKS>::kSmem;
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
