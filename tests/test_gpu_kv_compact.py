@@ -331,6 +331,24 @@ def test_compact_in_a_graph_and_on_another_stream():
         e.c.s.exponents += 1
 
 
+@pytest.mark.parametrize("n", [90, 700, 3000])
+def test_compact_in_place_in_a_graph(n):
+    """By clusters of 1 to 8 CTAs; every pass moves what the last one left, so the passes are counted alike."""
+    m, e = (Moves([n, n // 2], [5, 0], [n // 2, n // 3], seed=220, d=64, hidden=512) for _ in range(2))
+    k = m.lists()
+    st = torch.cuda.Stream()
+    g = torch.cuda.CUDAGraph()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(g, stream=st):
+        rdp.slora_kv_compact(m.c.s.kv, k, st)
+    for _ in range(3):
+        g.replay()
+        e.check()
+        torch.cuda.synchronize()
+        assert torch.equal(m.c.s.pages, e.c.s.pages) and torch.equal(m.c.s.exponents, e.c.s.exponents)
+    assert m.c.s.device_status() == 0
+
+
 def test_accepted_drafts_move_up_and_are_attended():
     """A tree of drafts is appended, its accepted branch moves up behind the sequence, the next token attends: as if
     only the branch had been appended, where its block's scale is the same."""
