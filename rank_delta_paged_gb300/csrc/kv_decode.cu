@@ -160,7 +160,7 @@ struct DecodeParams {
     int32_t box_rows;      // 16 if blocks are multiples of 16 tokens, else 8
     int32_t small_rows;
     int32_t rows;          // rows per unit: 8 * NT
-    int32_t min_tiles;     // a CTA's run is at least this long
+    int32_t min_tiles;     // a CTA's run is at least this long: more than kUnitCost, or a run would have no tile and its warps wait
     uint32_t bt_inverse;   // ceil(2^32 / block tokens): a token's block, or one more
     float *part;           // [CTAs][2] partial results
     Joins joins;           // a word per CTA: the unit that starts there and goes on in others

@@ -97,7 +97,7 @@ struct PrefillParams {
     AttendArgs a;
     int32_t small_rows;    // sequences with at most this many rows are another kernel's
     int32_t box_rows;      // 16 if blocks are multiples of 16 tokens, else 8
-    int32_t min_tiles;
+    int32_t min_tiles;     // of a CTA's run: more than kUnitCost, or a run would have no tile and its warps wait
     uint32_t bt_inverse;
     float scale;           // softmax scale * log2(e), not zero
     uint32_t unseen;       // what a product must be for a score of -infinity
