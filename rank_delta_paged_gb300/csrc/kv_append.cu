@@ -334,13 +334,14 @@ __device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d, 
 {
     if (FMT == SLORA_KV_INT8) {
         // The last bit of 1.5 2^23 + 128 is 1, so the sum's low byte is the code + 128, rounded to nearest even; the
-        // bytes above are the same for -127 .. 127, which leaves infinities and NaN to the conversions, whose
-        // pipe takes a quarter of the numbers per cycle.
+        // bytes above are the same for -128 .. 127, which leaves infinities and NaN to the conversions, whose
+        // pipe takes a quarter of the numbers per cycle.  Their -128 is no code, and no value is below -127 units but where
+        // the exponent is held at its limit (new_exponent): there all codes are the conversions'.
         const float magic = 12583040.f;
         const uint32_t u = __float_as_uint(__fmaf_rn(a, unit, magic)), v = __float_as_uint(__fmaf_rn(b, unit, magic));
         const uint32_t w = __float_as_uint(__fmaf_rn(c, unit, magic)), x = __float_as_uint(__fmaf_rn(d, unit, magic));
         const uint32_t k = 0x4B400000u;
-        if (__builtin_expect(((u ^ k) | (v ^ k) | (w ^ k) | (x ^ k)) < 256u, 1))
+        if (__builtin_expect(((u ^ k) | (v ^ k) | (w ^ k) | (x ^ k)) < 256u && unit > pow2(-kExpLimit), 1))
             return __byte_perm(__byte_perm(u, v, 0x0040), __byte_perm(w, x, 0x0040), 0x5410) ^ 0x80808080u;
         return encode4_odd(a * unit, b * unit, c * unit, d * unit);
     }
