@@ -606,7 +606,7 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *                source table).  In that block the tokens before first[s] are written too.
  *   new_len      device int32 [S] that gets first[s] + the kept tokens, or NULL; none of the other arrays
  * Scales: the exponent of every block that gets a token is the smallest e >= -40 for which every finite value of its
- * rows fits (as in append, with no regard for what it was): a row's codes are multiplied by a power
+ * rows fits, 60 at most (as in append, with no regard for what it was): a row's codes are multiplied by a power
  * of two, exact where they grow, rounded to nearest even where they shrink; NaN stays.  Rows of a written
  * block behind the last kept token are unspecified.  In place a page belongs to one sequence of the call;
  * with dst_table the sequences may share pages that are only read.

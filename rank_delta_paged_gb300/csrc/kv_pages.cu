@@ -258,7 +258,8 @@ __global__ void __launch_bounds__(2 * PT, kFill / (2 * PT)) compact_kernel(const
                 top = top > y ? top : y;
             }
             if (top != kBad) {
-                const int e = fit_exponent<FMT>(__uint_as_float(top));
+                // (no higher than is read: a -128 of the caller's stays as it is there)
+                const int e = min(fit_exponent<FMT>(__uint_as_float(top)), kExpLimit);
                 uint4 *page = reinterpret_cast<uint4 *>(a.c.pool + dst * a.c.page_bytes);
 #pragma unroll 2
                 for (int32_t x = pt; x < pieces; x += PT) {

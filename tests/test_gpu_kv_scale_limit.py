@@ -7,6 +7,7 @@ import torch
 import kv_reference as R
 import rank_delta_paged_gb300 as rdp
 from test_gpu_kv import Case, half
+from test_gpu_kv_compact import Moves
 
 pytestmark = pytest.mark.gpu
 TOP = 60
@@ -48,3 +49,33 @@ def test_normed_keys_next_to_the_largest_code(fmt, d, hidden, seqs):
                 page = c.table[s, p // c.bt, h, 0]
                 assert exps[page] == TOP
                 assert np.array_equal(got[page, p % c.bt], want[c.indptr[s] + i, h])
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_compaction_at_the_largest_scale(in_place):
+    """A code of -128, which only a caller can have written, at the largest exponent that is read: there is no scale above to
+    move it to, so it reads as it did, and so do the rows beside it."""
+    m = Moves([200, 70], [0, 3], [150, 60], fmt="int8", seed=91, in_place=in_place, edit=lowest_codes)
+    before, exps = m.c.values()
+    was = [[kept_values(m, before, exps, m.table, s, h, w, m.kept[0, m.indptr[s]:m.indptr[s + 1]]) for h in range(2) for w in range(2)]
+           for s in range(2)]
+    m.run()
+    after, exps = m.c.values()
+    assert m.c.s.device_status() == 0 and exps.max() <= TOP
+    to = m.table if m.dst is None else m.dst
+    now = [[kept_values(m, after, exps, to, s, h, w, m.first[s] + np.arange(m.n[s])) for h in range(2) for w in range(2)]
+           for s in range(2)]
+    for a, b in zip(was, now):
+        for x, y in zip(a, b):
+            assert np.array_equal(x, y)
+
+
+def lowest_codes(c):
+    """Every page at 2^60 with a -128 in its fifth row."""
+    c.exps[:] = TOP
+    c.pages[:, 4 * c.d + 7] = 0x80
+
+
+def kept_values(m, val, exps, table, s, h, w, at):
+    page = table[s, at // m.bt, h, w]
+    return val[page, at % m.bt] * 2.0 ** np.clip(exps[page].astype(float), -60, 60)[:, None]
