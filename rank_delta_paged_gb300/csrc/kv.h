@@ -57,6 +57,7 @@ struct AppendArgs {
     int64_t k_stride, v_stride, q_stride, q_out_stride;
     int32_t n_q;
     int32_t rot, interleaved, n_pos;    // rot 0: no rotation
+    int32_t pairs;                      // chunks of 8 channels that turn with the one `pairs` behind; all of a half if none do
     const float *cos, *sin;
     const int32_t *positions;           // nullptr: positions in the cache
     // The norm of keys and queries per head (kernels with NORM); weights nullptr: ones.

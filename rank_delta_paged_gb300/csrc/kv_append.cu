@@ -12,9 +12,9 @@
 // angles and exponents).  The scale of a block needs the largest value of all its new tokens
 // before the first code can be written, so a block's tokens stay in registers between the two.
 //
-// A lane holds 16 channels of a row, chunk ch of 8 of either half: where the whole row turns in halves,
-// partners and their angle are in one lane, and what a row costs besides its channels (page ids,
-// exponents, addresses) is shared by twice as many of them.  With 8 channels a lane and shuffles between partners
+// A lane holds 16 channels of a row, two chunks of 8.  Where rows turn in halves, whole or in part, they are
+// partners (Own), with one set of angles; and what a row costs besides its channels (page ids,
+// exponents, addresses) is shared by twice as many of them as with 8 a lane.  With 8 channels a lane and shuffles between partners
 // 512 single tokens of 40 heads took 15.3 us instead of 10.5, 5046 tokens 65 instead of 54 (their queries two heads at a time).
 //
 // Sequences with one new token (append_one_kernel): a CTA takes a share of the token's rows, keys,
@@ -87,35 +87,46 @@ __device__ __forceinline__ int fresh_tid()
     return t;
 }
 
-// A lane has 16 channels of a row: chunk ch of 8 in either half.  With the whole row rotated in halves a channel's partner
-// is then its own, and both turn by the same angle.
+// The two chunks of 8 channels that lane ch of a row holds.  With the first 2 m chunks turning in halves, lanes below m hold
+// a chunk and its partner, which turn by the same angles, and the others two chunks that do not turn; else chunk ch of
+// either half of the row (m is half the row's chunks: AppendArgs::pairs).  With chunk ch of either half for every rotation, partners
+// by shuffles and, where more than half the row turned, angles by channel, 96 of 128 channels took 95 us
+// instead of 50 on the 5046 tokens.
+struct Own {
+    int lo, hi;
+};
+template <int D>
+__device__ __forceinline__ Own own_chunks(const AppendArgs &a, int ch)
+{
+    const bool pair = ch < a.pairs;
+    return {pair ? ch : ch + a.pairs, ch + (pair ? a.pairs : D / 16)};
+}
+
+// The angles of this lane's channels.
 struct Rot {
     float c[8], s[8];
-    int32_t pos;
-    bool on;
+    bool on;            // whether its pair of chunks turns; adjacent pairs: whether the token does
 };
 
-// The angles of this lane's channels: of chunk ch and its partner where rows turn in halves, or (the first four, then the
-// last four) of its adjacent pairs.  Where more than half a row turns, but not all, rotate() looks them up.
+// The angles of chunks ch and its partner where rows turn in halves, or (the first four, then the last four) of the lane's
+// adjacent pairs.
 template <int D>
 __device__ __forceinline__ void load_rot(const AppendArgs &a, int32_t pos, int ch, Rot &r)
 {
     r.on = a.rot != 0;
-    r.pos = pos;
     if (r.on && (pos < 0 || pos >= a.n_pos)) {
         set_status(a.c.status, SLORA_DEV_BAD_POSITION);
         r.on = false;
     }
+    const bool halves = !a.interleaved;
+    if (halves && ch >= a.pairs) r.on = false;
     if (!r.on) return;
     const int64_t row = (int64_t)pos * (a.rot / 2);
     const float4 *cos = reinterpret_cast<const float4 *>(a.cos + row), *sin = reinterpret_cast<const float4 *>(a.sin + row);
-    const bool halves = !a.interleaved;
-    const int m = a.rot / 16;            // chunks of half the rotated channels
-    if (halves && 2 * m > D / 16 && a.rot != D) return;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
-        const int k = halves ? 2 * (ch < m ? ch : ch - m) + i : ch + i * (D / 16);
-        const bool turns = halves ? ch < 2 * m : ch * 8 + i * (D / 2) < a.rot;
+        const int k = halves ? 2 * ch + i : ch + i * (D / 16);
+        const bool turns = halves || ch * 8 + i * (D / 2) < a.rot;
         const float4 one = make_float4(1.f, 1.f, 1.f, 1.f), none = make_float4(0.f, 0.f, 0.f, 0.f);
         const float4 c = turns ? __ldg(cos + k) : one, s = turns ? __ldg(sin + k) : none;
         r.c[4 * i] = c.x, r.c[4 * i + 1] = c.y, r.c[4 * i + 2] = c.z, r.c[4 * i + 3] = c.w;
@@ -123,63 +134,26 @@ __device__ __forceinline__ void load_rot(const AppendArgs &a, int32_t pos, int c
     }
 }
 
-// Rotates this lane's channels; every lane of the warp calls it.  Products and sums are rounded one by one, so the codes
-// do not depend on contraction.
+// Rotates this lane's channels.  Products and sums are rounded one by one, so the codes do not depend on contraction.
 template <int D>
 __device__ __forceinline__ void rotate(const AppendArgs &a, const Rot &r, int ch, float (&x)[16])
 {
-    if (a.rot == 0) return;
+    if (!r.on) return;
     if (a.interleaved) {
-        if (r.on)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[2 * i], w = x[2 * i + 1];
-                if (ch * 8 + (i >> 2) * (D / 2) < a.rot) {
-                    x[2 * i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
-                    x[2 * i + 1] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
-                }
-            }
-    } else if (a.rot == D) {
-        if (r.on)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float u = x[i], w = x[8 + i];
-                x[i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
-                x[8 + i] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
-            }
-    } else {
-        // a part of the row in halves: the partners are other lanes', all of the first half's chunks if at most that turns
-        constexpr int LPR = D / 16;
-        const int m = a.rot / 16;
-        auto partner = [&](int k) { return k < m ? k + m : k < 2 * m ? k - m : k; };
-        if (2 * m <= LPR) {
-            const bool turns = r.on && ch < 2 * m;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const float y = __shfl_sync(~0u, x[i], partner(ch), LPR);
-                if (turns) x[i] = __fadd_rn(__fmul_rn(x[i], r.c[i]), __fmul_rn(y, ch < m ? -r.s[i] : r.s[i]));
-            }
-            return;
-        }
-        const int64_t row = (int64_t)r.pos * (a.rot / 2);
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
-            float y[2];
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int from = partner(ch + h * LPR);
-                const float u = __shfl_sync(~0u, x[i], from % LPR, LPR), w = __shfl_sync(~0u, x[8 + i], from % LPR, LPR);
-                y[h] = from < LPR ? u : w;
+            const float u = x[2 * i], w = x[2 * i + 1];
+            if (ch * 8 + (i >> 2) * (D / 2) < a.rot) {
+                x[2 * i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
+                x[2 * i + 1] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
             }
+        }
+    } else {
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int k = ch + h * LPR;
-                if (r.on && k < 2 * m) {
-                    const int64_t at = row + 8 * (k < m ? k : k - m) + i;
-                    const float sn = __ldg(a.sin + at);
-                    x[8 * h + i] = __fadd_rn(__fmul_rn(x[8 * h + i], __ldg(a.cos + at)), __fmul_rn(y[h], k < m ? -sn : sn));
-                }
-            }
+        for (int i = 0; i < 8; ++i) {
+            const float u = x[i], w = x[8 + i];
+            x[i] = __fsub_rn(__fmul_rn(u, r.c[i]), __fmul_rn(w, r.s[i]));
+            x[8 + i] = __fadd_rn(__fmul_rn(w, r.c[i]), __fmul_rn(u, r.s[i]));
         }
     }
 }
@@ -211,14 +185,23 @@ __device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b)
 }
 
 // The sum over a row's channels in an order that depends on D alone: the even and the odd channels of each 8, one after
-// another, then the eights by twos.  No product is contracted into it.
+// another, then the eights of either half by twos.  No product is contracted into it.
 template <int D>
-__device__ __forceinline__ float row_sum(const uint64_t (&x)[8])
+__device__ __forceinline__ float row_sum(const AppendArgs &p, int ch, const uint64_t (&x)[8])
 {
+    constexpr int LPR = D / 16;
     const float2 t = unpair(add2(add2(add2(x[0], x[1]), x[2]), x[3])), u = unpair(add2(add2(add2(x[4], x[5]), x[6]), x[7]));
     float a = __fadd_rn(t.x, t.y), b = __fadd_rn(u.x, u.y);
+    if (p.pairs != LPR) {
+        // chunks ch and ch + LPR, from the lanes that hold them (Own)
+        const int m = p.pairs, from_a = ch < m ? ch : ch - m, from_b = ch < m ? ch + LPR - m : ch;
+        const float a0 = __shfl_sync(~0u, a, from_a, LPR), a1 = __shfl_sync(~0u, b, from_a, LPR);
+        const float b0 = __shfl_sync(~0u, a, from_b, LPR), b1 = __shfl_sync(~0u, b, from_b, LPR);
+        a = ch >= m && ch < 2 * m ? a1 : a0;
+        b = ch < m && ch + LPR >= 2 * m ? b0 : b1;
+    }
 #pragma unroll
-    for (int k = 1; k < D / 16; k *= 2) {
+    for (int k = 1; k < LPR; k *= 2) {
         a = __fadd_rn(a, __shfl_xor_sync(~0u, a, k));
         b = __fadd_rn(b, __shfl_xor_sync(~0u, b, k));
     }
@@ -235,7 +218,7 @@ __device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const fl
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = pair(x[2 * i], x[2 * i + 1]);
     if (a.centered) {
-        const float m = -(row_sum<D>(y) * (1.f / D));
+        const float m = -(row_sum<D>(a, ch, y) * (1.f / D));
         const uint64_t mm = pair(m, m);
 #pragma unroll
         for (int i = 0; i < 8; ++i) y[i] = add2(y[i], mm);
@@ -246,14 +229,15 @@ __device__ __forceinline__ void normalise(const AppendArgs &a, bool on, const fl
         const float2 t = unpair(y[i]);
         z[i] = pair(__fmul_rn(t.x, t.x), __fmul_rn(t.y, t.y));
     }
-    const float r = rsqrtf(__fadd_rn(row_sum<D>(z) * (1.f / D), a.eps));
+    const float r = rsqrtf(__fadd_rn(row_sum<D>(a, ch, z) * (1.f / D), a.eps));
     const uint64_t rr = pair(r, r);
 #pragma unroll
     for (int i = 0; i < 8; ++i) y[i] = mul2(y[i], rr);
     if (w != nullptr) {
+        const Own own = own_chunks<D>(a, ch);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 v = __ldg(reinterpret_cast<const float4 *>(w + (i >> 1) * (D / 2)) + 2 * ch + (i & 1));
+            const float4 v = __ldg(reinterpret_cast<const float4 *>(w) + 2 * (i >> 1 ? own.hi : own.lo) + (i & 1));
             y[2 * i] = mul2(y[2 * i], pair(v.x, v.y));
             y[2 * i + 1] = mul2(y[2 * i + 1], pair(v.z, v.w));
         }
@@ -272,9 +256,9 @@ struct Raw {
     uint4 a, b;
 };
 template <int D>
-__device__ __forceinline__ Raw read_row(const __half *row, int ch)
+__device__ __forceinline__ Raw read_row(const __half *row, Own own)
 {
-    return {*reinterpret_cast<const uint4 *>(row + ch * 8), *reinterpret_cast<const uint4 *>(row + D / 2 + ch * 8)};
+    return {*reinterpret_cast<const uint4 *>(row + own.lo * 8), *reinterpret_cast<const uint4 *>(row + own.hi * 8)};
 }
 
 __device__ __forceinline__ void unpack(const Raw &v, float (&x)[16])
@@ -290,7 +274,7 @@ __device__ __forceinline__ void unpack(const Raw &v, float (&x)[16])
 
 // The rotated query of this lane in fp16.
 template <int D>
-__device__ __forceinline__ void write_query(__half *row, int ch, const float (&x)[16])
+__device__ __forceinline__ void write_query(__half *row, Own own, const float (&x)[16])
 {
     uint32_t w[8];
 #pragma unroll
@@ -298,8 +282,8 @@ __device__ __forceinline__ void write_query(__half *row, int ch, const float (&x
         const __half2 h = __floats2half2_rn(x[2 * i], x[2 * i + 1]);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    *reinterpret_cast<uint4 *>(row + ch * 8) = make_uint4(w[0], w[1], w[2], w[3]);
-    *reinterpret_cast<uint4 *>(row + D / 2 + ch * 8) = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4 *>(row + own.lo * 8) = make_uint4(w[0], w[1], w[2], w[3]);
+    *reinterpret_cast<uint4 *>(row + own.hi * 8) = make_uint4(w[4], w[5], w[6], w[7]);
 }
 
 // The largest finite magnitude.
@@ -357,11 +341,11 @@ __device__ __forceinline__ int new_exponent(float m)
 
 // This lane's codes to a row.
 template <int D, int FMT>
-__device__ __forceinline__ void write_codes(uint8_t *row, int ch, const float (&x)[16], float unit)
+__device__ __forceinline__ void write_codes(uint8_t *row, Own own, const float (&x)[16], float unit)
 {
 #pragma unroll
     for (int h = 0; h < 2; ++h)
-        *reinterpret_cast<uint2 *>(row + h * (D / 2) + ch * 8) =
+        *reinterpret_cast<uint2 *>(row + (h ? own.hi : own.lo) * 8) =
             make_uint2(encode4<FMT>(x[8 * h], x[8 * h + 1], x[8 * h + 2], x[8 * h + 3], unit),
                        encode4<FMT>(x[8 * h + 4], x[8 * h + 5], x[8 * h + 6], x[8 * h + 7], unit));
 }
@@ -409,6 +393,7 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
     const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
+    const Own own = own_chunks<D>(a, ch);
     griddep_wait();
     griddep_launch_dependents();
     const int32_t s = (int32_t)(blockIdx.x / (unsigned)p.splits), part = (int32_t)(blockIdx.x - (unsigned)s * p.splits);
@@ -432,7 +417,7 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     int32_t page = -1, old = kMinExponent;
     if (live) {
         const __half *src = query ? a.q + t0 * a.q_stride : val ? a.v + t0 * a.v_stride : a.k + t0 * a.k_stride;
-        raw = read_row<D>(src + (int64_t)h * D, ch);
+        raw = read_row<D>(src + (int64_t)h * D, own);
         if (!query) page = a.b.table[((int64_t)s * a.b.max_blocks + blk) * kv + 2 * h + val];
     }
     const bool turns = live && !val;
@@ -459,12 +444,12 @@ __global__ void __launch_bounds__(kThreads, NORM ? 4 : 5) append_one_kernel(cons
     }
     const float m = max_of(row_lanes, size_of(x));
     const int was = __shfl_sync(~0u, old, 0, LPR);
-    if (live && query) write_query<D>(a.q_out + t0 * a.q_out_stride + (int64_t)h * D, ch, x);
+    if (live && query) write_query<D>(a.q_out + t0 * a.q_out_stride + (int64_t)h * D, own, x);
     if (page < 0) return;
     const int fit = new_exponent<FMT, NORM>(m), e = held && was > fit ? was : fit;
     uint8_t *dst = a.c.pool + page * a.c.page_bytes;
     if (ch == 0) a.c.exps[page] = (int8_t)e;
-    write_codes<D, FMT>(dst + held * D, ch, x, pow2(-e));
+    write_codes<D, FMT>(dst + held * D, own, x, pow2(-e));
     if (held && was < e) rescale_rows<D, FMT, 8>(dst, ch, 0, 1, held, pow2(was - e));
 }
 
@@ -476,6 +461,7 @@ __global__ void __launch_bounds__(kThreads, kQCtas) rotate_kernel(const __grid_c
     const AppendArgs &a = p.a;
     const int tid = threadIdx.x, ch = tid % LPR, grp = tid / LPR;
     const unsigned row_lanes = ((1u << LPR) - 1u) << (tid & 31 & -LPR);
+    const Own own = own_chunks<D>(a, ch);
     // as append_kernel
     griddep_launch_dependents();
     const int32_t per = (a.n_q + p.q_run - 1) / p.q_run;
@@ -494,7 +480,7 @@ __global__ void __launch_bounds__(kThreads, kQCtas) rotate_kernel(const __grid_c
 #pragma unroll
             for (int k = 0; k < kQHeads; ++k) {
                 v[k] = {make_uint4(0, 0, 0, 0), make_uint4(0, 0, 0, 0)};
-                if (h + k < hend) v[k] = read_row<D>(src + (int64_t)(h + k) * D, ch);
+                if (h + k < hend) v[k] = read_row<D>(src + (int64_t)(h + k) * D, own);
             }
         };
         read(h0);
@@ -531,7 +517,7 @@ __global__ void __launch_bounds__(kThreads, kQCtas) rotate_kernel(const __grid_c
                 unpack(w[k], x);
                 if (NORM) normalise<D, false>(a, true, some && a.q_weight ? a.q_weight + head * a.q_weight_stride : nullptr, ch, x);
                 rotate<D>(a, r, ch, x);
-                if (some) write_query<D>(dst + (int64_t)head * D, ch, x);
+                if (some) write_query<D>(dst + (int64_t)head * D, own, x);
             }
         }
     }
@@ -546,6 +532,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
 {
     constexpr int LPR = D / 16, GROUPS = kBlockThreads / LPR;
     const int tid = fresh_tid(), ch = tid % LPR, grp = tid / LPR;
+    const Own own = own_chunks<D>(a, ch);
     // Shared memory of which every thread has pieces of its own: the rows of this page and the next ones, and the angles.
     extern __shared__ uint4 s_own[];
     uint4 *ring = s_own + tid;
@@ -553,15 +540,15 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
     auto piece = [&](int slot, int i, int h) { return ring + ((slot * PASSES + i) * 2 + h) * kBlockThreads; };
     auto read = [&](int32_t u, int slot) {
         if (u < u1) {
-            const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D + ch * 8;
+            const __half *src = (u & 1 ? a.v : a.k) + (int64_t)(u >> 1) * D;
             const int64_t stride = u & 1 ? a.v_stride : a.k_stride;
 #pragma unroll
             for (int i = 0; i < PASSES; ++i) {
                 const int r = i * GROUPS + grp;
                 if (r >= nt) break;
                 const __half *row = src + (int64_t)(row0 + r) * stride;
-                cp_async16(piece(slot, i, 0), row, 16);
-                cp_async16(piece(slot, i, 1), row + D / 2, 16);
+                cp_async16(piece(slot, i, 0), row + own.lo * 8, 16);
+                cp_async16(piece(slot, i, 1), row + own.hi * 8, 16);
             }
         }
         cp_async_commit();
@@ -569,16 +556,16 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
 #pragma unroll
     for (int k = 0; k < kStages - 1; ++k) read(u0 + k, k);
     // a row's angles are those of all heads: a thread keeps its own in shared memory
-    int32_t at[PASSES];                     // position, -1: not rotated
+    bool turns[PASSES];
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
         const int r = i * GROUPS + grp;
-        at[i] = -1;
+        turns[i] = false;
         if (a.rot == 0 || r >= nt) continue;
         Rot rt;
         load_rot<D>(a, position(a, row0 + r, from + r), ch, rt);
         if (!rt.on) continue;
-        at[i] = rt.pos;
+        turns[i] = true;
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
             const float *v = j < 2 ? rt.c + 4 * j : rt.s + 4 * (j - 2);
@@ -609,8 +596,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
             if (!val) {
                 if (NORM) normalise<D, false>(a, true, a.k_weight ? a.k_weight + (u >> 1) * a.k_weight_stride : nullptr, ch, x[i]);
                 Rot rt;
-                rt.pos = at[i];
-                rt.on = at[i] >= 0;
+                rt.on = turns[i];
                 if (rt.on)
 #pragma unroll
                     for (int j = 0; j < 4; ++j) {
@@ -637,7 +623,7 @@ __device__ __forceinline__ void full_rows(const AppendArgs &a, int32_t u0, int32
 #pragma unroll
         for (int i = 0; i < PASSES; ++i) {
             const int r = i * GROUPS + grp;
-            if (r < nt) write_codes<D, FMT>(dst + (held + r) * D, ch, x[i], unit);
+            if (r < nt) write_codes<D, FMT>(dst + (held + r) * D, own, x[i], unit);
         }
         if (held && old < e) rescale_rows<D, FMT, 1>(dst, ch, grp, GROUPS, held, pow2(old - e));
     }
@@ -839,6 +825,7 @@ cudaError_t launch_d(Params &p, int fmt, int num_sms, cudaStream_t stream, int *
     constexpr int groups = kThreads / (D / 16);
     const AppendArgs &a = p.a;
     const bool e4m3 = fmt == SLORA_KV_E4M3;
+    p.a.pairs = a.rot == 0 || a.interleaved ? D / 16 : a.rot / 16;
     cudaError_t e;
     {
         // a row per group of lanes
