@@ -64,11 +64,17 @@ class Streams:
         on, or drafts until accept()."""
         streams, xs = zip(*work)
         n = [len(x) for x in xs]
-        for s, m in zip(streams, n):
-            for b in range(s.length // self.block, (s.length + m - 1) // self.block + 1):
-                if b not in s.blocks:
-                    s.blocks[b] = np.empty((self.n_layers, self.n_heads, 2), np.int32)
-                    rdp.slora_pages_alloc(self.pool, s.blocks[b].size, s.blocks[b])
+        taken = []
+        try:
+            for s, m in zip(streams, n):
+                for b in range(s.length // self.block, (s.length + m - 1) // self.block + 1):
+                    if b not in s.blocks:
+                        s.blocks[b] = self._take()
+                        taken.append((s, b))
+        except rdp.SloraError:                          # a full pool: the streams stay as they were
+            for s, b in taken:
+                self._give_back(s.blocks.pop(b))
+            raise
         table = torch.from_numpy(self.table(streams)).cuda()
         indptr = np.concatenate([[0], np.cumsum(n)]).astype(np.int32)
         lengths = np.array([s.length + m for s, m in zip(streams, n)], np.int32)
@@ -110,17 +116,26 @@ class Streams:
         """A stream that goes on from here by itself."""
         child = Stream(s.length)
         whole, rest = divmod(s.length, self.block)
-        for b, pages in s.blocks.items():
-            if b == whole and rest:
-                child.blocks[b] = np.empty_like(pages)
-                rdp.slora_pages_alloc(self.pool, pages.size, child.blocks[b])
-                src, dst = (torch.from_numpy(p.ravel().copy()).cuda() for p in (pages, child.blocks[b]))
-                rows = torch.full((pages.size,), rest, dtype=torch.int32, device="cuda")
-                rdp.slora_kv_copy(self.kv, pages.size, src, dst, rows)
-            elif b < whole:
-                rdp.slora_pages_share(self.pool, pages.size, pages)
-                child.blocks[b] = pages
+        try:
+            for b, pages in s.blocks.items():
+                if b == whole and rest:
+                    child.blocks[b] = self._take()
+                    src, dst = (torch.from_numpy(p.ravel().copy()).cuda() for p in (pages, child.blocks[b]))
+                    rows = torch.full((pages.size,), rest, dtype=torch.int32, device="cuda")
+                    rdp.slora_kv_copy(self.kv, pages.size, src, dst, rows)
+                elif b < whole:
+                    rdp.slora_pages_share(self.pool, pages.size, pages)
+                    child.blocks[b] = pages
+        except rdp.SloraError:
+            self.drop(child)
+            raise
         return child
+
+    def _take(self):
+        """The pages of a block."""
+        pages = np.empty((self.n_layers, self.n_heads, 2), np.int32)
+        rdp.slora_pages_alloc(self.pool, pages.size, pages)
+        return pages
 
     def _give_back(self, pages):
         rdp.slora_pages_free(self.pool, pages.size, np.ascontiguousarray(pages))
