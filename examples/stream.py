@@ -44,6 +44,7 @@ class Streams:
         self.block = rdp.slora_kv_block_tokens(self.kv)
         rng = np.random.default_rng(seed)
         f32 = lambda a: torch.from_numpy(a.astype(np.float32)).cuda()  # noqa: E731
+        self.max_positions = max_positions
         self.w = f32(rng.normal(0, hidden ** -0.5, (n_layers, 4, hidden, hidden))).half()
         self.norms = [rdp.KVNorm(1e-6, False, f32(rng.normal(1, 0.1, head_dim)), 0, f32(rng.normal(1, 0.1, head_dim)), 0)
                       for _ in range(n_layers)]
@@ -64,6 +65,8 @@ class Streams:
         on, or drafts until accept()."""
         streams, xs = zip(*work)
         n = [len(x) for x in xs]
+        if any(s.length + m > self.max_positions for s, m in zip(streams, n)):
+            raise ValueError(f"a stream has {self.max_positions} positions")
         taken = []
         try:
             for s, m in zip(streams, n):

@@ -1,5 +1,5 @@
 """The streaming example's pages to the last one: drafts, forks and a full pool leave no page held by nobody and none held
-twice."""
+twice; positions end with the rotation's table."""
 import importlib.util
 import os
 
@@ -102,5 +102,23 @@ def test_a_full_pool_leaves_the_streams_as_they_were(example):
         e.step([(s, tokens(e, e.block + 1, 0))])         # all of it can be had again
         e.drop(s)
         assert rdp.slora_get_device_status(e.pool) == 0
+    finally:
+        e.close()
+
+
+def test_positions_end_with_the_rotation(example):
+    e = example.Streams(window=40, sinks=3, num_pages=512, max_positions=70)
+    try:
+        s = example.Stream()
+        e.step([(s, tokens(e, 60, 0))])
+        held = free(e)
+        with pytest.raises(ValueError):
+            e.step([(s, tokens(e, 11, 1))])
+        assert s.length == 60 and free(e) == held
+        e.step([(s, tokens(e, 10, 1))])
+        with pytest.raises(ValueError):
+            e.step([(s, tokens(e, 1, 1))])
+        assert s.length == 70 and rdp.slora_get_device_status(e.pool) == 0
+        e.drop(s)
     finally:
         e.close()
