@@ -31,6 +31,7 @@ NO_PAGE = -1
 class Stream:
     def __init__(self, length=0, blocks=None):
         self.length = length             # tokens in the cache
+        self.settled = length            # of which no fork has pages of its own: drafts lie behind them
         self.blocks = blocks or {}       # block -> int32 [layers][n_heads][2]
 
 
@@ -104,6 +105,8 @@ class Streams:
     def accept(self, s, drafts, kept):
         """Of the stream's last `drafts` tokens only those numbered kept[] (ascending) stay."""
         first, k = s.length - drafts, len(kept)
+        if first < s.settled:
+            raise ValueError("a fork holds pages of these drafts")
         L = self.n_layers
         ints = lambda a: torch.from_numpy(np.ascontiguousarray(a, np.int32)).cuda()  # noqa: E731
         if k:
@@ -118,6 +121,7 @@ class Streams:
     def fork(self, s):
         """A stream that goes on from here by itself."""
         child = Stream(s.length)
+        s.settled = s.length
         whole, rest = divmod(s.length, self.block)
         try:
             for b, pages in s.blocks.items():

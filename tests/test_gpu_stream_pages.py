@@ -1,5 +1,5 @@
 """The streaming example's pages to the last one: drafts, forks and a full pool leave no page held by nobody and none held
-twice; positions end with the rotation's table."""
+twice; positions end with the rotation's table; a fork settles drafts."""
 import importlib.util
 import os
 
@@ -120,5 +120,27 @@ def test_positions_end_with_the_rotation(example):
             e.step([(s, tokens(e, 1, 1))])
         assert s.length == 70 and rdp.slora_get_device_status(e.pool) == 0
         e.drop(s)
+    finally:
+        e.close()
+
+
+def test_a_fork_settles_what_was_drafted(example):
+    """Blocks that a fork shares are not rewritten."""
+    e = example.Streams(window=1000, num_pages=512)
+    try:
+        s = example.Stream()
+        e.step([(s, tokens(e, e.block - 4, 0))])
+        e.step([(s, tokens(e, 9, 1))])
+        f = e.fork(s)
+        for x in (s, f):
+            with pytest.raises(ValueError):
+                e.accept(x, 9, [0])
+            assert x.length == e.block + 5
+        e.step([(s, tokens(e, 3, 2))])
+        e.accept(s, 3, [0])
+        assert s.length == e.block + 6
+        for x in (s, f):
+            e.drop(x)
+        assert free(e) == 512
     finally:
         e.close()
