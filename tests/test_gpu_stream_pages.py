@@ -1,5 +1,5 @@
 """The streaming example's pages to the last one: drafts, forks and a full pool leave no page held by nobody and none held
-twice; positions end with the rotation's table; a fork settles drafts."""
+twice; positions end with the rotation's table; a fork settles drafts, and drafts are accepted as a prefix."""
 import importlib.util
 import os
 
@@ -144,3 +144,12 @@ def test_a_fork_settles_what_was_drafted(example):
         assert free(e) == 512
     finally:
         e.close()
+
+
+def test_the_run_accepts_prefixes(example, monkeypatch):
+    """A draft's keys have attended to every draft before it, so with causal drafts only a prefix may stay."""
+    some = []
+    accept = example.Streams.accept
+    monkeypatch.setattr(example.Streams, "accept", lambda e, s, drafts, kept: (some.append(list(kept)), accept(e, s, drafts, kept)))
+    assert example.main() == 0
+    assert some and all(k == list(range(len(k))) for k in some)
