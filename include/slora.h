@@ -610,9 +610,11 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * of two, exact where they grow, rounded to nearest even where they shrink; NaN stays.  Rows of a written
  * block behind the last kept token are unspecified.  In place a page belongs to one sequence of the call;
  * with dst_table the sequences may share pages that are only read.
- * A position that is out of order, below its destination or not below kv_len (SLORA_DEV_BAD_POSITION) or a bad page id
- * (SLORA_DEV_BAD_PAGE) leaves the block and head that it is for unwritten, a destination beyond its table
- * (SLORA_DEV_BAD_LENGTH) the block; a kv_len that is negative, beyond the block table or above 2^30, a first
+ * A position that is out of order, below its destination or not below kv_len (SLORA_DEV_BAD_POSITION) leaves the block and
+ * head that it is for unwritten, a destination beyond its table (SLORA_DEV_BAD_LENGTH) the block, and a bad page id, of a
+ * row's source or of the destination (SLORA_DEV_BAD_PAGE), the page that it is for.  Pages are keys or values, each by itself: the
+ * block's other page is written, as are the other blocks and new_len, so a sequence for which one of these was set is
+ * no longer whole.  A kv_len that is negative, beyond the block table or above 2^30, a first
  * outside [0, kv_len] or more kept tokens than there are from it on (SLORA_DEV_BAD_LENGTH), and offsets that decrease
  * or leave [0, K] (SLORA_DEV_BAD_SEGMENT), leave the sequence and its new_len as they were.
  *

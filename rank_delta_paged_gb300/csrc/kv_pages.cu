@@ -136,6 +136,8 @@ __device__ __forceinline__ int32_t load_span(const CompactArgs &a, int32_t s, Sp
 // A CTA takes one block of one head, keys and values: two pages, each by half of its threads, with its rows in shared
 // memory between the reads and the writes, where a thread finds what it has copied itself.  PT threads per page: 64,
 // or 128 for pages above 8192 bytes.
+// A page that cannot be used, as a source or to write to, keeps its half from writing, not the other: as everywhere
+// in the cache, work is skipped by the page.
 // In place a cluster of CTAs goes through a sequence's blocks from the first, a block each at a time: a block takes rows
 // from itself and later ones only, so what a round writes no later one reads, and within a round all have read
 // before one writes.  Where the next round's rows come from is looked up under this one's reads.
