@@ -603,7 +603,8 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   dst_table    device int32 [S][dst_blocks][n_kv_heads][2]: where the blocks from first[s] on go; NULL, or block_table
  *                itself: in place.  Only entries of written blocks are read.  A page that is written is none that the call
  *                reads, but that the block of first[s] may keep its page (or its page may be shared with the
- *                source table).  In that block the tokens before first[s] are written too.
+ *                source table).  In that block the tokens before first[s] are written too; a sequence that keeps
+ *                no token has nothing written, so its block of first[s] is still the source's page.
  *   new_len      device int32 [S] that gets first[s] + the kept tokens, or NULL; none of the other arrays
  * Scales: the exponent of every block that gets a token is the smallest e >= -40 for which every finite value of its
  * rows fits, 60 at most (as in append, with no regard for what it was): a row's codes are multiplied by a power

@@ -1,4 +1,5 @@
-"""GPU check of what a compaction leaves alone: a page that cannot be used is skipped by itself, keys and values apart."""
+"""GPU checks of what a compaction leaves alone: a page that cannot be used is skipped by itself, keys and values apart, and a
+sequence that keeps nothing has nothing written."""
 import numpy as np
 import pytest
 import torch
@@ -46,3 +47,16 @@ def test_a_bad_page_is_skipped_by_itself(fmt, w, source):
         assert np.array_equal(ge, we) and np.array_equal(got[rows], want[rows], equal_nan=True)
         assert np.array_equal(got[~(rows | behind)], before[~(rows | behind)], equal_nan=True)
         assert m.new_len.tolist() == [160, 140]
+
+
+@pytest.mark.parametrize("in_place", [False, True])
+def test_a_sequence_that_keeps_nothing(in_place):
+    """Its length becomes first, and the block of first stays where it is."""
+    m = Moves([300, 200, 64], [70, 10, 64], [0, 50, 0], seed=221, in_place=in_place)
+    before, exps = m.c.values()
+    m.check()
+    got, ge = m.c.values()
+    for s in (0, 2):
+        pages = m.table[s][m.table[s] >= 0]
+        assert np.array_equal(got[pages], before[pages], equal_nan=True) and np.array_equal(ge[pages], exps[pages])
+    assert m.new_len.tolist() == [70, 60, 64]
