@@ -476,7 +476,7 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * per page, i.e. per block of tokens and head, for keys and values apart:
  *     value = code * 2^exponent[page],   int8 exponent[num_pages], device memory of the cache
  * with exponents of -60 to 60: one that the caller wrote beyond them is read as the nearest of the
- * two (scores and sums are fp32).  append writes -40 to 11 by itself.
+ * two (scores and sums are fp32).  append writes -40 to 11 by itself, append with norms up to 60.
  * The format is that of the codes:
  *     SLORA_KV_E4M3  8-bit floats (4 exponent bits, 3 mantissa bits, largest value 448)
  *     SLORA_KV_INT8  integers -127 .. 127
@@ -541,8 +541,9 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * Each row x of head_dim channels of k and q becomes, before anything above is done with it,
  *     y = (x - m) / sqrt(mean((x - m)^2) + eps) * w      m = 0, or the mean of x with `centered`
  * in fp32 (the reciprocal square root to 2^-22 of its value, every other step rounded once, the sums in an
- * order that depends on head_dim alone, so that a token's codes depend on neither the batch nor the
- * kernel); values are not normalised.  A row with an infinity or a NaN becomes what the formula gives for it.
+ * order that depends on head_dim alone, so that the normed and rotated rows depend on neither the batch nor the
+ * kernel; a key's codes are its row's by its block's exponent, which is that of all the block's tokens);
+ * values are not normalised.  A row with an infinity or a NaN becomes what the formula gives for it.
  * Exponents end at 60 here, whatever the weights: keys beyond that become the largest code.
  * rope may be NULL here, with q too.
  *   norm

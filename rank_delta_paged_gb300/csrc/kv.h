@@ -15,11 +15,12 @@ namespace slora {
 namespace kv {
 
 // Smallest exponent of a block's scale: 2^-40 is below the smallest fp16 subnormal over
-// the largest code (2^-24 / 448), rotated values included, so it never costs precision, and
-// a block of zeros starts there and can grow.
+// the largest code (2^-24 / 448), rotated values included, so it never costs fp16 values precision, and
+// a block of zeros starts there and can grow.  (Normed keys are coarser for it where their weights leave a
+// block nothing above 2^-34.)
 constexpr int kMinExponent = -40;
 
-// Exponents beyond this are read as this; append writes -40 .. 11.  The softmax's sum carries
+// Exponents beyond this are read as this; append writes -40 .. 11, with norms up to this.  The softmax's sum carries
 // 2^-exponent of the value blocks, which must stay a normal fp32 number, and so must the
 // ratio of two scales.
 constexpr int kExpLimit = 60;
