@@ -3,14 +3,14 @@
     python examples/stream.py
 
 A stack of attention layers with random weights and normed queries and keys continues streams of
-tokens for as long as one likes.  Per layer and step:
+tokens up to the last position of the rotation's table.  Per layer and step:
 
     q, k, v = x W
     norms, rotation; k and v to the pages        slora_kv_append_norm
     attention over the window and the sinks      slora_kv_attend_sinks
 
 Blocks that the window has left and that hold no sink go back to the pool, so a stream holds the
-same number of pages however long it is.  A stream forks by sharing its whole blocks
+same number of pages however long it gets.  A stream forks by sharing its whole blocks
 (slora_pages_share) and copying the one it writes next (slora_kv_copy).  Drafted tokens run as
 one step, each after the ones before it, so the accepted ones are a prefix; the others are forgotten, and
 the block's scales are fitted to what is left (slora_kv_compact).
@@ -31,7 +31,7 @@ NO_PAGE = -1
 class Stream:
     def __init__(self, length=0, blocks=None):
         self.length = length             # tokens in the cache
-        self.settled = length            # of which no fork has pages of its own: drafts lie behind them
+        self.settled = length            # those of them that no accept() may take back: a fork has them too
         self.blocks = blocks or {}       # block -> int32 [layers][n_heads][2]
 
 
@@ -98,7 +98,7 @@ class Streams:
         return [x[indptr[i]:indptr[i + 1]] for i in range(len(streams))]
 
     def trim(self, s):
-        """Gives back the blocks that no later token sees."""
+        """Gives back the blocks that no later token sees, once the last drafts are accepted."""
         for b in [b for b in s.blocks if b * self.block >= self.sinks and (b + 1) * self.block <= s.length - self.window + 1]:
             self._give_back(s.blocks.pop(b))
 

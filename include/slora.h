@@ -576,7 +576,9 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  * token at position p sees the positions p - window + 1 .. p and those below n_sinks (up to p), each once.
  * window is 1 or more, n_sinks 0 .. 2^30 (0: slora_kv_attend with that window); the other arguments, and what is said of
  * them, are those of slora_kv_attend.  Blocks wholly between the sinks and the windows are not read: their pages can
- * be given back and their entries of the block table be -1, as in a stream that never ends.
+ * be given back and their entries of the block table be -1, so a long stream holds a bounded number of pages.  Keys stay
+ * turned by the positions that append was given: a query's distance to the sinks grows with the stream, and the rotation's table
+ * (n_positions) and the block table cover the whole of it.
  *
  * slora_kv_copy(): copies pages of the cache, rows and exponents, within the pool: a forked sequence gets its own
  * copy of the block that both would go on to write, and shares the others (slora_pages_share).
@@ -587,9 +589,14 @@ slora_status slora_lora_apply_noalloc(slora_pool_t pool, int32_t proj, const voi
  *   rows         device int32 [n], 0 .. block_tokens (0: nothing is copied), or NULL: all of them
  * A page id out of range (SLORA_DEV_BAD_PAGE) or a number of rows (SLORA_DEV_BAD_LENGTH) skips that page.
  *
- * slora_kv_compact(): moves the kept tokens of each sequence to the front, in place or into other pages: the
- * accepted branch of drafted tokens, or what is left of a long sequence when tokens are evicted.  The kept
+ * slora_kv_compact(): moves the kept tokens of each sequence to the front, in place or into other pages: what is left
+ * of a long sequence when tokens are evicted, or the accepted branch of drafted tokens.  The kept
  * tokens of sequence s, in order, become its tokens first[s], first[s] + 1, ..; the tokens before first[s] stay.
+ * Codes are moved as they are: a key is still turned by its old position and made of what its token attended to.  So after
+ * an eviction later tokens get `positions` that go on from the old length, not from new_len.  And drafts that
+ * were a chain, as slora_kv_attend runs them, are accepted as a prefix, which has nothing to move (its blocks' exponents are fitted
+ * anew); another branch is sound only if the caller appended the drafts with positions by their depth and
+ * attended to them by their tree, for which there is no mask here.
  *   n_seqs       S, 0 <= S <= 1 << 20
  *   n_kept       K, 0 <= K <= 1 << 30: entries of a list of kept tokens
  *   max_kept     the most kept tokens of a sequence; one with more is the caller's error (SLORA_DEV_BAD_SEGMENT)
