@@ -16,8 +16,8 @@ namespace kv {
 
 // Smallest exponent of a block's scale: 2^-40 is below the smallest fp16 subnormal over
 // the largest code (2^-24 / 448), rotated values included, so it never costs fp16 values precision, and
-// a block of zeros starts there and can grow.  (Normed keys are coarser for it where their weights leave a
-// block nothing above 2^-34.)
+// a block of zeros starts there and can grow.  (Normed keys can be coarser for it where their weights leave a
+// block nothing above 2^-32.)
 constexpr int kMinExponent = -40;
 
 // Exponents beyond this are read as this; append writes -40 .. 11, with norms up to this.  The softmax's sum carries

@@ -26,8 +26,8 @@
 // reads what it has written itself, holds the rows of the page and the next two (asynchronous copies) and
 // the rows' angles, which are the same for all heads of the block.  Their queries are a kernel of their own (rotate_kernel).
 //
-// Measured: 512 single tokens of 40 heads 10.5 us, with norms 14; 5046 tokens, of which 384 are single, of 32
-// heads 47.5 us (4.4 TB/s), with the mean taken out and a weight for each head 71; 16381 tokens of 8 heads of 64 42 us
+// Measured: 512 single tokens of 40 heads 10.6 us, with norms 14; 5046 tokens, of which 384 are single, of 32
+// heads 47 us (4.4 TB/s), with the mean taken out and a weight for each head 71; 16381 tokens of 8 heads of 64 42 us
 // (4.5 TB/s).  The instructions between the reads and the writes, the barrier of a page's maximum and the waits for
 // exponents take the time.
 // With two CTAs' worth of pages per block and CTAs found by a search of the token offsets, the
@@ -37,7 +37,8 @@
 // and with the call, take 26 us without, 45 with 215 of their 40960 pages growing and 55 with 9632 (INT8 25, 51 with
 // 246, 87 with 11157); row by row before the new codes were written it was 71 and 100.  The 5046 tokens some 60, then 80 with
 // 10720 pages growing.  Four rows per group of lanes, all their reads first: 9.3 us for the 512 tokens, 14.1 with norms, and 5.4 us
-// instead of 2.9 for one token.
+// instead of 2.9 for one token; for 2048 tokens 32.7 instead of 38.9 and 42.9 instead of 53.9 (not built: where it
+// starts to win is not known).
 // Pages above 8192 bytes have two rows per lane and one CTA per SM: 4096 tokens in prompts, cold, 52 us at 8192 bytes and
 // 32 heads (3.3 TB/s), 70 at 10240 and 40 (3.1 TB/s), 91 at 16384 and 64 (3.7 TB/s).
 #include <mutex>

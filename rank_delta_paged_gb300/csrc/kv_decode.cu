@@ -31,7 +31,8 @@
 // With SINKS the keys between a sequence's first tokens and its window are left out of the numbering of its tiles
 // (kv.h, key_shift), box by box of 16 (8) rows, so the sinks share the window's first tile.  256 single tokens over windows of
 // 4096 and 64 sinks: 341 us, 6.1 TB/s, 90 % of a plain copy's rate (322 without the sinks); one over 1020 and 4: 12.9; 48
-// sequences of 3 to 8 drafted tokens, 64 channels, over 1000 and 4: 42 us (43 without the sinks, by two CTAs per SM).
+// sequences of 3 to 8 drafted tokens, 64 channels, over 1000 and 4: 42.5 us by three CTAs per SM, 45.6 by two (without the
+// sinks, by two, 43).
 //
 // Measured: 512 single tokens over 30 to 1000 keys, 40 KV heads: 476 us, 5.7 TB/s; 4 over 60000 to 131000
 // keys: 116 us, 5.5 TB/s; one over 700: 11.7 us, of which the launch and the chain of dependent reads (lengths,
