@@ -123,7 +123,6 @@ class Streams:
     def fork(self, s):
         """A stream that goes on from here by itself."""
         child = Stream(s.length)
-        s.settled = s.length
         whole, rest = divmod(s.length, self.block)
         try:
             for b, pages in s.blocks.items():
@@ -138,6 +137,7 @@ class Streams:
         except rdp.SloraError:
             self.drop(child)
             raise
+        s.settled = s.length
         return child
 
     def _take(self):

@@ -488,7 +488,7 @@ __global__ void __launch_bounds__(kThreads, kQCtas) rotate_kernel(const __grid_c
         int32_t pos = a.positions && live ? a.positions[t] : 0;
         // rows outside every sequence, and those of a sequence that is skipped, are left alone
         // the last of n from lo that starts at or before t, a lane for every other of 2 LPR parts of them.  (64 sequences of
-        // a few tokens with 64 channels, whose rows have four lanes: one round more, and 0.9 us, with LPR parts.)
+        // a few tokens with 64 channels, whose rows have four lanes: one round more, and 0.6 us, with LPR parts.)
         int32_t lo = 0, n = a.b.S;
 #pragma unroll 1
         while (__any_sync(~0u, n > 1)) {

@@ -92,7 +92,7 @@ def test_a_full_pool_leaves_the_streams_as_they_were(example):
             assert err.value.status == 2 and t.length == 0 and t.blocks == {} and free(e) == n // 2
             with pytest.raises(rdp.SloraError):
                 e.fork(s)                                # a whole block to share, and one to copy
-            assert free(e) == n // 2
+            assert free(e) == n // 2 and s.settled == 0
             with pytest.raises(rdp.SloraError):
                 e.step([(s, tokens(e, e.block, 2))])
             assert s.length == e.block + 1 and all(np.array_equal(pages[b], s.blocks[b]) for b in s.blocks) and len(s.blocks) == 2
